@@ -28,6 +28,9 @@ __all__ = [
     "kvq_sparse_mla_attention_split_nvfp4_ds_mla_noalloc", "NOALLOC_SCRATCH_BYTES",
     "kvq_prefill_mla_attention_split_nvfp4_ds_mla", "kvq_prefill_mla_attention_split_fp8_ds_mla",
     "default_prefill_num_splits", "kvq_prefill_mla_attention_workspace",
+    "kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
+    "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes", "default_per_head_num_splits",
+    "PER_HEAD_MAX_SPLITS",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -41,6 +44,7 @@ STATUS_BAD_BATCH = 0x2
 STATUS_TIMEOUT = 0x4
 ATTN_MAX_SPLITS = 32
 NOALLOC_SCRATCH_BYTES = 24 << 20
+PER_HEAD_MAX_SPLITS = 128
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -93,6 +97,16 @@ _SIGNATURES = {
     "kvq_sparse_mla_attention_split_nvfp4_ds_mla_noalloc": [_P, _I64, _I64, _I64, _I32, _P, _I64, _I32, _P, _I64,
                                                             _I32, _I64, _I64, ctypes.c_float, _P, _I64, _I64, _P,
                                                             _I64, _I32, _P, _P],
+    "kvq_qk_norm_rope": [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I64, _I64, _I32, _I32,
+                         ctypes.c_float, _P, _I64, _I64, _P, _I64, _I64, _P, _P],
+    "kvq_window_attention_nvfp4_per_head": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _I64,
+                                            _I32, _I32, _I32, _I32, _P, _P, ctypes.c_float, _I32, _I32, _P, _I64,
+                                            _I64, _P, _I64, _I32, _I32, _P, _I64, _P, _P],
+    "kvq_tree_attention_nvfp4_per_head": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _I64,
+                                          _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, ctypes.c_float, _P, _I64,
+                                          _I64, _P, _I64, _I32, _I32, _P, _I64, _P, _P],
+    "kvq_compact_drafts_nvfp4_per_head": [_P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
+                                          _I32, _P, _I64, _I32, _P, _P],
 }
 
 
@@ -119,6 +133,8 @@ def load_library():
         handle.kvq_version.argtypes = []
         handle.kvq_sparse_mla_attention_split_workspace_bytes.restype = _I64
         handle.kvq_sparse_mla_attention_split_workspace_bytes.argtypes = [_I64, _I32, _I32]
+        handle.kvq_per_head_attention_workspace_bytes.restype = _I64
+        handle.kvq_per_head_attention_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32]
         _lib = handle
     return _lib
 
@@ -551,6 +567,242 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
                  0 if workspace is None else workspace.numel() * workspace.element_size()]
     _call(cname, *args, _status_ptr(status), _stream(stream, q.device))
     return out, (None if lse is False else lse)
+
+
+# --------------------------------------------------------------------------
+# serving from the per-head NVFP4 cache
+# --------------------------------------------------------------------------
+
+def _call_on(device, name: str, *args):
+    """_call with `device` current (the library launches on the current device)."""
+    if device.index == torch.cuda.current_device():
+        _call(name, *args)
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args)
+
+
+def _one_device(device, **tensors):
+    for name, t in tensors.items():
+        _need(t.device == device, f"{name}: expected a tensor on {device}, got {t.device}")
+
+
+def _stream_on(stream, device) -> int:
+    _need(not isinstance(stream, torch.cuda.Stream) or stream.device == device,
+          "stream: not a stream of the tensors' device")
+    return _stream(stream, device)
+
+
+def _heads(name, t, shape=None):
+    _need(t.dtype == torch.bfloat16 and t.is_cuda and t.dim() == 3 and t.stride(2) == 1
+          and (shape is None or tuple(t.shape) == shape),
+          f"{name}: expected a CUDA bf16 {list(shape) if shape else '[T, H, D]'} tensor with unit inner stride")
+
+
+def _rows_stride(t):
+    """Token and head strides for the library (a dimension of one element may carry any stride)."""
+    T, H, D = t.shape
+    sh = t.stride(1) if H > 1 else max(D, 8)
+    return (t.stride(0) if T > 1 else H * sh), sh
+
+
+def _row_stride(t):
+    """Row stride of a 2-d tensor for the library (that of a single row may be anything)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _int32_vector(name, t, n):
+    _need(t.dtype == torch.int32 and t.is_cuda and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
+          f"{name}: expected a contiguous CUDA int32 vector of {n}")
+
+
+def kvq_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float, interleaved=False, q_out=None,
+                     k_out=None, status=None, stream=None):
+    """RMS norm of every query and key head, then the rotation by its token's
+    position, in one pass: q bf16 [T, H, D], k bf16 [T, KH, D] (any token and
+    head strides, as slices of a packed projection have), q_weight / k_weight
+    bf16 [D], positions int64 [T], cos_sin fp32 [max_position, rot_dim]
+    (rot_dim / 2 cosines, then sines; rot_dim a multiple of 16, at most D).
+    Pairs are (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.  q_out /
+    k_out may be q / k.  Returns (q_out, k_out)."""
+    _heads("q", q)
+    T, H, D = q.shape
+    _heads("k", k)
+    _need(k.shape[0] == T and k.shape[2] == D, "q and k differ in tokens or head size")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(w.dtype == torch.bfloat16 and w.is_cuda and tuple(w.shape) == (D,) and w.is_contiguous(),
+              f"{name}: expected a contiguous CUDA bf16 [{D}] vector")
+    _need(positions.dtype == torch.int64 and positions.is_cuda and tuple(positions.shape) == (T,)
+          and positions.is_contiguous(), "positions: expected a contiguous CUDA int64 [T]")
+    _need(cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.dim() == 2
+          and (cos_sin.stride(1) == 1 or cos_sin.shape[1] <= 1),
+          "cos_sin: expected a CUDA fp32 [max_position, rot_dim] tensor with unit inner stride")
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, k.shape[1], D), dtype=torch.bfloat16, device=q.device)
+    _heads("q_out", q_out, (T, H, D))
+    _heads("k_out", k_out, (T, k.shape[1], D))
+    _one_device(q.device, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, cos_sin=cos_sin, q_out=q_out,
+                k_out=k_out)
+    _call_on(q.device, "kvq_qk_norm_rope", q.data_ptr(), *_rows_stride(q), k.data_ptr(), *_rows_stride(k),
+             q_weight.data_ptr(), k_weight.data_ptr(), positions.data_ptr(), T, H, k.shape[1], D, cos_sin.data_ptr(),
+             _row_stride(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+             float(eps), q_out.data_ptr(), *_rows_stride(q_out), k_out.data_ptr(), *_rows_stride(k_out),
+             _status_ptr(status), _stream_on(stream, q.device))
+    return q_out, k_out
+
+
+def kvq_per_head_attention_workspace_bytes(num_tokens: int, num_heads: int, head_size: int, num_splits: int) -> int:
+    """Bytes of workspace the per-head attention needs for num_splits > 1 (-1 for bad arguments)."""
+    return load_library().kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits)
+
+
+_sm_count = {}
+
+
+def _sms(device):
+    i = torch.cuda.current_device() if device is None or device.index is None else device.index
+    if i not in _sm_count:
+        _sm_count[i] = torch.cuda.get_device_properties(i).multi_processor_count
+    return _sm_count[i]
+
+
+def default_per_head_num_splits(max_query_len: int, num_heads: int, num_kv_heads: int, batch_size: int,
+                                max_seq_len: int, window: int = 0, num_sinks: int = 0, device=None) -> int:
+    """Key ranges of the per-head attention: as many as bring the CTAs to
+    four per SM, each with at least 256 keys, at most PER_HEAD_MAX_SPLITS."""
+    blocks = -(-max_query_len * (num_heads // num_kv_heads) // 16) * num_kv_heads * batch_size
+    keys = max_seq_len if window <= 0 else min(max_seq_len, window + max_query_len + num_sinks)
+    if blocks <= 0 or keys <= 0:
+        return 1
+    return max(1, min(PER_HEAD_MAX_SPLITS, keys // 256, 4 * _sms(device) // blocks))
+
+
+def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, kv_cache, k_scale, v_scale,
+                                        softmax_scale: float, max_query_len: int, max_seq_len: int, window: int = 0,
+                                        num_sinks: int = 0, layout="NHD", num_splits=None, workspace=None, out=None,
+                                        lse=None, status=None, stream=None):
+    """Causal attention over the per-head NVFP4 cache with a sliding window
+    (window <= 0: none) and num_sinks first tokens that stay visible.  q bf16
+    [T, H, D]; request b's query tokens [query_start[b], query_start[b+1])
+    (int32 [B+1], at most max_query_len each) are the last positions of its
+    seq_lens[b] entries (int32 [B], at most max_seq_len), read through
+    block_table int32 [B, W] from kv_cache (as kvq_reshape_and_cache_nvfp4
+    wrote it, layout "NHD" or "HND").  num_splits (default:
+    default_per_head_num_splits) key ranges; workspace for more than one: a
+    CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
+    (allocated here when None).  Returns (out bf16 [T, H, D], lse fp32 [T,
+    H]); lse=False skips the lse output."""
+    return _per_head_attention("kvq_window_attention_nvfp4_per_head", q, query_start, seq_lens, None, block_table,
+                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, int(window),
+                               int(num_sinks), layout, num_splits, workspace, out, lse, status, stream)
+
+
+def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
+                                      softmax_scale: float, max_query_len: int, max_seq_len: int, layout="NHD",
+                                      num_splits=None, workspace=None, out=None, lse=None, status=None, stream=None):
+    """Attention of drafted tokens that form a tree: request b's query tokens
+    are its drafts, the last entries of its sequence; draft i sees the whole
+    context before the drafts and draft j iff bit j % 64 of tree_mask[token
+    i, j // 64] (int64 [T, mask_words], 64 * mask_words >= max_query_len) is
+    set.  The rest is as in kvq_window_attention_nvfp4_per_head."""
+    _need(tree_mask.dtype == torch.int64 and tree_mask.is_cuda and tree_mask.dim() == 2
+          and tree_mask.shape[0] == q.shape[0] and (tree_mask.shape[1] <= 1 or tree_mask.stride(1) == 1),
+          "tree_mask: expected CUDA int64 [T, mask_words] rows")
+    return _per_head_attention("kvq_tree_attention_nvfp4_per_head", q, query_start, seq_lens, tree_mask, block_table,
+                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, 0, 0, layout,
+                               num_splits, workspace, out, lse, status, stream)
+
+
+def _per_head_attention(cname, q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
+                        softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout, num_splits, workspace,
+                        out, lse, status, stream):
+    _heads("q", q)
+    T, H, D = q.shape
+    _need(layout in LAYOUTS, f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
+    _need(kv_cache.dim() == 5, "kv_cache: expected a [P, 2, ...] tensor")
+    KH = kv_cache.shape[3 if layout == "NHD" else 2]
+    code, block_size = _per_head_cache(kv_cache, KH, D, layout)
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _int32_vector("seq_lens", seq_lens, B)
+    _int32_vector("query_start", query_start, B + 1)
+    _need(block_table.dtype == torch.int32 and block_table.is_cuda and block_table.dim() == 2
+          and block_table.shape[0] == B and (block_table.shape[1] <= 1 or block_table.stride(1) == 1),
+          "block_table: expected a CUDA int32 [B, W] tensor with unit inner stride")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(t.dtype == torch.float32 and t.is_cuda and t.numel() >= 1, f"{name}: CUDA fp32 scalar")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    _heads("out", out, (T, H, D))
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    if lse is not False:
+        _need(lse.dtype == torch.float32 and lse.is_cuda and tuple(lse.shape) == (T, H)
+              and (H <= 1 or lse.stride(1) == 1),
+              "lse: expected a CUDA fp32 [T, H] tensor with unit inner stride")
+        _one_device(q.device, lse=lse)
+    _one_device(q.device, query_start=query_start, seq_lens=seq_lens, block_table=block_table, kv_cache=kv_cache,
+                k_scale=k_scale, v_scale=v_scale, out=out)
+    if num_splits is None:
+        num_splits = 1 if KH == 0 else default_per_head_num_splits(int(max_query_len), H, KH, B, int(max_seq_len),
+                                                                   window, num_sinks, q.device)
+    if num_splits > 1 and workspace is None and T > 0:
+        workspace = torch.empty(kvq_per_head_attention_workspace_bytes(T, H, D, num_splits), dtype=torch.uint8,
+                                device=q.device)
+    if workspace is not None:
+        _need(workspace.is_cuda and workspace.is_contiguous(), "workspace: expected a contiguous CUDA tensor")
+        _one_device(q.device, workspace=workspace)
+    args = [q.data_ptr(), *_rows_stride(q), T, H, query_start.data_ptr(), seq_lens.data_ptr(), B, int(max_query_len)]
+    if tree_mask is not None:
+        _one_device(q.device, tree_mask=tree_mask)
+        args += [tree_mask.data_ptr(), _row_stride(tree_mask), tree_mask.shape[1]]
+    args += [block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
+             kv_cache.data_ptr(), kv_cache.shape[0], block_size, code, KH, D, k_scale.data_ptr(), v_scale.data_ptr(),
+             float(softmax_scale)]
+    if tree_mask is None:
+        args += [window, num_sinks]
+    args += [out.data_ptr(), *_rows_stride(out), None if lse is False else lse.data_ptr(),
+             0 if lse is False else _row_stride(lse), int(max_seq_len), int(num_splits),
+             None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.numel() * workspace.element_size()]
+    _call_on(q.device, cname, *args, _status_ptr(status), _stream_on(stream, q.device))
+    return out, (None if lse is False else lse)
+
+
+def kvq_compact_drafts_nvfp4_per_head(kv_cache, query_start, seq_lens, accepted, accepted_lens, block_table,
+                                      layout="NHD", status=None, stream=None):
+    """After a tree of drafts was checked: for each request b, copies the
+    cache entries of its accepted drafts accepted[b, :accepted_lens[b]]
+    (int32 [B, A], increasing draft numbers) to the first positions behind
+    its context (seq_lens[b] minus its query tokens), in every layer.
+    kv_cache: uint8 [P, 2, ...] as kvq_reshape_and_cache_nvfp4 takes it, or
+    [L, P, 2, ...] for L layers that share the block table (each layer
+    contiguous).  seq_lens is left to the caller."""
+    _need(layout in LAYOUTS, f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
+    _need(kv_cache.dim() in (5, 6), "kv_cache: expected a [P, 2, ...] or [L, P, 2, ...] tensor")
+    layers = kv_cache.shape[0] if kv_cache.dim() == 6 else 1
+    if layers == 0:
+        return
+    one = kv_cache[0] if kv_cache.dim() == 6 else kv_cache
+    D = one.shape[4] // 9 * 16
+    KH = one.shape[3 if layout == "NHD" else 2]
+    code, block_size = _per_head_cache(one, KH, D, layout)
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _int32_vector("seq_lens", seq_lens, B)
+    _int32_vector("query_start", query_start, B + 1)
+    _int32_vector("accepted_lens", accepted_lens, B)
+    for name, t in (("accepted", accepted), ("block_table", block_table)):
+        _need(t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[0] == B
+              and (t.shape[1] <= 1 or t.stride(1) == 1), f"{name}: expected CUDA int32 [B, ...] rows")
+    _one_device(kv_cache.device, query_start=query_start, seq_lens=seq_lens, accepted=accepted,
+                accepted_lens=accepted_lens, block_table=block_table)
+    _call_on(kv_cache.device, "kvq_compact_drafts_nvfp4_per_head", kv_cache.data_ptr(), layers,
+             kv_cache.stride(0) if layers > 1 else 0, one.shape[0], block_size, code, KH, D, query_start.data_ptr(),
+             seq_lens.data_ptr(), B, accepted.data_ptr(), _row_stride(accepted),
+             accepted_lens.data_ptr(), accepted.shape[1], block_table.data_ptr(),
+             _row_stride(block_table), block_table.shape[1], _status_ptr(status),
+             _stream_on(stream, kv_cache.device))
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

@@ -753,6 +753,295 @@ kvq_status kvq_sparse_mla_attention_split_nvfp4_ds_mla_noalloc(
       num_splits, scratch, need > 0 ? KVQ_NOALLOC_SCRATCH_BYTES : 0, d_status, stream);
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// serving from the per-head NVFP4 cache
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Rows of bf16 heads [tokens][heads][head_size] given by token and head strides.
+kvq_status check_heads(const char* fn, const char* name, const void* p, int64_t stride_t, int64_t stride_h,
+                       int32_t heads, int32_t head_size, bool output) {
+  KVQ_REQUIRE(p != nullptr && aligned(p, 16), "%s: %s must be non-NULL and 16-byte aligned", fn, name);
+  KVQ_REQUIRE(stride_t >= 0 && stride_h >= head_size && stride_t % 8 == 0 && stride_h % 8 == 0,
+              "%s: %s strides must be non-negative multiples of 8 elements with head stride >= head_size", fn, name);
+  KVQ_REQUIRE(stride_h <= (int64_t{1} << 40) / heads, "%s: %s head stride too large", fn, name);
+  if (output)
+    KVQ_REQUIRE(stride_t >= (heads - 1) * stride_h + head_size,
+                "%s: %s rows must not overlap (token stride >= (heads - 1) * head stride + head_size)", fn, name);
+  return KVQ_OK;
+}
+
+// A contiguous per-head cache; *region: bytes of one (page, side).
+kvq_status check_per_head_cache(const char* fn, const void* cache, int64_t num_pages, int32_t block_size,
+                                int32_t layout, int32_t num_kv_heads, int32_t head_size, int64_t* region) {
+  KVQ_REQUIRE(layout == KVQ_LAYOUT_NHD || layout == KVQ_LAYOUT_HND,
+              "%s: layout must be KVQ_LAYOUT_NHD (0) or KVQ_LAYOUT_HND (1)", fn);
+  KVQ_REQUIRE(cache != nullptr && aligned(cache, 16), "%s: kv_cache must be non-NULL and 16-byte aligned", fn);
+  KVQ_REQUIRE(num_pages > 0 && num_pages < (int64_t{1} << 31) && block_size > 0,
+              "%s: num_pages must be in [1, 2^31) and block_size positive", fn);
+  KVQ_REQUIRE(num_kv_heads > 0 && int64_t{block_size} * num_kv_heads < (int64_t{1} << 31),
+              "%s: need num_kv_heads > 0 and block_size * num_kv_heads below 2^31", fn);
+  *region = int64_t{block_size} * num_kv_heads * (head_size / 2 + head_size / 16);
+  return KVQ_OK;
+}
+
+kvq_status check_table(const char* fn, const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size,
+                       const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width) {
+  KVQ_REQUIRE(batch_size <= 65535, "%s: batch_size must be at most 65535", fn);
+  KVQ_REQUIRE(query_start != nullptr && seq_lens != nullptr && block_table != nullptr,
+              "%s: query_start, seq_lens and block_table must be non-NULL", fn);
+  KVQ_REQUIRE(aligned(query_start, 4) && aligned(seq_lens, 4) && aligned(block_table, 4),
+              "%s: int32 arrays must be 4-byte aligned", fn);
+  KVQ_REQUIRE(block_table_width > 0 && block_table_stride >= block_table_width,
+              "%s: need block_table_width > 0 and block_table_stride >= block_table_width", fn);
+  return KVQ_OK;
+}
+
+struct TreeMask {
+  const uint64_t* mask = nullptr;
+  int64_t stride = 0;
+  int32_t words = 0;
+};
+
+kvq_status per_head_attention(
+    const char* fn, const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache,
+    int64_t num_pages, int32_t block_size, int32_t layout, int32_t num_kv_heads, int32_t head_size,
+    const float* k_scale, const float* v_scale, float softmax_scale, int32_t window, int32_t num_sinks,
+    const TreeMask* tree, void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int64_t lse_stride_t,
+    int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes, int32_t* d_status,
+    kvq_stream_t stream) {
+  KVQ_REQUIRE(num_tokens >= 0 && batch_size >= 0 && max_query_len >= 0 && max_seq_len >= 0,
+              "%s: num_tokens, batch_size, max_query_len and max_seq_len must be >= 0", fn);
+  KVQ_REQUIRE(num_splits >= 1 && num_splits <= KVQ_PER_HEAD_MAX_SPLITS, "%s: num_splits must be in [1, %d] (got %d)",
+              fn, KVQ_PER_HEAD_MAX_SPLITS, num_splits);
+  KVQ_REQUIRE(num_sinks >= 0, "%s: num_sinks must be >= 0", fn);
+  if (num_tokens == 0 || batch_size == 0 || max_query_len == 0) return ok();
+  KVQ_REQUIRE(head_size == 64 || head_size == 128 || head_size == 256,
+              "%s: head_size must be 64, 128 or 256 (got %d)", fn, head_size);
+  KVQ_REQUIRE(num_kv_heads > 0 && num_heads > 0 && num_heads % num_kv_heads == 0,
+              "%s: num_heads must be a positive multiple of num_kv_heads (got %d, %d)", fn, num_heads, num_kv_heads);
+  KVQ_REQUIRE(num_tokens < (int64_t{1} << 31) && int64_t{max_query_len} * num_heads < (int64_t{1} << 31),
+              "%s: num_tokens and max_query_len * num_heads must stay below 2^31", fn);
+  int64_t region = 0;
+  if (kvq_status s = check_per_head_cache(fn, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size, &region))
+    return s;
+  KVQ_REQUIRE(region % 16 == 0, "%s: block_size * num_kv_heads * (head_size / 2 + head_size / 16) must be a multiple "
+              "of 16 (got %lld)", fn, static_cast<long long>(region));
+  if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "out", out, out_stride_t, out_stride_h, num_heads, head_size, true)) return s;
+  KVQ_REQUIRE(lse == nullptr || (aligned(lse, 4) && lse_stride_t >= num_heads),
+              "%s: lse must be 4-byte aligned with token stride >= num_heads", fn);
+  if (kvq_status s = check_table(fn, query_start, seq_lens, batch_size, block_table, block_table_stride,
+                                 block_table_width))
+    return s;
+  KVQ_REQUIRE(int64_t{block_table_width} * block_size < (int64_t{1} << 31) - 64,
+              "%s: block_table_width * block_size must stay below 2^31 - 64 positions", fn);
+  KVQ_REQUIRE(k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4),
+              "%s: k_scale / v_scale must be device fp32 scalars", fn);
+  KVQ_REQUIRE(softmax_scale == softmax_scale && softmax_scale > -3.0e38f && softmax_scale < 3.0e38f,
+              "%s: softmax_scale must be finite", fn);
+  if (tree != nullptr)
+    KVQ_REQUIRE(tree->mask != nullptr && aligned(tree->mask, 8) && tree->words >= 1 && tree->stride >= tree->words &&
+                    int64_t{tree->words} * 64 >= max_query_len,
+                "%s: tree_mask must be non-NULL, 8-byte aligned, with at least max_query_len bits per row and row "
+                "stride >= mask_words", fn);
+  KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
+  const int32_t group = num_heads / num_kv_heads;
+  KVQ_REQUIRE((int64_t{max_query_len} * group + 7) / 8 * num_kv_heads * num_splits < (int64_t{1} << 31),
+              "%s: max_query_len * num_heads * num_splits too large", fn);
+  if (num_splits > 1) {
+    const int64_t need = kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits);
+    KVQ_REQUIRE(need >= 0 && workspace != nullptr && aligned(workspace, 16) && workspace_bytes >= need,
+                "%s: workspace must be non-NULL, 16-byte aligned and at least %lld bytes (got %lld)", fn,
+                static_cast<long long>(need), static_cast<long long>(workspace_bytes));
+  }
+  if (kvq_status s = check_device(fn)) return s;
+  kvq::PerHeadAttentionArgs a{};
+  a.q = q;
+  a.q_stride_t = q_stride_t;
+  a.q_stride_h = q_stride_h;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_size = head_size;
+  a.group = group;
+  a.group_div = kvq::FastDiv::make(static_cast<uint32_t>(group));
+  a.query_start = query_start;
+  a.seq_lens = seq_lens;
+  a.batch_size = batch_size;
+  a.max_query_len = max_query_len;
+  a.block_table = block_table;
+  a.block_table_stride = block_table_stride;
+  a.block_table_width = block_table_width;
+  a.table_positions = block_table_width * block_size;
+  a.cache = kv_cache;
+  a.num_pages = num_pages;
+  a.block_size = block_size;
+  a.block_div = kvq::FastDiv::make(static_cast<uint32_t>(block_size));
+  a.region = region;
+  a.scales = int64_t{block_size} * num_kv_heads * (head_size / 2);
+  a.row_offset = layout == KVQ_LAYOUT_HND ? 1 : num_kv_heads;
+  a.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074);
+  a.window = window;
+  a.num_sinks = num_sinks;
+  if (tree != nullptr) {
+    a.tree_mask = tree->mask;
+    a.tree_stride = tree->stride;
+    a.tree_words = tree->words;
+  }
+  a.out = out;
+  a.out_stride_t = out_stride_t;
+  a.out_stride_h = out_stride_h;
+  a.lse = lse;
+  a.lse_stride_t = lse_stride_t;
+  a.status = d_status;
+  a.num_splits = num_splits;
+  if (num_splits > 1) {
+    // ranges of whole 64-key steps, sized from the keys that a row block can
+    // see: the whole sequence, or the window, a block's other tokens and the sinks
+    int64_t span = max_seq_len;
+    if (window > 0)
+      span = std::min<int64_t>(span, int64_t{window} + std::min(max_query_len, 256) + num_sinks);
+    const int64_t steps = std::max<int64_t>(1, (span + 63) / 64);
+    a.split_keys = static_cast<int32_t>((steps + num_splits - 1) / num_splits * 64);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_lse = static_cast<float*>(workspace) + num_tokens * num_heads * num_splits * head_size;
+  }
+  return launched(fn, kvq::launch_per_head_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_size,
+                                               int32_t num_splits) {
+  if (num_tokens <= 0 || num_heads <= 0 || head_size <= 0 || num_splits <= 0) return -1;
+  const int64_t row = (int64_t{head_size} + 1) * 4 * num_splits;          // < 2^64 / 2 for any int32 factors
+  if (row > INT64_MAX / 2 / num_heads || num_tokens > (INT64_MAX / 2) / (row * num_heads)) return -1;
+  return (num_tokens * num_heads * row + 15) / 16 * 16;
+}
+
+kvq_status kvq_window_attention_nvfp4_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache,
+    int64_t num_pages, int32_t block_size, int32_t layout, int32_t num_kv_heads, int32_t head_size,
+    const float* k_scale, const float* v_scale, float softmax_scale, int32_t window, int32_t num_sinks, void* out,
+    int64_t out_stride_t, int64_t out_stride_h, float* lse, int64_t lse_stride_t, int32_t max_seq_len,
+    int32_t num_splits, void* workspace, int64_t workspace_bytes, int32_t* d_status, kvq_stream_t stream) {
+  return per_head_attention("kvq_window_attention_nvfp4_per_head", q, q_stride_t, q_stride_h, num_tokens, num_heads,
+                            query_start, seq_lens, batch_size, max_query_len, block_table, block_table_stride,
+                            block_table_width, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size,
+                            k_scale, v_scale, softmax_scale, window, num_sinks, nullptr, out, out_stride_t,
+                            out_stride_h, lse, lse_stride_t, max_seq_len, num_splits, workspace, workspace_bytes,
+                            d_status, stream);
+}
+
+kvq_status kvq_tree_attention_nvfp4_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const uint64_t* tree_mask, int64_t tree_mask_stride, int32_t mask_words, const int32_t* block_table,
+    int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache, int64_t num_pages,
+    int32_t block_size, int32_t layout, int32_t num_kv_heads, int32_t head_size, const float* k_scale,
+    const float* v_scale, float softmax_scale, void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse,
+    int64_t lse_stride_t, int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes,
+    int32_t* d_status, kvq_stream_t stream) {
+  const TreeMask tree{tree_mask, tree_mask_stride, mask_words};
+  return per_head_attention("kvq_tree_attention_nvfp4_per_head", q, q_stride_t, q_stride_h, num_tokens, num_heads,
+                            query_start, seq_lens, batch_size, max_query_len, block_table, block_table_stride,
+                            block_table_width, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size,
+                            k_scale, v_scale, softmax_scale, 0, 0, &tree, out, out_stride_t, out_stride_h, lse,
+                            lse_stride_t, max_seq_len, num_splits, workspace, workspace_bytes, d_status, stream);
+}
+
+kvq_status kvq_qk_norm_rope(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t,
+                            int64_t k_stride_h, const void* q_weight, const void* k_weight, const int64_t* positions,
+                            int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                            const float* cos_sin, int64_t cos_sin_stride, int64_t max_position, int32_t rot_dim,
+                            int32_t interleaved, float eps, void* q_out, int64_t q_out_stride_t,
+                            int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t, int64_t k_out_stride_h,
+                            int32_t* d_status, kvq_stream_t stream) {
+  const char* fn = "kvq_qk_norm_rope";
+  KVQ_REQUIRE(num_tokens >= 0, "%s: num_tokens < 0", fn);
+  if (num_tokens == 0) return ok();
+  KVQ_REQUIRE(num_heads > 0 && num_kv_heads > 0, "%s: num_heads and num_kv_heads must be positive", fn);
+  KVQ_REQUIRE(head_size >= 16 && head_size <= 256 && head_size % 16 == 0,
+              "%s: head_size must be a multiple of 16 in [16, 256] (got %d)", fn, head_size);
+  KVQ_REQUIRE(rot_dim >= 0 && rot_dim <= head_size && rot_dim % 16 == 0,
+              "%s: rot_dim must be a multiple of 16 in [0, head_size] (got %d)", fn, rot_dim);
+  KVQ_REQUIRE(num_tokens * (int64_t{num_heads} + num_kv_heads) < (int64_t{1} << 31),
+              "%s: num_tokens * (num_heads + num_kv_heads) must stay below 2^31", fn);
+  if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "k", k, k_stride_t, k_stride_h, num_kv_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "q_out", q_out, q_out_stride_t, q_out_stride_h, num_heads, head_size, true))
+    return s;
+  if (kvq_status s = check_heads(fn, "k_out", k_out, k_out_stride_t, k_out_stride_h, num_kv_heads, head_size, true))
+    return s;
+  KVQ_REQUIRE(q_weight != nullptr && k_weight != nullptr && aligned(q_weight, 16) && aligned(k_weight, 16),
+              "%s: q_weight / k_weight must be non-NULL and 16-byte aligned", fn);
+  KVQ_REQUIRE(positions != nullptr && aligned(positions, 8), "%s: bad positions", fn);
+  KVQ_REQUIRE(max_position > 0, "%s: max_position must be positive", fn);
+  KVQ_REQUIRE(rot_dim == 0 || (cos_sin != nullptr && aligned(cos_sin, 16) && cos_sin_stride >= rot_dim &&
+                               cos_sin_stride % 4 == 0),
+              "%s: cos_sin must be 16-byte aligned with row stride >= rot_dim, a multiple of 4", fn);
+  KVQ_REQUIRE(eps >= 0.0f && eps < 3.0e38f, "%s: eps must be finite and >= 0", fn);
+  KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
+  int num_sms = 0;
+  if (kvq_status s = check_device(fn, &num_sms)) return s;
+  const kvq::NormRopeArgs a{q,          q_stride_t,  q_stride_h,     k,           k_stride_t,
+                            k_stride_h, q_weight,    k_weight,       positions,   num_tokens,
+                            num_heads,  num_kv_heads, head_size,     cos_sin,     cos_sin_stride,
+                            max_position, rot_dim,   interleaved != 0, eps,       q_out,
+                            q_out_stride_t, q_out_stride_h, k_out,   k_out_stride_t, k_out_stride_h,
+                            d_status};
+  return launched(fn, kvq::launch_qk_norm_rope(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_compact_drafts_nvfp4_per_head(
+    uint8_t* kv_cache, int32_t num_layers, int64_t layer_stride, int64_t num_pages, int32_t block_size,
+    int32_t layout, int32_t num_kv_heads, int32_t head_size, const int32_t* query_start, const int32_t* seq_lens,
+    int32_t batch_size, const int32_t* accepted, int64_t accepted_stride, const int32_t* accepted_lens,
+    int32_t max_accepted, const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    int32_t* d_status, kvq_stream_t stream) {
+  const char* fn = "kvq_compact_drafts_nvfp4_per_head";
+  KVQ_REQUIRE(num_layers >= 0 && batch_size >= 0 && max_accepted >= 0,
+              "%s: num_layers, batch_size and max_accepted must be >= 0", fn);
+  if (num_layers == 0 || batch_size == 0 || max_accepted == 0) return ok();
+  KVQ_REQUIRE(head_size >= 16 && head_size <= 1024 && head_size % 16 == 0,
+              "%s: head_size must be a multiple of 16 in [16, 1024] (got %d)", fn, head_size);
+  int64_t region = 0;
+  if (kvq_status s = check_per_head_cache(fn, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size, &region))
+    return s;
+  KVQ_REQUIRE(region % 8 == 0 && int64_t{block_size} * num_kv_heads * (head_size / 2) % 8 == 0,
+              "%s: block_size * num_kv_heads * full_dim must be a multiple of 8", fn);
+  KVQ_REQUIRE(num_layers <= 32767 && num_kv_heads <= 65535, "%s: at most 32767 layers and 65535 heads", fn);
+  KVQ_REQUIRE(num_layers == 1 || (layer_stride >= num_pages * 2 * region && layer_stride % 16 == 0),
+              "%s: layer_stride must be a multiple of 16 and cover a layer's pages (got %lld)", fn,
+              static_cast<long long>(layer_stride));
+  if (kvq_status s = check_table(fn, query_start, seq_lens, batch_size, block_table, block_table_stride,
+                                 block_table_width))
+    return s;
+  KVQ_REQUIRE(accepted != nullptr && accepted_lens != nullptr && aligned(accepted, 4) && aligned(accepted_lens, 4) &&
+                  accepted_stride >= max_accepted,
+              "%s: accepted / accepted_lens must be non-NULL, 4-byte aligned, with accepted_stride >= max_accepted", fn);
+  KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
+  if (kvq_status s = check_device(fn)) return s;
+  const kvq::CompactArgs a{kv_cache,        num_layers,    num_layers == 1 ? 0 : layer_stride, num_pages, block_size,
+                           layout,          num_kv_heads,  head_size,     query_start,        seq_lens,  batch_size,
+                           accepted,        accepted_stride, accepted_lens, max_accepted,     block_table,
+                           block_table_stride, block_table_width, d_status};
+  return launched(fn, kvq::launch_compact_drafts(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* kvq_last_error_string(void) { return g_last_error.c_str(); }
 
 int32_t kvq_version(void) { return 100; }

@@ -161,4 +161,96 @@ cudaError_t launch_selftest_convert(uint32_t first_bits, int64_t count, uint8_t*
                                     uint8_t* e4m3_hi, uint8_t* e2m1_lo, uint8_t* e2m1_hi,
                                     uint16_t* bf16_out, int num_sms, cudaStream_t stream);
 
+struct NormRopeArgs {
+  const void* q;
+  int64_t q_stride_t, q_stride_h;
+  const void* k;
+  int64_t k_stride_t, k_stride_h;
+  const void* q_weight;           // bf16 [head_size]
+  const void* k_weight;
+  const int64_t* positions;
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads;
+  int32_t head_size;
+  const float* cos_sin;           // fp32 [max_position, rot_dim]: cosines, then sines
+  int64_t cos_sin_stride;
+  int64_t max_position;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float eps;
+  void* q_out;
+  int64_t q_out_stride_t, q_out_stride_h;
+  void* k_out;
+  int64_t k_out_stride_t, k_out_stride_h;
+  int32_t* status;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention over the per-head NVFP4 cache: request b's query tokens
+// [query_start[b], query_start[b+1]) are the last positions of its sequence
+// [0, seq_lens[b]).
+struct PerHeadAttentionArgs {
+  const void* q;                  // bf16 [num_tokens, num_heads, head_size]
+  int64_t q_stride_t, q_stride_h;
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads, head_size;
+  int32_t group;                  // num_heads / num_kv_heads query heads share a key head
+  FastDiv group_div;
+  const int32_t* query_start;     // [batch_size + 1]
+  const int32_t* seq_lens;        // [batch_size]
+  int32_t batch_size;
+  int32_t max_query_len;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  int32_t block_table_width;
+  int32_t table_positions;        // block_table_width * block_size, < 2^31 - 64 (host check)
+  const uint8_t* cache;
+  int64_t num_pages;
+  int32_t block_size;
+  FastDiv block_div;
+  int64_t region;                 // bytes of one (page, side): K at 2 * page * region, V one region on
+  int64_t scales;                 // offset of the scale rows inside a region
+  int32_t row_offset, row_head;   // row of (offset, head) = offset * row_offset + head * row_head
+  const float* k_scale;
+  const float* v_scale;
+  float scale_log2;               // softmax_scale * log2(e)
+  int32_t window;                 // <= 0: none
+  int32_t num_sinks;
+  const uint64_t* tree_mask;      // tree form: [num_tokens, tree_words], else nullptr
+  int64_t tree_stride;
+  int32_t tree_words;
+  void* out;                      // bf16 [num_tokens, num_heads, head_size]
+  int64_t out_stride_t, out_stride_h;
+  float* lse;
+  int64_t lse_stride_t;
+  int32_t* status;
+  // split over the keys: range s of a row block takes its key steps
+  // [s * split_keys, +split_keys), the last one every key past them too
+  int32_t num_splits;
+  int32_t split_keys;
+  float* part_o;                  // fp32 [num_tokens, num_heads, num_splits, head_size], normalised
+  float* part_lse;                // fp32 [num_tokens, num_heads, num_splits], base 2
+};
+cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream);
+
+struct CompactArgs {
+  uint8_t* cache;
+  int32_t num_layers;
+  int64_t layer_stride;           // bytes
+  int64_t num_pages;
+  int32_t block_size, layout, num_kv_heads, head_size;
+  const int32_t* query_start;
+  const int32_t* seq_lens;
+  int32_t batch_size;
+  const int32_t* accepted;        // [batch_size, >= max_accepted]
+  int64_t accepted_stride;
+  const int32_t* accepted_lens;
+  int32_t max_accepted;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  int32_t block_table_width;
+  int32_t* status;
+};
+cudaError_t launch_compact_drafts(const CompactArgs& a, cudaStream_t stream);
+
 }  // namespace kvq

@@ -1,0 +1,697 @@
+// kvq_per_head_attention.cu -- attention read straight from the paged
+// per-head NVFP4 K/V cache, for grouped query heads, in two forms of mask:
+//   window  causal, with a sliding window and a few first tokens that stay
+//           visible: the query at position p sees key j iff j <= p and
+//           (window <= 0 or j > p - window or j < num_sinks);
+//   tree    drafted tokens at the end of the sequence: draft i sees the whole
+//           context before the drafts, and draft j iff bit j of its mask.
+// For query row (token t, head h) over its visible keys j of key head h /
+// group, with k_j, v_j the decoded entries (e2m1 * e4m3, exact):
+//   s_j = softmax_scale * k_scale * (q . k_j)
+//   out = v_scale * sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + ln sum
+// (no visible key: out = 0, lse = -inf).
+//
+// Few query rows (decode): the keys' bytes bound it, 9/16 byte per value.
+// One CTA of four warps per (block of 8 kRowTiles query rows, key head, range
+// of keys); the rows are (token, head) pairs of one request that share the
+// key head.  Each warp takes every fourth step of 32 keys, with its own
+// running maximum and sum, and the warps join at the end through shared
+// memory; ranges join in a second launch.  A warp copies a step's raw bytes
+// (32 entries of 9 D / 16 bytes, K and V) into its own three-stage ring with
+// asynchronous copies, two steps ahead, so that nothing but the warp's own
+// copies is ever waited for.
+//
+// The products run as S^T = K Q^T and O^T = V^T P^T on the warp's matrix
+// instruction (16 x 8 x 16, f16 in, fp32 sums): the keys (the head
+// dimensions) fill the 16-wide side, the query rows only an 8-wide one, so a
+// single token's 4 or 8 grouped heads waste little.  Every operand register
+// is decoded where it is used: for K, a lane's 16-byte piece of an entry is
+// D / 4 whole dimensions of one key; for V, a lane takes D / 8 dimensions of
+// four keys and merges two keys' nibbles into one byte before converting it,
+// so that a converted pair holds two keys.  The order of the dimensions and
+// of the keys inside the products is free, and chosen so that these pieces
+// are contiguous; q is loaded in the same order.  P^T comes from S^T by the
+// 8 x 8 transposing move.
+// f16 holds the decoded entries exactly (at most 6 significant bits, 2^-10 to
+// 2688).  A query row is scaled by the power of two that brings its largest
+// value to [2^14, 2^15): bf16's 8 bits stay exact in f16 down to 2^-28 of
+// that largest value, and what is lost below is under 2^-39 of it.  The
+// weights are kept as 2^(s - m + 6) with m at most 2^8 behind the true
+// maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
+#include "kvq_device.cuh"
+#include "kvq_launch.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 32;                   // keys per warp step
+constexpr int kStages = 3;
+constexpr float kGrow = 8.0f;               // the reference maximum moves when exceeded by 2^8
+constexpr float kShift = 6.0f;              // weights are 2^(s - m + kShift)
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Shared memory of one warp's stage: 32 data rows of K, of V, then their scale rows.
+template <int D>
+struct Stage {
+  static constexpr int kRow = D / 2, kScales = D / 16;
+  static constexpr int kV = kStep * kRow, kKs = 2 * kStep * kRow, kVs = kKs + kStep * kScales;
+  static constexpr int kBytes = kVs + kStep * kScales;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// `bytes` = kBytes, or 0: zero-filled, nothing read.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t bytes) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(kBytes), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return bits(__hmul2(half2_of(a), half2_of(b))); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
+
+// The four bytes of w (two e2m1 codes each) as f16 pairs.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// D += A B, A 16 x 16 (row), B 16 x 8 (col), f16 in, fp32 out.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 transpose of a b16 fragment held across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Stage row of the key with index n (0..7) inside an 8-key half: the rows of
+// keys 2c differ mod 4 over c, and those of 2c and 2c + 1 in parity, which
+// keeps the lanes' shared-memory reads apart.
+__device__ __forceinline__ uint32_t key_row(uint32_t n) { return (n & 1) ? 4 + ((n >> 1) ^ 1) : n >> 1; }
+// 16-byte chunk swizzles of the staged data rows.
+template <int D>
+__device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) {
+  return D == 256 ? chunk ^ (row & 1) : chunk;
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
+  return D == 256 ? chunk ^ ((row & 3) << 1) : D == 128 ? chunk ^ (row & 2) : chunk;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The keys of one block of query rows: positions [0, sinks) and [lo, hi), in
+// steps of 32.
+struct Keys {
+  int32_t sinks, lo, hi;
+  int32_t sink_steps, steps;
+
+  __device__ __forceinline__ int32_t base(int32_t step) const {
+    return step < sink_steps ? step * kStep : lo + (step - sink_steps) * kStep;
+  }
+  __device__ __forceinline__ int32_t limit(int32_t step) const { return step < sink_steps ? sinks : hi; }
+};
+
+struct Request {
+  int64_t token0;              // its first query token
+  int32_t tokens;              // its query tokens
+  int64_t first_pos;           // position of its first query token (may be negative)
+  bool cut;                    // the sequence goes past the block table
+  int32_t len;                 // its sequence, as far as the block table reaches
+};
+
+// The request, or false (skipped): its query tokens are not inside [0,
+// num_tokens), or more than max_query_len.
+__device__ __forceinline__ bool request_of(const PerHeadAttentionArgs& a, int b, Request& r) {
+  const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
+  if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || q1 - q0 > a.max_query_len) return false;
+  r.token0 = q0;
+  r.tokens = q1 - q0;
+  const int32_t len = max(0, __ldg(a.seq_lens + b));
+  r.first_pos = static_cast<int64_t>(len) - r.tokens;
+  r.len = min(len, a.table_positions);
+  r.cut = r.len < len;
+  return true;
+}
+
+// The keys that some token in [t0, t1] of the request sees.
+__device__ __forceinline__ Keys keys_of(const PerHeadAttentionArgs& a, const Request& r, int32_t t0, int32_t t1) {
+  Keys k;
+  if (a.tree_mask != nullptr) {
+    k.lo = k.sinks = 0;
+    k.hi = r.len;
+  } else {
+    const int64_t p0 = r.first_pos + t0, p1 = r.first_pos + t1;
+    k.hi = static_cast<int32_t>(min(static_cast<int64_t>(r.len), max(int64_t{0}, p1 + 1)));
+    k.lo = a.window > 0 ? static_cast<int32_t>(min(static_cast<int64_t>(k.hi), max(int64_t{0}, p0 - a.window + 1))) : 0;
+    k.sinks = min(a.num_sinks, k.lo);
+  }
+  k.sink_steps = (k.sinks + kStep - 1) / kStep;
+  k.steps = k.sink_steps + (k.hi - k.lo + kStep - 1) / kStep;
+  return k;
+}
+
+template <int D, int kRowTiles>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 4)
+    per_head_attention_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
+  using St = Stage<D>;
+  constexpr int kRows = 8 * kRowTiles;
+  constexpr int kKSteps = D / 16;                // 16-dimension steps of K Q^T
+  constexpr int kDimTiles = D / 16;              // 16-dimension tiles of V^T P^T
+  // (key head, row block, range); heads vary fastest, so that the heads of a
+  // token, neighbours in an NHD page, are read at about the same time
+  const uint32_t head = blockIdx.x % a.num_kv_heads, rest = blockIdx.x / a.num_kv_heads;
+  const int32_t rb = rest % row_blocks, split = rest / row_blocks;
+  const int b = blockIdx.y;
+  Request rq;
+  if (!request_of(a, b, rq)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
+    return;
+  }
+  const int64_t total_rows = static_cast<int64_t>(rq.tokens) * a.group;
+  const int64_t row0 = static_cast<int64_t>(rb) * kRows;
+  if (row0 >= total_rows) return;
+  const int32_t rows = static_cast<int32_t>(min(static_cast<int64_t>(kRows), total_rows - row0));
+  const int32_t t0 = a.group_div.div(static_cast<uint32_t>(row0));
+  const int32_t t1 = a.group_div.div(static_cast<uint32_t>(row0 + rows - 1));
+  const Keys keys = keys_of(a, rq, t0, t1);
+  int32_t s0 = 0, s1 = keys.steps;
+  if (a.num_splits > 1) {
+    const int64_t per = a.split_keys / kStep;
+    s0 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), split * per));
+    if (split < a.num_splits - 1) s1 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), (split + 1) * per));
+  }
+
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * St::kBytes);
+
+  // ---- asynchronous copies of one step ------------------------------------
+  bool bad_index = rq.cut && threadIdx.x == 0;
+  uint32_t valid_ring[kStages];                  // per stage: bit i = key i of the step exists
+  auto issue = [&](int32_t step, int stage) -> uint32_t {
+    const int32_t base = keys.base(step), limit = keys.limit(step);
+    const int32_t p = base + lane;
+    int32_t page = -1, row = 0;
+    if (p < limit) {
+      const uint32_t col = a.block_div.div(static_cast<uint32_t>(p));
+      if (col < static_cast<uint32_t>(a.block_table_width))
+        page = __ldg(a.block_table + b * a.block_table_stride + col);
+      if (page < 0 || page >= a.num_pages) {
+        page = -1;
+        bad_index = true;
+      }
+      row = static_cast<int32_t>(p - col * static_cast<uint32_t>(a.block_size)) * a.row_offset +
+            static_cast<int32_t>(head) * a.row_head;
+    }
+    const uint32_t st = ring + stage * St::kBytes;
+    constexpr int kLanes = St::kRow / 16;        // lanes that copy one data row
+#pragma unroll
+    for (int it = 0; it < kLanes; ++it) {
+      const int key = it * (32 / kLanes) + lane / kLanes;
+      const uint32_t chunk = lane % kLanes;
+      const int32_t pg = __shfl_sync(kFull, page, key), rw = __shfl_sync(kFull, row, key);
+      const uint8_t* src = a.cache;
+      if (pg >= 0) src += static_cast<int64_t>(pg) * 2 * a.region + static_cast<int64_t>(rw) * St::kRow + 16 * chunk;
+      const uint32_t n = pg >= 0 ? 16 : 0;
+      cp_async<16>(st + key * St::kRow + 16 * k_chunk<D>(key, chunk), src, n);
+      cp_async<16>(st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk), pg >= 0 ? src + a.region : src, n);
+    }
+    const uint8_t* src = a.cache;
+    if (page >= 0) src += static_cast<int64_t>(page) * 2 * a.region + a.scales + static_cast<int64_t>(row) * St::kScales;
+    const uint32_t n = page >= 0 ? St::kScales : 0;
+    cp_async<St::kScales>(st + St::kKs + lane * St::kScales, src, n);
+    cp_async<St::kScales>(st + St::kVs + lane * St::kScales, page >= 0 ? src + a.region : src, n);
+    return __ballot_sync(kFull, page >= 0);
+  };
+  // this warp's steps: first, first + kWarps, ...
+  const int32_t first = s0 + warp;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    valid_ring[i] = first + i * kWarps < s1 ? issue(first + i * kWarps, i) : 0;
+    cp_commit();
+  }
+
+  // ---- the query rows ------------------------------------------------------
+  // Lane (g, c) holds dimensions [c D/4, +D/4) of row 8 nt + g, scaled by a
+  // power of two; the score of row 2c + x is multiplied back by sc.
+  uint32_t q[kRowTiles][kKSteps][2];
+  float sc[kRowTiles][2];
+  int32_t pos_hi[kRowTiles][2], pos_lo[kRowTiles][2];     // window: last visible key, first inside the window
+  int64_t q_token[kRowTiles][2];                          // tree: the row's token
+  const float scale = a.scale_log2 * __ldg(a.k_scale);
+#pragma unroll
+  for (int nt = 0; nt < kRowTiles; ++nt) {
+    const int32_t r = 8 * nt + g;
+    float amax = 0.0f;
+    uint4 w[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const uint32_t flat = static_cast<uint32_t>(row0 + r), tk = a.group_div.div(flat);
+      const int32_t h = head * a.group + (flat - tk * a.group);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                        (rq.token0 + tk) * a.q_stride_t + h * a.q_stride_h + c * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        w[i] = __ldg(src + i);
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+    // largest value -> [2^14, 2^15); zero, infinite and subnormal rows as they are
+    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+    const int shift = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+    // 2^shift in two factors, each a normal number
+    const int sh0 = shift / 2, sh1 = shift - sh0;
+    const float f0 = __uint_as_float(static_cast<uint32_t>(127 + sh0) << 23);
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + sh1) << 23);
+    const float i0 = __uint_as_float(static_cast<uint32_t>(127 - sh0) << 23);
+    const float i1 = __uint_as_float(static_cast<uint32_t>(127 - sh1) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[nt][2 * i + (j >> 1)][j & 1] = pack_f16x2(bf16_lo(x[j]) * f0 * f1, bf16_hi(x[j]) * f0 * f1);
+    }
+    const float row_scale = scale * i0 * i1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      // row 2c + x of the tile is loaded by the lanes with g = 2c + x
+      sc[nt][x] = __shfl_sync(kFull, row_scale, (2 * c + x) * 4);
+      const int32_t rr = 8 * nt + 2 * c + x;
+      const uint32_t tk = a.group_div.div(static_cast<uint32_t>(row0 + min(rr, rows - 1)));
+      const int64_t p = rq.first_pos + tk;
+      pos_hi[nt][x] = rr < rows ? static_cast<int32_t>(max(int64_t{-1}, p)) : -1;
+      pos_lo[nt][x] = a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, p - a.window + 1)) : 0;
+      q_token[nt][x] = rq.token0 + tk;
+    }
+  }
+  // a step inside these positions is visible to every row
+  const int32_t all_hi = static_cast<int32_t>(max(int64_t{-1}, rq.first_pos + (a.tree_mask ? -1 : t0)));
+  const int32_t all_lo =
+      a.tree_mask == nullptr && a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, rq.first_pos + t1 - a.window + 1)) : 0;
+
+  float m[kRowTiles][2], l[kRowTiles][2];
+  float o[kDimTiles][kRowTiles][4];
+#pragma unroll
+  for (int nt = 0; nt < kRowTiles; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kDimTiles; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
+  }
+
+  const uint32_t rg = key_row(g), r0 = key_row(2 * c), r1 = key_row(2 * c + 1);
+  int stage = 0;
+  for (int32_t step = first; step < s1; step += kWarps) {
+    cp_wait<kStages - 2>();
+    __syncwarp();                                // the step has landed, and the stage before it has been read
+    const uint32_t valid = valid_ring[0];
+    valid_ring[0] = valid_ring[1];
+    {
+      const int32_t ahead = step + (kStages - 1) * kWarps;
+      const int st = stage == 0 ? kStages - 1 : stage - 1;
+      valid_ring[1] = ahead < s1 ? issue(ahead, st) : 0;
+      cp_commit();
+    }
+    const uint32_t st = ring + stage * St::kBytes;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    static_assert(kStages == 3, "two steps in flight");
+
+    // ---- S^T = K Q^T -------------------------------------------------------
+    float s[2][kRowTiles][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < kRowTiles; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
+      const uint32_t ra = 16 * mt + rg, rb2 = ra + 8;
+      const uint32_t ka = st + ra * St::kRow, kb = st + rb2 * St::kRow;
+      // the lane's D / 64 scales of each row
+      uint32_t sa, sb;
+      if constexpr (D == 64) {
+        sa = lds8(st + St::kKs + ra * 4 + c) * 0x0101u;
+        sb = lds8(st + St::kKs + rb2 * 4 + c) * 0x0101u;
+      } else if constexpr (D == 128) {
+        sa = lds16(st + St::kKs + ra * 8 + 2 * c);
+        sb = lds16(st + St::kKs + rb2 * 8 + 2 * c);
+      } else {
+        sa = lds32(st + St::kKs + ra * 16 + 4 * c);
+        sb = lds32(st + St::kKs + rb2 * 16 + 4 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i) {       // 32 dimensions (16 at D = 64) at a time
+        uint32_t wa[4], wb[4];
+        if constexpr (D == 64) {
+          const uint2 x = lds64(ka + 8 * c), y = lds64(kb + 8 * c);
+          wa[0] = x.x; wa[1] = x.y; wb[0] = y.x; wb[1] = y.y;
+        } else {
+          const uint32_t chunk = D == 256 ? 2 * c + i : c;
+          const uint4 x = lds128(ka + 16 * k_chunk<D>(ra, chunk)), y = lds128(kb + 16 * k_chunk<D>(rb2, chunk));
+          wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
+          wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+        }
+        const uint32_t fa = bits(e4m3x2_to_half2(sa >> (16 * i))), fb = bits(e4m3x2_to_half2(sb >> (16 * i)));
+#pragma unroll
+        for (int j = 0; j < (D == 64 ? 2 : 4); ++j) {   // 8 dimensions: two 16-wide product steps
+          const uint32_t sel = (j >> 1) && D != 64 ? 0x3232 : 0x1010;
+          const uint32_t sfa = prmt(fa, fa, sel), sfb = prmt(fb, fb, sel);
+          uint32_t ha[4], hb[4];
+          e2m1x8(wa[j], ha);
+          e2m1x8(wb[j], hb);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t a0 = hmul2(ha[2 * e], sfa), a1 = hmul2(hb[2 * e], sfb);
+            const uint32_t a2 = hmul2(ha[2 * e + 1], sfa), a3 = hmul2(hb[2 * e + 1], sfb);
+            const int ks = (D == 64 ? 2 : 4) * 2 * i + 2 * j + e;
+#pragma unroll
+            for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(s[mt][nt], a0, a1, a2, a3, q[nt][ks][0], q[nt][ks][1]);
+          }
+        }
+      }
+    }
+
+    // ---- weights -----------------------------------------------------------
+    // s[mt][nt][2 y + x]: key 16 mt + 8 y + key_row(g), query row 8 nt + 2 c + x
+    const int32_t base = keys.base(step);
+    const bool all = valid == kFull && base + kStep - 1 <= all_hi && (base >= all_lo || base + kStep <= a.num_sinks);
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < kRowTiles; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float& v = s[mt][nt][2 * y + x];
+            v *= sc[nt][x];
+            if (!all) {
+              const int32_t i = 16 * mt + 8 * y + rg, p = base + i;
+              bool see = (valid >> i) & 1;
+              if (a.tree_mask == nullptr) {
+                see = see && p <= pos_hi[nt][x] && (p >= pos_lo[nt][x] || p < a.num_sinks);
+              } else if (see && p >= rq.first_pos) {
+                const int32_t d = static_cast<int32_t>(p - rq.first_pos);
+                see = (d >> 6) < a.tree_words &&
+                      ((__ldg(a.tree_mask + q_token[nt][x] * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
+              }
+              if (!see) v = -INFINITY;
+            }
+            top = fmaxf(top, v);
+          }
+        grow |= top > m[nt][x] + kGrow;
+      }
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < kRowTiles; ++nt) {
+        float alpha[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float top = fmaxf(fmaxf(s[0][nt][x], s[0][nt][2 + x]), fmaxf(s[1][nt][x], s[1][nt][2 + x]));
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+          alpha[x] = 1.0f;
+          if (top > m[nt][x]) {
+            alpha[x] = ex2(m[nt][x] - top);      // 0 while m is -inf
+            m[nt][x] = top;
+          }
+          l[nt][x] *= alpha[x];
+        }
+#pragma unroll
+        for (int t = 0; t < kDimTiles; ++t) {
+          o[t][nt][0] *= alpha[0];
+          o[t][nt][1] *= alpha[1];
+          o[t][nt][2] *= alpha[0];
+          o[t][nt][3] *= alpha[1];
+        }
+      }
+    }
+    uint32_t p[2][kRowTiles][2];                 // P^T, keys 2c, 2c + 1 and 8 on, of query row g
+#pragma unroll
+    for (int nt = 0; nt < kRowTiles; ++nt) {
+      const float off0 = kShift - (m[nt][0] == -INFINITY ? 0.0f : m[nt][0]);
+      const float off1 = kShift - (m[nt][1] == -INFINITY ? 0.0f : m[nt][1]);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float w0 = ex2(s[mt][nt][2 * y] + off0), w1 = ex2(s[mt][nt][2 * y + 1] + off1);
+          l[nt][0] += w0;
+          l[nt][1] += w1;
+          p[mt][nt][y] = transpose8(pack_f16x2(w0, w1));
+        }
+    }
+
+    // ---- O^T += V^T P^T ----------------------------------------------------
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      // keys 2c and 2c + 1 (rows x0, x1) and the two 8 keys on (y0, y1)
+      const uint32_t x0 = 16 * mt + r0, x1 = 16 * mt + r1, y0 = x0 + 8, y1 = x1 + 8;
+      const uint32_t vs = st + St::kVs, vd = st + St::kV;
+#pragma unroll
+      for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {    // one scale group (16 dimensions; 8 at D = 64) at a time
+        const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
+        uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
+        uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
+        // A NaN scale (no write of finite values makes one) reads as zero, so
+        // that a hidden entry that was never written cannot reach any row.
+        sx &= __heq2_mask(half2_of(sx), half2_of(sx));
+        sy &= __heq2_mask(half2_of(sy), half2_of(sy));
+        uint32_t w[4][2];
+        auto load = [&](uint32_t row, uint32_t (&d)[2]) {
+          if constexpr (D == 64) {
+            d[0] = lds32(vd + row * St::kRow + 4 * g);
+          } else {
+            const uint32_t at = D == 128 ? 8 * g : 16 * g + 8 * i;
+            const uint2 x = lds64(vd + row * St::kRow + 16 * v_chunk<D>(row, at >> 4) + (at & 8));
+            d[0] = x.x;
+            d[1] = x.y;
+          }
+        };
+        load(x0, w[0]);
+        load(x1, w[1]);
+        load(y0, w[2]);
+        load(y1, w[3]);
+#pragma unroll
+        for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {   // 8 dimensions
+          // bytes holding (first key's, second key's) codes of the even and odd dimensions
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t ex[4], od[4], ey[4], oy[4];
+          e2m1x8((w[0][j] & kLow) | ((w[1][j] << 4) & ~kLow), ex);
+          e2m1x8(((w[0][j] >> 4) & kLow) | (w[1][j] & ~kLow), od);
+          e2m1x8((w[2][j] & kLow) | ((w[3][j] << 4) & ~kLow), ey);
+          e2m1x8(((w[2][j] >> 4) & kLow) | (w[3][j] & ~kLow), oy);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {          // dimensions 2 e and 2 e + 1 of the eight
+            const uint32_t a0 = hmul2(ex[e], sx), a1 = hmul2(od[e], sx), a2 = hmul2(ey[e], sy), a3 = hmul2(oy[e], sy);
+            const int t = (D == 64 ? 0 : 8 * i + 4 * j) + e;
+#pragma unroll
+            for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+          }
+        }
+      }
+    }
+  }
+  if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
+
+  // ---- join the four warps -------------------------------------------------
+  cp_wait<0>();
+  __syncthreads();                               // every ring is idle
+  float* jo = reinterpret_cast<float*>(smem);    // [kWarps][kRows][D]
+  __shared__ float jm[kWarps][kRows], jl[kWarps][kRows];
+#pragma unroll
+  for (int nt = 0; nt < kRowTiles; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float sum = l[nt][x];
+      sum += __shfl_xor_sync(kFull, sum, 4);
+      sum += __shfl_xor_sync(kFull, sum, 8);
+      sum += __shfl_xor_sync(kFull, sum, 16);
+      const int r = 8 * nt + 2 * c + x;
+      if (g == 0) {
+        jm[warp][r] = m[nt][x];
+        jl[warp][r] = sum;
+      }
+      // dimensions [g D/8, +D/8): two per tile
+      float* dst = jo + (warp * kRows + r) * D + g * (D / 8);
+#pragma unroll
+      for (int t = 0; t < kDimTiles; ++t)
+        *reinterpret_cast<float2*>(dst + 2 * t) = make_float2(o[t][nt][x], o[t][nt][2 + x]);
+    }
+  __syncthreads();
+  const float v_scale = __ldg(a.v_scale);
+  for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
+    const int r = i / (D / 8), d = (i % (D / 8)) * 8;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, jm[w][r]);
+    float sum = 0.0f, acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      // a warp that saw nothing holds zeros
+      const float f = jm[w][r] == -INFINITY ? 1.0f : ex2(jm[w][r] - top);
+      sum += f * jl[w][r];
+      const float4* src = reinterpret_cast<const float4*>(jo + (w * kRows + r) * D + d);
+      const float4 u = src[0], v = src[1];
+      acc[0] += f * u.x; acc[1] += f * u.y; acc[2] += f * u.z; acc[3] += f * u.w;
+      acc[4] += f * v.x; acc[5] += f * v.y; acc[6] += f * v.z; acc[7] += f * v.w;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float lse2 = sum == 0.0f ? -INFINITY : top + (log2f(sum) - kShift);
+    const uint32_t flat = static_cast<uint32_t>(row0 + r), tk = a.group_div.div(flat);
+    const int64_t token = rq.token0 + tk;
+    const int32_t h = head * a.group + (flat - tk * a.group);
+    if (a.num_splits > 1) {
+      const int64_t pr = (token * a.num_heads + h) * a.num_splits + split;
+      float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + d);
+      dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+      dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
+      if (d == 0) a.part_lse[pr] = lse2;
+    } else {
+      const float f = inv * v_scale;
+      st16(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t + h * a.out_stride_h + d,
+           make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                      pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f)));
+      if (d == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = lse2 * kLn2;
+    }
+  }
+}
+
+// Joins the ranges of every row: with L_s the base-2 log-sum-exp of range s
+// and o_s its normalised output, out = sum 2^(L_s - M) o_s / sum 2^(L_s - M).
+// One warp per (token, head) row of a live request; a range that saw nothing
+// (-inf) weighs nothing.
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) per_head_join_kernel(const PerHeadAttentionArgs a) {
+  const int64_t flat = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, b = blockIdx.y;
+  Request rq;
+  if (!request_of(a, b, rq) || flat >= static_cast<int64_t>(rq.tokens) * a.num_heads) return;
+  const int64_t row = rq.token0 * a.num_heads + flat;
+  const float* ls = a.part_lse + row * a.num_splits;
+  float top = -INFINITY;
+  for (int s = lane; s < a.num_splits; s += 32) top = fmaxf(top, ls[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  constexpr int kDims = D / 32;                          // per lane
+  float acc[kDims], den = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kDims; ++i) acc[i] = 0.0f;
+  const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
+  for (int s = 0; s < a.num_splits; ++s) {
+    const float w = ls[s] == -INFINITY ? 0.0f : ex2(ls[s] - top);
+    if (w == 0.0f) continue;                             // uniform over the warp
+    den += w;
+#pragma unroll
+    for (int i = 0; i < kDims; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(s) * D + i);
+      acc[i] += w * v.x;
+      acc[i + 1] += w * v.y;
+    }
+  }
+  const float f = (den == 0.0f ? 0.0f : 1.0f / den) * __ldg(a.v_scale);
+  const int64_t token = row / a.num_heads, h = row - token * a.num_heads;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
+                                              h * a.out_stride_h + kDims * lane);
+#pragma unroll
+  for (int i = 0; i < kDims; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+  if (lane == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
+}
+
+template <int D, int kRowTiles>
+cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = kWarps * kStages * Stage<D>::kBytes;
+  static_assert(kSmem >= kWarps * 8 * kRowTiles * D * 4, "the joined rows fit the rings");
+  cudaError_t e = cudaFuncSetAttribute(per_head_attention_kernel<D, kRowTiles>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
+  const int64_t blocks = (rows + 8 * kRowTiles - 1) / (8 * kRowTiles);
+  const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
+  per_head_attention_kernel<D, kRowTiles><<<grid, kThreads, kSmem, stream>>>(a, static_cast<int32_t>(blocks));
+  if ((e = cudaGetLastError()) != cudaSuccess || a.num_splits == 1) return e;
+  const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
+  per_head_join_kernel<D><<<dim3(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps),
+                                 static_cast<unsigned>(a.batch_size)), kJoinWarps * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream) {
+  const bool one_tile = static_cast<int64_t>(a.max_query_len) * a.group <= 8;
+  switch (a.head_size) {
+    case 64: return one_tile ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
+    case 128: return one_tile ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
+    default: return launch_rows<256, 1>(a, stream);      // two tiles would not fit the registers
+  }
+}
+
+}  // namespace kvq

@@ -537,6 +537,170 @@ kvq_status kvq_req_index_to_global_slot(
     int32_t* out, int64_t out_stride,
     int32_t* d_status, kvq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving a model from the per-head NVFP4 cache: what runs before its write
+ * (kvq_qk_norm_rope), the attention that reads it (window and tree), and the
+ * move of accepted drafts inside it.  The cache is the one that
+ * kvq_reshape_and_cache_nvfp4 writes ([P2] "Implementation breakdown" item 4
+ * and "Key source snippets"; its decode consumer is what [P2] leaves
+ * unimplemented); its entry of (position, head, side) stands for
+ * (e2m1 * sf) * scale.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kvq_qk_norm_rope -- RMS norm of each query and key head and the rotation by
+ * its token's position, in one pass.  For a head x with its side's weight w:
+ *   y_d = x_d * w_d / sqrt(sum_i x_i^2 / head_size + eps)
+ *   pair j < rot_dim / 2 of y, (a, b) at dimensions (j, j + rot_dim / 2), or
+ *   (2j, 2j + 1) when `interleaved`, becomes (a c - b s, b c + a s) with
+ *   c = cos_sin[p][j], s = cos_sin[p][rot_dim / 2 + j], p = positions[token];
+ * dimensions from rot_dim on are normalised only.  fp32 throughout, rounded
+ * once to bf16.  A token whose position is outside [0, max_position) is
+ * skipped (nothing written, KVQ_STATUS_BAD_INDEX).
+ * q, q_out: bf16 [num_tokens, num_heads, head_size], k, k_out: bf16
+ * [num_tokens, num_kv_heads, head_size]; token and head strides in elements
+ * (multiples of 8).  An output may be its input (same pointer and strides);
+ * any other overlap of outputs with inputs is not allowed.  head_size: a
+ * multiple of 16 in [16, 256]; rot_dim: a multiple of 16 in [0, head_size].
+ * q_weight, k_weight: bf16 [head_size], 16-byte aligned.  positions: int64
+ * [num_tokens].  cos_sin: fp32 [max_position, >= rot_dim], 16-byte aligned,
+ * row stride a multiple of 4.
+ */
+kvq_status kvq_qk_norm_rope(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* q_weight, const void* k_weight,
+    const int64_t* positions, int64_t num_tokens,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+    const float* cos_sin, int64_t cos_sin_stride, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+    float eps,
+    void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+    void* k_out, int64_t k_out_stride_t, int64_t k_out_stride_h,
+    int32_t* d_status, kvq_stream_t stream);
+
+#define KVQ_PER_HEAD_MAX_SPLITS 128    /* key ranges of the per-head attention */
+
+/*
+ * kvq_per_head_attention_workspace_bytes -- bytes of workspace that the two
+ * attention entry points below need with num_splits > 1: num_tokens *
+ * num_heads * num_splits * (head_size + 1) * 4, rounded up to 16.  -1 for a
+ * non-positive argument or a size past INT64_MAX / 2.
+ */
+int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_size,
+                                               int32_t num_splits);
+
+/*
+ * kvq_window_attention_nvfp4_per_head -- causal attention over the per-head
+ * NVFP4 cache with a sliding window and a few first tokens that stay visible.
+ * Request b < batch_size owns the query tokens [query_start[b],
+ * query_start[b+1]) (n of them, at most max_query_len), which are the last n
+ * positions of its sequence of seq_lens[b] entries (their own keys and values
+ * are in the cache already): query i has position p = seq_lens[b] - n + i and
+ * sees key j iff j <= p and (window <= 0 or j > p - window or j < num_sinks).
+ * For head h, with key head h / (num_heads / num_kv_heads):
+ *   s_j = softmax_scale * k_scale * (q . K_j)      K_j, V_j = e2m1 * sf, exact
+ *   out = v_scale * sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
+ *   lse = m + ln(sum_j exp(s_j - m)),   m = max_j s_j
+ * A query that sees nothing (a negative position: a padded request of length
+ * 0) gets out = 0 and lse = -inf.  Position j is entry j % block_size of page
+ * block_table[b * block_table_stride + j / block_size]; one whose column is
+ * >= block_table_width or whose page is outside [0, num_pages) is skipped
+ * (KVQ_STATUS_BAD_INDEX).  A request whose query range is not inside [0,
+ * num_tokens) or is longer than max_query_len is skipped, its rows untouched
+ * (KVQ_STATUS_BAD_BATCH), as are rows of no request.
+ * Entries that no query of a tile may see have no effect, whatever they hold.
+ * A NaN scale byte in a visible key makes its rows NaN; in a visible value
+ * group it reads as zero.  (No write of finite values stores one.)
+ * Arithmetic: products on the tensor cores with fp32 sums (entries exact in
+ * f16; a query row is scaled by a power of two into f16, exact down to 2^-28
+ * of its largest value); the softmax in fp32; the weights rounded to f16
+ * (relative 2^-11) for the weighted sum; out rounded once to bf16.
+ * q: bf16 [num_tokens, num_heads, head_size] with token and head strides in
+ * elements (multiples of 8); head_size 64, 128 or 256; num_heads a multiple
+ * of num_kv_heads.  out: the same shape, rows not overlapping.  lse: fp32
+ * [num_tokens, num_heads], token stride lse_stride_t, or NULL.  kv_cache,
+ * layout, k_scale, v_scale: as kvq_reshape_and_cache_nvfp4, and block_size *
+ * num_kv_heads * full_dim a multiple of 16 and block_table_width * block_size
+ * below 2^31 - 64.  query_start: int32 [batch_size + 1]; seq_lens: int32
+ * [batch_size]; batch_size <= 65535.
+ * num_splits: key ranges per block of query rows (1 ..
+ * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU;
+ * above 1, the ranges (sized from max_seq_len, which bounds seq_lens; a longer
+ * sequence is attended in full all the same, its last range taking the rest)
+ * write partial results to `workspace` (16-byte aligned,
+ * kvq_per_head_attention_workspace_bytes; overwritten, no other call may use
+ * it while this one runs) and a second launch joins them.
+ */
+kvq_status kvq_window_attention_nvfp4_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    const uint8_t* kv_cache, int64_t num_pages, int32_t block_size, int32_t layout,
+    int32_t num_kv_heads, int32_t head_size,
+    const float* k_scale, const float* v_scale,
+    float softmax_scale, int32_t window, int32_t num_sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* lse, int64_t lse_stride_t,
+    int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes,
+    int32_t* d_status, kvq_stream_t stream);
+
+/*
+ * kvq_tree_attention_nvfp4_per_head -- attention of drafted tokens that form
+ * a tree, over the per-head NVFP4 cache.  Request b's n query tokens are its
+ * drafts, the last n entries of its sequence of seq_lens[b]: draft i sees
+ * every position before the drafts (j < seq_lens[b] - n) and draft j, at
+ * position seq_lens[b] - n + j, iff bit j % 64 of word j / 64 of its mask row
+ * is set (its own bit included: a draft whose mask leaves itself out does not
+ * see itself).  Everything else is as in kvq_window_attention_nvfp4_per_head.
+ * tree_mask: 64-bit words [num_tokens, mask_words], row stride
+ * tree_mask_stride words, 64 * mask_words >= max_query_len.
+ */
+kvq_status kvq_tree_attention_nvfp4_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const uint64_t* tree_mask, int64_t tree_mask_stride, int32_t mask_words,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    const uint8_t* kv_cache, int64_t num_pages, int32_t block_size, int32_t layout,
+    int32_t num_kv_heads, int32_t head_size,
+    const float* k_scale, const float* v_scale,
+    float softmax_scale,
+    void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* lse, int64_t lse_stride_t,
+    int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes,
+    int32_t* d_status, kvq_stream_t stream);
+
+/*
+ * kvq_compact_drafts_nvfp4_per_head -- after a tree of drafts was checked,
+ * moves the accepted ones' entries to consecutive positions, in every layer.
+ * Request b's drafts are the last n = query_start[b+1] - query_start[b]
+ * entries of its sequence of seq_lens[b], base = seq_lens[b] - n their first
+ * position; with a_i = accepted[b * accepted_stride + i], the entry (K and V,
+ * data and scales, all heads) of position base + a_i is copied to position
+ * base + i, for i < accepted_lens[b].  The a_i are draft numbers in [0, n),
+ * strictly increasing; a request whose list is not so (or whose length is
+ * outside [0, max_accepted]) is left as it is (KVQ_STATUS_BAD_INDEX), as is
+ * one with n < 0 or n > seq_lens[b] (KVQ_STATUS_BAD_BATCH).  A position whose
+ * block-table column or page is out of range is skipped
+ * (KVQ_STATUS_BAD_INDEX).  The drafts' positions of different requests are
+ * different entries (shared pages hold no drafts); other entries are never
+ * touched.  seq_lens itself is the caller's to update (base + accepted_lens).
+ * kv_cache: num_layers caches laid out as kvq_reshape_and_cache_nvfp4's,
+ * layer_stride bytes apart (a multiple of 16; ignored for one layer), all
+ * addressed by the same block_table int32 [batch_size, >=
+ * block_table_width].  head_size: a multiple of 16 up to 1024.  accepted:
+ * int32 [batch_size, >= max_accepted]; accepted_lens: int32 [batch_size].
+ */
+kvq_status kvq_compact_drafts_nvfp4_per_head(
+    uint8_t* kv_cache, int32_t num_layers, int64_t layer_stride,
+    int64_t num_pages, int32_t block_size, int32_t layout,
+    int32_t num_kv_heads, int32_t head_size,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size,
+    const int32_t* accepted, int64_t accepted_stride, const int32_t* accepted_lens, int32_t max_accepted,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    int32_t* d_status, kvq_stream_t stream);
+
 /*
  * kvq_selftest_convert -- exposes the device number-format converters the
  * kernels above use, for exhaustive testing.  For i < count and f the float
