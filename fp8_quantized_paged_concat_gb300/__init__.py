@@ -572,38 +572,75 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 # --------------------------------------------------------------------------
 # serving from the per-head NVFP4 cache
 # --------------------------------------------------------------------------
+#
+# These calls run once per layer and decoded token, where the host's part of a
+# call can outlast the kernel: their checks build no message unless one fails,
+# and the current stream is asked for without making a Stream object.
 
-def _call_on(device, name: str, *args):
-    """_call with `device` current (the library launches on the current device)."""
-    if device.index == torch.cuda.current_device():
-        _call(name, *args)
+_BF16, _F32, _I32T, _I64T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_sm_count = {}
+
+
+def _sms(device):
+    i = device if isinstance(device, int) else torch.device("cuda" if device is None else device).index
+    if i is None:
+        i = torch.cuda.current_device()
+    if i not in _sm_count:
+        _sm_count[i] = torch.cuda.get_device_properties(i).multi_processor_count
+    return _sm_count[i]
+
+
+def _launch(index, stream, status, name, args):
+    """The library call `name` on device `index` (the library launches on the
+    current one), with the status word and the stream as its last arguments."""
+    if status is not None and (status.dtype is not _I32T or status.get_device() != index or status.numel() < 1):
+        raise ValueError(f"status: expected an int32 tensor on cuda:{index} with at least one element")
+    word = None if status is None else status.data_ptr()
+    if stream is None:
+        raw = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError(f"stream: expected a stream of cuda:{index}, the tensors' device")
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            _call(name, *args)
+        raw = int(stream)
+    if torch.cuda.current_device() == index:
+        _call(name, *args, word, raw)
+    else:
+        with torch.cuda.device(index):
+            _call(name, *args, word, raw)
 
 
-def _one_device(device, **tensors):
-    for name, t in tensors.items():
-        _need(t.device == device, f"{name}: expected a tensor on {device}, got {t.device}")
+def _tensor(name, t, dtype, index, dims):
+    """A tensor of that type and rank on device `index`, its innermost stride 1."""
+    if (t.dtype is not dtype or t.get_device() != index or t.dim() != dims
+            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        raise ValueError(f"{name}: expected a CUDA {dtype} tensor of rank {dims} with unit inner stride on "
+                         f"cuda:{index}, got {t.dtype} of shape {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
-def _stream_on(stream, device) -> int:
-    _need(not isinstance(stream, torch.cuda.Stream) or stream.device == device,
-          "stream: not a stream of the tensors' device")
-    return _stream(stream, device)
+def _shaped(name, t, shape):
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _heads(name, t, shape=None):
-    _need(t.dtype == torch.bfloat16 and t.is_cuda and t.dim() == 3 and t.stride(2) == 1
-          and (shape is None or tuple(t.shape) == shape),
-          f"{name}: expected a CUDA bf16 {list(shape) if shape else '[T, H, D]'} tensor with unit inner stride")
+def _first(name, t):
+    """The device that the other tensors of the call have to be on: that of bf16 [T, H, D] heads."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    _tensor(name, t, _BF16, index, 3)
+    return index
 
 
-def _rows_stride(t):
+def _heads_strides(t):
     """Token and head strides for the library (a dimension of one element may carry any stride)."""
     T, H, D = t.shape
-    sh = t.stride(1) if H > 1 else max(D, 8)
-    return (t.stride(0) if T > 1 else H * sh), sh
+    st, sh, _ = t.stride()
+    if H <= 1:
+        sh = D
+    return (st if T > 1 else H * sh), sh
 
 
 def _row_stride(t):
@@ -611,9 +648,23 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _int32_vector(name, t, n):
-    _need(t.dtype == torch.int32 and t.is_cuda and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-          f"{name}: expected a contiguous CUDA int32 vector of {n}")
+def _scale_ptr(name, t, index):
+    if t.dtype is not _F32 or t.get_device() != index or t.numel() < 1:
+        raise ValueError(f"{name}: expected an fp32 scalar on cuda:{index}")
+    return t.data_ptr()
+
+
+def _cache_shape(kv_cache, head_size, layout, index):
+    """(layout code, block_size, heads) of a contiguous per-head cache; head_size None: from the cache."""
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
+    _tensor("kv_cache", kv_cache, _U8, index, 5)
+    _, sides, a, b, full = kv_cache.shape
+    if sides != 2 or not kv_cache.is_contiguous() or full % 9 or (head_size is not None and full * 16 != head_size * 9):
+        inner = "block_size, H" if layout == "NHD" else "H, block_size"
+        raise ValueError(f"kv_cache: expected a contiguous [P, 2, {inner}, D/2 + D/16] tensor for layout {layout}"
+                         f"{'' if head_size is None else f' with D = {head_size}'}, got {tuple(kv_cache.shape)}")
+    return (0, a, b) if layout == "NHD" else (1, b, a)
 
 
 def kvq_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float, interleaved=False, q_out=None,
@@ -625,47 +676,39 @@ def kvq_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float, i
     (rot_dim / 2 cosines, then sines; rot_dim a multiple of 16, at most D).
     Pairs are (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.  q_out /
     k_out may be q / k.  Returns (q_out, k_out)."""
-    _heads("q", q)
+    index = _first("q", q)
     T, H, D = q.shape
-    _heads("k", k)
-    _need(k.shape[0] == T and k.shape[2] == D, "q and k differ in tokens or head size")
+    _tensor("k", k, _BF16, index, 3)
+    KH = k.shape[1]
+    _shaped("k", k, (T, KH, D))
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _need(w.dtype == torch.bfloat16 and w.is_cuda and tuple(w.shape) == (D,) and w.is_contiguous(),
-              f"{name}: expected a contiguous CUDA bf16 [{D}] vector")
-    _need(positions.dtype == torch.int64 and positions.is_cuda and tuple(positions.shape) == (T,)
-          and positions.is_contiguous(), "positions: expected a contiguous CUDA int64 [T]")
-    _need(cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.dim() == 2
-          and (cos_sin.stride(1) == 1 or cos_sin.shape[1] <= 1),
-          "cos_sin: expected a CUDA fp32 [max_position, rot_dim] tensor with unit inner stride")
+        _tensor(name, w, _BF16, index, 1)
+        _shaped(name, w, (D,))
+    _tensor("positions", positions, _I64T, index, 1)
+    _shaped("positions", positions, (T,))
+    _tensor("cos_sin", cos_sin, _F32, index, 2)
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        q_out = q.new_empty((T, H, D))
+    else:
+        _tensor("q_out", q_out, _BF16, index, 3)
+        _shaped("q_out", q_out, q.shape)
     if k_out is None:
-        k_out = torch.empty((T, k.shape[1], D), dtype=torch.bfloat16, device=q.device)
-    _heads("q_out", q_out, (T, H, D))
-    _heads("k_out", k_out, (T, k.shape[1], D))
-    _one_device(q.device, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, cos_sin=cos_sin, q_out=q_out,
-                k_out=k_out)
-    _call_on(q.device, "kvq_qk_norm_rope", q.data_ptr(), *_rows_stride(q), k.data_ptr(), *_rows_stride(k),
-             q_weight.data_ptr(), k_weight.data_ptr(), positions.data_ptr(), T, H, k.shape[1], D, cos_sin.data_ptr(),
-             _row_stride(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-             float(eps), q_out.data_ptr(), *_rows_stride(q_out), k_out.data_ptr(), *_rows_stride(k_out),
-             _status_ptr(status), _stream_on(stream, q.device))
+        k_out = k.new_empty((T, KH, D))
+    else:
+        _tensor("k_out", k_out, _BF16, index, 3)
+        _shaped("k_out", k_out, k.shape)
+    max_position, rot = cos_sin.shape
+    _launch(index, stream, status, "kvq_qk_norm_rope",
+            (q.data_ptr(), *_heads_strides(q), k.data_ptr(), *_heads_strides(k), q_weight.data_ptr(),
+             k_weight.data_ptr(), positions.data_ptr(), T, H, KH, D, cos_sin.data_ptr(), _row_stride(cos_sin),
+             max_position, rot, 1 if interleaved else 0, eps, q_out.data_ptr(), *_heads_strides(q_out),
+             k_out.data_ptr(), *_heads_strides(k_out)))
     return q_out, k_out
 
 
 def kvq_per_head_attention_workspace_bytes(num_tokens: int, num_heads: int, head_size: int, num_splits: int) -> int:
     """Bytes of workspace the per-head attention needs for num_splits > 1 (-1 for bad arguments)."""
     return load_library().kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits)
-
-
-_sm_count = {}
-
-
-def _sms(device):
-    i = torch.cuda.current_device() if device is None or device.index is None else device.index
-    if i not in _sm_count:
-        _sm_count[i] = torch.cuda.get_device_properties(i).multi_processor_count
-    return _sm_count[i]
 
 
 def default_per_head_num_splits(max_query_len: int, num_heads: int, num_kv_heads: int, batch_size: int,
@@ -695,8 +738,8 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     (allocated here when None).  Returns (out bf16 [T, H, D], lse fp32 [T,
     H]); lse=False skips the lse output."""
     return _per_head_attention("kvq_window_attention_nvfp4_per_head", q, query_start, seq_lens, None, block_table,
-                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, int(window),
-                               int(num_sinks), layout, num_splits, workspace, out, lse, status, stream)
+                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, window,
+                               num_sinks, layout, num_splits, workspace, out, lse, status, stream)
 
 
 def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
@@ -707,9 +750,6 @@ def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block
     context before the drafts and draft j iff bit j % 64 of tree_mask[token
     i, j // 64] (int64 [T, mask_words], 64 * mask_words >= max_query_len) is
     set.  The rest is as in kvq_window_attention_nvfp4_per_head."""
-    _need(tree_mask.dtype == torch.int64 and tree_mask.is_cuda and tree_mask.dim() == 2
-          and tree_mask.shape[0] == q.shape[0] and (tree_mask.shape[1] <= 1 or tree_mask.stride(1) == 1),
-          "tree_mask: expected CUDA int64 [T, mask_words] rows")
     return _per_head_attention("kvq_tree_attention_nvfp4_per_head", q, query_start, seq_lens, tree_mask, block_table,
                                kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, 0, 0, layout,
                                num_splits, workspace, out, lse, status, stream)
@@ -718,55 +758,49 @@ def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block
 def _per_head_attention(cname, q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
                         softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout, num_splits, workspace,
                         out, lse, status, stream):
-    _heads("q", q)
+    index = _first("q", q)
     T, H, D = q.shape
-    _need(layout in LAYOUTS, f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
-    _need(kv_cache.dim() == 5, "kv_cache: expected a [P, 2, ...] tensor")
-    KH = kv_cache.shape[3 if layout == "NHD" else 2]
-    code, block_size = _per_head_cache(kv_cache, KH, D, layout)
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    _int32_vector("seq_lens", seq_lens, B)
-    _int32_vector("query_start", query_start, B + 1)
-    _need(block_table.dtype == torch.int32 and block_table.is_cuda and block_table.dim() == 2
-          and block_table.shape[0] == B and (block_table.shape[1] <= 1 or block_table.stride(1) == 1),
-          "block_table: expected a CUDA int32 [B, W] tensor with unit inner stride")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(t.dtype == torch.float32 and t.is_cuda and t.numel() >= 1, f"{name}: CUDA fp32 scalar")
+    code, block_size, KH = _cache_shape(kv_cache, D, layout, index)
+    _tensor("seq_lens", seq_lens, _I32T, index, 1)
+    B = seq_lens.shape[0]
+    _tensor("query_start", query_start, _I32T, index, 1)
+    _shaped("query_start", query_start, (B + 1,))
+    _tensor("block_table", block_table, _I32T, index, 2)
+    W = block_table.shape[1]
+    _shaped("block_table", block_table, (B, W))
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    _heads("out", out, (T, H, D))
+        out = q.new_empty((T, H, D))
+    else:
+        _tensor("out", out, _BF16, index, 3)
+        _shaped("out", out, q.shape)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    if lse is not False:
-        _need(lse.dtype == torch.float32 and lse.is_cuda and tuple(lse.shape) == (T, H)
-              and (H <= 1 or lse.stride(1) == 1),
-              "lse: expected a CUDA fp32 [T, H] tensor with unit inner stride")
-        _one_device(q.device, lse=lse)
-    _one_device(q.device, query_start=query_start, seq_lens=seq_lens, block_table=block_table, kv_cache=kv_cache,
-                k_scale=k_scale, v_scale=v_scale, out=out)
+        lse = torch.empty((T, H), dtype=_F32, device=q.device)
+    elif lse is not False:
+        _tensor("lse", lse, _F32, index, 2)
+        _shaped("lse", lse, (T, H))
     if num_splits is None:
-        num_splits = 1 if KH == 0 else default_per_head_num_splits(int(max_query_len), H, KH, B, int(max_seq_len),
-                                                                   window, num_sinks, q.device)
-    if num_splits > 1 and workspace is None and T > 0:
-        workspace = torch.empty(kvq_per_head_attention_workspace_bytes(T, H, D, num_splits), dtype=torch.uint8,
-                                device=q.device)
+        num_splits = default_per_head_num_splits(max_query_len, H, KH, B, max_seq_len, window, num_sinks,
+                                                 index) if KH else 1
     if workspace is not None:
-        _need(workspace.is_cuda and workspace.is_contiguous(), "workspace: expected a contiguous CUDA tensor")
-        _one_device(q.device, workspace=workspace)
-    args = [q.data_ptr(), *_rows_stride(q), T, H, query_start.data_ptr(), seq_lens.data_ptr(), B, int(max_query_len)]
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
+    elif num_splits > 1 and T > 0:
+        workspace = torch.empty(max(0, kvq_per_head_attention_workspace_bytes(T, H, D, num_splits)), dtype=_U8,
+                                device=q.device)
+    mask = ()
     if tree_mask is not None:
-        _one_device(q.device, tree_mask=tree_mask)
-        args += [tree_mask.data_ptr(), _row_stride(tree_mask), tree_mask.shape[1]]
-    args += [block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
-             kv_cache.data_ptr(), kv_cache.shape[0], block_size, code, KH, D, k_scale.data_ptr(), v_scale.data_ptr(),
-             float(softmax_scale)]
-    if tree_mask is None:
-        args += [window, num_sinks]
-    args += [out.data_ptr(), *_rows_stride(out), None if lse is False else lse.data_ptr(),
-             0 if lse is False else _row_stride(lse), int(max_seq_len), int(num_splits),
-             None if workspace is None else workspace.data_ptr(),
-             0 if workspace is None else workspace.numel() * workspace.element_size()]
-    _call_on(q.device, cname, *args, _status_ptr(status), _stream_on(stream, q.device))
+        _tensor("tree_mask", tree_mask, _I64T, index, 2)
+        words = tree_mask.shape[1]
+        _shaped("tree_mask", tree_mask, (T, words))
+        mask = (tree_mask.data_ptr(), _row_stride(tree_mask), words)
+    _launch(index, stream, status, cname,
+            (q.data_ptr(), *_heads_strides(q), T, H, query_start.data_ptr(), seq_lens.data_ptr(), B, max_query_len,
+             *mask, block_table.data_ptr(), _row_stride(block_table), W, kv_cache.data_ptr(), kv_cache.shape[0],
+             block_size, code, KH, D, _scale_ptr("k_scale", k_scale, index), _scale_ptr("v_scale", v_scale, index),
+             softmax_scale, *(() if mask else (window, num_sinks)), out.data_ptr(), *_heads_strides(out),
+             None if lse is False else lse.data_ptr(), 0 if lse is False else _row_stride(lse), max_seq_len,
+             num_splits, None if workspace is None else workspace.data_ptr(),
+             0 if workspace is None else workspace.numel() * workspace.element_size()))
     return out, (None if lse is False else lse)
 
 
@@ -779,30 +813,29 @@ def kvq_compact_drafts_nvfp4_per_head(kv_cache, query_start, seq_lens, accepted,
     kv_cache: uint8 [P, 2, ...] as kvq_reshape_and_cache_nvfp4 takes it, or
     [L, P, 2, ...] for L layers that share the block table (each layer
     contiguous).  seq_lens is left to the caller."""
-    _need(layout in LAYOUTS, f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
-    _need(kv_cache.dim() in (5, 6), "kv_cache: expected a [P, 2, ...] or [L, P, 2, ...] tensor")
-    layers = kv_cache.shape[0] if kv_cache.dim() == 6 else 1
-    if layers == 0:
-        return
-    one = kv_cache[0] if kv_cache.dim() == 6 else kv_cache
-    D = one.shape[4] // 9 * 16
-    KH = one.shape[3 if layout == "NHD" else 2]
-    code, block_size = _per_head_cache(one, KH, D, layout)
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    _int32_vector("seq_lens", seq_lens, B)
-    _int32_vector("query_start", query_start, B + 1)
-    _int32_vector("accepted_lens", accepted_lens, B)
+    index = kv_cache.get_device()
+    if index < 0 or kv_cache.dim() not in (5, 6):
+        raise ValueError("kv_cache: expected a CUDA [P, 2, ...] or [L, P, 2, ...] tensor")
+    layers, layer_stride, one = 1, 0, kv_cache
+    if kv_cache.dim() == 6:
+        layers = kv_cache.shape[0]
+        if layers == 0:
+            return
+        layer_stride, one = kv_cache.stride(0), kv_cache[0]
+    code, block_size, KH = _cache_shape(one, None, layout, index)
+    _tensor("seq_lens", seq_lens, _I32T, index, 1)
+    B = seq_lens.shape[0]
+    for name, t, n in (("query_start", query_start, B + 1), ("accepted_lens", accepted_lens, B)):
+        _tensor(name, t, _I32T, index, 1)
+        _shaped(name, t, (n,))
     for name, t in (("accepted", accepted), ("block_table", block_table)):
-        _need(t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[0] == B
-              and (t.shape[1] <= 1 or t.stride(1) == 1), f"{name}: expected CUDA int32 [B, ...] rows")
-    _one_device(kv_cache.device, query_start=query_start, seq_lens=seq_lens, accepted=accepted,
-                accepted_lens=accepted_lens, block_table=block_table)
-    _call_on(kv_cache.device, "kvq_compact_drafts_nvfp4_per_head", kv_cache.data_ptr(), layers,
-             kv_cache.stride(0) if layers > 1 else 0, one.shape[0], block_size, code, KH, D, query_start.data_ptr(),
-             seq_lens.data_ptr(), B, accepted.data_ptr(), _row_stride(accepted),
-             accepted_lens.data_ptr(), accepted.shape[1], block_table.data_ptr(),
-             _row_stride(block_table), block_table.shape[1], _status_ptr(status),
-             _stream_on(stream, kv_cache.device))
+        _tensor(name, t, _I32T, index, 2)
+        _shaped(name, t, (B, t.shape[1]))
+    _launch(index, stream, status, "kvq_compact_drafts_nvfp4_per_head",
+            (kv_cache.data_ptr(), layers, layer_stride, one.shape[0], block_size, code, KH, one.shape[4] // 9 * 16,
+             query_start.data_ptr(), seq_lens.data_ptr(), B, accepted.data_ptr(), _row_stride(accepted),
+             accepted_lens.data_ptr(), accepted.shape[1], block_table.data_ptr(), _row_stride(block_table),
+             block_table.shape[1]))
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

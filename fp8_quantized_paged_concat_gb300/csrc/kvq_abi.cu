@@ -839,8 +839,8 @@ kvq_status per_head_attention(
   if (kvq_status s = check_table(fn, query_start, seq_lens, batch_size, block_table, block_table_stride,
                                  block_table_width))
     return s;
-  KVQ_REQUIRE(int64_t{block_table_width} * block_size < (int64_t{1} << 31) - 64,
-              "%s: block_table_width * block_size must stay below 2^31 - 64 positions", fn);
+  KVQ_REQUIRE(int64_t{block_table_width} * block_size < (int64_t{1} << 31) - 256,
+              "%s: block_table_width * block_size must stay below 2^31 - 256 positions", fn);
   KVQ_REQUIRE(k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4),
               "%s: k_scale / v_scale must be device fp32 scalars", fn);
   KVQ_REQUIRE(softmax_scale == softmax_scale && softmax_scale > -3.0e38f && softmax_scale < 3.0e38f,
@@ -905,13 +905,13 @@ kvq_status per_head_attention(
   a.status = d_status;
   a.num_splits = num_splits;
   if (num_splits > 1) {
-    // ranges of whole 64-key steps, sized from the keys that a row block can
+    // ranges of whole 128-key steps, sized from the keys that a row block can
     // see: the whole sequence, or the window, a block's other tokens and the sinks
     int64_t span = max_seq_len;
     if (window > 0)
       span = std::min<int64_t>(span, int64_t{window} + std::min(max_query_len, 256) + num_sinks);
-    const int64_t steps = std::max<int64_t>(1, (span + 63) / 64);
-    a.split_keys = static_cast<int32_t>((steps + num_splits - 1) / num_splits * 64);
+    const int64_t steps = std::max<int64_t>(1, (span + 127) / 128);
+    a.split_keys = static_cast<int32_t>((steps + num_splits - 1) / num_splits * 128);
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = static_cast<float*>(workspace) + num_tokens * num_heads * num_splits * head_size;
   }

@@ -203,7 +203,7 @@ struct PerHeadAttentionArgs {
   const int32_t* block_table;
   int64_t block_table_stride;
   int32_t block_table_width;
-  int32_t table_positions;        // block_table_width * block_size, < 2^31 - 64 (host check)
+  int32_t table_positions;        // block_table_width * block_size, < 2^31 - 256 (host check)
   const uint8_t* cache;
   int64_t num_pages;
   int32_t block_size;
@@ -232,6 +232,8 @@ struct PerHeadAttentionArgs {
   float* part_lse;                // fp32 [num_tokens, num_heads, num_splits], base 2
 };
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream);
+// Its kernel for many query rows per key head (without the join of ranges).
+cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream);
 
 struct CompactArgs {
   uint8_t* cache;

@@ -38,8 +38,7 @@
 // that largest value, and what is lost below is under 2^-39 of it.  The
 // weights are kept as 2^(s - m + 6) with m at most 2^8 behind the true
 // maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
-#include "kvq_device.cuh"
-#include "kvq_launch.h"
+#include "kvq_per_head_attention.cuh"
 
 namespace kvq {
 namespace {
@@ -48,9 +47,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                   // keys per warp step
 constexpr int kStages = 3;
-constexpr float kGrow = 8.0f;               // the reference maximum moves when exceeded by 2^8
-constexpr float kShift = 6.0f;              // weights are 2^(s - m + kShift)
-constexpr float kLn2 = 0.69314718055994530942f;
 
 // Shared memory of one warp's stage: 32 data rows of K, of V, then their scale rows.
 template <int D>
@@ -60,9 +56,6 @@ struct Stage {
   static constexpr int kBytes = kVs + kStep * kScales;
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // `bytes` = kBytes, or 0: zero-filled, nothing read.
 template <int kBytes>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t bytes) {
@@ -75,29 +68,6 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return bits(__hmul2(half2_of(a), half2_of(b))); }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
-
-// The four bytes of w (two e2m1 codes each) as f16 pairs.
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
-}
 
 // D += A B, A 16 x 16 (row), B 16 x 8 (col), f16 in, fp32 out.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -155,57 +125,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   return v;
 }
 
-// The keys of one block of query rows: positions [0, sinks) and [lo, hi), in
-// steps of 32.
-struct Keys {
-  int32_t sinks, lo, hi;
-  int32_t sink_steps, steps;
-
-  __device__ __forceinline__ int32_t base(int32_t step) const {
-    return step < sink_steps ? step * kStep : lo + (step - sink_steps) * kStep;
-  }
-  __device__ __forceinline__ int32_t limit(int32_t step) const { return step < sink_steps ? sinks : hi; }
-};
-
-struct Request {
-  int64_t token0;              // its first query token
-  int32_t tokens;              // its query tokens
-  int64_t first_pos;           // position of its first query token (may be negative)
-  bool cut;                    // the sequence goes past the block table
-  int32_t len;                 // its sequence, as far as the block table reaches
-};
-
-// The request, or false (skipped): its query tokens are not inside [0,
-// num_tokens), or more than max_query_len.
-__device__ __forceinline__ bool request_of(const PerHeadAttentionArgs& a, int b, Request& r) {
-  const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
-  if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || q1 - q0 > a.max_query_len) return false;
-  r.token0 = q0;
-  r.tokens = q1 - q0;
-  const int32_t len = max(0, __ldg(a.seq_lens + b));
-  r.first_pos = static_cast<int64_t>(len) - r.tokens;
-  r.len = min(len, a.table_positions);
-  r.cut = r.len < len;
-  return true;
-}
-
-// The keys that some token in [t0, t1] of the request sees.
-__device__ __forceinline__ Keys keys_of(const PerHeadAttentionArgs& a, const Request& r, int32_t t0, int32_t t1) {
-  Keys k;
-  if (a.tree_mask != nullptr) {
-    k.lo = k.sinks = 0;
-    k.hi = r.len;
-  } else {
-    const int64_t p0 = r.first_pos + t0, p1 = r.first_pos + t1;
-    k.hi = static_cast<int32_t>(min(static_cast<int64_t>(r.len), max(int64_t{0}, p1 + 1)));
-    k.lo = a.window > 0 ? static_cast<int32_t>(min(static_cast<int64_t>(k.hi), max(int64_t{0}, p0 - a.window + 1))) : 0;
-    k.sinks = min(a.num_sinks, k.lo);
-  }
-  k.sink_steps = (k.sinks + kStep - 1) / kStep;
-  k.steps = k.sink_steps + (k.hi - k.lo + kStep - 1) / kStep;
-  return k;
-}
-
 template <int D, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 4)
     per_head_attention_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
@@ -229,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   const int32_t rows = static_cast<int32_t>(min(static_cast<int64_t>(kRows), total_rows - row0));
   const int32_t t0 = a.group_div.div(static_cast<uint32_t>(row0));
   const int32_t t1 = a.group_div.div(static_cast<uint32_t>(row0 + rows - 1));
-  const Keys keys = keys_of(a, rq, t0, t1);
+  const Keys<kStep> keys = keys_of<kStep>(a, rq, t0, t1);
   int32_t s0 = 0, s1 = keys.steps;
   if (a.num_splits > 1) {
     const int64_t per = a.split_keys / kStep;
@@ -318,27 +237,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-    // largest value -> [2^14, 2^15); zero, infinite and subnormal rows as they are
-    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-    const int shift = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
-    // 2^shift in two factors, each a normal number
-    const int sh0 = shift / 2, sh1 = shift - sh0;
-    const float f0 = __uint_as_float(static_cast<uint32_t>(127 + sh0) << 23);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + sh1) << 23);
-    const float i0 = __uint_as_float(static_cast<uint32_t>(127 - sh0) << 23);
-    const float i1 = __uint_as_float(static_cast<uint32_t>(127 - sh1) << 23);
+    const RowScale rs = row_scale(amax);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        q[nt][2 * i + (j >> 1)][j & 1] = pack_f16x2(bf16_lo(x[j]) * f0 * f1, bf16_hi(x[j]) * f0 * f1);
+        q[nt][2 * i + (j >> 1)][j & 1] = pack_f16x2(bf16_lo(x[j]) * rs.f[0] * rs.f[1], bf16_hi(x[j]) * rs.f[0] * rs.f[1]);
     }
-    const float row_scale = scale * i0 * i1;
+    const float back = scale * rs.i[0] * rs.i[1];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       // row 2c + x of the tile is loaded by the lanes with g = 2c + x
-      sc[nt][x] = __shfl_sync(kFull, row_scale, (2 * c + x) * 4);
+      sc[nt][x] = __shfl_sync(kFull, back, (2 * c + x) * 4);
       const int32_t rr = 8 * nt + 2 * c + x;
       const uint32_t tk = a.group_div.div(static_cast<uint32_t>(row0 + min(rr, rows - 1)));
       const int64_t p = rq.first_pos + tk;
@@ -516,10 +427,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
         uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
         uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
-        // A NaN scale (no write of finite values makes one) reads as zero, so
-        // that a hidden entry that was never written cannot reach any row.
-        sx &= __heq2_mask(half2_of(sx), half2_of(sx));
-        sy &= __heq2_mask(half2_of(sy), half2_of(sy));
+        sx = finite_scales(sx);
+        sy = finite_scales(sy);
         uint32_t w[4][2];
         auto load = [&](uint32_t row, uint32_t (&d)[2]) {
           if constexpr (D == 64) {
@@ -637,7 +546,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) per_head_join_kernel(const Pe
   const int64_t row = rq.token0 * a.num_heads + flat;
   const float* ls = a.part_lse + row * a.num_splits;
   float top = -INFINITY;
-  for (int s = lane; s < a.num_splits; s += 32) top = fmaxf(top, ls[s]);
+  bool abandoned = false;
+  for (int s = lane; s < a.num_splits; s += 32) {
+    top = fmaxf(top, ls[s]);
+    abandoned |= __float_as_uint(ls[s]) == kAbandoned;
+  }
+  if (__any_sync(kFull, abandoned)) return;              // a range whose CTA gave up: the row stays unwritten
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   constexpr int kDims = D / 32;                          // per lane
@@ -669,29 +583,40 @@ template <int D, int kRowTiles>
 cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   constexpr int kSmem = kWarps * kStages * Stage<D>::kBytes;
   static_assert(kSmem >= kWarps * 8 * kRowTiles * D * 4, "the joined rows fit the rings");
-  cudaError_t e = cudaFuncSetAttribute(per_head_attention_kernel<D, kRowTiles>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(per_head_attention_kernel<D, kRowTiles>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
   const int64_t blocks = (rows + 8 * kRowTiles - 1) / (8 * kRowTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
   per_head_attention_kernel<D, kRowTiles><<<grid, kThreads, kSmem, stream>>>(a, static_cast<int32_t>(blocks));
-  if ((e = cudaGetLastError()) != cudaSuccess || a.num_splits == 1) return e;
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
-  per_head_join_kernel<D><<<dim3(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps),
-                                 static_cast<unsigned>(a.batch_size)), kJoinWarps * 32, 0, stream>>>(a);
+  const dim3 grid(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
+  per_head_join_kernel<D><<<grid, kJoinWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  const bool one_tile = static_cast<int64_t>(a.max_query_len) * a.group <= 8;
-  switch (a.head_size) {
-    case 64: return one_tile ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
-    case 128: return one_tile ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
-    default: return launch_rows<256, 1>(a, stream);      // two tiles would not fit the registers
-  }
+  const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
+  cudaError_t e;
+  if (rows > 32)
+    e = launch_per_head_prefill(a, stream);
+  else if (a.head_size == 64)
+    e = rows <= 8 ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
+  else if (a.head_size == 128)
+    e = rows <= 8 ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
+  else
+    e = launch_rows<256, 1>(a, stream);              // two tiles would not fit the registers
+  if (e != cudaSuccess || a.num_splits == 1) return e;
+  return a.head_size == 64 ? launch_join<64>(a, stream)
+                           : a.head_size == 128 ? launch_join<128>(a, stream) : launch_join<256>(a, stream);
 }
 
 }  // namespace kvq

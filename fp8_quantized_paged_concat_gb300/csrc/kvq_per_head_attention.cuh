@@ -1,0 +1,110 @@
+// kvq_per_head_attention.cuh -- what the two attention kernels over the
+// per-head NVFP4 cache share: the requests, the keys a block of query rows
+// sees, and the decoding of e2m1 codes.
+#pragma once
+
+#include "kvq_device.cuh"
+#include "kvq_launch.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+// The weights of the softmax are kept as 2^(s - m + kShift) in f16, where the
+// reference m lags the true maximum by at most kGrow: they stay below 2^14.
+constexpr float kGrow = 8.0f;
+constexpr float kShift = 6.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// Base-2 log-sum-exp of a key range whose CTA gave up: its rows stay unwritten.
+constexpr uint32_t kAbandoned = 0x7fc0deadu;
+
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return bits(__hmul2(half2_of(a), half2_of(b))); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
+
+// The four bytes of w (two e2m1 codes each) as f16 pairs: one conversion per
+// pair, which takes its byte without a shift.  64 conversions per clock and
+// SM, the rate of any integer instruction, so that 8 values cost 4 of them;
+// shifts and masks that place the code bits in an f16 cost 11.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// Scales of values (f16 pairs): a NaN (no write of finite values makes one)
+// reads as zero, so that a hidden entry that was never written cannot reach
+// any row through a weight of zero.
+__device__ __forceinline__ uint32_t finite_scales(uint32_t s) { return s & __heq2_mask(half2_of(s), half2_of(s)); }
+
+// The power of two that brings a query row's largest value to [2^14, 2^15),
+// as two factors f[0] f[1], and the one that takes it back, i[0] i[1].
+// Rows of zeros, subnormals or infinities stay as they are.
+struct RowScale {
+  float f[2], i[2];
+};
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+  const int shift = ex == 0 || ex == 255 ? 0 : 127 + 14 - ex;
+  const int sh0 = shift / 2, sh1 = shift - sh0;
+  return {{__uint_as_float(static_cast<uint32_t>(127 + sh0) << 23), __uint_as_float(static_cast<uint32_t>(127 + sh1) << 23)},
+          {__uint_as_float(static_cast<uint32_t>(127 - sh0) << 23), __uint_as_float(static_cast<uint32_t>(127 - sh1) << 23)}};
+}
+
+// The keys of one block of query rows: positions [0, sinks) and [lo, hi), in
+// steps of kStep.
+template <int kStep>
+struct Keys {
+  int32_t sinks, lo, hi;
+  int32_t sink_steps, steps;
+
+  __device__ __forceinline__ int32_t base(int32_t step) const {
+    return step < sink_steps ? step * kStep : lo + (step - sink_steps) * kStep;
+  }
+  __device__ __forceinline__ int32_t limit(int32_t step) const { return step < sink_steps ? sinks : hi; }
+};
+
+struct Request {
+  int64_t token0;              // its first query token
+  int32_t tokens;              // its query tokens
+  int64_t first_pos;           // position of its first query token (may be negative)
+  bool cut;                    // the sequence goes past the block table
+  int32_t len;                 // its sequence, as far as the block table reaches
+};
+
+// The request, or false (skipped): its query tokens are not inside [0,
+// num_tokens), or more than max_query_len.
+__device__ __forceinline__ bool request_of(const PerHeadAttentionArgs& a, int b, Request& r) {
+  const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
+  if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || q1 - q0 > a.max_query_len) return false;
+  r.token0 = q0;
+  r.tokens = q1 - q0;
+  const int32_t len = max(0, __ldg(a.seq_lens + b));
+  r.first_pos = static_cast<int64_t>(len) - r.tokens;
+  r.len = min(len, a.table_positions);
+  r.cut = r.len < len;
+  return true;
+}
+
+// The keys that some token in [t0, t1] of the request sees.
+template <int kStep>
+__device__ __forceinline__ Keys<kStep> keys_of(const PerHeadAttentionArgs& a, const Request& r, int32_t t0, int32_t t1) {
+  Keys<kStep> k;
+  if (a.tree_mask != nullptr) {
+    k.lo = k.sinks = 0;
+    k.hi = r.len;
+  } else {
+    const int64_t p0 = r.first_pos + t0, p1 = r.first_pos + t1;
+    k.hi = static_cast<int32_t>(min(static_cast<int64_t>(r.len), max(int64_t{0}, p1 + 1)));
+    k.lo = a.window > 0 ? static_cast<int32_t>(min(static_cast<int64_t>(k.hi), max(int64_t{0}, p0 - a.window + 1))) : 0;
+    k.sinks = min(a.num_sinks, k.lo);
+  }
+  k.sink_steps = (k.sinks + kStep - 1) / kStep;
+  k.steps = k.sink_steps + (k.hi - k.lo + kStep - 1) / kStep;
+  return k;
+}
+
+}  // namespace
+}  // namespace kvq
