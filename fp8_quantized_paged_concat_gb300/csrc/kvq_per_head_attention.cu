@@ -56,19 +56,6 @@ struct Stage {
   static constexpr int kBytes = kVs + kStep * kScales;
 };
 
-// `bytes` = kBytes, or 0: zero-filled, nothing read.
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t bytes) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(kBytes), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
-
 // D += A B, A 16 x 16 (row), B 16 x 8 (col), f16 in, fp32 out.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -96,33 +83,6 @@ __device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) {
 template <int D>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
   return D == 256 ? chunk ^ ((row & 3) << 1) : D == 128 ? chunk ^ (row & 2) : chunk;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 template <int D, int kRowTiles>
@@ -318,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
           wa[0] = x.x; wa[1] = x.y; wb[0] = y.x; wb[1] = y.y;
         } else {
           const uint32_t chunk = D == 256 ? 2 * c + i : c;
-          const uint4 x = lds128(ka + 16 * k_chunk<D>(ra, chunk)), y = lds128(kb + 16 * k_chunk<D>(rb2, chunk));
+          const uint4 x = ld_shared16(ka + 16 * k_chunk<D>(ra, chunk)), y = ld_shared16(kb + 16 * k_chunk<D>(rb2, chunk));
           wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
           wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
         }

@@ -5,20 +5,24 @@
 //
 // Design: one CTA per (block of 128 kTiles query rows, key head, range of
 // keys), one CTA per SM; the rows are (token, head) pairs of one request.
-// Two row tiles (kTiles = 2) share every decoded key tile, and their softmax
-// and products alternate: while one tile's scores become weights, the tensor
-// core works on the other tile.
-//   - tensor memory: O of tile w in columns [D w, +D); scores S (128 x kKeys
-//     fp32) in columns 256 on, one buffer per row tile (two buffers for a
-//     single tile); the weights P (f16) overwrite the first half of their S;
-//   - shared memory: q in f16 (scaled by each row's power of two), K tiles
-//     and V tiles (kKeys x D f16, 128-byte swizzle), two stages each; K is
-//     free once its scores are formed, V once its product is;
-//   - producer warps decode the entries: 8 lanes take 8 rows of a 64-column
-//     block, so that their 16-byte stores fall in different banks; a tile's
-//     loads are issued a tile ahead, its page ids two;
-//   - one thread issues the products, per key tile t: P_0 V, S_0(t + 1), P_1
-//     V, S_1(t + 1) (for a single row tile S(t + 1), then P V(t));
+// Two row tiles (kTiles = 2) share every decoded tile of 64 keys, and their
+// softmax and products alternate.
+//   - tensor memory: O of row tile w in columns [D w, +D); its scores S (128 x
+//     64 fp32) in two buffers from column 256 on, so that the scores of tile t
+//     + 1 are formed while the weights of tile t are computed; the weights P
+//     (f16) overwrite the first half of their S.  (128 keys per tile would
+//     leave room for one buffer: product, scores and weights of a row tile
+//     then wait for one another, 5900 clocks per 128 keys where the products
+//     need 2048.)
+//   - shared memory: q in f16 (scaled by each row's power of two), K tiles and
+//     V tiles (64 x D f16, 128-byte swizzle, kStages of each), and a ring of
+//     raw entries per side;
+//   - four warps decode the keys and three the values: raw entries come in by
+//     asynchronous copies, kRing - 1 chunks ahead (each warp copies what it
+//     decodes, so that it waits for no other); 8 lanes take 8 rows of a
+//     64-column block, so that their 16-byte stores fall in different banks;
+//   - one warp issues the products: per key tile t, S_w(t + 1) of every row
+//     tile, then O_w += P_w(t) V(t);
 //   - four softmax warps per row tile, one thread per row, in one pass over
 //     the scores: the weights are formed against the reference maximum of the
 //     tiles before, and only when a score exceeds it by 2^8 is the pass
@@ -26,6 +30,8 @@
 //     are again at most 1).
 // Every wait is bounded; on expiry the CTA records KVQ_STATUS_TIMEOUT, drains
 // its products, frees its tensor memory and leaves its rows unwritten.
+#include <type_traits>
+
 #include "kvq_per_head_attention.cuh"
 
 namespace kvq {
@@ -33,29 +39,44 @@ namespace {
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;
-constexpr int kStages = 2;
-constexpr int kValidRing = 4;
+constexpr int64_t kMaxPos = INT32_MAX - 256;      // positions stay below it (host check)
+constexpr int kKeys = 64;                         // keys per tile
+constexpr int kValidRing = 16;
 constexpr uint32_t kBlockBytes = 128 * 128;       // 64 dimensions of 128 rows of q
+constexpr uint32_t kKBlock = kKeys * 128;         // 64 dimensions of a key tile
 
 template <int D, int kTiles>
 struct Shape {
-  static constexpr int kKeys = D == 256 ? 64 : 128;          // keys per tile
+  // warps: softmax, four that decode keys, the products', three that decode
+  // values; in whole warpgroups, whose registers are split by role (the
+  // threads start with an equal share, and the shares add up to no more)
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kProducers = kTiles == 2 ? 4 : 8;
-  static constexpr int kMmaWarp = kSoftmaxWarps + kProducers;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kKeyWarps = 4, kValueWarps = 3;
+  static constexpr int kMmaWarp = kSoftmaxWarps + kKeyWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1 + kValueWarps);
+  static constexpr int kStartRegs = kTiles == 2 ? 128 : 168;
+  static constexpr int kSoftmaxRegs = kTiles == 2 ? 152 : 200;
+  static constexpr int kOtherRegs = kTiles == 2 ? 104 : 144;
+  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kStartRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
-  static constexpr uint32_t kKBlock = kKeys * 128;
-  static constexpr uint32_t kTileBytes = kBlocks * kKBlock;  // one stage of K or V
+  static constexpr int kStages = D == 256 ? 2 : 3;           // decoded tiles of K, of V
+  static constexpr uint32_t kTileBytes = kBlocks * kKBlock;
   static constexpr uint32_t kQTile = kBlocks * kBlockBytes;
   static constexpr uint32_t kK = kTiles * kQTile;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
-  static constexpr uint32_t kMisc = kV + kStages * kTileBytes;
+  // raw entries of one side: rings of chunks of keys, data rows then scale rows
+  static constexpr int kChunk = D == 256 ? 32 : 64;
+  static constexpr int kParts = kKeys / kChunk;              // chunks per tile
+  static constexpr int kRing = D == 256 ? 3 : 4;
+  static constexpr uint32_t kRawScales = kChunk * (D / 2);
+  static constexpr uint32_t kRawBytes = kRawScales + kChunk * (D / 16);
+  static constexpr uint32_t kRawK = kV + kStages * kTileBytes;
+  static constexpr uint32_t kRawV = kRawK + kRing * kRawBytes;
+  static constexpr uint32_t kMisc = kRawV + kRing * kRawBytes;
   // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
   static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kTiles * D <= 256 && 256 + 2 * kKeys <= 512, "tensor memory");
-  static constexpr int kPasses = kKeys / (8 * kProducers);   // rows of a tile per producer lane
+  static_assert(kTiles * D <= 256 && kMisc % 16 == 0, "tensor memory, alignment");
 };
 
 // kind::f16 with f16 operands, fp32 sums; A is K-major.
@@ -81,40 +102,46 @@ __device__ __forceinline__ uint32_t tree_bits(const uint64_t* row, int32_t words
   return static_cast<uint32_t>(v);
 }
 
-// Raw pieces of one tile's rows in a producer lane: 16 (D = 64: 16, 128: 32,
-// 256: 64) codes and their scales.
+// A producer lane's piece of one entry side: D / 4 codes and their scales.
 template <int D>
 struct Piece {
-  static constexpr int kWords = D / 32;              // 32-bit words of codes per lane (8 codes each)
+  static constexpr int kWords = D / 32;              // 32-bit words of codes (8 codes each)
   uint32_t w[kWords];
   uint32_t sf;
 };
 
+// Byte offset of part i of lane part k (0..3) of raw row r: rows are D / 2
+// bytes apart, their pieces permuted so that 8 rows' reads of one part fall
+// in different banks.
 template <int D>
-__device__ __forceinline__ void load_piece(const uint8_t* data, const uint8_t* scales, int k, Piece<D>& e) {
+__device__ __forceinline__ uint32_t raw_offset(uint32_t r, uint32_t k, uint32_t i) {
+  if constexpr (D == 64) return r * 32 + 8 * (k ^ ((r >> 1) & 2));
+  if constexpr (D == 128) return r * 64 + 16 * (k ^ ((r >> 1) & 3));
+  return r * 128 + 16 * ((2 * k + i) ^ (r & 7));
+}
+
+template <int D>
+__device__ __forceinline__ void load_piece(uint32_t data, uint32_t scales, uint32_t r, uint32_t k, Piece<D>& e) {
   if constexpr (D == 64) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(data + 8 * k));
+    const uint2 v = lds64(data + raw_offset<D>(r, k, 0));
     e.w[0] = v.x;
     e.w[1] = v.y;
-    e.sf = __ldg(scales + k);
+    e.sf = lds8(scales + r * 4 + k);
   } else {
 #pragma unroll
     for (int i = 0; i < D / 128; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(data + (D / 8) * k) + i);
+      const uint4 v = ld_shared16(data + raw_offset<D>(r, k, i));
       e.w[4 * i] = v.x;
       e.w[4 * i + 1] = v.y;
       e.w[4 * i + 2] = v.z;
       e.w[4 * i + 3] = v.w;
     }
-    if constexpr (D == 128)
-      e.sf = __ldg(reinterpret_cast<const uint16_t*>(scales + 2 * k));
-    else
-      e.sf = __ldg(reinterpret_cast<const uint32_t*>(scales + 4 * k));
+    e.sf = D == 128 ? lds16(scales + r * 8 + 2 * k) : lds32(scales + r * 16 + 4 * k);
   }
 }
 
 // Decodes a piece and stores its 16-byte chunks into row r of a tile.
-template <int D, uint32_t kKBlock, bool kValues>
+template <int D, bool kValues>
 __device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, const Piece<D>& e) {
   // a lane's D / 4 dimensions: block (D / 4) k / 64, chunks from ((D / 4) k % 64) / 8 on
   const uint32_t base = tile + (D * k / 256) * kKBlock + r * 128u + ((r & 7u) << 4);
@@ -134,11 +161,119 @@ __device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, co
   }
 }
 
+// ---------------------------------------------------------------------------
+// producers: the keys or the values of every tile
+// ---------------------------------------------------------------------------
+//
+// kWarps warps share a chunk's rows in groups of 8: warp `me` takes groups me,
+// me + kWarps, ...; lane (k = lane / 8, lane % 8) takes dimensions k D / 4 ..
+// +D / 4 of row lane % 8 of its groups.  Page ids are loaded a chunk before
+// the copies that use them start, and looked at only there.
+template <int D, int kTiles, bool kValues>
+__device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, uint32_t head, const Keys<kKeys>& keys,
+                                        int32_t s0, int32_t n_tiles, int me, int lane, bool bad_index, uint32_t base,
+                                        uint32_t full, uint32_t empty, uint32_t valid_full, uint8_t* valid_ring,
+                                        volatile int* s_abort) {
+  using S = Shape<D, kTiles>;
+  constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
+  constexpr int kGroups = S::kChunk / 8, kPasses = (kGroups + kWarps - 1) / kWarps;
+  const uint32_t k = lane >> 3;
+  const uint32_t tiles = base + (kValues ? S::kV : S::kK), raw_ring = base + (kValues ? S::kRawV : S::kRawK);
+  const int32_t chunks = n_tiles * S::kParts;
+  const uint8_t* side = a.cache + (kValues ? a.region : 0);
+  const int32_t* table = a.block_table + b * a.block_table_stride;
+  int32_t id[kPasses];                              // page ids of the next chunk to be copied
+  auto row_of = [&](int i) { return static_cast<uint32_t>(8 * (me + kWarps * i) + (lane & 7)); };
+  auto position = [&](int32_t h, int i) {           // of the lane's row in pass i of chunk h
+    return static_cast<uint32_t>(keys.base(s0 + h / S::kParts) + (h % S::kParts) * S::kChunk) + row_of(i);
+  };
+  auto load_ids = [&](int32_t h) {
+    if (h >= chunks) return;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      id[i] = -1;
+      const uint32_t p = position(h, i), col = a.block_div.div(p);
+      if (me + kWarps * i < kGroups && p < static_cast<uint32_t>(keys.limit(s0 + h / S::kParts)) &&
+          col < static_cast<uint32_t>(a.block_table_width))
+        id[i] = __ldg(table + col);
+    }
+  };
+  auto start = [&](int32_t h) {                     // one group of copies, empty past the last chunk
+    if (h < chunks) {
+      const int32_t t = h / S::kParts;
+      const uint32_t limit = static_cast<uint32_t>(keys.limit(s0 + t));
+      const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        if (me + kWarps * i >= kGroups) continue;   // uniform over the warp
+        const uint32_t r = row_of(i), p = position(h, i);
+        const bool ok = p < limit && id[i] >= 0 && id[i] < a.num_pages;
+        bad_index = bad_index || (p < limit && !ok);
+        const uint32_t off = p - a.block_div.div(p) * static_cast<uint32_t>(a.block_size);
+        const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
+        const uint8_t* region = side + static_cast<int64_t>(ok ? id[i] : 0) * 2 * a.region;
+        const uint8_t* src = ok ? region + row * (D / 2) + (D / 8) * k : side;
+        constexpr int kPiece = D == 64 ? 8 : 16;
+#pragma unroll
+        for (int j = 0; j < (D == 256 ? 2 : 1); ++j)
+          cp_async<kPiece>(raw + raw_offset<D>(r, k, j), src + 16 * j, ok ? kPiece : 0);
+        if (k == 0)
+          cp_async<D / 16>(raw + S::kRawScales + r * (D / 16), ok ? region + a.scales + row * (D / 16) : side,
+                           ok ? D / 16 : 0);
+        if constexpr (!kValues) {
+          // Which keys exist, for the softmax; a slot's last reader is long
+          // done (kRing - 1 chunks ahead of a tile whose buffers are free).
+          const uint32_t rows = __ballot_sync(kFull, ok);
+          if (lane == 0)
+            valid_ring[8 * (t % kValidRing) + (h % S::kParts) * (S::kChunk / 8) + me + kWarps * i] =
+                static_cast<uint8_t>(rows);
+        }
+      }
+    }
+    cp_commit();
+  };
+  load_ids(0);
+#pragma unroll
+  for (int h = 0; h < S::kRing - 1; ++h) {
+    start(h);
+    load_ids(h + 1);
+  }
+  for (int32_t h = 0; h < chunks; ++h) {
+    const int32_t t = h / S::kParts;
+    const int st = t % S::kStages;
+    cp_wait<S::kRing - 2>();
+    __syncwarp();                                   // chunk h is there, and chunk h - 1 has been read
+    start(h + S::kRing - 1);
+    load_ids(h + S::kRing);
+    const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
+    Piece<D> e[kPasses];                            // all read first, so that their latencies overlap
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (me + kWarps * i < kGroups) load_piece<D>(raw, raw + S::kRawScales, row_of(i), k, e[i]);
+    if (h % S::kParts == 0 && t >= S::kStages &&
+        !warp_wait_or_abort(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort))
+      break;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (me + kWarps * i < kGroups)
+        store_piece<D, kValues>(tiles + st * S::kTileBytes, (h % S::kParts) * S::kChunk + row_of(i), k, e[i]);
+    if (h % S::kParts == S::kParts - 1) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (!kValues) mbar_arrive(valid_full + 8 * (t % kValidRing));
+        mbar_arrive(full + 8 * st);
+      }
+    }
+  }
+  cp_wait<0>();                                     // no copy outlives the CTA
+  if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
+}
+
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
   using S = Shape<D, kTiles>;
-  constexpr int kKeys = S::kKeys;
   // (key head, row block, range): heads vary fastest; the last row blocks of a
   // causal chunk, which see the most keys, come first
   const uint32_t head = blockIdx.x % a.num_kv_heads, rest = blockIdx.x / a.num_kv_heads;
@@ -178,51 +313,59 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
   const uint32_t bar = base + S::kMisc;
-  const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;   // [kStages] each
-  const uint32_t s_full = bar + 64, p_full = bar + 80, o_done = bar + 96;                   // [2] each
-  const uint32_t valid_full = bar + 112, drain = bar + 144;                                 // [kValidRing], 1
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 160);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 164);
-  uint8_t* valid_ring = smem + S::kMisc + 256;     // [kValidRing][16]: bit per key of the tile
-  static_assert(kStages == 2 && kValidRing == 4, "barrier layout");
+  const uint32_t k_full = bar, k_empty = bar + 24, v_full = bar + 48, v_empty = bar + 72;   // [kStages] each
+  const uint32_t s_full = bar + 96, p_full = bar + 128;            // [row tile][buffer]
+  const uint32_t o_done = bar + 160, drain = bar + 176, q_full = bar + 184;                 // [row tile], 1, 1
+  const uint32_t valid_full = bar + 192;                           // [kValidRing]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 320);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 324);
+  uint8_t* valid_ring = smem + S::kMisc + 352;     // [kValidRing][8]: bit per key of the tile
+  static_assert(S::kStages <= 3 && 192 + 8 * kValidRing <= 320 && 352 + 8 * kValidRing <= 512, "barrier layout");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(s_tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + 8 * i, S::kProducers);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(k_full + 8 * i, S::kKeyWarps);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, S::kProducers);
+      mbar_init(v_full + 8 * i, S::kValueWarps);
       mbar_init(v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
-      mbar_init(o_done + 8 * i, 1);
     }
-    for (int i = 0; i < kValidRing; ++i) mbar_init(valid_full + 8 * i, S::kProducers);
+    for (int i = 0; i < 2; ++i) mbar_init(o_done + 8 * i, 1);
+    for (int i = 0; i < kValidRing; ++i) mbar_init(valid_full + 8 * i, S::kKeyWarps);
     mbar_init(drain, 1);
+    mbar_init(q_full, S::kSoftmaxWarps);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
-  const bool is_softmax = warp < S::kSoftmaxWarps;
-  const bool is_producer = !is_softmax && warp < S::kMmaWarp;
-  const int tile = warp >> 2;                       // softmax: row tile
-  const int32_t row = static_cast<int32_t>(threadIdx.x);   // softmax: row of the block
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
 
-  // ---- softmax threads: their query row -> shared memory ------------------
-  float sc = 0.0f;                                  // score -> base-2 exponent
-  int64_t token = 0;
-  int32_t q_head = 0;
-  int32_t pos_hi = -1, pos_lo = 0;
-  if (is_softmax) {
-    const bool live = row < rows;
+  if (warp < S::kSoftmaxWarps) {
+    // ---- softmax: thread = query row ----------------------------------------
+    more_registers<S::kSoftmaxRegs>();
+    const int tile = warp >> 2;                     // its row tile
+    const int32_t row = static_cast<int32_t>(threadIdx.x);
+    // the query row -> shared memory
+    float sc = 0.0f;                                // score -> base-2 exponent
+    int64_t token = 0;
+    int32_t q_head = 0;
+    int32_t pos_hi = -1, pos_lo = 0;
+    const bool has_row = row < rows;
     const uint4* src = nullptr;
     float amax = 0.0f;
-    if (live) {
+    if (has_row) {
       const uint32_t flat = static_cast<uint32_t>(row0 + row), tk = a.group_div.div(flat);
       token = rq.token0 + tk;
       q_head = head * a.group + (flat - tk * a.group);
@@ -245,7 +388,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
 #pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
       uint4 v = make_uint4(0, 0, 0, 0);             // rows past the block's are zero
-      if (live) {
+      if (has_row) {
         const uint4 x = __ldg(src + i);
         v = make_uint4(pack_f16x2(bf16_lo(x.x) * rs.f[0] * rs.f[1], bf16_hi(x.x) * rs.f[0] * rs.f[1]),
                        pack_f16x2(bf16_lo(x.y) * rs.f[0] * rs.f[1], bf16_hi(x.y) * rs.f[0] * rs.f[1]),
@@ -255,311 +398,130 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       st_shared16(q_tile + (i >> 3) * kBlockBytes + sw128_offset(row & 127, i & 7), v);
     }
     fence_async_smem();
-  }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
 
-  // ---- producers: the first tile's loads ----------------------------------
-  // Lane (k = lane / 8, lane % 8) takes D / 4 dimensions of rows 8 (warp +
-  // kProducers i) + lane % 8, i < kPasses.
-  const int k = lane >> 3;
-  const uint32_t r0 = 8 * (warp - S::kSoftmaxWarps) + (lane & 7);
-  bool bad_index = rq.cut && threadIdx.x == 0;
-  Piece<D> pk[S::kPasses], pv[S::kPasses];
-  int32_t page[S::kPasses], in_page[S::kPasses], next[S::kPasses];   // this tile's pages and rows, the next one's ids
-  // page id of key r of tile t: -1 past the range, INT32_MAX for a column past the table or a negative id
-  auto page_id = [&](int32_t t, uint32_t r) -> int32_t {
-    if (t >= n_tiles) return -1;
-    const int32_t p = keys.base(s0 + t) + static_cast<int32_t>(r);
-    if (p >= keys.limit(s0 + t)) return -1;
-    const uint32_t col = a.block_div.div(static_cast<uint32_t>(p));
-    if (col >= static_cast<uint32_t>(a.block_table_width)) return INT32_MAX;
-    const int32_t id = __ldg(a.block_table + b * a.block_table_stride + col);
-    return id < 0 ? INT32_MAX : id;
-  };
-  // turns the ids loaded for tile t into pages and rows
-  auto resolve = [&](int32_t t) {
-#pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) {
-      page[i] = next[i];
-      in_page[i] = 0;
-      if (page[i] >= a.num_pages) {
-        bad_index = true;
-        page[i] = -1;
-      }
-      if (page[i] >= 0) {
-        const uint32_t p = keys.base(s0 + t) + r0 + 8 * S::kProducers * i;
-        const uint32_t off = p - a.block_div.div(p) * static_cast<uint32_t>(a.block_size);
-        in_page[i] = static_cast<int32_t>(off) * a.row_offset + static_cast<int32_t>(head) * a.row_head;
-      }
-    }
-  };
-  auto load = [&](int side, Piece<D> (&e)[S::kPasses]) {
-#pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) {
-      if (page[i] < 0) {
-        e[i] = Piece<D>{};                          // decodes to zeros
-        continue;
-      }
-      const uint8_t* region = a.cache + (static_cast<int64_t>(page[i]) * 2 + side) * a.region;
-      load_piece<D>(region + static_cast<int64_t>(in_page[i]) * (D / 2),
-                    region + a.scales + static_cast<int64_t>(in_page[i]) * (D / 16), k, e[i]);
-    }
-  };
-  if (is_producer) {
-#pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) next[i] = page_id(0, r0 + 8 * S::kProducers * i);
-    resolve(0);
-    if (n_tiles > 0) {
-      load(0, pk);
-      load(1, pv);
-    }
-#pragma unroll
-    for (int i = 0; i < S::kPasses; ++i) next[i] = page_id(1, r0 + 8 * S::kProducers * i);
-  }
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  const uint32_t tmem = *s_tmem;
-
-  int mma_issued = 0;
-  float m = -INFINITY, l = 0.0f;
-  if (is_softmax) {
-    // ---- softmax ------------------------------------------------------------
+    float m = -INFINITY, l = 0.0f;
+    bool done = true;
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
     for (int32_t t = 0; t < n_tiles; ++t) {
-      const int buf = kTiles == 2 ? tile : t & 1;
+      const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
       // which of the tile's keys the row sees
-      const int32_t p0 = keys.base(s0 + t), limit = keys.limit(s0 + t);
-      if (!warp_wait_or_abort(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) break;
-      uint32_t see[kKeys / 32];
-      bool all = p0 + kKeys <= limit;
-#pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
-        see[c] = reinterpret_cast<const volatile uint32_t*>(valid_ring + 16 * (t % kValidRing))[c];
-        all = all && see[c] == kFull;
+      const int32_t p0 = keys.base(s0 + t);
+      if (!warp_wait_or_abort(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) {
+        done = false;
+        break;
       }
+      const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
+      bool all = (valid.x & valid.y) == kFull;
       if (a.tree_mask != nullptr)
         all = all && p0 + kKeys <= rq.first_pos;
       else
         all = all && p0 + kKeys - 1 <= pos_hi && (p0 >= pos_lo || p0 + kKeys <= a.num_sinks);
       const bool masked = __any_sync(kFull, !all && row < rows);
-      if (masked) {
+      uint32_t see[2] = {0, 0};
+      if (masked && row < rows) {
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
           const int32_t pc = p0 + 32 * c;
           uint32_t w;
-          if (row >= rows)
-            w = 0;
-          else if (a.tree_mask != nullptr)
-            w = (rq.first_pos > 0 ? range_bits(pc, 0, static_cast<int32_t>(min(rq.first_pos - 1, int64_t{INT32_MAX} - 64))) : 0u) |
+          if (a.tree_mask != nullptr)
+            w = (rq.first_pos > 0 ? range_bits(pc, 0, static_cast<int32_t>(min(rq.first_pos - 1, kMaxPos))) : 0u) |
                 tree_bits(a.tree_mask + token * a.tree_stride, a.tree_words, pc - rq.first_pos);
           else
             w = range_bits(pc, pos_lo, pos_hi) | range_bits(pc, 0, min(a.num_sinks - 1, pos_hi));
-          see[c] &= w;
+          see[c] = (c == 0 ? valid.x : valid.y) & w;
         }
       }
-      if (!warp_wait_or_abort(s_full + 8 * buf, (kTiles == 2 ? t : t >> 1) & 1, s_abort)) break;
+      if (!warp_wait_or_abort(s_full + 8 * buf, (t >> 1) & 1, s_abort)) {
+        done = false;
+        break;
+      }
       fence_after_sync();
 
-      uint32_t p[kKeys / 2];
+      uint32_t s[64], p[32];
+      tmem_ld64(s_col, s);
       float top, sum;
       // weights against the reference m: p, their sum, and the largest exponent
-      auto pass = [&](float off) {
+      auto pass = [&](float off, auto with_mask) {
         float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          float s[32];
-          tmem_ld32(s_col + 32 * c, s);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float2 z = ffma2(make_float2(s[i], s[i + 1]), make_float2(sc, sc), make_float2(off, off));
-            if (masked) {
-              z.x = (see[c] >> i) & 1 ? z.x : -INFINITY;
-              z.y = (see[c] >> (i + 1)) & 1 ? z.y : -INFINITY;
-            }
-            tops[(i >> 1) & 3] = fmax3(tops[(i >> 1) & 3], z.x, z.y);
-            const float2 w = make_float2(ex2(z.x), ex2(z.y));
-            sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
-            p[16 * c + (i >> 1)] = pack_f16x2(w.x, w.y);
+        for (int i = 0; i < 64; i += 2) {
+          float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
+                           make_float2(off, off));
+          if constexpr (with_mask.value) {
+            z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
+            z.y = (see[i >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
           }
+          tops[(i >> 1) & 3] = fmax3(tops[(i >> 1) & 3], z.x, z.y);
+          const float2 w = make_float2(ex2(z.x), ex2(z.y));
+          sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
+          p[i >> 1] = pack_f16x2(w.x, w.y);
         }
         const float2 both = fadd2(sums[0], sums[1]);
         sum = both.x + both.y;
         top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]);
       };
+      auto weights = [&](float off) {               // warp-uniform choice
+        if (masked)
+          pass(off, std::true_type{});
+        else
+          pass(off, std::false_type{});
+      };
       const float m_use = m == -INFINITY ? 0.0f : m;
-      pass(kShift - m_use);
+      weights(kShift - m_use);
       const bool grow = top > -INFINITY && (m == -INFINITY || top > kShift + kGrow);
-      float alpha = 1.0f;
       if (__any_sync(kFull, grow)) {
+        float alpha = 1.0f;
         if (grow) {
           const float m_new = top - kShift + m_use;
           alpha = ex2(m - m_new);                   // 0 while m is -inf
           m = m_new;
         }
-        pass(kShift - (m == -INFINITY ? 0.0f : m));
-      }
-      l = l * alpha + sum;
-      // the product of the tile before is done: O may be rescaled (and the
-      // barrier's phases stay in step)
-      if (t > 0 && !warp_wait_or_abort(o_done + 8 * (kTiles == 2 ? tile : 0), (t - 1) & 1, s_abort)) break;
-      if (t > 0 && __any_sync(kFull, alpha != 1.0f)) {
-        fence_after_sync();
+        weights(kShift - (m == -INFINITY ? 0.0f : m));
+        l *= alpha;
+        if (t > 0) {
+          // O is rescaled once the product of the tile before is done.  (The
+          // barrier is waited on only here: the scores of tile t follow the
+          // product of tile t - 2, so the phase cannot be mistaken.)
+          if (!warp_wait_or_abort(o_done + 8 * tile, (t - 1) & 1, s_abort)) {
+            done = false;
+            break;
+          }
+          fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld32(o_col + 32 * c, o);
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_col + 32 * c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(o_col + 32 * c, o);
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(o_col + 32 * c, o);
+          }
         }
       }
-#pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) tmem_st16(s_col + 16 * c, p + 16 * c);
+      l += sum;
+      tmem_st32_start(s_col, p);
+      tmem_st_wait();
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * (kTiles == 2 ? tile : 0));
+      if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
-  } else if (is_producer) {
-    // ---- producers ----------------------------------------------------------
-    for (int32_t t = 0; t < n_tiles; ++t) {
-      const int st = t % kStages;
-      // which keys exist, for the softmax (the ring slot's last reader was
-      // four tiles ago: scores of tile t - 2, whose buffer K(t) takes, exist
-      // only once the weights of tile t - 4 were used)
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i) {
-        const uint32_t have = __ballot_sync(kFull, page[i] >= 0);
-        if (lane == 0) valid_ring[16 * (t % kValidRing) + (r0 >> 3) + S::kProducers * i] = static_cast<uint8_t>(have);
-      }
-      if (t >= kStages && !warp_wait_or_abort(k_empty + 8 * st, (t / kStages - 1) & 1, s_abort)) break;
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i)
-        store_piece<D, S::kKBlock, false>(base + S::kK + st * S::kTileBytes, r0 + 8 * S::kProducers * i, k, pk[i]);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(valid_full + 8 * (t % kValidRing));
-        mbar_arrive(k_full + 8 * st);
-      }
-      if (t + 1 < n_tiles) {
-        resolve(t + 1);
-        load(0, pk);
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) next[i] = page_id(t + 2, r0 + 8 * S::kProducers * i);
-      }
-      if (t >= kStages && !warp_wait_or_abort(v_empty + 8 * st, (t / kStages - 1) & 1, s_abort)) break;
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i)
-        store_piece<D, S::kKBlock, true>(base + S::kV + st * S::kTileBytes, r0 + 8 * S::kProducers * i, k, pv[i]);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full + 8 * st);
-      if (t + 1 < n_tiles) load(1, pv);
-    }
-  } else if (lane == 0) {
-    // ---- products (one thread) ----------------------------------------------
-    constexpr uint32_t kIdescS = idesc_f16(128, kKeys, false);
-    constexpr uint32_t kIdescO = idesc_f16(128, D, true);
-    const uint64_t qdesc = sw128_desc(base, 16, 1024);
-    const uint64_t kdesc = sw128_desc(base + S::kK, 16, 1024);
-    const uint64_t vdesc = sw128_desc(base + S::kV, S::kKBlock, 1024);
-    auto scores = [&](int32_t t, int w) {           // S of row tile w (K is there)
-      const int st = t % kStages, buf = kTiles == 2 ? w : t & 1;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        mma_bf16(tmem + kSCol + kKeys * buf,
-                 qdesc + ((w * S::kQTile + (ks >> 2) * kBlockBytes + 32 * (ks & 3)) >> 4),
-                 kdesc + ((st * S::kTileBytes + (ks >> 2) * S::kKBlock + 32 * (ks & 3)) >> 4), kIdescS, ks != 0);
-      mma_commit(s_full + 8 * buf);
-      mma_issued = 1;
-    };
-    auto outputs = [&](int32_t t, int w) {          // O of row tile w += P V(t)
-      const int st = t % kStages, buf = kTiles == 2 ? w : t & 1;
-#pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks)
-        mma_bf16_ta(tmem + w * D, tmem + kSCol + kKeys * buf + 8 * ks, vdesc + ((st * S::kTileBytes + 2048 * ks) >> 4),
-                    kIdescO, (t > 0 || ks > 0) ? 1u : 0u);
-    };
-    auto have_k = [&](int32_t t) { return wait_or_abort(k_full + 8 * (t % kStages), (t / kStages) & 1, s_abort); };
-    auto have_v = [&](int32_t t) { return wait_or_abort(v_full + 8 * (t % kStages), (t / kStages) & 1, s_abort); };
-    if (n_tiles > 0 && have_k(0)) {
-      fence_after_sync();
-#pragma unroll
-      for (int w = 0; w < kTiles; ++w) scores(0, w);
-      mma_commit(k_empty);
-      for (int32_t t = 0; t < n_tiles; ++t) {
-        if constexpr (kTiles == 1) {
-          if (t + 1 < n_tiles) {
-            if (!have_k(t + 1)) break;
-            fence_after_sync();
-            scores(t + 1, 0);
-            mma_commit(k_empty + 8 * ((t + 1) % kStages));
-          }
-          if (!have_v(t) || !wait_or_abort(p_full, t & 1, s_abort)) break;
-          fence_after_sync();
-          outputs(t, 0);
-          mma_commit(v_empty + 8 * (t % kStages));
-          mma_commit(o_done);
-        } else {
-          bool ok = have_v(t);
-#pragma unroll
-          for (int w = 0; w < 2 && ok; ++w) {
-            ok = wait_or_abort(p_full + 8 * w, t & 1, s_abort);
-            if (!ok) break;
-            fence_after_sync();
-            outputs(t, w);
-            if (w == 1) mma_commit(v_empty + 8 * (t % kStages));
-            mma_commit(o_done + 8 * w);
-            if (t + 1 < n_tiles) {
-              if (w == 0) {
-                ok = have_k(t + 1);
-                if (!ok) break;
-                fence_after_sync();
-              }
-              scores(t + 1, w);
-              if (w == 1) mma_commit(k_empty + 8 * ((t + 1) % kStages));
-            }
-          }
-          if (!ok) break;
-        }
-      }
-    }
-  }
-
-  // Every role has left its loop: drain the products still in flight.
-  fence_before_sync();
-  const bool any_mma = __syncthreads_or(mma_issued) != 0;
-  fence_after_sync();
-  bool aborted = *s_abort != 0;
-  if (any_mma) {
-    if (threadIdx.x == S::kMmaWarp * 32) mma_commit(drain);
-    const long long start = clock64();
-    while (!mbar_try_wait(drain, 0)) {              // bounded, ignores the abort flag
-      if (clock64() - start > kDrainCycles) {
-        aborted = true;
-        break;
-      }
-    }
-  }
-  fence_after_sync();
-  if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
-  aborted = __syncthreads_or(aborted) != 0;
-  if (aborted && threadIdx.x == 0) report(a.status, KVQ_STATUS_TIMEOUT);
-
-  if (is_softmax) {
-    const bool live = row < rows && !aborted;
+    // the last products are done, one after the other: O is complete
+    if (done && n_tiles > 1) done = warp_wait_or_abort(o_done + 8 * tile, (n_tiles - 2) & 1, s_abort);
+    if (done && n_tiles > 0) done = warp_wait_or_abort(o_done + 8 * tile, (n_tiles - 1) & 1, s_abort);
+    fence_after_sync();
+    const bool live = row < rows && done;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
     const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
     const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
-    const uint32_t o_col = tmem + ((warp & 3) * 32u << 16) + tile * D;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       float o[32];
-      if (n_tiles > 0 && !aborted) {                // uniform over the CTA
+      if (n_tiles > 0 && done) {                    // uniform over the warp
         tmem_ld32(o_col + 32 * c, o);
       } else {
 #pragma unroll
@@ -582,14 +544,88 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       __syncwarp();                                 // the next load is the whole warp's
     }
     if (a.num_splits > 1) {
-      if (row < rows) a.part_lse[part] = aborted ? __uint_as_float(kAbandoned) : lse2;
+      if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
     } else if (live && a.lse != nullptr) {
       a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
+    }
+  } else {
+    fewer_registers<S::kOtherRegs>();
+    if (warp < S::kMmaWarp) {
+      produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
+                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, valid_full,
+                                valid_ring, s_abort);
+    } else if (warp > S::kMmaWarp) {
+      produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kMmaWarp - 1, lane, false, base, v_full, v_empty,
+                               valid_full, valid_ring, s_abort);
+    } else {
+      // ---- products (one elected lane; the warp waits together) --------------
+      constexpr uint32_t kIdescS = idesc_f16(128, kKeys, false);
+      constexpr uint32_t kIdescO = idesc_f16(128, D, true);
+      const uint32_t elected = elect_lane();
+      const uint64_t qdesc = sw128_desc(base, 16, 1024);
+      const uint64_t kdesc = sw128_desc(base + S::kK, 16, 1024);
+      const uint64_t vdesc = sw128_desc(base + S::kV, kKBlock, 1024);
+      auto scores = [&](int32_t t) {                // S of every row tile (K is there)
+        const uint64_t kd = kdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
+#pragma unroll
+        for (int w = 0; w < kTiles; ++w) {
+          const int buf = 2 * w + (t & 1);
+          const uint64_t qd = qdesc + ((w * S::kQTile) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            warp_mma(elected, tmem + kSCol + kKeys * buf, qd + (((ks >> 2) * kBlockBytes + 32 * (ks & 3)) >> 4),
+                     kd + (((ks >> 2) * kKBlock + 32 * (ks & 3)) >> 4), kIdescS, ks != 0);
+          warp_commit(elected, s_full + 8 * buf);
+        }
+        warp_commit(elected, k_empty + 8 * (t % S::kStages));
+      };
+      auto outputs = [&](int32_t t, int w) {        // O of row tile w += P V(t)
+        const uint32_t p_col = tmem + kSCol + kKeys * (2 * w + (t & 1));
+        const uint64_t vd = vdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          warp_mma_ta(elected, tmem + w * D, p_col + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
+                      (t > 0 || ks > 0) ? 1u : 0u);
+        warp_commit(elected, o_done + 8 * w);
+      };
+      auto have = [&](uint32_t bar, int32_t phase) {
+        const bool ok = warp_wait_or_abort(bar, phase & 1, s_abort);
+        fence_after_sync();
+        return ok;
+      };
+      if (n_tiles > 0 && have(q_full, 0) && have(k_full, 0)) {
+        scores(0);
+        bool ok = true;
+        for (int32_t t = 0; t < n_tiles && ok; ++t) {
+          if (t + 1 < n_tiles) {
+            if (!have(k_full + 8 * ((t + 1) % S::kStages), (t + 1) / S::kStages)) break;
+            scores(t + 1);
+          }
+          if (!have(v_full + 8 * (t % S::kStages), t / S::kStages)) break;
+#pragma unroll
+          for (int w = 0; w < kTiles; ++w) {
+            ok = ok && have(p_full + 8 * (2 * w + (t & 1)), t >> 1);
+            if (ok) outputs(t, w);
+          }
+          if (ok) warp_commit(elected, v_empty + 8 * (t % S::kStages));
+        }
+      }
+      // drain the products still in flight (bounded, whatever the abort flag says)
+      warp_commit(elected, drain);
+      const long long start = clock64();
+      while (!mbar_try_wait(drain, 0)) {
+        if (clock64() - start > kDrainCycles) {
+          *s_abort = 1;
+          break;
+        }
+      }
+      __syncwarp();
     }
   }
 
   fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0 && *s_abort) report(a.status, KVQ_STATUS_TIMEOUT);
   if (warp == 0) {
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
