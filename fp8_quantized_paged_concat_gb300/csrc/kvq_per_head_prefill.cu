@@ -17,17 +17,18 @@
 //   - shared memory: q in f16 (scaled by each row's power of two), K tiles and
 //     V tiles (64 x D f16, 128-byte swizzle, kStages of each), and a ring of
 //     raw entries per side;
-//   - four warps decode the keys and three the values: raw entries come in by
+//   - three warps decode the keys and three the values: raw entries come in by
 //     asynchronous copies, kRing - 1 chunks ahead (each warp copies what it
 //     decodes, so that it waits for no other); 8 lanes take 8 rows of a
 //     64-column block, so that their 16-byte stores fall in different banks;
-//   - one warp issues the products: per key tile t, S_w(t + 1) of every row
-//     tile, then O_w += P_w(t) V(t);
+//   - one warp issues the scores' products S_w(t) = Q_w K(t)^T, another the
+//     outputs' O_w += P_w(t) V(t): a wait costs either about 200 clocks, which
+//     the other's products cover;
 //   - four softmax warps per row tile, one thread per row, in one pass over
 //     the scores: the weights are formed against the reference maximum of the
-//     tiles before, and only when a score exceeds it by 2^8 is the pass
-//     repeated with the new one and O rescaled (after which the row's weights
-//     are again at most 1).
+//     tiles before, without a maximum of their own; only when their sum shows
+//     that one of them may exceed it by 2^8 is the tile's maximum taken, the
+//     pass repeated and O rescaled.
 // Every wait is bounded; on expiry the CTA records KVQ_STATUS_TIMEOUT, drains
 // its products, frees its tensor memory and leaves its rows unwritten.
 #include <type_traits>
@@ -39,6 +40,7 @@ namespace {
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;
+constexpr float kMaxWeight = 16384.0f;            // 2^(kShift + kGrow): far below f16's largest value
 constexpr int64_t kMaxPos = INT32_MAX - 256;      // positions stay below it (host check)
 constexpr int kKeys = 64;                         // keys per tile
 constexpr int kValidRing = 16;
@@ -47,13 +49,15 @@ constexpr uint32_t kKBlock = kKeys * 128;         // 64 dimensions of a key tile
 
 template <int D, int kTiles>
 struct Shape {
-  // warps: softmax, four that decode keys, the products', three that decode
-  // values; in whole warpgroups, whose registers are split by role (the
-  // threads start with an equal share, and the shares add up to no more)
+  // warps: softmax, three that decode keys, the one that issues the scores'
+  // products, three that decode values, the one that issues the outputs'; in
+  // whole warpgroups, whose registers are split by role (the threads start
+  // with an equal share, and the shares add up to no more)
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kKeyWarps = 4, kValueWarps = 3;
-  static constexpr int kMmaWarp = kSoftmaxWarps + kKeyWarps;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1 + kValueWarps);
+  static constexpr int kKeyWarps = 3, kValueWarps = 3;
+  static constexpr int kScoreWarp = kSoftmaxWarps + kKeyWarps;
+  static constexpr int kOutputWarp = kScoreWarp + 1 + kValueWarps;
+  static constexpr int kThreads = 32 * (kOutputWarp + 1);
   static constexpr int kStartRegs = kTiles == 2 ? 128 : 168;
   static constexpr int kSoftmaxRegs = kTiles == 2 ? 152 : 200;
   static constexpr int kOtherRegs = kTiles == 2 ? 104 : 144;
@@ -78,6 +82,12 @@ struct Shape {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static_assert(kTiles * D <= 256 && kMisc % 16 == 0, "tensor memory, alignment");
 };
+
+// warp_wait_or_abort whose usual case, the phase complete or completed while
+// the first try sleeps, takes no clock and no loop.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* s_abort) {
+  return __all_sync(kFull, mbar_try_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
+}
 
 // kind::f16 with f16 operands, fp32 sums; A is K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
@@ -166,9 +176,10 @@ __device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, co
 // ---------------------------------------------------------------------------
 //
 // kWarps warps share a chunk's rows in groups of 8: warp `me` takes groups me,
-// me + kWarps, ...; lane (k = lane / 8, lane % 8) takes dimensions k D / 4 ..
-// +D / 4 of row lane % 8 of its groups.  Page ids are loaded a chunk before
-// the copies that use them start, and looked at only there.
+// me + kWarps, ... in passes.  Lane l looks up row l of the warp's rows (pass
+// l / 8, row l % 8 of its group): page id, loaded a chunk before its copies
+// start and looked at only there, address, scale copy.  For the data of pass
+// i it is lane part k = l / 8 (dimensions k D / 4 .. +D / 4) of row l % 8.
 template <int D, int kTiles, bool kValues>
 __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, uint32_t head, const Keys<kKeys>& keys,
                                         int32_t s0, int32_t n_tiles, int me, int lane, bool bad_index, uint32_t base,
@@ -177,66 +188,68 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   using S = Shape<D, kTiles>;
   constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
   constexpr int kGroups = S::kChunk / 8, kPasses = (kGroups + kWarps - 1) / kWarps;
+  static_assert(kPasses <= 4, "a lane per row");
   const uint32_t k = lane >> 3;
   const uint32_t tiles = base + (kValues ? S::kV : S::kK), raw_ring = base + (kValues ? S::kRawV : S::kRawK);
   const int32_t chunks = n_tiles * S::kParts;
   const uint8_t* side = a.cache + (kValues ? a.region : 0);
   const int32_t* table = a.block_table + b * a.block_table_stride;
-  int32_t id[kPasses];                              // page ids of the next chunk to be copied
-  auto row_of = [&](int i) { return static_cast<uint32_t>(8 * (me + kWarps * i) + (lane & 7)); };
-  auto position = [&](int32_t h, int i) {           // of the lane's row in pass i of chunk h
-    return static_cast<uint32_t>(keys.base(s0 + h / S::kParts) + (h % S::kParts) * S::kChunk) + row_of(i);
-  };
-  auto load_ids = [&](int32_t h) {
-    if (h >= chunks) return;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      id[i] = -1;
-      const uint32_t p = position(h, i), col = a.block_div.div(p);
-      if (me + kWarps * i < kGroups && p < static_cast<uint32_t>(keys.limit(s0 + h / S::kParts)) &&
-          col < static_cast<uint32_t>(a.block_table_width))
-        id[i] = __ldg(table + col);
-    }
+  auto row_of = [&](int pass) { return static_cast<uint32_t>(8 * (me + kWarps * pass) + (lane & 7)); };
+  const uint32_t own_row = row_of(lane >> 3);       // of the warp's rows, the one this lane looks up
+  const bool has_row = own_row < S::kChunk && (lane >> 3) < kPasses;
+  uint32_t next_p = 0;                              // its position in the next chunk to be copied,
+  int32_t next_id = -1;                             // its page id, -1 where there is none to be had,
+  bool next_in = false;                             // and whether the position is one of the keys
+  auto look_up = [&](int32_t h) {
+    const int32_t step = s0 + h / S::kParts;
+    next_p = static_cast<uint32_t>(keys.base(step)) + (h % S::kParts) * S::kChunk + own_row;
+    next_in = has_row && h < chunks && next_p < static_cast<uint32_t>(keys.limit(step));
+    const uint32_t col = a.block_div.div(next_p);
+    next_id = -1;
+    if (next_in && col < static_cast<uint32_t>(a.block_table_width)) next_id = __ldg(table + col);
   };
   auto start = [&](int32_t h) {                     // one group of copies, empty past the last chunk
     if (h < chunks) {
-      const int32_t t = h / S::kParts;
-      const uint32_t limit = static_cast<uint32_t>(keys.limit(s0 + t));
       const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
+      const bool ok = next_in && next_id >= 0 && next_id < a.num_pages;
+      bad_index = bad_index || (next_in && !ok);
+      const uint32_t off = next_p - a.block_div.div(next_p) * static_cast<uint32_t>(a.block_size);
+      const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
+      const uint8_t* region = side + static_cast<int64_t>(next_id) * 2 * a.region;
+      const uint64_t data = reinterpret_cast<uint64_t>(ok ? region + row * (D / 2) : side);
+      if (has_row)
+        cp_async<D / 16>(raw + S::kRawScales + own_row * (D / 16), ok ? region + a.scales + row * (D / 16) : side,
+                         ok ? D / 16 : 0);
+      const uint32_t rows = __ballot_sync(kFull, ok);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
+        const int from = 8 * i + (lane & 7);
+        const uint64_t row_data =
+            static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(data >> 32), from)) << 32 |
+            __shfl_sync(kFull, static_cast<uint32_t>(data), from);
         if (me + kWarps * i >= kGroups) continue;   // uniform over the warp
-        const uint32_t r = row_of(i), p = position(h, i);
-        const bool ok = p < limit && id[i] >= 0 && id[i] < a.num_pages;
-        bad_index = bad_index || (p < limit && !ok);
-        const uint32_t off = p - a.block_div.div(p) * static_cast<uint32_t>(a.block_size);
-        const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
-        const uint8_t* region = side + static_cast<int64_t>(ok ? id[i] : 0) * 2 * a.region;
-        const uint8_t* src = ok ? region + row * (D / 2) + (D / 8) * k : side;
+        const bool there = (rows >> from) & 1;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(row_data) + (there ? (D / 8) * k : 0);
         constexpr int kPiece = D == 64 ? 8 : 16;
 #pragma unroll
         for (int j = 0; j < (D == 256 ? 2 : 1); ++j)
-          cp_async<kPiece>(raw + raw_offset<D>(r, k, j), src + 16 * j, ok ? kPiece : 0);
-        if (k == 0)
-          cp_async<D / 16>(raw + S::kRawScales + r * (D / 16), ok ? region + a.scales + row * (D / 16) : side,
-                           ok ? D / 16 : 0);
-        if constexpr (!kValues) {
-          // Which keys exist, for the softmax; a slot's last reader is long
-          // done (kRing - 1 chunks ahead of a tile whose buffers are free).
-          const uint32_t rows = __ballot_sync(kFull, ok);
-          if (lane == 0)
-            valid_ring[8 * (t % kValidRing) + (h % S::kParts) * (S::kChunk / 8) + me + kWarps * i] =
-                static_cast<uint8_t>(rows);
-        }
+          cp_async<kPiece>(raw + raw_offset<D>(row_of(i), k, j), src + 16 * j, there ? kPiece : 0);
+      }
+      // Which keys exist, for the softmax; a slot's last reader is long done
+      // (kRing - 1 chunks ahead of a tile whose buffers are free).
+      if constexpr (!kValues) {
+        if (lane < kPasses && me + kWarps * lane < kGroups)
+          valid_ring[8 * ((h / S::kParts) % kValidRing) + (h % S::kParts) * kGroups + me + kWarps * lane] =
+              static_cast<uint8_t>(rows >> (8 * lane));
       }
     }
     cp_commit();
   };
-  load_ids(0);
+  look_up(0);
 #pragma unroll
   for (int h = 0; h < S::kRing - 1; ++h) {
     start(h);
-    load_ids(h + 1);
+    look_up(h + 1);
   }
   for (int32_t h = 0; h < chunks; ++h) {
     const int32_t t = h / S::kParts;
@@ -244,15 +257,13 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     cp_wait<S::kRing - 2>();
     __syncwarp();                                   // chunk h is there, and chunk h - 1 has been read
     start(h + S::kRing - 1);
-    load_ids(h + S::kRing);
+    look_up(h + S::kRing);
     const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
     Piece<D> e[kPasses];                            // all read first, so that their latencies overlap
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (me + kWarps * i < kGroups) load_piece<D>(raw, raw + S::kRawScales, row_of(i), k, e[i]);
-    if (h % S::kParts == 0 && t >= S::kStages &&
-        !warp_wait_or_abort(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort))
-      break;
+    if (h % S::kParts == 0 && t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (me + kWarps * i < kGroups)
@@ -314,13 +325,13 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t base = smem_u32(smem);
   const uint32_t bar = base + S::kMisc;
   const uint32_t k_full = bar, k_empty = bar + 24, v_full = bar + 48, v_empty = bar + 72;   // [kStages] each
-  const uint32_t s_full = bar + 96, p_full = bar + 128;            // [row tile][buffer]
-  const uint32_t o_done = bar + 160, drain = bar + 176, q_full = bar + 184;                 // [row tile], 1, 1
-  const uint32_t valid_full = bar + 192;                           // [kValidRing]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 320);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 324);
+  const uint32_t s_full = bar + 96, p_full = bar + 128, o_done = bar + 160;                 // [row tile][buffer] each
+  const uint32_t drain = bar + 192, q_full = bar + 208;            // [2], 1
+  const uint32_t valid_full = bar + 216;                           // [kValidRing]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 344);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 348);
   uint8_t* valid_ring = smem + S::kMisc + 352;     // [kValidRing][8]: bit per key of the tile
-  static_assert(S::kStages <= 3 && 192 + 8 * kValidRing <= 320 && 352 + 8 * kValidRing <= 512, "barrier layout");
+  static_assert(S::kStages <= 3 && 216 + 8 * kValidRing <= 344 && 352 + 8 * kValidRing <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -338,10 +349,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(o_done + 8 * i, 1);
     for (int i = 0; i < kValidRing; ++i) mbar_init(valid_full + 8 * i, S::kKeyWarps);
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
     mbar_init(q_full, S::kSoftmaxWarps);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
 
-    float m = -INFINITY, l = 0.0f;
+    float m = has_row ? -INFINITY : 0.0f, l = 0.0f;
     bool done = true;
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
       // which of the tile's keys the row sees
       const int32_t p0 = keys.base(s0 + t);
-      if (!warp_wait_or_abort(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) {
+      if (!warp_wait(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) {
         done = false;
         break;
       }
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           see[c] = (c == 0 ? valid.x : valid.y) & w;
         }
       }
-      if (!warp_wait_or_abort(s_full + 8 * buf, (t >> 1) & 1, s_abort)) {
+      if (!warp_wait(s_full + 8 * buf, (t >> 1) & 1, s_abort)) {
         done = false;
         break;
       }
@@ -443,11 +455,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
 
       uint32_t s[64], p[32];
       tmem_ld64(s_col, s);
-      float top, sum;
-      // weights against the reference m: p, their sum, and the largest exponent
+      float sum;
+      // weights against the reference m: p and their sum
       auto pass = [&](float off, auto with_mask) {
         float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
           float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
@@ -456,38 +467,43 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
             z.y = (see[i >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
           }
-          tops[(i >> 1) & 3] = fmax3(tops[(i >> 1) & 3], z.x, z.y);
           const float2 w = make_float2(ex2(z.x), ex2(z.y));
           sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
           p[i >> 1] = pack_f16x2(w.x, w.y);
         }
         const float2 both = fadd2(sums[0], sums[1]);
         sum = both.x + both.y;
-        top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]);
       };
-      auto weights = [&](float off) {               // warp-uniform choice
+      auto weights = [&]() {                        // warp-uniform choice
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
         if (masked)
           pass(off, std::true_type{});
         else
           pass(off, std::false_type{});
       };
-      const float m_use = m == -INFINITY ? 0.0f : m;
-      weights(kShift - m_use);
-      const bool grow = top > -INFINITY && (m == -INFINITY || top > kShift + kGrow);
-      if (__any_sync(kFull, grow)) {
-        float alpha = 1.0f;
-        if (grow) {
-          const float m_new = top - kShift + m_use;
-          alpha = ex2(m - m_new);                   // 0 while m is -inf
-          m = m_new;
+      weights();
+      // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
+      // sum is takes a new reference, its tile's maximum (as its first tile).
+      if (__any_sync(kFull, m == -INFINITY || sum > kMaxWeight)) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const float z = __uint_as_float(s[i]) * sc;
+          if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
         }
-        weights(kShift - (m == -INFINITY ? 0.0f : m));
+        float alpha = 1.0f;
+        if (top > m && (m == -INFINITY || sum > kMaxWeight)) {
+          alpha = ex2(m - top);                     // 0 while m is -inf
+          m = top;
+        }
+        weights();
         l *= alpha;
         if (t > 0) {
           // O is rescaled once the product of the tile before is done.  (The
-          // barrier is waited on only here: the scores of tile t follow the
-          // product of tile t - 2, so the phase cannot be mistaken.)
-          if (!warp_wait_or_abort(o_done + 8 * tile, (t - 1) & 1, s_abort)) {
+          // barrier is waited on only here: the scores of tile t - 1 followed
+          // the product of tile t - 3 and that of tile t + 1 awaits this one's
+          // weights, so the phase cannot be mistaken.)
+          if (!warp_wait(o_done + 8 * (2 * tile + ((t - 1) & 1)), ((t - 1) >> 1) & 1, s_abort)) {
             done = false;
             break;
           }
@@ -509,9 +525,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
-    // the last products are done, one after the other: O is complete
-    if (done && n_tiles > 1) done = warp_wait_or_abort(o_done + 8 * tile, (n_tiles - 2) & 1, s_abort);
-    if (done && n_tiles > 0) done = warp_wait_or_abort(o_done + 8 * tile, (n_tiles - 1) & 1, s_abort);
+    // the last product is done: O is complete
+    if (done && n_tiles > 0)
+      done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
     fence_after_sync();
     const bool live = row < rows && done;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -550,76 +566,77 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     }
   } else {
     fewer_registers<S::kOtherRegs>();
-    if (warp < S::kMmaWarp) {
-      produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
-                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, valid_full,
-                                valid_ring, s_abort);
-    } else if (warp > S::kMmaWarp) {
-      produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kMmaWarp - 1, lane, false, base, v_full, v_empty,
-                               valid_full, valid_ring, s_abort);
-    } else {
-      // ---- products (one elected lane; the warp waits together) --------------
-      constexpr uint32_t kIdescS = idesc_f16(128, kKeys, false);
-      constexpr uint32_t kIdescO = idesc_f16(128, D, true);
-      const uint32_t elected = elect_lane();
-      const uint64_t qdesc = sw128_desc(base, 16, 1024);
-      const uint64_t kdesc = sw128_desc(base + S::kK, 16, 1024);
-      const uint64_t vdesc = sw128_desc(base + S::kV, kKBlock, 1024);
-      auto scores = [&](int32_t t) {                // S of every row tile (K is there)
-        const uint64_t kd = kdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
-#pragma unroll
-        for (int w = 0; w < kTiles; ++w) {
-          const int buf = 2 * w + (t & 1);
-          const uint64_t qd = qdesc + ((w * S::kQTile) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            warp_mma(elected, tmem + kSCol + kKeys * buf, qd + (((ks >> 2) * kBlockBytes + 32 * (ks & 3)) >> 4),
-                     kd + (((ks >> 2) * kKBlock + 32 * (ks & 3)) >> 4), kIdescS, ks != 0);
-          warp_commit(elected, s_full + 8 * buf);
-        }
-        warp_commit(elected, k_empty + 8 * (t % S::kStages));
-      };
-      auto outputs = [&](int32_t t, int w) {        // O of row tile w += P V(t)
-        const uint32_t p_col = tmem + kSCol + kKeys * (2 * w + (t & 1));
-        const uint64_t vd = vdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          warp_mma_ta(elected, tmem + w * D, p_col + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
-                      (t > 0 || ks > 0) ? 1u : 0u);
-        warp_commit(elected, o_done + 8 * w);
-      };
-      auto have = [&](uint32_t bar, int32_t phase) {
-        const bool ok = warp_wait_or_abort(bar, phase & 1, s_abort);
-        fence_after_sync();
-        return ok;
-      };
-      if (n_tiles > 0 && have(q_full, 0) && have(k_full, 0)) {
-        scores(0);
-        bool ok = true;
-        for (int32_t t = 0; t < n_tiles && ok; ++t) {
-          if (t + 1 < n_tiles) {
-            if (!have(k_full + 8 * ((t + 1) % S::kStages), (t + 1) / S::kStages)) break;
-            scores(t + 1);
-          }
-          if (!have(v_full + 8 * (t % S::kStages), t / S::kStages)) break;
-#pragma unroll
-          for (int w = 0; w < kTiles; ++w) {
-            ok = ok && have(p_full + 8 * (2 * w + (t & 1)), t >> 1);
-            if (ok) outputs(t, w);
-          }
-          if (ok) warp_commit(elected, v_empty + 8 * (t % S::kStages));
-        }
-      }
-      // drain the products still in flight (bounded, whatever the abort flag says)
-      warp_commit(elected, drain);
+    auto have = [&](uint32_t bar, int32_t phase) {
+      const bool ok = warp_wait(bar, phase & 1, s_abort);
+      fence_after_sync();
+      return ok;
+    };
+    // the warp's products still in flight are drained (bounded, whatever the abort flag says)
+    auto drained = [&](uint32_t elected, uint32_t bar) {
+      warp_commit(elected, bar);
       const long long start = clock64();
-      while (!mbar_try_wait(drain, 0)) {
+      while (!mbar_try_wait(bar, 0)) {
         if (clock64() - start > kDrainCycles) {
           *s_abort = 1;
           break;
         }
       }
       __syncwarp();
+    };
+    if (warp < S::kScoreWarp) {
+      produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
+                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, valid_full,
+                                valid_ring, s_abort);
+    } else if (warp == S::kScoreWarp) {
+      // ---- S_w(t) = Q_w K(t)^T (one elected lane; the warp waits together) -----
+      constexpr uint32_t kIdesc = idesc_f16(128, kKeys, false);
+      const uint32_t elected = elect_lane();
+      const uint64_t qdesc = sw128_desc(base, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
+      bool ok = n_tiles > 0 && have(q_full, 0);
+      for (int32_t t = 0; t < n_tiles && ok; ++t) {
+        ok = have(k_full + 8 * (t % S::kStages), t / S::kStages);
+        const uint64_t kd = kdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
+#pragma unroll
+        for (int w = 0; w < kTiles; ++w) {
+          // the buffer held the scores, then the weights, of tile t - 2
+          if (t >= 2) ok = ok && have(o_done + 8 * (2 * w + (t & 1)), (t >> 1) - 1);
+          if (!ok) break;
+          const uint64_t qd = qdesc + ((w * S::kQTile) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            warp_mma(elected, tmem + kSCol + kKeys * (2 * w + (t & 1)),
+                     qd + (((ks >> 2) * kBlockBytes + 32 * (ks & 3)) >> 4),
+                     kd + (((ks >> 2) * kKBlock + 32 * (ks & 3)) >> 4), kIdesc, ks != 0);
+          warp_commit(elected, s_full + 8 * (2 * w + (t & 1)));
+        }
+        if (ok) warp_commit(elected, k_empty + 8 * (t % S::kStages));
+      }
+      drained(elected, drain);
+    } else if (warp < S::kOutputWarp) {
+      produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
+                               v_empty, valid_full, valid_ring, s_abort);
+    } else {
+      // ---- O_w += P_w(t) V(t) ---------------------------------------------------
+      constexpr uint32_t kIdesc = idesc_f16(128, D, true);
+      const uint32_t elected = elect_lane();
+      const uint64_t vdesc = sw128_desc(base + S::kV, kKBlock, 1024);
+      bool ok = true;
+      for (int32_t t = 0; t < n_tiles && ok; ++t) {
+        ok = have(v_full + 8 * (t % S::kStages), t / S::kStages);
+        const uint64_t vd = vdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
+#pragma unroll
+        for (int w = 0; w < kTiles; ++w) {
+          ok = ok && have(p_full + 8 * (2 * w + (t & 1)), t >> 1);
+          if (!ok) break;
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            warp_mma_ta(elected, tmem + w * D, tmem + kSCol + kKeys * (2 * w + (t & 1)) + 8 * ks,
+                        vd + ((2048 * ks) >> 4), kIdesc, (t > 0 || ks > 0) ? 1u : 0u);
+          warp_commit(elected, o_done + 8 * (2 * w + (t & 1)));
+        }
+        if (ok) warp_commit(elected, v_empty + 8 * (t % S::kStages));
+      }
+      drained(elected, drain + 8);
     }
   }
 
