@@ -3,7 +3,8 @@
 Thin Python binding over libkvq.so (include/kvq.h): each function has the
 name of the C entry point, checks dtypes / devices / shapes of the torch
 tensors it is given, passes their data pointers and strides and the current
-CUDA stream, and raises RuntimeError on a non-OK status.  Every step of the
+CUDA stream, and raises RuntimeError on a non-OK status (through ctypes, or,
+for the calls that serve from the per-head cache, a small extension module).  Every step of the
 computation runs in the library's sm_103a kernels; there is no fallback.  The
 library is built by ``__graft_entry__.build()`` (or
 ``python -m fp8_quantized_paged_concat_gb300._build``); importing this
@@ -13,6 +14,8 @@ missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -29,7 +32,8 @@ __all__ = [
     "kvq_prefill_mla_attention_split_nvfp4_ds_mla", "kvq_prefill_mla_attention_split_fp8_ds_mla",
     "default_prefill_num_splits", "kvq_prefill_mla_attention_workspace",
     "kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
-    "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes", "default_per_head_num_splits",
+    "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
+    "kvq_per_head_attention_default_splits",
     "PER_HEAD_MAX_SPLITS",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
@@ -135,6 +139,8 @@ def load_library():
         handle.kvq_sparse_mla_attention_split_workspace_bytes.argtypes = [_I64, _I32, _I32]
         handle.kvq_per_head_attention_workspace_bytes.restype = _I64
         handle.kvq_per_head_attention_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32]
+        handle.kvq_per_head_attention_default_splits.restype = _I32
+        handle.kvq_per_head_attention_default_splits.argtypes = [_I32] * 9
         _lib = handle
     return _lib
 
@@ -573,98 +579,30 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 # serving from the per-head NVFP4 cache
 # --------------------------------------------------------------------------
 #
-# These calls run once per layer and decoded token, where the host's part of a
-# call can outlast the kernel: their checks build no message unless one fails,
-# and the current stream is asked for without making a Stream object.
+# These calls run once per layer and decoded token.  Their checks, allocations
+# and launch are in the extension module built beside the library
+# (csrc/kvq_binding.cpp): ValueError for tensors of the wrong type, shape or
+# device, RuntimeError for what the library refuses.
 
-_BF16, _F32, _I32T, _I64T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_sm_count = {}
-
-
-def _sms(device):
-    i = device if isinstance(device, int) else torch.device("cuda" if device is None else device).index
-    if i is None:
-        i = torch.cuda.current_device()
-    if i not in _sm_count:
-        _sm_count[i] = torch.cuda.get_device_properties(i).multi_processor_count
-    return _sm_count[i]
+_native = None
+_NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
+                   "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
+                   "kvq_per_head_attention_default_splits", "kvq_last_error_string")
 
 
-def _launch(index, stream, status, name, args):
-    """The library call `name` on device `index` (the library launches on the
-    current one), with the status word and the stream as its last arguments."""
-    if status is not None and (status.dtype is not _I32T or status.get_device() != index or status.numel() < 1):
-        raise ValueError(f"status: expected an int32 tensor on cuda:{index} with at least one element")
-    word = None if status is None else status.data_ptr()
-    if stream is None:
-        raw = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        if stream.device.index != index:
-            raise ValueError(f"stream: expected a stream of cuda:{index}, the tensors' device")
-        raw = stream.cuda_stream
-    else:
-        raw = int(stream)
-    if torch.cuda.current_device() == index:
-        _call(name, *args, word, raw)
-    else:
-        with torch.cuda.device(index):
-            _call(name, *args, word, raw)
-
-
-def _tensor(name, t, dtype, index, dims):
-    """A tensor of that type and rank on device `index`, its innermost stride 1."""
-    if (t.dtype is not dtype or t.get_device() != index or t.dim() != dims
-            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
-        raise ValueError(f"{name}: expected a CUDA {dtype} tensor of rank {dims} with unit inner stride on "
-                         f"cuda:{index}, got {t.dtype} of shape {tuple(t.shape)}, strides {t.stride()} on {t.device}")
-
-
-def _shaped(name, t, shape):
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _first(name, t):
-    """The device that the other tensors of the call have to be on: that of bf16 [T, H, D] heads."""
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    _tensor(name, t, _BF16, index, 3)
-    return index
-
-
-def _heads_strides(t):
-    """Token and head strides for the library (a dimension of one element may carry any stride)."""
-    T, H, D = t.shape
-    st, sh, _ = t.stride()
-    if H <= 1:
-        sh = D
-    return (st if T > 1 else H * sh), sh
-
-
-def _row_stride(t):
-    """Row stride of a 2-d tensor for the library (that of a single row may be anything)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _scale_ptr(name, t, index):
-    if t.dtype is not _F32 or t.get_device() != index or t.numel() < 1:
-        raise ValueError(f"{name}: expected an fp32 scalar on cuda:{index}")
-    return t.data_ptr()
-
-
-def _cache_shape(kv_cache, head_size, layout, index):
-    """(layout code, block_size, heads) of a contiguous per-head cache; head_size None: from the cache."""
-    if layout not in LAYOUTS:
-        raise ValueError(f"layout: expected one of {sorted(LAYOUTS)}, got {layout!r}")
-    _tensor("kv_cache", kv_cache, _U8, index, 5)
-    _, sides, a, b, full = kv_cache.shape
-    if sides != 2 or not kv_cache.is_contiguous() or full % 9 or (head_size is not None and full * 16 != head_size * 9):
-        inner = "block_size, H" if layout == "NHD" else "H, block_size"
-        raise ValueError(f"kv_cache: expected a contiguous [P, 2, {inner}, D/2 + D/16] tensor for layout {layout}"
-                         f"{'' if head_size is None else f' with D = {head_size}'}, got {tuple(kv_cache.shape)}")
-    return (0, a, b) if layout == "NHD" else (1, b, a)
+def _load_native():
+    """Loads the extension module (once) and hands it the library's entry points."""
+    global _native
+    path = os.path.join(_HERE, "_lib", "kvq_native.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+    handle = load_library()
+    loader = importlib.machinery.ExtensionFileLoader("kvq_native", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("kvq_native", loader))
+    loader.exec_module(module)
+    module.bind({name: ctypes.cast(getattr(handle, name), _P).value for name in _NATIVE_ENTRIES})
+    _native = module
+    return module
 
 
 def kvq_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float, interleaved=False, q_out=None,
@@ -676,34 +614,8 @@ def kvq_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float, i
     (rot_dim / 2 cosines, then sines; rot_dim a multiple of 16, at most D).
     Pairs are (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.  q_out /
     k_out may be q / k.  Returns (q_out, k_out)."""
-    index = _first("q", q)
-    T, H, D = q.shape
-    _tensor("k", k, _BF16, index, 3)
-    KH = k.shape[1]
-    _shaped("k", k, (T, KH, D))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _tensor(name, w, _BF16, index, 1)
-        _shaped(name, w, (D,))
-    _tensor("positions", positions, _I64T, index, 1)
-    _shaped("positions", positions, (T,))
-    _tensor("cos_sin", cos_sin, _F32, index, 2)
-    if q_out is None:
-        q_out = q.new_empty((T, H, D))
-    else:
-        _tensor("q_out", q_out, _BF16, index, 3)
-        _shaped("q_out", q_out, q.shape)
-    if k_out is None:
-        k_out = k.new_empty((T, KH, D))
-    else:
-        _tensor("k_out", k_out, _BF16, index, 3)
-        _shaped("k_out", k_out, k.shape)
-    max_position, rot = cos_sin.shape
-    _launch(index, stream, status, "kvq_qk_norm_rope",
-            (q.data_ptr(), *_heads_strides(q), k.data_ptr(), *_heads_strides(k), q_weight.data_ptr(),
-             k_weight.data_ptr(), positions.data_ptr(), T, H, KH, D, cos_sin.data_ptr(), _row_stride(cos_sin),
-             max_position, rot, 1 if interleaved else 0, eps, q_out.data_ptr(), *_heads_strides(q_out),
-             k_out.data_ptr(), *_heads_strides(k_out)))
-    return q_out, k_out
+    return (_native or _load_native()).norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, q_out,
+                                                 k_out, status, stream)
 
 
 def kvq_per_head_attention_workspace_bytes(num_tokens: int, num_heads: int, head_size: int, num_splits: int) -> int:
@@ -711,15 +623,13 @@ def kvq_per_head_attention_workspace_bytes(num_tokens: int, num_heads: int, head
     return load_library().kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits)
 
 
-def default_per_head_num_splits(max_query_len: int, num_heads: int, num_kv_heads: int, batch_size: int,
-                                max_seq_len: int, window: int = 0, num_sinks: int = 0, device=None) -> int:
-    """Key ranges of the per-head attention: as many as bring the CTAs to
-    four per SM, each with at least 256 keys, at most PER_HEAD_MAX_SPLITS."""
-    blocks = -(-max_query_len * (num_heads // num_kv_heads) // 16) * num_kv_heads * batch_size
-    keys = max_seq_len if window <= 0 else min(max_seq_len, window + max_query_len + num_sinks)
-    if blocks <= 0 or keys <= 0:
-        return 1
-    return max(1, min(PER_HEAD_MAX_SPLITS, keys // 256, 4 * _sms(device) // blocks))
+def kvq_per_head_attention_default_splits(max_query_len: int, num_heads: int, num_kv_heads: int, head_size: int,
+                                          batch_size: int, max_seq_len: int, window: int = 0, num_sinks: int = 0,
+                                          tree: bool = False) -> int:
+    """The key ranges per block of query rows that the per-head attention
+    uses on the current device when num_splits is left out."""
+    return load_library().kvq_per_head_attention_default_splits(max_query_len, num_heads, num_kv_heads, head_size,
+                                                                batch_size, max_seq_len, window, num_sinks, int(tree))
 
 
 def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, kv_cache, k_scale, v_scale,
@@ -733,13 +643,13 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     seq_lens[b] entries (int32 [B], at most max_seq_len), read through
     block_table int32 [B, W] from kv_cache (as kvq_reshape_and_cache_nvfp4
     wrote it, layout "NHD" or "HND").  num_splits (default:
-    default_per_head_num_splits) key ranges; workspace for more than one: a
-    CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
-    (allocated here when None).  Returns (out bf16 [T, H, D], lse fp32 [T,
-    H]); lse=False skips the lse output."""
-    return _per_head_attention("kvq_window_attention_nvfp4_per_head", q, query_start, seq_lens, None, block_table,
-                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, window,
-                               num_sinks, layout, num_splits, workspace, out, lse, status, stream)
+    kvq_per_head_attention_default_splits) key ranges; workspace for more than
+    one: a CUDA tensor of at least kvq_per_head_attention_workspace_bytes
+    bytes (allocated here when None).  Returns (out bf16 [T, H, D], lse fp32
+    [T, H]); lse=False skips the lse output."""
+    return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, k_scale, v_scale,
+                                                 softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
+                                                 num_splits, workspace, out, lse, status, stream)
 
 
 def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
@@ -750,58 +660,11 @@ def kvq_tree_attention_nvfp4_per_head(q, query_start, seq_lens, tree_mask, block
     context before the drafts and draft j iff bit j % 64 of tree_mask[token
     i, j // 64] (int64 [T, mask_words], 64 * mask_words >= max_query_len) is
     set.  The rest is as in kvq_window_attention_nvfp4_per_head."""
-    return _per_head_attention("kvq_tree_attention_nvfp4_per_head", q, query_start, seq_lens, tree_mask, block_table,
-                               kv_cache, k_scale, v_scale, softmax_scale, max_query_len, max_seq_len, 0, 0, layout,
-                               num_splits, workspace, out, lse, status, stream)
-
-
-def _per_head_attention(cname, q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale, v_scale,
-                        softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout, num_splits, workspace,
-                        out, lse, status, stream):
-    index = _first("q", q)
-    T, H, D = q.shape
-    code, block_size, KH = _cache_shape(kv_cache, D, layout, index)
-    _tensor("seq_lens", seq_lens, _I32T, index, 1)
-    B = seq_lens.shape[0]
-    _tensor("query_start", query_start, _I32T, index, 1)
-    _shaped("query_start", query_start, (B + 1,))
-    _tensor("block_table", block_table, _I32T, index, 2)
-    W = block_table.shape[1]
-    _shaped("block_table", block_table, (B, W))
-    if out is None:
-        out = q.new_empty((T, H, D))
-    else:
-        _tensor("out", out, _BF16, index, 3)
-        _shaped("out", out, q.shape)
-    if lse is None:
-        lse = torch.empty((T, H), dtype=_F32, device=q.device)
-    elif lse is not False:
-        _tensor("lse", lse, _F32, index, 2)
-        _shaped("lse", lse, (T, H))
-    if num_splits is None:
-        num_splits = default_per_head_num_splits(max_query_len, H, KH, B, max_seq_len, window, num_sinks,
-                                                 index) if KH else 1
-    if workspace is not None:
-        if workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
-    elif num_splits > 1 and T > 0:
-        workspace = torch.empty(max(0, kvq_per_head_attention_workspace_bytes(T, H, D, num_splits)), dtype=_U8,
-                                device=q.device)
-    mask = ()
-    if tree_mask is not None:
-        _tensor("tree_mask", tree_mask, _I64T, index, 2)
-        words = tree_mask.shape[1]
-        _shaped("tree_mask", tree_mask, (T, words))
-        mask = (tree_mask.data_ptr(), _row_stride(tree_mask), words)
-    _launch(index, stream, status, cname,
-            (q.data_ptr(), *_heads_strides(q), T, H, query_start.data_ptr(), seq_lens.data_ptr(), B, max_query_len,
-             *mask, block_table.data_ptr(), _row_stride(block_table), W, kv_cache.data_ptr(), kv_cache.shape[0],
-             block_size, code, KH, D, _scale_ptr("k_scale", k_scale, index), _scale_ptr("v_scale", v_scale, index),
-             softmax_scale, *(() if mask else (window, num_sinks)), out.data_ptr(), *_heads_strides(out),
-             None if lse is False else lse.data_ptr(), 0 if lse is False else _row_stride(lse), max_seq_len,
-             num_splits, None if workspace is None else workspace.data_ptr(),
-             0 if workspace is None else workspace.numel() * workspace.element_size()))
-    return out, (None if lse is False else lse)
+    if tree_mask is None:
+        raise ValueError("tree_mask: expected a tensor")
+    return (_native or _load_native()).attention(q, query_start, seq_lens, tree_mask, block_table, kv_cache, k_scale,
+                                                 v_scale, softmax_scale, max_query_len, max_seq_len, 0, 0, layout,
+                                                 num_splits, workspace, out, lse, status, stream)
 
 
 def kvq_compact_drafts_nvfp4_per_head(kv_cache, query_start, seq_lens, accepted, accepted_lens, block_table,
@@ -813,29 +676,8 @@ def kvq_compact_drafts_nvfp4_per_head(kv_cache, query_start, seq_lens, accepted,
     kv_cache: uint8 [P, 2, ...] as kvq_reshape_and_cache_nvfp4 takes it, or
     [L, P, 2, ...] for L layers that share the block table (each layer
     contiguous).  seq_lens is left to the caller."""
-    index = kv_cache.get_device()
-    if index < 0 or kv_cache.dim() not in (5, 6):
-        raise ValueError("kv_cache: expected a CUDA [P, 2, ...] or [L, P, 2, ...] tensor")
-    layers, layer_stride, one = 1, 0, kv_cache
-    if kv_cache.dim() == 6:
-        layers = kv_cache.shape[0]
-        if layers == 0:
-            return
-        layer_stride, one = kv_cache.stride(0), kv_cache[0]
-    code, block_size, KH = _cache_shape(one, None, layout, index)
-    _tensor("seq_lens", seq_lens, _I32T, index, 1)
-    B = seq_lens.shape[0]
-    for name, t, n in (("query_start", query_start, B + 1), ("accepted_lens", accepted_lens, B)):
-        _tensor(name, t, _I32T, index, 1)
-        _shaped(name, t, (n,))
-    for name, t in (("accepted", accepted), ("block_table", block_table)):
-        _tensor(name, t, _I32T, index, 2)
-        _shaped(name, t, (B, t.shape[1]))
-    _launch(index, stream, status, "kvq_compact_drafts_nvfp4_per_head",
-            (kv_cache.data_ptr(), layers, layer_stride, one.shape[0], block_size, code, KH, one.shape[4] // 9 * 16,
-             query_start.data_ptr(), seq_lens.data_ptr(), B, accepted.data_ptr(), _row_stride(accepted),
-             accepted_lens.data_ptr(), accepted.shape[1], block_table.data_ptr(), _row_stride(block_table),
-             block_table.shape[1]))
+    (_native or _load_native()).compact(kv_cache, query_start, seq_lens, accepted, accepted_lens, block_table, layout,
+                                        status, stream)
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

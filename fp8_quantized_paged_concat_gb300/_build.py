@@ -4,13 +4,15 @@ Each .cu file under csrc/ is compiled in parallel with nvcc for sm_103a only
 (precise division and square root, no fast math: the quantizers rely on
 IEEE-rounded divisions), then linked into
 fp8_quantized_paged_concat_gb300/_lib/libkvq.so against the shared CUDA
-runtime, the same one PyTorch loads.
+runtime, the same one PyTorch loads.  Beside it, and at the same time, the
+extension module kvq_native.so is compiled with g++ against PyTorch's headers.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "kvq")
 LIBRARY = os.path.join(PKG, "_lib", "libkvq.so")
+NATIVE = os.path.join(PKG, "_lib", "kvq_native.so")
 
 SOURCES = ["kvq_abi.cu", "kvq_write.cu", "kvq_gather.cu", "kvq_per_head.cu", "kvq_index.cu",
            "kvq_attention.cu", "kvq_selftest.cu", "kvq_norm_rope.cu", "kvq_per_head_attention.cu",
@@ -40,6 +43,34 @@ def _headers_mtime() -> float:
     paths += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
+
+
+def _older(path: str, than: float) -> bool:
+    return not os.path.exists(path) or os.path.getmtime(path) < than
+
+
+def build_native(force: bool = False) -> str:
+    """Compiles kvq_native.so, the extension module, if its source or PyTorch is newer."""
+    import torch
+
+    source = os.path.join(CSRC, "kvq_binding.cpp")
+    if not (force or _older(NATIVE, max(os.path.getmtime(source), os.path.getmtime(torch.__file__)))):
+        return NATIVE
+    os.makedirs(os.path.dirname(NATIVE), exist_ok=True)
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE + ".tmp.%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", source, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *("-I" + i for i in includes),
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath," + os.path.join(home, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on kvq_binding.cpp:\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), library: str = LIBRARY,
@@ -66,8 +97,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), library: s
                 print(r.stderr)
         return o
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        native = pool.submit(build_native, force or _older(NATIVE, hdr))
         objs = list(pool.map(compile_one, SOURCES))
+        native.result()
     if force or not os.path.exists(library) or os.path.getmtime(library) < max(map(os.path.getmtime, objs)):
         tmp = library + ".tmp.%d" % os.getpid()
         cmd = [compiler, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,

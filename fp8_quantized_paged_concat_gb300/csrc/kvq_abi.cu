@@ -930,6 +930,25 @@ int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_h
   return (num_tokens * num_heads * row + 15) / 16 * 16;
 }
 
+int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
+                                              int32_t head_size, int32_t batch_size, int32_t max_seq_len,
+                                              int32_t window, int32_t num_sinks, int32_t tree) {
+  if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || batch_size <= 0 || max_seq_len <= 0 ||
+      num_sinks < 0)
+    return 1;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  const int64_t rows = int64_t{max_query_len} * (num_heads / num_kv_heads);
+  int64_t keys = max_seq_len;
+  if (window > 0 && !tree) keys = std::min<int64_t>(keys, int64_t{window} + std::min(max_query_len, 256) + num_sinks);
+  const int64_t block = kvq::per_head_block_rows(rows, head_size);
+  const int64_t blocks = (rows + block - 1) / block * num_kv_heads * batch_size;
+  const bool few = block <= 16;                  // the kernel for few rows: four CTAs per SM
+  const int64_t want = (few ? 4 : 1) * static_cast<int64_t>(sms) / blocks;
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / 256, want})));
+}
+
 kvq_status kvq_window_attention_nvfp4_per_head(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
     const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,

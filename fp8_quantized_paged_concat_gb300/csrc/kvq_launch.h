@@ -231,6 +231,9 @@ struct PerHeadAttentionArgs {
   float* part_o;                  // fp32 [num_tokens, num_heads, num_splits, head_size], normalised
   float* part_lse;                // fp32 [num_tokens, num_heads, num_splits], base 2
 };
+// Query rows of a CTA's block in the kernel that a call with `rows` (token,
+// head) rows per request and key head takes.
+int64_t per_head_block_rows(int64_t rows, int32_t head_size);
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream);
 // Its kernel for many query rows per key head (without the join of ranges).
 cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream);

@@ -563,17 +563,23 @@ cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+int64_t per_head_block_rows(int64_t rows, int32_t head_size) {
+  if (rows <= 8) return 8;
+  if (rows <= 32) return head_size == 256 ? 8 : 16;  // two row tiles of D = 256 would not fit the registers
+  return rows <= 128 || head_size == 256 ? 128 : 256;
+}
+
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
+  const int64_t block = per_head_block_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size);
   cudaError_t e;
-  if (rows > 32)
+  if (block > 16)
     e = launch_per_head_prefill(a, stream);
   else if (a.head_size == 64)
-    e = rows <= 8 ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
+    e = block == 8 ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
   else if (a.head_size == 128)
-    e = rows <= 8 ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
+    e = block == 8 ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
   else
-    e = launch_rows<256, 1>(a, stream);              // two tiles would not fit the registers
+    e = launch_rows<256, 1>(a, stream);
   if (e != cudaSuccess || a.num_splits == 1) return e;
   return a.head_size == 64 ? launch_join<64>(a, stream)
                            : a.head_size == 128 ? launch_join<128>(a, stream) : launch_join<256>(a, stream);

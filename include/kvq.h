@@ -590,6 +590,15 @@ int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_h
                                                int32_t num_splits);
 
 /*
+ * kvq_per_head_attention_default_splits -- a good num_splits for the two
+ * attention entry points below on the current device, from the call's bounds
+ * (tree: 1 for the tree form).  1 for arguments that make no call.
+ */
+int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
+                                              int32_t head_size, int32_t batch_size, int32_t max_seq_len,
+                                              int32_t window, int32_t num_sinks, int32_t tree);
+
+/*
  * kvq_window_attention_nvfp4_per_head -- causal attention over the per-head
  * NVFP4 cache with a sliding window and a few first tokens that stay visible.
  * Request b < batch_size owns the query tokens [query_start[b],
