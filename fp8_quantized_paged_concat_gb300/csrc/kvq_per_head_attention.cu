@@ -121,59 +121,72 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   const uint32_t g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * St::kBytes);
 
-  // ---- asynchronous copies of one step ------------------------------------
+  // ---- asynchronous copies -------------------------------------------------
+  // Lane l looks up key l of a step: page id, loaded a step before the copies
+  // that use it start and looked at only there, address, scale copies; the
+  // data rows are copied 16 bytes a lane, kLanes lanes to a row.
+  const int32_t* table = a.block_table + b * a.block_table_stride;
   bool bad_index = rq.cut && threadIdx.x == 0;
-  uint32_t valid_ring[kStages];                  // per stage: bit i = key i of the step exists
-  auto issue = [&](int32_t step, int stage) -> uint32_t {
-    const int32_t base = keys.base(step), limit = keys.limit(step);
-    const int32_t p = base + lane;
-    int32_t page = -1, row = 0;
-    if (p < limit) {
-      const uint32_t col = a.block_div.div(static_cast<uint32_t>(p));
-      if (col < static_cast<uint32_t>(a.block_table_width))
-        page = __ldg(a.block_table + b * a.block_table_stride + col);
-      if (page < 0 || page >= a.num_pages) {
-        page = -1;
-        bad_index = true;
-      }
-      row = static_cast<int32_t>(p - col * static_cast<uint32_t>(a.block_size)) * a.row_offset +
-            static_cast<int32_t>(head) * a.row_head;
-    }
-    const uint32_t st = ring + stage * St::kBytes;
-    constexpr int kLanes = St::kRow / 16;        // lanes that copy one data row
+  uint32_t next_p = 0;                           // the lane's position in the next step to be copied,
+  int32_t next_id = -1;                          // its page id, -1 where there is none to be had,
+  bool next_in = false;                          // and whether the position is one of the keys
+  auto look_up = [&](int32_t step) {
+    next_p = static_cast<uint32_t>(keys.base(step)) + lane;
+    next_in = step < s1 && next_p < static_cast<uint32_t>(keys.limit(step));
+    const uint32_t col = a.block_div.div(next_p);
+    next_id = -1;
+    if (next_in && col < static_cast<uint32_t>(a.block_table_width)) next_id = __ldg(table + col);
+  };
+  // one group of copies (empty past the range); returns the step's keys that exist
+  auto start = [&](int32_t step, int stage) -> uint32_t {
+    uint32_t there = 0;
+    if (step < s1) {
+      const bool ok = next_in && next_id >= 0 && next_id < a.num_pages;
+      bad_index = bad_index || (next_in && !ok);
+      there = __ballot_sync(kFull, ok);
+      const uint32_t off = next_p - a.block_div.div(next_p) * static_cast<uint32_t>(a.block_size);
+      const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
+      const uint8_t* region = a.cache + static_cast<int64_t>(next_id) * 2 * a.region;
+      const uint32_t st = ring + stage * St::kBytes;
+      const uint8_t* scales = ok ? region + a.scales + row * St::kScales : a.cache;
+      cp_async<St::kScales>(st + St::kKs + lane * St::kScales, scales, ok ? St::kScales : 0);
+      cp_async<St::kScales>(st + St::kVs + lane * St::kScales, scales + (ok ? a.region : 0), ok ? St::kScales : 0);
+      const uint64_t data = reinterpret_cast<uint64_t>(ok ? region + row * St::kRow : a.cache);
+      constexpr int kLanes = St::kRow / 16;      // lanes that copy one data row
 #pragma unroll
-    for (int it = 0; it < kLanes; ++it) {
-      const int key = it * (32 / kLanes) + lane / kLanes;
-      const uint32_t chunk = lane % kLanes;
-      const int32_t pg = __shfl_sync(kFull, page, key), rw = __shfl_sync(kFull, row, key);
-      const uint8_t* src = a.cache;
-      if (pg >= 0) src += static_cast<int64_t>(pg) * 2 * a.region + static_cast<int64_t>(rw) * St::kRow + 16 * chunk;
-      const uint32_t n = pg >= 0 ? 16 : 0;
-      cp_async<16>(st + key * St::kRow + 16 * k_chunk<D>(key, chunk), src, n);
-      cp_async<16>(st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk), pg >= 0 ? src + a.region : src, n);
+      for (int it = 0; it < kLanes; ++it) {
+        const int key = it * (32 / kLanes) + lane / kLanes;
+        const uint32_t chunk = lane % kLanes;
+        const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(data >> 32), key)) << 32 |
+                            __shfl_sync(kFull, static_cast<uint32_t>(data), key);
+        const bool have = (there >> key) & 1;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(at) + 16 * chunk;
+        cp_async<16>(st + key * St::kRow + 16 * k_chunk<D>(key, chunk), have ? src : a.cache, have ? 16 : 0);
+        cp_async<16>(st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk), have ? src + a.region : a.cache,
+                     have ? 16 : 0);
+      }
     }
-    const uint8_t* src = a.cache;
-    if (page >= 0) src += static_cast<int64_t>(page) * 2 * a.region + a.scales + static_cast<int64_t>(row) * St::kScales;
-    const uint32_t n = page >= 0 ? St::kScales : 0;
-    cp_async<St::kScales>(st + St::kKs + lane * St::kScales, src, n);
-    cp_async<St::kScales>(st + St::kVs + lane * St::kScales, page >= 0 ? src + a.region : src, n);
-    return __ballot_sync(kFull, page >= 0);
+    cp_commit();
+    return there;
   };
   // this warp's steps: first, first + kWarps, ...
   const int32_t first = s0 + warp;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    valid_ring[i] = first + i * kWarps < s1 ? issue(first + i * kWarps, i) : 0;
-    cp_commit();
-  }
+  uint32_t valid_ring[2];                        // of the two steps in flight: bit i = key i exists
+  static_assert(kStages == 3, "two steps in flight");
+  look_up(first);
+  valid_ring[0] = start(first, 0);
+  look_up(first + kWarps);
+  valid_ring[1] = start(first + kWarps, 1);
+  look_up(first + 2 * kWarps);
 
   // ---- the query rows ------------------------------------------------------
   // Lane (g, c) holds dimensions [c D/4, +D/4) of row 8 nt + g, scaled by a
   // power of two; the score of row 2c + x is multiplied back by sc.
   uint32_t q[kRowTiles][kKSteps][2];
-  float sc[kRowTiles][2];
+  float sc[kRowTiles][2], hidden[kRowTiles][2];
   int32_t pos_hi[kRowTiles][2], pos_lo[kRowTiles][2];     // window: last visible key, first inside the window
   int64_t q_token[kRowTiles][2];                          // tree: the row's token
+  float m[kRowTiles][2], l[kRowTiles][2];                 // reference maximum, sum
   const float scale = a.scale_log2 * __ldg(a.k_scale);
 #pragma unroll
   for (int nt = 0; nt < kRowTiles; ++nt) {
@@ -210,12 +223,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     for (int x = 0; x < 2; ++x) {
       // row 2c + x of the tile is loaded by the lanes with g = 2c + x
       sc[nt][x] = __shfl_sync(kFull, back, (2 * c + x) * 4);
+      if (sc[nt][x] == 0.0f) sc[nt][x] = 1e-30f;            // as good as 0 for any score, but 0 for no infinity
+      hidden[nt][x] = sc[nt][x] < 0.0f ? INFINITY : -INFINITY;
       const int32_t rr = 8 * nt + 2 * c + x;
       const uint32_t tk = a.group_div.div(static_cast<uint32_t>(row0 + min(rr, rows - 1)));
       const int64_t p = rq.first_pos + tk;
       pos_hi[nt][x] = rr < rows ? static_cast<int32_t>(max(int64_t{-1}, p)) : -1;
       pos_lo[nt][x] = a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, p - a.window + 1)) : 0;
       q_token[nt][x] = rq.token0 + tk;
+      m[nt][x] = rr < rows ? -INFINITY : 0.0f;
+      l[nt][x] = 0.0f;
     }
   }
   // a step inside these positions is visible to every row
@@ -223,15 +240,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   const int32_t all_lo =
       a.tree_mask == nullptr && a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, rq.first_pos + t1 - a.window + 1)) : 0;
 
-  float m[kRowTiles][2], l[kRowTiles][2];
   float o[kDimTiles][kRowTiles][4];
 #pragma unroll
-  for (int nt = 0; nt < kRowTiles; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.0f;
+  for (int t = 0; t < kDimTiles; ++t)
 #pragma unroll
-    for (int t = 0; t < kDimTiles; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
-  }
+    for (int nt = 0; nt < kRowTiles; ++nt) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
 
   const uint32_t rg = key_row(g), r0 = key_row(2 * c), r1 = key_row(2 * c + 1);
   int stage = 0;
@@ -240,15 +253,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     __syncwarp();                                // the step has landed, and the stage before it has been read
     const uint32_t valid = valid_ring[0];
     valid_ring[0] = valid_ring[1];
-    {
-      const int32_t ahead = step + (kStages - 1) * kWarps;
-      const int st = stage == 0 ? kStages - 1 : stage - 1;
-      valid_ring[1] = ahead < s1 ? issue(ahead, st) : 0;
-      cp_commit();
-    }
+    valid_ring[1] = start(step + 2 * kWarps, stage == 0 ? 2 : stage - 1);
+    look_up(step + 3 * kWarps);
     const uint32_t st = ring + stage * St::kBytes;
     stage = stage + 1 == kStages ? 0 : stage + 1;
-    static_assert(kStages == 3, "two steps in flight");
 
     // ---- S^T = K Q^T -------------------------------------------------------
     float s[2][kRowTiles][4];
@@ -306,41 +314,59 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     // s[mt][nt][2 y + x]: key 16 mt + 8 y + key_row(g), query row 8 nt + 2 c + x
     const int32_t base = keys.base(step);
     const bool all = valid == kFull && base + kStep - 1 <= all_hi && (base >= all_lo || base + kStep <= a.num_sinks);
+    if (!all) {
+#pragma unroll
+      for (int nt = 0; nt < kRowTiles; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t i = 8 * e + rg, p = base + i;      // e = 2 mt + y
+            bool see = (valid >> i) & 1;
+            if (a.tree_mask == nullptr) {
+              see = see && p <= pos_hi[nt][x] && (p >= pos_lo[nt][x] || p < a.num_sinks);
+            } else if (see && p >= rq.first_pos) {
+              const int32_t d = static_cast<int32_t>(p - rq.first_pos);
+              see = (d >> 6) < a.tree_words &&
+                    ((__ldg(a.tree_mask + q_token[nt][x] * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
+            }
+            // hidden: the score whose scaled value is -inf
+            if (!see) s[e >> 1][nt][2 * (e & 1) + x] = hidden[nt][x];
+          }
+    }
+    // Weights against the reference m, the maximum of steps before: no
+    // maximum of their own is taken unless their sum shows that one of them
+    // may exceed it by 2^kGrow (or there is no reference yet).
+    float2 w[kRowTiles][4], sum[kRowTiles];
+    auto weights = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < kRowTiles; ++nt) {
+        const float2 off = make_float2(kShift - (m[nt][0] == -INFINITY ? 0.0f : m[nt][0]),
+                                       kShift - (m[nt][1] == -INFINITY ? 0.0f : m[nt][1]));
+        sum[nt] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* v = &s[e >> 1][nt][2 * (e & 1)];
+          const float2 z = ffma2(make_float2(v[0], v[1]), make_float2(sc[nt][0], sc[nt][1]), off);
+          w[nt][e] = make_float2(ex2(z.x), ex2(z.y));
+          sum[nt] = fadd2(sum[nt], w[nt][e]);
+        }
+      }
+    };
+    weights();
     bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < kRowTiles; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float& v = s[mt][nt][2 * y + x];
-            v *= sc[nt][x];
-            if (!all) {
-              const int32_t i = 16 * mt + 8 * y + rg, p = base + i;
-              bool see = (valid >> i) & 1;
-              if (a.tree_mask == nullptr) {
-                see = see && p <= pos_hi[nt][x] && (p >= pos_lo[nt][x] || p < a.num_sinks);
-              } else if (see && p >= rq.first_pos) {
-                const int32_t d = static_cast<int32_t>(p - rq.first_pos);
-                see = (d >> 6) < a.tree_words &&
-                      ((__ldg(a.tree_mask + q_token[nt][x] * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
-              }
-              if (!see) v = -INFINITY;
-            }
-            top = fmaxf(top, v);
-          }
-        grow |= top > m[nt][x] + kGrow;
-      }
+      grow = grow || sum[nt].x > kMaxWeight || sum[nt].y > kMaxWeight || m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
     if (__any_sync(kFull, grow)) {
 #pragma unroll
       for (int nt = 0; nt < kRowTiles; ++nt) {
         float alpha[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float top = fmaxf(fmaxf(s[0][nt][x], s[0][nt][2 + x]), fmaxf(s[1][nt][x], s[1][nt][2 + x]));
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, s[e >> 1][nt][2 * (e & 1) + x] * sc[nt][x]);
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -359,21 +385,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
           o[t][nt][3] *= alpha[1];
         }
       }
+      weights();
     }
     uint32_t p[2][kRowTiles][2];                 // P^T, keys 2c, 2c + 1 and 8 on, of query row g
 #pragma unroll
     for (int nt = 0; nt < kRowTiles; ++nt) {
-      const float off0 = kShift - (m[nt][0] == -INFINITY ? 0.0f : m[nt][0]);
-      const float off1 = kShift - (m[nt][1] == -INFINITY ? 0.0f : m[nt][1]);
+      l[nt][0] += sum[nt].x;
+      l[nt][1] += sum[nt].y;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float w0 = ex2(s[mt][nt][2 * y] + off0), w1 = ex2(s[mt][nt][2 * y + 1] + off1);
-          l[nt][0] += w0;
-          l[nt][1] += w1;
-          p[mt][nt][y] = transpose8(pack_f16x2(w0, w1));
-        }
+      for (int e = 0; e < 4; ++e) p[e >> 1][nt][e & 1] = transpose8(pack_f16x2(w[nt][e].x, w[nt][e].y));
     }
 
     // ---- O^T += V^T P^T ----------------------------------------------------

@@ -14,6 +14,7 @@ namespace {
 // reference m lags the true maximum by at most kGrow: they stay below 2^14.
 constexpr float kGrow = 8.0f;
 constexpr float kShift = 6.0f;
+constexpr float kMaxWeight = 16384.0f;            // 2^(kShift + kGrow), far below f16's largest value
 constexpr float kLn2 = 0.69314718055994530942f;
 // Base-2 log-sum-exp of a key range whose CTA gave up: its rows stay unwritten.
 constexpr uint32_t kAbandoned = 0x7fc0deadu;

@@ -40,7 +40,6 @@ namespace {
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;
-constexpr float kMaxWeight = 16384.0f;            // 2^(kShift + kGrow): far below f16's largest value
 constexpr int64_t kMaxPos = INT32_MAX - 256;      // positions stay below it (host check)
 constexpr int kKeys = 64;                         // keys per tile
 constexpr int kValidRing = 16;

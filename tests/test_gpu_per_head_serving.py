@@ -268,6 +268,15 @@ def test_strides_and_extreme_queries(kvq, new):
     assert np.all(out[:, :, 128:].cpu().numpy().view(np.uint16) == CANARY)
 
 
+@pytest.mark.parametrize("new", [1, 50])
+def test_scale_signs(kvq, new):
+    """Scales of zero and below it: uniform weights over the visible keys, and the order of the scores reversed."""
+    for scale in (0.0, -0.11):
+        b = Batch([(75, new), (40, new)], 8, 2, 128, 16, "NHD", 20)
+        b.scale = scale
+        check(kvq.kvq_window_attention_nvfp4_per_head(**b.device(), window=40, num_sinks=3), b.want(window=40, sinks=3))
+
+
 @pytest.mark.parametrize("new", [1, 64])
 def test_offsets_past_32_bits(kvq, new):
     """Pages more than 2^32 bytes into the cache."""
