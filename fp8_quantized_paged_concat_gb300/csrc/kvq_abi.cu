@@ -830,8 +830,9 @@ kvq_status per_head_attention(
   int64_t region = 0;
   if (kvq_status s = check_per_head_cache(fn, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size, &region))
     return s;
-  KVQ_REQUIRE(region % 16 == 0, "%s: block_size * num_kv_heads * (head_size / 2 + head_size / 16) must be a multiple "
-              "of 16 (got %lld)", fn, static_cast<long long>(region));
+  KVQ_REQUIRE(region % 16 == 0 && region < (int64_t{1} << 31),
+              "%s: block_size * num_kv_heads * (head_size / 2 + head_size / 16) must be a multiple of 16 below 2^31 "
+              "(got %lld)", fn, static_cast<long long>(region));
   if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
   if (kvq_status s = check_heads(fn, "out", out, out_stride_t, out_stride_h, num_heads, head_size, true)) return s;
   KVQ_REQUIRE(lse == nullptr || (aligned(lse, 4) && lse_stride_t >= num_heads),
@@ -883,8 +884,8 @@ kvq_status per_head_attention(
   a.num_pages = num_pages;
   a.block_size = block_size;
   a.block_div = kvq::FastDiv::make(static_cast<uint32_t>(block_size));
-  a.region = region;
-  a.scales = int64_t{block_size} * num_kv_heads * (head_size / 2);
+  a.region = static_cast<uint32_t>(region);
+  a.scales = static_cast<uint32_t>(int64_t{block_size} * num_kv_heads * (head_size / 2));
   a.row_offset = layout == KVQ_LAYOUT_HND ? 1 : num_kv_heads;
   a.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
   a.k_scale = k_scale;

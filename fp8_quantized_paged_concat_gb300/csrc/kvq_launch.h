@@ -208,8 +208,8 @@ struct PerHeadAttentionArgs {
   int64_t num_pages;
   int32_t block_size;
   FastDiv block_div;
-  int64_t region;                 // bytes of one (page, side): K at 2 * page * region, V one region on
-  int64_t scales;                 // offset of the scale rows inside a region
+  uint32_t region;                // bytes of one (page, side), < 2^31: K at 2 * page * region, V one region on
+  uint32_t scales;                // offset of the scale rows inside a region
   int32_t row_offset, row_head;   // row of (offset, head) = offset * row_offset + head * row_head
   const float* k_scale;
   const float* v_scale;

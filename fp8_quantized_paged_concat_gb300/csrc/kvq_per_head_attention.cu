@@ -126,32 +126,27 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   // that use it start and looked at only there, address, scale copies; the
   // data rows are copied 16 bytes a lane, kLanes lanes to a row.
   const int32_t* table = a.block_table + b * a.block_table_stride;
+  const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
   bool bad_index = rq.cut && threadIdx.x == 0;
-  uint32_t next_p = 0;                           // the lane's position in the next step to be copied,
-  int32_t next_id = -1;                          // its page id, -1 where there is none to be had,
-  bool next_in = false;                          // and whether the position is one of the keys
+  LookUp next;                                   // the lane's key of the next step to be copied
   auto look_up = [&](int32_t step) {
-    next_p = static_cast<uint32_t>(keys.base(step)) + lane;
-    next_in = step < s1 && next_p < static_cast<uint32_t>(keys.limit(step));
-    const uint32_t col = a.block_div.div(next_p);
-    next_id = -1;
-    if (next_in && col < static_cast<uint32_t>(a.block_table_width)) next_id = __ldg(table + col);
+    const uint32_t p = static_cast<uint32_t>(keys.base(step)) + lane;
+    next = look_up_position(a, table, head_row, step < s1 && p < static_cast<uint32_t>(keys.limit(step)), p);
   };
   // one group of copies (empty past the range); returns the step's keys that exist
   auto start = [&](int32_t step, int stage) -> uint32_t {
     uint32_t there = 0;
     if (step < s1) {
-      const bool ok = next_in && next_id >= 0 && next_id < a.num_pages;
-      bad_index = bad_index || (next_in && !ok);
+      const bool ok = next.in && next.id >= 0 && next.id < a.num_pages;
+      bad_index = bad_index || (next.in && !ok);
       there = __ballot_sync(kFull, ok);
-      const uint32_t off = next_p - a.block_div.div(next_p) * static_cast<uint32_t>(a.block_size);
-      const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
-      const uint8_t* region = a.cache + static_cast<int64_t>(next_id) * 2 * a.region;
+      const uint8_t* page = at_offset(a.cache, ok ? next.id : 0, 2 * a.region);   // some page where there is none
+      const uint32_t row = ok ? next.row : 0;
       const uint32_t st = ring + stage * St::kBytes;
-      const uint8_t* scales = ok ? region + a.scales + row * St::kScales : a.cache;
+      const uint8_t* scales = at_offset(page + a.scales, row, St::kScales);
       cp_async<St::kScales>(st + St::kKs + lane * St::kScales, scales, ok ? St::kScales : 0);
-      cp_async<St::kScales>(st + St::kVs + lane * St::kScales, scales + (ok ? a.region : 0), ok ? St::kScales : 0);
-      const uint64_t data = reinterpret_cast<uint64_t>(ok ? region + row * St::kRow : a.cache);
+      cp_async<St::kScales>(st + St::kVs + lane * St::kScales, scales + a.region, ok ? St::kScales : 0);
+      const uint64_t data = reinterpret_cast<uint64_t>(at_offset(page, row, St::kRow));
       constexpr int kLanes = St::kRow / 16;      // lanes that copy one data row
 #pragma unroll
       for (int it = 0; it < kLanes; ++it) {
@@ -159,11 +154,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         const uint32_t chunk = lane % kLanes;
         const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(data >> 32), key)) << 32 |
                             __shfl_sync(kFull, static_cast<uint32_t>(data), key);
-        const bool have = (there >> key) & 1;
         const uint8_t* src = reinterpret_cast<const uint8_t*>(at) + 16 * chunk;
-        cp_async<16>(st + key * St::kRow + 16 * k_chunk<D>(key, chunk), have ? src : a.cache, have ? 16 : 0);
-        cp_async<16>(st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk), have ? src + a.region : a.cache,
-                     have ? 16 : 0);
+        const uint32_t k_dst = st + key * St::kRow + 16 * k_chunk<D>(key, chunk);
+        const uint32_t v_dst = st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk);
+        const uint32_t n = (there >> key) & 1 ? 16 : 0;
+        cp_async<16>(k_dst, src, n);
+        cp_async<16>(v_dst, src + a.region, n);
       }
     }
     cp_commit();
@@ -293,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         const uint32_t fa = bits(e4m3x2_to_half2(sa >> (16 * i))), fb = bits(e4m3x2_to_half2(sb >> (16 * i)));
 #pragma unroll
         for (int j = 0; j < (D == 64 ? 2 : 4); ++j) {   // 8 dimensions: two 16-wide product steps
-          const uint32_t sel = (j >> 1) && D != 64 ? 0x3232 : 0x1010;
-          const uint32_t sfa = prmt(fa, fa, sel), sfb = prmt(fb, fb, sel);
+          // (the broadcast of one half is an operand modifier of the product)
+          const uint32_t sfa = (j >> 1) && D != 64 ? high_both(fa) : low_both(fa);
+          const uint32_t sfb = (j >> 1) && D != 64 ? high_both(fb) : low_both(fb);
           uint32_t ha[4], hb[4];
           e2m1x8(wa[j], ha);
           e2m1x8(wb[j], hb);
@@ -407,8 +404,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
         uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
         uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
-        sx = finite_scales(sx);
-        sy = finite_scales(sy);
+        if (!all) {                              // else no entry of the step is hidden from any row
+          sx = finite_scales(sx);
+          sy = finite_scales(sy);
+        }
         uint32_t w[4][2];
         auto load = [&](uint32_t row, uint32_t (&d)[2]) {
           if constexpr (D == 64) {

@@ -22,6 +22,8 @@ constexpr uint32_t kAbandoned = 0x7fc0deadu;
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return bits(__hmul2(half2_of(a), half2_of(b))); }
+__device__ __forceinline__ uint32_t low_both(uint32_t w) { return bits(__low2half2(half2_of(w))); }
+__device__ __forceinline__ uint32_t high_both(uint32_t w) { return bits(__high2half2(half2_of(w))); }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
 
 // The four bytes of w (two e2m1 codes each) as f16 pairs: one conversion per
@@ -97,10 +99,32 @@ struct Keys {
   int32_t sink_steps, steps;
 
   __device__ __forceinline__ int32_t base(int32_t step) const {
-    return step < sink_steps ? step * kStep : lo + (step - sink_steps) * kStep;
+    return step * kStep + (step < sink_steps ? 0 : lo - sink_steps * kStep);
   }
   __device__ __forceinline__ int32_t limit(int32_t step) const { return step < sink_steps ? sinks : hi; }
 };
+
+// One lane's look-up of a position: its page id, loaded a step before the
+// copies that need it start and looked at only there, and its row.
+struct LookUp {
+  uint32_t row;                // of (position, head) in its page's side region
+  int32_t id;                  // page id, -1 where there is none to be had
+  bool in;                     // the position is one of the keys
+};
+__device__ __forceinline__ LookUp look_up_position(const PerHeadAttentionArgs& a, const int32_t* table, uint32_t head_row,
+                                                   bool in, uint32_t p) {
+  LookUp u;
+  const uint32_t col = a.block_div.div(p);
+  u.in = in;
+  u.row = (p - col * static_cast<uint32_t>(a.block_size)) * static_cast<uint32_t>(a.row_offset) + head_row;
+  u.id = -1;
+  if (in && col < static_cast<uint32_t>(a.block_table_width)) u.id = __ldg(table + col);
+  return u;
+}
+// a + b c in 64 bits, b and c 32 (one instruction).
+__device__ __forceinline__ const uint8_t* at_offset(const uint8_t* a, uint32_t b, uint32_t c) {
+  return a + static_cast<uint64_t>(b) * c;
+}
 
 struct Request {
   int64_t token0;              // its first query token

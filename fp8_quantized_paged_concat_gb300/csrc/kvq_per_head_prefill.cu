@@ -161,7 +161,7 @@ __device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, co
     if constexpr (kValues) s2 = finite_scales(s2);
 #pragma unroll
     for (int j = 0; j < (D == 64 ? 2 : 4); ++j) {
-      const uint32_t sf = prmt(s2, s2, j < 2 ? 0x1010 : 0x3232);
+      const uint32_t sf = j < 2 ? low_both(s2) : high_both(s2);
       uint32_t h[4];
       e2m1x8(e.w[4 * p + j], h);
       st_shared16(base ^ ((chunk0 + 4 * p + j) << 4),
@@ -196,28 +196,23 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   auto row_of = [&](int pass) { return static_cast<uint32_t>(8 * (me + kWarps * pass) + (lane & 7)); };
   const uint32_t own_row = row_of(lane >> 3);       // of the warp's rows, the one this lane looks up
   const bool has_row = own_row < S::kChunk && (lane >> 3) < kPasses;
-  uint32_t next_p = 0;                              // its position in the next chunk to be copied,
-  int32_t next_id = -1;                             // its page id, -1 where there is none to be had,
-  bool next_in = false;                             // and whether the position is one of the keys
+  const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
+  LookUp next;                                      // its position in the next chunk to be copied
   auto look_up = [&](int32_t h) {
     const int32_t step = s0 + h / S::kParts;
-    next_p = static_cast<uint32_t>(keys.base(step)) + (h % S::kParts) * S::kChunk + own_row;
-    next_in = has_row && h < chunks && next_p < static_cast<uint32_t>(keys.limit(step));
-    const uint32_t col = a.block_div.div(next_p);
-    next_id = -1;
-    if (next_in && col < static_cast<uint32_t>(a.block_table_width)) next_id = __ldg(table + col);
+    const uint32_t p = static_cast<uint32_t>(keys.base(step)) + (h % S::kParts) * S::kChunk + own_row;
+    next = look_up_position(a, table, head_row, has_row && h < chunks && p < static_cast<uint32_t>(keys.limit(step)), p);
   };
   auto start = [&](int32_t h) {                     // one group of copies, empty past the last chunk
     if (h < chunks) {
       const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
-      const bool ok = next_in && next_id >= 0 && next_id < a.num_pages;
-      bad_index = bad_index || (next_in && !ok);
-      const uint32_t off = next_p - a.block_div.div(next_p) * static_cast<uint32_t>(a.block_size);
-      const int64_t row = static_cast<int64_t>(off) * a.row_offset + static_cast<int64_t>(head) * a.row_head;
-      const uint8_t* region = side + static_cast<int64_t>(next_id) * 2 * a.region;
-      const uint64_t data = reinterpret_cast<uint64_t>(ok ? region + row * (D / 2) : side);
+      const bool ok = next.in && next.id >= 0 && next.id < a.num_pages;
+      bad_index = bad_index || (next.in && !ok);
+      const uint8_t* region = at_offset(side, ok ? next.id : 0, 2 * a.region);    // some page where there is none
+      const uint32_t row = ok ? next.row : 0;
+      const uint64_t data = reinterpret_cast<uint64_t>(at_offset(region, row, D / 2));
       if (has_row)
-        cp_async<D / 16>(raw + S::kRawScales + own_row * (D / 16), ok ? region + a.scales + row * (D / 16) : side,
+        cp_async<D / 16>(raw + S::kRawScales + own_row * (D / 16), at_offset(region + a.scales, row, D / 16),
                          ok ? D / 16 : 0);
       const uint32_t rows = __ballot_sync(kFull, ok);
 #pragma unroll
@@ -228,7 +223,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
             __shfl_sync(kFull, static_cast<uint32_t>(data), from);
         if (me + kWarps * i >= kGroups) continue;   // uniform over the warp
         const bool there = (rows >> from) & 1;
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(row_data) + (there ? (D / 8) * k : 0);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(row_data) + (D / 8) * k;
         constexpr int kPiece = D == 64 ? 8 : 16;
 #pragma unroll
         for (int j = 0; j < (D == 256 ? 2 : 1); ++j)

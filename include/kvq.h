@@ -629,8 +629,8 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * of num_kv_heads.  out: the same shape, rows not overlapping.  lse: fp32
  * [num_tokens, num_heads], token stride lse_stride_t, or NULL.  kv_cache,
  * layout, k_scale, v_scale: as kvq_reshape_and_cache_nvfp4, and block_size *
- * num_kv_heads * full_dim a multiple of 16 and block_table_width * block_size
- * below 2^31 - 256.  query_start: int32 [batch_size + 1]; seq_lens: int32
+ * num_kv_heads * full_dim a multiple of 16 below 2^31 and block_table_width *
+ * block_size below 2^31 - 256.  query_start: int32 [batch_size + 1]; seq_lens: int32
  * [batch_size]; batch_size <= 65535.
  * num_splits: key ranges per block of query rows (1 ..
  * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU;
