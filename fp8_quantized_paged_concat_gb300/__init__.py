@@ -34,7 +34,7 @@ __all__ = [
     "kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
     "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
     "kvq_per_head_attention_default_splits",
-    "PER_HEAD_MAX_SPLITS",
+    "PER_HEAD_MAX_SPLITS", "PER_HEAD_CLUSTER_SPLITS",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -49,6 +49,7 @@ STATUS_TIMEOUT = 0x4
 ATTN_MAX_SPLITS = 32
 NOALLOC_SCRATCH_BYTES = 24 << 20
 PER_HEAD_MAX_SPLITS = 128
+PER_HEAD_CLUSTER_SPLITS = 8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -140,7 +141,7 @@ def load_library():
         handle.kvq_per_head_attention_workspace_bytes.restype = _I64
         handle.kvq_per_head_attention_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32]
         handle.kvq_per_head_attention_default_splits.restype = _I32
-        handle.kvq_per_head_attention_default_splits.argtypes = [_I32] * 9
+        handle.kvq_per_head_attention_default_splits.argtypes = [_I32] * 9 + [_P]
         _lib = handle
     return _lib
 
@@ -625,11 +626,15 @@ def kvq_per_head_attention_workspace_bytes(num_tokens: int, num_heads: int, head
 
 def kvq_per_head_attention_default_splits(max_query_len: int, num_heads: int, num_kv_heads: int, head_size: int,
                                           batch_size: int, max_seq_len: int, window: int = 0, num_sinks: int = 0,
-                                          tree: bool = False) -> int:
+                                          tree: bool = False) -> tuple:
     """The key ranges per block of query rows that the per-head attention
-    uses on the current device when num_splits is left out."""
-    return load_library().kvq_per_head_attention_default_splits(max_query_len, num_heads, num_kv_heads, head_size,
-                                                                batch_size, max_seq_len, window, num_sinks, int(tree))
+    uses on the current device when num_splits is left out, and whether they
+    join through a workspace."""
+    use_workspace = _I32(0)
+    splits = load_library().kvq_per_head_attention_default_splits(
+        max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks, int(tree),
+        ctypes.byref(use_workspace))
+    return splits, bool(use_workspace.value)
 
 
 def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, kv_cache, k_scale, v_scale,
@@ -643,10 +648,11 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     seq_lens[b] entries (int32 [B], at most max_seq_len), read through
     block_table int32 [B, W] from kv_cache (as kvq_reshape_and_cache_nvfp4
     wrote it, layout "NHD" or "HND").  num_splits (default:
-    kvq_per_head_attention_default_splits) key ranges; workspace for more than
-    one: a CUDA tensor of at least kvq_per_head_attention_workspace_bytes
-    bytes (allocated here when None).  Returns (out bf16 [T, H, D], lse fp32
-    [T, H]); lse=False skips the lse output."""
+    kvq_per_head_attention_default_splits) key ranges, joined inside clusters
+    (up to PER_HEAD_CLUSTER_SPLITS, no workspace) or through a workspace: a
+    CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
+    (allocated here when one is needed and None is given).  Returns (out bf16
+    [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, k_scale, v_scale,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)

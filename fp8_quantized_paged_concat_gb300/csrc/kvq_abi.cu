@@ -855,7 +855,8 @@ kvq_status per_head_attention(
   const int32_t group = num_heads / num_kv_heads;
   KVQ_REQUIRE((int64_t{max_query_len} * group + 7) / 8 * num_kv_heads * num_splits < (int64_t{1} << 31),
               "%s: max_query_len * num_heads * num_splits too large", fn);
-  if (num_splits > 1) {
+  const bool cluster = num_splits > 1 && num_splits <= KVQ_PER_HEAD_CLUSTER_SPLITS && workspace == nullptr;
+  if (num_splits > 1 && !cluster) {
     const int64_t need = kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits);
     KVQ_REQUIRE(need >= 0 && workspace != nullptr && aligned(workspace, 16) && workspace_bytes >= need,
                 "%s: workspace must be non-NULL, 16-byte aligned and at least %lld bytes (got %lld)", fn,
@@ -905,7 +906,8 @@ kvq_status per_head_attention(
   a.lse_stride_t = lse_stride_t;
   a.status = d_status;
   a.num_splits = num_splits;
-  if (num_splits > 1) {
+  a.cluster = cluster;
+  if (num_splits > 1 && !cluster) {
     // ranges of whole 128-key steps, sized from the keys that a row block can
     // see: the whole sequence, or the window, a block's other tokens and the sinks
     int64_t span = max_seq_len;
@@ -933,21 +935,18 @@ int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_h
 
 int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
                                               int32_t head_size, int32_t batch_size, int32_t max_seq_len,
-                                              int32_t window, int32_t num_sinks, int32_t tree) {
+                                              int32_t window, int32_t num_sinks, int32_t tree,
+                                              int32_t* use_workspace) {
+  if (use_workspace != nullptr) *use_workspace = 0;
   if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || batch_size <= 0 || max_seq_len <= 0 ||
       num_sinks < 0)
     return 1;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 1;
-  const int64_t rows = int64_t{max_query_len} * (num_heads / num_kv_heads);
-  int64_t keys = max_seq_len;
-  if (window > 0 && !tree) keys = std::min<int64_t>(keys, int64_t{window} + std::min(max_query_len, 256) + num_sinks);
-  const int64_t block = kvq::per_head_block_rows(rows, head_size);
-  const int64_t blocks = (rows + block - 1) / block * num_kv_heads * batch_size;
-  const bool few = block <= 16;                  // the kernel for few rows: four CTAs per SM
-  const int64_t want = (few ? 4 : 1) * static_cast<int64_t>(sms) / blocks;
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / 256, want})));
+  return kvq::per_head_default_splits(max_query_len, num_heads / num_kv_heads, num_kv_heads, head_size, batch_size,
+                                      max_seq_len, tree ? 0 : window, num_sinks, sms, use_workspace);
 }
 
 kvq_status kvq_window_attention_nvfp4_per_head(

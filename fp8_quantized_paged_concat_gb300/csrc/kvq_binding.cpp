@@ -283,16 +283,22 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check("lse", lse, at::kFloat, dev, 2);
       shaped("lse", lse, {T, H});
     }
-    const int32_t splits = a[14] == Py_None
-                               ? lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window,
-                                                    sinks, tree)
-                               : int32("num_splits", a[14]);
+    // the ranges of a block join in a cluster, or through a workspace
+    int32_t use_workspace = 0;
+    int32_t splits;
+    if (a[14] == Py_None) {
+      splits = lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks, tree,
+                                  &use_workspace);
+    } else {
+      splits = int32("num_splits", a[14]);
+      use_workspace = splits > KVQ_PER_HEAD_CLUSTER_SPLITS;
+    }
     at::Tensor workspace;
     if (a[15] != Py_None) {
       workspace = tensor("workspace", a[15]);
       if (!workspace.is_cuda() || workspace.get_device() != dev || !workspace.is_contiguous())
         bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
-    } else if (splits > 1 && T > 0) {
+    } else if (use_workspace && T > 0) {
       const int64_t bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
       if (bytes > 0) workspace = at::empty({bytes}, q.options().dtype(at::kByte));
     }

@@ -38,6 +38,8 @@
 // that largest value, and what is lost below is under 2^-39 of it.  The
 // weights are kept as 2^(s - m + 6) with m at most 2^8 behind the true
 // maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
+#include <algorithm>
+
 #include "kvq_per_head_attention.cuh"
 
 namespace kvq {
@@ -92,10 +94,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   constexpr int kRows = 8 * kRowTiles;
   constexpr int kKSteps = D / 16;                // 16-dimension steps of K Q^T
   constexpr int kDimTiles = D / 16;              // 16-dimension tiles of V^T P^T
-  // (key head, row block, range); heads vary fastest, so that the heads of a
-  // token, neighbours in an NHD page, are read at about the same time
-  const uint32_t head = blockIdx.x % a.num_kv_heads, rest = blockIdx.x / a.num_kv_heads;
-  const int32_t rb = rest % row_blocks, split = rest / row_blocks;
+  const Place place = place_of(a, row_blocks);
+  const uint32_t head = place.head;
+  const int32_t rb = place.row_block, split = place.split;
   const int b = blockIdx.y;
   Request rq;
   if (!request_of(a, b, rq)) {
@@ -109,12 +110,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   const int32_t t0 = a.group_div.div(static_cast<uint32_t>(row0));
   const int32_t t1 = a.group_div.div(static_cast<uint32_t>(row0 + rows - 1));
   const Keys<kStep> keys = keys_of<kStep>(a, rq, t0, t1);
-  int32_t s0 = 0, s1 = keys.steps;
-  if (a.num_splits > 1) {
-    const int64_t per = a.split_keys / kStep;
-    s0 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), split * per));
-    if (split < a.num_splits - 1) s1 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), (split + 1) * per));
-  }
+  int32_t s0, s1;
+  range_of(a, keys, split, s0, s1);
 
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -470,15 +467,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         *reinterpret_cast<float2*>(dst + 2 * t) = make_float2(o[t][nt][x], o[t][nt][2 + x]);
     }
   __syncthreads();
-  const float v_scale = __ldg(a.v_scale);
+  __shared__ float cm[kRows], cl[kRows];         // of the four warps together, for the cluster
   for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
     const int r = i / (D / 8), d = (i % (D / 8)) * 8;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, jm[w][r]);
-    float sum = 0.0f, acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+    float sum = 0.0f, acc[8] = {};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       // a warp that saw nothing holds zeros
@@ -489,25 +484,35 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       acc[0] += f * u.x; acc[1] += f * u.y; acc[2] += f * u.z; acc[3] += f * u.w;
       acc[4] += f * v.x; acc[5] += f * v.y; acc[6] += f * v.z; acc[7] += f * v.w;
     }
+    if (a.cluster) {                             // in the place of the first warp's, read by this thread only
+      float4* dst = reinterpret_cast<float4*>(jo + r * D + d);
+      dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (d == 0) {
+        cm[r] = top;
+        cl[r] = sum;
+      }
+      continue;
+    }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const float lse2 = sum == 0.0f ? -INFINITY : top + (log2f(sum) - kShift);
-    const uint32_t flat = static_cast<uint32_t>(row0 + r), tk = a.group_div.div(flat);
-    const int64_t token = rq.token0 + tk;
-    const int32_t h = head * a.group + (flat - tk * a.group);
+    const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + r));
     if (a.num_splits > 1) {
-      const int64_t pr = (token * a.num_heads + h) * a.num_splits + split;
+      const int64_t pr = (at.token * a.num_heads + at.head) * a.num_splits + split;
       float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + d);
       dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
       dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
       if (d == 0) a.part_lse[pr] = lse2;
     } else {
-      const float f = inv * v_scale;
-      st16(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t + h * a.out_stride_h + d,
+      const float f = inv * __ldg(a.v_scale);
+      st16(static_cast<__nv_bfloat16*>(a.out) + at.token * a.out_stride_t + at.head * a.out_stride_h + d,
            make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
                       pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f)));
-      if (d == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = lse2 * kLn2;
+      if (d == 0 && a.lse != nullptr) a.lse[at.token * a.lse_stride_t + at.head] = lse2 * kLn2;
     }
   }
+  if (a.cluster)
+    join_cluster(a, rq, head, row0, rows, split, D, smem_u32(jo), 4 * D, smem_u32(cm), smem_u32(cl));
 }
 
 // Joins the ranges of every row: with L_s the base-2 log-sum-exp of range s
@@ -568,8 +573,8 @@ cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
   const int64_t blocks = (rows + 8 * kRowTiles - 1) / (8 * kRowTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  per_head_attention_kernel<D, kRowTiles><<<grid, kThreads, kSmem, stream>>>(a, static_cast<int32_t>(blocks));
-  return cudaGetLastError();
+  return launch_ranges(per_head_attention_kernel<D, kRowTiles>, a, grid, kThreads, kSmem, static_cast<int32_t>(blocks),
+                       stream);
 }
 
 template <int D>
@@ -588,6 +593,34 @@ int64_t per_head_block_rows(int64_t rows, int32_t head_size) {
   return rows <= 128 || head_size == 256 ? 128 : 256;
 }
 
+int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t num_kv_heads, int32_t head_size,
+                                int64_t batch_size, int64_t max_seq_len, int64_t window, int64_t num_sinks, int sms,
+                                int32_t* use_workspace) {
+  const int64_t rows = max_query_len * group, block = per_head_block_rows(rows, head_size);
+  const int64_t blocks = (rows + block - 1) / block * num_kv_heads * batch_size;
+  const bool few = block <= 16;
+  const int64_t resident = (few ? 4 : 1) * static_cast<int64_t>(sms);
+  const bool windowed = window > 0 && window < max_seq_len;
+  const int64_t keys =
+      windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
+  const int64_t least = few ? 128 : 256;             // keys of a range: a step per warp, four tiles
+  if (blocks >= resident / 2) {
+    // The GPU is full: ranges only even out requests of different lengths (a
+    // window's are all alike), four to a CTA's place.
+    if (windowed || blocks >= 4 * resident) return 1;
+    const int64_t n = std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / 1024, (4 * resident + blocks - 1) / blocks});
+    if (n <= 1) return 1;
+    if (use_workspace != nullptr) *use_workspace = 1;
+    return static_cast<int32_t>(n);
+  }
+  // The call is short of CTAs: up to a cluster's ranges cost no second launch.
+  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / least, resident / blocks}));
+  if (n <= KVQ_PER_HEAD_CLUSTER_SPLITS) return static_cast<int32_t>(n);
+  if (keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least) return KVQ_PER_HEAD_CLUSTER_SPLITS;
+  if (use_workspace != nullptr) *use_workspace = 1;
+  return static_cast<int32_t>(n);
+}
+
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t block = per_head_block_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size);
   cudaError_t e;
@@ -599,7 +632,7 @@ cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_
     e = block == 8 ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
   else
     e = launch_rows<256, 1>(a, stream);
-  if (e != cudaSuccess || a.num_splits == 1) return e;
+  if (e != cudaSuccess || a.num_splits == 1 || a.cluster) return e;
   return a.head_size == 64 ? launch_join<64>(a, stream)
                            : a.head_size == 128 ? launch_join<128>(a, stream) : launch_join<256>(a, stream);
 }

@@ -279,10 +279,10 @@ template <int D, int kTiles>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
   using S = Shape<D, kTiles>;
-  // (key head, row block, range): heads vary fastest; the last row blocks of a
-  // causal chunk, which see the most keys, come first
-  const uint32_t head = blockIdx.x % a.num_kv_heads, rest = blockIdx.x / a.num_kv_heads;
-  const int32_t rb = row_blocks - 1 - static_cast<int32_t>(rest % row_blocks), split = rest / row_blocks;
+  // the last row blocks of a causal chunk, which see the most keys, come first
+  const Place place = place_of(a, row_blocks);
+  const uint32_t head = place.head;
+  const int32_t rb = row_blocks - 1 - place.row_block, split = place.split;
   const int b = blockIdx.y;
   Request rq;
   if (!request_of(a, b, rq)) {                     // uniform over the CTA, as every return up here
@@ -296,20 +296,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const int32_t t0 = a.group_div.div(static_cast<uint32_t>(row0));
   const int32_t t1 = a.group_div.div(static_cast<uint32_t>(row0 + rows - 1));
   const Keys<kKeys> keys = keys_of<kKeys>(a, rq, t0, t1);
-  int32_t s0 = 0, s1 = keys.steps;
-  if (a.num_splits > 1) {
-    const int64_t per = a.split_keys / kKeys;
-    s0 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), split * per));
-    if (split < a.num_splits - 1) s1 = static_cast<int32_t>(min(static_cast<int64_t>(keys.steps), (split + 1) * per));
-    if (s0 == s1) {
-      // an empty range: it weighs nothing when the ranges are joined
-      for (int r = threadIdx.x; r < rows; r += S::kThreads) {
-        const uint32_t flat = static_cast<uint32_t>(row0 + r), tk = a.group_div.div(flat);
-        const int64_t row = (rq.token0 + tk) * a.num_heads + head * a.group + (flat - tk * a.group);
-        a.part_lse[row * a.num_splits + split] = -INFINITY;
-      }
-      return;
+  int32_t s0, s1;
+  range_of(a, keys, split, s0, s1);
+  if (a.num_splits > 1 && !a.cluster && s0 == s1) {
+    // an empty range: it weighs nothing when the ranges are joined
+    for (int r = threadIdx.x; r < rows; r += S::kThreads) {
+      const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + r));
+      a.part_lse[(at.token * a.num_heads + at.head) * a.num_splits + split] = -INFINITY;
     }
+    return;
   }
   const int32_t n_tiles = s1 - s0;
 
@@ -358,6 +353,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
 
+  float m = -INFINITY, l = 0.0f;                    // softmax: reference maximum, sum
+  bool done = true;                                 // and whether every wait of the row's was met
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
     more_registers<S::kSoftmaxRegs>();
@@ -407,8 +404,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
 
-    float m = has_row ? -INFINITY : 0.0f, l = 0.0f;
-    bool done = true;
+    if (!has_row) m = 0.0f;
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
     for (int32_t t = 0; t < n_tiles; ++t) {
@@ -523,40 +519,42 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
     fence_after_sync();
-    const bool live = row < rows && done;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
-    const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
-    const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
+    if (!a.cluster) {
+      const bool live = row < rows && done;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
+      const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
+      const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      if (n_tiles > 0 && done) {                    // uniform over the warp
-        tmem_ld32(o_col + 32 * c, o);
-      } else {
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (n_tiles > 0 && done) {                    // uniform over the warp
+          tmem_ld32(o_col + 32 * c, o);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+        if (live && a.num_splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
+                                                q_head * a.out_stride_h + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                                pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
+                                pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+        }
+        __syncwarp();                                 // the next load is the whole warp's
       }
-      if (live && a.num_splits > 1) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-      } else if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
-                                              q_head * a.out_stride_h + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                              pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
-                              pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+      if (a.num_splits > 1) {
+        if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
+      } else if (live && a.lse != nullptr) {
+        a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
       }
-      __syncwarp();                                 // the next load is the whole warp's
-    }
-    if (a.num_splits > 1) {
-      if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
-    } else if (live && a.lse != nullptr) {
-      a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
     }
   } else {
     fewer_registers<S::kOtherRegs>();
@@ -637,6 +635,38 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *s_abort) report(a.status, KVQ_STATUS_TIMEOUT);
+  if (a.cluster) {
+    // O rows -> shared memory (q, K and V are no longer read), padded by 16
+    // bytes against bank conflicts; then the cluster's ranges are joined
+    constexpr uint32_t kStride = 4 * D + 16;
+    static_assert(128 * kTiles * kStride <= S::kMisc, "the rows fit");
+    __shared__ float cm[128 * kTiles], cl[128 * kTiles];
+    if (warp < S::kSoftmaxWarps) {
+      fence_after_sync();
+      const uint32_t to = base + threadIdx.x * kStride;
+      const uint32_t o_col = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (n_tiles > 0 && done) {                  // uniform over the warp
+          tmem_ld32(o_col + 32 * c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared16(to + 128 * c + 16 * i, make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                                        __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])));
+      }
+      cm[threadIdx.x] = done ? (l == 0.0f ? -INFINITY : m) : __uint_as_float(kAbandoned);
+      cl[threadIdx.x] = l;
+    }
+    asm volatile("" ::: "memory");                  // st_shared16 carries no clobber
+    join_cluster(a, rq, head, row0, rows, split, D, base, kStride, smem_u32(cm), smem_u32(cl));
+    fence_before_sync();
+    __syncthreads();
+  }
   if (warp == 0) {
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
@@ -651,8 +681,8 @@ cudaError_t launch(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (static_cast<int64_t>(a.max_query_len) * a.group + 128 * kTiles - 1) / (128 * kTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  per_head_prefill_kernel<D, kTiles><<<grid, S::kThreads, S::kSmem, stream>>>(a, static_cast<int32_t>(blocks));
-  return cudaGetLastError();
+  return launch_ranges(per_head_prefill_kernel<D, kTiles>, a, grid, S::kThreads, S::kSmem, static_cast<int32_t>(blocks),
+                       stream);
 }
 
 }  // namespace

@@ -579,10 +579,11 @@ kvq_status kvq_qk_norm_rope(
     int32_t* d_status, kvq_stream_t stream);
 
 #define KVQ_PER_HEAD_MAX_SPLITS 128    /* key ranges of the per-head attention */
+#define KVQ_PER_HEAD_CLUSTER_SPLITS 8  /* of them, as many as need no workspace */
 
 /*
  * kvq_per_head_attention_workspace_bytes -- bytes of workspace that the two
- * attention entry points below need with num_splits > 1: num_tokens *
+ * attention entry points below need to join through it: num_tokens *
  * num_heads * num_splits * (head_size + 1) * 4, rounded up to 16.  -1 for a
  * non-positive argument or a size past INT64_MAX / 2.
  */
@@ -592,11 +593,13 @@ int64_t kvq_per_head_attention_workspace_bytes(int64_t num_tokens, int32_t num_h
 /*
  * kvq_per_head_attention_default_splits -- a good num_splits for the two
  * attention entry points below on the current device, from the call's bounds
- * (tree: 1 for the tree form).  1 for arguments that make no call.
+ * (tree: 1 for the tree form), and in *use_workspace (may be NULL) whether it
+ * is meant with a workspace.  1, without, for arguments that make no call.
  */
 int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
                                               int32_t head_size, int32_t batch_size, int32_t max_seq_len,
-                                              int32_t window, int32_t num_sinks, int32_t tree);
+                                              int32_t window, int32_t num_sinks, int32_t tree,
+                                              int32_t* use_workspace);
 
 /*
  * kvq_window_attention_nvfp4_per_head -- causal attention over the per-head
@@ -633,12 +636,15 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * block_size below 2^31 - 256.  query_start: int32 [batch_size + 1]; seq_lens: int32
  * [batch_size]; batch_size <= 65535.
  * num_splits: key ranges per block of query rows (1 ..
- * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU;
- * above 1, the ranges (sized from max_seq_len, which bounds seq_lens; a longer
- * sequence is attended in full all the same, its last range taking the rest)
- * write partial results to `workspace` (16-byte aligned,
+ * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU.  With
+ * workspace = NULL (at most KVQ_PER_HEAD_CLUSTER_SPLITS ranges) a block's
+ * ranges are equal shares of its keys, run as one thread-block cluster and
+ * join there.  With a workspace (16-byte aligned, at least
  * kvq_per_head_attention_workspace_bytes; overwritten, no other call may use
- * it while this one runs) and a second launch joins them.
+ * it while this one runs) the ranges are sized from max_seq_len, which bounds
+ * seq_lens, the same for every request (a longer sequence is attended in full
+ * all the same, its last range taking the rest); they write partial results
+ * there and a second launch joins them.
  */
 kvq_status kvq_window_attention_nvfp4_per_head(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,

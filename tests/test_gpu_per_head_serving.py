@@ -39,6 +39,13 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
 
+def through_workspace(kvq, call, splits):
+    """The arguments of a call whose ranges join through a workspace, not in clusters."""
+    T, H, D = call["q"].shape
+    need = max(16, kvq.kvq_per_head_attention_workspace_bytes(T, H, D, splits))
+    return dict(call, num_splits=splits, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+
+
 class Batch:
     """Requests with (context, new tokens), a shuffled block table, queries."""
 
@@ -114,41 +121,43 @@ SHAPES = [(64, "NHD", 4, 4, 16), (64, "HND", 6, 2, 24), (128, "NHD", 8, 2, 16), 
 
 @pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (37, 4), (64, 40), (500, 1000)])
-@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("splits", [1, 3, -3])
 def test_window_decode(kvq, dim, layout, heads, kv, block, window, sinks, splits):
     """One new token per request: sequences of 1 (the token alone) up to
     several tiles, windows and sinks that cut inside pages and tiles."""
     b = Batch([(0, 1), (1, 1), (31, 1), (32, 1), (95, 1), (130, 1), (301, 1)], heads, kv, dim, block, layout, 11)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    got = kvq.kvq_window_attention_nvfp4_per_head(**b.device(), window=window, num_sinks=sinks, num_splits=splits,
-                                                  status=status)
+    call = dict(b.device(), num_splits=splits) if splits > 0 else through_workspace(kvq, b.device(), -splits)
+    got = kvq.kvq_window_attention_nvfp4_per_head(**call, window=window, num_sinks=sinks, status=status)
     assert int(status.item()) == 0
     check(got, b.want(window=window, sinks=sinks))
 
 
 @pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
-@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 1), (0, 0, 4), (29, 5, 1), (29, 5, 2), (100, 0, 1)])
+@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 1), (0, 0, 4), (0, 0, -2), (29, 5, 1), (29, 5, 2), (29, 5, -3),
+                                                 (100, 0, 1), (0, 0, 8)])
 def test_window_chunks(kvq, dim, layout, heads, kv, block, window, sinks, splits):
     """Chunks of new tokens: alone, behind a context, ragged, and none at all."""
     b = Batch([(0, 37), (50, 3), (17, 0), (120, 41), (0, 1), (70, 20)], heads, kv, dim, block, layout, 12)
-    got = kvq.kvq_window_attention_nvfp4_per_head(**b.device(), window=window, num_sinks=sinks, num_splits=splits)
+    call = dict(b.device(), num_splits=splits) if splits > 0 else through_workspace(kvq, b.device(), -splits)
+    got = kvq.kvq_window_attention_nvfp4_per_head(**call, window=window, num_sinks=sinks)
     check(got, b.want(window=window, sinks=sinks))
 
 
 @pytest.mark.parametrize("new", [1, 130])
-@pytest.mark.parametrize("splits", [1, 5])
+@pytest.mark.parametrize("splits", [1, 5, -5])
 def test_padded_requests_see_nothing_and_other_rows_are_left(kvq, new, splits):
     """A padded request (length 0, or shorter than its query tokens) gives
     zeros and -inf where it sees nothing; rows behind the last request keep
     their contents, with and without an lse output."""
     b = Batch([(60, new), (0, new), (5, new)], 8, 2, 128, 16, "NHD", 13, extra_tokens=4)
     b.lens = [60 + new, 0, max(new - 3, 0)]
-    d = b.device()
+    d = dict(b.device(), num_splits=splits) if splits > 0 else through_workspace(kvq, b.device(), -splits)
     T = b.q_bits.shape[0]
     for with_lse in (True, False):
         out = torch.full((T, 8, 128), CANARY, dtype=torch.int16, device=DEV).view(torch.bfloat16)
         lse = torch.full((T, 8), 123.0, device=DEV) if with_lse else False
-        got = kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=splits, out=out, lse=lse)
+        got = kvq.kvq_window_attention_nvfp4_per_head(**d, out=out, lse=lse)
         want = b.want()
         if with_lse:
             check(got, want, rows=T - 4)
@@ -221,7 +230,7 @@ def test_bad_pages_and_requests(kvq, new):
     b.table = full
     # request 1's range is reversed
     d = b.device()
-    for splits in (1, 3):
+    for splits in (1, 3, 9):
         out = torch.full((3 * new, 4, 128), CANARY, dtype=torch.int16, device=DEV).view(torch.bfloat16)
         status.zero_()
         bad = dict(d, query_start=i32([0, 2 * new, new, 3 * new]), seq_lens=i32([100 + new, 50, 100 + 2 * new]),
@@ -297,15 +306,16 @@ def test_long_sequence_default_splits(kvq):
     window that the reference can hold."""
     b = Batch([(20000, 1)], 8, 1, 128, 16, "NHD", 19)
     d = b.device()
-    assert kvq.kvq_per_head_attention_default_splits(1, 8, 1, 128, 1, 20001) > 8
+    assert kvq.kvq_per_head_attention_default_splits(1, 8, 1, 128, 1, 20001) == (128, True)
     a0, l0 = kvq.kvq_window_attention_nvfp4_per_head(**d)
     a1, l1 = kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=1)
     want = b.want()
     check((a0, l0), want)
     check((a1, l1), want)
     # a max_seq_len that is too small only makes the ranges uneven
-    a2, l2 = kvq.kvq_window_attention_nvfp4_per_head(**dict(d, max_seq_len=64), num_splits=7)
+    a2, l2 = kvq.kvq_window_attention_nvfp4_per_head(**through_workspace(kvq, dict(d, max_seq_len=64), 7))
     check((a2, l2), want)
+    check(kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=8), want)
 
 
 # --------------------------------------------------------------------------
@@ -313,14 +323,15 @@ def test_long_sequence_default_splits(kvq):
 # --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
-@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("splits", [1, 3, -4])
 def test_tree(kvq, dim, layout, heads, kv, block, splits):
     """Random trees behind contexts of 0 to several tiles, up to 70 drafts
     (two mask words), masks that leave a draft nothing but the context and,
     without a context, nothing at all."""
     b = Batch([(0, 5), (1, 1), (100, 70), (64, 64), (33, 17), (0, 3)], heads, kv, dim, block, layout, 21)
     rows = random_tree(b.reqs, 2, b.rng, empty=(2, 7, 157))
-    got = kvq.kvq_tree_attention_nvfp4_per_head(**b.device(), tree_mask=mask_dev(rows), num_splits=splits)
+    call = dict(b.device(), num_splits=splits) if splits > 0 else through_workspace(kvq, b.device(), -splits)
+    got = kvq.kvq_tree_attention_nvfp4_per_head(**call, tree_mask=mask_dev(rows))
     want = b.want(tree=rows)
     assert np.isneginf(want[1][2]).all() and np.isneginf(want[1][157]).all()
     check(got, want)
@@ -510,26 +521,30 @@ def test_speculative_step_end_to_end(kvq):
     assert torch.equal(ra[0].view(torch.int16), rb[0].view(torch.int16)) and torch.equal(ra[1], rb[1])
 
 
-@pytest.mark.parametrize("new,splits", [(1, 4), (80, 1), (80, 2)])
-def test_graphs_and_streams(kvq, new, splits):
+@pytest.mark.parametrize("new,splits", [(1, 4), (1, 1), (80, 1), (80, 2)])
+@pytest.mark.parametrize("joined", ["cluster", "workspace"])
+def test_graphs_and_streams(kvq, new, splits, joined):
     """Two captured calls with workspaces of their own, replayed on new
     inputs, and a call on a side stream give the eager call's bits."""
     bs = [Batch([(300, new), (40, new)], 8, 2, 128, 16, "NHD", 61 + i) for i in range(2)]
     ds = [b.device() for b in bs]
-    eager = [kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=splits) for d in ds]
+    cluster = joined == "cluster"
+    eager = [kvq.kvq_window_attention_nvfp4_per_head(**(dict(d, num_splits=splits) if cluster else
+                                                        through_workspace(kvq, d, splits))) for d in ds]
     need = kvq.kvq_per_head_attention_workspace_bytes(2 * new, 8, 128, splits)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out = torch.empty_like(eager[0][0])
     lse = torch.empty_like(eager[0][1])
     kvq.kvq_window_attention_nvfp4_per_head(**ds[0], num_splits=splits, out=out, lse=lse, stream=side,
-                                            workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+                                            workspace=None if cluster else
+                                            torch.empty(need, dtype=torch.uint8, device=DEV))
     side.synchronize()
     assert torch.equal(out.view(torch.int16), eager[0][0].view(torch.int16)) and torch.equal(lse, eager[0][1])
     graphs = []
     for i in range(2):
         d = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in ds[i].items()}
-        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        ws = None if cluster else torch.empty(need, dtype=torch.uint8, device=DEV)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             got = kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=splits, workspace=ws)
