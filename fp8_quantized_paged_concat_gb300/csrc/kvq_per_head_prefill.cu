@@ -17,7 +17,7 @@
 //   - shared memory: q in f16 (scaled by each row's power of two), K tiles and
 //     V tiles (64 x D f16, 128-byte swizzle, kStages of each), and a ring of
 //     raw entries per side;
-//   - three warps decode the keys and three the values: raw entries come in by
+//   - some warps decode the keys and as many the values: raw entries come in by
 //     asynchronous copies, kRing - 1 chunks ahead (each warp copies what it
 //     decodes, so that it waits for no other); 8 lanes take 8 rows of a
 //     64-column block, so that their 16-byte stores fall in different banks;
@@ -48,19 +48,21 @@ constexpr uint32_t kKBlock = kKeys * 128;         // 64 dimensions of a key tile
 
 template <int D, int kTiles>
 struct Shape {
-  // warps: softmax, three that decode keys, the one that issues the scores'
-  // products, three that decode values, the one that issues the outputs'; in
-  // whole warpgroups, whose registers are split by role (the threads start
-  // with an equal share, and the shares add up to no more)
+  // Warps: softmax; those that decode keys, and the one that issues the
+  // scores' products; those that decode values, and the one that issues the
+  // outputs'; in whole warpgroups, whose registers are split by role (the
+  // threads start with an equal share, and the shares add up to no more).
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kKeyWarps = 3, kValueWarps = 3;
+  static constexpr int kKeyWarps = kTiles == 2 ? 3 : 5, kValueWarps = kKeyWarps;
   static constexpr int kScoreWarp = kSoftmaxWarps + kKeyWarps;
   static constexpr int kOutputWarp = kScoreWarp + 1 + kValueWarps;
   static constexpr int kThreads = 32 * (kOutputWarp + 1);
-  static constexpr int kStartRegs = kTiles == 2 ? 128 : 168;
+  static_assert(kThreads == 512, "warpgroups");
+  static constexpr int kStartRegs = 128;
   static constexpr int kSoftmaxRegs = kTiles == 2 ? 152 : 200;
-  static constexpr int kOtherRegs = kTiles == 2 ? 104 : 144;
-  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kStartRegs, "register split");
+  static constexpr int kOtherRegs = kTiles == 2 ? 104 : 96;
+  static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
+                    kThreads * kStartRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
   static constexpr int kStages = D == 256 ? 2 : 3;           // decoded tiles of K, of V
   static constexpr uint32_t kTileBytes = kBlocks * kKBlock;
@@ -360,49 +362,62 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     more_registers<S::kSoftmaxRegs>();
     const int tile = warp >> 2;                     // its row tile
     const int32_t row = static_cast<int32_t>(threadIdx.x);
-    // the query row -> shared memory
-    float sc = 0.0f;                                // score -> base-2 exponent
     int64_t token = 0;
     int32_t q_head = 0;
     int32_t pos_hi = -1, pos_lo = 0;
     const bool has_row = row < rows;
-    const uint4* src = nullptr;
-    float amax = 0.0f;
+    uint64_t src = 0;
     if (has_row) {
-      const uint32_t flat = static_cast<uint32_t>(row0 + row), tk = a.group_div.div(flat);
-      token = rq.token0 + tk;
-      q_head = head * a.group + (flat - tk * a.group);
-      const int64_t p = rq.first_pos + tk;
+      const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + row));
+      token = at.token;
+      q_head = at.head;
+      const int64_t p = rq.first_pos + (token - rq.token0);
       pos_hi = static_cast<int32_t>(max(int64_t{-1}, min(p, static_cast<int64_t>(rq.len) - 1)));
-      pos_lo = a.window > 0 ? static_cast<int32_t>(min(static_cast<int64_t>(rq.len), max(int64_t{0}, p - a.window + 1))) : 0;
-      src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride_t +
-                                           q_head * a.q_stride_h);
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = __ldg(src + i);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
-      }
+      if (a.window > 0)
+        pos_lo = static_cast<int32_t>(min(static_cast<int64_t>(rq.len), max(int64_t{0}, p - a.window + 1)));
+      src = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride_t +
+                                       q_head * a.q_stride_h);
     }
-    const RowScale rs = row_scale(amax);
-    sc = a.scale_log2 * __ldg(a.k_scale) * rs.i[0] * rs.i[1];
-    const uint32_t q_tile = base + tile * S::kQTile;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);             // rows past the block's are zero
-      if (has_row) {
-        const uint4 x = __ldg(src + i);
-        v = make_uint4(pack_f16x2(bf16_lo(x.x) * rs.f[0] * rs.f[1], bf16_hi(x.x) * rs.f[0] * rs.f[1]),
-                       pack_f16x2(bf16_lo(x.y) * rs.f[0] * rs.f[1], bf16_hi(x.y) * rs.f[0] * rs.f[1]),
-                       pack_f16x2(bf16_lo(x.z) * rs.f[0] * rs.f[1], bf16_hi(x.z) * rs.f[0] * rs.f[1]),
-                       pack_f16x2(bf16_lo(x.w) * rs.f[0] * rs.f[1], bf16_hi(x.w) * rs.f[0] * rs.f[1]));
+    // The warp's 32 query rows -> shared memory: D / 8 lanes to a row (16
+    // bytes each), eight rows' loads of a lane in flight.  Rows past the
+    // block's are zero.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;
+    float amax = 0.0f;                              // of the thread's own row
+#pragma unroll 1
+    for (int r0 = 0; r0 < kRounds; r0 += 8) {
+      uint4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int from = (r0 + i) * kAtOnce + lane / kLanes;
+        const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(src >> 32), from)) << 32 |
+                            __shfl_sync(kFull, static_cast<uint32_t>(src), from);
+        x[i] = at != 0 ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
       }
-      st_shared16(q_tile + (i >> 3) * kBlockBytes + sw128_offset(row & 127, i & 7), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const float own = __shfl_sync(kFull, top, (lane % kAtOnce) * kLanes);
+        if (lane / kAtOnce == r0 + i) amax = own;
+        const RowScale rs = row_scale(top);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[j] = pack_f16x2(bf16_lo(w[j]) * rs.f[0] * rs.f[1], bf16_hi(w[j]) * rs.f[0] * rs.f[1]);
+        const uint32_t r = (warp & 3) * 32 + (r0 + i) * kAtOnce + lane / kLanes, c = lane % kLanes;
+        st_shared16(base + tile * S::kQTile + (c >> 3) * kBlockBytes + sw128_offset(r, c & 7),
+                    make_uint4(h[0], h[1], h[2], h[3]));
+      }
     }
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
+    const RowScale rs = row_scale(amax);
+    const float sc = a.scale_log2 * __ldg(a.k_scale) * rs.i[0] * rs.i[1];   // score -> base-2 exponent
 
     if (!has_row) m = 0.0f;
     const uint32_t lanes = (warp & 3) * 32u << 16;
