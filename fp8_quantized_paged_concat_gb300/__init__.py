@@ -649,8 +649,8 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     block_table int32 [B, W] from kv_cache (as kvq_reshape_and_cache_nvfp4
     wrote it, layout "NHD" or "HND").  num_splits (default:
     kvq_per_head_attention_default_splits) key ranges, joined inside clusters
-    (up to PER_HEAD_CLUSTER_SPLITS, no workspace) or through a workspace: a
-    CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
+    (up to PER_HEAD_CLUSTER_SPLITS of calls with at most 32 query rows per
+    request and key head; no workspace) or through a workspace: a CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
     (allocated here when one is needed and None is given).  Returns (out bf16
     [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, k_scale, v_scale,

@@ -855,7 +855,8 @@ kvq_status per_head_attention(
   const int32_t group = num_heads / num_kv_heads;
   KVQ_REQUIRE((int64_t{max_query_len} * group + 7) / 8 * num_kv_heads * num_splits < (int64_t{1} << 31),
               "%s: max_query_len * num_heads * num_splits too large", fn);
-  const bool cluster = num_splits > 1 && num_splits <= KVQ_PER_HEAD_CLUSTER_SPLITS && workspace == nullptr;
+  const bool cluster = num_splits > 1 && num_splits <= KVQ_PER_HEAD_CLUSTER_SPLITS && workspace == nullptr &&
+                       int64_t{max_query_len} * group <= KVQ_PER_HEAD_CLUSTER_ROWS;
   if (num_splits > 1 && !cluster) {
     const int64_t need = kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits);
     KVQ_REQUIRE(need >= 0 && workspace != nullptr && aligned(workspace, 16) && workspace_bytes >= need,

@@ -291,7 +291,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   &use_workspace);
     } else {
       splits = int32("num_splits", a[14]);
-      use_workspace = splits > KVQ_PER_HEAD_CLUSTER_SPLITS;
+      use_workspace = splits > KVQ_PER_HEAD_CLUSTER_SPLITS ||
+                      (splits > 1 && c.heads > 0 && max_query * (H / c.heads) > KVQ_PER_HEAD_CLUSTER_ROWS);
     }
     at::Tensor workspace;
     if (a[15] != Py_None) {

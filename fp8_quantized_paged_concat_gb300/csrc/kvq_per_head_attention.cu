@@ -87,6 +87,81 @@ __device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
   return D == 256 ? chunk ^ ((row & 3) << 1) : D == 128 ? chunk ^ (row & 2) : chunk;
 }
 
+// Distributed shared memory of a cluster: the address in CTA `rank`'s shared
+// memory that corresponds to `addr` in one's own, loads from there, and the
+// cluster's barrier (also for the shared memory before and after it).
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The ranges of a cluster joined: CTA `rank` of num_splits takes its share of
+// the (row, 8 dimensions) of the block.  In every CTA `o` holds the rows' fp32
+// sums (rows `stride` bytes apart), `m` and `l` their reference maxima and
+// denominators.  Every thread of the cluster comes here.
+__device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, const Request& rq, uint32_t kv_head,
+                                             int64_t row0, int32_t rows, int32_t rank, int32_t dims, uint32_t o,
+                                             uint32_t stride, uint32_t m, uint32_t l) {
+  cluster_sync();
+  const float v_scale = __ldg(a.v_scale);
+  const int32_t chunks = dims / 8;
+  // (distributed shared memory gives an SM about 14 bytes a clock: the shares are equal)
+  for (int32_t i = rank + threadIdx.x * a.num_splits; i < rows * chunks; i += a.num_splits * blockDim.x) {
+    const int32_t r = i / chunks, d = (i - r * chunks) * 8;
+    // every load is issued before the first is used
+    constexpr int kMax = KVQ_PER_HEAD_CLUSTER_SPLITS;
+    float ms[kMax], ls[kMax];
+    float4 u[kMax], w[kMax];
+#pragma unroll
+    for (int32_t s = 0; s < kMax; ++s) {
+      ms[s] = -INFINITY;
+      ls[s] = 0.0f;
+      u[s] = w[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s < a.num_splits) {
+        ms[s] = cluster_load(cluster_addr(m + 4 * r, s));
+        ls[s] = cluster_load(cluster_addr(l + 4 * r, s));
+        const uint32_t at = cluster_addr(o + r * stride + 4 * d, s);
+        u[s] = cluster_load4(at);
+        w[s] = cluster_load4(at + 16);
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int32_t s = 0; s < kMax; ++s) top = fmaxf(top, ms[s]);
+    float sum = 0.0f, acc[8] = {};
+#pragma unroll
+    for (int32_t s = 0; s < kMax; ++s) {
+      const float f = ms[s] == -INFINITY ? 1.0f : ex2(ms[s] - top);  // a range that saw nothing holds zeros
+      sum += f * ls[s];
+      acc[0] += f * u[s].x; acc[1] += f * u[s].y; acc[2] += f * u[s].z; acc[3] += f * u[s].w;
+      acc[4] += f * w[s].x; acc[5] += f * w[s].y; acc[6] += f * w[s].z; acc[7] += f * w[s].w;
+    }
+    const RowAt at = row_at(a, rq, kv_head, static_cast<uint32_t>(row0 + r));
+    const float f = (sum == 0.0f ? 0.0f : 1.0f / sum) * v_scale;
+    st16(static_cast<__nv_bfloat16*>(a.out) + at.token * a.out_stride_t + at.head * a.out_stride_h + d,
+         make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                    pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f)));
+    if (d == 0 && a.lse != nullptr)
+      a.lse[at.token * a.lse_stride_t + at.head] = sum == 0.0f ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+  }
+  cluster_sync();                                // no CTA leaves while its memory is read
+}
+
 template <int D, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 4)
     per_head_attention_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
@@ -113,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   int32_t s0, s1;
   range_of(a, keys, split, s0, s1);
 
+  allow_dependents();
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t g = lane >> 2, c = lane & 3;
@@ -522,18 +598,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 constexpr int kJoinWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) per_head_join_kernel(const PerHeadAttentionArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const PerHeadAttentionArgs a) {
+  wait_for_previous();
   const int64_t flat = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   Request rq;
   if (!request_of(a, b, rq) || flat >= static_cast<int64_t>(rq.tokens) * a.num_heads) return;
   const int64_t row = rq.token0 * a.num_heads + flat;
   const float* ls = a.part_lse + row * a.num_splits;
-  float top = -INFINITY;
+  // lane l holds ranges l, l + 32, ...
+  constexpr int kPer = KVQ_PER_HEAD_MAX_SPLITS / 32;
+  float own[kPer], top = -INFINITY;
   bool abandoned = false;
-  for (int s = lane; s < a.num_splits; s += 32) {
-    top = fmaxf(top, ls[s]);
-    abandoned |= __float_as_uint(ls[s]) == kAbandoned;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    own[j] = 32 * j + lane < a.num_splits ? ls[32 * j + lane] : -INFINITY;
+    top = fmaxf(top, own[j]);
+    abandoned |= __float_as_uint(own[j]) == kAbandoned;
   }
   if (__any_sync(kFull, abandoned)) return;              // a range whose CTA gave up: the row stays unwritten
 #pragma unroll
@@ -542,16 +623,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) per_head_join_kernel(const Pe
   float acc[kDims], den = 0.0f;
 #pragma unroll
   for (int i = 0; i < kDims; ++i) acc[i] = 0.0f;
-  const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
-  for (int s = 0; s < a.num_splits; ++s) {
-    const float w = ls[s] == -INFINITY ? 0.0f : ex2(ls[s] - top);
-    if (w == 0.0f) continue;                             // uniform over the warp
-    den += w;
 #pragma unroll
-    for (int i = 0; i < kDims; i += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(s) * D + i);
-      acc[i] += w * v.x;
-      acc[i + 1] += w * v.y;
+  for (int j = 0; j < kPer; ++j) {
+    own[j] = own[j] == -INFINITY ? 0.0f : ex2(own[j] - top);   // the range's weight
+    den += own[j];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+  const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
+  // eight ranges' rows in flight (those of an empty range were never written, and are not read)
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    for (int s0 = 0; s0 < 32 && 32 * j + s0 < a.num_splits; s0 += 8) {
+      float w[8];
+      float2 v[8][kDims / 2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[k] = __shfl_sync(kFull, own[j], s0 + k);
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i)
+          v[k][i] = w[k] == 0.0f ? make_float2(0.0f, 0.0f)
+                                 : *reinterpret_cast<const float2*>(po + static_cast<int64_t>(32 * j + s0 + k) * D + 2 * i);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i) {
+          acc[2 * i] += w[k] * v[k][i].x;
+          acc[2 * i + 1] += w[k] * v[k][i].y;
+        }
     }
   }
   const float f = (den == 0.0f ? 0.0f : 1.0f / den) * __ldg(a.v_scale);
@@ -561,6 +661,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) per_head_join_kernel(const Pe
 #pragma unroll
   for (int i = 0; i < kDims; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
   if (lane == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
+}
+
+// Launches `kernel`, the ranges of a block as a cluster where they are joined in one.
+template <class Kernel>
+cudaError_t launch_ranges(Kernel kernel, const PerHeadAttentionArgs& a, dim3 grid, int threads, int smem,
+                          int32_t row_blocks, cudaStream_t stream) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute cluster = {};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = a.num_splits;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  config.attrs = &cluster;
+  config.numAttrs = a.cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&config, kernel, a, row_blocks);
 }
 
 template <int D, int kRowTiles>
@@ -580,9 +698,17 @@ cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
-  const dim3 grid(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
-  per_head_join_kernel<D><<<grid, kJoinWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  // a dependent launch: it is under way while the ranges still run
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
+  config.blockDim = dim3(kJoinWarps * 32);
+  config.stream = stream;
+  cudaLaunchAttribute dependent = {};
+  dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dependent.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &dependent;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, per_head_join_kernel<D>, a);
 }
 
 }  // namespace
@@ -613,10 +739,13 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
     if (use_workspace != nullptr) *use_workspace = 1;
     return static_cast<int32_t>(n);
   }
-  // The call is short of CTAs: up to a cluster's ranges cost no second launch.
+  // The call is short of CTAs.  A cluster's ranges cost no second launch (few
+  // rows; more rows' partial results pass faster through memory than between
+  // the SMs of a cluster).
   const int64_t n = std::max<int64_t>(1, std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / least, resident / blocks}));
-  if (n <= KVQ_PER_HEAD_CLUSTER_SPLITS) return static_cast<int32_t>(n);
-  if (keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least) return KVQ_PER_HEAD_CLUSTER_SPLITS;
+  if (few && n <= KVQ_PER_HEAD_CLUSTER_SPLITS) return static_cast<int32_t>(n);
+  if (few && keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least) return KVQ_PER_HEAD_CLUSTER_SPLITS;
+  if (n == 1) return 1;
   if (use_workspace != nullptr) *use_workspace = 1;
   return static_cast<int32_t>(n);
 }

@@ -37,28 +37,10 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
-// Distributed shared memory of a cluster: the address in CTA `rank`'s shared
-// memory that corresponds to `addr` in one's own, loads from there, and the
-// cluster's barrier (also for the shared memory before and after it).
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float cluster_load(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+// Dependent launches: the next kernel of the stream may be launched once every
+// CTA has said so or left, and waits, before it reads, for this one's end.
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Asynchronous copies into shared memory; `bytes` = kBytes, or 0: zero-filled,
 // nothing read.
@@ -233,66 +215,6 @@ struct RowAt {
 __device__ __forceinline__ RowAt row_at(const PerHeadAttentionArgs& a, const Request& r, uint32_t kv_head, uint32_t flat) {
   const uint32_t tk = a.group_div.div(flat);
   return {r.token0 + tk, static_cast<int32_t>(kv_head * a.group + (flat - tk * a.group))};
-}
-
-// The ranges of a cluster joined: CTA `rank` of num_splits takes its share of
-// the (row, 8 dimensions) of the block.  In every CTA `o` holds the rows' fp32
-// sums (rows `stride` bytes apart), `m` and `l` their reference maxima and
-// denominators (fp32; m = kAbandoned: the CTA gave up, and the row stays
-// unwritten).  Every thread of the cluster comes here.
-__device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, const Request& rq, uint32_t kv_head,
-                                             int64_t row0, int32_t rows, int32_t rank, int32_t dims, uint32_t o,
-                                             uint32_t stride, uint32_t m, uint32_t l) {
-  cluster_sync();
-  const float v_scale = __ldg(a.v_scale);
-  const int32_t chunks = dims / 8;
-  for (int32_t i = rank * blockDim.x + threadIdx.x; i < rows * chunks; i += a.num_splits * blockDim.x) {
-    const int32_t r = i / chunks, d = (i - r * chunks) * 8;
-    float top = -INFINITY;
-    bool abandoned = false;
-    for (int32_t s = 0; s < a.num_splits; ++s) {
-      const float v = cluster_load(cluster_addr(m + 4 * r, s));
-      abandoned = abandoned || __float_as_uint(v) == kAbandoned;
-      top = fmaxf(top, v);
-    }
-    if (abandoned) continue;
-    float sum = 0.0f, acc[8] = {};
-    for (int32_t s = 0; s < a.num_splits; ++s) {
-      const float v = cluster_load(cluster_addr(m + 4 * r, s));
-      const float f = v == -INFINITY ? 1.0f : ex2(v - top);        // a range that saw nothing holds zeros
-      sum += f * cluster_load(cluster_addr(l + 4 * r, s));
-      const uint32_t at = cluster_addr(o + r * stride + 4 * d, s);
-      const float4 u = cluster_load4(at), w = cluster_load4(at + 16);
-      acc[0] += f * u.x; acc[1] += f * u.y; acc[2] += f * u.z; acc[3] += f * u.w;
-      acc[4] += f * w.x; acc[5] += f * w.y; acc[6] += f * w.z; acc[7] += f * w.w;
-    }
-    const RowAt at = row_at(a, rq, kv_head, static_cast<uint32_t>(row0 + r));
-    const float f = (sum == 0.0f ? 0.0f : 1.0f / sum) * v_scale;
-    st16(static_cast<__nv_bfloat16*>(a.out) + at.token * a.out_stride_t + at.head * a.out_stride_h + d,
-         make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
-                    pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f)));
-    if (d == 0 && a.lse != nullptr)
-      a.lse[at.token * a.lse_stride_t + at.head] = sum == 0.0f ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
-  }
-  cluster_sync();                                // no CTA leaves while its memory is read
-}
-
-// Launches `kernel`, the ranges of a block as a cluster where they are joined in one.
-template <class Kernel>
-cudaError_t launch_ranges(Kernel kernel, const PerHeadAttentionArgs& a, dim3 grid, int threads, int smem,
-                          int32_t row_blocks, cudaStream_t stream) {
-  cudaLaunchConfig_t config = {};
-  config.gridDim = grid;
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = stream;
-  cudaLaunchAttribute cluster = {};
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = a.num_splits;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  config.attrs = &cluster;
-  config.numAttrs = a.cluster ? 1 : 0;
-  return cudaLaunchKernelEx(&config, kernel, a, row_blocks);
 }
 
 }  // namespace

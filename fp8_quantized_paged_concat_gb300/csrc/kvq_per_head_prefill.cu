@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const Keys<kKeys> keys = keys_of<kKeys>(a, rq, t0, t1);
   int32_t s0, s1;
   range_of(a, keys, split, s0, s1);
-  if (a.num_splits > 1 && !a.cluster && s0 == s1) {
+  if (a.num_splits > 1 && s0 == s1) {
     // an empty range: it weighs nothing when the ranges are joined
     for (int r = threadIdx.x; r < rows; r += S::kThreads) {
       const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + r));
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     return;
   }
   const int32_t n_tiles = s1 - s0;
+  allow_dependents();
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -350,51 +351,61 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
+  // Softmax threads: their query row, and the loads of the warp's 32 rows, D /
+  // 8 lanes to a row (16 bytes each), with a single row tile a batch of them in
+  // flight while the CTA sets up (two have no registers to spare for it).
+  // Rows past the block's are zero.
+  const int32_t row = static_cast<int32_t>(threadIdx.x);
+  bool has_row = false;
+  int64_t token = 0;
+  int32_t q_head = 0, pos_hi = -1, pos_lo = 0;
+  uint64_t src = 0;
+  auto set_row = [&]() {
+    has_row = warp < S::kSoftmaxWarps && row < rows;
+    if (!has_row) return;
+    const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + row));
+    token = at.token;
+    q_head = at.head;
+    const int64_t p = rq.first_pos + (token - rq.token0);
+    pos_hi = static_cast<int32_t>(max(int64_t{-1}, min(p, static_cast<int64_t>(rq.len) - 1)));
+    if (a.window > 0)
+      pos_lo = static_cast<int32_t>(min(static_cast<int64_t>(rq.len), max(int64_t{0}, p - a.window + 1)));
+    src = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride_t +
+                                     q_head * a.q_stride_h);
+  };
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;
+  constexpr int kBatch = kTiles == 2 || kRounds < 16 ? 8 : 16;
+  uint4 x[kBatch];
+  auto load_rows = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int from = (r0 + i) * kAtOnce + lane / kLanes;
+      const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(src >> 32), from)) << 32 |
+                          __shfl_sync(kFull, static_cast<uint32_t>(src), from);
+      x[i] = at != 0 ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (kTiles == 1) {
+    set_row();
+    if (warp < S::kSoftmaxWarps) load_rows(0);
+  }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
 
-  float m = -INFINITY, l = 0.0f;                    // softmax: reference maximum, sum
-  bool done = true;                                 // and whether every wait of the row's was met
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
     more_registers<S::kSoftmaxRegs>();
     const int tile = warp >> 2;                     // its row tile
-    const int32_t row = static_cast<int32_t>(threadIdx.x);
-    int64_t token = 0;
-    int32_t q_head = 0;
-    int32_t pos_hi = -1, pos_lo = 0;
-    const bool has_row = row < rows;
-    uint64_t src = 0;
-    if (has_row) {
-      const RowAt at = row_at(a, rq, head, static_cast<uint32_t>(row0 + row));
-      token = at.token;
-      q_head = at.head;
-      const int64_t p = rq.first_pos + (token - rq.token0);
-      pos_hi = static_cast<int32_t>(max(int64_t{-1}, min(p, static_cast<int64_t>(rq.len) - 1)));
-      if (a.window > 0)
-        pos_lo = static_cast<int32_t>(min(static_cast<int64_t>(rq.len), max(int64_t{0}, p - a.window + 1)));
-      src = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride_t +
-                                       q_head * a.q_stride_h);
-    }
-    // The warp's 32 query rows -> shared memory: D / 8 lanes to a row (16
-    // bytes each), eight rows' loads of a lane in flight.  Rows past the
-    // block's are zero.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;
+    if (kTiles == 2) set_row();
+    // the warp's 32 query rows -> shared memory
     float amax = 0.0f;                              // of the thread's own row
 #pragma unroll 1
-    for (int r0 = 0; r0 < kRounds; r0 += 8) {
-      uint4 x[8];
+    for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
+      if (kTiles == 2 || r0 > 0) load_rows(r0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int from = (r0 + i) * kAtOnce + lane / kLanes;
-        const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(src >> 32), from)) << 32 |
-                            __shfl_sync(kFull, static_cast<uint32_t>(src), from);
-        x[i] = at != 0 ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         float top = 0.0f;
 #pragma unroll
@@ -419,7 +430,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     const RowScale rs = row_scale(amax);
     const float sc = a.scale_log2 * __ldg(a.k_scale) * rs.i[0] * rs.i[1];   // score -> base-2 exponent
 
-    if (!has_row) m = 0.0f;
+    float m = has_row ? -INFINITY : 0.0f, l = 0.0f; // reference maximum, sum
+    bool done = true;                               // every wait was met
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
     for (int32_t t = 0; t < n_tiles; ++t) {
@@ -486,10 +498,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         else
           pass(off, std::false_type{});
       };
-      weights();
       // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
       // sum is takes a new reference, its tile's maximum (as its first tile).
-      if (__any_sync(kFull, m == -INFINITY || sum > kMaxWeight)) {
+      const bool fresh = t == 0 || __any_sync(kFull, m == -INFINITY);
+      if (!fresh) weights();
+      if (fresh || __any_sync(kFull, sum > kMaxWeight)) {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
@@ -497,7 +510,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
         }
         float alpha = 1.0f;
-        if (top > m && (m == -INFINITY || sum > kMaxWeight)) {
+        if (top > m) {
           alpha = ex2(m - top);                     // 0 while m is -inf
           m = top;
         }
@@ -534,42 +547,40 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
     fence_after_sync();
-    if (!a.cluster) {
-      const bool live = row < rows && done;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
-      const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
-      const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
+    const bool live = row < rows && done;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
+    const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
+    const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        if (n_tiles > 0 && done) {                    // uniform over the warp
-          tmem_ld32(o_col + 32 * c, o);
-        } else {
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      if (n_tiles > 0 && done) {                    // uniform over the warp
+        tmem_ld32(o_col + 32 * c, o);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-        }
-        if (live && a.num_splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
-                                                q_head * a.out_stride_h + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                                pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
-                                pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
-        }
-        __syncwarp();                                 // the next load is the whole warp's
+        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
       }
-      if (a.num_splits > 1) {
-        if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
-      } else if (live && a.lse != nullptr) {
-        a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
+      if (live && a.num_splits > 1) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+      } else if (live) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
+                                              q_head * a.out_stride_h + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[i] = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                              pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
+                              pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
       }
+      __syncwarp();                                 // the next load is the whole warp's
+    }
+    if (a.num_splits > 1) {
+      if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
+    } else if (live && a.lse != nullptr) {
+      a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
     }
   } else {
     fewer_registers<S::kOtherRegs>();
@@ -650,38 +661,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *s_abort) report(a.status, KVQ_STATUS_TIMEOUT);
-  if (a.cluster) {
-    // O rows -> shared memory (q, K and V are no longer read), padded by 16
-    // bytes against bank conflicts; then the cluster's ranges are joined
-    constexpr uint32_t kStride = 4 * D + 16;
-    static_assert(128 * kTiles * kStride <= S::kMisc, "the rows fit");
-    __shared__ float cm[128 * kTiles], cl[128 * kTiles];
-    if (warp < S::kSoftmaxWarps) {
-      fence_after_sync();
-      const uint32_t to = base + threadIdx.x * kStride;
-      const uint32_t o_col = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * D;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        if (n_tiles > 0 && done) {                  // uniform over the warp
-          tmem_ld32(o_col + 32 * c, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_shared16(to + 128 * c + 16 * i, make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                                                        __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])));
-      }
-      cm[threadIdx.x] = done ? (l == 0.0f ? -INFINITY : m) : __uint_as_float(kAbandoned);
-      cl[threadIdx.x] = l;
-    }
-    asm volatile("" ::: "memory");                  // st_shared16 carries no clobber
-    join_cluster(a, rq, head, row0, rows, split, D, base, kStride, smem_u32(cm), smem_u32(cl));
-    fence_before_sync();
-    __syncthreads();
-  }
   if (warp == 0) {
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
@@ -696,8 +675,8 @@ cudaError_t launch(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (static_cast<int64_t>(a.max_query_len) * a.group + 128 * kTiles - 1) / (128 * kTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  return launch_ranges(per_head_prefill_kernel<D, kTiles>, a, grid, S::kThreads, S::kSmem, static_cast<int32_t>(blocks),
-                       stream);
+  per_head_prefill_kernel<D, kTiles><<<grid, S::kThreads, S::kSmem, stream>>>(a, static_cast<int32_t>(blocks));
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -579,7 +579,8 @@ kvq_status kvq_qk_norm_rope(
     int32_t* d_status, kvq_stream_t stream);
 
 #define KVQ_PER_HEAD_MAX_SPLITS 128    /* key ranges of the per-head attention */
-#define KVQ_PER_HEAD_CLUSTER_SPLITS 8  /* of them, as many as need no workspace */
+#define KVQ_PER_HEAD_CLUSTER_SPLITS 8  /* of them, as many as need no workspace for a call with at most */
+#define KVQ_PER_HEAD_CLUSTER_ROWS   32 /* max_query_len * num_heads / num_kv_heads rows */
 
 /*
  * kvq_per_head_attention_workspace_bytes -- bytes of workspace that the two
@@ -637,9 +638,10 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * [batch_size]; batch_size <= 65535.
  * num_splits: key ranges per block of query rows (1 ..
  * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU.  With
- * workspace = NULL (at most KVQ_PER_HEAD_CLUSTER_SPLITS ranges) a block's
- * ranges are equal shares of its keys, run as one thread-block cluster and
- * join there.  With a workspace (16-byte aligned, at least
+ * workspace = NULL (at most KVQ_PER_HEAD_CLUSTER_SPLITS ranges, and
+ * max_query_len * num_heads / num_kv_heads at most KVQ_PER_HEAD_CLUSTER_ROWS)
+ * a block's ranges are equal shares of its keys, run as one thread-block
+ * cluster and join there.  With a workspace (16-byte aligned, at least
  * kvq_per_head_attention_workspace_bytes; overwritten, no other call may use
  * it while this one runs) the ranges are sized from max_seq_len, which bounds
  * seq_lens, the same for every request (a longer sequence is attended in full

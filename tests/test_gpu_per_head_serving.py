@@ -521,8 +521,8 @@ def test_speculative_step_end_to_end(kvq):
     assert torch.equal(ra[0].view(torch.int16), rb[0].view(torch.int16)) and torch.equal(ra[1], rb[1])
 
 
-@pytest.mark.parametrize("new,splits", [(1, 4), (1, 1), (80, 1), (80, 2)])
-@pytest.mark.parametrize("joined", ["cluster", "workspace"])
+@pytest.mark.parametrize("new,splits,joined", [(1, 4, "cluster"), (1, 4, "workspace"), (1, 1, "cluster"),
+                                               (80, 1, "workspace"), (80, 2, "workspace")])
 def test_graphs_and_streams(kvq, new, splits, joined):
     """Two captured calls with workspaces of their own, replayed on new
     inputs, and a call on a side stream give the eager call's bits."""
