@@ -143,14 +143,13 @@ struct Request {
 // num_tokens), or more than max_query_len.
 __device__ __forceinline__ bool request_of(const PerHeadAttentionArgs& a, int b, Request& r) {
   const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
-  if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || q1 - q0 > a.max_query_len) return false;
+  const int32_t len = max(0, __ldg(a.seq_lens + b));
   r.token0 = q0;
   r.tokens = q1 - q0;
-  const int32_t len = max(0, __ldg(a.seq_lens + b));
   r.first_pos = static_cast<int64_t>(len) - r.tokens;
   r.len = min(len, a.table_positions);
   r.cut = r.len < len;
-  return true;
+  return q0 >= 0 && q1 >= q0 && q1 <= a.num_tokens && static_cast<int64_t>(q1) - q0 <= a.max_query_len;
 }
 
 // The keys that some token in [t0, t1] of the request sees.

@@ -90,6 +90,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(kFull, mbar_try_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
 }
 
+// The CTA's set-up is done (tensor memory, barriers): every role comes here
+// once, after what it can start before.
+__device__ __forceinline__ void set_up_done() {
+  fence_before_sync();
+  asm volatile("bar.sync 0;" ::: "memory");
+  fence_after_sync();
+}
+
 // kind::f16 with f16 operands, fp32 sums; A is K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -247,6 +255,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     start(h);
     look_up(h + 1);
   }
+  set_up_done();
   for (int32_t h = 0; h < chunks; ++h) {
     const int32_t t = h / S::kParts;
     const int st = t % S::kStages;
@@ -385,18 +394,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       x[i] = at != 0 ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
     }
   };
-  if (kTiles == 1) {
-    set_row();
-    if (warp < S::kSoftmaxWarps) load_rows(0);
-  }
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
-
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
+    if (kTiles == 1) {
+      set_row();
+      load_rows(0);
+    }
+    set_up_done();
     more_registers<S::kSoftmaxRegs>();
+    const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
     const int tile = warp >> 2;                     // its row tile
     if (kTiles == 2) set_row();
     // the warp's 32 query rows -> shared memory
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           pass(off, std::false_type{});
       };
       // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
-      // sum is takes a new reference, its tile's maximum (as its first tile).
+      // sum is takes a new reference, its tile's maximum (as in its first tile).
       const bool fresh = t == 0 || __any_sync(kFull, m == -INFINITY);
       if (!fresh) weights();
       if (fresh || __any_sync(kFull, sum > kMaxWeight)) {
@@ -608,6 +614,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     } else if (warp == S::kScoreWarp) {
       // ---- S_w(t) = Q_w K(t)^T (one elected lane; the warp waits together) -----
       constexpr uint32_t kIdesc = idesc_f16(128, kKeys, false);
+      set_up_done();
+      const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
       const uint32_t elected = elect_lane();
       const uint64_t qdesc = sw128_desc(base, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
       bool ok = n_tiles > 0 && have(q_full, 0);
@@ -636,6 +644,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     } else {
       // ---- O_w += P_w(t) V(t) ---------------------------------------------------
       constexpr uint32_t kIdesc = idesc_f16(128, D, true);
+      set_up_done();
+      const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
       const uint32_t elected = elect_lane();
       const uint64_t vdesc = sw128_desc(base + S::kV, kKBlock, 1024);
       bool ok = true;
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   if (threadIdx.x == 0 && *s_abort) report(a.status, KVQ_STATUS_TIMEOUT);
   if (warp == 0) {
     fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(*s_tmem), "r"(kTmemCols) : "memory");
   }
 }
 
