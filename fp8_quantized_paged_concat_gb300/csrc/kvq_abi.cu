@@ -1043,7 +1043,7 @@ kvq_status kvq_compact_drafts_nvfp4_per_head(
     return s;
   KVQ_REQUIRE(region % 8 == 0 && int64_t{block_size} * num_kv_heads * (head_size / 2) % 8 == 0,
               "%s: block_size * num_kv_heads * full_dim must be a multiple of 8", fn);
-  KVQ_REQUIRE(num_layers <= 32767 && num_kv_heads <= 65535, "%s: at most 32767 layers and 65535 heads", fn);
+  KVQ_REQUIRE(num_layers <= 65535 && num_kv_heads <= 32767, "%s: at most 65535 layers and 32767 heads", fn);
   KVQ_REQUIRE(num_layers == 1 || (layer_stride >= num_pages * 2 * region && layer_stride % 16 == 0),
               "%s: layer_stride must be a multiple of 16 and cover a layer's pages (got %lld)", fn,
               static_cast<long long>(layer_stride));
@@ -1054,12 +1054,14 @@ kvq_status kvq_compact_drafts_nvfp4_per_head(
                   accepted_stride >= max_accepted,
               "%s: accepted / accepted_lens must be non-NULL, 4-byte aligned, with accepted_stride >= max_accepted", fn);
   KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
-  if (kvq_status s = check_device(fn)) return s;
+  int num_sms = 0;
+  if (kvq_status s = check_device(fn, &num_sms)) return s;
   const kvq::CompactArgs a{kv_cache,        num_layers,    num_layers == 1 ? 0 : layer_stride, num_pages, block_size,
                            layout,          num_kv_heads,  head_size,     query_start,        seq_lens,  batch_size,
                            accepted,        accepted_stride, accepted_lens, max_accepted,     block_table,
-                           block_table_stride, block_table_width, d_status};
-  return launched(fn, kvq::launch_compact_drafts(a, reinterpret_cast<cudaStream_t>(stream)));
+                           block_table_stride, block_table_width,
+                           kvq::FastDiv::make(static_cast<uint32_t>(block_size)), d_status};
+  return launched(fn, kvq::launch_compact_drafts(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* kvq_last_error_string(void) { return g_last_error.c_str(); }

@@ -8,40 +8,47 @@
 // a later move, so the moves are made in chunks, in order, and only inside a
 // chunk must every read come before the first write.
 //
-// Bound: latency (a few KB per request and layer; 26 MB moved in the largest
-// measured call).  One CTA per (request, layer, side, head chunk); a thread
-// keeps up to kUnits units of a chunk in registers between its loads and its
-// stores.
+// Bound: latency, of the chain from the request's lengths over its accepted
+// list and the block table to the entries (26 MB move in the largest measured
+// call).  So a CTA goes down that chain once, for one side and as many heads
+// of a request as its threads hold, and then moves several layers' entries:
+// a thread keeps kUnits units of kLayers layers in registers between its
+// loads, all issued together, and its stores.  64 requests x 32 layers of 8
+// heads: 19 us (one CTA per layer and head: 80 us).
+#include <algorithm>
+
 #include "kvq_device.cuh"
 #include "kvq_launch.h"
 
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kUnits = 4;                    // units per thread and chunk
+constexpr int kThreads = 256;
+constexpr int kUnits = 2;                    // units per thread and chunk
+constexpr int kLayers = 4;                   // layers in flight
 
-// Row index of (offset, head) in its page's side region.
-__device__ __forceinline__ int64_t row_of(const CompactArgs& a, uint32_t off, int head) {
-  return a.layout == KVQ_LAYOUT_HND ? static_cast<int64_t>(head) * a.block_size + off
-                                    : static_cast<int64_t>(off) * a.num_kv_heads + head;
-}
-
-// Page holding position p of request b, or -1.
-__device__ __forceinline__ int64_t page_of(const CompactArgs& a, int b, int64_t p) {
-  const int64_t col = p / a.block_size;
-  if (p < 0 || col >= a.block_table_width) return -1;
+// Page in column `col` of request b's table, or -1.
+__device__ __forceinline__ int64_t page_of(const CompactArgs& a, int b, uint32_t col) {
+  if (col >= static_cast<uint32_t>(a.block_table_width)) return -1;
   const int32_t id = __ldg(a.block_table + b * a.block_table_stride + col);
   return id >= 0 && id < a.num_pages ? id : -1;
 }
 
-// Unit: 8 data bytes, or one scale word (kScaleBytes).  Units of an entry's
-// head row: head_size / 16 data units, then its scale words.
-template <int kScaleBytes>
-__global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactArgs a) {
-  const int b = blockIdx.x, head = blockIdx.y;
-  const int layer = blockIdx.z >> 1, side = blockIdx.z & 1;
-  const bool first = head == 0 && blockIdx.z == 0;
+template <int kBytes>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+
+// Unit: kDataBytes data bytes, or kScaleBytes scale bytes.  heads: of a CTA.
+template <int kDataBytes, int kScaleBytes>
+__global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactArgs a, int heads, int layers_per_cta) {
+  using Data = typename Word<kDataBytes>::type;
+  const int b = blockIdx.x, side = blockIdx.y & 1;
+  const int head0 = static_cast<int>(blockIdx.y >> 1) * heads;
+  const int layer0 = blockIdx.z * layers_per_cta, layer1 = min(a.num_layers, layer0 + layers_per_cta);
+  const bool first = blockIdx.y == 0 && blockIdx.z == 0;
   const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
   const int64_t n = static_cast<int64_t>(q1) - q0, len = __ldg(a.seq_lens + b);
   const int32_t m = __ldg(a.accepted_lens + b);
@@ -50,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactA
     if (first && threadIdx.x == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
     return;
   }
-  const int64_t base = len - n;
+  const uint32_t base = static_cast<uint32_t>(len - n);
   const int32_t* acc = a.accepted + b * a.accepted_stride;
   bool bad = m < 0 || m > a.max_accepted;
   if (!bad) {
@@ -63,75 +70,105 @@ __global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactA
     if (first && threadIdx.x == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
     return;
   }
-  const int groups = a.head_size / kGroup, words = groups / kScaleBytes, per_row = groups + words;
-  const int64_t data_dim = a.head_size / 2;
-  const int64_t scales = static_cast<int64_t>(a.block_size) * a.num_kv_heads * data_dim;
+  const int groups = a.head_size / kGroup;
+  const int data_units = a.head_size / 2 / kDataBytes, row_units = data_units + groups / kScaleBytes;
+  const int my_heads = min(heads, a.num_kv_heads - head0), move_units = my_heads * row_units;
+  const int64_t scales = static_cast<int64_t>(a.block_size) * a.num_kv_heads * (a.head_size / 2);
   const int64_t region = scales + static_cast<int64_t>(a.block_size) * a.num_kv_heads * groups;
-  uint8_t* cache = a.cache + layer * a.layer_stride + side * region;
-  const int rows = max(1, kThreads * kUnits / per_row);    // moves per chunk
-  for (int i0 = 0; i0 < m; i0 += rows) {
-    const int units = min(rows, m - i0) * per_row;
-    uint2 v[kUnits];
-    uint8_t* to[kUnits];
+  uint8_t* cache = a.cache + side * region;
+  const int moves = max(1, kThreads * kUnits / move_units);      // per chunk (the host sees to move_units)
+  for (int i0 = 0; i0 < m; i0 += moves) {
+    const int units = min(moves, m - i0) * move_units;
+    int64_t from[kUnits], to[kUnits];                      // offsets in a layer, -1: nothing to move
+    bool is_data[kUnits];
     bool missing = false;
-    // (per_row can exceed what the threads hold at once only for head sizes
-    // past kThreads * kUnits * 8; the host bounds head_size well below that)
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
       const int u = threadIdx.x + j * kThreads;
-      to[j] = nullptr;
+      to[j] = -1;
       if (u >= units) continue;
-      const int i = i0 + u / per_row, w = u % per_row;
-      const int64_t from_p = base + __ldg(acc + i), to_p = base + i;
+      const int i = i0 + u / move_units, in_move = u % move_units;
+      const int head = head0 + in_move / row_units, w = in_move % row_units;
+      const uint32_t from_p = base + static_cast<uint32_t>(__ldg(acc + i)), to_p = base + i;   // below seq_lens[b]
       if (from_p == to_p) continue;
-      const int64_t from_page = page_of(a, b, from_p), to_page = page_of(a, b, to_p);
+      const uint32_t from_col = a.block_div.div(from_p), to_col = a.block_div.div(to_p);
+      const int64_t from_page = page_of(a, b, from_col), to_page = page_of(a, b, to_col);
       if (from_page < 0 || to_page < 0) {
         missing = true;
         continue;
       }
-      const int64_t from_row = row_of(a, static_cast<uint32_t>(from_p % a.block_size), head);
-      const int64_t to_row = row_of(a, static_cast<uint32_t>(to_p % a.block_size), head);
-      const uint8_t* src = cache + from_page * 2 * region;
-      uint8_t* dst = cache + to_page * 2 * region;
-      if (w < groups) {
-        v[j] = *reinterpret_cast<const uint2*>(src + from_row * data_dim + 8 * w);
-        to[j] = dst + to_row * data_dim + 8 * w;
-      } else {
-        const int64_t s = scales + kScaleBytes * (w - groups);
-        if constexpr (kScaleBytes == 4)
-          v[j].x = *reinterpret_cast<const uint32_t*>(src + s + from_row * groups);
-        else
-          v[j].x = src[s + from_row * groups];
-        to[j] = dst + s + to_row * groups;
-      }
+      // row of (offset, head) in its page's side region
+      const int64_t off0 = from_p - from_col * static_cast<uint32_t>(a.block_size);
+      const int64_t off1 = to_p - to_col * static_cast<uint32_t>(a.block_size);
+      const int64_t row0 = a.layout == KVQ_LAYOUT_HND ? static_cast<int64_t>(head) * a.block_size + off0
+                                                      : off0 * a.num_kv_heads + head;
+      const int64_t row1 = row0 + (off1 - off0) * (a.layout == KVQ_LAYOUT_HND ? 1 : a.num_kv_heads);
+      is_data[j] = w < data_units;
+      const int64_t pitch = is_data[j] ? a.head_size / 2 : groups;
+      const int64_t in_row = is_data[j] ? kDataBytes * w : scales + kScaleBytes * (w - data_units);
+      from[j] = from_page * 2 * region + row0 * pitch + in_row;
+      to[j] = to_page * 2 * region + row1 * pitch + in_row;
     }
-    if (missing && head == 0 && blockIdx.z == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
-    __syncthreads();
+    if (missing && first) report(a.status, KVQ_STATUS_BAD_INDEX);
+    for (int l0 = layer0; l0 < layer1; l0 += kLayers) {
+      Data v[kUnits][kLayers];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      if (to[j] == nullptr) continue;
-      const int w = (threadIdx.x + j * kThreads) % per_row;
-      if (w < groups)
-        st8(to[j], v[j]);
-      else if constexpr (kScaleBytes == 4)
-        st4(to[j], v[j].x);
-      else
-        *to[j] = static_cast<uint8_t>(v[j].x);
+      for (int j = 0; j < kUnits; ++j) {
+#pragma unroll
+        for (int l = 0; l < kLayers; ++l) {
+          if (to[j] < 0 || l0 + l >= layer1) continue;
+          const uint8_t* src = cache + (l0 + l) * a.layer_stride + from[j];
+          if (is_data[j])
+            v[j][l] = *reinterpret_cast<const Data*>(src);
+          else if constexpr (kScaleBytes == 4)
+            v[j][l].x = *reinterpret_cast<const uint32_t*>(src);
+          else
+            v[j][l].x = *src;
+        }
+      }
+      __syncthreads();                                     // every read of the chunk in these layers is done
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+#pragma unroll
+        for (int l = 0; l < kLayers; ++l) {
+          if (to[j] < 0 || l0 + l >= layer1) continue;
+          uint8_t* dst = cache + (l0 + l) * a.layer_stride + to[j];
+          if (is_data[j])
+            *reinterpret_cast<Data*>(dst) = v[j][l];
+          else if constexpr (kScaleBytes == 4)
+            *reinterpret_cast<uint32_t*>(dst) = v[j][l].x;
+          else
+            *dst = static_cast<uint8_t>(v[j][l].x);
+        }
+      }
     }
   }
 }
 
+template <int kDataBytes, int kScaleBytes>
+cudaError_t launch(const CompactArgs& a, int num_sms, cudaStream_t stream) {
+  const int groups = a.head_size / kGroup;
+  const int row_units = a.head_size / 2 / kDataBytes + groups / kScaleBytes;   // at most 192 (head_size <= 1024)
+  const int heads = std::max(1, std::min(a.num_kv_heads, kThreads * kUnits / row_units));
+  const int64_t chunks = (a.num_kv_heads + heads - 1) / heads;
+  // layers of a CTA: as many as leave about eight CTAs to an SM
+  const int64_t ctas = static_cast<int64_t>(a.batch_size) * 2 * chunks * a.num_layers;
+  const int per_cta = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas / (8 * num_sms))));
+  const dim3 grid(static_cast<unsigned>(a.batch_size), static_cast<unsigned>(2 * chunks),
+                  static_cast<unsigned>((a.num_layers + per_cta - 1) / per_cta));
+  compact_drafts_kernel<kDataBytes, kScaleBytes><<<grid, kThreads, 0, stream>>>(a, heads, per_cta);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_compact_drafts(const CompactArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.batch_size), static_cast<unsigned>(a.num_kv_heads),
-                  static_cast<unsigned>(2 * a.num_layers));
-  // scale rows are moved in words when they and the regions allow it
-  if ((a.head_size / kGroup) % 4 == 0)
-    compact_drafts_kernel<4><<<grid, kThreads, 0, stream>>>(a);
-  else
-    compact_drafts_kernel<1><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_compact_drafts(const CompactArgs& a, int num_sms, cudaStream_t stream) {
+  // data in 16 bytes and scales in words where the rows and regions allow it
+  // (a region is a multiple of 8 bytes: host check)
+  const int64_t region = static_cast<int64_t>(a.block_size) * a.num_kv_heads * (a.head_size / 2 + a.head_size / kGroup);
+  const bool wide = a.head_size % 32 == 0 && region % 16 == 0;
+  if ((a.head_size / kGroup) % 4 == 0) return wide ? launch<16, 4>(a, num_sms, stream) : launch<8, 4>(a, num_sms, stream);
+  return wide ? launch<16, 1>(a, num_sms, stream) : launch<8, 1>(a, num_sms, stream);
 }
 
 }  // namespace kvq

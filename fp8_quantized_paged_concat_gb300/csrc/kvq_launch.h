@@ -260,8 +260,9 @@ struct CompactArgs {
   const int32_t* block_table;
   int64_t block_table_stride;
   int32_t block_table_width;
+  FastDiv block_div;              // position -> table column
   int32_t* status;
 };
-cudaError_t launch_compact_drafts(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_compact_drafts(const CompactArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace kvq
