@@ -17,8 +17,8 @@
 // key head.  Each warp takes every fourth step of 32 keys, with its own
 // running maximum and sum, and the warps join at the end through shared
 // memory; ranges join in a second launch.  A warp copies a step's raw bytes
-// (32 entries of 9 D / 16 bytes, K and V) into its own three-stage ring with
-// asynchronous copies, two steps ahead, so that nothing but the warp's own
+// (32 entries of 9 D / 16 bytes, K and V) into its own two-stage ring with
+// asynchronous copies, a step ahead, so that nothing but the warp's own
 // copies is ever waited for.
 //
 // The products run as S^T = K Q^T and O^T = V^T P^T on the warp's matrix
@@ -48,7 +48,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                   // keys per warp step
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 // Shared memory of one warp's stage: 32 data rows of K, of V, then their scale rows.
 template <int D>
@@ -240,21 +240,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   };
   // this warp's steps: first, first + kWarps, ...
   const int32_t first = s0 + warp;
-  uint32_t valid_ring[2];                        // of the two steps in flight: bit i = key i exists
-  static_assert(kStages == 3, "two steps in flight");
+  uint32_t valid_ring[kStages - 1];              // of the steps in flight: bit i = key i exists
   look_up(first);
-  valid_ring[0] = start(first, 0);
-  look_up(first + kWarps);
-  valid_ring[1] = start(first + kWarps, 1);
-  look_up(first + 2 * kWarps);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    valid_ring[i] = start(first + i * kWarps, i);
+    look_up(first + (i + 1) * kWarps);
+  }
 
   // ---- the query rows ------------------------------------------------------
   // Lane (g, c) holds dimensions [c D/4, +D/4) of row 8 nt + g, scaled by a
   // power of two; the score of row 2c + x is multiplied back by sc.
   uint32_t q[kRowTiles][kKSteps][2];
-  float sc[kRowTiles][2], hidden[kRowTiles][2];
-  int32_t pos_hi[kRowTiles][2], pos_lo[kRowTiles][2];     // window: last visible key, first inside the window
-  int64_t q_token[kRowTiles][2];                          // tree: the row's token
+  float sc[kRowTiles][2];
   float m[kRowTiles][2], l[kRowTiles][2];                 // reference maximum, sum
   const float scale = a.scale_log2 * __ldg(a.k_scale);
 #pragma unroll
@@ -293,13 +291,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       // row 2c + x of the tile is loaded by the lanes with g = 2c + x
       sc[nt][x] = __shfl_sync(kFull, back, (2 * c + x) * 4);
       if (sc[nt][x] == 0.0f) sc[nt][x] = 1e-30f;            // as good as 0 for any score, but 0 for no infinity
-      hidden[nt][x] = sc[nt][x] < 0.0f ? INFINITY : -INFINITY;
       const int32_t rr = 8 * nt + 2 * c + x;
-      const uint32_t tk = a.group_div.div(static_cast<uint32_t>(row0 + min(rr, rows - 1)));
-      const int64_t p = rq.first_pos + tk;
-      pos_hi[nt][x] = rr < rows ? static_cast<int32_t>(max(int64_t{-1}, p)) : -1;
-      pos_lo[nt][x] = a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, p - a.window + 1)) : 0;
-      q_token[nt][x] = rq.token0 + tk;
       m[nt][x] = rr < rows ? -INFINITY : 0.0f;
       l[nt][x] = 0.0f;
     }
@@ -321,9 +313,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     cp_wait<kStages - 2>();
     __syncwarp();                                // the step has landed, and the stage before it has been read
     const uint32_t valid = valid_ring[0];
-    valid_ring[0] = valid_ring[1];
-    valid_ring[1] = start(step + 2 * kWarps, stage == 0 ? 2 : stage - 1);
-    look_up(step + 3 * kWarps);
+#pragma unroll
+    for (int i = 0; i + 2 < kStages; ++i) valid_ring[i] = valid_ring[i + 1];
+    valid_ring[kStages - 2] = start(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    look_up(step + kStages * kWarps);
     const uint32_t st = ring + stage * St::kBytes;
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
@@ -388,21 +381,27 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 #pragma unroll
       for (int nt = 0; nt < kRowTiles; ++nt)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          const int32_t rr = 8 * nt + 2 * c + x;
+          const int32_t tk = static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(row0 + min(rr, rows - 1))));
+          const int64_t at = rq.first_pos + tk;            // the row's position
+          const int32_t hi = rr < rows ? static_cast<int32_t>(max(int64_t{-1}, at)) : -1;
+          const int32_t lo = a.window > 0 ? static_cast<int32_t>(max(int64_t{0}, at - a.window + 1)) : 0;
+          const float hidden = sc[nt][x] < 0.0f ? INFINITY : -INFINITY;   // the score whose scaled value is -inf
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int32_t i = 8 * e + rg, p = base + i;      // e = 2 mt + y
+            const int32_t i = 8 * e + rg, p = base + i;    // e = 2 mt + y
             bool see = (valid >> i) & 1;
             if (a.tree_mask == nullptr) {
-              see = see && p <= pos_hi[nt][x] && (p >= pos_lo[nt][x] || p < a.num_sinks);
+              see = see && p <= hi && (p >= lo || p < a.num_sinks);
             } else if (see && p >= rq.first_pos) {
               const int32_t d = static_cast<int32_t>(p - rq.first_pos);
               see = (d >> 6) < a.tree_words &&
-                    ((__ldg(a.tree_mask + q_token[nt][x] * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
+                    ((__ldg(a.tree_mask + (rq.token0 + tk) * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
             }
-            // hidden: the score whose scaled value is -inf
-            if (!see) s[e >> 1][nt][2 * (e & 1) + x] = hidden[nt][x];
+            if (!see) s[e >> 1][nt][2 * (e & 1) + x] = hidden;
           }
+        }
     }
     // Weights against the reference m, the maximum of steps before: no
     // maximum of their own is taken unless their sum shows that one of them
@@ -730,23 +729,29 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
   const int64_t least = few ? 128 : 256;             // keys of a range: a step per warp, four tiles
-  if (blocks >= resident / 2) {
-    // The GPU is full: ranges only even out requests of different lengths (a
-    // window's are all alike), four to a CTA's place.
-    if (windowed || blocks >= 4 * resident) return 1;
-    const int64_t n = std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / 1024, (4 * resident + blocks - 1) / blocks});
-    if (n <= 1) return 1;
-    if (use_workspace != nullptr) *use_workspace = 1;
-    return static_cast<int32_t>(n);
+  int64_t n;
+  bool clustered = false;
+  if (!windowed && keys >= 4096 && 8 * blocks >= resident) {
+    // Long contexts, of lengths that may differ from request to request: six
+    // ranges to a CTA's place even them out (two where there are more blocks
+    // than places; equal lengths would do with one, which is 7 % faster then).
+    n = std::min<int64_t>(keys / 1024, ((few && blocks >= resident ? 2 : 6) * resident + blocks - 1) / blocks);
+  } else {
+    // As many as the call is short of CTAs.  A cluster's ranges cost no second
+    // launch (few rows; more rows' partial results pass faster through memory
+    // than between the SMs of a cluster: 192 KB in 6 us).
+    n = std::min<int64_t>(keys / least, resident / blocks);
+    if (few && n > KVQ_PER_HEAD_CLUSTER_SPLITS && keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least)
+      n = KVQ_PER_HEAD_CLUSTER_SPLITS;
+    clustered = few && n <= KVQ_PER_HEAD_CLUSTER_SPLITS;
   }
-  // The call is short of CTAs.  A cluster's ranges cost no second launch (few
-  // rows; more rows' partial results pass faster through memory than between
-  // the SMs of a cluster).
-  const int64_t n = std::max<int64_t>(1, std::min<int64_t>({KVQ_PER_HEAD_MAX_SPLITS, keys / least, resident / blocks}));
-  if (few && n <= KVQ_PER_HEAD_CLUSTER_SPLITS) return static_cast<int32_t>(n);
-  if (few && keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least) return KVQ_PER_HEAD_CLUSTER_SPLITS;
-  if (n == 1) return 1;
-  if (use_workspace != nullptr) *use_workspace = 1;
+  n = std::max<int64_t>(1, std::min<int64_t>(KVQ_PER_HEAD_MAX_SPLITS, n));
+  if (n > 1 && !clustered) {
+    // no more than the ranges of whole 128-key steps come to
+    const int64_t steps = (keys + 127) / 128, per = (steps + n - 1) / n;
+    n = (steps + per - 1) / per;
+    if (use_workspace != nullptr) *use_workspace = n > 1;
+  }
   return static_cast<int32_t>(n);
 }
 
