@@ -131,7 +131,7 @@ struct Piece {
 
 // Byte offset of part i of lane part k (0..3) of raw row r: rows are D / 2
 // bytes apart, their pieces permuted so that 8 rows' reads of one part fall
-// in different banks.
+// in different banks.  (The permutation repeats every 8 rows.)
 template <int D>
 __device__ __forceinline__ uint32_t raw_offset(uint32_t r, uint32_t k, uint32_t i) {
   if constexpr (D == 64) return r * 32 + 8 * (k ^ ((r >> 1) & 2));
@@ -139,32 +139,46 @@ __device__ __forceinline__ uint32_t raw_offset(uint32_t r, uint32_t k, uint32_t 
   return r * 128 + 16 * ((2 * k + i) ^ (r & 7));
 }
 
+// A lane's places in the raw ring and in the decoded tiles, for the row of
+// its first pass; a later pass's are a whole number of 8-row groups on.
 template <int D>
-__device__ __forceinline__ void load_piece(uint32_t data, uint32_t scales, uint32_t r, uint32_t k, Piece<D>& e) {
+struct Lane {
+  uint32_t raw[D == 256 ? 2 : 1], sf, tile[D / 32];
+  __device__ __forceinline__ Lane(uint32_t r, uint32_t k, uint32_t scales) {
+#pragma unroll
+    for (int i = 0; i < (D == 256 ? 2 : 1); ++i) raw[i] = raw_offset<D>(r, k, i);
+    sf = scales + r * (D / 16) + (D / 64) * k;
+    // D / 4 dimensions: block (D / 4) k / 64, chunks from ((D / 4) k % 64) / 8 on
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      tile[j] = (D * k / 256) * kKBlock + r * 128u + ((((D / 32 * k) & 7) + j) ^ (r & 7u)) * 16u;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_piece(uint32_t raw, const Lane<D>& at, int groups, Piece<D>& e) {
   if constexpr (D == 64) {
-    const uint2 v = lds64(data + raw_offset<D>(r, k, 0));
+    const uint2 v = lds64(raw + at.raw[0] + groups * 8 * (D / 2));
     e.w[0] = v.x;
     e.w[1] = v.y;
-    e.sf = lds8(scales + r * 4 + k);
+    e.sf = lds8(raw + at.sf + groups * 8 * (D / 16));
   } else {
 #pragma unroll
     for (int i = 0; i < D / 128; ++i) {
-      const uint4 v = ld_shared16(data + raw_offset<D>(r, k, i));
+      const uint4 v = ld_shared16(raw + at.raw[i] + groups * 8 * (D / 2));
       e.w[4 * i] = v.x;
       e.w[4 * i + 1] = v.y;
       e.w[4 * i + 2] = v.z;
       e.w[4 * i + 3] = v.w;
     }
-    e.sf = D == 128 ? lds16(scales + r * 8 + 2 * k) : lds32(scales + r * 16 + 4 * k);
+    const uint32_t sf = raw + at.sf + groups * 8 * (D / 16);
+    e.sf = D == 128 ? lds16(sf) : lds32(sf);
   }
 }
 
-// Decodes a piece and stores its 16-byte chunks into row r of a tile.
+// Decodes a piece and stores its 16-byte chunks into its row of a tile.
 template <int D, bool kValues>
-__device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, const Piece<D>& e) {
-  // a lane's D / 4 dimensions: block (D / 4) k / 64, chunks from ((D / 4) k % 64) / 8 on
-  const uint32_t base = tile + (D * k / 256) * kKBlock + r * 128u + ((r & 7u) << 4);
-  const uint32_t chunk0 = (D / 32 * k) & 7;
+__device__ __forceinline__ void store_piece(uint32_t tile, const Lane<D>& at, int groups, const Piece<D>& e) {
 #pragma unroll
   for (int p = 0; p < (D + 127) / 128; ++p) {        // two scales at a time
     uint32_t s2 = bits(e4m3x2_to_half2(e.sf >> (16 * p)));
@@ -174,7 +188,7 @@ __device__ __forceinline__ void store_piece(uint32_t tile, uint32_t r, int k, co
       const uint32_t sf = j < 2 ? low_both(s2) : high_both(s2);
       uint32_t h[4];
       e2m1x8(e.w[4 * p + j], h);
-      st_shared16(base ^ ((chunk0 + 4 * p + j) << 4),
+      st_shared16(tile + at.tile[4 * p + j] + groups * 1024,
                   make_uint4(hmul2(h[0], sf), hmul2(h[1], sf), hmul2(h[2], sf), hmul2(h[3], sf)));
     }
   }
@@ -203,8 +217,8 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   const int32_t chunks = n_tiles * S::kParts;
   const uint8_t* side = a.cache + (kValues ? a.region : 0);
   const int32_t* table = a.block_table + b * a.block_table_stride;
-  auto row_of = [&](int pass) { return static_cast<uint32_t>(8 * (me + kWarps * pass) + (lane & 7)); };
-  const uint32_t own_row = row_of(lane >> 3);       // of the warp's rows, the one this lane looks up
+  const Lane<D> at(8 * me + (lane & 7), k, S::kRawScales);
+  const uint32_t own_row = 8 * (me + kWarps * (lane >> 3)) + (lane & 7);   // of the warp's rows, the one it looks up
   const bool has_row = own_row < S::kChunk && (lane >> 3) < kPasses;
   const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
   LookUp next;                                      // its position in the next chunk to be copied
@@ -237,7 +251,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
         constexpr int kPiece = D == 64 ? 8 : 16;
 #pragma unroll
         for (int j = 0; j < (D == 256 ? 2 : 1); ++j)
-          cp_async<kPiece>(raw + raw_offset<D>(row_of(i), k, j), src + 16 * j, there ? kPiece : 0);
+          cp_async<kPiece>(raw + at.raw[j] + i * kWarps * 8 * (D / 2), src + 16 * j, there ? kPiece : 0);
       }
       // Which keys exist, for the softmax; a slot's last reader is long done
       // (kRing - 1 chunks ahead of a tile whose buffers are free).
@@ -267,12 +281,12 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     Piece<D> e[kPasses];                            // all read first, so that their latencies overlap
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      if (me + kWarps * i < kGroups) load_piece<D>(raw, raw + S::kRawScales, row_of(i), k, e[i]);
+      if (me + kWarps * i < kGroups) load_piece<D>(raw, at, i * kWarps, e[i]);
     if (h % S::kParts == 0 && t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (me + kWarps * i < kGroups)
-        store_piece<D, kValues>(tiles + st * S::kTileBytes, (h % S::kParts) * S::kChunk + row_of(i), k, e[i]);
+        store_piece<D, kValues>(tiles + st * S::kTileBytes + (h % S::kParts) * S::kChunk * 128, at, i * kWarps, e[i]);
     if (h % S::kParts == S::kParts - 1) {
       fence_async_smem();
       __syncwarp();
@@ -440,24 +454,32 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     bool done = true;                               // every wait was met
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
+    // Steps [full0, full1) of the keys are visible whole to every row of the
+    // warp (those whose pages all exist): no mask is looked at there.
+    int32_t full0 = keys.sink_steps, full1;
+    if (a.tree_mask != nullptr) {
+      full1 = rq.first_pos <= 0 ? 0 : static_cast<int32_t>(min(rq.first_pos, static_cast<int64_t>(rq.len)) / kKeys);
+    } else {
+      const int32_t hi = __reduce_min_sync(kFull, has_row ? pos_hi : INT32_MAX);
+      const int32_t lo = __reduce_max_sync(kFull, has_row ? pos_lo : 0);
+      full0 += (max(lo - keys.lo, 0) + kKeys - 1) / kKeys;
+      const int32_t whole = min(hi, keys.hi - 1) + 1 - keys.lo;        // positions from keys.lo on
+      full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
+    }
+    bool fresh = true;                              // some row has no reference yet (uniform over the warp)
     for (int32_t t = 0; t < n_tiles; ++t) {
       const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
       // which of the tile's keys the row sees
-      const int32_t p0 = keys.base(s0 + t);
       if (!warp_wait(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) {
         done = false;
         break;
       }
       const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
-      bool all = (valid.x & valid.y) == kFull;
-      if (a.tree_mask != nullptr)
-        all = all && p0 + kKeys <= rq.first_pos;
-      else
-        all = all && p0 + kKeys - 1 <= pos_hi && (p0 >= pos_lo || p0 + kKeys <= a.num_sinks);
-      const bool masked = __any_sync(kFull, !all && row < rows);
+      const bool masked = s0 + t < full0 || s0 + t >= full1 || (valid.x & valid.y) != kFull;
       uint32_t see[2] = {0, 0};
-      if (masked && row < rows) {
+      if (masked && has_row) {
+        const int32_t p0 = keys.base(s0 + t);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int32_t pc = p0 + 32 * c;
@@ -506,7 +528,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       };
       // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
       // sum is takes a new reference, its tile's maximum (as in its first tile).
-      const bool fresh = t == 0 || __any_sync(kFull, m == -INFINITY);
       if (!fresh) weights();
       if (fresh || __any_sync(kFull, sum > kMaxWeight)) {
         float top = -INFINITY;
@@ -520,6 +541,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           alpha = ex2(m - top);                     // 0 while m is -inf
           m = top;
         }
+        fresh = __any_sync(kFull, m == -INFINITY);
         weights();
         l *= alpha;
         if (t > 0) {
