@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <sstream>
 #include <string>
 
@@ -110,9 +111,9 @@ int32_t* status_word(PyObject* o, int index) {
   return static_cast<int32_t*>(t.data_ptr());
 }
 
-// The raw stream: the current one of the device, a torch stream's, or a number.
-kvq_stream_t stream_of(PyObject* o, int index) {
-  if (o == Py_None) return reinterpret_cast<kvq_stream_t>(c10::cuda::getCurrentCUDAStream(index).stream());
+// The stream of the call: the current one of the device, a torch stream, or a raw handle.
+cudaStream_t stream_of(PyObject* o, int index) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
   PyObject* handle = o;
   PyObject* owned = nullptr;
   if (!PyLong_Check(o)) {
@@ -128,8 +129,37 @@ kvq_stream_t stream_of(PyObject* o, int index) {
   void* p = PyLong_AsVoidPtr(handle);
   Py_XDECREF(owned);
   if (p == nullptr && PyErr_Occurred()) pending();
-  return static_cast<kvq_stream_t>(p);
+  return static_cast<cudaStream_t>(p);
 }
+
+// Where a call runs: its tensors' device, and its stream.  What the call
+// allocates comes from that stream's memory, so that nothing else still uses
+// it and a workspace can be freed on return; results are known to the caller's
+// current stream as well, and may be freed there.
+class Scope {
+ public:
+  Scope(PyObject* stream_object, int dev) : device_(static_cast<c10::DeviceIndex>(dev)) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev);
+    raw_ = stream_of(stream_object, dev);
+    if (raw_ == current.stream()) return;
+    callers_ = current;
+    const auto index = static_cast<c10::DeviceIndex>(dev);
+    guard_.reset_stream(raw_ == nullptr ? c10::cuda::getDefaultCUDAStream(index)
+                                        : c10::cuda::getStreamFromExternal(raw_, index));
+  }
+  kvq_stream_t stream() const { return reinterpret_cast<kvq_stream_t>(raw_); }
+  at::Tensor result(c10::IntArrayRef shape, const at::TensorOptions& options) const {
+    at::Tensor t = at::empty(shape, options);
+    if (callers_) t.record_stream(*callers_);
+    return t;
+  }
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+  std::optional<c10::cuda::CUDAStream> callers_;
+  cudaStream_t raw_ = nullptr;
+};
 
 struct CacheShape {
   int32_t layout, block_size, heads, head_size;
@@ -228,9 +258,9 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float eps = real(a[6]);
     const int interleaved = PyObject_IsTrue(a[7]);
     if (interleaved < 0) pending();
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    const at::Tensor qo = a[8] == Py_None ? at::empty({T, H, D}, q.options()) : tensor("q_out", a[8]);
-    const at::Tensor ko = a[9] == Py_None ? at::empty({T, KH, D}, k.options()) : tensor("k_out", a[9]);
+    const Scope scope(a[11], dev);
+    const at::Tensor qo = a[8] == Py_None ? scope.result({T, H, D}, q.options()) : tensor("q_out", a[8]);
+    const at::Tensor ko = a[9] == Py_None ? scope.result({T, KH, D}, k.options()) : tensor("k_out", a[9]);
     check("q_out", qo, at::kBFloat16, dev, 3);
     check("k_out", ko, at::kBFloat16, dev, 3);
     shaped("q_out", qo, {T, H, D});
@@ -240,7 +270,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           static_cast<const int64_t*>(pos.data_ptr()), T, dim(H), dim(KH), dim(D),
                           static_cast<const float*>(table.data_ptr()), row_stride(table), table.size(0),
                           dim(table.size(1)), interleaved, eps, qo.data_ptr(), sqo.t, sqo.h, ko.data_ptr(), sko.t, sko.h,
-                          status_word(a[10], dev), stream_of(a[11], dev)),
+                          status_word(a[10], dev), scope.stream()),
          "kvq_qk_norm_rope");
     return pair(qo, &ko);
   });
@@ -272,14 +302,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t max_query = int32("max_query_len", a[9]), max_seq = int32("max_seq_len", a[10]);
     const int32_t window = int32("window", a[11]), sinks = int32("num_sinks", a[12]);
     const bool tree = a[3] != Py_None;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    const at::Tensor out = a[16] == Py_None ? at::empty({T, H, D}, q.options()) : tensor("out", a[16]);
+    const Scope scope(a[19], dev);
+    const at::Tensor out = a[16] == Py_None ? scope.result({T, H, D}, q.options()) : tensor("out", a[16]);
     check("out", out, at::kBFloat16, dev, 3);
     shaped("out", out, {T, H, D});
     const bool want_lse = a[17] != Py_False;
     at::Tensor lse;
     if (want_lse) {
-      lse = a[17] == Py_None ? at::empty({T, H}, q.options().dtype(at::kFloat)) : tensor("lse", a[17]);
+      lse = a[17] == Py_None ? scope.result({T, H}, q.options().dtype(at::kFloat)) : tensor("lse", a[17]);
       check("lse", lse, at::kFloat, dev, 2);
       shaped("lse", lse, {T, H});
     }
@@ -309,7 +339,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* lse_ptr = want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
     const int64_t lse_stride = want_lse ? row_stride(lse) : 0;
     int32_t* status = status_word(a[18], dev);
-    const kvq_stream_t stream = stream_of(a[19], dev);
+    const kvq_stream_t stream = scope.stream();
     const auto* start_p = static_cast<const int32_t*>(start.data_ptr());
     const auto* lens_p = static_cast<const int32_t*>(lens.data_ptr());
     const auto* table_p = static_cast<const int32_t*>(table.data_ptr());
@@ -358,14 +388,14 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shaped("accepted", accepted, {B, accepted.size(1)});
     check("block_table", table, at::kInt, dev, 2);
     shaped("block_table", table, {B, table.size(1)});
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    const Scope scope(a[8], dev);
     must(lib.compact(static_cast<uint8_t*>(cache.data_ptr()), dim(layers), many ? cache.stride(0) : 0,
                      cache.size(many ? 1 : 0), c.block_size, c.layout, c.heads, c.head_size,
                      static_cast<const int32_t*>(start.data_ptr()), static_cast<const int32_t*>(lens.data_ptr()), dim(B),
                      static_cast<const int32_t*>(accepted.data_ptr()), row_stride(accepted),
                      static_cast<const int32_t*>(counts.data_ptr()), dim(accepted.size(1)),
                      static_cast<const int32_t*>(table.data_ptr()), row_stride(table), dim(table.size(1)),
-                     status_word(a[7], dev), stream_of(a[8], dev)),
+                     status_word(a[7], dev), scope.stream()),
          "kvq_compact_drafts_nvfp4_per_head");
     Py_RETURN_NONE;
   });

@@ -672,6 +672,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       const uint64_t vdesc = sw128_desc(base + S::kV, kKBlock, 1024);
       bool ok = true;
       for (int32_t t = 0; t < n_tiles && ok; ++t) {
+#ifdef KVQ_ATTN_STALL_TILE
+        // Failure-detection build only (tests/test_gpu_per_head_timeout.py):
+        // no product from this tile on, as if the tensor work never
+        // completed; the other roles' bounded waits run out.
+        if (t == KVQ_ATTN_STALL_TILE) break;
+#endif
         ok = have(v_full + 8 * (t % S::kStages), t / S::kStages);
         const uint64_t vd = vdesc + (((t % S::kStages) * S::kTileBytes) >> 4);
 #pragma unroll

@@ -560,3 +560,77 @@ def test_graphs_and_streams(kvq, new, splits, joined):
         for i, (_, _, got, _) in enumerate(graphs):
             want = eager[1 - i if swap else i]
             assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_side_stream_results_and_workspaces_are_the_streams(kvq, raw):
+    """Calls on another stream that allocate their results and workspace: bits
+    of the eager calls, whatever the current stream does with freed memory."""
+    b = Batch([(900, 60), (333, 60)], 8, 2, 128, 16, "NHD", 71)
+    d = b.device()
+    eager = kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        got.append(kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=4,
+                                                           stream=side.cuda_stream if raw else side))
+        # as large as the workspace just given back, and written at once on the current stream
+        torch.empty(kvq.kvq_per_head_attention_workspace_bytes(120, 8, 128, 4), dtype=torch.uint8, device=DEV).fill_(0xFF)
+    torch.cuda.current_stream().wait_stream(side)
+    for out, lse in got:
+        assert torch.equal(out.view(torch.int16), eager[0].view(torch.int16)) and torch.equal(lse, eager[1])
+
+
+def test_shared_pages_and_the_widest_batch(kvq):
+    """The largest batch, its requests all on the same pages with the same
+    query: every row has the first one's bits, and those are right."""
+    b = Batch([(33, 1)], 4, 2, 64, 16, "NHD", 72)
+    d = b.device()
+    n = 65535
+    d.update(q=d["q"].expand(n, -1, -1), query_start=torch.arange(n + 1, dtype=torch.int32, device=DEV),
+             seq_lens=d["seq_lens"].expand(n).contiguous(), block_table=d["block_table"].expand(n, -1).contiguous())
+    for splits in (1, 2):
+        out, lse = kvq.kvq_window_attention_nvfp4_per_head(**d, num_splits=splits)
+        check((out[:1], lse[:1]), b.want())
+        assert torch.equal(out.view(torch.int16), out[:1].view(torch.int16).expand_as(out))
+        assert torch.equal(lse, lse[:1].expand_as(lse))
+
+
+def test_python_calls_refuse_what_does_not_fit(kvq):
+    """Types, shapes, layouts and workspaces that no launch may see."""
+    b = Batch([(40, 1), (8, 1)], 4, 2, 128, 16, "NHD", 73)
+    d = b.device()
+    call = kvq.kvq_window_attention_nvfp4_per_head
+    wrong = [("q", d["q"].float(), "q: expected"), ("q", d["q"][0], "q: expected"), ("q", d["q"][..., ::2], "q: expected"),
+             ("query_start", d["query_start"][:-1], "query_start: expected"),
+             ("seq_lens", d["seq_lens"].long(), "seq_lens: expected"), ("seq_lens", d["seq_lens"].cpu(), "seq_lens: expected"),
+             ("block_table", d["block_table"][:1], "block_table: expected"),
+             ("kv_cache", d["kv_cache"][:, :1], "kv_cache: expected"), ("kv_cache", d["kv_cache"][:, :, ::2], "kv_cache: expected"),
+             ("kv_cache", d["kv_cache"][..., :-9], "kv_cache: expected"), ("layout", "NDH", "layout: expected"),
+             ("layout", 1, "layout: expected"), ("k_scale", d["k_scale"].double(), "k_scale: expected"),
+             ("max_query_len", 1 << 31, "max_query_len: out of range"),
+             ("out", torch.empty(2, 4, 64, dtype=torch.bfloat16, device=DEV), "out: expected"),
+             ("lse", torch.empty(2, 3, device=DEV), "lse: expected"),
+             ("status", torch.empty(0, dtype=torch.int32, device=DEV), "status: expected")]
+    for name, value, needle in wrong:
+        with pytest.raises(ValueError, match=needle):
+            call(**{**d, name: value})
+    with pytest.raises(RuntimeError, match="workspace must be"):
+        call(**d, num_splits=2, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(RuntimeError, match="num_splits"):
+        call(**d, num_splits=129)
+    with pytest.raises(RuntimeError, match="head_size"):
+        q = torch.zeros(2, 4, 96, dtype=torch.bfloat16, device=DEV)
+        call(**dict(d, q=q, kv_cache=torch.zeros(4, 2, 16, 2, 54, dtype=torch.uint8, device=DEV)))
+    with pytest.raises(ValueError, match="tree_mask: expected"):
+        tree = {k: v for k, v in d.items()}
+        kvq.kvq_tree_attention_nvfp4_per_head(**tree, tree_mask=torch.zeros(1, 1, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="accepted_lens: expected"):
+        kvq.kvq_compact_drafts_nvfp4_per_head(d["kv_cache"], d["query_start"], d["seq_lens"], i32([[0], [0]]), i32([1]),
+                                              d["block_table"])
+    with pytest.raises(ValueError, match="positions: expected"):
+        w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+        kvq.kvq_qk_norm_rope(d["q"], d["q"], w, w, i32([0, 1]), torch.zeros(8, 128, device=DEV), 1e-6)
+    out, lse = call(**d)                                    # nothing above left an error behind
+    check((out, lse), b.want())
