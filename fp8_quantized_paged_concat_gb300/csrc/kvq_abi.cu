@@ -863,7 +863,8 @@ kvq_status per_head_attention(
                 "%s: workspace must be non-NULL, 16-byte aligned and at least %lld bytes (got %lld)", fn,
                 static_cast<long long>(need), static_cast<long long>(workspace_bytes));
   }
-  if (kvq_status s = check_device(fn)) return s;
+  int num_sms = 0;
+  if (kvq_status s = check_device(fn, &num_sms)) return s;
   kvq::PerHeadAttentionArgs a{};
   a.q = q;
   a.q_stride_t = q_stride_t;
@@ -919,7 +920,7 @@ kvq_status per_head_attention(
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = static_cast<float*>(workspace) + num_tokens * num_heads * num_splits * head_size;
   }
-  return launched(fn, kvq::launch_per_head_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(fn, kvq::launch_per_head_attention(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -710,43 +710,69 @@ cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&config, per_head_join_kernel<D>, a);
 }
 
+// CTAs of the few-row kernel that share an SM (its launch bounds).
+constexpr int resident_ctas(int32_t head_size, int64_t block) { return head_size == 256 ? 2 : block == 16 ? 3 : 4; }
+
+// Rows per block of the few-row kernel.  16 rows share a decoded key where
+// such blocks fill the GPU (128 requests x 2048 keys, head size 128, 16 rows:
+// 111 us against 126 with two blocks of 8; 32 rows: 183 against 230); a
+// smaller call is short of CTAs, and blocks of 8 halve its chain (one request
+// x 1024 keys, 16 rows: 12.9 against 15.0 us; 16384 keys: 23 against 31).
+// D = 256 has no registers for 16.
+int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, int sms) {
+  return rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16) * int64_t{sms}
+             ? 16 : 8;
+}
+
+// The most rows per request and key head that go to the few-row kernel, which
+// decodes every key once per block of rows; above, the tensor memory kernel
+// decodes it once.  us of the one and the other, 128 requests x 2048 keys x 8
+// key heads (4 at D = 256):
+//   D =  64: 48 rows 169 / 218, 64 rows 214 / 220, 96 rows 314 / 224
+//   D = 128: 24 rows 181 / 232, 32 rows 183 / 234, 48 rows 265 / 240
+//   D = 256: 16 rows 144 / 187, 24 rows 199 / 189, 32 rows 251 / 189
+int64_t most_few_rows(int32_t head_size) { return head_size == 64 ? 64 : head_size == 128 ? 32 : 16; }
+
 }  // namespace
 
-int64_t per_head_block_rows(int64_t rows, int32_t head_size) {
-  if (rows <= 8) return 8;
-  if (rows <= 32) return head_size == 256 ? 8 : 16;  // two row tiles of D = 256 would not fit the registers
-  return rows <= 128 || head_size == 256 ? 128 : 256;
-}
+// Rows per block of the tensor memory kernel: one row tile, or two that share
+// a decoded key (32 requests of 1024 keys x 256 rows, head size 128: 70 us
+// against 99 with blocks of 128; D = 256 has tensor memory for one).
+int64_t per_head_prefill_rows(int64_t rows, int32_t head_size) { return rows <= 128 || head_size == 256 ? 128 : 256; }
 
 int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t num_kv_heads, int32_t head_size,
                                 int64_t batch_size, int64_t max_seq_len, int64_t window, int64_t num_sinks, int sms,
                                 int32_t* use_workspace) {
-  const int64_t rows = max_query_len * group, block = per_head_block_rows(rows, head_size);
-  const int64_t blocks = (rows + block - 1) / block * num_kv_heads * batch_size;
-  const bool few = block <= 16;
-  const int64_t resident = (few ? 4 : 1) * static_cast<int64_t>(sms);
+  const int64_t rows = max_query_len * group, groups = num_kv_heads * batch_size;
   const bool windowed = window > 0 && window < max_seq_len;
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
-  const int64_t least = few ? 128 : 256;             // keys of a range: a step per warp, four tiles
+  const bool few = rows <= most_few_rows(head_size);
+  const bool ragged = !windowed && keys >= 4096 && batch_size > 1;   // long contexts, whose lengths may differ
+  // A small call's ranges run as clusters of the few-row kernel: no second launch.
+  if (rows <= KVQ_PER_HEAD_CLUSTER_ROWS) {
+    constexpr int64_t kMax = KVQ_PER_HEAD_CLUSTER_SPLITS, kLeast = 128;       // a step per warp
+    const int64_t blocks = (rows + 7) / 8 * groups, places = resident_ctas(head_size, 8) * int64_t{sms};
+    const bool long_small = ragged && 8 * blocks >= places;
+    const int64_t n = std::min<int64_t>(keys / kLeast, places / blocks);
+    if (!long_small && n > 1 && (n <= kMax || keys <= kMax * 8 * kLeast)) return static_cast<int32_t>(std::min(n, kMax));
+  }
+  const int64_t block = few ? few_rows(rows, groups, head_size, 1, sms) : per_head_prefill_rows(rows, head_size);
+  const int64_t blocks = (rows + block - 1) / block * groups;
+  const int64_t places = (few ? resident_ctas(head_size, block) : 1) * int64_t{sms};
   int64_t n;
-  bool clustered = false;
-  if (!windowed && keys >= 4096 && 8 * blocks >= resident) {
-    // Long contexts, of lengths that may differ from request to request: six
-    // ranges to a CTA's place even them out (two where there are more blocks
-    // than places; equal lengths would do with one, which is 7 % faster then).
-    n = std::min<int64_t>(keys / 1024, ((few && blocks >= resident ? 2 : 6) * resident + blocks - 1) / blocks);
+  if (ragged && 8 * blocks >= places) {
+    // several ranges to a CTA's place even the lengths out: six of the few-row
+    // kernel's (two where there are more blocks than places; equal lengths
+    // would do with one, which is 7 % faster then), three of the tensor memory
+    // kernel's, which cost more to start
+    const int64_t per_place = !few ? 3 : blocks >= places ? 2 : 6;
+    n = std::min<int64_t>(keys / 1024, (per_place * places + blocks - 1) / blocks);
   } else {
-    // As many as the call is short of CTAs.  A cluster's ranges cost no second
-    // launch (few rows; more rows' partial results pass faster through memory
-    // than between the SMs of a cluster: 192 KB in 6 us).
-    n = std::min<int64_t>(keys / least, resident / blocks);
-    if (few && n > KVQ_PER_HEAD_CLUSTER_SPLITS && keys <= KVQ_PER_HEAD_CLUSTER_SPLITS * 8 * least)
-      n = KVQ_PER_HEAD_CLUSTER_SPLITS;
-    clustered = few && n <= KVQ_PER_HEAD_CLUSTER_SPLITS;
+    n = std::min<int64_t>(keys / (few ? 128 : 256), places / blocks);   // as many as the call is short of CTAs
   }
   n = std::max<int64_t>(1, std::min<int64_t>(KVQ_PER_HEAD_MAX_SPLITS, n));
-  if (n > 1 && !clustered) {
+  if (n > 1) {
     // no more than the ranges of whole 128-key steps come to
     const int64_t steps = (keys + 127) / 128, per = (steps + n - 1) / n;
     n = (steps + per - 1) / per;
@@ -755,10 +781,11 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
   return static_cast<int32_t>(n);
 }
 
-cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  const int64_t block = per_head_block_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size);
+cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, int sms, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
+  const int64_t block = few_rows(rows, static_cast<int64_t>(a.num_kv_heads) * a.batch_size, a.head_size, a.num_splits, sms);
   cudaError_t e;
-  if (block > 16)
+  if (!a.cluster && rows > most_few_rows(a.head_size))
     e = launch_per_head_prefill(a, stream);
   else if (a.head_size == 64)
     e = block == 8 ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);

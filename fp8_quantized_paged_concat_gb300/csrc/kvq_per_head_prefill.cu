@@ -721,7 +721,7 @@ cudaError_t launch(const PerHeadAttentionArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   // two row tiles share a decoded key tile wherever a request can fill them
-  const bool two = per_head_block_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size) == 256;
+  const bool two = per_head_prefill_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size) == 256;
   switch (a.head_size) {
     case 64: return two ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
     case 128: return two ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
