@@ -762,11 +762,14 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
   const int64_t places = (few ? resident_ctas(head_size, block) : 1) * int64_t{sms};
   int64_t n;
   if (ragged && 8 * blocks >= places) {
-    // several ranges to a CTA's place even the lengths out: six of the few-row
-    // kernel's (two where there are more blocks than places; equal lengths
-    // would do with one, which is 7 % faster then), three of the tensor memory
-    // kernel's, which cost more to start
-    const int64_t per_place = !few ? 3 : blocks >= places ? 2 : 6;
+    // Several ranges to a CTA's place even the lengths out.  The few-row
+    // kernel: six, or two where there are more blocks than places (32 requests
+    // of 7k to 34k keys: 164 us; one range per place 217; equal lengths would
+    // do with one, 4 to 20 % faster then).  The tensor memory kernel, whose
+    // ranges cost more to start: three (32 requests x 8192 keys x 48 rows at D =
+    // 256: 203 us, six 232), or six where there are more blocks than places (32
+    // trees of 64 drafts behind 7k to 34k keys: 611 us, three 655, one 795).
+    const int64_t per_place = few == (blocks >= places) ? (few ? 2 : 3) : 6;
     n = std::min<int64_t>(keys / 1024, (per_place * places + blocks - 1) / blocks);
   } else {
     n = std::min<int64_t>(keys / (few ? 128 : 256), places / blocks);   // as many as the call is short of CTAs

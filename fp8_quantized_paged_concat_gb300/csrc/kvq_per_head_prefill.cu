@@ -84,10 +84,11 @@ struct Shape {
   static_assert(kTiles * D <= 256 && kMisc % 16 == 0, "tensor memory, alignment");
 };
 
-// warp_wait_or_abort whose usual case, the phase complete or completed while
-// the first try sleeps, takes no clock and no loop.
+// warp_wait_or_abort whose usual case, the phase complete already, takes one
+// test, without the clock, the loop and the suspension of a waiting try
+// (trees 32 x 64: 576 -> 566 us).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* s_abort) {
-  return __all_sync(kFull, mbar_try_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
+  return __all_sync(kFull, mbar_test_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
 }
 
 // The CTA's set-up is done (tensor memory, barriers): every role comes here
@@ -206,7 +207,7 @@ __device__ __forceinline__ void store_piece(uint32_t tile, const Lane<D>& at, in
 template <int D, int kTiles, bool kValues>
 __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, uint32_t head, const Keys<kKeys>& keys,
                                         int32_t s0, int32_t n_tiles, int me, int lane, bool bad_index, uint32_t base,
-                                        uint32_t full, uint32_t empty, uint32_t valid_full, uint8_t* valid_ring,
+                                        uint32_t full, uint32_t empty, uint8_t* valid_ring,
                                         volatile int* s_abort) {
   using S = Shape<D, kTiles>;
   constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
@@ -290,10 +291,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     if (h % S::kParts == S::kParts - 1) {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (!kValues) mbar_arrive(valid_full + 8 * (t % kValidRing));
-        mbar_arrive(full + 8 * st);
-      }
+      if (lane == 0) mbar_arrive(full + 8 * st);
     }
   }
   cp_wait<0>();                                     // no copy outlives the CTA
@@ -342,11 +340,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t k_full = bar, k_empty = bar + 24, v_full = bar + 48, v_empty = bar + 72;   // [kStages] each
   const uint32_t s_full = bar + 96, p_full = bar + 128, o_done = bar + 160;                 // [row tile][buffer] each
   const uint32_t drain = bar + 192, q_full = bar + 208;            // [2], 1
-  const uint32_t valid_full = bar + 216;                           // [kValidRing]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 344);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 348);
-  uint8_t* valid_ring = smem + S::kMisc + 352;     // [kValidRing][8]: bit per key of the tile
-  static_assert(S::kStages <= 3 && 216 + 8 * kValidRing <= 344 && 352 + 8 * kValidRing <= 512, "barrier layout");
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 216);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 220);
+  uint8_t* valid_ring = smem + S::kMisc + 224;     // [kValidRing][8]: bit per key of the tile
+  static_assert(S::kStages <= 3 && 224 + 8 * kValidRing <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -362,11 +359,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       mbar_init(v_empty + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 2);
       mbar_init(p_full + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
-    for (int i = 0; i < kValidRing; ++i) mbar_init(valid_full + 8 * i, S::kKeyWarps);
     mbar_init(drain, 1);
     mbar_init(drain + 8, 1);
     mbar_init(q_full, S::kSoftmaxWarps);
@@ -470,11 +466,13 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     for (int32_t t = 0; t < n_tiles; ++t) {
       const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
-      // which of the tile's keys the row sees
-      if (!warp_wait(valid_full + 8 * (t % kValidRing), (t / kValidRing) & 1, s_abort)) {
+      if (!warp_wait(s_full + 8 * buf, (t >> 1) & 1, s_abort)) {
         done = false;
         break;
       }
+      fence_after_sync();
+
+      // which of the tile's keys the row sees
       const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
       const bool masked = s0 + t < full0 || s0 + t >= full1 || (valid.x & valid.y) != kFull;
       uint32_t see[2] = {0, 0};
@@ -492,12 +490,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           see[c] = (c == 0 ? valid.x : valid.y) & w;
         }
       }
-      if (!warp_wait(s_full + 8 * buf, (t >> 1) & 1, s_abort)) {
-        done = false;
-        break;
-      }
-      fence_after_sync();
-
+      __syncwarp();                                 // the load is the whole warp's
       uint32_t s[64], p[32];
       tmem_ld64(s_col, s);
       float sum;
@@ -631,7 +624,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     };
     if (warp < S::kScoreWarp) {
       produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
-                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, valid_full,
+                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty,
                                 valid_ring, s_abort);
     } else if (warp == S::kScoreWarp) {
       // ---- S_w(t) = Q_w K(t)^T (one elected lane; the warp waits together) -----
@@ -656,13 +649,16 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
                      qd + (((ks >> 2) * kBlockBytes + 32 * (ks & 3)) >> 4),
                      kd + (((ks >> 2) * kKBlock + 32 * (ks & 3)) >> 4), kIdesc, ks != 0);
           warp_commit(elected, s_full + 8 * (2 * w + (t & 1)));
+          // an arrival of this warp's own too: the masks that the key warps wrote
+          // before their tile pass on to the softmax
+          if (lane == 0) mbar_arrive(s_full + 8 * (2 * w + (t & 1)));
         }
         if (ok) warp_commit(elected, k_empty + 8 * (t % S::kStages));
       }
       drained(elected, drain);
     } else if (warp < S::kOutputWarp) {
       produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
-                               v_empty, valid_full, valid_ring, s_abort);
+                               v_empty, valid_ring, s_abort);
     } else {
       // ---- O_w += P_w(t) V(t) ---------------------------------------------------
       constexpr uint32_t kIdesc = idesc_f16(128, D, true);
