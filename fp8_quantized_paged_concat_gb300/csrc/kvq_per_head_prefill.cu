@@ -471,6 +471,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         break;
       }
       fence_after_sync();
+      uint32_t s[64], p[32];
+      tmem_ld64(s_col, s);
 
       // which of the tile's keys the row sees
       const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
@@ -490,9 +492,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           see[c] = (c == 0 ? valid.x : valid.y) & w;
         }
       }
-      __syncwarp();                                 // the load is the whole warp's
-      uint32_t s[64], p[32];
-      tmem_ld64(s_col, s);
       float sum;
       // weights against the reference m: p and their sum
       auto pass = [&](float off, auto with_mask) {
