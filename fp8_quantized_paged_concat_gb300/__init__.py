@@ -4,8 +4,8 @@ Thin Python binding over libkvq.so (include/kvq.h): each function has the
 name of the C entry point, checks dtypes / devices / shapes of the torch
 tensors it is given, passes their data pointers and strides and the current
 CUDA stream, and raises RuntimeError on a non-OK status (through ctypes, or,
-for the calls that serve from the per-head cache, a small extension module).  Every step of the
-computation runs in the library's sm_103a kernels; there is no fallback.  The
+for the calls that serve from the per-head cache, a small extension module).
+Every step of the computation runs in the library's sm_103a kernels; there is no fallback.  The
 library is built by ``__graft_entry__.build()`` (or
 ``python -m fp8_quantized_paged_concat_gb300._build``); importing this
 package does not load it, the first call does, and fails loudly if it is
@@ -650,9 +650,10 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     wrote it, layout "NHD" or "HND").  num_splits (default:
     kvq_per_head_attention_default_splits) key ranges, joined inside clusters
     (up to PER_HEAD_CLUSTER_SPLITS of calls with at most 32 query rows per
-    request and key head; no workspace) or through a workspace: a CUDA tensor of at least kvq_per_head_attention_workspace_bytes bytes
-    (allocated here when one is needed and None is given).  Returns (out bf16
-    [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
+    request and key head; no workspace) or through a workspace: a CUDA tensor
+    of at least kvq_per_head_attention_workspace_bytes bytes (allocated here,
+    on the call's stream, when one is needed and None is given).  Returns (out
+    bf16 [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, k_scale, v_scale,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)

@@ -17,7 +17,7 @@
 // signs are folded once per group into two factors per dimension, so that a
 // value costs two multiplications and one fused multiply-add.  A pair's other
 // half, when it is rot/2 away, sits rot/16 lanes on: its raw bf16 values come
-// by four shuffles.  16384 tokens x (32 + 8) heads of 128: 62 us, 5.5 TB/s
+// by four shuffles.  16384 tokens x (32 + 8) heads of 128: 59 us, 5.9 TB/s
 // (normalised fp32 values with unfused factors: 74 us).
 #include "kvq_device.cuh"
 #include "kvq_launch.h"
@@ -159,7 +159,7 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
 template <int kLanes>
 cudaError_t launch_heads(const NormRopeArgs& a, int num_sms, cudaStream_t stream) {
   // Eight heads per lane group share one table row and one set of weights and
-  // keep eight loads in flight (head size 128, 32 + 8 heads: 16384 tokens 62
+  // keep eight loads in flight (head size 128, 32 + 8 heads: 16384 tokens 59
   // us, with four heads 70, two 85, one 115); a call that gives the SMs less
   // than one CTA each that way takes one head per group (64 tokens: 6.8
   // against 8.8 us; at 256 tokens the two are equal).

@@ -16,7 +16,10 @@
 // of keys); the rows are (token, head) pairs of one request that share the
 // key head.  Each warp takes every fourth step of 32 keys, with its own
 // running maximum and sum, and the warps join at the end through shared
-// memory; ranges join in a second launch.  A warp copies a step's raw bytes
+// memory; the ranges of a small call run as a cluster and join through its
+// distributed shared memory (one request, window of 1024, 64 heads: 10.2 us
+// with its launch; with a second launch 14.0), others in a second launch,
+// under way before the first ends.  A warp copies a step's raw bytes
 // (32 entries of 9 D / 16 bytes, K and V) into its own two-stage ring with
 // asynchronous copies, a step ahead, so that nothing but the warp's own
 // copies is ever waited for.
@@ -38,6 +41,11 @@
 // that largest value, and what is lost below is under 2^-39 of it.  The
 // weights are kept as 2^(s - m + 6) with m at most 2^8 behind the true
 // maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
+//
+// Measured: 128 requests x 4100 keys x 32 heads (8 key heads) of 128, 606 MB:
+// 117 us, 5.2 TB/s; about 640 warp instructions per step of 32 keys for 4
+// rows, and their issue, not the copies, sets the pace (3 stages or 5 CTAs an
+// SM are slower: registers).
 #include <algorithm>
 
 #include "kvq_per_head_attention.cuh"

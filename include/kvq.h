@@ -4,7 +4,9 @@
  * The library writes bf16 key/value activations into quantized paged caches
  * and gathers quantized pages back into contiguous bf16 workspaces, for
  * DeepSeek-style sparse MLA (352-byte nvfp4_ds_mla and 656-byte fp8_ds_mla
- * entries) and for a per-head NVFP4 K/V cache.
+ * entries) and for a per-head NVFP4 K/V cache.  It also holds the attention
+ * over either cache and, for the per-head one, what a serving step needs
+ * around it: query/key norm with rotation, and the move of accepted drafts.
  *
  * Conventions shared by every entry point
  *   - Pointers named by a tensor are DEVICE pointers owned by the caller.  The
@@ -57,8 +59,9 @@ typedef int32_t kvq_status;
 /* Bits a kernel ORs into *d_status. */
 #define KVQ_STATUS_BAD_INDEX   0x1  /* slot, block id or position out of range (skipped) */
 #define KVQ_STATUS_BAD_BATCH   0x2  /* workspace_starts not non-decreasing within [0, T],
-                                       or a row before the first request (skipped)       */
-#define KVQ_STATUS_TIMEOUT     0x4  /* a bounded wait of the attention kernel (on its own
+                                       or a row before the first request, or a request's
+                                       query range not inside its bounds (skipped)       */
+#define KVQ_STATUS_TIMEOUT     0x4  /* a bounded wait of an attention kernel (on its own
                                        tensor-core work or on another of its warp roles)
                                        expired; the outputs concerned were not written  */
 
@@ -623,19 +626,24 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * (KVQ_STATUS_BAD_BATCH), as are rows of no request.
  * Entries that no query of a tile may see have no effect, whatever they hold.
  * A NaN scale byte in a visible key makes its rows NaN; in a visible value
- * group it reads as zero.  (No write of finite values stores one.)
+ * group it does so or reads as zero.  (No write of finite values stores one.)
  * Arithmetic: products on the tensor cores with fp32 sums (entries exact in
  * f16; a query row is scaled by a power of two into f16, exact down to 2^-28
  * of its largest value); the softmax in fp32; the weights rounded to f16
  * (relative 2^-11) for the weighted sum; out rounded once to bf16.
  * q: bf16 [num_tokens, num_heads, head_size] with token and head strides in
  * elements (multiples of 8); head_size 64, 128 or 256; num_heads a multiple
- * of num_kv_heads.  out: the same shape, rows not overlapping.  lse: fp32
+ * of num_kv_heads.  out: the same shape, token stride >= (num_heads - 1) *
+ * head stride + head_size; out and lse overlap no input.  lse: fp32
  * [num_tokens, num_heads], token stride lse_stride_t, or NULL.  kv_cache,
  * layout, k_scale, v_scale: as kvq_reshape_and_cache_nvfp4, and block_size *
  * num_kv_heads * full_dim a multiple of 16 below 2^31 and block_table_width *
- * block_size below 2^31 - 256.  query_start: int32 [batch_size + 1]; seq_lens: int32
- * [batch_size]; batch_size <= 65535.
+ * block_size below 2^31 - 256.  query_start: int32 [batch_size + 1], the
+ * requests' ranges disjoint; seq_lens: int32 [batch_size]; batch_size <= 65535.
+ * Calls of few query rows per request and key head run on the warps' matrix
+ * instructions and wait for nothing but their own copies; the others run on
+ * tensor memory with bounded waits, on whose expiry the rows concerned stay
+ * unwritten (KVQ_STATUS_TIMEOUT).
  * num_splits: key ranges per block of query rows (1 ..
  * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU.  With
  * workspace = NULL (at most KVQ_PER_HEAD_CLUSTER_SPLITS ranges, and
@@ -700,9 +708,8 @@ kvq_status kvq_tree_attention_nvfp4_per_head(
  * outside [0, max_accepted]) is left as it is (KVQ_STATUS_BAD_INDEX), as is
  * one with n < 0 or n > seq_lens[b] (KVQ_STATUS_BAD_BATCH).  A position whose
  * block-table column or page is out of range is skipped
- * (KVQ_STATUS_BAD_INDEX).  The drafts' positions of different requests are
- * different entries (shared pages hold no drafts); other entries are never
- * touched.  seq_lens itself is the caller's to update (base + accepted_lens).
+ * (KVQ_STATUS_BAD_INDEX).  All draft positions of a call are different
+ * entries (shared pages hold no drafts); other entries are never touched.  seq_lens itself is the caller's to update (base + accepted_lens).
  * kv_cache: num_layers caches laid out as kvq_reshape_and_cache_nvfp4's,
  * layer_stride bytes apart (a multiple of 16; ignored for one layer), all
  * addressed by the same block_table int32 [batch_size, >=
