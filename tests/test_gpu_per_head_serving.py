@@ -634,3 +634,49 @@ def test_python_calls_refuse_what_does_not_fit(kvq):
         kvq.kvq_qk_norm_rope(d["q"], d["q"], w, w, i32([0, 1]), torch.zeros(8, 128, device=DEV), 1e-6)
     out, lse = call(**d)                                    # nothing above left an error behind
     check((out, lse), b.want())
+
+
+@pytest.mark.parametrize("new,ctx", [(1, 9000), (24, 3000), (100, 5000)])
+def test_calls_at_once_and_captured_with_default_ranges(kvq, new, ctx):
+    """Two calls in flight on two streams, and a captured call that sizes its
+    ranges and allocates its workspace itself, replayed: the eager bits."""
+    bs = [Batch([(ctx, new)], 8, 2, 128, 16, "NHD", 81 + i) for i in range(2)]
+    masks = [mask_dev(random_tree([(ctx, new)], 2, b.rng)) for b in bs]
+    ds = [b.device() for b in bs]
+    for d, m in zip(ds, masks):
+        d["tree_mask"] = m
+    eager = [kvq.kvq_tree_attention_nvfp4_per_head(**d) for d in ds]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[kvq.kvq_tree_attention_nvfp4_per_head(**d, stream=s) for d, s in zip(ds, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    d = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in ds[0].items()}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = kvq.kvq_tree_attention_nvfp4_per_head(**d)
+    for i in (0, 1, 0):
+        for k, v in ds[i].items():
+            if isinstance(v, torch.Tensor):
+                d[k].copy_(v)
+        g.replay()
+        torch.cuda.synchronize()
+        got.append([tuple(t.clone() for t in captured) if j == i else eager[j] for j in range(2)])
+    for pair in got:
+        for (out, lse), want in zip(pair, eager):
+            assert torch.equal(out.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
+def test_compact_layers_apart_in_memory(kvq):
+    """Layers that are slices of a larger allocation: what lies between them stays."""
+    rng = np.random.default_rng(91)
+    cache = ref.Cache(3, 6, 16, 2, 128, "NHD", rng)
+    table = np.array([[3, 1, 5]])
+    start, lens, acc, n = [0, 9], [40], np.array([[1, 4, 6, 8]]), [4]
+    inner = cache.shape()[1:]
+    whole = torch.full((3, 6 + 2, *inner[1:]), 0xA5, dtype=torch.uint8, device=DEV)
+    view = whole[:, :6]
+    view.copy_(dev(cache.raw).view(cache.shape()))
+    kvq.kvq_compact_drafts_nvfp4_per_head(view, i32(start), i32(lens), i32(acc.tolist()), i32(n), i32(table.tolist()))
+    want = ref.compact(cache, start, lens, acc, n, table)
+    np.testing.assert_array_equal(view.reshape(want.shape).cpu().numpy(), want)
+    assert torch.all(whole[:, 6:] == 0xA5)
