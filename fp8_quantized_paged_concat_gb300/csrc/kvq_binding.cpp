@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -148,8 +148,13 @@ class Scope {
                                         : c10::cuda::getStreamFromExternal(raw_, index));
   }
   kvq_stream_t stream() const { return reinterpret_cast<kvq_stream_t>(raw_); }
-  at::Tensor result(c10::IntArrayRef shape, const at::TensorOptions& options) const {
-    at::Tensor t = at::empty(shape, options);
+  // (created here, not through the dispatcher: 1.0 against 1.3 us each)
+  at::Tensor buffer(c10::IntArrayRef shape, at::ScalarType type) const {
+    return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, device_.current_device().index()),
+                                             std::nullopt));
+  }
+  at::Tensor result(c10::IntArrayRef shape, at::ScalarType type) const {
+    at::Tensor t = buffer(shape, type);
     if (callers_) t.record_stream(*callers_);
     return t;
   }
@@ -259,8 +264,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[7]);
     if (interleaved < 0) pending();
     const Scope scope(a[11], dev);
-    const at::Tensor qo = a[8] == Py_None ? scope.result({T, H, D}, q.options()) : tensor("q_out", a[8]);
-    const at::Tensor ko = a[9] == Py_None ? scope.result({T, KH, D}, k.options()) : tensor("k_out", a[9]);
+    const at::Tensor qo = a[8] == Py_None ? scope.result({T, H, D}, at::kBFloat16) : tensor("q_out", a[8]);
+    const at::Tensor ko = a[9] == Py_None ? scope.result({T, KH, D}, at::kBFloat16) : tensor("k_out", a[9]);
     check("q_out", qo, at::kBFloat16, dev, 3);
     check("k_out", ko, at::kBFloat16, dev, 3);
     shaped("q_out", qo, {T, H, D});
@@ -303,13 +308,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t window = int32("window", a[11]), sinks = int32("num_sinks", a[12]);
     const bool tree = a[3] != Py_None;
     const Scope scope(a[19], dev);
-    const at::Tensor out = a[16] == Py_None ? scope.result({T, H, D}, q.options()) : tensor("out", a[16]);
+    const at::Tensor out = a[16] == Py_None ? scope.result({T, H, D}, at::kBFloat16) : tensor("out", a[16]);
     check("out", out, at::kBFloat16, dev, 3);
     shaped("out", out, {T, H, D});
     const bool want_lse = a[17] != Py_False;
     at::Tensor lse;
     if (want_lse) {
-      lse = a[17] == Py_None ? scope.result({T, H}, q.options().dtype(at::kFloat)) : tensor("lse", a[17]);
+      lse = a[17] == Py_None ? scope.result({T, H}, at::kFloat) : tensor("lse", a[17]);
       check("lse", lse, at::kFloat, dev, 2);
       shaped("lse", lse, {T, H});
     }
@@ -331,7 +336,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
     } else if (use_workspace && T > 0) {
       const int64_t bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
-      if (bytes > 0) workspace = at::empty({bytes}, q.options().dtype(at::kByte));
+      if (bytes > 0) workspace = scope.buffer({bytes}, at::kByte);
     }
     void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
     const int64_t ws_bytes = workspace.defined() ? workspace.numel() * static_cast<int64_t>(workspace.element_size()) : 0;
