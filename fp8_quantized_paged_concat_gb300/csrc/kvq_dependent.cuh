@@ -1,0 +1,43 @@
+// kvq_dependent.cuh -- dependent launches: a kernel that is set up while the
+// one before it in the stream still runs.
+//
+// Every thread of such a kernel calls wait_for_previous() before its first
+// access to memory (tensor memory among it, which a CTA before it may still
+// have to take), on every path: so a kernel ends after the one before it, and
+// what a stream orders stays ordered along a chain of them.  Measured, calls
+// queued: a single-token attention 10.2 -> 7.5 us, a compaction of one layer
+// 4.1 -> 3.1, of 32 layers 16.4 -> 13.9, a tree of one user 20.5 -> 19.0.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace kvq {
+namespace {
+
+// The next kernel of the stream may be set up once every CTA has said so or left.
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Returns when the kernels before are complete and their writes visible.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches kernel(args...) as a dependent one; cluster > 1: in clusters of that many CTAs (along x).
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,
+                             cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  config.attrs = at;
+  config.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace
+}  // namespace kvq

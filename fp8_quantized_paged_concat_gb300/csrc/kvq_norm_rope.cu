@@ -17,8 +17,9 @@
 // signs are folded once per group into two factors per dimension, so that a
 // value costs two multiplications and one fused multiply-add.  A pair's other
 // half, when it is rot/2 away, sits rot/16 lanes on: its raw bf16 values come
-// by four shuffles.  16384 tokens x (32 + 8) heads of 128: 59 us, 5.9 TB/s
+// by four shuffles.  16384 tokens x (32 + 8) heads of 128: 57 us, 6.1 TB/s
 // (normalised fp32 values with unfused factors: 74 us).
+#include "kvq_dependent.cuh"
 #include "kvq_device.cuh"
 #include "kvq_launch.h"
 
@@ -42,6 +43,8 @@ __device__ __forceinline__ Values unpack8(const uint4& w) {
 template <int kLanes, int kHeads, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_kernel(const NormRopeArgs a, FastDiv chunk_div,
                                                                    int q_chunks) {
+  wait_for_previous();
+  allow_dependents();
   const uint32_t group = static_cast<uint32_t>((static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes);
   const int li = threadIdx.x % kLanes;
   // group -> (token, chunk of kHeads heads): the query side's chunks, then the key side's
@@ -149,17 +152,14 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
   const uint64_t threads = static_cast<uint64_t>(a.num_tokens) * chunks * kLanes;
   const unsigned blocks = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
   const FastDiv div = FastDiv::make(static_cast<uint32_t>(chunks));
-  if (a.interleaved)
-    qk_norm_rope_kernel<kLanes, kHeads, true><<<blocks, kThreads, 0, stream>>>(a, div, q_chunks);
-  else
-    qk_norm_rope_kernel<kLanes, kHeads, false><<<blocks, kThreads, 0, stream>>>(a, div, q_chunks);
-  return cudaGetLastError();
+  return launch_dependent(a.interleaved ? qk_norm_rope_kernel<kLanes, kHeads, true> : qk_norm_rope_kernel<kLanes, kHeads, false>,
+                          dim3(blocks), kThreads, 0, 1, stream, a, div, q_chunks);
 }
 
 template <int kLanes>
 cudaError_t launch_heads(const NormRopeArgs& a, int num_sms, cudaStream_t stream) {
   // Eight heads per lane group share one table row and one set of weights and
-  // keep eight loads in flight (head size 128, 32 + 8 heads: 16384 tokens 59
+  // keep eight loads in flight (head size 128, 32 + 8 heads: 16384 tokens 57
   // us, with four heads 70, two 85, one 115); a call that gives the SMs less
   // than one CTA each that way takes one head per group (64 tokens: 6.8
   // against 8.8 us; at 256 tokens the two are equal).

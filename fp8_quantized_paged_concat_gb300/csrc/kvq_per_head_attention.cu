@@ -17,9 +17,9 @@
 // key head.  Each warp takes every fourth step of 32 keys, with its own
 // running maximum and sum, and the warps join at the end through shared
 // memory; the ranges of a small call run as a cluster and join through its
-// distributed shared memory (one request, window of 1024, 64 heads: 10.2 us
-// with its launch; with a second launch 14.0), others in a second launch,
-// under way before the first ends.  A warp copies a step's raw bytes
+// distributed shared memory (one request, window of 1024, 64 heads: 7.5 us;
+// a second launch costs about 4 more), others in a second launch.  A warp
+// copies a step's raw bytes
 // (32 entries of 9 D / 16 bytes, K and V) into its own two-stage ring with
 // asynchronous copies, a step ahead, so that nothing but the warp's own
 // copies is ever waited for.
@@ -43,7 +43,7 @@
 // maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
 //
 // Measured: 128 requests x 4100 keys x 32 heads (8 key heads) of 128, 606 MB:
-// 117 us, 5.2 TB/s; about 640 warp instructions per step of 32 keys for 4
+// 115 us, 5.3 TB/s; about 640 warp instructions per step of 32 keys for 4
 // rows, and their issue, not the copies, sets the pace (3 stages or 5 CTAs an
 // SM are slower: registers).
 #include <algorithm>
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   constexpr int kRows = 8 * kRowTiles;
   constexpr int kKSteps = D / 16;                // 16-dimension steps of K Q^T
   constexpr int kDimTiles = D / 16;              // 16-dimension tiles of V^T P^T
+  wait_for_previous();
   const Place place = place_of(a, row_blocks);
   const uint32_t head = place.head;
   const int32_t rb = place.row_block, split = place.split;
@@ -670,24 +671,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const
   if (lane == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
 }
 
-// Launches `kernel`, the ranges of a block as a cluster where they are joined in one.
-template <class Kernel>
-cudaError_t launch_ranges(Kernel kernel, const PerHeadAttentionArgs& a, dim3 grid, int threads, int smem,
-                          int32_t row_blocks, cudaStream_t stream) {
-  cudaLaunchConfig_t config = {};
-  config.gridDim = grid;
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = stream;
-  cudaLaunchAttribute cluster = {};
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = a.num_splits;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  config.attrs = &cluster;
-  config.numAttrs = a.cluster ? 1 : 0;
-  return cudaLaunchKernelEx(&config, kernel, a, row_blocks);
-}
-
 template <int D, int kRowTiles>
 cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   constexpr int kSmem = kWarps * kStages * Stage<D>::kBytes;
@@ -698,24 +681,15 @@ cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
   const int64_t blocks = (rows + 8 * kRowTiles - 1) / (8 * kRowTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  return launch_ranges(per_head_attention_kernel<D, kRowTiles>, a, grid, kThreads, kSmem, static_cast<int32_t>(blocks),
-                       stream);
+  return launch_dependent(per_head_attention_kernel<D, kRowTiles>, grid, kThreads, kSmem, a.cluster ? a.num_splits : 1,
+                          stream, a, static_cast<int32_t>(blocks));
 }
 
 template <int D>
 cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
-  // a dependent launch: it is under way while the ranges still run
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
-  config.blockDim = dim3(kJoinWarps * 32);
-  config.stream = stream;
-  cudaLaunchAttribute dependent = {};
-  dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  dependent.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &dependent;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, per_head_join_kernel<D>, a);
+  const dim3 grid(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
+  return launch_dependent(per_head_join_kernel<D>, grid, kJoinWarps * 32, 0, 1, stream, a);
 }
 
 // CTAs of the few-row kernel that share an SM (its launch bounds).

@@ -3,6 +3,7 @@
 // sees, and the decoding of e2m1 codes.
 #pragma once
 
+#include "kvq_dependent.cuh"
 #include "kvq_device.cuh"
 #include "kvq_launch.h"
 #include "kvq_tcgen05.cuh"
@@ -36,11 +37,6 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
-
-// Dependent launches: the next kernel of the stream may be launched once every
-// CTA has said so or left, and waits, before it reads, for this one's end.
-__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Asynchronous copies into shared memory; `bytes` = kBytes, or 0: zero-filled,
 // nothing read.

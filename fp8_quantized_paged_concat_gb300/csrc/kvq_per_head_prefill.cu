@@ -310,6 +310,7 @@ template <int D, int kTiles>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
   using S = Shape<D, kTiles>;
+  wait_for_previous();
   // the last row blocks of a causal chunk, which see the most keys, come first
   const Place place = place_of(a, row_blocks);
   const uint32_t head = place.head;
@@ -716,8 +717,8 @@ cudaError_t launch(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (static_cast<int64_t>(a.max_query_len) * a.group + 128 * kTiles - 1) / (128 * kTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  per_head_prefill_kernel<D, kTiles><<<grid, S::kThreads, S::kSmem, stream>>>(a, static_cast<int32_t>(blocks));
-  return cudaGetLastError();
+  return launch_dependent(per_head_prefill_kernel<D, kTiles>, grid, S::kThreads, S::kSmem, 1, stream, a,
+                          static_cast<int32_t>(blocks));
 }
 
 }  // namespace

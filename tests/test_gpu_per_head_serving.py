@@ -680,3 +680,45 @@ def test_compact_layers_apart_in_memory(kvq):
     want = ref.compact(cache, start, lens, acc, n, table)
     np.testing.assert_array_equal(view.reshape(want.shape).cpu().numpy(), want)
     assert torch.all(whole[:, 6:] == 0xA5)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_a_chain_of_calls_runs_in_order(kvq, new):
+    """Each call reads what the one before it wrote (queries, cache entries,
+    the in-place rotation): queued and captured, the bits of a run that waits
+    after every call."""
+    b = Batch([(700, new), (90, new), (33, new)], 8, 2, 128, 16, "NHD", 95)
+    d = b.device()
+    T = b.start[-1]
+    w = bf16_dev(ref.to_bf16(1 + 0.1 * b.rng.standard_normal(128)))
+    table = dev(b.rng.standard_normal((800, 128)).astype(np.float32))
+    pos = dev(b.rng.integers(0, 800, T))
+    accepted, count = i32([[new - 1]] * 3), i32([1] * 3)
+    kept = {k: d[k].clone() for k in ("q", "kv_cache")}
+
+    def chain(wait):
+        q, cache = kept["q"].clone(), kept["kv_cache"].clone()
+        k = q[:, :2].clone()
+        out = []
+        for _ in range(12):
+            kvq.kvq_qk_norm_rope(q, k, w, w, pos, table, 1e-6, q_out=q, k_out=k)
+            wait()
+            kvq.kvq_compact_drafts_nvfp4_per_head(cache, d["query_start"], d["seq_lens"], accepted, count, d["block_table"])
+            wait()
+            o, lse = kvq.kvq_window_attention_nvfp4_per_head(**{**d, "q": q, "kv_cache": cache})
+            wait()
+            q, k = o, o[:, 2:4].clone()
+            wait()
+            out += [o.clone(), lse]
+        return out + [cache]
+
+    want = chain(torch.cuda.synchronize)
+    got = [chain(lambda: None)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = chain(lambda: None)
+    g.replay()
+    torch.cuda.synchronize()
+    for run in (*got, captured):
+        for a, c in zip(run, want):
+            assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
