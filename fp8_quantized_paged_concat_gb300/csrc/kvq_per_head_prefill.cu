@@ -230,13 +230,12 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   const uint32_t own_row = 8 * (me + kWarps * (lane >> 3)) + (lane & 7);   // of the warp's rows, the one it looks up
   const bool has_row = own_row < S::kChunk && (lane >> 3) < kPasses;
   const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
-  LookUp next;                                      // its position in the next chunk to be copied
-  auto look_up = [&](int32_t h) {
+  auto look_up = [&](int32_t h) {                   // its position in chunk h
     const int32_t step = s0 + h / S::kParts;
     const uint32_t p = static_cast<uint32_t>(keys.base(step)) + (h % S::kParts) * S::kChunk + own_row;
-    next = look_up_position(a, table, head_row, has_row && h < chunks && p < static_cast<uint32_t>(keys.limit(step)), p);
+    return look_up_position(a, table, head_row, has_row && h < chunks && p < static_cast<uint32_t>(keys.limit(step)), p);
   };
-  auto start = [&](int32_t h) {                     // one group of copies, empty past the last chunk
+  auto start = [&](int32_t h, const LookUp& next) { // one group of copies, empty past the last chunk
     if (h < chunks) {
       const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
       const bool ok = next.in && next.id >= 0 && next.id < a.num_pages;
@@ -272,11 +271,21 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     }
     cp_commit();
   };
-  look_up(0);
+  LookUp next;
+  if constexpr (kTiles == 1) {
+    LookUp first[S::kRing - 1];                     // all under way before the first is looked at
 #pragma unroll
-  for (int h = 0; h < S::kRing - 1; ++h) {
-    start(h);
-    look_up(h + 1);
+    for (int h = 0; h < S::kRing - 1; ++h) first[h] = look_up(h);
+    next = look_up(S::kRing - 1);
+#pragma unroll
+    for (int h = 0; h < S::kRing - 1; ++h) start(h, first[h]);
+  } else {
+    next = look_up(0);
+#pragma unroll
+    for (int h = 0; h < S::kRing - 1; ++h) {
+      start(h, next);
+      next = look_up(h + 1);
+    }
   }
   set_up_done();
   for (int32_t h = 0; h < chunks; ++h) {
@@ -284,8 +293,8 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     const int st = t % S::kStages;
     cp_wait<S::kRing - 2>();
     __syncwarp();                                   // chunk h is there, and chunk h - 1 has been read
-    start(h + S::kRing - 1);
-    look_up(h + S::kRing);
+    start(h + S::kRing - 1, next);
+    next = look_up(h + S::kRing);
     const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
     Piece<D> e[kPasses];                            // all read first, so that their latencies overlap
 #pragma unroll
@@ -311,6 +320,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
   using S = Shape<D, kTiles>;
   wait_for_previous();
+  const float k_scale = __ldg(a.k_scale);           // in flight beside the request
   // the last row blocks of a causal chunk, which see the most keys, come first
   const Place place = place_of(a, row_blocks);
   const uint32_t head = place.head;
@@ -379,10 +389,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
-  // Softmax threads: their query row, and the loads of the warp's 32 rows, D /
-  // 8 lanes to a row (16 bytes each), with a single row tile a batch of them in
-  // flight while the CTA sets up (two have no registers to spare for it).
-  // Rows past the block's are zero.
+  // Softmax threads: their query row.  Rows past the block's are zero.
   const int32_t row = static_cast<int32_t>(threadIdx.x);
   bool has_row = false;
   int64_t token = 0;
@@ -401,59 +408,55 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     src = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride_t +
                                      q_head * a.q_stride_h);
   };
-  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;
-  constexpr int kBatch = kTiles == 2 || kRounds < 16 ? 8 : 16;
-  uint4 x[kBatch];
-  auto load_rows = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int from = (r0 + i) * kAtOnce + lane / kLanes;
-      const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(src >> 32), from)) << 32 |
-                          __shfl_sync(kFull, static_cast<uint32_t>(src), from);
-      x[i] = at != 0 ? __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
-    }
-  };
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
-    if (kTiles == 1) {
-      set_row();
-      load_rows(0);
+    const int tile = warp >> 2;                     // its row tile
+    set_row();
+    // The warp's 32 query rows come in as they are, D / 8 lanes to a row,
+    // while the CTA sets up; then each thread scales its own in place.  (Short
+    // loops: a CTA runs this code once, and fetching it took longer than the
+    // loads, 2.1 us with the rows in registers.)
+    const uint32_t q_rows = base + tile * S::kQTile + (warp & 3) * (32 * 128);
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += kAtOnce) {
+      const int from = i + lane / kLanes, c = lane % kLanes;
+      const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(src >> 32), from)) << 32 |
+                          __shfl_sync(kFull, static_cast<uint32_t>(src), from);
+      cp_async<16>(q_rows + (c >> 3) * kBlockBytes + sw128_offset(from, c & 7),
+                   reinterpret_cast<const uint4*>(at != 0 ? at : reinterpret_cast<uint64_t>(a.q)) + (at != 0 ? c : 0),
+                   at != 0 ? 16 : 0);
     }
+    cp_commit();
     set_up_done();
     more_registers<S::kSoftmaxRegs>();
     const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
-    const int tile = warp >> 2;                     // its row tile
-    if (kTiles == 2) set_row();
-    // the warp's 32 query rows -> shared memory
-    float amax = 0.0f;                              // of the thread's own row
-#pragma unroll 1
-    for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
-      if (kTiles == 2 || r0 > 0) load_rows(r0);
+    cp_wait<0>();
+    __syncwarp();
+    float amax = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = ld_shared16(q_rows + (c >> 3) * kBlockBytes + sw128_offset(lane, c & 7));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float top = 0.0f;
+      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+    }
+    const RowScale rs = row_scale(amax);
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint32_t at = q_rows + (c >> 3) * kBlockBytes + sw128_offset(lane, c & 7);
+      const uint4 x = ld_shared16(at);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const float own = __shfl_sync(kFull, top, (lane % kAtOnce) * kLanes);
-        if (lane / kAtOnce == r0 + i) amax = own;
-        const RowScale rs = row_scale(top);
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[j] = pack_f16x2(bf16_lo(w[j]) * rs.f[0] * rs.f[1], bf16_hi(w[j]) * rs.f[0] * rs.f[1]);
-        const uint32_t r = (warp & 3) * 32 + (r0 + i) * kAtOnce + lane / kLanes, c = lane % kLanes;
-        st_shared16(base + tile * S::kQTile + (c >> 3) * kBlockBytes + sw128_offset(r, c & 7),
-                    make_uint4(h[0], h[1], h[2], h[3]));
-      }
+      for (int j = 0; j < 4; ++j)
+        h[j] = pack_f16x2(bf16_lo(w[j]) * rs.f[0] * rs.f[1], bf16_hi(w[j]) * rs.f[0] * rs.f[1]);
+      st_shared16(at, make_uint4(h[0], h[1], h[2], h[3]));
     }
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
-    const RowScale rs = row_scale(amax);
-    const float sc = a.scale_log2 * __ldg(a.k_scale) * rs.i[0] * rs.i[1];   // score -> base-2 exponent
+    const float sc = a.scale_log2 * k_scale * rs.i[0] * rs.i[1];   // score -> base-2 exponent
 
     float m = has_row ? -INFINITY : 0.0f, l = 0.0f; // reference maximum, sum
     bool done = true;                               // every wait was met
@@ -572,43 +575,77 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
+    const float v_scale = __ldg(a.v_scale);
     // the last product is done: O is complete
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
     fence_after_sync();
-    const bool live = row < rows && done;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kShift);
     const int64_t part = (token * a.num_heads + q_head) * a.num_splits + split;
-    const float f = a.num_splits > 1 ? inv : inv * __ldg(a.v_scale);
+    if (done) {                                     // uniform over the warp
+      // The rows leave in pieces of 128 bytes (32 fp32 or 64 bf16), eight lanes
+      // to a piece, through the shared memory of the warp's query rows, which
+      // no product reads any more (each lane storing its own row touches 32
+      // lines at a time: 2.2 us a CTA).
+      const float f = a.num_splits > 1 ? inv : inv * v_scale;
+      const uint32_t stage = bar - S::kMisc + tile * S::kQTile + (lanes >> 9);     // 32 rows of 128 bytes a warp
+      const uint64_t mine =
+          row >= rows ? 0
+          : a.num_splits > 1
+              ? reinterpret_cast<uint64_t>(a.part_o + part * D)
+              : reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t + q_head * a.out_stride_h);
+      uint64_t to[8];                               // of rows 4 i + lane / 8
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int from = 4 * i + (lane >> 3);
+        to[i] = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(mine >> 32), from)) << 32 |
+                __shfl_sync(kFull, static_cast<uint32_t>(mine), from);
+      }
+      auto columns = [&](int c, float (&o)[32]) {
+        if (n_tiles > 0) {
+          tmem_ld32(o_col + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= f;
+      };
+      const int pieces = a.num_splits > 1 ? D / 32 : D / 64;
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      if (n_tiles > 0 && done) {                    // uniform over the warp
-        tmem_ld32(o_col + 32 * c, o);
-      } else {
+      for (int c = 0; c < pieces; ++c) {
+        float o[32];
+        if (a.num_splits > 1) {
+          columns(32 * c, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          for (int j = 0; j < 8; ++j)
+            st_shared16(stage + sw128_offset(lane, j),
+                        make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                                   __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3])));
+        } else {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            columns(64 * c + 32 * half, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared16(stage + sw128_offset(lane, 4 * half + j),
+                          make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                     pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = ld_shared16(stage + sw128_offset(4 * i + (lane >> 3), lane & 7));
+          if (to[i] != 0) st16(reinterpret_cast<uint8_t*>(to[i]) + 128 * c + 16 * (lane & 7), v);
+        }
+        __syncwarp();                               // read before the next piece, whose load is the whole warp's
       }
-      if (live && a.num_splits > 1) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-      } else if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
-                                              q_head * a.out_stride_h + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                              pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
-                              pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
-      }
-      __syncwarp();                                 // the next load is the whole warp's
     }
     if (a.num_splits > 1) {
       if (row < rows) a.part_lse[part] = done ? lse2 : __uint_as_float(kAbandoned);
-    } else if (live && a.lse != nullptr) {
+    } else if (row < rows && done && a.lse != nullptr) {
       a.lse[token * a.lse_stride_t + q_head] = lse2 * kLn2;
     }
   } else {
