@@ -433,25 +433,41 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
     cp_wait<0>();
     __syncwarp();
-    float amax = 0.0f;
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 x = ld_shared16(q_rows + (c >> 3) * kBlockBytes + sw128_offset(lane, c & 7));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    // (eight pieces at a time: the decoding warps' copies keep a load waiting
+    // for a hundred clocks)
+    uint32_t top = 0;                               // largest bits below the signs, of either half
+#pragma unroll 1
+    for (int c = 0; c < D / 8; c += 8) {
+      const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
+      uint4 x[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+      for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        top = __vimax3_u16x2(top, x[i].x & kAbs, x[i].y & kAbs);
+        top = __vimax3_u16x2(top, x[i].z & kAbs, x[i].w & kAbs);
+      }
     }
-    const RowScale rs = row_scale(amax);
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      const uint32_t at = q_rows + (c >> 3) * kBlockBytes + sw128_offset(lane, c & 7);
-      const uint4 x = ld_shared16(at);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t h[4];
+    const RowScale rs = row_scale(__uint_as_float(max(top << 16, top & 0xFFFF0000u)));
+#pragma unroll 1
+    for (int c = 0; c < D / 8; c += 8) {
+      const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
+      uint4 x[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        h[j] = pack_f16x2(bf16_lo(w[j]) * rs.f[0] * rs.f[1], bf16_hi(w[j]) * rs.f[0] * rs.f[1]);
-      st_shared16(at, make_uint4(h[0], h[1], h[2], h[3]));
+      for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = fmul2(fmul2(make_float2(bf16_lo(w[j]), bf16_hi(w[j])), make_float2(rs.f[0], rs.f[0])),
+                                 make_float2(rs.f[1], rs.f[1]));
+          h[j] = pack_f16x2(v.x, v.y);
+        }
+        st_shared16(at + sw128_offset(lane, i), make_uint4(h[0], h[1], h[2], h[3]));
+      }
     }
     fence_async_smem();
     __syncwarp();
