@@ -125,8 +125,8 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, const Request& rq, uint32_t kv_head,
                                              int64_t row0, int32_t rows, int32_t rank, int32_t dims, uint32_t o,
                                              uint32_t stride, uint32_t m, uint32_t l) {
-  cluster_sync();
   const float v_scale = __ldg(a.v_scale);
+  cluster_sync();
   const int32_t chunks = dims / 8;
   // (distributed shared memory gives an SM about 14 bytes a clock: the shares are equal)
   for (int32_t i = rank + threadIdx.x * a.num_splits; i < rows * chunks; i += a.num_splits * blockDim.x) {
@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
 
   // ---- join the four warps -------------------------------------------------
+  const float v_scale = __ldg(a.v_scale);        // under way meanwhile
   cp_wait<0>();
   __syncthreads();                               // every ring is idle
   float* jo = reinterpret_cast<float*>(smem);    // [kWarps][kRows][D]
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
       if (d == 0) a.part_lse[pr] = lse2;
     } else {
-      const float f = inv * __ldg(a.v_scale);
+      const float f = inv * v_scale;
       st16(static_cast<__nv_bfloat16*>(a.out) + at.token * a.out_stride_t + at.head * a.out_stride_h + d,
            make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
                       pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f)));
@@ -602,32 +603,49 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 // Joins the ranges of every row: with L_s the base-2 log-sum-exp of range s
 // and o_s its normalised output, out = sum 2^(L_s - M) o_s / sum 2^(L_s - M).
 // One warp per (token, head) row of a live request; a range that saw nothing
-// (-inf) weighs nothing.
+// (-inf) weighs nothing.  Latency bounds it, so the chain is short: the call's
+// own arrays are read before the ranges are waited for (what wrote them was
+// complete when their kernel started), and the first ranges' rows are loaded
+// beside their L_s, not after.
 constexpr int kJoinWarps = 4;
 
-template <int D>
+template <int D, int kBatch>                             // kBatch: ranges in flight
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const PerHeadAttentionArgs a) {
-  wait_for_previous();
   const int64_t flat = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   Request rq;
-  if (!request_of(a, b, rq) || flat >= static_cast<int64_t>(rq.tokens) * a.num_heads) return;
-  const int64_t row = rq.token0 * a.num_heads + flat;
+  const bool live = request_of(a, b, rq) && flat < static_cast<int64_t>(rq.tokens) * a.num_heads;
+  const float v_scale = __ldg(a.v_scale);
+  const int64_t row = live ? rq.token0 * a.num_heads + flat : 0;
   const float* ls = a.part_lse + row * a.num_splits;
+  constexpr int kDims = D / 32;                          // per lane
+  const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
+  wait_for_previous();
+  if (!live) return;
+  float2 v[kBatch][kDims / 2];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int i = 0; i < kDims / 2; ++i)
+        v[k][i] = s0 + k < a.num_splits ? *reinterpret_cast<const float2*>(po + static_cast<int64_t>(s0 + k) * D + 2 * i)
+                                        : make_float2(0.0f, 0.0f);
+  };
   // lane l holds ranges l, l + 32, ...
   constexpr int kPer = KVQ_PER_HEAD_MAX_SPLITS / 32;
   float own[kPer], top = -INFINITY;
   bool abandoned = false;
 #pragma unroll
+  for (int j = 0; j < kPer; ++j) own[j] = 32 * j + lane < a.num_splits ? ls[32 * j + lane] : -INFINITY;
+  load(0);
+#pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    own[j] = 32 * j + lane < a.num_splits ? ls[32 * j + lane] : -INFINITY;
     top = fmaxf(top, own[j]);
     abandoned |= __float_as_uint(own[j]) == kAbandoned;
   }
   if (__any_sync(kFull, abandoned)) return;              // a range whose CTA gave up: the row stays unwritten
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  constexpr int kDims = D / 32;                          // per lane
   float acc[kDims], den = 0.0f;
 #pragma unroll
   for (int i = 0; i < kDims; ++i) acc[i] = 0.0f;
@@ -638,31 +656,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
-  const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
-  // eight ranges' rows in flight (those of an empty range were never written, and are not read)
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    for (int s0 = 0; s0 < 32 && 32 * j + s0 < a.num_splits; s0 += 8) {
-      float w[8];
-      float2 v[8][kDims / 2];
+    for (int s0 = 0; s0 < 32 && 32 * j + s0 < a.num_splits; s0 += kBatch) {
+      if (j + s0 > 0) load(32 * j + s0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        w[k] = __shfl_sync(kFull, own[j], s0 + k);
-#pragma unroll
-        for (int i = 0; i < kDims / 2; ++i)
-          v[k][i] = w[k] == 0.0f ? make_float2(0.0f, 0.0f)
-                                 : *reinterpret_cast<const float2*>(po + static_cast<int64_t>(32 * j + s0 + k) * D + 2 * i);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = __shfl_sync(kFull, own[j], s0 + k);
+        // the row of an empty range was never written: what was loaded is not used
 #pragma unroll
         for (int i = 0; i < kDims / 2; ++i) {
-          acc[2 * i] += w[k] * v[k][i].x;
-          acc[2 * i + 1] += w[k] * v[k][i].y;
+          acc[2 * i] += w == 0.0f ? 0.0f : w * v[k][i].x;
+          acc[2 * i + 1] += w == 0.0f ? 0.0f : w * v[k][i].y;
         }
+      }
     }
   }
-  const float f = (den == 0.0f ? 0.0f : 1.0f / den) * __ldg(a.v_scale);
+  const float f = (den == 0.0f ? 0.0f : 1.0f / den) * v_scale;
   const int64_t token = row / a.num_heads, h = row - token * a.num_heads;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
                                               h * a.out_stride_h + kDims * lane);
@@ -689,7 +699,11 @@ template <int D>
 cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
   const dim3 grid(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
-  return launch_dependent(per_head_join_kernel<D>, grid, kJoinWarps * 32, 0, 1, stream, a);
+  // as many ranges in flight as a row has, up to 16 (one user's tree in 19
+  // ranges: 16.3 us, eight in flight 17.4), but no more: they cost registers,
+  // and calls of few ranges have many rows (trees 32 x 64 in 4: 574 us, 595)
+  return launch_dependent(a.num_splits <= 4 ? per_head_join_kernel<D, 4> : per_head_join_kernel<D, D == 256 ? 8 : 16>, grid,
+                          kJoinWarps * 32, 0, 1, stream, a);
 }
 
 // CTAs of the few-row kernel that share an SM (its launch bounds).

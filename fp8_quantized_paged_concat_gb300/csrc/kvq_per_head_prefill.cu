@@ -651,11 +651,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           }
         }
         __syncwarp();
+        uint4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = ld_shared16(stage + sw128_offset(4 * i + (lane >> 3), lane & 7));
-          if (to[i] != 0) st16(reinterpret_cast<uint8_t*>(to[i]) + 128 * c + 16 * (lane & 7), v);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = ld_shared16(stage + sw128_offset(4 * i + (lane >> 3), lane & 7));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (to[i] != 0) st16(reinterpret_cast<uint8_t*>(to[i]) + 128 * c + 16 * (lane & 7), v[i]);
         __syncwarp();                               // read before the next piece, whose load is the whole warp's
       }
     }
