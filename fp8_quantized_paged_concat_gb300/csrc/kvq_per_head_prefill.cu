@@ -18,7 +18,7 @@
 //     V tiles (64 x D f16, 128-byte swizzle, kStages of each), and a ring of
 //     raw entries per side;
 //   - some warps decode the keys and as many the values: raw entries come in by
-//     asynchronous copies, kRing - 1 chunks ahead (each warp copies what it
+//     asynchronous copies, kRing chunks ahead (each warp copies what it
 //     decodes, so that it waits for no other); 8 lanes take 8 rows of a
 //     64-column block, so that their 16-byte stores fall in different banks;
 //   - one warp issues the scores' products S_w(t) = Q_w K(t)^T, another the
@@ -262,7 +262,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
           cp_async<kPiece>(raw + at.raw[j] + i * kWarps * 8 * (D / 2), src + 16 * j, there ? kPiece : 0);
       }
       // Which keys exist, for the softmax; a slot's last reader is long done
-      // (kRing - 1 chunks ahead of a tile whose buffers are free).
+      // (kRing chunks ahead of a tile whose buffers are free).
       if constexpr (!kValues) {
         if (lane < kPasses && me + kWarps * lane < kGroups)
           valid_ring[8 * ((h / S::kParts) % kValidRing) + (h % S::kParts) * kGroups + me + kWarps * lane] =
@@ -273,43 +273,45 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   };
   LookUp next;
   if constexpr (kTiles == 1) {
-    LookUp first[S::kRing - 1];                     // all under way before the first is looked at
+    LookUp first[S::kRing];                         // all under way before the first is looked at
 #pragma unroll
-    for (int h = 0; h < S::kRing - 1; ++h) first[h] = look_up(h);
-    next = look_up(S::kRing - 1);
+    for (int h = 0; h < S::kRing; ++h) first[h] = look_up(h);
+    next = look_up(S::kRing);
 #pragma unroll
-    for (int h = 0; h < S::kRing - 1; ++h) start(h, first[h]);
+    for (int h = 0; h < S::kRing; ++h) start(h, first[h]);
   } else {
     next = look_up(0);
 #pragma unroll
-    for (int h = 0; h < S::kRing - 1; ++h) {
+    for (int h = 0; h < S::kRing; ++h) {
       start(h, next);
       next = look_up(h + 1);
     }
   }
   set_up_done();
-  for (int32_t h = 0; h < chunks; ++h) {
-    const int32_t t = h / S::kParts;
-    const int st = t % S::kStages;
-    cp_wait<S::kRing - 2>();
-    __syncwarp();                                   // chunk h is there, and chunk h - 1 has been read
-    start(h + S::kRing - 1, next);
-    next = look_up(h + S::kRing);
+  Piece<D> e[kPasses];                              // of the next chunk: read a chunk ahead, all at once
+  auto read = [&](int32_t h) {
+    cp_wait<S::kRing - 1>();
+    __syncwarp();                                   // chunk h is there
     const uint32_t raw = raw_ring + (h % S::kRing) * S::kRawBytes;
-    Piece<D> e[kPasses];                            // all read first, so that their latencies overlap
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (me + kWarps * i < kGroups) load_piece<D>(raw, at, i * kWarps, e[i]);
+  };
+  read(0);
+  for (int32_t h = 0; h < chunks; ++h) {
+    const int32_t t = h / S::kParts;
+    const int st = t % S::kStages;
     if (h % S::kParts == 0 && t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       if (me + kWarps * i < kGroups)
         store_piece<D, kValues>(tiles + st * S::kTileBytes + (h % S::kParts) * S::kChunk * 128, at, i * kWarps, e[i]);
-    if (h % S::kParts == S::kParts - 1) {
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + 8 * st);
-    }
+    if (h % S::kParts == S::kParts - 1) fence_async_smem();
+    __syncwarp();                                   // and chunk h has been read
+    if (h % S::kParts == S::kParts - 1 && lane == 0) mbar_arrive(full + 8 * st);
+    start(h + S::kRing, next);
+    next = look_up(h + S::kRing + 1);
+    read(h + 1);
   }
   cp_wait<0>();                                     // no copy outlives the CTA
   if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
