@@ -217,6 +217,12 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F body) {
     return body();
   } catch (const BadArgument& e) {
     if (e.type != nullptr) PyErr_SetString(e.type, e.text.c_str());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch != nullptr ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type != nullptr) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

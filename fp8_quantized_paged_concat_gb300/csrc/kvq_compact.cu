@@ -31,7 +31,7 @@ constexpr int kLayers = 4;                   // layers in flight
 // Page in column `col` of request b's table, or -1.
 __device__ __forceinline__ int64_t page_of(const CompactArgs& a, int b, uint32_t col) {
   if (col >= static_cast<uint32_t>(a.block_table_width)) return -1;
-  const int32_t id = __ldg(a.block_table + b * a.block_table_stride + col);
+  const int32_t id = load_global(a.block_table + b * a.block_table_stride + col);
   return id >= 0 && id < a.num_pages ? id : -1;
 }
 
@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactA
   const int head0 = static_cast<int>(blockIdx.y >> 1) * heads;
   const int layer0 = blockIdx.z * layers_per_cta, layer1 = min(a.num_layers, layer0 + layers_per_cta);
   const bool first = blockIdx.y == 0 && blockIdx.z == 0;
-  const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
-  const int64_t n = static_cast<int64_t>(q1) - q0, len = __ldg(a.seq_lens + b);
-  const int32_t m = __ldg(a.accepted_lens + b);
+  const int32_t q0 = load_global(a.query_start + b), q1 = load_global(a.query_start + b + 1);
+  const int64_t n = static_cast<int64_t>(q1) - q0, len = load_global(a.seq_lens + b);
+  const int32_t m = load_global(a.accepted_lens + b);
   if (m == 0) return;
   if (n < 0 || len < n) {                                  // uniform over the CTA
     if (first && threadIdx.x == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactA
   bool bad = m < 0 || m > a.max_accepted;
   if (!bad) {
     for (int i = threadIdx.x; i < m; i += kThreads) {
-      const int32_t x = __ldg(acc + i);
-      if (x < 0 || x >= n || (i > 0 && x <= __ldg(acc + i - 1))) bad = true;
+      const int32_t x = load_global(acc + i);
+      if (x < 0 || x >= n || (i > 0 && x <= load_global(acc + i - 1))) bad = true;
     }
   }
   if (__syncthreads_or(bad)) {                             // a malformed list: the request is left as it is
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) compact_drafts_kernel(const CompactA
       if (u >= units) continue;
       const int i = i0 + u / move_units, in_move = u % move_units;
       const int head = head0 + in_move / row_units, w = in_move % row_units;
-      const uint32_t from_p = base + static_cast<uint32_t>(__ldg(acc + i)), to_p = base + i;   // below seq_lens[b]
+      const uint32_t from_p = base + static_cast<uint32_t>(load_global(acc + i)), to_p = base + i;   // below seq_lens[b]
       if (from_p == to_p) continue;
       const uint32_t from_col = a.block_div.div(from_p), to_col = a.block_div.div(to_p);
       const int64_t from_page = page_of(a, b, from_col), to_page = page_of(a, b, to_col);

@@ -19,6 +19,14 @@ __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontro
 // Returns when the kernels before are complete and their writes visible.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A load of what a kernel before may have written.  A plain one: the compiler
+// may move a load through the read-only path (__ldg) up past the wait, and
+// that path promises nothing for data written while the kernel is resident.
+template <class T>
+__device__ __forceinline__ T load_global(const T* p) {
+  return *p;
+}
+
 // Launches kernel(args...) as a dependent one; cluster > 1: in clusters of that many CTAs (along x).
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster,

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_kernel(const NormRop
   for (int j = 0; j < kHeads; ++j)
     raw[j] = live_lane && j < heads ? *reinterpret_cast<const uint4*>(in + j * in_h) : make_uint4(0, 0, 0, 0);
 
-  const int64_t pos = live_token ? __ldg(a.positions + token) : 0;
+  const int64_t pos = live_token ? load_global(a.positions + token) : 0;
   const bool bad = live_token && (pos < 0 || pos >= a.max_position);
   if (bad && li == 0 && chunk == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
   const bool live = live_lane && !bad;
@@ -80,12 +80,12 @@ __global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_kernel(const NormRop
   Values own{}, other{};
   if (live) {
     const uint4* w = static_cast<const uint4*>(is_q ? a.q_weight : a.k_weight);
-    own = unpack8(__ldg(w + li));
+    own = unpack8(load_global(w + li));
     if (rotated) {
       const float* row = a.cos_sin + pos * a.cos_sin_stride;
       if constexpr (kInterleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * li));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * li));
+        const float4 c = load_global(reinterpret_cast<const float4*>(row + 4 * li));
+        const float4 s = load_global(reinterpret_cast<const float4*>(row + half + 4 * li));
         const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -93,13 +93,13 @@ __global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_kernel(const NormRop
           own.v[i] = fmul2(own.v[i], make_float2(cs[i], cs[i]));
         }
       } else {
-        other = unpack8(__ldg(w + partner));
+        other = unpack8(load_global(w + partner));
         const float2* c = reinterpret_cast<const float2*>(row + 8 * li - (second ? half : 0));
         const float2* s = reinterpret_cast<const float2*>(row + half + 8 * li - (second ? half : 0));
         const float sign = second ? 1.0f : -1.0f;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + i)), s4 = __ldg(reinterpret_cast<const float4*>(s + i));
+          const float4 c4 = load_global(reinterpret_cast<const float4*>(c + i)), s4 = load_global(reinterpret_cast<const float4*>(s + i));
           own.v[i] = fmul2(own.v[i], make_float2(c4.x, c4.y));
           own.v[i + 1] = fmul2(own.v[i + 1], make_float2(c4.z, c4.w));
           other.v[i] = fmul2(other.v[i], make_float2(sign * s4.x, sign * s4.y));

@@ -125,7 +125,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, const Request& rq, uint32_t kv_head,
                                              int64_t row0, int32_t rows, int32_t rank, int32_t dims, uint32_t o,
                                              uint32_t stride, uint32_t m, uint32_t l) {
-  const float v_scale = __ldg(a.v_scale);
+  const float v_scale = load_global(a.v_scale);
   cluster_sync();
   const int32_t chunks = dims / 8;
   // (distributed shared memory gives an SM about 14 bytes a clock: the shares are equal)
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   uint32_t q[kRowTiles][kKSteps][2];
   float sc[kRowTiles][2];
   float m[kRowTiles][2], l[kRowTiles][2];                 // reference maximum, sum
-  const float scale = a.scale_log2 * __ldg(a.k_scale);
+  const float scale = a.scale_log2 * load_global(a.k_scale);
 #pragma unroll
   for (int nt = 0; nt < kRowTiles; ++nt) {
     const int32_t r = 8 * nt + g;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
                                                         (rq.token0 + tk) * a.q_stride_t + h * a.q_stride_h + c * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        w[i] = __ldg(src + i);
+        w[i] = load_global(src + i);
         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
             } else if (see && p >= rq.first_pos) {
               const int32_t d = static_cast<int32_t>(p - rq.first_pos);
               see = (d >> 6) < a.tree_words &&
-                    ((__ldg(a.tree_mask + (rq.token0 + tk) * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
+                    ((load_global(a.tree_mask + (rq.token0 + tk) * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
             }
             if (!see) s[e >> 1][nt][2 * (e & 1) + x] = hidden;
           }
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
 
   // ---- join the four warps -------------------------------------------------
-  const float v_scale = __ldg(a.v_scale);        // under way meanwhile
+  const float v_scale = load_global(a.v_scale);        // under way meanwhile
   cp_wait<0>();
   __syncthreads();                               // every ring is idle
   float* jo = reinterpret_cast<float*>(smem);    // [kWarps][kRows][D]
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   Request rq;
   const bool live = request_of(a, b, rq) && flat < static_cast<int64_t>(rq.tokens) * a.num_heads;
-  const float v_scale = __ldg(a.v_scale);
+  const float v_scale = load_global(a.v_scale);
   const int64_t row = live ? rq.token0 * a.num_heads + flat : 0;
   const float* ls = a.part_lse + row * a.num_splits;
   constexpr int kDims = D / 32;                          // per lane

@@ -119,7 +119,7 @@ __device__ __forceinline__ LookUp look_up_position(const PerHeadAttentionArgs& a
   u.in = in;
   u.row = (p - col * static_cast<uint32_t>(a.block_size)) * static_cast<uint32_t>(a.row_offset) + head_row;
   u.id = -1;
-  if (in && col < static_cast<uint32_t>(a.block_table_width)) u.id = __ldg(table + col);
+  if (in && col < static_cast<uint32_t>(a.block_table_width)) u.id = load_global(table + col);
   return u;
 }
 // a + b c in 64 bits, b and c 32 (one instruction).
@@ -138,8 +138,8 @@ struct Request {
 // The request, or false (skipped): its query tokens are not inside [0,
 // num_tokens), or more than max_query_len.
 __device__ __forceinline__ bool request_of(const PerHeadAttentionArgs& a, int b, Request& r) {
-  const int32_t q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
-  const int32_t len = max(0, __ldg(a.seq_lens + b));
+  const int32_t q0 = load_global(a.query_start + b), q1 = load_global(a.query_start + b + 1);
+  const int32_t len = max(0, load_global(a.seq_lens + b));
   r.token0 = q0;
   r.tokens = q1 - q0;
   r.first_pos = static_cast<int64_t>(len) - r.tokens;

@@ -122,11 +122,11 @@ __device__ __forceinline__ uint32_t range_bits(int32_t p0, int32_t lo, int32_t h
 // Bits d .. d + 31 of a mask row (bits outside it are 0).
 __device__ __forceinline__ uint32_t tree_bits(const uint64_t* row, int32_t words, int64_t d) {
   if (d <= -32) return 0;
-  if (d < 0) return static_cast<uint32_t>(__ldg(row) << static_cast<int>(-d));
+  if (d < 0) return static_cast<uint32_t>(load_global(row) << static_cast<int>(-d));
   const int64_t w = d >> 6;
   const int sh = static_cast<int>(d & 63);
-  uint64_t v = w < words ? __ldg(row + w) >> sh : 0;
-  if (sh > 32 && w + 1 < words) v |= __ldg(row + w + 1) << (64 - sh);
+  uint64_t v = w < words ? load_global(row + w) >> sh : 0;
+  if (sh > 32 && w + 1 < words) v |= load_global(row + w + 1) << (64 - sh);
   return static_cast<uint32_t>(v);
 }
 
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
   using S = Shape<D, kTiles>;
   wait_for_previous();
-  const float k_scale = __ldg(a.k_scale);           // in flight beside the request
+  const float k_scale = load_global(a.k_scale);           // in flight beside the request
   // the last row blocks of a causal chunk, which see the most keys, come first
   const Place place = place_of(a, row_blocks);
   const uint32_t head = place.head;
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
-    const float v_scale = __ldg(a.v_scale);
+    const float v_scale = load_global(a.v_scale);
     // the last product is done: O is complete
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);

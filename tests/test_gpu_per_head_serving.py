@@ -722,3 +722,62 @@ def test_a_chain_of_calls_runs_in_order(kvq, new):
     for run in (*got, captured):
         for a, c in zip(run, want):
             assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
+def test_out_of_memory_is_torchs_own_error(kvq):
+    """A workspace past the allocator's limit (set low for the call): torch's
+    error, and the next call is as before."""
+    b = Batch([(300, 1)], 8, 2, 128, 16, "NHD", 97)
+    d = b.device()
+    want = kvq.kvq_window_attention_nvfp4_per_head(**d)
+    q = torch.zeros(1 << 16, 8, 128, dtype=torch.bfloat16, device=DEV)       # 128 MiB; 32 GiB of workspace
+    wide = dict(d, q=q, query_start=i32([0, 1]), num_splits=128)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.02)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            kvq.kvq_window_attention_nvfp4_per_head(**wide)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    got = kvq.kvq_window_attention_nvfp4_per_head(**d)
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_what_the_kernel_before_wrote_is_what_is_read(kvq, new):
+    """Lengths, tables, masks, positions and scales written by a kernel that
+    is queued directly before the call: the bits of a run that waits."""
+    b = Batch([(400, new), (90, new)], 8, 2, 128, 16, "NHD", 98)
+    d = b.device()
+    d["tree_mask"] = mask_dev(random_tree(b.reqs, 1, b.rng))
+    T = b.start[-1]
+    w = bf16_dev(ref.to_bf16(1 + 0.1 * b.rng.standard_normal(128)))
+    table = dev(b.rng.standard_normal((800, 128)).astype(np.float32))
+    pos = dev(b.rng.integers(0, 800, T))
+    names = ("seq_lens", "block_table", "tree_mask", "k_scale", "v_scale", "query_start")
+    other = {n: d[n].clone() for n in names}
+    other["seq_lens"] = d["seq_lens"] - i32([37, 11])
+    other["block_table"] = d["block_table"].flip(0).contiguous()
+    other["tree_mask"] = torch.zeros_like(d["tree_mask"])
+    other["k_scale"], other["v_scale"] = d["k_scale"] * 0.5, d["v_scale"] * -2
+    pos2, w2 = pos.flip(0).contiguous(), (w.float() * 0.5).bfloat16()
+
+    def rounds(wait):
+        live = {n: d[n].clone() for n in names}
+        p, wl = pos.clone(), w.clone()
+        out = []
+        for i in range(8):
+            for n in names:
+                live[n].copy_((other if i % 2 else d)[n])
+                wait()
+            out += kvq.kvq_tree_attention_nvfp4_per_head(**{**d, **live})
+            wait()
+            wl.copy_(w2 if i % 2 else w)
+            p.copy_(pos2 if i % 2 else pos)
+            wait()
+            out += kvq.kvq_qk_norm_rope(d["q"], d["q"], wl, wl, p, table, 1e-6)
+            wait()
+        return out
+
+    want, got = rounds(torch.cuda.synchronize), rounds(lambda: None)
+    assert all(torch.equal(a.view(torch.uint8), c.view(torch.uint8)) for a, c in zip(got, want))
