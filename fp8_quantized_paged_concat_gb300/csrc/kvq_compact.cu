@@ -14,7 +14,7 @@
 // of a request as its threads hold, and then moves several layers' entries:
 // a thread keeps kUnits units of kLayers layers in registers between its
 // loads, all issued together, and its stores.  64 requests x 32 layers of 8
-// heads: 14 us (one CTA per layer and head: 80 us).
+// heads: 13 us (one CTA per layer and head: 80 us).
 #include <algorithm>
 
 #include "kvq_dependent.cuh"

@@ -17,7 +17,7 @@
 // key head.  Each warp takes every fourth step of 32 keys, with its own
 // running maximum and sum, and the warps join at the end through shared
 // memory; the ranges of a small call run as a cluster and join through its
-// distributed shared memory (one request, window of 1024, 64 heads: 7.5 us;
+// distributed shared memory (one request, window of 1024, 64 heads: 7.1 us;
 // a second launch costs about 4 more), others in a second launch.  A warp
 // copies a step's raw bytes
 // (32 entries of 9 D / 16 bytes, K and V) into its own two-stage ring with
@@ -711,7 +711,7 @@ constexpr int resident_ctas(int32_t head_size, int64_t block) { return head_size
 
 // Rows per block of the few-row kernel.  16 rows share a decoded key where
 // such blocks fill the GPU (128 requests x 2048 keys, head size 128, 16 rows:
-// 111 us against 126 with two blocks of 8; 32 rows: 183 against 230); a
+// 113 us against 126 with two blocks of 8; 32 rows: 187 against 230); a
 // smaller call is short of CTAs, and blocks of 8 halve its chain (one request
 // x 1024 keys, 16 rows: 12.9 against 15.0 us; 16384 keys: 23 against 31).
 // D = 256 has no registers for 16.
@@ -725,7 +725,7 @@ int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits
 // decodes it once.  us of the one and the other, 128 requests x 2048 keys x 8
 // key heads (4 at D = 256):
 //   D =  64: 48 rows 169 / 218, 64 rows 214 / 220, 96 rows 314 / 224
-//   D = 128: 24 rows 181 / 232, 32 rows 183 / 234, 48 rows 265 / 240
+//   D = 128: 24 rows 185 / 232, 32 rows 187 / 234, 48 rows 265 / 240
 //   D = 256: 16 rows 144 / 187, 24 rows 199 / 189, 32 rows 251 / 189
 int64_t most_few_rows(int32_t head_size) { return head_size == 64 ? 64 : head_size == 128 ? 32 : 16; }
 
@@ -760,7 +760,7 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
   if (ragged && 8 * blocks >= places) {
     // Several ranges to a CTA's place even the lengths out.  The few-row
     // kernel: six, or two where there are more blocks than places (32 requests
-    // of 7k to 34k keys: 164 us; one range per place 217; equal lengths would
+    // of 7k to 34k keys: 161 us; one range per place 217; equal lengths would
     // do with one, 4 to 20 % faster then).  The tensor memory kernel, whose
     // ranges cost more to start: three (32 requests x 8192 keys x 48 rows at D =
     // 256: 203 us, six 232), or six where there are more blocks than places (32
