@@ -9,6 +9,8 @@
 // 4.1 -> 3.1, of 32 layers 16.4 -> 13.9, a tree of one user 20.5 -> 19.0.
 #pragma once
 
+#include <cstdint>
+
 #include <cuda_runtime.h>
 
 namespace kvq {
@@ -25,6 +27,15 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 template <class T>
 __device__ __forceinline__ T load_global(const T* p) {
   return *p;
+}
+// The same, opaque, where registers are short: plain loads of an unrolled loop
+// are merged and held (mask words in the few-row attention's blocks of 16
+// rows: spills, calls 2 to 4 % slower; its blocks of 8 have the registers, and
+// a single-token call takes 7.1 us with plain loads, 7.4 with opaque ones).
+__device__ __forceinline__ uint64_t load_global64(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
 }
 
 // Launches kernel(args...) as a dependent one; cluster > 1: in clusters of that many CTAs (along x).

@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
               see = see && p <= hi && (p >= lo || p < a.num_sinks);
             } else if (see && p >= rq.first_pos) {
               const int32_t d = static_cast<int32_t>(p - rq.first_pos);
+              const uint64_t* word = a.tree_mask + (rq.token0 + tk) * a.tree_stride + (d >> 6);
               see = (d >> 6) < a.tree_words &&
-                    ((load_global(a.tree_mask + (rq.token0 + tk) * a.tree_stride + (d >> 6)) >> (d & 63)) & 1);
+                    (((kRowTiles == 2 ? load_global64(word) : load_global(word)) >> (d & 63)) & 1);
             }
             if (!see) s[e >> 1][nt][2 * (e & 1) + x] = hidden;
           }
@@ -711,7 +712,7 @@ constexpr int resident_ctas(int32_t head_size, int64_t block) { return head_size
 
 // Rows per block of the few-row kernel.  16 rows share a decoded key where
 // such blocks fill the GPU (128 requests x 2048 keys, head size 128, 16 rows:
-// 113 us against 126 with two blocks of 8; 32 rows: 187 against 230); a
+// 111 us against 126 with two blocks of 8; 32 rows: 183 against 230); a
 // smaller call is short of CTAs, and blocks of 8 halve its chain (one request
 // x 1024 keys, 16 rows: 12.9 against 15.0 us; 16384 keys: 23 against 31).
 // D = 256 has no registers for 16.
@@ -725,7 +726,7 @@ int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits
 // decodes it once.  us of the one and the other, 128 requests x 2048 keys x 8
 // key heads (4 at D = 256):
 //   D =  64: 48 rows 169 / 218, 64 rows 214 / 220, 96 rows 314 / 224
-//   D = 128: 24 rows 185 / 232, 32 rows 187 / 234, 48 rows 265 / 240
+//   D = 128: 24 rows 181 / 232, 32 rows 183 / 234, 48 rows 265 / 240
 //   D = 256: 16 rows 144 / 187, 24 rows 199 / 189, 32 rows 251 / 189
 int64_t most_few_rows(int32_t head_size) { return head_size == 64 ? 64 : head_size == 128 ? 32 : 16; }
 
