@@ -781,3 +781,36 @@ def test_what_the_kernel_before_wrote_is_what_is_read(kvq, new):
 
     want, got = rounds(torch.cuda.synchronize), rounds(lambda: None)
     assert all(torch.equal(a.view(torch.uint8), c.view(torch.uint8)) for a, c in zip(got, want))
+
+
+@pytest.mark.parametrize("dim,heads,kv,new", [(64, 8, 2, 3), (64, 8, 2, 5), (64, 10, 2, 3), (128, 8, 2, 3), (128, 14, 2, 4)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_many_requests_of_a_few_rows(kvq, dim, heads, kv, new, tree):
+    """Enough requests to fill the GPU with blocks of 16 query rows (ragged
+    lengths, 9 to 28 rows per request and key head)."""
+    rng = np.random.default_rng(99)
+    reqs = [(int(c), new if i % 3 else int(rng.integers(0, new + 1))) for i, c in enumerate(rng.integers(0, 50, 240))]
+    b = Batch(reqs, heads, kv, dim, 16, "NHD", 100)
+    d = dict(b.device(), max_query_len=new)
+    if tree:
+        rows = random_tree(reqs, 1, b.rng, empty=(3, 17))
+        check(kvq.kvq_tree_attention_nvfp4_per_head(**d, tree_mask=mask_dev(rows)), b.want(tree=rows))
+    else:
+        check(kvq.kvq_window_attention_nvfp4_per_head(**d, window=21, num_sinks=2), b.want(window=21, sinks=2))
+    check(kvq.kvq_window_attention_nvfp4_per_head(**through_workspace(kvq, d, 3)), b.want())
+
+
+@pytest.mark.parametrize("dim,heads,kv,new", [(64, 6, 2, 11), (64, 6, 2, 21), (64, 6, 2, 22), (128, 8, 2, 8), (128, 8, 2, 9),
+                                              (256, 4, 2, 8), (256, 4, 2, 9), (256, 4, 2, 16)])
+@pytest.mark.parametrize("splits", [1, 2, -2, None])
+def test_rows_on_both_sides_of_the_kernels_limits(kvq, dim, heads, kv, new, splits):
+    """33 to 66 rows at head size 64, 32 and 36 at 128, 16 to 32 at 256: whole,
+    in clusters where the call may, and through a workspace."""
+    reqs = [(70, new), (3, new), (300, new - 1)]
+    b = Batch(reqs, heads, kv, dim, 16, "HND", 101)
+    d = b.device()
+    rows = random_tree(reqs, 1, b.rng, empty=(1,))
+    if splits is not None:
+        d = through_workspace(kvq, d, -splits) if splits < 0 else dict(d, num_splits=splits)
+    check(kvq.kvq_tree_attention_nvfp4_per_head(**d, tree_mask=mask_dev(rows)), b.want(tree=rows))
+    check(kvq.kvq_window_attention_nvfp4_per_head(**d, window=100, num_sinks=5), b.want(window=100, sinks=5))
