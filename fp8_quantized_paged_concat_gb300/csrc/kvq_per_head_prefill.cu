@@ -67,8 +67,10 @@ struct Shape {
   static constexpr int kThreads = 32 * (kOutputWarp + 1);
   static_assert(kThreads == 512, "warpgroups");
   static constexpr int kStartRegs = 128;
-  static constexpr int kSoftmaxRegs = kTiles == 2 ? 152 : 200;
-  static constexpr int kOtherRegs = kTiles == 2 ? 104 : 96;
+  // (two row tiles: 152 / 104 and 136 / 120 spill in the loops; 4 x 4096 tokens
+  // 898 us with the former, 861 with 144 / 112)
+  static constexpr int kSoftmaxRegs = kTiles == 2 ? 144 : 200;
+  static constexpr int kOtherRegs = kTiles == 2 ? 112 : 96;
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
                     kThreads * kStartRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
@@ -271,23 +273,28 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
     }
     cp_commit();
   };
+  // The first look-ups are under way before the CTA's set-up is waited for: all
+  // of the first chunks', or one (two row tiles: registers).
   LookUp next;
   if constexpr (kTiles == 1) {
-    LookUp first[S::kRing];                         // all under way before the first is looked at
+    LookUp first[S::kRing];
 #pragma unroll
     for (int h = 0; h < S::kRing; ++h) first[h] = look_up(h);
     next = look_up(S::kRing);
+    set_up_done();
 #pragma unroll
     for (int h = 0; h < S::kRing; ++h) start(h, first[h]);
   } else {
     next = look_up(0);
-#pragma unroll
+    set_up_done();
+    // (rolled, the code is fetched sooner: short ragged chunks at D = 64 29.3
+    // against 31.4 us; at D = 128 it spills in the loop below, 875 against 861)
+#pragma unroll (D == 64 ? 1 : S::kRing)
     for (int h = 0; h < S::kRing; ++h) {
       start(h, next);
       next = look_up(h + 1);
     }
   }
-  set_up_done();
   Piece<D> e[kPasses];                              // of the next chunk: read a chunk ahead, all at once
   auto read = [&](int32_t h) {
     cp_wait<S::kRing - 1>();
