@@ -30,7 +30,7 @@
 //     that one of them may exceed it by 2^8 is the tile's maximum taken, the
 //     pass repeated and O rescaled.
 // Measured: 4 requests x 4096 new tokens x 32 heads (8 key heads) of 128,
-// window 4096: 893 us = 1232 TFLOP/s, about 1800 clocks per pair of row tiles
+// window 4096: 860 us = 1279 TFLOP/s, about 1700 clocks per pair of row tiles
 // and 64 keys, of which the products take 1280 (768 for the scores, whose 64
 // columns run at two thirds of the full rate).  The softmax warps set the pace: about
 // 1000 clocks for the exponentials, sums and f16 weights of the two row tiles
