@@ -47,6 +47,7 @@
 // rows, and their issue, not the copies, sets the pace (3 stages or 5 CTAs an
 // SM are slower: registers).
 #include <algorithm>
+#include <cmath>
 
 #include "kvq_per_head_attention.cuh"
 
@@ -746,13 +747,21 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
   const bool few = rows <= most_few_rows(head_size);
   const bool ragged = !windowed && keys >= 4096 && batch_size > 1;   // long contexts, whose lengths may differ
-  // A small call's ranges run as clusters of the few-row kernel: no second launch.
+  // A small call's ranges run as clusters of the few-row kernel: no second
+  // launch.  Where the GPU has room for many more ranges than a cluster takes,
+  // that pays for fewer keys (head size 128, us of a cluster of 8 and of 16
+  // ranges through a workspace: one request, 8 key heads, 2048 keys 7.0 / 7.1,
+  // 4096 keys 8.6 / 7.9, 8000 keys 10.9 / 9.0; four requests, room for 19,
+  // 4096 keys 10.6 / 13.2, 8000 keys 14.3 / 15.4), and so it is where only two
+  // CTAs share an SM (head size 256, four requests, 4 key heads: 2048 keys 12.6 /
+  // 13.5, 4096 keys 16.0 / 15.6, 8000 keys 22.2 / 17.4).
   if (rows <= KVQ_PER_HEAD_CLUSTER_ROWS) {
     constexpr int64_t kMax = KVQ_PER_HEAD_CLUSTER_SPLITS, kLeast = 128;       // a step per warp
     const int64_t blocks = (rows + 7) / 8 * groups, places = resident_ctas(head_size, 8) * int64_t{sms};
     const bool long_small = ragged && 8 * blocks >= places;
-    const int64_t n = std::min<int64_t>(keys / kLeast, places / blocks);
-    if (!long_small && n > 1 && (n <= kMax || keys <= kMax * 8 * kLeast)) return static_cast<int32_t>(std::min(n, kMax));
+    const int64_t room = places / blocks, n = std::min<int64_t>(keys / kLeast, room);
+    if (!long_small && n > 1 && (n <= kMax || keys <= kMax * (room >= 4 * kMax || head_size == 256 ? 320 : 1024)))
+      return static_cast<int32_t>(std::min(n, kMax));
   }
   const int64_t block = few ? few_rows(rows, groups, head_size, 1, sms) : per_head_prefill_rows(rows, head_size);
   const int64_t blocks = (rows + block - 1) / block * groups;
@@ -769,7 +778,12 @@ int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t nu
     const int64_t per_place = few == (blocks >= places) ? (few ? 2 : 3) : 6;
     n = std::min<int64_t>(keys / 1024, (per_place * places + blocks - 1) / blocks);
   } else {
-    n = std::min<int64_t>(keys / (few ? 128 : 256), places / blocks);   // as many as the call is short of CTAs
+    // As many as the call is short of CTAs, of at least 256 keys in the tensor
+    // memory kernel.  In the few-row kernel a range costs keys / n steps and the
+    // join n rows: their sum is least where n grows with the root of the keys
+    // (one request, 8 key heads of 128: 8000 keys in 16 ranges 9.0 us, 32 9.4, 64
+    // 11.5; 12000 keys 10.3, 10.6, 12.4; 65536 keys 46, 37, 33).
+    n = std::min<int64_t>(few ? static_cast<int64_t>(std::sqrt(keys / 16.0)) : keys / 256, places / blocks);
   }
   n = std::max<int64_t>(1, std::min<int64_t>(KVQ_PER_HEAD_MAX_SPLITS, n));
   if (n > 1) {
