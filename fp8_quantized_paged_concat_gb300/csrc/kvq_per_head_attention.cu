@@ -605,25 +605,24 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 // Joins the ranges of every row: with L_s the base-2 log-sum-exp of range s
 // and o_s its normalised output, out = sum 2^(L_s - M) o_s / sum 2^(L_s - M).
 // One warp per (token, head) row of a live request; a range that saw nothing
-// (-inf) weighs nothing.  Latency bounds it, so the chain is short: the call's
-// own arrays are read before the ranges are waited for (what wrote them was
-// complete when their kernel started), and the first ranges' rows are loaded
-// beside their L_s, not after.
+// (-inf) weighs nothing.  Latency bounds it, so the chain is short: the first
+// ranges' rows are loaded beside their L_s, not after.  The call's own arrays
+// are read after the wait like everything else: what an earlier kernel wrote
+// is promised to be visible only there.
 constexpr int kJoinWarps = 4;
 
 template <int D, int kBatch>                             // kBatch: ranges in flight
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const PerHeadAttentionArgs a) {
   const int64_t flat = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, b = blockIdx.y;
+  wait_for_previous();
+  const float v_scale = load_global(a.v_scale);          // in flight beside the request
   Request rq;
-  const bool live = request_of(a, b, rq) && flat < static_cast<int64_t>(rq.tokens) * a.num_heads;
-  const float v_scale = load_global(a.v_scale);
-  const int64_t row = live ? rq.token0 * a.num_heads + flat : 0;
+  if (!request_of(a, b, rq) || flat >= static_cast<int64_t>(rq.tokens) * a.num_heads) return;
+  const int64_t row = rq.token0 * a.num_heads + flat;
   const float* ls = a.part_lse + row * a.num_splits;
   constexpr int kDims = D / 32;                          // per lane
   const float* po = a.part_o + row * a.num_splits * D + kDims * lane;
-  wait_for_previous();
-  if (!live) return;
   float2 v[kBatch][kDims / 2];
   auto load = [&](int s0) {
 #pragma unroll

@@ -814,3 +814,34 @@ def test_rows_on_both_sides_of_the_kernels_limits(kvq, dim, heads, kv, new, spli
         d = through_workspace(kvq, d, -splits) if splits < 0 else dict(d, num_splits=splits)
     check(kvq.kvq_tree_attention_nvfp4_per_head(**d, tree_mask=mask_dev(rows)), b.want(tree=rows))
     check(kvq.kvq_window_attention_nvfp4_per_head(**d, window=100, num_sinks=5), b.want(window=100, sinks=5))
+
+
+@pytest.mark.parametrize("new,splits", [(1, 4), (1, 40), (40, 3)])
+def test_what_the_kernel_before_wrote_is_what_the_join_reads(kvq, new, splits):
+    """The same for a call whose ranges join through a workspace, in a second
+    kernel: lengths, query ranges and value scale written directly before it."""
+    b = Batch([(900, new), (700, new), (90, new)], 8, 2, 128, 16, "NHD", 102)
+    d = through_workspace(kvq, b.device(), splits)
+    names = ("query_start", "seq_lens", "v_scale")
+    other = dict(query_start=i32([0, new, new, 3 * new]), seq_lens=d["seq_lens"] - i32([37, 300, 5]),
+                 v_scale=d["v_scale"] * -2)
+    d["max_query_len"] = 2 * new
+
+    def rounds(wait):
+        live = {n: d[n].clone() for n in names}
+        out = []
+        for i in range(16):
+            for n in names:
+                live[n].copy_((other if i % 2 else d)[n])
+                wait()
+            o = torch.full((3 * new, 8, 128), CANARY, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+            wait()
+            out += kvq.kvq_window_attention_nvfp4_per_head(**{**d, **live}, out=o)
+            wait()
+        return out
+
+    want, got = rounds(torch.cuda.synchronize), rounds(lambda: None)
+    assert all(torch.equal(a.view(torch.uint8), c.view(torch.uint8)) for a, c in zip(got, want))
+    check(want[:2], b.want())
+    b.start, b.lens, b.v_scale = [0, new, new, 3 * new], other["seq_lens"].tolist(), b.v_scale * np.float32(-2)
+    check(want[2:4], b.want())
