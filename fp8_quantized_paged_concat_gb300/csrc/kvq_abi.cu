@@ -1,8 +1,10 @@
 // kvq_abi.cu -- the extern "C" entry points declared in include/kvq.h:
 // host-side validation, device check, launch on the caller's stream, status.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <algorithm>
+#include <limits>
 #include <mutex>
 #include <string>
 
@@ -844,8 +846,9 @@ kvq_status per_head_attention(
               "%s: block_table_width * block_size must stay below 2^31 - 256 positions", fn);
   KVQ_REQUIRE(k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4),
               "%s: k_scale / v_scale must be device fp32 scalars", fn);
-  KVQ_REQUIRE(softmax_scale == softmax_scale && softmax_scale > -3.0e38f && softmax_scale < 3.0e38f,
-              "%s: softmax_scale must be finite", fn);
+  const double scale_log2 = static_cast<double>(softmax_scale) * 1.4426950408889634074;
+  KVQ_REQUIRE(std::fabs(scale_log2) <= std::numeric_limits<float>::max(),
+              "%s: softmax_scale must be finite, its product with log2(e) as well", fn);
   if (tree != nullptr)
     KVQ_REQUIRE(tree->mask != nullptr && aligned(tree->mask, 8) && tree->words >= 1 && tree->stride >= tree->words &&
                     int64_t{tree->words} * 64 >= max_query_len,
@@ -893,7 +896,7 @@ kvq_status per_head_attention(
   a.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634074);
+  a.scale_log2 = static_cast<float>(scale_log2);
   a.window = window;
   a.num_sinks = num_sinks;
   if (tree != nullptr) {

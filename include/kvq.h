@@ -638,8 +638,9 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * [num_tokens, num_heads], token stride lse_stride_t, or NULL.  kv_cache,
  * layout, k_scale, v_scale: as kvq_reshape_and_cache_nvfp4, and block_size *
  * num_kv_heads * full_dim a multiple of 16 below 2^31 and block_table_width *
- * block_size below 2^31 - 256.  query_start: int32 [batch_size + 1], the
- * requests' ranges disjoint; seq_lens: int32 [batch_size]; batch_size <= 65535.
+ * block_size below 2^31 - 256.  softmax_scale: softmax_scale * log2(e) is
+ * finite in fp32.  query_start: int32 [batch_size + 1], the requests' ranges
+ * disjoint; seq_lens: int32 [batch_size]; batch_size <= 65535.
  * Calls of few query rows per request and key head run on the warps' matrix
  * instructions and wait for nothing but their own copies; the others run on
  * tensor memory with bounded waits, on whose expiry the rows concerned stay

@@ -151,6 +151,18 @@ def test_attention_accepts_good_arguments(lib, over):
 
 
 @no_gpu_only
+@pytest.mark.parametrize("scale,good", [(2.35e38, True), (-2.35e38, True), (2.4e38, False), (-2.4e38, False), (2.99e38, False)])
+def test_softmax_scales_that_overflow_in_base_two_are_refused(lib, scale, good):
+    """The kernels' factor is softmax_scale * log2(e), in fp32: past 2.3586e38 it would be infinite."""
+    assert np.isfinite(np.float32(np.float64(np.float32(scale)) * np.log2(np.e))) == good
+    for name, args in (("kvq_window_attention_nvfp4_per_head", window_args), ("kvq_tree_attention_nvfp4_per_head", tree_args)):
+        if good:
+            assert getattr(lib, name)(*args(softmax_scale=scale).values()) in (2, 3), err(lib)
+        else:
+            rejected(lib, name, args(softmax_scale=scale), "softmax_scale must be finite")
+
+
+@no_gpu_only
 @pytest.mark.parametrize("over", [dict(num_tokens=0), dict(batch_size=0), dict(max_query_len=0)])
 def test_empty_calls_do_nothing(lib, over):
     """No rows: nothing else is looked at."""
