@@ -652,7 +652,8 @@ def kvq_window_attention_nvfp4_per_head(q, query_start, seq_lens, block_table, k
     (up to PER_HEAD_CLUSTER_SPLITS of calls with at most 32 query rows per
     request and key head; no workspace) or through a workspace: a CUDA tensor
     of at least kvq_per_head_attention_workspace_bytes bytes (allocated here,
-    on the call's stream, when one is needed and None is given).  Returns (out
+    on the call's stream, when one is needed and None is given; left alone
+    when num_splits is left out and its default needs none).  Returns (out
     bf16 [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, k_scale, v_scale,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,

@@ -337,9 +337,11 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     at::Tensor workspace;
     if (a[15] != Py_None) {
-      workspace = tensor("workspace", a[15]);
-      if (!workspace.is_cuda() || workspace.get_device() != dev || !workspace.is_contiguous())
+      const at::Tensor& given = tensor("workspace", a[15]);
+      if (!given.is_cuda() || given.get_device() != dev || !given.is_contiguous())
         bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
+      // default ranges that join without one run without it
+      if (use_workspace || a[14] != Py_None) workspace = given;
     } else if (use_workspace && T > 0) {
       const int64_t bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
       if (bytes > 0) workspace = scope.buffer({bytes}, at::kByte);

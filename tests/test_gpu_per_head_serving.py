@@ -845,3 +845,33 @@ def test_what_the_kernel_before_wrote_is_what_the_join_reads(kvq, new, splits):
     check(want[:2], b.want())
     b.start, b.lens, b.v_scale = [0, new, new, 3 * new], other["seq_lens"].tolist(), b.v_scale * np.float32(-2)
     check(want[2:4], b.want())
+
+
+def test_a_workspace_that_the_default_ranges_do_not_need(kvq):
+    """An engine keeps one workspace for all its calls: a call whose default
+    ranges join in a cluster runs as without it, however small it is, and one
+    whose ranges need it uses it."""
+    b = Batch([(2000, 1)], 8, 2, 128, 16, "NHD", 103)
+    d = b.device()
+    splits, use_workspace = kvq.kvq_per_head_attention_default_splits(1, 8, 2, 128, 1, 2001)
+    assert splits > 1 and not use_workspace
+    want = kvq.kvq_window_attention_nvfp4_per_head(**d)
+    check(want, b.want())
+    mine = torch.full((64,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine)
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+    assert torch.all(mine == 0x5A)
+    with pytest.raises(ValueError, match="workspace: expected"):
+        kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine.cpu())
+    # ranges asked for by number go through the workspace that is given
+    with pytest.raises(RuntimeError, match="workspace must be"):
+        kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine, num_splits=splits)
+    b = Batch([(20000, 1)], 8, 1, 128, 16, "NHD", 104)
+    d = b.device()
+    splits, use_workspace = kvq.kvq_per_head_attention_default_splits(1, 8, 1, 128, 1, 20001)
+    assert use_workspace
+    with pytest.raises(RuntimeError, match="workspace must be"):
+        kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine)
+    mine = torch.zeros(kvq.kvq_per_head_attention_workspace_bytes(1, 8, 128, splits), dtype=torch.uint8, device=DEV)
+    got, want = kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine), kvq.kvq_window_attention_nvfp4_per_head(**d)
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.any(mine != 0)
