@@ -594,7 +594,9 @@ _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "k
 def _load_native():
     """Loads the extension module (once) and hands it the library's entry points."""
     global _native
-    path = os.path.join(_HERE, "_lib", "kvq_native.so")
+    from . import _build
+
+    path = _build.native_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
     handle = load_library()

@@ -5,7 +5,7 @@ Each .cu file under csrc/ is compiled in parallel with nvcc for sm_103a only
 IEEE-rounded divisions), then linked into
 fp8_quantized_paged_concat_gb300/_lib/libkvq.so against the shared CUDA
 runtime, the same one PyTorch loads.  Beside it, and at the same time, the
-extension module kvq_native.so is compiled with g++ against PyTorch's headers.
+extension module kvq_native is compiled with g++ against PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,7 +22,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "kvq")
 LIBRARY = os.path.join(PKG, "_lib", "libkvq.so")
-NATIVE = os.path.join(PKG, "_lib", "kvq_native.so")
 
 SOURCES = ["kvq_abi.cu", "kvq_write.cu", "kvq_gather.cu", "kvq_per_head.cu", "kvq_index.cu",
            "kvq_attention.cu", "kvq_selftest.cu", "kvq_norm_rope.cu", "kvq_per_head_attention.cu",
@@ -45,23 +45,29 @@ def _headers_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
-def _older(path: str, than: float) -> bool:
-    return not os.path.exists(path) or os.path.getmtime(path) < than
+def native_path() -> str:
+    """The extension module's file, which carries the names of the Python and
+    the PyTorch whose binary interfaces it was compiled against."""
+    import torch
+
+    return os.path.join(PKG, "_lib", f"kvq_native-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_native(force: bool = False) -> str:
-    """Compiles kvq_native.so, the extension module, if its source or PyTorch is newer."""
+    """Compiles the extension module if its sources or PyTorch are newer."""
     import torch
 
+    native = native_path()
     source = os.path.join(CSRC, "kvq_binding.cpp")
-    if not (force or _older(NATIVE, max(os.path.getmtime(source), os.path.getmtime(torch.__file__)))):
-        return NATIVE
-    os.makedirs(os.path.dirname(NATIVE), exist_ok=True)
+    newest = max(os.path.getmtime(source), _headers_mtime(), os.path.getmtime(torch.__file__))
+    if not (force or not os.path.exists(native) or os.path.getmtime(native) < newest):
+        return native
+    os.makedirs(os.path.dirname(native), exist_ok=True)
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     includes = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = NATIVE + ".tmp.%d" % os.getpid()
+    tmp = native + ".tmp.%d" % os.getpid()
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", source, "-o", tmp,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *("-I" + i for i in includes),
            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
@@ -69,13 +75,16 @@ def build_native(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on kvq_binding.cpp:\n{r.stderr}")
-    os.replace(tmp, NATIVE)
-    return NATIVE
+    os.replace(tmp, native)
+    return native
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), library: str = LIBRARY,
           objdir: str = OBJDIR) -> str:
     """Compiles and links libkvq.so if any source is newer; returns its path.
+    The extension module is compiled beside it; where that fails (no g++, no
+    PyTorch headers) the library, which needs neither, is complete all the
+    same, and a warning says why the calls of the module will be missing.
     ``extra_flags`` / ``library`` / ``objdir`` build a variant elsewhere (for
     example with -D tuning knobs) without touching the default library."""
     os.makedirs(objdir, exist_ok=True)
@@ -98,9 +107,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), library: s
         return o
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        native = pool.submit(build_native, force or _older(NATIVE, hdr))
+        native = pool.submit(build_native, force)
         objs = list(pool.map(compile_one, SOURCES))
-        native.result()
     if force or not os.path.exists(library) or os.path.getmtime(library) < max(map(os.path.getmtime, objs)):
         tmp = library + ".tmp.%d" % os.getpid()
         cmd = [compiler, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
@@ -109,6 +117,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), library: s
         if r.returncode != 0:
             raise RuntimeError(f"linking libkvq.so failed:\n{r.stderr}")
         os.replace(tmp, library)
+    if native.exception() is not None:
+        warnings.warn(f"the extension module was not built: {native.exception()}", stacklevel=2)
     return library
 
 
