@@ -10,6 +10,7 @@
 
 #include "kvq.h"
 #include "kvq_launch.h"
+#include "kvq_per_head_plan.h"
 
 namespace {
 
@@ -950,8 +951,11 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 1;
-  return kvq::per_head_default_splits(max_query_len, num_heads / num_kv_heads, num_kv_heads, head_size, batch_size,
-                                      max_seq_len, tree ? 0 : window, num_sinks, sms, use_workspace);
+  const kvq::PerHeadRanges r =
+      kvq::per_head_default_ranges(max_query_len, num_heads / num_kv_heads, num_kv_heads, head_size, batch_size,
+                                   max_seq_len, tree ? 0 : window, num_sinks, sms);
+  if (use_workspace != nullptr) *use_workspace = r.workspace;
+  return r.splits;
 }
 
 kvq_status kvq_window_attention_nvfp4_per_head(

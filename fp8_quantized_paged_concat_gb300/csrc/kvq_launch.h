@@ -234,13 +234,8 @@ struct PerHeadAttentionArgs {
   float* part_o;                  // fp32 [num_tokens, num_heads, num_splits, head_size], normalised
   float* part_lse;                // fp32 [num_tokens, num_heads, num_splits], base 2
 };
-int32_t per_head_default_splits(int64_t max_query_len, int64_t group, int64_t num_kv_heads, int32_t head_size,
-                                int64_t batch_size, int64_t max_seq_len, int64_t window, int64_t num_sinks, int sms,
-                                int32_t* use_workspace);
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, int sms, cudaStream_t stream);
-// Its kernel for many query rows per key head (without the join of ranges),
-// and the query rows of one of its CTAs.
-int64_t per_head_prefill_rows(int64_t rows, int32_t head_size);
+// Its kernel for many query rows per key head (without the join of ranges).
 cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream);
 
 struct CompactArgs {

@@ -42,6 +42,7 @@
 #include <type_traits>
 
 #include "kvq_per_head_attention.cuh"
+#include "kvq_per_head_plan.h"
 
 namespace kvq {
 namespace {
