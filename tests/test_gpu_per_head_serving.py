@@ -875,3 +875,99 @@ def test_a_workspace_that_the_default_ranges_do_not_need(kvq):
     mine = torch.zeros(kvq.kvq_per_head_attention_workspace_bytes(1, 8, 128, splits), dtype=torch.uint8, device=DEV)
     got, want = kvq.kvq_window_attention_nvfp4_per_head(**d, workspace=mine), kvq.kvq_window_attention_nvfp4_per_head(**d)
     assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.any(mine != 0)
+
+
+# --------------------------------------------------------------------------
+# a running maximum that grows
+# --------------------------------------------------------------------------
+
+GROWTH_SIGNS = (1.0, 1.0, 0.4, -1.0)           # of a key head's four query heads: two grow, one slowly, one falls
+
+
+def growing_batch(reqs, dim, layout, seed, unit, per_step):
+    """Four query heads on one key head whose scores rise with the position:
+    a key of 32-key step i has ones in per_step * i of its dimensions (each
+    worth `unit` in base two to the first two heads) and zeros elsewhere."""
+    b = Batch(reqs, 4, 1, dim, 16, layout, seed)
+    for r, length in enumerate(b.lens):
+        for p in range(length):
+            page, off = b.table[r, p // 16], p % 16
+            code = np.zeros(dim, np.uint8)
+            code[b.rng.permutation(dim)[:per_step * (p // 32)]] = 2              # e2m1 1.0
+            data, scales = b.cache.spans(off, 0)
+            b.cache.raw[0, page, 0, data] = code[0::2] | code[1::2] << 4
+            b.cache.raw[0, page, 0, scales] = 0x38                               # e4m3 1.0
+    c = unit / (np.log2(np.e) * b.scale * float(b.k_scale))
+    q = c * np.array(GROWTH_SIGNS)[None, :, None] * (1 + 0.05 * b.rng.standard_normal(b.q_bits.shape))
+    b.q_bits = ref.to_bf16(q)
+    return b
+
+
+def base_two_scores(b, token, head):
+    """The row's scores of the first request's keys up to its own position."""
+    ctx = b.reqs[0][0]
+    keys = np.stack([k for k, _ in ref.keys_of(b.cache, b.table[0], 0, range(ctx + token + 1))])
+    return (keys @ ref.bf16(b.q_bits)[token, head]) * (np.log2(np.e) * b.scale * float(b.k_scale))
+
+
+def growths(scores, steps):
+    """How often a reference maximum, taken from the first of `steps` (lists
+    of groups of keys), is exceeded by a group whose weights against it sum to
+    more than 2^8, each time taking the step's maximum; and the last such step."""
+    m, count, last = None, 0, 0
+    for i, groups in enumerate(steps):
+        top = max(scores[g].max() for g in groups)
+        if m is None:
+            m = top
+        elif max(np.exp2(scores[g] - m).sum() for g in groups) > 2.0 ** 8 * 1.05:
+            m, count, last = max(m, top), count + 1, i
+    return count, last
+
+
+@pytest.mark.parametrize("dim,layout", [(64, "NHD"), (128, "HND"), (256, "NHD")])
+@pytest.mark.parametrize("new", [20, 40])
+@pytest.mark.parametrize("splits", [1, -2])
+def test_many_rows_whose_maximum_grows(kvq, dim, layout, new, splits):
+    """80 and 160 rows per key head (one row tile and two, or two blocks at
+    head size 256), up to eight tiles of 64 keys of which nearly every one
+    exceeds the reference: O is rescaled again and again, and what it held
+    before still counts for a twentieth, so that one rescaling missed among a
+    request's last two is off by five tolerances or more."""
+    b = growing_batch([(470, new), (0, new), (95, new), (170, new), (240, new)], dim, layout, 111, 0.56, 4)
+    s = base_two_scores(b, 0, 0)
+    count, last = growths(s, [[np.arange(i, min(i + 64, len(s)))] for i in range(0, len(s), 64)])
+    assert count >= 5 and last >= 6
+    assert growths(base_two_scores(b, 0, 3), [[np.arange(i, i + 64)] for i in range(0, 448, 64)])[0] == 0
+    d = b.device()
+    check(kvq.kvq_window_attention_nvfp4_per_head(**(dict(d, num_splits=splits) if splits > 0 else
+                                                     through_workspace(kvq, d, -splits))), b.want())
+
+
+@pytest.mark.parametrize("dim,layout", [(64, "HND"), (128, "NHD"), (256, "HND")])
+@pytest.mark.parametrize("new", [1, 2])
+@pytest.mark.parametrize("splits", [1, 3, -2])
+def test_few_rows_whose_maximum_grows(kvq, dim, layout, new, splits):
+    """4 and 8 rows per key head: a warp takes every fourth step of 32 keys
+    and sums four keys of it per lane."""
+    b = growing_batch([(660, new), (0, new), (200, new), (330, new)], dim, layout, 112, 0.5417, 3)
+    s = base_two_scores(b, 0, 0)
+    own = [[np.arange(i + r, i + 32, 8) for r in range(8)] for i in range(0, 640, 128)]         # the first warp's steps
+    count, last = growths(s, own)
+    assert count >= 3 and last >= 3
+    d = b.device()
+    check(kvq.kvq_window_attention_nvfp4_per_head(**(dict(d, num_splits=splits) if splits > 0 else
+                                                     through_workspace(kvq, d, -splits))), b.want())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_blocks_of_16_rows_whose_maximum_grows(kvq, dim):
+    """480 requests on the same pages with the same four tokens: blocks of 16
+    rows fill the GPU.  Every request has the first one's bits."""
+    b = growing_batch([(660, 4)], dim, "NHD", 113, 0.5417, 3)
+    d, n = b.device(), 480
+    d.update(q=d["q"].repeat(n, 1, 1), query_start=torch.arange(0, 4 * n + 1, 4, dtype=torch.int32, device=DEV),
+             seq_lens=d["seq_lens"].repeat(n), block_table=d["block_table"].repeat(n, 1), num_splits=1)
+    out, lse = kvq.kvq_window_attention_nvfp4_per_head(**d)
+    check((out[:4], lse[:4]), b.want())
+    assert torch.equal(out.view(torch.int16), out[:4].view(torch.int16).repeat(n, 1, 1))
+    assert torch.equal(lse, lse[:4].repeat(n, 1))
