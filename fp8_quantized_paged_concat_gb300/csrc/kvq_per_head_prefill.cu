@@ -264,8 +264,11 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
         for (int j = 0; j < (D == 256 ? 2 : 1); ++j)
           cp_async<kPiece>(raw + at.raw[j] + i * kWarps * 8 * (D / 2), src + 16 * j, there ? kPiece : 0);
       }
-      // Which keys exist, for the softmax; a slot's last reader is long done
-      // (kRing chunks ahead of a tile whose buffers are free).
+      // Which keys exist, for the softmax.  A slot's last reader is done: with
+      // tile t under way here, kRing chunks ahead of it at most, tile t -
+      // kStages has left its buffer, so that its scores are formed, for which
+      // the weights of tile t - kStages - 2 had to leave theirs.
+      static_assert((S::kParts - 1 + S::kRing) / S::kParts + S::kStages + 2 <= kValidRing, "mask slots");
       if constexpr (!kValues) {
         if (lane < kPasses && me + kWarps * lane < kGroups)
           valid_ring[8 * ((h / S::kParts) % kValidRing) + (h % S::kParts) * kGroups + me + kWarps * lane] =

@@ -971,3 +971,19 @@ def test_blocks_of_16_rows_whose_maximum_grows(kvq, dim):
     check((out[:4], lse[:4]), b.want())
     assert torch.equal(out.view(torch.int16), out[:4].view(torch.int16).repeat(n, 1, 1))
     assert torch.equal(lse, lse[:4].repeat(n, 1))
+
+
+@pytest.mark.parametrize("dim,layout", [(64, "HND"), (128, "NHD"), (256, "NHD")])
+@pytest.mark.parametrize("new", [30, 40])
+def test_many_rows_over_more_tiles_than_mask_slots(kvq, dim, layout, new):
+    """One range of 24 tiles of 64 keys (their existence masks go round a
+    ring of 16 slots), with pages out of range behind position 1024 and a
+    table that ends inside the sequence."""
+    b = Batch([(1490, new), (1400, new)], 4, 1, dim, 16, layout, 114)
+    b.table[0, [3, 66, 67, 81]] = [-1, 10 ** 6, -5, b.cache.raw.shape[1]]
+    b.table[1, 70] = -1
+    b.table = np.ascontiguousarray(b.table[:, :89])         # 1424 positions
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = kvq.kvq_window_attention_nvfp4_per_head(**b.device(), num_splits=1, status=status)
+    assert int(status.item()) == kvq.STATUS_BAD_INDEX
+    check(got, b.want())
