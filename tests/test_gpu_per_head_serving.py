@@ -987,3 +987,17 @@ def test_many_rows_over_more_tiles_than_mask_slots(kvq, dim, layout, new):
     got = kvq.kvq_window_attention_nvfp4_per_head(**b.device(), num_splits=1, status=status)
     assert int(status.item()) == kvq.STATUS_BAD_INDEX
     check(got, b.want())
+
+
+@pytest.mark.parametrize("dim,heads,kv", [(64, 4, 2), (128, 8, 2), (256, 4, 1)])
+@pytest.mark.parametrize("new", [3, 40, 70])
+@pytest.mark.parametrize("splits", [1, -2])
+def test_tree_chain_has_the_windows_bits(kvq, dim, heads, kv, new, splits):
+    """A tree that is one chain sees the keys that plain causal attention
+    sees: both forms of mask give the same bits, in both kernels."""
+    b = Batch([(77, new), (10, new), (0, new), (300, new)], heads, kv, dim, 16, "NHD", 115)
+    rows = [[((2 << i) - 1) >> (64 * w) & (2 ** 64 - 1) for w in range(2)] for _, n in b.reqs for i in range(n)]
+    d = through_workspace(kvq, b.device(), -splits) if splits < 0 else dict(b.device(), num_splits=splits)
+    want = kvq.kvq_window_attention_nvfp4_per_head(**d)
+    got = kvq.kvq_tree_attention_nvfp4_per_head(**d, tree_mask=mask_dev(rows))
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
