@@ -10,11 +10,13 @@
 //
 // Bound: latency, of the chain from the request's lengths over its accepted
 // list and the block table to the entries (26 MB move in the largest measured
-// call).  So a CTA goes down that chain once, for one side and as many heads
-// of a request as its threads hold, and then moves several layers' entries:
-// a thread keeps kUnits units of kLayers layers in registers between its
-// loads, all issued together, and its stores.  64 requests x 32 layers of 8
-// heads: 13 us (one CTA per layer and head: 80 us).
+// call), once per wave of CTAs.  So a CTA goes down that chain once, for one
+// side and as many heads of a request as its threads hold, and then moves
+// several layers' entries: a thread keeps kUnits units of kLayers layers in
+// registers between its loads, all issued together, and its stores.  64
+// requests x 32 layers of 8 heads: 13 us, in 1408 CTAs of 3 layers, three of
+// which share an SM (74 registers a thread), so three waves (one CTA per layer
+// and head: 80 us).
 #include <algorithm>
 
 #include "kvq_dependent.cuh"
@@ -154,7 +156,8 @@ cudaError_t launch(const CompactArgs& a, int num_sms, cudaStream_t stream) {
   const int row_units = a.head_size / 2 / kDataBytes + groups / kScaleBytes;   // at most 192 (head_size <= 1024)
   const int heads = std::max(1, std::min(a.num_kv_heads, kThreads * kUnits / row_units));
   const int64_t chunks = (a.num_kv_heads + heads - 1) / heads;
-  // layers of a CTA: as many as leave about eight CTAs to an SM
+  // layers of a CTA: as many as leave about eight CTAs to each SM of the whole
+  // grid, of which three run at a time
   const int64_t ctas = static_cast<int64_t>(a.batch_size) * 2 * chunks * a.num_layers;
   const int per_cta = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ctas / (8 * num_sms))));
   const dim3 grid(static_cast<unsigned>(a.batch_size), static_cast<unsigned>(2 * chunks),

@@ -4,9 +4,10 @@
 // Every thread of such a kernel calls wait_for_previous() before its first
 // access to memory (tensor memory among it, which a CTA before it may still
 // have to take), on every path: so a kernel ends after the one before it, and
-// what a stream orders stays ordered along a chain of them.  Measured, calls
-// queued: a single-token attention 10.2 -> 7.5 us, a compaction of one layer
-// 4.1 -> 3.1, of 32 layers 16.4 -> 13.9, a tree of one user 20.5 -> 19.0.
+// what a stream orders stays ordered along a chain of them.  Measured, the
+// same call queued from Python over and over: a single-token attention 8.2 ->
+// 7.0 us, a compaction of one layer 6.2 -> 3.4, of 32 layers 15.1 -> 13.1, a
+// tree of one user 20.5 -> 16.3; in a graph 0 to 0.4 us less.
 #pragma once
 
 #include <cstdint>
@@ -30,8 +31,9 @@ __device__ __forceinline__ T load_global(const T* p) {
 }
 // The same, opaque, where registers are short: plain loads of an unrolled loop
 // are merged and held (mask words in the few-row attention's blocks of 16
-// rows: spills, calls 2 to 4 % slower; its blocks of 8 have the registers, and
-// a single-token call takes 7.1 us with plain loads, 7.4 with opaque ones).
+// rows at head size 128: 80 bytes of spill loads a thread, 28 with opaque ones;
+// 128 requests x 2048 keys 99.7 against 96.1 us, as trees 103 against 96; its
+// blocks of 8 take the same time either way).
 __device__ __forceinline__ uint64_t load_global64(const uint64_t* p) {
   uint64_t v;
   asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));

@@ -159,10 +159,10 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
 template <int kLanes>
 cudaError_t launch_heads(const NormRopeArgs& a, int num_sms, cudaStream_t stream) {
   // Eight heads per lane group share one table row and one set of weights and
-  // keep eight loads in flight (head size 128, 32 + 8 heads: 16384 tokens 57
-  // us, with four heads 70, two 85, one 115); a call that gives the SMs less
-  // than one CTA each that way takes one head per group (64 tokens: 6.8
-  // against 8.8 us; at 256 tokens the two are equal).
+  // keep eight loads in flight (head size 128, 32 + 8 heads, in a graph: 16384
+  // tokens 54 us, with four heads 61, two 75, one 102); a call that gives the
+  // SMs less than one CTA each that way takes one head per group (64 tokens:
+  // 1.8 against 2.6 us; 256 tokens 2.7 against 2.9; 1024 tokens 6.9 against 4.9).
   const int64_t chunks = (a.num_heads + kManyHeads - 1) / kManyHeads + (a.num_kv_heads + kManyHeads - 1) / kManyHeads;
   return a.num_tokens * chunks * kLanes >= static_cast<int64_t>(num_sms) * kThreads
              ? launch<kLanes, kManyHeads>(a, stream)

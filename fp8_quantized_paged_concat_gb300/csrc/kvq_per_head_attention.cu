@@ -17,8 +17,9 @@
 // key head.  Each warp takes every fourth step of 32 keys, with its own
 // running maximum and sum, and the warps join at the end through shared
 // memory; the ranges of a small call run as a cluster and join through its
-// distributed shared memory (one request, window of 1024, 64 heads: 7.1 us;
-// a second launch costs about 4 more), others in a second launch.  A warp
+// distributed shared memory (one request, window of 1024, 64 heads: 7.1 us,
+// 7.6 through a workspace and a second launch, 10.4 unsplit), others in a
+// second launch.  A warp
 // copies a step's raw bytes
 // (32 entries of 9 D / 16 bytes, K and V) into its own two-stage ring with
 // asynchronous copies, a step ahead, so that nothing but the warp's own
@@ -40,7 +41,12 @@
 // value to [2^14, 2^15): bf16's 8 bits stay exact in f16 down to 2^-28 of
 // that largest value, and what is lost below is under 2^-39 of it.  The
 // weights are kept as 2^(s - m + 6) with m at most 2^8 behind the true
-// maximum (so <= 2^14) and rounded to f16 (relative 2^-11).
+// maximum (so <= 2^14) and rounded to f16 (relative 2^-11), the type that the
+// matrix instruction takes beside the entries' own: fp32 operands would go
+// through tf32 at half the rate with no more mantissa, bf16 would lose eight
+// times as much, and the result's bf16 rounding (2^-8) hides it (the measured
+// cases' error against 64 bits is 0.00167 of the largest value with it, 0.00166
+// in fp32).  Their sum is taken before the rounding, in fp32.
 //
 // Measured: 128 requests x 4100 keys x 32 heads (8 key heads) of 128, 606 MB:
 // 115 us, 5.3 TB/s; about 640 warp instructions per step of 32 keys for 4
@@ -698,9 +704,9 @@ template <int D>
 cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
   const int64_t join = static_cast<int64_t>(a.max_query_len) * a.num_heads;
   const dim3 grid(static_cast<unsigned>((join + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(a.batch_size));
-  // as many ranges in flight as a row has, up to 16 (one user's tree in 19
-  // ranges: 16.3 us, eight in flight 17.4), but no more: they cost registers,
-  // and calls of few ranges have many rows (trees 32 x 64 in 4: 574 us, 595)
+  // as many ranges in flight as a row has, up to 16 (one user's tree in 16
+  // ranges: 16.3 us, eight in flight 17.0), but no more: they cost registers,
+  // and calls of few ranges have many rows (trees 32 x 64 in 4: 500 us, 523)
   return launch_dependent(a.num_splits <= 4 ? per_head_join_kernel<D, 4> : per_head_join_kernel<D, D == 256 ? 8 : 16>, grid,
                           kJoinWarps * 32, 0, 1, stream, a);
 }

@@ -37,8 +37,11 @@
 // on an SM quarter (512 by the exponentials' rate alone, 530 when nothing else
 // runs there), the rest for loads, stores and waits.  Making the two row
 // tiles take turns at it cost more (1115 us) than the contention (943 then).
-// Every wait is bounded; on expiry the CTA records KVQ_STATUS_TIMEOUT, drains
-// its products, frees its tensor memory and leaves its rows unwritten.
+// Every wait of a role on another role or on its products is bounded; on
+// expiry the CTA records KVQ_STATUS_TIMEOUT, drains its products, frees its
+// tensor memory and leaves its rows unwritten.  (The set-up waits otherwise:
+// for the kernel before, at the block's barrier, which every thread reaches,
+// and for tensor memory, which whoever holds it gives back without this CTA.)
 #include <type_traits>
 
 #include "kvq_per_head_attention.cuh"

@@ -324,9 +324,13 @@ __device__ __forceinline__ void prefetch_l2_line(const void* addr) {
   asm volatile("prefetch.global.L2 [%0];" :: "l"(addr) : "memory");
 }
 
-// 2^x for x <= 0 (0 for -inf): the hardware approximation, relative error
-// below 2^-22, flushed to zero below 2^-126 (weights that small vanish next
-// to the largest weight, which is at least 2^-8).
+// 2^x (0 for -inf, infinite from x = 128 on): the hardware approximation,
+// relative error below 2^-22, flushed to zero below 2^-126.  As a weight of a
+// softmax: x <= 0 in the attention over latent entries, x <= 14 over the
+// per-head cache once a reference maximum stands; there a pass whose
+// reference has fallen behind may see larger x, infinities among the results,
+// and is repeated with a new one.  A row's largest weight is at least 2^-8, so
+// those that are flushed vanish next to it.
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

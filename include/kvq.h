@@ -642,9 +642,11 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
  * finite in fp32.  query_start: int32 [batch_size + 1], the requests' ranges
  * disjoint; seq_lens: int32 [batch_size]; batch_size <= 65535.
  * Calls of few query rows per request and key head run on the warps' matrix
- * instructions and wait for nothing but their own copies; the others run on
- * tensor memory with bounded waits, on whose expiry the rows concerned stay
- * unwritten (KVQ_STATUS_TIMEOUT).
+ * instructions and wait for their own copies, at their blocks' barriers and,
+ * where their ranges run as a cluster, at its barrier, which all of its blocks
+ * reach; the others run on tensor memory with bounded waits of its warps on one
+ * another, on whose expiry the rows concerned stay unwritten
+ * (KVQ_STATUS_TIMEOUT).
  * num_splits: key ranges per block of query rows (1 ..
  * KVQ_PER_HEAD_MAX_SPLITS), for calls with too few rows to fill the GPU.  With
  * workspace = NULL (at most KVQ_PER_HEAD_CLUSTER_SPLITS ranges, and
