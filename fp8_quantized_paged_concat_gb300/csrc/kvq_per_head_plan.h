@@ -115,7 +115,10 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
       n = ranges(4);
       if (few_rows(rows, groups, head_size, n, sms) != 16) block = 8;
     }
-    if (block != 16) n = ranges(few == (blocks() >= places()) ? (few ? 2 : 3) : 6);
+    if (block != 16) {
+      const bool many = blocks() >= places();
+      n = ranges(few ? (many ? 2 : 6) : (many ? 6 : 3));
+    }
   } else {
     // As many as the call is short of CTAs, of at least 256 keys in the tensor
     // memory kernel.  In the few-row kernel a range costs keys / n steps and the
