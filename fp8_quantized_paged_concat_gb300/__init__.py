@@ -35,6 +35,7 @@ __all__ = [
     "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
     "kvq_per_head_attention_default_splits",
     "PER_HEAD_MAX_SPLITS", "PER_HEAD_CLUSTER_SPLITS",
+    "kvq_rope_append_fp8_per_head", "FP8_SCALE_BIAS",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -50,6 +51,7 @@ ATTN_MAX_SPLITS = 32
 NOALLOC_SCRATCH_BYTES = 24 << 20
 PER_HEAD_MAX_SPLITS = 128
 PER_HEAD_CLUSTER_SPLITS = 8
+FP8_SCALE_BIAS = 127
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -110,6 +112,9 @@ _SIGNATURES = {
     "kvq_tree_attention_nvfp4_per_head": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _I64,
                                           _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, ctypes.c_float, _P, _I64,
                                           _I64, _P, _I64, _I32, _I32, _P, _I64, _P, _P],
+    "kvq_rope_append_fp8_per_head": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64,
+                                     _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _I64, _I32, _I32, _P,
+                                     _I64, _I64, _P, _I64, _I64, _P, _P],
     "kvq_compact_drafts_nvfp4_per_head": [_P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
                                           _I32, _P, _I64, _I32, _P, _P],
 }
@@ -587,8 +592,8 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 
 _native = None
 _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
-                   "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
-                   "kvq_per_head_attention_default_splits", "kvq_last_error_string")
+                   "kvq_compact_drafts_nvfp4_per_head", "kvq_rope_append_fp8_per_head",
+                   "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
 
 
 def _load_native():
@@ -688,6 +693,29 @@ def kvq_compact_drafts_nvfp4_per_head(kv_cache, query_start, seq_lens, accepted,
     contiguous).  seq_lens is left to the caller."""
     (_native or _load_native()).compact(kv_cache, query_start, seq_lens, accepted, accepted_lens, block_table, layout,
                                         status, stream)
+
+
+# --------------------------------------------------------------------------
+# serving from the per-head e4m3 cache
+# --------------------------------------------------------------------------
+
+def kvq_rope_append_fp8_per_head(q, k, v, positions, cos_sin, query_start, seq_lens, block_table, kv_cache, kv_scales,
+                                 max_query_len: int, interleaved=False, layout="NHD", q_out=None, k_out=None, status=None,
+                                 stream=None):
+    """Rotates the queries q bf16 [T, H, D] and keys k bf16 [T, KH, D] of new
+    tokens by positions int64 [T] (cos_sin and interleaved as in
+    kvq_qk_norm_rope) and appends keys and values v bf16 [T, KH, D] to the
+    per-head e4m3 cache: kv_cache uint8 [P, 2, block_size, KH, D] (layout
+    "NHD") or [P, 2, KH, block_size, D] ("HND"), with the scale 2^(x -
+    FP8_SCALE_BIAS) of each page, side and head in kv_scales uint8 [P, 2, KH],
+    which grows with what the page holds.  Request b's tokens [query_start[b],
+    query_start[b+1]) (int32 [B+1], at most max_query_len each) become the
+    last positions of its seq_lens[b] entries (int32 [B], the new ones among
+    them) in the pages of block_table int32 [B, W].  q may be None.  q_out /
+    k_out may be q / k; k_out=False leaves the rotated keys out.  Returns
+    (q_out, k_out), None for what is left out."""
+    return (_native or _load_native()).append(q, k, v, positions, cos_sin, query_start, seq_lens, block_table, kv_cache,
+                                              kv_scales, max_query_len, interleaved, layout, q_out, k_out, status, stream)
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

@@ -791,6 +791,18 @@ kvq_status check_per_head_cache(const char* fn, const void* cache, int64_t num_p
   return KVQ_OK;
 }
 
+// The same for the e4m3 cache and its scales.
+kvq_status check_fp8_cache(const char* fn, const void* cache, const void* scales, int64_t num_pages, int32_t block_size,
+                           int32_t layout, int32_t num_kv_heads, int32_t head_size, int64_t* region) {
+  if (kvq_status s = check_per_head_cache(fn, cache, num_pages, block_size, layout, num_kv_heads, head_size, region))
+    return s;
+  *region = int64_t{block_size} * num_kv_heads * head_size;
+  KVQ_REQUIRE(*region < (int64_t{1} << 31), "%s: block_size * num_kv_heads * head_size must stay below 2^31 (got %lld)",
+              fn, static_cast<long long>(*region));
+  KVQ_REQUIRE(scales != nullptr, "%s: kv_scales must be non-NULL", fn);
+  return KVQ_OK;
+}
+
 kvq_status check_table(const char* fn, const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size,
                        const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width) {
   KVQ_REQUIRE(batch_size <= 65535, "%s: batch_size must be at most 65535", fn);
@@ -1070,6 +1082,98 @@ kvq_status kvq_compact_drafts_nvfp4_per_head(
                            block_table_stride, block_table_width,
                            kvq::FastDiv::make(static_cast<uint32_t>(block_size)), d_status};
   return launched(fn, kvq::launch_compact_drafts(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_rope_append_fp8_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h, const int64_t* positions, int64_t num_tokens,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_size, const float* cos_sin, int64_t cos_sin_stride,
+    int64_t max_position, int32_t rot_dim, int32_t interleaved, const int32_t* query_start, const int32_t* seq_lens,
+    int32_t batch_size, int32_t max_query_len, const int32_t* block_table, int64_t block_table_stride,
+    int32_t block_table_width, uint8_t* kv_cache, uint8_t* kv_scales, int64_t num_pages, int32_t block_size,
+    int32_t layout, void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t,
+    int64_t k_out_stride_h, int32_t* d_status, kvq_stream_t stream) {
+  const char* fn = "kvq_rope_append_fp8_per_head";
+  KVQ_REQUIRE(num_tokens >= 0 && batch_size >= 0 && max_query_len >= 0,
+              "%s: num_tokens, batch_size and max_query_len must be >= 0", fn);
+  if (num_tokens == 0 || batch_size == 0 || max_query_len == 0) return ok();
+  KVQ_REQUIRE(head_size == 64 || head_size == 128 || head_size == 256,
+              "%s: head_size must be 64, 128 or 256 (got %d)", fn, head_size);
+  KVQ_REQUIRE(num_kv_heads > 0 && (q == nullptr || num_heads > 0),
+              "%s: num_kv_heads and, with q, num_heads must be positive", fn);
+  KVQ_REQUIRE(rot_dim >= 0 && rot_dim <= head_size && rot_dim % 16 == 0,
+              "%s: rot_dim must be a multiple of 16 in [0, head_size] (got %d)", fn, rot_dim);
+  KVQ_REQUIRE(num_tokens < (int64_t{1} << 31) &&
+                  int64_t{max_query_len} * (int64_t{num_kv_heads} * 4 + (q == nullptr ? 0 : num_heads)) < (int64_t{1} << 31),
+              "%s: num_tokens and max_query_len * (num_heads + 4 * num_kv_heads) must stay below 2^31", fn);
+  int64_t region = 0;
+  if (kvq_status s = check_fp8_cache(fn, kv_cache, kv_scales, num_pages, block_size, layout, num_kv_heads, head_size,
+                                     &region))
+    return s;
+  if (q != nullptr) {
+    if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
+    if (kvq_status s = check_heads(fn, "q_out", q_out, q_out_stride_t, q_out_stride_h, num_heads, head_size, true))
+      return s;
+  }
+  if (kvq_status s = check_heads(fn, "k", k, k_stride_t, k_stride_h, num_kv_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "v", v, v_stride_t, v_stride_h, num_kv_heads, head_size, false)) return s;
+  if (k_out != nullptr)
+    if (kvq_status s = check_heads(fn, "k_out", k_out, k_out_stride_t, k_out_stride_h, num_kv_heads, head_size, true))
+      return s;
+  KVQ_REQUIRE(positions != nullptr && aligned(positions, 8), "%s: bad positions", fn);
+  KVQ_REQUIRE(max_position > 0, "%s: max_position must be positive", fn);
+  KVQ_REQUIRE(rot_dim == 0 || (cos_sin != nullptr && aligned(cos_sin, 16) && cos_sin_stride >= rot_dim &&
+                               cos_sin_stride % 4 == 0),
+              "%s: cos_sin must be 16-byte aligned with row stride >= rot_dim, a multiple of 4", fn);
+  if (kvq_status s = check_table(fn, query_start, seq_lens, batch_size, block_table, block_table_stride,
+                                 block_table_width))
+    return s;
+  KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
+  int num_sms = 0;
+  if (kvq_status s = check_device(fn, &num_sms)) return s;
+  kvq::AppendArgs a{};
+  a.q = q;
+  a.q_stride_t = q_stride_t;
+  a.q_stride_h = q_stride_h;
+  a.k = k;
+  a.k_stride_t = k_stride_t;
+  a.k_stride_h = k_stride_h;
+  a.v = v;
+  a.v_stride_t = v_stride_t;
+  a.v_stride_h = v_stride_h;
+  a.positions = positions;
+  a.num_tokens = num_tokens;
+  a.num_heads = q == nullptr ? 0 : num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_size = head_size;
+  a.cos_sin = cos_sin;
+  a.cos_sin_stride = cos_sin_stride;
+  a.max_position = max_position;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.query_start = query_start;
+  a.seq_lens = seq_lens;
+  a.batch_size = batch_size;
+  a.max_query_len = max_query_len;
+  a.block_table = block_table;
+  a.block_table_stride = block_table_stride;
+  a.block_table_width = block_table_width;
+  a.cache = kv_cache;
+  a.scales = kv_scales;
+  a.num_pages = num_pages;
+  a.block_size = block_size;
+  a.block_div = kvq::FastDiv::make(static_cast<uint32_t>(block_size));
+  a.region = static_cast<uint32_t>(region);
+  a.row_offset = layout == KVQ_LAYOUT_HND ? 1 : num_kv_heads;
+  a.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
+  a.q_out = q_out;
+  a.q_out_stride_t = q_out_stride_t;
+  a.q_out_stride_h = q_out_stride_h;
+  a.k_out = k_out;
+  a.k_out_stride_t = k_out_stride_t;
+  a.k_out_stride_h = k_out_stride_h;
+  a.status = d_status;
+  return launched(fn, kvq::launch_rope_append(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char* kvq_last_error_string(void) { return g_last_error.c_str(); }

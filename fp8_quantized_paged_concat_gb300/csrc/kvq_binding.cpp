@@ -1,5 +1,5 @@
 // kvq_binding.cpp -- the Python side of the calls that serve a model from the
-// per-head NVFP4 cache, as a CPython extension: it checks the torch tensors
+// per-head caches, as a CPython extension: it checks the torch tensors
 // (types, devices, shapes), allocates what the caller left out, and calls the
 // C entry point on the tensors' device and the current stream.  These calls
 // run once per layer and decoded token, where the same checks in Python take
@@ -37,6 +37,7 @@ struct Library {
   decltype(&kvq_window_attention_nvfp4_per_head) window = nullptr;
   decltype(&kvq_tree_attention_nvfp4_per_head) tree = nullptr;
   decltype(&kvq_compact_drafts_nvfp4_per_head) compact = nullptr;
+  decltype(&kvq_rope_append_fp8_per_head) append = nullptr;
   decltype(&kvq_per_head_attention_workspace_bytes) workspace_bytes = nullptr;
   decltype(&kvq_per_head_attention_default_splits) default_splits = nullptr;
   decltype(&kvq_last_error_string) last_error = nullptr;
@@ -169,11 +170,15 @@ class Scope {
 struct CacheShape {
   int32_t layout, block_size, heads, head_size;
 };
-// A contiguous per-head cache (its last five dimensions, from `from` on).
-CacheShape cache_shape(const at::Tensor& cache, int64_t from, PyObject* layout, int64_t head_size) {
+bool is_nhd(PyObject* layout) {
   const bool nhd = PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "NHD") == 0;
   if (!nhd && !(PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "HND") == 0))
     bad("layout: expected one of ['HND', 'NHD']");
+  return nhd;
+}
+// A contiguous per-head cache (its last five dimensions, from `from` on).
+CacheShape cache_shape(const at::Tensor& cache, int64_t from, PyObject* layout, int64_t head_size) {
+  const bool nhd = is_nhd(layout);
   const auto s = cache.sizes().slice(from), st = cache.strides().slice(from);
   bool contiguous = true;
   int64_t expect = 1;
@@ -188,6 +193,31 @@ CacheShape cache_shape(const at::Tensor& cache, int64_t from, PyObject* layout, 
         ", D/2 + D/16] tensor" + (head_size >= 0 ? " with D = " + std::to_string(head_size) : std::string()) + ", got " +
         shape_text(cache.sizes()));
   return {nhd ? 0 : 1, static_cast<int32_t>(block), static_cast<int32_t>(heads), static_cast<int32_t>(full / 9 * 16)};
+}
+
+bool contiguous(const at::Tensor& t) {
+  int64_t expect = 1;
+  for (int64_t i = t.dim() - 1; i >= 0; --i) {
+    if (t.size(i) > 1 && t.stride(i) != expect) return false;
+    expect *= t.size(i);
+  }
+  return true;
+}
+// A contiguous per-head e4m3 cache of `heads` heads (-1: any) of head_size, and its scales.
+CacheShape fp8_cache_shape(const at::Tensor& cache, const at::Tensor& scales, PyObject* layout, int64_t heads,
+                           int64_t head_size, int dev) {
+  const bool nhd = is_nhd(layout);
+  check("kv_cache", cache, at::kByte, dev, 5);
+  const int64_t block = cache.size(nhd ? 2 : 3), kv = cache.size(nhd ? 3 : 2);
+  if (cache.size(1) != 2 || cache.size(4) != head_size || !contiguous(cache) || block > INT32_MAX || kv > INT32_MAX ||
+      (heads >= 0 && kv != heads))
+    bad(std::string("kv_cache: expected a contiguous [P, 2, ") + (nhd ? "block_size, H" : "H, block_size") +
+        ", D] tensor with D = " + std::to_string(head_size) + (heads >= 0 ? ", H = " + std::to_string(heads) : "") +
+        ", got " + shape_text(cache.sizes()));
+  check("kv_scales", scales, at::kByte, dev, 3);
+  shaped("kv_scales", scales, {cache.size(0), 2, kv});
+  if (!contiguous(scales)) bad("kv_scales: expected a contiguous tensor");
+  return {nhd ? 0 : 1, static_cast<int32_t>(block), static_cast<int32_t>(kv), static_cast<int32_t>(head_size)};
 }
 
 void must(kvq_status status, const char* name) {
@@ -231,9 +261,10 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F body) {
   return nullptr;
 }
 
+// (a, b); None where a tensor is missing.
 PyObject* pair(const at::Tensor& a, const at::Tensor* b) {
-  PyObject* x = THPVariable_Wrap(a);
-  PyObject* y = b != nullptr ? THPVariable_Wrap(*b) : Py_NewRef(Py_None);
+  PyObject* x = a.defined() ? THPVariable_Wrap(a) : Py_NewRef(Py_None);
+  PyObject* y = b != nullptr && b->defined() ? THPVariable_Wrap(*b) : Py_NewRef(Py_None);
   if (x == nullptr || y == nullptr) {
     Py_XDECREF(x);
     Py_XDECREF(y);
@@ -414,6 +445,73 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// q (None: keys and values only), k, v, positions, cos_sin, query_start, seq_lens, block_table, kv_cache, kv_scales,
+// max_query_len, interleaved, layout, q_out, k_out (False: none), status, stream
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const at::Tensor& k = tensor("k", a[1]);
+    const int dev = device_of("k", k);
+    check("k", k, at::kBFloat16, dev, 3);
+    const int64_t T = k.size(0), KH = k.size(1), D = k.size(2);
+    const at::Tensor& v = tensor("v", a[2]);
+    check("v", v, at::kBFloat16, dev, 3);
+    shaped("v", v, {T, KH, D});
+    at::Tensor q;
+    if (a[0] != Py_None) {
+      q = tensor("q", a[0]);
+      check("q", q, at::kBFloat16, dev, 3);
+      shaped("q", q, {T, q.size(1), D});
+    }
+    const int64_t H = q.defined() ? q.size(1) : 0;
+    const at::Tensor& pos = tensor("positions", a[3]);
+    check("positions", pos, at::kLong, dev, 1);
+    shaped("positions", pos, {T});
+    const at::Tensor& turns = tensor("cos_sin", a[4]);
+    check("cos_sin", turns, at::kFloat, dev, 2);
+    const at::Tensor &start = tensor("query_start", a[5]), &lens = tensor("seq_lens", a[6]);
+    check("seq_lens", lens, at::kInt, dev, 1);
+    const int64_t B = lens.size(0);
+    check("query_start", start, at::kInt, dev, 1);
+    shaped("query_start", start, {B + 1});
+    const at::Tensor& table = tensor("block_table", a[7]);
+    check("block_table", table, at::kInt, dev, 2);
+    shaped("block_table", table, {B, table.size(1)});
+    const at::Tensor &cache = tensor("kv_cache", a[8]), &scales = tensor("kv_scales", a[9]);
+    const CacheShape c = fp8_cache_shape(cache, scales, a[12], KH, D, dev);
+    const int32_t max_query = int32("max_query_len", a[10]);
+    const int interleaved = PyObject_IsTrue(a[11]);
+    if (interleaved < 0) pending();
+    const Scope scope(a[16], dev);
+    at::Tensor qo, ko;
+    Strides sq{}, sqo{}, sko{};
+    if (q.defined()) {
+      qo = a[13] == Py_None ? scope.result({T, H, D}, at::kBFloat16) : tensor("q_out", a[13]);
+      check("q_out", qo, at::kBFloat16, dev, 3);
+      shaped("q_out", qo, {T, H, D});
+      sq = head_strides(q);
+      sqo = head_strides(qo);
+    }
+    if (a[14] != Py_False) {
+      ko = a[14] == Py_None ? scope.result({T, KH, D}, at::kBFloat16) : tensor("k_out", a[14]);
+      check("k_out", ko, at::kBFloat16, dev, 3);
+      shaped("k_out", ko, {T, KH, D});
+      sko = head_strides(ko);
+    }
+    const Strides sk = head_strides(k), sv = head_strides(v);
+    must(lib.append(q.defined() ? q.data_ptr() : nullptr, sq.t, sq.h, k.data_ptr(), sk.t, sk.h, v.data_ptr(), sv.t, sv.h,
+                    static_cast<const int64_t*>(pos.data_ptr()), T, dim(H), dim(KH), dim(D),
+                    static_cast<const float*>(turns.data_ptr()), row_stride(turns), turns.size(0), dim(turns.size(1)),
+                    interleaved, static_cast<const int32_t*>(start.data_ptr()),
+                    static_cast<const int32_t*>(lens.data_ptr()), dim(B), max_query,
+                    static_cast<const int32_t*>(table.data_ptr()), row_stride(table), dim(table.size(1)),
+                    static_cast<uint8_t*>(cache.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()), cache.size(0),
+                    c.block_size, c.layout, qo.defined() ? qo.data_ptr() : nullptr, sqo.t, sqo.h,
+                    ko.defined() ? ko.data_ptr() : nullptr, sko.t, sko.h, status_word(a[15], dev), scope.stream()),
+         "kvq_rope_append_fp8_per_head");
+    return pair(qo, &ko);
+  });
+}
+
 // bind({entry point: address}): the library whose entry points the calls use
 PyObject* bind(PyObject*, PyObject* table) {
   Library found;
@@ -428,6 +526,7 @@ PyObject* bind(PyObject*, PyObject* table) {
   if (!set("kvq_qk_norm_rope", found.qk_norm_rope) || !set("kvq_window_attention_nvfp4_per_head", found.window) ||
       !set("kvq_tree_attention_nvfp4_per_head", found.tree) ||
       !set("kvq_compact_drafts_nvfp4_per_head", found.compact) ||
+      !set("kvq_rope_append_fp8_per_head", found.append) ||
       !set("kvq_per_head_attention_workspace_bytes", found.workspace_bytes) ||
       !set("kvq_per_head_attention_default_splits", found.default_splits) ||
       !set("kvq_last_error_string", found.last_error))
@@ -441,6 +540,7 @@ PyMethodDef methods[] = {
     {"norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_rope)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attention)), METH_FASTCALL, nullptr},
     {"compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(compact)), METH_FASTCALL, nullptr},
+    {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kvq_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

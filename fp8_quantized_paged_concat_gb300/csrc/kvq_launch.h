@@ -238,6 +238,46 @@ cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, int sms, cu
 // Its kernel for many query rows per key head (without the join of ranges).
 cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream);
 
+// The new tokens of every request, rotated and appended to the per-head e4m3
+// cache: request b's tokens [query_start[b], query_start[b+1]) become the last
+// positions of its sequence [0, seq_lens[b]).
+struct AppendArgs {
+  const void* q;                  // bf16 [num_tokens, num_heads, head_size], or nullptr: keys and values only
+  int64_t q_stride_t, q_stride_h;
+  const void* k;                  // bf16 [num_tokens, num_kv_heads, head_size]
+  int64_t k_stride_t, k_stride_h;
+  const void* v;
+  int64_t v_stride_t, v_stride_h;
+  const int64_t* positions;       // of the rotation
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads, head_size;
+  const float* cos_sin;           // fp32 [max_position, rot_dim]: cosines, then sines
+  int64_t cos_sin_stride;
+  int64_t max_position;
+  int32_t rot_dim;
+  int32_t interleaved;
+  const int32_t* query_start;     // [batch_size + 1]
+  const int32_t* seq_lens;        // [batch_size]
+  int32_t batch_size;
+  int32_t max_query_len;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  int32_t block_table_width;
+  uint8_t* cache;
+  uint8_t* scales;                // [num_pages, 2, num_kv_heads]
+  int64_t num_pages;
+  int32_t block_size;
+  FastDiv block_div;
+  uint32_t region;                // bytes of one (page, side), < 2^31: K at 2 * page * region, V one region on
+  int32_t row_offset, row_head;   // row of (offset, head) = offset * row_offset + head * row_head
+  void* q_out;
+  int64_t q_out_stride_t, q_out_stride_h;
+  void* k_out;                    // rotated keys, or nullptr
+  int64_t k_out_stride_t, k_out_stride_h;
+  int32_t* status;
+};
+cudaError_t launch_rope_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
+
 struct CompactArgs {
   uint8_t* cache;
   int32_t num_layers;

@@ -728,6 +728,82 @@ kvq_status kvq_compact_drafts_nvfp4_per_head(
     const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
     int32_t* d_status, kvq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving a model from a per-head e4m3 cache, with a scale for each page,
+ * side and head: the append of new tokens, with the rotation on the way, and
+ * the attention that reads the cache; and the attention over whole prompts,
+ * whose keys and values are still at hand as they were computed.  A step of
+ * a batch appends its tokens, then attends.  (No passage of the pages: they
+ * have e4m3 entries for the latent cache only.)
+ *
+ * kv_cache: contiguous uint8 [num_pages, 2, block_size, num_kv_heads,
+ * head_size] (layout KVQ_LAYOUT_NHD) or [num_pages, 2, num_kv_heads,
+ * block_size, head_size] (KVQ_LAYOUT_HND) of e4m3 codes, K on side 0 and V on
+ * side 1.  kv_scales: contiguous uint8 [num_pages, 2, num_kv_heads]: byte x
+ * is the scale 2^e, e = x - KVQ_FP8_SCALE_BIAS (the E8M0 format of OCP MX
+ * v1.0); an e outside [KVQ_FP8_SCALE_MIN_EXP, KVQ_FP8_SCALE_MAX_EXP], which
+ * no call writes, is read as the nearer of the two.  An entry's value is
+ * e4m3 * 2^e.
+ * ------------------------------------------------------------------------ */
+#define KVQ_FP8_SCALE_BIAS     127
+#define KVQ_FP8_SCALE_MIN_EXP  (-60)
+#define KVQ_FP8_SCALE_MAX_EXP  60
+
+/*
+ * kvq_rope_append_fp8_per_head -- rotates the queries and keys of the
+ * requests' new tokens and appends keys and values to the cache.
+ * Request b < batch_size owns the tokens [query_start[b], query_start[b+1])
+ * (n of them, at most max_query_len), which become the last n positions of
+ * its sequence of seq_lens[b] entries: token i gets position seq_lens[b] - n
+ * + i, entry j % block_size of page block_table[b * block_table_stride + j /
+ * block_size] for position j.  For a pair (a, b) of a query or key head,
+ * dimensions (j, j + rot_dim / 2), or (2j, 2j + 1) when `interleaved`, j <
+ * rot_dim / 2:
+ *   (a, b) -> (a c - b s, b c + a s),  c = cos_sin[p][j], s = cos_sin[p][rot_dim / 2 + j],
+ *   p = positions[token],
+ * each product and each sum rounded to fp32; dimensions from rot_dim on stay.
+ * Then, for each page that gets entries, side and head, with A the largest
+ * magnitude of its new entries (a NaN counts for nothing):
+ *   e = the least integer with A <= 448 * 2^e, in [-60, 60] (-60 for A = 0);
+ *   a page that starts with the request's new tokens takes e as its scale,
+ *   whatever it held before; one that holds entries before them takes the
+ *   larger of e and its own, and where that grows the codes of those entries
+ *   become e4m3_rn(value * 2^-e) (exact but for what falls below 2^-6);
+ *   code = e4m3_rn_sat(y * 2^-e) of each new value y (NaN stays NaN).
+ * Entries behind the sequence are never touched.
+ * q_out, k_out: the rotated queries and keys, rounded to bf16; q may be NULL
+ * (q_out then unused), and k_out NULL (not wanted).
+ * A token whose rotation position is outside [0, max_position) is skipped:
+ * no output, its entry as it was (KVQ_STATUS_BAD_INDEX).  A page whose column
+ * is >= block_table_width or whose id is outside [0, num_pages) gets nothing
+ * (KVQ_STATUS_BAD_INDEX); k_out is written all the same.  A request whose
+ * token range is not inside [0, num_tokens), is longer than max_query_len or
+ * than its sequence is skipped, its rows untouched (KVQ_STATUS_BAD_BATCH), as
+ * are rows of no request.  No two requests of a call append to the same page.
+ * q, q_out: bf16 [num_tokens, num_heads, head_size]; k, v, k_out: bf16
+ * [num_tokens, num_kv_heads, head_size]; token and head strides in elements
+ * (multiples of 8).  q_out may be q and k_out may be k (same pointer and
+ * strides); any other overlap of outputs with inputs is not allowed.
+ * head_size: 64, 128 or 256; rot_dim: a multiple of 16 in [0, head_size].
+ * cos_sin: fp32 [max_position, >= rot_dim], 16-byte aligned, row stride a
+ * multiple of 4.  positions: int64 [num_tokens].  query_start: int32
+ * [batch_size + 1], the requests' ranges disjoint; seq_lens: int32
+ * [batch_size]; batch_size <= 65535.
+ */
+kvq_status kvq_rope_append_fp8_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h,
+    const int64_t* positions, int64_t num_tokens,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+    const float* cos_sin, int64_t cos_sin_stride, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    uint8_t* kv_cache, uint8_t* kv_scales, int64_t num_pages, int32_t block_size, int32_t layout,
+    void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+    void* k_out, int64_t k_out_stride_t, int64_t k_out_stride_h,
+    int32_t* d_status, kvq_stream_t stream);
+
 /*
  * kvq_selftest_convert -- exposes the device number-format converters the
  * kernels above use, for exhaustive testing.  For i < count and f the float
