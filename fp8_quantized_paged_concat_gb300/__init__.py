@@ -35,7 +35,8 @@ __all__ = [
     "kvq_compact_drafts_nvfp4_per_head", "kvq_per_head_attention_workspace_bytes",
     "kvq_per_head_attention_default_splits",
     "PER_HEAD_MAX_SPLITS", "PER_HEAD_CLUSTER_SPLITS",
-    "kvq_rope_append_fp8_per_head", "FP8_SCALE_BIAS",
+    "kvq_rope_append_fp8_per_head", "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits",
+    "FP8_SCALE_BIAS",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -115,6 +116,10 @@ _SIGNATURES = {
     "kvq_rope_append_fp8_per_head": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64,
                                      _I64, _I32, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _I64, _I32, _I32, _P,
                                      _I64, _I64, _P, _I64, _I64, _P, _P],
+    "kvq_window_attention_fp8_per_head": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _I64,
+                                          _I32, _I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64,
+                                          _I32, _I32, _P, _I64, _P, _P],
+    "kvq_fp8_attention_default_splits": [_I32] * 8 + [_P],
     "kvq_compact_drafts_nvfp4_per_head": [_P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
                                           _I32, _P, _I64, _I32, _P, _P],
 }
@@ -593,6 +598,7 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 _native = None
 _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
                    "kvq_compact_drafts_nvfp4_per_head", "kvq_rope_append_fp8_per_head",
+                   "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits",
                    "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
 
 
@@ -716,6 +722,31 @@ def kvq_rope_append_fp8_per_head(q, k, v, positions, cos_sin, query_start, seq_l
     (q_out, k_out), None for what is left out."""
     return (_native or _load_native()).append(q, k, v, positions, cos_sin, query_start, seq_lens, block_table, kv_cache,
                                               kv_scales, max_query_len, interleaved, layout, q_out, k_out, status, stream)
+
+
+def kvq_fp8_attention_default_splits(max_query_len: int, num_heads: int, num_kv_heads: int, head_size: int,
+                                     batch_size: int, max_seq_len: int, window: int = 0, num_sinks: int = 0) -> tuple:
+    """kvq_per_head_attention_default_splits for the per-head e4m3 cache."""
+    use_workspace = _I32(0)
+    splits = load_library().kvq_fp8_attention_default_splits(
+        max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks,
+        ctypes.byref(use_workspace))
+    return splits, bool(use_workspace.value)
+
+
+def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_cache, kv_scales, softmax_scale: float,
+                                      max_query_len: int, max_seq_len: int, window: int = 0, num_sinks: int = 0,
+                                      layout="NHD", num_splits=None, workspace=None, out=None, lse=None, status=None,
+                                      stream=None):
+    """Causal attention over the per-head e4m3 cache (kv_cache and kv_scales
+    as kvq_rope_append_fp8_per_head fills them) with a sliding window (window
+    <= 0: none) and num_sinks first tokens that stay visible; everything else
+    as in kvq_window_attention_nvfp4_per_head, num_splits from
+    kvq_fp8_attention_default_splits.  Returns (out bf16 [T, H, D], lse fp32
+    [T, H]); lse=False skips the lse output."""
+    return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, kv_scales, False,
+                                                 softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
+                                                 num_splits, workspace, out, lse, status, stream)
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

@@ -826,10 +826,11 @@ kvq_status per_head_attention(
     const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
     const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache,
     int64_t num_pages, int32_t block_size, int32_t layout, int32_t num_kv_heads, int32_t head_size,
-    const float* k_scale, const float* v_scale, float softmax_scale, int32_t window, int32_t num_sinks,
-    const TreeMask* tree, void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int64_t lse_stride_t,
+    const float* k_scale, const float* v_scale, const uint8_t* page_scales, float softmax_scale, int32_t window,
+    int32_t num_sinks, const TreeMask* tree, void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int64_t lse_stride_t,
     int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes, int32_t* d_status,
     kvq_stream_t stream) {
+  const bool fp8 = page_scales != nullptr;
   KVQ_REQUIRE(num_tokens >= 0 && batch_size >= 0 && max_query_len >= 0 && max_seq_len >= 0,
               "%s: num_tokens, batch_size, max_query_len and max_seq_len must be >= 0", fn);
   KVQ_REQUIRE(num_splits >= 1 && num_splits <= KVQ_PER_HEAD_MAX_SPLITS, "%s: num_splits must be in [1, %d] (got %d)",
@@ -843,11 +844,17 @@ kvq_status per_head_attention(
   KVQ_REQUIRE(num_tokens < (int64_t{1} << 31) && int64_t{max_query_len} * num_heads < (int64_t{1} << 31),
               "%s: num_tokens and max_query_len * num_heads must stay below 2^31", fn);
   int64_t region = 0;
-  if (kvq_status s = check_per_head_cache(fn, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size, &region))
-    return s;
-  KVQ_REQUIRE(region % 16 == 0 && region < (int64_t{1} << 31),
-              "%s: block_size * num_kv_heads * (head_size / 2 + head_size / 16) must be a multiple of 16 below 2^31 "
-              "(got %lld)", fn, static_cast<long long>(region));
+  if (fp8) {
+    if (kvq_status s = check_fp8_cache(fn, kv_cache, page_scales, num_pages, block_size, layout, num_kv_heads, head_size,
+                                       &region))
+      return s;
+  } else {
+    if (kvq_status s = check_per_head_cache(fn, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size, &region))
+      return s;
+    KVQ_REQUIRE(region % 16 == 0 && region < (int64_t{1} << 31),
+                "%s: block_size * num_kv_heads * (head_size / 2 + head_size / 16) must be a multiple of 16 below 2^31 "
+                "(got %lld)", fn, static_cast<long long>(region));
+  }
   if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
   if (kvq_status s = check_heads(fn, "out", out, out_stride_t, out_stride_h, num_heads, head_size, true)) return s;
   KVQ_REQUIRE(lse == nullptr || (aligned(lse, 4) && lse_stride_t >= num_heads),
@@ -857,7 +864,7 @@ kvq_status per_head_attention(
     return s;
   KVQ_REQUIRE(int64_t{block_table_width} * block_size < (int64_t{1} << 31) - 256,
               "%s: block_table_width * block_size must stay below 2^31 - 256 positions", fn);
-  KVQ_REQUIRE(k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4),
+  KVQ_REQUIRE(fp8 || (k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4)),
               "%s: k_scale / v_scale must be device fp32 scalars", fn);
   const double scale_log2 = static_cast<double>(softmax_scale) * 1.4426950408889634074;
   KVQ_REQUIRE(std::fabs(scale_log2) <= std::numeric_limits<float>::max(),
@@ -904,11 +911,12 @@ kvq_status per_head_attention(
   a.block_size = block_size;
   a.block_div = kvq::FastDiv::make(static_cast<uint32_t>(block_size));
   a.region = static_cast<uint32_t>(region);
-  a.scales = static_cast<uint32_t>(int64_t{block_size} * num_kv_heads * (head_size / 2));
+  a.scales = fp8 ? 0 : static_cast<uint32_t>(int64_t{block_size} * num_kv_heads * (head_size / 2));
   a.row_offset = layout == KVQ_LAYOUT_HND ? 1 : num_kv_heads;
   a.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.page_scales = page_scales;
   a.scale_log2 = static_cast<float>(scale_log2);
   a.window = window;
   a.num_sinks = num_sinks;
@@ -939,6 +947,24 @@ kvq_status per_head_attention(
   return launched(fn, kvq::launch_per_head_attention(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int32_t default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                       int32_t batch_size, int32_t max_seq_len, int32_t window, int32_t num_sinks, bool fp8,
+                       int32_t* use_workspace) {
+  if (use_workspace != nullptr) *use_workspace = 0;
+  if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || batch_size <= 0 || max_seq_len <= 0 ||
+      num_sinks < 0)
+    return 1;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  const kvq::PerHeadRanges r =
+      kvq::per_head_default_ranges(max_query_len, num_heads / num_kv_heads, num_kv_heads, head_size, batch_size,
+                                   max_seq_len, window, num_sinks, sms, fp8);
+  if (use_workspace != nullptr) *use_workspace = r.workspace;
+  return r.splits;
+}
+
 }  // namespace
 
 extern "C" {
@@ -955,19 +981,8 @@ int32_t kvq_per_head_attention_default_splits(int32_t max_query_len, int32_t num
                                               int32_t head_size, int32_t batch_size, int32_t max_seq_len,
                                               int32_t window, int32_t num_sinks, int32_t tree,
                                               int32_t* use_workspace) {
-  if (use_workspace != nullptr) *use_workspace = 0;
-  if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || batch_size <= 0 || max_seq_len <= 0 ||
-      num_sinks < 0)
-    return 1;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
-  const kvq::PerHeadRanges r =
-      kvq::per_head_default_ranges(max_query_len, num_heads / num_kv_heads, num_kv_heads, head_size, batch_size,
-                                   max_seq_len, tree ? 0 : window, num_sinks, sms);
-  if (use_workspace != nullptr) *use_workspace = r.workspace;
-  return r.splits;
+  return default_splits(max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, tree ? 0 : window,
+                        num_sinks, false, use_workspace);
 }
 
 kvq_status kvq_window_attention_nvfp4_per_head(
@@ -981,9 +996,34 @@ kvq_status kvq_window_attention_nvfp4_per_head(
   return per_head_attention("kvq_window_attention_nvfp4_per_head", q, q_stride_t, q_stride_h, num_tokens, num_heads,
                             query_start, seq_lens, batch_size, max_query_len, block_table, block_table_stride,
                             block_table_width, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size,
-                            k_scale, v_scale, softmax_scale, window, num_sinks, nullptr, out, out_stride_t,
+                            k_scale, v_scale, nullptr, softmax_scale, window, num_sinks, nullptr, out, out_stride_t,
                             out_stride_h, lse, lse_stride_t, max_seq_len, num_splits, workspace, workspace_bytes,
                             d_status, stream);
+}
+
+kvq_status kvq_window_attention_fp8_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache,
+    const uint8_t* kv_scales, int64_t num_pages, int32_t block_size, int32_t layout, int32_t num_kv_heads,
+    int32_t head_size, float softmax_scale, int32_t window, int32_t num_sinks, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, int32_t max_seq_len, int32_t num_splits, void* workspace,
+    int64_t workspace_bytes, int32_t* d_status, kvq_stream_t stream) {
+  const char* fn = "kvq_window_attention_fp8_per_head";
+  KVQ_REQUIRE(kv_scales != nullptr || num_tokens == 0 || batch_size == 0 || max_query_len == 0,
+              "%s: kv_scales must be non-NULL", fn);
+  return per_head_attention(fn, q, q_stride_t, q_stride_h, num_tokens, num_heads, query_start, seq_lens, batch_size,
+                            max_query_len, block_table, block_table_stride, block_table_width, kv_cache, num_pages,
+                            block_size, layout, num_kv_heads, head_size, nullptr, nullptr, kv_scales, softmax_scale,
+                            window, num_sinks, nullptr, out, out_stride_t, out_stride_h, lse, lse_stride_t, max_seq_len,
+                            num_splits, workspace, workspace_bytes, d_status, stream);
+}
+
+int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
+                                         int32_t head_size, int32_t batch_size, int32_t max_seq_len, int32_t window,
+                                         int32_t num_sinks, int32_t* use_workspace) {
+  return default_splits(max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks,
+                        true, use_workspace);
 }
 
 kvq_status kvq_tree_attention_nvfp4_per_head(
@@ -999,7 +1039,7 @@ kvq_status kvq_tree_attention_nvfp4_per_head(
   return per_head_attention("kvq_tree_attention_nvfp4_per_head", q, q_stride_t, q_stride_h, num_tokens, num_heads,
                             query_start, seq_lens, batch_size, max_query_len, block_table, block_table_stride,
                             block_table_width, kv_cache, num_pages, block_size, layout, num_kv_heads, head_size,
-                            k_scale, v_scale, softmax_scale, 0, 0, &tree, out, out_stride_t, out_stride_h, lse,
+                            k_scale, v_scale, nullptr, softmax_scale, 0, 0, &tree, out, out_stride_t, out_stride_h, lse,
                             lse_stride_t, max_seq_len, num_splits, workspace, workspace_bytes, d_status, stream);
 }
 

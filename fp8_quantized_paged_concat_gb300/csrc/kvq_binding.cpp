@@ -38,6 +38,8 @@ struct Library {
   decltype(&kvq_tree_attention_nvfp4_per_head) tree = nullptr;
   decltype(&kvq_compact_drafts_nvfp4_per_head) compact = nullptr;
   decltype(&kvq_rope_append_fp8_per_head) append = nullptr;
+  decltype(&kvq_window_attention_fp8_per_head) fp8_window = nullptr;
+  decltype(&kvq_fp8_attention_default_splits) fp8_default_splits = nullptr;
   decltype(&kvq_per_head_attention_workspace_bytes) workspace_bytes = nullptr;
   decltype(&kvq_per_head_attention_default_splits) default_splits = nullptr;
   decltype(&kvq_last_error_string) last_error = nullptr;
@@ -318,7 +320,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// q, query_start, seq_lens, tree_mask (None: window form), block_table, kv_cache, k_scale, v_scale, softmax_scale,
+// q, query_start, seq_lens, tree_mask (None: window form), block_table, kv_cache, k_scale, v_scale (False: k_scale
+// is the e4m3 cache's kv_scales), softmax_scale,
 // max_query_len, max_seq_len, window, num_sinks, layout, num_splits, workspace, out, lse, status, stream
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 20, [&]() -> PyObject* {
@@ -338,8 +341,19 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shaped("block_table", table, {B, W});
     const at::Tensor& cache = tensor("kv_cache", a[5]);
     check("kv_cache", cache, at::kByte, dev, 5);
-    const CacheShape c = cache_shape(cache, 0, a[13], D);
-    const float *ks = scale_word("k_scale", a[6], dev), *vs = scale_word("v_scale", a[7], dev);
+    const bool fp8 = a[7] == Py_False;
+    CacheShape c;
+    const float *ks = nullptr, *vs = nullptr;
+    const uint8_t* page_scales = nullptr;
+    if (fp8) {
+      const at::Tensor& scales = tensor("kv_scales", a[6]);
+      c = fp8_cache_shape(cache, scales, a[13], -1, D, dev);
+      page_scales = static_cast<const uint8_t*>(scales.data_ptr());
+    } else {
+      c = cache_shape(cache, 0, a[13], D);
+      ks = scale_word("k_scale", a[6], dev);
+      vs = scale_word("v_scale", a[7], dev);
+    }
     const float scale = real(a[8]);
     const int32_t max_query = int32("max_query_len", a[9]), max_seq = int32("max_seq_len", a[10]);
     const int32_t window = int32("window", a[11]), sinks = int32("num_sinks", a[12]);
@@ -359,8 +373,10 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t use_workspace = 0;
     int32_t splits;
     if (a[14] == Py_None) {
-      splits = lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks, tree,
-                                  &use_workspace);
+      splits = fp8 ? lib.fp8_default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks,
+                                            &use_workspace)
+                   : lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks, tree,
+                                        &use_workspace);
     } else {
       splits = int32("num_splits", a[14]);
       use_workspace = splits > KVQ_PER_HEAD_CLUSTER_SPLITS ||
@@ -388,7 +404,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* lens_p = static_cast<const int32_t*>(lens.data_ptr());
     const auto* table_p = static_cast<const int32_t*>(table.data_ptr());
     const auto* cache_p = static_cast<const uint8_t*>(cache.data_ptr());
-    if (tree) {
+    if (fp8) {
+      must(lib.fp8_window(q.data_ptr(), sq.t, sq.h, T, dim(H), start_p, lens_p, dim(B), max_query, table_p,
+                          row_stride(table), dim(W), cache_p, page_scales, cache.size(0), c.block_size, c.layout, c.heads,
+                          c.head_size, scale, window, sinks, out.data_ptr(), so.t, so.h, lse_ptr, lse_stride, max_seq,
+                          splits, ws, ws_bytes, status, stream),
+           "kvq_window_attention_fp8_per_head");
+    } else if (tree) {
       const at::Tensor& mask = tensor("tree_mask", a[3]);
       check("tree_mask", mask, at::kLong, dev, 2);
       shaped("tree_mask", mask, {T, mask.size(1)});
@@ -527,6 +549,8 @@ PyObject* bind(PyObject*, PyObject* table) {
       !set("kvq_tree_attention_nvfp4_per_head", found.tree) ||
       !set("kvq_compact_drafts_nvfp4_per_head", found.compact) ||
       !set("kvq_rope_append_fp8_per_head", found.append) ||
+      !set("kvq_window_attention_fp8_per_head", found.fp8_window) ||
+      !set("kvq_fp8_attention_default_splits", found.fp8_default_splits) ||
       !set("kvq_per_head_attention_workspace_bytes", found.workspace_bytes) ||
       !set("kvq_per_head_attention_default_splits", found.default_splits) ||
       !set("kvq_last_error_string", found.last_error))

@@ -186,7 +186,7 @@ struct NormRopeArgs {
 };
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t stream);
 
-// Attention over the per-head NVFP4 cache: request b's query tokens
+// Attention over a per-head cache, NVFP4 or e4m3: request b's query tokens
 // [query_start[b], query_start[b+1]) are the last positions of its sequence
 // [0, seq_lens[b]).
 struct PerHeadAttentionArgs {
@@ -211,8 +211,9 @@ struct PerHeadAttentionArgs {
   uint32_t region;                // bytes of one (page, side), < 2^31: K at 2 * page * region, V one region on
   uint32_t scales;                // offset of the scale rows inside a region
   int32_t row_offset, row_head;   // row of (offset, head) = offset * row_offset + head * row_head
-  const float* k_scale;
+  const float* k_scale;           // NVFP4: the tensors' scales (e4m3: nullptr)
   const float* v_scale;
+  const uint8_t* page_scales;     // e4m3: [num_pages, 2, num_kv_heads] (NVFP4: nullptr)
   float scale_log2;               // softmax_scale * log2(e)
   int32_t window;                 // <= 0: none
   int32_t num_sinks;

@@ -58,17 +58,23 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                   // keys per warp step
 constexpr int kStages = 2;
 
-// Shared memory of one warp's stage: 32 data rows of K, of V, then their scale rows.
-template <int D>
+// Shared memory of one warp's stage: 32 data rows of K, of V, then their scale
+// rows (an e4m3 entry has none: its page's two scales stay in registers).
+// kWarps: an SM holds 201 KB of e4m3 stages at D = 128 with four warps a CTA, at
+// D = 256 with two.
+template <int D, bool kFp8>
 struct Stage {
-  static constexpr int kRow = D / 2, kScales = D / 16;
+  static constexpr int kWarps = kFp8 && D == 256 ? 2 : 4;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRow = kFp8 ? D : D / 2, kScales = kFp8 ? 0 : D / 16;
   static constexpr int kV = kStep * kRow, kKs = 2 * kStep * kRow, kVs = kKs + kStep * kScales;
   static constexpr int kBytes = kVs + kStep * kScales;
+  static constexpr int ctas(int row_tiles) {                     // per SM
+    return kFp8 ? (D == 64 ? (row_tiles == 2 ? 3 : 4) : 3) : D == 256 ? 2 : row_tiles == 2 ? 3 : 4;
+  }
 };
 
 // D += A B, A 16 x 16 (row), B 16 x 8 (col), f16 in, fp32 out.
@@ -90,13 +96,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // keys 2c differ mod 4 over c, and those of 2c and 2c + 1 in parity, which
 // keeps the lanes' shared-memory reads apart.
 __device__ __forceinline__ uint32_t key_row(uint32_t n) { return (n & 1) ? 4 + ((n >> 1) ^ 1) : n >> 1; }
-// 16-byte chunk swizzles of the staged data rows.
-template <int D>
+// 16-byte chunk swizzles of the staged data rows: the eight lanes that read
+// at once (two keys' four pieces; of values four keys' two) fall in different banks.
+template <int D, bool kFp8>
 __device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) {
+  if constexpr (kFp8) return D == 256 ? chunk ^ (chunk >> 3) ^ ((row & 1) << 1) : D == 128 ? chunk ^ (row & 1) : chunk;
   return D == 256 ? chunk ^ (row & 1) : chunk;
 }
-template <int D>
+template <int D, bool kFp8>
 __device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
+  if constexpr (kFp8)
+    return D == 256 ? chunk ^ ((row & 1) << 2) ^ ((row >> 1) & 1) : D == 128 ? chunk ^ ((row & 3) << 1) : chunk ^ (row & 2);
   return D == 256 ? chunk ^ ((row & 3) << 1) : D == 128 ? chunk ^ (row & 2) : chunk;
 }
 
@@ -130,7 +140,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, const Request& rq, uint32_t kv_head,
                                              int64_t row0, int32_t rows, int32_t rank, int32_t dims, uint32_t o,
                                              uint32_t stride, uint32_t m, uint32_t l) {
-  const float v_scale = load_global(a.v_scale);
+  const float v_scale = a.v_scale != nullptr ? load_global(a.v_scale) : 1.0f;
   cluster_sync();
   const int32_t chunks = dims / 8;
   // (distributed shared memory gives an SM about 14 bytes a clock: the shares are equal)
@@ -175,10 +185,11 @@ __device__ __forceinline__ void join_cluster(const PerHeadAttentionArgs& a, cons
   cluster_sync();                                // no CTA leaves while its memory is read
 }
 
-template <int D, int kRowTiles>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 4)
+template <int D, int kRowTiles, bool kFp8>
+__global__ void __launch_bounds__(Stage<D, kFp8>::kThreads, Stage<D, kFp8>::ctas(kRowTiles))
     per_head_attention_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
-  using St = Stage<D>;
+  using St = Stage<D, kFp8>;
+  constexpr int kWarps = St::kWarps, kThreads = St::kThreads;
   constexpr int kRows = 8 * kRowTiles;
   constexpr int kKSteps = D / 16;                // 16-dimension steps of K Q^T
   constexpr int kDimTiles = D / 16;              // 16-dimension tiles of V^T P^T
@@ -216,13 +227,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
   bool bad_index = rq.cut && threadIdx.x == 0;
   LookUp next;                                   // the lane's key of the next step to be copied
+  uint32_t scales_ring[kStages - 1] = {};        // e4m3: the lane's key's scale bytes in the steps in flight, K then V
   auto look_up = [&](int32_t step) {
     const uint32_t p = static_cast<uint32_t>(keys.base(step)) + lane;
     next = look_up_position(a, table, head_row, step < s1 && p < static_cast<uint32_t>(keys.limit(step)), p);
   };
   // one group of copies (empty past the range); returns the step's keys that exist
-  auto start = [&](int32_t step, int stage) -> uint32_t {
+  auto start = [&](int32_t step, int stage, uint32_t& page_scales) -> uint32_t {
     uint32_t there = 0;
+    if constexpr (kFp8) page_scales = KVQ_FP8_SCALE_BIAS;    // a key that is not there: no value, and no 0 times infinity
     if (step < s1) {
       const bool ok = next.in && next.id >= 0 && next.id < a.num_pages;
       bad_index = bad_index || (next.in && !ok);
@@ -230,9 +243,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       const uint8_t* page = at_offset(a.cache, ok ? next.id : 0, 2 * a.region);   // some page where there is none
       const uint32_t row = ok ? next.row : 0;
       const uint32_t st = ring + stage * St::kBytes;
-      const uint8_t* scales = at_offset(page + a.scales, row, St::kScales);
-      cp_async<St::kScales>(st + St::kKs + lane * St::kScales, scales, ok ? St::kScales : 0);
-      cp_async<St::kScales>(st + St::kVs + lane * St::kScales, scales + a.region, ok ? St::kScales : 0);
+      if constexpr (kFp8) {
+        if (ok) {
+          const uint8_t* scales = a.page_scales + static_cast<uint64_t>(next.id) * (2u * a.num_kv_heads) + head;
+          page_scales = page_scale(load_global(scales)) | page_scale(load_global(scales + a.num_kv_heads)) << 8;
+        }
+      } else {
+        const uint8_t* scales = at_offset(page + a.scales, row, St::kScales);
+        cp_async<St::kScales>(st + St::kKs + lane * St::kScales, scales, ok ? St::kScales : 0);
+        cp_async<St::kScales>(st + St::kVs + lane * St::kScales, scales + a.region, ok ? St::kScales : 0);
+      }
       const uint64_t data = reinterpret_cast<uint64_t>(at_offset(page, row, St::kRow));
       constexpr int kLanes = St::kRow / 16;      // lanes that copy one data row
 #pragma unroll
@@ -242,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(data >> 32), key)) << 32 |
                             __shfl_sync(kFull, static_cast<uint32_t>(data), key);
         const uint8_t* src = reinterpret_cast<const uint8_t*>(at) + 16 * chunk;
-        const uint32_t k_dst = st + key * St::kRow + 16 * k_chunk<D>(key, chunk);
-        const uint32_t v_dst = st + St::kV + key * St::kRow + 16 * v_chunk<D>(key, chunk);
+        const uint32_t k_dst = st + key * St::kRow + 16 * k_chunk<D, kFp8>(key, chunk);
+        const uint32_t v_dst = st + St::kV + key * St::kRow + 16 * v_chunk<D, kFp8>(key, chunk);
         const uint32_t n = (there >> key) & 1 ? 16 : 0;
         cp_async<16>(k_dst, src, n);
         cp_async<16>(v_dst, src + a.region, n);
@@ -258,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   look_up(first);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    valid_ring[i] = start(first + i * kWarps, i);
+    valid_ring[i] = start(first + i * kWarps, i, scales_ring[i]);
     look_up(first + (i + 1) * kWarps);
   }
 
@@ -268,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   uint32_t q[kRowTiles][kKSteps][2];
   float sc[kRowTiles][2];
   float m[kRowTiles][2], l[kRowTiles][2];                 // reference maximum, sum
-  const float scale = a.scale_log2 * load_global(a.k_scale);
+  const float scale = kFp8 ? a.scale_log2 : a.scale_log2 * load_global(a.k_scale);
 #pragma unroll
   for (int nt = 0; nt < kRowTiles; ++nt) {
     const int32_t r = 8 * nt + g;
@@ -304,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     for (int x = 0; x < 2; ++x) {
       // row 2c + x of the tile is loaded by the lanes with g = 2c + x
       sc[nt][x] = __shfl_sync(kFull, back, (2 * c + x) * 4);
-      if (sc[nt][x] == 0.0f) sc[nt][x] = 1e-30f;            // as good as 0 for any score, but 0 for no infinity
+      if (sc[nt][x] == 0.0f) sc[nt][x] = kFp8 ? 1e-37f : 1e-30f;   // as good as 0 for any score, but 0 for no infinity
       const int32_t rr = 8 * nt + 2 * c + x;
       m[nt][x] = rr < rows ? -INFINITY : 0.0f;
       l[nt][x] = 0.0f;
@@ -321,15 +341,20 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 #pragma unroll
     for (int nt = 0; nt < kRowTiles; ++nt) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
 
+  uint32_t v_ref = 0;                            // e4m3: o counts in units of the scale with this byte (0: none yet)
   const uint32_t rg = key_row(g), r0 = key_row(2 * c), r1 = key_row(2 * c + 1);
   int stage = 0;
   for (int32_t step = first; step < s1; step += kWarps) {
     cp_wait<kStages - 2>();
     __syncwarp();                                // the step has landed, and the stage before it has been read
-    const uint32_t valid = valid_ring[0];
+    const uint32_t valid = valid_ring[0], page_scales = scales_ring[0];
 #pragma unroll
-    for (int i = 0; i + 2 < kStages; ++i) valid_ring[i] = valid_ring[i + 1];
-    valid_ring[kStages - 2] = start(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+    for (int i = 0; i + 2 < kStages; ++i) {
+      valid_ring[i] = valid_ring[i + 1];
+      scales_ring[i] = scales_ring[i + 1];
+    }
+    valid_ring[kStages - 2] =
+        start(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1, scales_ring[kStages - 2]);
     look_up(step + kStages * kWarps);
     const uint32_t st = ring + stage * St::kBytes;
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -342,46 +367,63 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       for (int nt = 0; nt < kRowTiles; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
       const uint32_t ra = 16 * mt + rg, rb2 = ra + 8;
       const uint32_t ka = st + ra * St::kRow, kb = st + rb2 * St::kRow;
-      // the lane's D / 64 scales of each row
-      uint32_t sa, sb;
-      if constexpr (D == 64) {
-        sa = lds8(st + St::kKs + ra * 4 + c) * 0x0101u;
-        sb = lds8(st + St::kKs + rb2 * 4 + c) * 0x0101u;
-      } else if constexpr (D == 128) {
-        sa = lds16(st + St::kKs + ra * 8 + 2 * c);
-        sb = lds16(st + St::kKs + rb2 * 8 + 2 * c);
-      } else {
-        sa = lds32(st + St::kKs + ra * 16 + 4 * c);
-        sb = lds32(st + St::kKs + rb2 * 16 + 4 * c);
-      }
+      if constexpr (kFp8) {
 #pragma unroll
-      for (int i = 0; i < (D + 127) / 128; ++i) {       // 32 dimensions (16 at D = 64) at a time
-        uint32_t wa[4], wb[4];
-        if constexpr (D == 64) {
-          const uint2 x = lds64(ka + 8 * c), y = lds64(kb + 8 * c);
-          wa[0] = x.x; wa[1] = x.y; wb[0] = y.x; wb[1] = y.y;
-        } else {
-          const uint32_t chunk = D == 256 ? 2 * c + i : c;
-          const uint4 x = ld_shared16(ka + 16 * k_chunk<D>(ra, chunk)), y = ld_shared16(kb + 16 * k_chunk<D>(rb2, chunk));
-          wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
-          wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+        for (int i = 0; i < D / 64; ++i) {              // 16 dimensions of the lane's: four product steps
+          const uint4 x = ld_shared16(ka + 16 * k_chunk<D, true>(ra, c * (D / 64) + i));
+          const uint4 y = ld_shared16(kb + 16 * k_chunk<D, true>(rb2, c * (D / 64) + i));
+          const uint32_t wa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = bits(e4m3x2_to_half2(wa[j])), a1 = bits(e4m3x2_to_half2(wb[j]));
+            const uint32_t a2 = bits(e4m3x2_to_half2(wa[j] >> 16)), a3 = bits(e4m3x2_to_half2(wb[j] >> 16));
+#pragma unroll
+            for (int nt = 0; nt < kRowTiles; ++nt)
+              mma_f16(s[mt][nt], a0, a1, a2, a3, q[nt][4 * i + j][0], q[nt][4 * i + j][1]);
+          }
         }
-        const uint32_t fa = bits(e4m3x2_to_half2(sa >> (16 * i))), fb = bits(e4m3x2_to_half2(sb >> (16 * i)));
+      } else {
+        // the lane's D / 64 scales of each row
+        uint32_t sa, sb;
+        if constexpr (D == 64) {
+          sa = lds8(st + St::kKs + ra * 4 + c) * 0x0101u;
+          sb = lds8(st + St::kKs + rb2 * 4 + c) * 0x0101u;
+        } else if constexpr (D == 128) {
+          sa = lds16(st + St::kKs + ra * 8 + 2 * c);
+          sb = lds16(st + St::kKs + rb2 * 8 + 2 * c);
+        } else {
+          sa = lds32(st + St::kKs + ra * 16 + 4 * c);
+          sb = lds32(st + St::kKs + rb2 * 16 + 4 * c);
+        }
 #pragma unroll
-        for (int j = 0; j < (D == 64 ? 2 : 4); ++j) {   // 8 dimensions: two 16-wide product steps
-          // (the broadcast of one half is an operand modifier of the product)
-          const uint32_t sfa = (j >> 1) && D != 64 ? high_both(fa) : low_both(fa);
-          const uint32_t sfb = (j >> 1) && D != 64 ? high_both(fb) : low_both(fb);
-          uint32_t ha[4], hb[4];
-          e2m1x8(wa[j], ha);
-          e2m1x8(wb[j], hb);
+        for (int i = 0; i < (D + 127) / 128; ++i) {       // 32 dimensions (16 at D = 64) at a time
+          uint32_t wa[4], wb[4];
+          if constexpr (D == 64) {
+            const uint2 x = lds64(ka + 8 * c), y = lds64(kb + 8 * c);
+            wa[0] = x.x; wa[1] = x.y; wb[0] = y.x; wb[1] = y.y;
+          } else {
+            const uint32_t chunk = D == 256 ? 2 * c + i : c;
+            const uint4 x = ld_shared16(ka + 16 * k_chunk<D, false>(ra, chunk)), y = ld_shared16(kb + 16 * k_chunk<D, false>(rb2, chunk));
+            wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w;
+            wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[3] = y.w;
+          }
+          const uint32_t fa = bits(e4m3x2_to_half2(sa >> (16 * i))), fb = bits(e4m3x2_to_half2(sb >> (16 * i)));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t a0 = hmul2(ha[2 * e], sfa), a1 = hmul2(hb[2 * e], sfb);
-            const uint32_t a2 = hmul2(ha[2 * e + 1], sfa), a3 = hmul2(hb[2 * e + 1], sfb);
-            const int ks = (D == 64 ? 2 : 4) * 2 * i + 2 * j + e;
+          for (int j = 0; j < (D == 64 ? 2 : 4); ++j) {   // 8 dimensions: two 16-wide product steps
+            // (the broadcast of one half is an operand modifier of the product)
+            const uint32_t sfa = (j >> 1) && D != 64 ? high_both(fa) : low_both(fa);
+            const uint32_t sfb = (j >> 1) && D != 64 ? high_both(fb) : low_both(fb);
+            uint32_t ha[4], hb[4];
+            e2m1x8(wa[j], ha);
+            e2m1x8(wb[j], hb);
 #pragma unroll
-            for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(s[mt][nt], a0, a1, a2, a3, q[nt][ks][0], q[nt][ks][1]);
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t a0 = hmul2(ha[2 * e], sfa), a1 = hmul2(hb[2 * e], sfb);
+              const uint32_t a2 = hmul2(ha[2 * e + 1], sfa), a3 = hmul2(hb[2 * e + 1], sfb);
+              const int ks = (D == 64 ? 2 : 4) * 2 * i + 2 * j + e;
+#pragma unroll
+              for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(s[mt][nt], a0, a1, a2, a3, q[nt][ks][0], q[nt][ks][1]);
+            }
           }
         }
       }
@@ -418,6 +460,31 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
           }
         }
     }
+    // e4m3: the scales of the thread's four keys.  A key's scale multiplies its
+    // scores; a value's multiplies its weight, relative to a reference v_ref in
+    // whose units o counts, so that f16 weights keep their precision: the
+    // reference follows the step's largest scale once that is above it, or more
+    // than 2^6 below.
+    float kf[4], vf[4];
+    if constexpr (kFp8) {
+      const uint32_t top = __reduce_max_sync(kFull, page_scales >> 8);
+      if (top > v_ref || (top != 0 && top + 6 < v_ref)) {
+        const float f = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - top) << 23);
+        v_ref = top;
+#pragma unroll
+        for (int t = 0; t < kDimTiles; ++t)
+#pragma unroll
+          for (int nt = 0; nt < kRowTiles; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[t][nt][x] *= f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = __shfl_sync(kFull, page_scales, 8 * e + rg);
+        kf[e] = __uint_as_float((w & 0xFF) << 23);
+        vf[e] = __uint_as_float((w >> 8) == 0 ? 0u : (127 + (w >> 8) - v_ref) << 23);
+      }
+    }
     // Weights against the reference m, the maximum of steps before: no
     // maximum of their own is taken unless their sum shows that one of them
     // may exceed it by 2^kGrow (or there is no reference yet).
@@ -431,7 +498,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float* v = &s[e >> 1][nt][2 * (e & 1)];
-          const float2 z = ffma2(make_float2(v[0], v[1]), make_float2(sc[nt][0], sc[nt][1]), off);
+          float2 z;
+          if constexpr (kFp8)                    // (two steps: a hidden score stays infinite whatever its page's scale)
+            z = ffma2(fmul2(make_float2(v[0], v[1]), make_float2(sc[nt][0], sc[nt][1])), make_float2(kf[e], kf[e]), off);
+          else
+            z = ffma2(make_float2(v[0], v[1]), make_float2(sc[nt][0], sc[nt][1]), off);
           w[nt][e] = make_float2(ex2(z.x), ex2(z.y));
           sum[nt] = fadd2(sum[nt], w[nt][e]);
         }
@@ -450,7 +521,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
         for (int x = 0; x < 2; ++x) {
           float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, s[e >> 1][nt][2 * (e & 1) + x] * sc[nt][x]);
+          for (int e = 0; e < 4; ++e) {
+            const float z = s[e >> 1][nt][2 * (e & 1) + x] * sc[nt][x];
+            top = fmaxf(top, kFp8 ? z * kf[e] : z);
+          }
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -477,7 +551,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       l[nt][0] += sum[nt].x;
       l[nt][1] += sum[nt].y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e >> 1][nt][e & 1] = transpose8(pack_f16x2(w[nt][e].x, w[nt][e].y));
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = kFp8 ? fmul2(w[nt][e], make_float2(vf[e], vf[e])) : w[nt][e];
+        p[e >> 1][nt][e & 1] = transpose8(pack_f16x2(x.x, x.y));
+      }
     }
 
     // ---- O^T += V^T P^T ----------------------------------------------------
@@ -485,46 +562,92 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
     for (int mt = 0; mt < 2; ++mt) {
       // keys 2c and 2c + 1 (rows x0, x1) and the two 8 keys on (y0, y1)
       const uint32_t x0 = 16 * mt + r0, x1 = 16 * mt + r1, y0 = x0 + 8, y1 = x1 + 8;
-      const uint32_t vs = st + St::kVs, vd = st + St::kV;
+      if constexpr (kFp8) {
+        const uint32_t vd = st + St::kV;
 #pragma unroll
-      for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {    // one scale group (16 dimensions; 8 at D = 64) at a time
-        const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
-        uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
-        uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
-        if (!all) {                              // else no entry of the step is hidden from any row
-          sx = finite_scales(sx);
-          sy = finite_scales(sy);
-        }
-        uint32_t w[4][2];
-        auto load = [&](uint32_t row, uint32_t (&d)[2]) {
-          if constexpr (D == 64) {
-            d[0] = lds32(vd + row * St::kRow + 4 * g);
-          } else {
-            const uint32_t at = D == 128 ? 8 * g : 16 * g + 8 * i;
-            const uint2 x = lds64(vd + row * St::kRow + 16 * v_chunk<D>(row, at >> 4) + (at & 8));
-            d[0] = x.x;
-            d[1] = x.y;
+        for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {  // 16 of the lane's dimensions (8 at D = 64)
+          uint32_t w[4][4];
+          auto load = [&](uint32_t row, uint32_t (&d)[4]) {
+            const uint32_t at = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
+            const uint32_t from = vd + row * St::kRow + 16 * v_chunk<D, true>(row, at);
+            if constexpr (D == 64) {
+              const uint2 x = lds64(from + 8 * (g & 1));
+              d[0] = x.x;
+              d[1] = x.y;
+            } else {
+              const uint4 x = ld_shared16(from);
+              d[0] = x.x;
+              d[1] = x.y;
+              d[2] = x.z;
+              d[3] = x.w;
+            }
+          };
+          load(x0, w[0]);
+          load(x1, w[1]);
+          load(y0, w[2]);
+          load(y1, w[3]);
+          constexpr int kWords = D == 64 ? 2 : 4;
+          if (!all) {                            // else no entry of the step is hidden from any row
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < kWords; ++j) w[k][j] = finite_codes(w[k][j]);
           }
-        };
-        load(x0, w[0]);
-        load(x1, w[1]);
-        load(y0, w[2]);
-        load(y1, w[3]);
 #pragma unroll
-        for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {   // 8 dimensions
-          // bytes holding (first key's, second key's) codes of the even and odd dimensions
-          constexpr uint32_t kLow = 0x0F0F0F0Fu;
-          uint32_t ex[4], od[4], ey[4], oy[4];
-          e2m1x8((w[0][j] & kLow) | ((w[1][j] << 4) & ~kLow), ex);
-          e2m1x8(((w[0][j] >> 4) & kLow) | (w[1][j] & ~kLow), od);
-          e2m1x8((w[2][j] & kLow) | ((w[3][j] << 4) & ~kLow), ey);
-          e2m1x8(((w[2][j] >> 4) & kLow) | (w[3][j] & ~kLow), oy);
+          for (int j = 0; j < kWords; ++j)       // 4 dimensions
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {          // dimensions 2 e and 2 e + 1 of the eight
-            const uint32_t a0 = hmul2(ex[e], sx), a1 = hmul2(od[e], sx), a2 = hmul2(ey[e], sy), a3 = hmul2(oy[e], sy);
-            const int t = (D == 64 ? 0 : 8 * i + 4 * j) + e;
+            for (int e = 0; e < 2; ++e) {        // dimensions 2 e and 2 e + 1 of the four, a pair of keys each
+              const uint32_t x = prmt(w[0][j], w[1][j], e ? 0x7362 : 0x5140);
+              const uint32_t y = prmt(w[2][j], w[3][j], e ? 0x7362 : 0x5140);
+              const uint32_t a0 = bits(e4m3x2_to_half2(x)), a1 = bits(e4m3x2_to_half2(x >> 16));
+              const uint32_t a2 = bits(e4m3x2_to_half2(y)), a3 = bits(e4m3x2_to_half2(y >> 16));
+              const int t = 8 * i + 2 * j + e;
 #pragma unroll
-            for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+              for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+            }
+        }
+      } else {
+        const uint32_t vs = st + St::kVs, vd = st + St::kV;
+#pragma unroll
+        for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {    // one scale group (16 dimensions; 8 at D = 64) at a time
+          const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
+          uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
+          uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
+          if (!all) {                              // else no entry of the step is hidden from any row
+            sx = finite_scales(sx);
+            sy = finite_scales(sy);
+          }
+          uint32_t w[4][2];
+          auto load = [&](uint32_t row, uint32_t (&d)[2]) {
+            if constexpr (D == 64) {
+              d[0] = lds32(vd + row * St::kRow + 4 * g);
+            } else {
+              const uint32_t at = D == 128 ? 8 * g : 16 * g + 8 * i;
+              const uint2 x = lds64(vd + row * St::kRow + 16 * v_chunk<D, false>(row, at >> 4) + (at & 8));
+              d[0] = x.x;
+              d[1] = x.y;
+            }
+          };
+          load(x0, w[0]);
+          load(x1, w[1]);
+          load(y0, w[2]);
+          load(y1, w[3]);
+#pragma unroll
+          for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {   // 8 dimensions
+            // bytes holding (first key's, second key's) codes of the even and odd dimensions
+            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+            uint32_t ex[4], od[4], ey[4], oy[4];
+            e2m1x8((w[0][j] & kLow) | ((w[1][j] << 4) & ~kLow), ex);
+            e2m1x8(((w[0][j] >> 4) & kLow) | (w[1][j] & ~kLow), od);
+            e2m1x8((w[2][j] & kLow) | ((w[3][j] << 4) & ~kLow), ey);
+            e2m1x8(((w[2][j] >> 4) & kLow) | (w[3][j] & ~kLow), oy);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {          // dimensions 2 e and 2 e + 1 of the eight
+              const uint32_t a0 = hmul2(ex[e], sx), a1 = hmul2(od[e], sx), a2 = hmul2(ey[e], sy), a3 = hmul2(oy[e], sy);
+              const int t = (D == 64 ? 0 : 8 * i + 4 * j) + e;
+#pragma unroll
+              for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+            }
           }
         }
       }
@@ -533,10 +656,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
   if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
 
   // ---- join the four warps -------------------------------------------------
-  const float v_scale = load_global(a.v_scale);        // under way meanwhile
+  const float v_scale = kFp8 ? 1.0f : load_global(a.v_scale);   // under way meanwhile
   cp_wait<0>();
   __syncthreads();                               // every ring is idle
   float* jo = reinterpret_cast<float*>(smem);    // [kWarps][kRows][D]
+  const float unit = kFp8 ? __uint_as_float(v_ref << 23) : 1.0f;   // of this warp's sums
   __shared__ float jm[kWarps][kRows], jl[kWarps][kRows];
 #pragma unroll
   for (int nt = 0; nt < kRowTiles; ++nt)
@@ -555,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : kRowTiles == 2 ? 3 : 
       float* dst = jo + (warp * kRows + r) * D + g * (D / 8);
 #pragma unroll
       for (int t = 0; t < kDimTiles; ++t)
-        *reinterpret_cast<float2*>(dst + 2 * t) = make_float2(o[t][nt][x], o[t][nt][2 + x]);
+        *reinterpret_cast<float2*>(dst + 2 * t) =
+            kFp8 ? make_float2(o[t][nt][x] * unit, o[t][nt][2 + x] * unit) : make_float2(o[t][nt][x], o[t][nt][2 + x]);
     }
   __syncthreads();
   __shared__ float cm[kRows], cl[kRows];         // of the four warps together, for the cluster
@@ -620,7 +745,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const
   const int64_t flat = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   wait_for_previous();
-  const float v_scale = load_global(a.v_scale);          // in flight beside the request
+  const float v_scale = a.v_scale != nullptr ? load_global(a.v_scale) : 1.0f;   // in flight beside the request
   Request rq;
   if (!request_of(a, b, rq) || flat >= static_cast<int64_t>(rq.tokens) * a.num_heads) return;
   const int64_t row = rq.token0 * a.num_heads + flat;
@@ -686,17 +811,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) per_head_join_kernel(const
   if (lane == 0 && a.lse != nullptr) a.lse[token * a.lse_stride_t + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
 }
 
-template <int D, int kRowTiles>
+template <int D, int kRowTiles, bool kFp8>
 cudaError_t launch_rows(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = kWarps * kStages * Stage<D>::kBytes;
-  static_assert(kSmem >= kWarps * 8 * kRowTiles * D * 4, "the joined rows fit the rings");
-  const cudaError_t e = cudaFuncSetAttribute(per_head_attention_kernel<D, kRowTiles>,
+  using St = Stage<D, kFp8>;
+  constexpr int kSmem = St::kWarps * kStages * St::kBytes;
+  static_assert(kSmem >= St::kWarps * 8 * kRowTiles * D * 4, "the joined rows fit the rings");
+  const cudaError_t e = cudaFuncSetAttribute(per_head_attention_kernel<D, kRowTiles, kFp8>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.max_query_len) * a.group;
   const int64_t blocks = (rows + 8 * kRowTiles - 1) / (8 * kRowTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  return launch_dependent(per_head_attention_kernel<D, kRowTiles>, grid, kThreads, kSmem, a.cluster ? a.num_splits : 1,
+  return launch_dependent(per_head_attention_kernel<D, kRowTiles, kFp8>, grid, St::kThreads, kSmem, a.cluster ? a.num_splits : 1,
                           stream, a, static_cast<int32_t>(blocks));
 }
 
@@ -711,21 +837,25 @@ cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
                           kJoinWarps * 32, 0, 1, stream, a);
 }
 
+template <bool kFp8>
+cudaError_t launch_few_rows(const PerHeadAttentionArgs& a, int64_t block, cudaStream_t stream) {
+  switch (a.head_size) {
+    case 64: return block == 8 ? launch_rows<64, 1, kFp8>(a, stream) : launch_rows<64, 2, kFp8>(a, stream);
+    case 128: return block == 8 ? launch_rows<128, 1, kFp8>(a, stream) : launch_rows<128, 2, kFp8>(a, stream);
+    default: return launch_rows<256, 1, kFp8>(a, stream);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, int sms, cudaStream_t stream) {
+  const bool fp8 = a.page_scales != nullptr;
   const int64_t block = per_head_block(static_cast<int64_t>(a.max_query_len) * a.group,
                                        static_cast<int64_t>(a.num_kv_heads) * a.batch_size, a.head_size, a.num_splits,
-                                       a.cluster, sms);
-  cudaError_t e;
-  if (block > 16)
-    e = launch_per_head_prefill(a, stream);
-  else if (a.head_size == 64)
-    e = block == 8 ? launch_rows<64, 1>(a, stream) : launch_rows<64, 2>(a, stream);
-  else if (a.head_size == 128)
-    e = block == 8 ? launch_rows<128, 1>(a, stream) : launch_rows<128, 2>(a, stream);
-  else
-    e = launch_rows<256, 1>(a, stream);
+                                       a.cluster, sms, fp8);
+  const cudaError_t e = block > 16 ? launch_per_head_prefill(a, stream)
+                        : fp8      ? launch_few_rows<true>(a, block, stream)
+                                   : launch_few_rows<false>(a, block, stream);
   if (e != cudaSuccess || a.num_splits == 1 || a.cluster) return e;
   return a.head_size == 64 ? launch_join<64>(a, stream)
                            : a.head_size == 128 ? launch_join<128>(a, stream) : launch_join<256>(a, stream);

@@ -78,6 +78,17 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
 // any row through a weight of zero.
 __device__ __forceinline__ uint32_t finite_scales(uint32_t s) { return s & __heq2_mask(half2_of(s), half2_of(s)); }
 
+// e4m3 codes: a NaN reads as zero, for the same reason.  (Bit 7 of a byte's
+// low seven bits plus one marks 0x7F.)
+__device__ __forceinline__ uint32_t finite_codes(uint32_t w) {
+  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return w & ~(nan - (nan >> 7));
+}
+// A page's scale byte: the exponent field of the fp32 scale.
+__device__ __forceinline__ uint32_t page_scale(uint32_t byte) {
+  return max(uint32_t{KVQ_FP8_SCALE_BIAS + KVQ_FP8_SCALE_MIN_EXP}, min(uint32_t{KVQ_FP8_SCALE_BIAS + KVQ_FP8_SCALE_MAX_EXP}, byte));
+}
+
 // The power of two that brings a query row's largest value to [2^14, 2^15),
 // as two factors f[0] f[1], and the one that takes it back, i[0] i[1].
 // Rows of zeros, subnormals or infinities stay as they are.

@@ -12,7 +12,9 @@
 namespace kvq {
 
 // CTAs of the few-row kernel that share an SM (its launch bounds).
-constexpr int64_t resident_ctas(int32_t head_size, int64_t block) { return head_size == 256 ? 2 : block == 16 ? 3 : 4; }
+constexpr int64_t resident_ctas(int32_t head_size, int64_t block, bool fp8 = false) {
+  return fp8 ? (head_size == 64 && block != 16 ? 4 : 3) : head_size == 256 ? 2 : block == 16 ? 3 : 4;
+}
 
 // Rows per block of the few-row kernel.  16 rows share a decoded key where
 // such blocks and their ranges fill the GPU (128 requests x 2048 keys, head
@@ -21,8 +23,8 @@ constexpr int64_t resident_ctas(int32_t head_size, int64_t block) { return head_
 // chain (one request x 1024 keys, 16 rows: 6.9 us against 8.8; with long
 // contexts, whose ranges are many, blocks of 16 would be as good: 16384 keys
 // 16.9 against 15.7).  D = 256 has no registers for 16.
-inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, int sms) {
-  return rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16) * int64_t{sms}
+inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, int sms, bool fp8 = false) {
+  return rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16, fp8) * int64_t{sms}
              ? 16 : 8;
 }
 
@@ -35,7 +37,9 @@ inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t
 //   D = 256: 16 rows 124 / 170, 24 rows 187 / 171, 32 rows 236 / 171
 // (The limit at D = 64 was set when the tensor memory kernel took 220 there; a
 // call this large is now past the crossing at 64 rows.)
-inline int64_t most_few_rows(int32_t head_size) { return head_size == 64 ? 64 : head_size == 128 ? 32 : 16; }
+inline int64_t most_few_rows(int32_t head_size, bool fp8 = false) {
+  return fp8 ? INT32_MAX : head_size == 64 ? 64 : head_size == 128 ? 32 : 16;
+}
 
 // Rows per block of the tensor memory kernel: one row tile, or two that share
 // a decoded key (32 requests of 1024 keys x 256 rows, head size 128: 41 us
@@ -43,9 +47,10 @@ inline int64_t most_few_rows(int32_t head_size) { return head_size == 64 ? 64 : 
 inline int64_t per_head_prefill_rows(int64_t rows, int32_t head_size) { return rows <= 128 || head_size == 256 ? 128 : 256; }
 
 // Rows per block of the kernel that a call runs.
-inline int64_t per_head_block(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, bool cluster, int sms) {
-  return !cluster && rows > most_few_rows(head_size) ? per_head_prefill_rows(rows, head_size)
-                                                     : few_rows(rows, groups, head_size, splits, sms);
+inline int64_t per_head_block(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, bool cluster, int sms,
+                              bool fp8 = false) {
+  return !cluster && rows > most_few_rows(head_size, fp8) ? per_head_prefill_rows(rows, head_size)
+                                                     : few_rows(rows, groups, head_size, splits, sms, fp8);
 }
 
 // The default key ranges per block of rows, whether they join through a
@@ -57,12 +62,12 @@ struct PerHeadRanges {
 };
 inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t group, int64_t num_kv_heads,
                                              int32_t head_size, int64_t batch_size, int64_t max_seq_len,
-                                             int64_t window, int64_t num_sinks, int sms) {
+                                             int64_t window, int64_t num_sinks, int sms, bool fp8 = false) {
   const int64_t rows = max_query_len * group, groups = num_kv_heads * batch_size;
   const bool windowed = window > 0 && window < max_seq_len;
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
-  const bool few = rows <= most_few_rows(head_size);
+  const bool few = rows <= most_few_rows(head_size, fp8);
   const bool ragged = !windowed && keys >= 4096 && batch_size > 1;   // long contexts, whose lengths may differ
   // A small call's ranges run as clusters of the few-row kernel: no second
   // launch.  Where the GPU has room for many more ranges than a cluster takes,
@@ -74,7 +79,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
   // 11.9, 4096 keys 14.9 / 13.9, 8000 keys 22.2 / 17.7).
   if (rows <= KVQ_PER_HEAD_CLUSTER_ROWS) {
     constexpr int64_t kMax = KVQ_PER_HEAD_CLUSTER_SPLITS, kLeast = 128;       // a step per warp
-    const int64_t blocks = (rows + 7) / 8 * groups, places = resident_ctas(head_size, 8) * int64_t{sms};
+    const int64_t blocks = (rows + 7) / 8 * groups, places = resident_ctas(head_size, 8, fp8) * int64_t{sms};
     const bool long_small = ragged && 8 * blocks >= places;
     const int64_t room = places / blocks, n = std::min<int64_t>(keys / kLeast, room);
     if (!long_small && n > 1 && (n <= kMax || keys <= kMax * (room >= 4 * kMax || head_size == 256 ? 320 : 1024)))
@@ -86,9 +91,9 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
     const int64_t steps = (keys + 127) / 128, per = (steps + n - 1) / n;
     return (steps + per - 1) / per;
   };
-  int64_t block = few ? few_rows(rows, groups, head_size, 1, sms) : per_head_prefill_rows(rows, head_size);
+  int64_t block = few ? few_rows(rows, groups, head_size, 1, sms, fp8) : per_head_prefill_rows(rows, head_size);
   const auto blocks = [&] { return (rows + block - 1) / block * groups; };
-  const auto places = [&] { return (few ? resident_ctas(head_size, block) : 1) * int64_t{sms}; };
+  const auto places = [&] { return (few ? resident_ctas(head_size, block, fp8) : 1) * int64_t{sms}; };
   int64_t n;
   if (ragged && 8 * blocks() >= places()) {
     // Several ranges to a CTA's place even the lengths out.
@@ -113,7 +118,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
     if (few && rows > 8 && head_size != 256) {
       block = 16;
       n = ranges(4);
-      if (few_rows(rows, groups, head_size, n, sms) != 16) block = 8;
+      if (few_rows(rows, groups, head_size, n, sms, fp8) != 16) block = 8;
     }
     if (block != 16) {
       const bool many = blocks() >= places();

@@ -805,6 +805,43 @@ kvq_status kvq_rope_append_fp8_per_head(
     int32_t* d_status, kvq_stream_t stream);
 
 /*
+ * kvq_window_attention_fp8_per_head -- causal attention over the per-head e4m3
+ * cache with a sliding window and a few first tokens that stay visible:
+ * kvq_window_attention_nvfp4_per_head (its requests, masks, outputs, statuses,
+ * bounds, waits and key ranges, with kvq_fp8_attention_default_splits) with
+ *   s_j = softmax_scale * (q . K_j),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
+ * over this cache's values.  A NaN code in a visible key makes its rows NaN;
+ * in a visible value it makes its dimension NaN or reads as zero; a row that
+ * does not see it never has it.
+ * Arithmetic: products on the tensor cores with fp32 sums (codes exact in
+ * f16; a query row scaled by a power of two into f16, exact down to 2^-28 of
+ * its largest value); a key's scale multiplies its fp32 scores, a value's its
+ * weight (a power of two, relative to one among the 2^6 above the largest of
+ * the keys processed together), which is then rounded to f16 (relative
+ * 2^-11); the softmax in fp32; out rounded once to bf16.
+ */
+kvq_status kvq_window_attention_fp8_per_head(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    const uint8_t* kv_cache, const uint8_t* kv_scales, int64_t num_pages, int32_t block_size, int32_t layout,
+    int32_t num_kv_heads, int32_t head_size,
+    float softmax_scale, int32_t window, int32_t num_sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* lse, int64_t lse_stride_t,
+    int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes,
+    int32_t* d_status, kvq_stream_t stream);
+
+/*
+ * kvq_fp8_attention_default_splits -- kvq_per_head_attention_default_splits
+ * for the e4m3 cache.
+ */
+int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
+                                         int32_t head_size, int32_t batch_size, int32_t max_seq_len,
+                                         int32_t window, int32_t num_sinks, int32_t* use_workspace);
+
+/*
  * kvq_selftest_convert -- exposes the device number-format converters the
  * kernels above use, for exhaustive testing.  For i < count and f the float
  * whose bit pattern is first_bits + i (mod 2^32):

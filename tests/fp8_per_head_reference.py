@@ -114,3 +114,72 @@ def append(cache, q, k, v, positions, cos_sin, start, lens, table, interleaved, 
                     for (off, _, _), x in zip(entries, new):
                         cache.codes[page, side, off, h] = to_e4m3(x.astype(np.float32) * np.float32(2.0 ** -e))
     return status
+
+
+def attend(x, K, V, see, scale, weight_eps, tiny, q_lost=2.0 ** -39):
+    """out, lse and tolerances of query rows x [R, D] over keys K, V [L, D] with see [R, L], in 64 bits.
+
+    The kernels' arithmetic: the score error e_s is that of an fp32 sum of D
+    exact products and of two more roundings, and of what the query's f16
+    form loses (q_lost of its row's largest value; 0 where it stays bf16); a
+    weight carries one rounding (weight_eps) and the exponential's 2^-20; a
+    weight too small for its format's normal range is off by at most tiny [D]
+    of the sum's unit, for each key; the two fp32 sums over n keys n 2^-24
+    each; the result one bf16 rounding."""
+    R, D = x.shape
+    out, lse = np.zeros((R, V.shape[1])), np.full(R, -np.inf)
+    tol_o, tol_l = np.zeros((R, V.shape[1])), np.zeros(R)
+    for r in range(R):
+        k, v = K[see[r]], V[see[r]]
+        if not len(k):
+            continue
+        s = (k @ x[r]) * scale
+        m = s.max()
+        w = np.exp(s - m)
+        den = w.sum()
+        out[r] = (w @ v) / den
+        lse[r] = m + np.log(den)
+        size = abs(scale) * (np.abs(k) @ np.abs(x[r])).max()
+        e_s = (D + 4) * 2.0 ** -24 * size + abs(scale) * np.abs(k).sum(1).max() * np.abs(x[r]).max() * q_lost
+        sums = (len(k) + 32) * 2.0 ** -24
+        tol_o[r] = (weight_eps + 2 * e_s + 2 * sums + 2.0 ** -18) * (w @ np.abs(v)) / den + len(k) * tiny \
+            + 2.0 ** -8 * np.abs(out[r]) + 1e-30
+        tol_l[r] = e_s + sums + 2.0 ** -19 + 2.0 ** -21 * abs(lse[r])
+    return out, lse, tol_o, tol_l
+
+
+def visible(n, length, first, window, sinks):
+    """[n, length]: which keys the n queries at positions first, first + 1, ... see."""
+    p, j = first + np.arange(n)[:, None], np.arange(length)[None]
+    return (j <= p) & ((window <= 0) | (j > p - window) | (j < sinks))
+
+
+def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0):
+    """Attention over the cache.  Weights are f16 (2^-11), in units in which
+    the largest is at least 2^6; what is below f16's normal range is off by
+    2^-25 of them, times the reference scale, at most 2^6 above the largest of
+    a value's page."""
+    T, H, D = q.shape
+    g = H // cache.heads
+    out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
+    tol_o, tol_l = np.zeros((T, H, D)), np.zeros((T, H))
+    pages = cache.codes.shape[0]
+    for b, length in enumerate(lens):
+        t0, t1 = start[b], start[b + 1]
+        n, length = t1 - t0, max(0, length)
+        at = np.arange(length)
+        col = at // cache.block
+        page = np.where(col < len(table[b]), np.asarray(table[b])[np.minimum(col, len(table[b]) - 1)], -1)
+        there = (page >= 0) & (page < pages)
+        page = np.where(there, page, 0)
+        see = np.repeat(visible(n, length, length - n, window, sinks) & there, g, 0)
+        for kh in range(cache.heads):
+            e = np.clip(cache.scales[page, :, kh].astype(int) - BIAS, LEAST, MOST)
+            code = cache.codes[page, :, at % cache.block, kh]
+            K, V = (e4m3(code[:, i]) * 2.0 ** e[:, i, None] for i in (0, 1))
+            tiny = 2.0 ** -25 * (2.0 ** e[:, 1].max() if length else 0.0) * 448
+            rows = q[t0:t1, kh * g:(kh + 1) * g].reshape(n * g, D)
+            got = attend(rows, K, V, see, scale, 2.0 ** -11, tiny)
+            for to, x in zip((out, lse, tol_o, tol_l), got):
+                to[t0:t1, kh * g:(kh + 1) * g] = x.reshape(n, g, *x.shape[1:])
+    return out, lse, tol_o, tol_l

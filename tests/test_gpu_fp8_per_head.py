@@ -238,3 +238,315 @@ def test_append_on_another_stream_and_in_a_graph(kvq):
     assert np.array_equal(bits_of(qo), got[0]) and np.array_equal(bits_of(ko), got[1])
     assert np.array_equal(case.cache.from_raw(cache.cpu().numpy()), got[2])
     assert np.array_equal(scales.cpu().numpy(), got[3])
+
+
+# --------------------------------------------------------------------------
+# attention over the cache
+# --------------------------------------------------------------------------
+
+def through_workspace(kvq, call, splits):
+    """The arguments of a call whose ranges join through a workspace, not in clusters."""
+    T, H, D = call["q"].shape
+    need = max(16, kvq.kvq_per_head_attention_workspace_bytes(T, H, D, splits))
+    return dict(call, num_splits=splits, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+
+
+class Batch:
+    """Requests with (context, new tokens), a shuffled block table, queries."""
+
+    def __init__(self, reqs, heads, kv_heads, dim, block, layout, seed, extra_tokens=0, q_scale=1.0, exponents=(-9, -6)):
+        rng = np.random.default_rng(seed)
+        self.reqs, self.rng, self.layout = reqs, rng, layout
+        self.lens = [c + n for c, n in reqs]
+        self.start = np.cumsum([0] + [n for _, n in reqs]).tolist()
+        total, self.table = pages_for(reqs, block, rng)
+        self.cache = ref.Cache(total, block, kv_heads, dim, layout, rng, exponents)
+        T = self.start[-1] + extra_tokens
+        self.q_bits = ref.to_bf16(rng.standard_normal((T, heads, dim)) * q_scale)
+        self.scale = dim ** -0.5
+
+    def device(self):
+        return dict(q=bf16_dev(self.q_bits), query_start=i32(self.start), seq_lens=i32(self.lens),
+                    block_table=dev(self.table.astype(np.int32)), kv_cache=dev(self.cache.raw()),
+                    kv_scales=dev(self.cache.scales), softmax_scale=self.scale,
+                    max_query_len=max([n for _, n in self.reqs] + [0]), max_seq_len=max(self.lens + [0]),
+                    layout=self.layout)
+
+    def want(self, **mask):
+        return ref.cached_attention(self.cache, ref.bf16(self.q_bits), self.start, self.lens, self.table, self.scale, **mask)
+
+
+def attend(kvq, call, splits, **mask):
+    """splits < 0: through a workspace; None: the default."""
+    if splits is not None:
+        call = dict(call, num_splits=splits) if splits > 0 else through_workspace(kvq, call, -splits)
+    return kvq.kvq_window_attention_fp8_per_head(**call, **mask)
+
+
+def check(got, want, rows=None):
+    out, lse, tol_o, tol_l = want
+    o, l = ref.bf16(bits_of(got[0])), got[1].cpu().numpy().astype(np.float64)
+    sl = slice(0, rows)
+    err = np.abs(o[sl] - out[sl])
+    assert np.all(err <= tol_o[sl]), f"out: worst error / tolerance {np.nanmax(err / tol_o[sl])}"
+    dead = np.isneginf(lse[sl])
+    assert np.array_equal(np.isneginf(l[sl]), dead)
+    le = np.abs(l[sl][~dead] - lse[sl][~dead])
+    assert np.all(le <= tol_l[sl][~dead]), f"lse: worst error / tolerance {np.max(le / tol_l[sl][~dead])}"
+
+
+SHAPES = [(64, "NHD", 4, 2, 16), (64, "HND", 7, 1, 24), (128, "NHD", 8, 2, 16), (128, "HND", 6, 3, 64), (128, "NHD", 5, 5, 1),
+          (256, "NHD", 4, 2, 32), (256, "HND", 3, 1, 24), (128, "HND", 32, 1, 48)]
+
+
+@pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (37, 4), (64, 40), (500, 1000)])
+@pytest.mark.parametrize("splits", [1, 3, -3, None])
+def test_decode(kvq, dim, layout, heads, kv, block, window, sinks, splits):
+    b = Batch([(0, 1), (31, 1), (32, 1), (300, 1), (129, 1), (1, 1)], heads, kv, dim, block, layout, 31 + dim + block)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = attend(kvq, b.device(), splits, window=window, num_sinks=sinks, status=status)
+    check(got, b.want(window=window, sinks=sinks))
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
+@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 1), (0, 0, -2), (29, 5, 1), (29, 5, -3), (100, 0, None)])
+def test_chunks(kvq, dim, layout, heads, kv, block, window, sinks, splits):
+    b = Batch([(0, 70), (65, 33), (200, 1), (7, 64), (0, 0), (130, 129)], heads, kv, dim, block, layout, 57 + dim + block)
+    check(attend(kvq, b.device(), splits, window=window, num_sinks=sinks), b.want(window=window, sinks=sinks))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("block", [8, 16, 64])
+@pytest.mark.parametrize("new", [1, 3, 40, 70])
+@pytest.mark.parametrize("splits", [1, 3, -2])
+def test_scales_far_apart(kvq, dim, block, new, splits):
+    """Pages whose scales differ by up to 2^30 either way, so that the references rise and fall."""
+    if splits > 1 and new > 8:
+        pytest.skip("clusters take few rows")
+    b = Batch([(700, new), (63, new)], 4, 1, dim, block, "NHD", 71 + dim + block + new)
+    pages = b.cache.scales.shape[0]
+    b.cache.scales[:, 0] = (127 - 7 + b.rng.integers(-3, 2, (pages, 1))).astype(np.uint8)
+    b.cache.scales[:, 1] = (127 - 7 + b.rng.choice([0, 0, 1, -1, 5, 9, -8, 15, -15], (pages, 1))).astype(np.uint8)
+    check(attend(kvq, b.device(), splits), b.want())
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_scales_at_and_past_the_ends(kvq, new):
+    """The least and the largest scale, and bytes outside them, which read as the nearer one."""
+    b = Batch([(200, new), (90, new)], 4, 2, 128, 16, "HND", 83, q_scale=1.0)
+    pages = b.cache.scales.shape[0]
+    b.cache.scales[:, 0] = 127 - 9
+    b.cache.scales[:, 1] = b.rng.choice([0, 66, 67, 70], (pages, 2)).astype(np.uint8)
+    check(attend(kvq, b.device(), None), b.want())
+    b.cache.scales[:, 1] = b.rng.choice([255, 188, 187, 180], (pages, 2)).astype(np.uint8)
+    check(attend(kvq, b.device(), None), b.want())
+    b.cache.scales[:, 0] = b.rng.choice([0, 67, 80], (pages, 2)).astype(np.uint8)     # scores of about zero
+    check(attend(kvq, b.device(), None, window=50), b.want(window=50))
+
+
+@pytest.mark.parametrize("new", [1, 130])
+@pytest.mark.parametrize("splits", [1, 5, -5])
+def test_padded_requests_see_nothing_and_other_rows_are_left(kvq, new, splits):
+    if splits > 1 and new > 8:
+        pytest.skip("clusters take few rows")
+    b = Batch([(50, new), (0, new), (90, new)], 8, 2, 128, 16, "NHD", 91, extra_tokens=5)
+    b.lens[1] = 0                                                     # its queries have negative positions
+    call = b.device()
+    out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
+    lse = torch.full(b.q_bits.shape[:2], 7.5, device=DEV)
+    got = attend(kvq, dict(call, out=out, lse=lse), splits)
+    live = b.start[-1]
+    check(got, b.want(), live)
+    assert np.all(bits_of(out)[live:] == CANARY) and bool((lse[live:] == 7.5).all())
+    assert bool((out[b.start[1]:b.start[2]] == 0).all()) and bool(torch.isneginf(lse[b.start[1]:b.start[2]]).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("splits", [1, -4])
+def test_hidden_entries_have_no_effect(kvq, dim, new, splits):
+    """NaN codes wherever no query sees them: page tails, pages of no request, positions before the windows."""
+    b = Batch([(130, new), (40, new)], 4, 2, dim, 16, "NHD", 97 + dim)
+    mask = dict(window=50, sinks=3)
+    want = b.want(**mask)
+    clean = b.device()
+    seen = np.zeros(b.cache.codes.shape[:1] + (16,), bool)
+    for r, length in enumerate(b.lens):
+        first = length - new
+        for p in range(length):
+            if p < 3 or p > first - 50:
+                seen[b.table[r, p // 16], p % 16] = True
+    codes = b.cache.codes.copy()
+    b.cache.codes = np.where(seen[:, None, :, None, None], codes, 0xFF).astype(np.uint8)
+    call = dict(clean, kv_cache=dev(b.cache.raw()))
+    got = attend(kvq, call, splits, window=50, num_sinks=3)
+    check(got, want)
+    same = attend(kvq, clean, splits, window=50, num_sinks=3)
+    assert np.array_equal(bits_of(got[0]), bits_of(same[0])) and torch.equal(got[1], same[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [5, 70])
+def test_later_tokens_nan_does_not_reach_earlier_rows(kvq, dim, new):
+    b = Batch([(40, new)], 4, 2, dim, 16, "NHD", 101 + dim)
+    want = b.want()
+    p = 40 + new - 2                                                  # the last but one
+    b.cache.codes[b.table[0, p // 16], :, p % 16] = 0x7F
+    got = attend(kvq, b.device(), None)
+    out, lse = ref.bf16(bits_of(got[0])), got[1].cpu().numpy()
+    assert np.all(np.abs(out[:new - 2] - want[0][:new - 2]) <= want[2][:new - 2])
+    assert np.all(np.isfinite(lse[:new - 2])) and np.all(np.isnan(lse[new - 2:])) and np.all(np.isnan(out[new - 2:]))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_bad_pages_and_requests(kvq, new):
+    b = Batch([(100, new), (60, new), (50, new), (200, new)], 8, 2, 128, 16, "HND", 103)
+    b.table[0, 2] = -1
+    b.table[1, 1] = b.cache.codes.shape[0]
+    b.table = b.table[:, :10].copy()                                  # request 3 goes past the table
+    want = b.want()
+    call = b.device()
+    call["query_start"][3] += new + 1                                 # 2: too many tokens, 3: a negative range
+    out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = attend(kvq, dict(call, out=out, status=status), None)
+    check(got, want, 2 * new)
+    assert np.all(bits_of(out)[2 * new:] == CANARY)
+    assert int(status.item()) == kvq.STATUS_BAD_INDEX | kvq.STATUS_BAD_BATCH
+    call = b.device()
+    status.zero_()
+    check(attend(kvq, dict(call, status=status), None), want)
+    assert int(status.item()) == kvq.STATUS_BAD_INDEX
+
+
+@pytest.mark.parametrize("new", [2, 90])
+def test_strides_and_extreme_queries(kvq, new):
+    """Queries and outputs as slices of wider rows; rows of zeros, of the largest and of the smallest values."""
+    b = Batch([(60, new), (33, new)], 6, 2, 64, 16, "NHD", 107)
+    b.q_bits[0] = 0
+    b.q_bits[1, 0] = ref.to_bf16(np.full(64, 1e-38))
+    b.q_bits[1, 1] = ref.to_bf16(np.full(64, 3e30))
+    b.q_bits[1, 1, 1:] = ref.to_bf16(np.full(63, 1e-30))
+    b.scale = 1e-31
+    call = b.device()
+    T = b.q_bits.shape[0]
+    wide = torch.zeros((T, 10, 64), dtype=torch.bfloat16, device=DEV)
+    wide[:, 2:8] = call["q"]
+    outs = torch.zeros((T, 9, 64), dtype=torch.bfloat16, device=DEV)
+    lses = torch.zeros((T, 11), device=DEV)
+    got = attend(kvq, dict(call, q=wide[:, 2:8], out=outs[:, 1:7], lse=lses[:, 3:9]), None)
+    check(got, b.want())
+    assert bool((outs[:, 0] == 0).all()) and bool((outs[:, 7:] == 0).all()) and bool((lses[:, :3] == 0).all())
+    for scale in (0.0, -0.125):
+        b.scale = scale
+        b.q_bits[1, 1] = b.q_bits[2, 1]
+        check(attend(kvq, b.device(), None, window=20), b.want(window=20))
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_offsets_past_32_bits(kvq, new):
+    """Pages beyond the first 4 GB of the cache."""
+    block, kv, dim = 64, 8, 128
+    pages = (1 << 32) // (2 * block * kv * dim) + 40
+    b = Batch([(150, new)], 8, kv, dim, block, "NHD", 109)
+    raw = torch.zeros((pages, 2, block, kv, dim), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros((pages, 2, kv), dtype=torch.uint8, device=DEV)
+    call = b.device()
+    want = b.want()
+    used = b.table[0][b.table[0] >= 0]
+    moved = {int(p): pages - 1 - 3 * i for i, p in enumerate(used)}
+    for p, to in moved.items():
+        raw[to], scales[to] = call["kv_cache"][p], call["kv_scales"][p]
+    b.table = np.array([[moved.get(int(p), -1) for p in b.table[0]]])
+    call = dict(call, kv_cache=raw, kv_scales=scales, block_table=dev(b.table.astype(np.int32)))
+    check(attend(kvq, call, None), want)
+    # and appended there
+    key = torch.randn((new, kv, dim), device=DEV).to(torch.bfloat16)
+    kvq.kvq_rope_append_fp8_per_head(None, key, key, torch.zeros(new, dtype=torch.int64, device=DEV),
+                                     torch.cat([torch.ones((1, 8)), torch.zeros((1, 8))], 1).to(DEV), i32([0, new]),
+                                     i32([150 + new]), call["block_table"], raw, scales, new)
+    p = 150 + new - 1
+    page = int(b.table[0, p // block])
+    e = scales[page, 1].float() - 127
+    back = raw[page, 1, p % block].view(torch.float8_e4m3fn).float() * torch.exp2(e)[:, None]
+    assert bool(((back - key[-1].float()).abs() <= 2.0 ** -4 * key[-1].float().abs() + 2.0 ** -10 * torch.exp2(e)[:, None]).all())
+
+
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 1), (256, 1), (128, 8), (128, 80)])
+def test_long_sequences_with_default_splits(kvq, dim, new):
+    b = Batch([(5000, new), (17, new), (2900, new)], 8, 2, dim, 64, "NHD", 113)
+    check(attend(kvq, b.device(), None), b.want())
+
+
+@pytest.mark.parametrize("dim,layout", [(64, "HND"), (128, "NHD"), (256, "NHD")])
+@pytest.mark.parametrize("new", [1, 2, 20, 40])
+@pytest.mark.parametrize("splits", [1, -2])
+def test_rows_whose_maximum_grows(kvq, dim, layout, new, splits):
+    """Scores that rise along the keys, past every reference, and fall again."""
+    b = Batch([(450, new), (200, new)], 4, 2, dim, 16, layout, 127 + dim + new)
+    for r, length in enumerate(b.lens):
+        for col in range(-(-length // 16)):
+            b.cache.scales[b.table[r, col], 0] = 127 - 16 + min(col // 2, 9)
+    check(attend(kvq, b.device(), splits), b.want())
+
+
+@pytest.mark.parametrize("dim,heads,kv,new", [(64, 6, 2, 11), (64, 6, 2, 21), (64, 6, 2, 22), (128, 8, 2, 8), (128, 8, 2, 9),
+                                              (256, 8, 2, 4), (256, 8, 2, 5), (128, 14, 2, 4)])
+@pytest.mark.parametrize("splits", [1, -2, None])
+def test_rows_on_both_sides_of_the_kernels_limits(kvq, dim, heads, kv, new, splits):
+    b = Batch([(300, new), (77, new)], heads, kv, dim, 16, "NHD", 131)
+    check(attend(kvq, b.device(), splits), b.want())
+
+
+@pytest.mark.parametrize("dim,heads,kv,new", [(64, 8, 2, 3), (128, 8, 2, 3), (128, 14, 2, 4), (256, 8, 2, 3)])
+def test_many_requests_of_a_few_rows(kvq, dim, heads, kv, new):
+    """Enough requests that blocks of 16 rows fill the GPU."""
+    b = Batch([(int(c), new) for c in np.random.default_rng(5).integers(0, 40, 300)], heads, kv, dim, 16, "NHD", 137)
+    check(attend(kvq, b.device(), None), b.want())
+
+
+@pytest.mark.parametrize("new,splits", [(1, 4), (1, -4), (1, 1), (40, 1), (40, -3)])
+def test_graphs_and_streams(kvq, new, splits):
+    b = Batch([(300, new), (90, new)], 8, 2, 128, 16, "NHD", 139)
+    call = b.device()
+    want = attend(kvq, call, splits)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = attend(kvq, dict(call, stream=side), splits)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits_of(got[0]), bits_of(want[0])) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        inside = attend(kvq, call, splits)
+    call["q"].copy_(call["q"].flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    again = attend(kvq, call, splits)
+    assert np.array_equal(bits_of(inside[0]), bits_of(again[0])) and torch.equal(inside[1], again[1])
+
+
+def test_attention_refuses_what_does_not_fit(kvq):
+    call = Batch([(30, 1)], 4, 2, 64, 16, "NHD", 149).device()
+
+    def refused(kind, match, **over):
+        with pytest.raises(kind, match=match):
+            kvq.kvq_window_attention_fp8_per_head(**{**call, **over})
+
+    refused(ValueError, "kv_scales", kv_scales=None)
+    refused(ValueError, "kv_scales", kv_scales=call["kv_scales"].float())
+    refused(ValueError, "kv_scales", kv_scales=call["kv_scales"][:-1])
+    refused(ValueError, "kv_scales", kv_scales=call["kv_scales"].transpose(0, 1).contiguous().transpose(0, 1))
+    refused(ValueError, "kv_scales", kv_scales=call["kv_scales"].cpu())
+    refused(ValueError, "kv_cache", kv_cache=call["kv_cache"][..., :32])
+    refused(ValueError, "kv_cache", kv_cache=call["kv_cache"].float())
+    refused(ValueError, "kv_cache", layout="HND", kv_cache=call["kv_cache"][:, :, :, :1])
+    refused(ValueError, "layout", layout="XYZ")
+    refused(ValueError, "q", q=call["q"].float())
+    refused(ValueError, "seq_lens", seq_lens=call["seq_lens"].long())
+    refused(ValueError, "query_start", query_start=call["query_start"][:1])
+    refused(RuntimeError, "num_heads", q=call["q"][:, :3])
+    refused(RuntimeError, "num_splits", num_splits=129)
+    refused(RuntimeError, "softmax_scale", softmax_scale=float("nan"))
+    refused(RuntimeError, "num_sinks", num_sinks=-1)
