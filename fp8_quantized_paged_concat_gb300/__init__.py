@@ -36,7 +36,7 @@ __all__ = [
     "kvq_per_head_attention_default_splits",
     "PER_HEAD_MAX_SPLITS", "PER_HEAD_CLUSTER_SPLITS",
     "kvq_rope_append_fp8_per_head", "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits",
-    "FP8_SCALE_BIAS",
+    "FP8_SCALE_BIAS", "kvq_prompt_attention",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -120,6 +120,8 @@ _SIGNATURES = {
                                           _I32, _I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64,
                                           _I32, _I32, _P, _I64, _P, _P],
     "kvq_fp8_attention_default_splits": [_I32] * 8 + [_P],
+    "kvq_prompt_attention": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32,
+                             ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P],
     "kvq_compact_drafts_nvfp4_per_head": [_P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
                                           _I32, _P, _I64, _I32, _P, _P],
 }
@@ -598,7 +600,7 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 _native = None
 _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
                    "kvq_compact_drafts_nvfp4_per_head", "kvq_rope_append_fp8_per_head",
-                   "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits",
+                   "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits", "kvq_prompt_attention",
                    "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
 
 
@@ -747,6 +749,19 @@ def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, kv_scales, False,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)
+
+
+def kvq_prompt_attention(q, k, v, seq_start, softmax_scale: float, max_seq_len: int, window: int = 0, num_sinks: int = 0,
+                         out=None, lse=None, status=None, stream=None):
+    """Causal attention over whole prompts, whose keys and values are at hand
+    in bf16: q bf16 [T, H, D], k and v bf16 [T, KH, D] (any token and head
+    strides, as slices of a packed projection have); sequence b is the rows
+    [seq_start[b], seq_start[b+1]) (int32 [B+1], at most max_seq_len each),
+    with a sliding window (window <= 0: none) and num_sinks first tokens that
+    stay visible.  Rows of no sequence are left as they are.  Returns (out
+    bf16 [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
+    return (_native or _load_native()).prompt(q, k, v, seq_start, softmax_scale, max_seq_len, window, num_sinks, out, lse,
+                                              status, stream)
 
 
 def kvq_selftest_convert(first_bits: int, count: int, device="cuda", stream=None):

@@ -1216,6 +1216,74 @@ kvq_status kvq_rope_append_fp8_per_head(
   return launched(fn, kvq::launch_rope_append(a, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+kvq_status kvq_prompt_attention(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t,
+                                int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                                int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                                const int32_t* seq_start, int32_t batch_size, int32_t max_seq_len, float softmax_scale,
+                                int32_t window, int32_t num_sinks, void* out, int64_t out_stride_t,
+                                int64_t out_stride_h, float* lse, int64_t lse_stride_t, int32_t* d_status,
+                                kvq_stream_t stream) {
+  const char* fn = "kvq_prompt_attention";
+  KVQ_REQUIRE(num_tokens >= 0 && batch_size >= 0 && max_seq_len >= 0,
+              "%s: num_tokens, batch_size and max_seq_len must be >= 0", fn);
+  KVQ_REQUIRE(num_sinks >= 0, "%s: num_sinks must be >= 0", fn);
+  if (num_tokens == 0 || batch_size == 0 || max_seq_len == 0) return ok();
+  KVQ_REQUIRE(head_size == 64 || head_size == 128 || head_size == 256,
+              "%s: head_size must be 64, 128 or 256 (got %d)", fn, head_size);
+  KVQ_REQUIRE(num_kv_heads > 0 && num_heads > 0 && num_heads % num_kv_heads == 0,
+              "%s: num_heads must be a positive multiple of num_kv_heads (got %d, %d)", fn, num_heads, num_kv_heads);
+  KVQ_REQUIRE(batch_size <= 65535, "%s: batch_size must be at most 65535", fn);
+  KVQ_REQUIRE(num_tokens * num_heads < (int64_t{1} << 31) - (int64_t{1} << 16) * num_kv_heads &&
+                  std::min<int64_t>(num_tokens, max_seq_len) < (int64_t{1} << 31) - 256,
+              "%s: num_tokens * num_heads (and 65536 * num_kv_heads beside it) must stay below 2^31", fn);
+  if (kvq_status s = check_heads(fn, "q", q, q_stride_t, q_stride_h, num_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "k", k, k_stride_t, k_stride_h, num_kv_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "v", v, v_stride_t, v_stride_h, num_kv_heads, head_size, false)) return s;
+  if (kvq_status s = check_heads(fn, "out", out, out_stride_t, out_stride_h, num_heads, head_size, true)) return s;
+  constexpr int64_t kMost = int64_t{1} << 38;        // bytes of a copied tensor's stride: below 2^40
+  KVQ_REQUIRE(k_stride_t > 0 && v_stride_t > 0 && k_stride_t < kMost && v_stride_t < kMost && k_stride_h < kMost &&
+                  v_stride_h < kMost,
+              "%s: k and v strides must be positive and below 2^38", fn);
+  KVQ_REQUIRE(lse == nullptr || (aligned(lse, 4) && lse_stride_t >= num_heads),
+              "%s: lse must be 4-byte aligned with token stride >= num_heads", fn);
+  KVQ_REQUIRE(seq_start != nullptr && aligned(seq_start, 4), "%s: seq_start must be non-NULL and 4-byte aligned", fn);
+  const double scale_log2 = static_cast<double>(softmax_scale) * 1.4426950408889634074;
+  KVQ_REQUIRE(std::fabs(scale_log2) <= std::numeric_limits<float>::max(),
+              "%s: softmax_scale must be finite, its product with log2(e) as well", fn);
+  KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
+  if (kvq_status s = check_device(fn)) return s;
+  kvq::PromptAttentionArgs a{};
+  a.q = q;
+  a.q_stride_t = q_stride_t;
+  a.q_stride_h = q_stride_h;
+  a.k = k;
+  a.k_stride_t = k_stride_t;
+  a.k_stride_h = k_stride_h;
+  a.v = v;
+  a.v_stride_t = v_stride_t;
+  a.v_stride_h = v_stride_h;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_size = head_size;
+  a.group = num_heads / num_kv_heads;
+  a.group_div = kvq::FastDiv::make(static_cast<uint32_t>(a.group));
+  a.kv_heads_div = kvq::FastDiv::make(static_cast<uint32_t>(num_kv_heads));
+  a.seq_start = seq_start;
+  a.batch_size = batch_size;
+  a.max_seq_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, num_tokens));
+  a.scale_log2 = static_cast<float>(scale_log2);
+  a.window = window;
+  a.num_sinks = num_sinks;
+  a.out = out;
+  a.out_stride_t = out_stride_t;
+  a.out_stride_h = out_stride_h;
+  a.lse = lse;
+  a.lse_stride_t = lse_stride_t;
+  a.status = d_status;
+  return launched(fn, kvq::launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* kvq_last_error_string(void) { return g_last_error.c_str(); }
 
 int32_t kvq_version(void) { return 100; }

@@ -63,7 +63,6 @@
 // long limit) for the MMAs in flight, frees its TMEM, leaves its outputs
 // unwritten and returns.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -71,6 +70,7 @@
 #include "kvq.h"
 #include "kvq_launch.h"
 #include "kvq_tcgen05.cuh"
+#include "kvq_tensor_map.h"
 
 namespace kvq {
 namespace {
@@ -1097,20 +1097,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_splits_kernel(cons
 }
 
 }  // namespace
-
-// The driver's tensor-map encoder, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
 
 // Tensor map of the query rows, tiles of 64 dimensions x 128 rows with the
 // 128-byte swizzle: sparse form [tokens][heads][576] (a tile is 128 heads of

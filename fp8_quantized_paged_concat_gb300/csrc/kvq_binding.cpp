@@ -39,6 +39,7 @@ struct Library {
   decltype(&kvq_compact_drafts_nvfp4_per_head) compact = nullptr;
   decltype(&kvq_rope_append_fp8_per_head) append = nullptr;
   decltype(&kvq_window_attention_fp8_per_head) fp8_window = nullptr;
+  decltype(&kvq_prompt_attention) prompt = nullptr;
   decltype(&kvq_fp8_attention_default_splits) fp8_default_splits = nullptr;
   decltype(&kvq_per_head_attention_workspace_bytes) workspace_bytes = nullptr;
   decltype(&kvq_per_head_attention_default_splits) default_splits = nullptr;
@@ -534,6 +535,44 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// q, k, v, seq_start, softmax_scale, max_seq_len, window, num_sinks, out, lse (False: none), status, stream
+PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const at::Tensor& q = tensor("q", a[0]);
+    const int dev = device_of("q", q);
+    check("q", q, at::kBFloat16, dev, 3);
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+    const at::Tensor &k = tensor("k", a[1]), &v = tensor("v", a[2]);
+    check("k", k, at::kBFloat16, dev, 3);
+    const int64_t KH = k.size(1);
+    shaped("k", k, {T, KH, D});
+    check("v", v, at::kBFloat16, dev, 3);
+    shaped("v", v, {T, KH, D});
+    const at::Tensor& start = tensor("seq_start", a[3]);
+    check("seq_start", start, at::kInt, dev, 1);
+    if (start.size(0) < 1) bad("seq_start: expected at least one element");
+    const float scale = real(a[4]);
+    const int32_t max_seq = int32("max_seq_len", a[5]), window = int32("window", a[6]), sinks = int32("num_sinks", a[7]);
+    const Scope scope(a[11], dev);
+    const at::Tensor out = a[8] == Py_None ? scope.result({T, H, D}, at::kBFloat16) : tensor("out", a[8]);
+    check("out", out, at::kBFloat16, dev, 3);
+    shaped("out", out, {T, H, D});
+    at::Tensor lse;
+    if (a[9] != Py_False) {
+      lse = a[9] == Py_None ? scope.result({T, H}, at::kFloat) : tensor("lse", a[9]);
+      check("lse", lse, at::kFloat, dev, 2);
+      shaped("lse", lse, {T, H});
+    }
+    const Strides sq = head_strides(q), sk = head_strides(k), sv = head_strides(v), so = head_strides(out);
+    must(lib.prompt(q.data_ptr(), sq.t, sq.h, k.data_ptr(), sk.t, sk.h, v.data_ptr(), sv.t, sv.h, T, dim(H), dim(KH),
+                    dim(D), static_cast<const int32_t*>(start.data_ptr()), dim(start.size(0) - 1), max_seq, scale, window,
+                    sinks, out.data_ptr(), so.t, so.h, lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                    lse.defined() ? row_stride(lse) : 0, status_word(a[10], dev), scope.stream()),
+         "kvq_prompt_attention");
+    return pair(out, &lse);
+  });
+}
+
 // bind({entry point: address}): the library whose entry points the calls use
 PyObject* bind(PyObject*, PyObject* table) {
   Library found;
@@ -550,6 +589,7 @@ PyObject* bind(PyObject*, PyObject* table) {
       !set("kvq_compact_drafts_nvfp4_per_head", found.compact) ||
       !set("kvq_rope_append_fp8_per_head", found.append) ||
       !set("kvq_window_attention_fp8_per_head", found.fp8_window) ||
+      !set("kvq_prompt_attention", found.prompt) ||
       !set("kvq_fp8_attention_default_splits", found.fp8_default_splits) ||
       !set("kvq_per_head_attention_workspace_bytes", found.workspace_bytes) ||
       !set("kvq_per_head_attention_default_splits", found.default_splits) ||
@@ -564,6 +604,7 @@ PyMethodDef methods[] = {
     {"norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_rope)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attention)), METH_FASTCALL, nullptr},
     {"compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(compact)), METH_FASTCALL, nullptr},
+    {"prompt", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prompt)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

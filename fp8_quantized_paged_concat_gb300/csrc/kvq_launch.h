@@ -279,6 +279,34 @@ struct AppendArgs {
 };
 cudaError_t launch_rope_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
 
+// Attention over whole prompts: sequence b is the rows [seq_start[b],
+// seq_start[b+1]) of q, k, v and out.
+struct PromptAttentionArgs {
+  const void* q;                  // bf16 [num_tokens, num_heads, head_size]
+  int64_t q_stride_t, q_stride_h;
+  const void* k;                  // bf16 [num_tokens, num_kv_heads, head_size]
+  int64_t k_stride_t, k_stride_h;
+  const void* v;
+  int64_t v_stride_t, v_stride_h;
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads, head_size;
+  int32_t group;                  // num_heads / num_kv_heads query heads share a key head
+  FastDiv group_div;
+  FastDiv kv_heads_div;
+  const int32_t* seq_start;       // [batch_size + 1]
+  int32_t batch_size;
+  int32_t max_seq_len;
+  float scale_log2;               // softmax_scale * log2(e)
+  int32_t window;                 // <= 0: none
+  int32_t num_sinks;
+  void* out;
+  int64_t out_stride_t, out_stride_h;
+  float* lse;
+  int64_t lse_stride_t;
+  int32_t* status;
+};
+cudaError_t launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t stream);
+
 struct CompactArgs {
   uint8_t* cache;
   int32_t num_layers;

@@ -98,13 +98,6 @@ struct Shape {
   static_assert(kTiles * D <= 256 && kMisc % 16 == 0, "tensor memory, alignment");
 };
 
-// warp_wait_or_abort whose usual case, the phase complete already, takes one
-// test, without the clock, the loop and the suspension of a waiting try
-// (trees 32 x 64: 576 -> 566 us).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* s_abort) {
-  return __all_sync(kFull, mbar_test_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
-}
-
 // The CTA's set-up is done (tensor memory, barriers): every role comes here
 // once, after what it can start before.
 __device__ __forceinline__ void set_up_done() {
@@ -117,12 +110,6 @@ __device__ __forceinline__ void set_up_done() {
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// Bits i (0..31) with lo <= p0 + i <= hi.
-__device__ __forceinline__ uint32_t range_bits(int32_t p0, int32_t lo, int32_t hi) {
-  const int32_t a = max(lo - p0, 0), b = min(hi - p0, 31);
-  return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
 }
 
 // Bits d .. d + 31 of a mask row (bits outside it are 0).

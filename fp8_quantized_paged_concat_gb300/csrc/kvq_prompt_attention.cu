@@ -1,0 +1,628 @@
+// kvq_prompt_attention.cu -- causal attention over whole prompts: packed
+// sequences of different lengths, grouped query heads, a sliding window and a
+// few first tokens that stay visible.  For query row (token i, head h) of a
+// sequence, over its tokens j <= i with window <= 0 or j > i - window or j <
+// num_sinks, and key head h / group:
+//   s_j = softmax_scale * (q . k_j),  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
+//   lse = m + ln sum_j exp(s_j - m).
+// The products bound it: 4 D flops for each (row, visible key).
+//
+// Design: one CTA per SM, for (block of 128 kTiles query rows, key head,
+// sequence); the rows are (token, head) pairs of the sequence that share the
+// key head, so that every tile of keys serves the whole group.
+//   - tensor memory: O of row tile w in columns [D w, +D), two score buffers
+//     of kKeys columns from column 256 on: with two row tiles one each, with
+//     one row tile taken in turn.  A buffer's weights P (bf16) overwrite its
+//     first half.
+//   - one warp issues the products, in the order S(0) S(1) [PV(0) S(2)] [PV(1)
+//     S(3)] ... over the (row tile, key tile) pairs: while the weights of one
+//     are computed, the products of the other run.  The tensor core takes them
+//     in that order, so that S(i + 2) needs no wait for the PV(i) that reads
+//     its buffer.
+//   - one warp has the copy engine land the tiles of K and V (tensor maps,
+//     128-byte swizzle), two the query rows (their order is not a box's).
+//   - four softmax warps per row tile, one thread per row, one pass over the
+//     scores: the weights are formed against the reference maximum of the tiles
+//     before, without a maximum of their own; only when their sum shows that
+//     one of them exceeds it by more than 2^kGrow is the tile's maximum taken,
+//     the pass repeated and O rescaled.  (bf16 weights have fp32's range, so
+//     that a reference far behind costs no precision.)
+//   - a tile's copy may bring rows that no query sees: the next sequence's,
+//     padding, or later tokens.  Their scores are replaced, and their values,
+//     whose weight is 0, are made harmless in shared memory: rows past the
+//     sequence are zeroed, and in tiles that some row does not see whole NaN
+//     and infinities are (one warp looks through them).
+// Every wait of a role on another role or on its products is bounded; on
+// expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
+// frees its tensor memory and leaves its rows unwritten.
+#include <type_traits>
+
+#include "kvq_per_head_attention.cuh"
+#include "kvq_tensor_map.h"
+
+namespace kvq {
+namespace {
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 256;
+constexpr float kMaxSum = 16777216.0f;            // 2^24: weights against a reference this far behind are still finite
+constexpr int kSlots = 2;                         // work items known at once
+
+template <int D, int kTiles>
+struct Shape {
+  static constexpr int kKeys = D == 256 ? 64 : 128;          // keys per tile
+  static constexpr int kSoftmaxWarps = 4 * kTiles;
+  static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kQueryWarp = kProductWarp + 1;
+  static constexpr int kQueryWarps = 2, kCheckWarp = kQueryWarp + 1;
+  static constexpr int kWarps = kQueryWarp + kQueryWarps;
+  static constexpr int kThreads = 32 * kWarps;
+  // (two row tiles: 168 registers a thread at launch, split by role)
+  static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+  static_assert(kTiles == 1 || 32 * kSoftmaxWarps * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+  static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
+  static constexpr int kStages = 2;                          // tiles of K, of V
+  static constexpr uint32_t kQBlock = 128 * 128;             // 64 dimensions of a row tile
+  static constexpr uint32_t kQTile = kBlocks * kQBlock;
+  static constexpr uint32_t kKBlock = kKeys * 128;           // 64 dimensions of a key tile
+  static constexpr uint32_t kTileBytes = kBlocks * kKBlock;
+  static constexpr uint32_t kK = kTiles * kQTile;
+  static constexpr uint32_t kV = kK + kStages * kTileBytes;
+  static constexpr uint32_t kOut = kV + kStages * kTileBytes;          // 4 KB of output rows per softmax warp
+  static constexpr uint32_t kMisc = kOut + kSoftmaxWarps * 4096;
+  // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
+  static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+  static_assert(kTiles * D <= 256 && kSCol + 2 * kKeys <= kTmemCols, "tensor memory");
+};
+
+// What a CTA works on at a time.
+struct Item {
+  int32_t token0;              // the sequence's first token
+  int32_t n;                   // its tokens
+  int32_t row0, rows;          // the block of its rows; rows = 0: no more items
+  int32_t head;                // key head
+};
+
+// The keys that some token in [t0, t1] of a sequence of n sees.
+template <int kKeys>
+__device__ __forceinline__ Keys<kKeys> prompt_keys(const PromptAttentionArgs& a, int32_t t0, int32_t t1) {
+  Keys<kKeys> k;
+  k.hi = t1 + 1;
+  k.lo = a.window > 0 ? max(0, t0 - a.window + 1) : 0;
+  k.sinks = min(a.num_sinks, k.lo);
+  k.sink_steps = (k.sinks + kKeys - 1) / kKeys;
+  k.steps = k.sink_steps + (k.hi - k.lo + kKeys - 1) / kKeys;
+  return k;
+}
+
+// The block of rows with number `index` of all key heads' blocks.  Sequence b's
+// blocks have the numbers from first(b) = floor(seq_start[b] group / block) + b
+// on: those of the sequences before it are fewer.  The last blocks of a
+// sequence, which see the most keys, come first.  One warp looks b up.
+template <int kBlock>
+__device__ __forceinline__ Item item_at(const PromptAttentionArgs& a, uint32_t index, int lane) {
+  const uint32_t j = a.kv_heads_div.div(index);
+  Item it{};
+  it.head = static_cast<int32_t>(index - j * a.num_kv_heads);
+  auto first = [&](int32_t b) {
+    return static_cast<int64_t>(load_global(a.seq_start + b)) * a.group / kBlock + b;
+  };
+  // the largest b < batch_size with first(b) <= j, 32 candidates at a time
+  int32_t lo = 0, hi = a.batch_size;                 // first(lo) <= j (or lo = 0), first(hi) > j (or hi = batch_size)
+  while (hi - lo > 1) {
+    const int32_t step = (hi - lo + 31) / 32, b = lo + step * lane;
+    const uint32_t below = __ballot_sync(kFull, b < hi && (lane == 0 || first(b) <= j));
+    const int32_t at = 31 - __clz(below);            // (lane 0 always is)
+    hi = min(hi, lo + step * (at + 1));
+    lo = lo + step * at;
+  }
+  const int32_t q0 = load_global(a.seq_start + lo), q1 = load_global(a.seq_start + lo + 1);
+  const int64_t n = static_cast<int64_t>(q1) - q0;
+  if (q0 < 0 || n < 0 || q1 > a.num_tokens || n > a.max_seq_len) {
+    if (lane == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
+    return it;
+  }
+  const int64_t total = n * a.group, blocks = (total + kBlock - 1) / kBlock;
+  const int64_t mine = blocks - 1 - (static_cast<int64_t>(j) - (static_cast<int64_t>(q0) * a.group / kBlock + lo));
+  if (mine < 0 || mine >= blocks) return it;
+  it.token0 = q0;
+  it.n = static_cast<int32_t>(n);
+  it.row0 = static_cast<int32_t>(mine * kBlock);
+  it.rows = static_cast<int32_t>(min(static_cast<int64_t>(kBlock), total - mine * kBlock));
+  return it;
+}
+
+template <int D, int kTiles>
+__global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
+    prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<D, kTiles>;
+  constexpr int kKeys = S::kKeys;
+  constexpr int kBlock = 128 * kTiles;
+  wait_for_previous();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bar = base + S::kMisc;
+  const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_good = bar + 48, v_empty = bar + 64;   // [kStages]
+  const uint32_t s_full = bar + 80, p_full = bar + 96, o_done = bar + 112;      // [score buffer]
+  const uint32_t o_free = bar + 128;                                            // [row tile]
+  const uint32_t q_full = bar + 144, q_free = bar + 152, drain = bar + 160;
+  const uint32_t item_full = bar + 168, item_free = bar + 184;                  // [kSlots]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 200);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 204);
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 208);
+  static_assert(208 + kSlots * sizeof(Item) <= 512, "barrier layout");
+
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(s_tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_good + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+      mbar_init(o_free + 8 * i, 4);
+      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_free + 8 * i, S::kWarps - 1);
+    }
+    mbar_init(q_full, S::kQueryWarps);
+    mbar_init(q_free, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  allow_dependents();
+  const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
+
+  auto have = [&](uint32_t bar, uint32_t phase) {
+    const bool ok = warp_wait(bar, phase & 1, s_abort);
+    fence_after_sync();
+    return ok;
+  };
+  // Item number k of this CTA (false: none, or given up).
+  auto next_item = [&](uint32_t k, Item& it) {
+    if (!have(item_full + 8 * (k % kSlots), k / kSlots)) return false;
+    const volatile Item& s = items[k % kSlots];
+    it.token0 = s.token0;
+    it.n = s.n;
+    it.row0 = s.row0;
+    it.rows = s.rows;
+    it.head = s.head;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_free + 8 * (k % kSlots));
+    return it.rows > 0;
+  };
+  auto keys_of_item = [&](const Item& it) {
+    return prompt_keys<kKeys>(a, static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0))),
+                              static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0 + it.rows - 1))));
+  };
+  // Steps [full0, full1) of the keys are visible whole to every row with a
+  // last key of at least hi and a first (but for the sinks) of at most lo.
+  auto full_steps = [&](const Keys<kKeys>& keys, int32_t hi, int32_t lo, int32_t& full0, int32_t& full1) {
+    full0 = keys.sink_steps + (max(lo - keys.lo, 0) + kKeys - 1) / kKeys;
+    const int32_t whole = min(hi, keys.hi - 1) + 1 - keys.lo;           // positions from keys.lo on
+    full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
+  };
+
+  Item it;
+  if (warp < S::kSoftmaxWarps) {
+    // ---- softmax: thread = query row ----------------------------------------
+    if constexpr (kTiles == 2) more_registers<S::kSoftmaxRegs>();
+    const int tile = warp >> 2;
+    const uint32_t lanes = (warp & 3) * 32u << 16;
+    const uint32_t o_col = tmem + lanes + tile * D;
+    const float sc = a.scale_log2;
+    uint32_t pairs = 0;                             // (row tile, key tile) pairs of the items before
+    for (uint32_t k = 0; next_item(k, it); ++k) {
+      const Keys<kKeys> keys = keys_of_item(it);
+      const int32_t row = static_cast<int32_t>(threadIdx.x);
+      const bool has_row = row < it.rows;
+      const uint32_t flat = static_cast<uint32_t>(it.row0 + min(row, it.rows - 1));
+      const int32_t pos = static_cast<int32_t>(a.group_div.div(flat));
+      const int32_t q_head = it.head * a.group + static_cast<int32_t>(flat - static_cast<uint32_t>(pos) * a.group);
+      const int32_t pos_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      int32_t full0, full1;
+      full_steps(keys, __reduce_min_sync(kFull, pos), __reduce_max_sync(kFull, pos_lo), full0, full1);
+
+      float m = -INFINITY, l = 0.0f;                // reference maximum, sum
+      bool done = true;                             // every wait was met
+      for (int32_t t = 0; t < keys.steps; ++t) {
+        const uint32_t pair = pairs + (kTiles == 2 ? 2 * t + tile : t);
+        const uint32_t buf = pair & 1;
+        const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
+        if (!have(s_full + 8 * buf, pair >> 1)) {
+          done = false;
+          break;
+        }
+        uint32_t see[kKeys / 32] = {};
+        const bool masked = t < full0 || t >= full1;
+        if (masked) {
+          const int32_t p0 = keys.base(t), end = min(pos, keys.limit(t) - 1);
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+            see[c] = range_bits(p0 + 32 * c, pos_lo, end) | range_bits(p0 + 32 * c, 0, min(a.num_sinks - 1, end));
+        }
+        uint32_t s[kKeys / 64][64], p[kKeys / 2];
+        float sum;
+        auto load = [&]() {
+#pragma unroll
+          for (int h = 0; h < kKeys / 64; ++h) tmem_ld64(s_col + 64 * h, s[h]);
+        };
+        auto pass = [&](float off, auto with_mask) {
+          float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2) {
+            float2 z = ffma2(make_float2(__uint_as_float(s[i >> 6][i & 63]), __uint_as_float(s[i >> 6][(i & 63) + 1])),
+                             make_float2(sc, sc), make_float2(off, off));
+            if constexpr (with_mask.value) {
+              z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
+              z.y = (see[i >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
+            }
+            const float2 w = make_float2(ex2(z.x), ex2(z.y));
+            sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
+            p[i >> 1] = pack_bf16x2(w.x, w.y);
+          }
+          const float2 both = fadd2(sums[0], sums[1]);
+          sum = both.x + both.y;
+        };
+        auto weights = [&]() {                      // warp-uniform choice
+          const float off = m == -INFINITY ? 0.0f : -m;
+          if (masked)
+            pass(off, std::true_type{});
+          else
+            pass(off, std::false_type{});
+        };
+        load();
+        // (a row of its own accord, so that its bits do not depend on its neighbours')
+        bool behind = true;
+        if (t > 0) {
+          weights();
+          behind = m == -INFINITY || !(sum <= kMaxSum);
+        }
+        if (__any_sync(kFull, behind)) {
+          if (t > 0) load();
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) {
+            const float z = __uint_as_float(s[i >> 6][i & 63]) * sc;
+            if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
+          }
+          float alpha = 1.0f;
+          if (behind && top > m) {
+            alpha = ex2(m - top);                   // 0 while m is -inf
+            m = top;
+          }
+          weights();
+          l *= alpha;
+          if (t > 0) {
+            // O is rescaled once the product of the tile before is done: with two
+            // row tiles this tile's scores follow it, with one they do not.
+            if (kTiles == 1 && !have(o_done + 8 * (buf ^ 1), (pair - 1) >> 1)) {
+              done = false;
+              break;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(o_col + 32 * c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(o_col + 32 * c, o);
+            }
+          }
+        }
+        l += sum;
+#pragma unroll
+        for (int h = 0; h < kKeys / 64; ++h) tmem_st32_start(s_col + 32 * h, p + 32 * h);
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * buf);
+      }
+      // the last product is done: O is complete
+      const uint32_t last = pairs + (kTiles == 2 ? 2 * (keys.steps - 1) + tile : keys.steps - 1);
+      pairs += kTiles * keys.steps;
+      if (done) done = have(o_done + 8 * (last & 1), last >> 1);
+      if (!done) break;                             // uniform over the warp
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      // The rows leave in pieces of 64 values (128 bytes), eight lanes to a
+      // piece, through the warp's 4 KB of shared memory.
+      const uint32_t stage = base + S::kOut + warp * 4096;
+      const int64_t token = static_cast<int64_t>(it.token0) + pos;
+      const uint64_t mine =
+          has_row ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
+                                               q_head * a.out_stride_h)
+                  : 0;
+      uint64_t to[8];                               // of rows 4 i + lane / 8
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int from = 4 * i + (lane >> 3);
+        to[i] = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(mine >> 32), from)) << 32 |
+                __shfl_sync(kFull, static_cast<uint32_t>(mine), from);
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float o[32];
+          tmem_ld32(o_col + 64 * c + 32 * half, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared16(stage + sw128_offset(lane, 4 * half + j),
+                        make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                   pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
+        }
+        if (c == D / 64 - 1) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free + 8 * tile);
+        }
+        __syncwarp();
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ld_shared16(stage + sw128_offset(4 * i + (lane >> 3), lane & 7));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (to[i] != 0) st16(reinterpret_cast<uint8_t*>(to[i]) + 128 * c + 16 * (lane & 7), v[i]);
+        __syncwarp();                               // read before the next piece, whose load is the whole warp's
+      }
+      if (has_row && a.lse != nullptr)
+        a.lse[token * a.lse_stride_t + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  } else {
+    if constexpr (kTiles == 2) fewer_registers<S::kOtherRegs>();
+    const uint32_t elected = elect_lane();
+    if (warp == S::kCopyWarp) {
+      // ---- items, and the copies of K and V ------------------------------------
+      uint32_t tiles = 0;                           // of the items before
+      uint32_t copied[2] = {0, 0};                  // tiles of K, of V
+      uint32_t index = blockIdx.x;
+      for (uint32_t k = 0;; ++k) {
+        it = item_at<kBlock>(a, index, lane);
+        if (k > 0) it.rows = 0;
+        if (k >= kSlots && !have(item_free + 8 * (k % kSlots), k / kSlots - 1)) break;
+        if (lane == 0) {
+          volatile Item& s = items[k % kSlots];
+          s.token0 = it.token0;
+          s.n = it.n;
+          s.row0 = it.row0;
+          s.rows = it.rows;
+          s.head = it.head;
+          mbar_arrive(item_full + 8 * (k % kSlots));
+        }
+        __syncwarp();
+        if (it.rows == 0) break;
+        const Keys<kKeys> keys = keys_of_item(it);
+        bool ok = true;
+        for (int32_t t = 0; t < keys.steps && ok; ++t) {
+          const uint32_t at = tiles + t, st = at % S::kStages;
+          const int32_t key = it.token0 + keys.base(t);
+          auto copy = [&](uint32_t full, uint32_t empty, uint32_t to, const CUtensorMap* map, uint32_t& count) {
+            if (at >= S::kStages && !have(empty + 8 * st, at / S::kStages - 1)) return false;
+            if (elected) {
+              mbar_arrive_expect_tx(full + 8 * st, S::kTileBytes);
+#pragma unroll
+              for (int i = 0; i < S::kBlocks; ++i)
+                tma_load_3d(base + to + st * S::kTileBytes + i * S::kKBlock, map, 64 * i, it.head, key, full + 8 * st);
+            }
+            __syncwarp();
+            ++count;
+            return true;
+          };
+          ok = copy(k_full, k_empty, S::kK, &kmap, copied[0]) && copy(v_full, v_empty, S::kV, &vmap, copied[1]);
+        }
+        if (!ok) break;
+        tiles += keys.steps;
+      }
+      // no copy outlives the CTA (bounded, whatever the abort flag says)
+      const long long start = clock64();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        for (uint32_t i = copied[x] > S::kStages ? copied[x] - S::kStages : 0; i < copied[x]; ++i)
+          while (!mbar_try_wait((x == 0 ? k_full : v_full) + 8 * (i % S::kStages), (i / S::kStages) & 1))
+            if (clock64() - start > kDrainCycles) break;
+      }
+      __syncwarp();
+    } else if (warp == S::kProductWarp) {
+      // ---- the products (one elected lane; the warp waits together) ------------
+      constexpr uint32_t kIdescS = idesc_bf16(128, kKeys, false), kIdescO = idesc_bf16(128, D, true);
+      const uint64_t qdesc = sw128_desc(base, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
+      const uint64_t vdesc = sw128_desc(base + S::kV, S::kKBlock, 1024);
+      uint32_t pairs = 0, tiles = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+        const Keys<kKeys> keys = keys_of_item(it);
+        const int32_t n = kTiles * keys.steps;
+        // S_w(t) = Q_w K(t)^T
+        auto scores = [&](int32_t i) {
+          const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
+          const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
+          if (w == 0 && !have(k_full + 8 * st, (tiles + t) / S::kStages)) return false;
+          const uint64_t qd = qdesc + ((w * S::kQTile) >> 4), kd = kdesc + ((st * S::kTileBytes) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            warp_mma(elected, tmem + kSCol + kKeys * buf, qd + (((ks >> 2) * S::kQBlock + 32 * (ks & 3)) >> 4),
+                     kd + (((ks >> 2) * S::kKBlock + 32 * (ks & 3)) >> 4), kIdescS, ks != 0);
+          warp_commit(elected, s_full + 8 * buf);
+          if (w == kTiles - 1) warp_commit(elected, k_empty + 8 * st);
+          if (i == n - 1) warp_commit(elected, q_free);
+          return true;
+        };
+        ok = have(q_full, k) && scores(0) && (n == 1 || scores(1));
+        for (int32_t i = 0; i < n && ok; ++i) {
+          const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
+          const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
+#ifdef KVQ_ATTN_STALL_TILE
+          // Failure-detection build only: no product from this tile on, as if
+          // the tensor work never completed; the other roles' bounded waits run out.
+          if (t == KVQ_ATTN_STALL_TILE) {
+            ok = false;
+            break;
+          }
+#endif
+          // O_w += P_w(t) V(t)
+          ok = have(p_full + 8 * buf, (pairs + i) >> 1);
+          if (ok && t == 0 && k > 0) ok = have(o_free + 8 * w, k - 1);
+          if (ok && w == 0) ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
+          if (!ok) break;
+          const uint64_t vd = vdesc + ((st * S::kTileBytes) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            warp_mma_ta(elected, tmem + w * D, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
+                        (t > 0 || ks > 0) ? 1u : 0u);
+          warp_commit(elected, o_done + 8 * buf);
+          if (w == kTiles - 1) warp_commit(elected, v_empty + 8 * st);
+          if (i + 2 < n) ok = scores(i + 2);
+        }
+        pairs += n;
+        tiles += keys.steps;
+      }
+      // the products still in flight are drained (bounded, whatever the abort flag says)
+      warp_commit(elected, drain);
+      const long long start = clock64();
+      while (!mbar_try_wait(drain, 0)) {
+        if (clock64() - start > kDrainCycles) {
+          *s_abort = 1;
+          break;
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---- the query rows; one of the two warps looks through V ----------------
+      const int me = warp - S::kQueryWarp;
+      if (blockIdx.x == 0 && me == 0) {               // sequences that item_at may not come across
+        for (int32_t b = lane; b < a.batch_size; b += 32) {
+          const int32_t q0 = load_global(a.seq_start + b), q1 = load_global(a.seq_start + b + 1);
+          if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || static_cast<int64_t>(q1) - q0 > a.max_seq_len)
+            report(a.status, KVQ_STATUS_BAD_BATCH);
+        }
+      }
+      uint32_t tiles = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+        const Keys<kKeys> keys = keys_of_item(it);
+        if (k > 0 && !have(q_free, k - 1)) break;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;        // lanes to a row, rows at once
+        const int c = lane % kLanes, sub = lane / kLanes;
+        constexpr int kRows = kBlock / S::kQueryWarps;
+#pragma unroll 4
+        for (int r = me * kRows; r < (me + 1) * kRows; r += kAtOnce) {
+          const int rr = r + sub;
+          const bool live = rr < it.rows;
+          const uint32_t flat = static_cast<uint32_t>(it.row0 + (live ? rr : 0)), tk = a.group_div.div(flat);
+          const int32_t h = it.head * a.group + static_cast<int32_t>(flat - tk * a.group);
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                     (static_cast<int64_t>(it.token0) + tk) * a.q_stride_t + h * a.q_stride_h + 8 * c;
+          cp_async<16>(base + (rr >> 7) * S::kQTile + (c >> 3) * S::kQBlock + sw128_offset(rr & 127, c & 7), src,
+                       live ? 16 : 0);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        if (warp == S::kCheckWarp) {
+          const int32_t t0 = static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0)));
+          const int32_t t1 = static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0 + it.rows - 1)));
+          int32_t full0, full1;
+          full_steps(keys, t0, a.window > 0 ? max(0, t1 - a.window + 1) : 0, full0, full1);
+          for (int32_t t = 0; t < keys.steps; ++t) {
+            const uint32_t at = tiles + t, st = at % S::kStages;
+            ok = have(v_full + 8 * st, at / S::kStages);
+            if (!ok) break;
+            if (t < full0 || t >= full1) {
+              const int32_t there = keys.limit(t) - keys.base(t);   // the tile's rows of keys; those past them: zeros
+              const uint32_t v = base + S::kV + st * S::kTileBytes;
+#pragma unroll 4
+              for (uint32_t i = lane; i < S::kTileBytes / 16; i += 32) {
+                uint4 x = ld_shared16(v + 16 * i);
+                const bool in = static_cast<int32_t>((i >> 3) % kKeys) < there;
+                constexpr uint32_t kAbs = 0x7FFF7FFFu;
+                uint32_t top = __vimax3_u16x2(x.x & kAbs, x.y & kAbs, x.z & kAbs);
+                top = __vimax3_u16x2(top, x.w & kAbs, 0u);
+                if (!in || (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+                  auto finite = [&](uint32_t w) {
+                    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+                  };
+                  x = in ? make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w)) : make_uint4(0, 0, 0, 0);
+                  st_shared16(v + 16 * i, x);
+                }
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(v_good + 8 * st);
+          }
+        }
+        tiles += keys.steps;
+      }
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && *s_abort) report(a.status, KVQ_STATUS_TIMEOUT);
+  if (warp == 0) {
+    fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(*s_tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Tensor map of keys or values [tokens][heads][D], tiles of 64 dimensions of
+// kKeys tokens of one head with the 128-byte swizzle; tokens past the last
+// one are zero-filled.
+template <int D, int kKeys>
+bool key_tensor_map(const void* p, int64_t stride_t, int64_t stride_h, int32_t heads, int64_t tokens, CUtensorMap* map) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2};
+  const cuuint32_t box[3] = {64, 1, kKeys}, elem_strides[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, elem_strides,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int kTiles>
+cudaError_t launch(const PromptAttentionArgs& a, cudaStream_t stream) {
+  using S = Shape<D, kTiles>;
+  CUtensorMap kmap, vmap;
+  if (!key_tensor_map<D, S::kKeys>(a.k, a.k_stride_t, a.k_stride_h, a.num_kv_heads, a.num_tokens, &kmap) ||
+      !key_tensor_map<D, S::kKeys>(a.v, a.v_stride_t, a.v_stride_h, a.num_kv_heads, a.num_tokens, &vmap))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kTiles>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = a.num_tokens * a.group / (128 * kTiles) + a.batch_size;     // the numbers of item_at
+  return launch_dependent(prompt_attention_kernel<D, kTiles>, dim3(static_cast<unsigned>(blocks * a.num_kv_heads)),
+                          S::kThreads, S::kSmem, 1, stream, a, kmap, vmap);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t stream) {
+  // two row tiles share a key tile wherever a sequence can fill them
+  const bool two = static_cast<int64_t>(a.max_seq_len) * a.group > 128;
+  switch (a.head_size) {
+    case 64: return two ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
+    case 128: return two ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
+    default: return launch<256, 1>(a, stream);       // one tile's O fills half of the tensor memory
+  }
+}
+
+}  // namespace kvq

@@ -842,6 +842,50 @@ int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_head
                                          int32_t window, int32_t num_sinks, int32_t* use_workspace);
 
 /*
+ * kvq_prompt_attention -- causal attention over whole prompts whose keys and
+ * values are at hand in bf16 (before or beside their append to a cache), with
+ * a sliding window and a few first tokens that stay visible.  Sequence b <
+ * batch_size is the rows [seq_start[b], seq_start[b+1]) of q, k, v and out, at
+ * most max_seq_len of them; its query i sees its key j iff j <= i and (window
+ * <= 0 or j > i - window or j < num_sinks).  For head h, with key head h /
+ * (num_heads / num_kv_heads):
+ *   s_j = softmax_scale * (q . k_j),  m = max_j s_j
+ *   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+ *   lse = m + ln(sum_j exp(s_j - m))
+ * lse is what the result is joined by with attention over other keys.
+ * seq_start does not decrease.  A sequence whose range is not inside [0,
+ * num_tokens) or is longer than max_seq_len is skipped, its rows untouched
+ * (KVQ_STATUS_BAD_BATCH; where seq_start decreases, rows of other sequences
+ * may be left untouched too), as are rows of no sequence, which may hold
+ * anything.  NaN and infinities in a key or value have no effect on queries
+ * that do not see it; in a visible value they come through or read as zero.
+ * Arithmetic: products on the tensor cores (bf16, fp32 sums); the softmax in
+ * fp32; the weights rounded to bf16 (relative 2^-8) for the weighted sum,
+ * their sum taken before; out rounded once to bf16.  Waits of the kernel's
+ * warps on one another are bounded; on expiry the rows concerned stay
+ * unwritten (KVQ_STATUS_TIMEOUT).
+ * q: bf16 [num_tokens, num_heads, head_size]; k, v: bf16 [num_tokens,
+ * num_kv_heads, head_size]; token and head strides in elements (multiples of
+ * 8; those of k and v positive and below 2^38); head_size 64, 128 or 256;
+ * num_heads a multiple of num_kv_heads.  out: as q, token stride >=
+ * (num_heads - 1) * head stride + head_size.  lse: fp32 [num_tokens,
+ * num_heads], token stride lse_stride_t, or NULL.  out and lse overlap no
+ * input.  softmax_scale: softmax_scale * log2(e) is finite in fp32.
+ * seq_start: int32 [batch_size + 1]; batch_size <= 65535; num_tokens *
+ * num_heads + 65536 * num_kv_heads < 2^31.
+ */
+kvq_status kvq_prompt_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h,
+    int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+    const int32_t* seq_start, int32_t batch_size, int32_t max_seq_len,
+    float softmax_scale, int32_t window, int32_t num_sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* lse, int64_t lse_stride_t,
+    int32_t* d_status, kvq_stream_t stream);
+
+/*
  * kvq_selftest_convert -- exposes the device number-format converters the
  * kernels above use, for exhaustive testing.  For i < count and f the float
  * whose bit pattern is first_bits + i (mod 2^32):

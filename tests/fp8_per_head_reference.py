@@ -183,3 +183,22 @@ def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0):
             for to, x in zip((out, lse, tol_o, tol_l), got):
                 to[t0:t1, kh * g:(kh + 1) * g] = x.reshape(n, g, *x.shape[1:])
     return out, lse, tol_o, tol_l
+
+
+def prompt_attention(q, k, v, start, scale, window=0, sinks=0):
+    """Attention over whole prompts.  Weights are bf16 (2^-8), flushed below 2^-126 of the largest."""
+    T, H, D = q.shape
+    KH = k.shape[1]
+    g = H // KH
+    out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
+    tol_o, tol_l = np.zeros((T, H, D)), np.zeros((T, H))
+    for t0, t1 in zip(start[:-1], start[1:]):
+        n = t1 - t0
+        see = np.repeat(visible(n, n, 0, window, sinks), g, 0)
+        for kh in range(KH):
+            V = v[t0:t1, kh]
+            rows = q[t0:t1, kh * g:(kh + 1) * g].reshape(n * g, D)
+            got = attend(rows, k[t0:t1, kh], V, see, scale, 2.0 ** -8, 2.0 ** -100 * np.abs(V).max(initial=0), 0.0)
+            for to, x in zip((out, lse, tol_o, tol_l), got):
+                to[t0:t1, kh * g:(kh + 1) * g] = x.reshape(n, g, *x.shape[1:])
+    return out, lse, tol_o, tol_l
