@@ -51,6 +51,7 @@ constexpr int kSlots = 2;                         // work items known at once
 template <int D, int kTiles>
 struct Shape {
   static constexpr int kKeys = D == 256 ? 64 : 128;          // keys per tile
+  static constexpr int kFirst = kKeys == 128 ? 96 : 32;      // of them, those whose weights are handed on first
   static constexpr int kSoftmaxWarps = 4 * kTiles;
   static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kQueryWarp = kProductWarp + 1;
   static constexpr int kQueryWarps = 2, kCheckWarp = kQueryWarp + 1;
@@ -132,6 +133,28 @@ __device__ __forceinline__ Item item_at(const PromptAttentionArgs& a, uint32_t i
   return it;
 }
 
+// kCount (a multiple of 32) columns of scores are asked for; they are there
+// after tmem_loaded, which takes the registers through itself so that nothing
+// that uses them moves up past the wait.
+template <int kCount>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kCount]) {
+#pragma unroll
+  for (int i = 0; i < kCount; i += 32) tmem_ld32_start(taddr + i, r + i);
+}
+template <int kCount>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[kCount]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kCount; i += 32) held32(r + i);
+}
+// kCount (a multiple of 16) columns stored without waiting.
+template <int kCount>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[kCount]) {
+#pragma unroll
+  for (int i = 0; i + 32 <= kCount; i += 32) tmem_st32_start(taddr + i, v + i);
+  if constexpr (kCount % 32 != 0) tmem_st16_start(taddr + kCount / 32 * 32, v + kCount / 32 * 32);
+}
+
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -146,14 +169,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t base = smem_u32(smem);
   const uint32_t bar = base + S::kMisc;
   const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_good = bar + 48, v_empty = bar + 64;   // [kStages]
-  const uint32_t s_full = bar + 80, p_full = bar + 96, o_done = bar + 112;      // [score buffer]
-  const uint32_t o_free = bar + 128;                                            // [row tile]
-  const uint32_t q_full = bar + 144, q_free = bar + 152, drain = bar + 160;
-  const uint32_t item_full = bar + 168, item_free = bar + 184;                  // [kSlots]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 200);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 204);
-  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 208);
-  static_assert(208 + kSlots * sizeof(Item) <= 512, "barrier layout");
+  // score buffers: scores there, first and all weights there, their products done
+  const uint32_t s_full = bar + 80, p_first = bar + 96, p_full = bar + 112, o_first = bar + 128, o_done = bar + 144;
+  const uint32_t o_free = bar + 160;                                            // [row tile]
+  const uint32_t q_full = bar + 176, q_free = bar + 184, drain = bar + 192;
+  const uint32_t item_full = bar + 200, item_free = bar + 216;                  // [kSlots]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 232);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 236);
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 240);
+  static_assert(240 + kSlots * sizeof(Item) <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -169,7 +193,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       mbar_init(v_good + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_first + 8 * i, 4);
       mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_first + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
       mbar_init(o_free + 8 * i, 4);
       mbar_init(item_full + 8 * i, 1);
@@ -255,82 +281,95 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           for (int c = 0; c < kKeys / 32; ++c)
             see[c] = range_bits(p0 + 32 * c, pos_lo, end) | range_bits(p0 + 32 * c, 0, min(a.num_sinks - 1, end));
         }
-        uint32_t s[kKeys / 64][64], p[kKeys / 2];
-        float sum;
-        auto load = [&]() {
+        // The weights of kCount keys from column kFrom on, against the reference m,
+        // are formed, handed on and summed.  `before`: the barrier and phase of the
+        // product into O before these weights' (0: no wait needed, or nothing in O).
+        auto part = [&](auto from_c, auto& s, uint32_t before, uint32_t phase, bool in_o, uint32_t ready) {
+          constexpr int kFrom = decltype(from_c)::value;
+          constexpr int kCount = static_cast<int>(sizeof(s) / 4);
+          uint32_t p[kCount / 2];
+          float sum;
+          auto pass = [&](auto with_mask) {
+            const float off = m == -INFINITY ? 0.0f : -m;
+            float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int h = 0; h < kKeys / 64; ++h) tmem_ld64(s_col + 64 * h, s[h]);
-        };
-        auto pass = [&](float off, auto with_mask) {
-          float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-          for (int i = 0; i < kKeys; i += 2) {
-            float2 z = ffma2(make_float2(__uint_as_float(s[i >> 6][i & 63]), __uint_as_float(s[i >> 6][(i & 63) + 1])),
-                             make_float2(sc, sc), make_float2(off, off));
-            if constexpr (with_mask.value) {
-              z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
-              z.y = (see[i >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
+            for (int i = 0; i < kCount; i += 2) {
+              float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
+                               make_float2(off, off));
+              if constexpr (with_mask.value) {
+                z.x = (see[(kFrom + i) >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
+                z.y = (see[(kFrom + i) >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
+              }
+              const float2 w = make_float2(ex2(z.x), ex2(z.y));
+              sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
+              p[i >> 1] = pack_bf16x2(w.x, w.y);
             }
-            const float2 w = make_float2(ex2(z.x), ex2(z.y));
-            sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
-            p[i >> 1] = pack_bf16x2(w.x, w.y);
+            const float2 both = fadd2(sums[0], sums[1]);
+            sum = both.x + both.y;
+          };
+          auto weights = [&]() {                    // warp-uniform choice
+            if (masked)
+              pass(std::true_type{});
+            else
+              pass(std::false_type{});
+          };
+          // (a row takes a new reference of its own accord, so that its bits do not
+          // depend on its neighbours')
+          bool behind = true;
+          if (t > 0 || kFrom > 0) {
+            weights();
+            behind = m == -INFINITY || !(sum <= kMaxSum);
           }
-          const float2 both = fadd2(sums[0], sums[1]);
-          sum = both.x + both.y;
-        };
-        auto weights = [&]() {                      // warp-uniform choice
-          const float off = m == -INFINITY ? 0.0f : -m;
-          if (masked)
-            pass(off, std::true_type{});
-          else
-            pass(off, std::false_type{});
-        };
-        load();
-        // (a row of its own accord, so that its bits do not depend on its neighbours')
-        bool behind = true;
-        if (t > 0) {
-          weights();
-          behind = m == -INFINITY || !(sum <= kMaxSum);
-        }
-        if (__any_sync(kFull, behind)) {
-          if (t > 0) load();
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i) {
-            const float z = __uint_as_float(s[i >> 6][i & 63]) * sc;
-            if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
-          }
-          float alpha = 1.0f;
-          if (behind && top > m) {
-            alpha = ex2(m - top);                   // 0 while m is -inf
-            m = top;
-          }
-          weights();
-          l *= alpha;
-          if (t > 0) {
-            // O is rescaled once the product of the tile before is done: with two
-            // row tiles this tile's scores follow it, with one they do not.
-            if (kTiles == 1 && !have(o_done + 8 * (buf ^ 1), (pair - 1) >> 1)) {
-              done = false;
-              break;
+          if (__any_sync(kFull, behind)) {
+            if (t > 0 || kFrom > 0) {
+              tmem_load(s_col + kFrom, s);
+              tmem_loaded(s);
             }
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) {
+              const float z = __uint_as_float(s[i]) * sc;
+              if (!masked || ((see[(kFrom + i) >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
+            }
+            float alpha = 1.0f;
+            if (behind && top > m) {
+              alpha = ex2(m - top);                 // 0 while m is -inf
+              m = top;
+            }
+            weights();
+            l *= alpha;
+            if (in_o) {
+              if (before != 0 && !have(before, phase)) return false;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(o_col + 32 * c, o);
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld32(o_col + 32 * c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(o_col + 32 * c, o);
+                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                tmem_st32(o_col + 32 * c, o);
+              }
             }
           }
-        }
-        l += sum;
-#pragma unroll
-        for (int h = 0; h < kKeys / 64; ++h) tmem_st32_start(s_col + 32 * h, p + 32 * h);
-        tmem_st_wait();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * buf);
+          l += sum;
+          tmem_store(s_col + kFrom / 2, p);
+          tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + 8 * buf);
+          return true;
+        };
+        uint32_t first[S::kFirst], rest[kKeys - S::kFirst];
+        tmem_load(s_col, first);
+        tmem_loaded(first);
+        tmem_load(s_col + S::kFirst, rest);         // under way meanwhile
+        // The product before: of the tile before, which with two row tiles this
+        // tile's scores follow, with one they do not; then of these first weights.
+        done = part(std::integral_constant<int, 0>{}, first, kTiles == 1 ? o_done + 8 * (buf ^ 1) : 0, (pair - 1) >> 1, t > 0,
+                    p_first);
+        if (!done) break;
+        tmem_loaded(rest);
+        done = part(std::integral_constant<int, S::kFirst>{}, rest, o_first + 8 * buf, pair >> 1, true, p_full);
+        if (!done) break;
       }
       // the last product is done: O is complete
       const uint32_t last = pairs + (kTiles == 2 ? 2 * (keys.steps - 1) + tile : keys.steps - 1);
@@ -449,10 +488,13 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         const Keys<kKeys> keys = keys_of_item(it);
         const int32_t n = kTiles * keys.steps;
         // S_w(t) = Q_w K(t)^T
+        auto keys_there = [&](int32_t i) {
+          const uint32_t at = tiles + (kTiles == 2 ? i >> 1 : i);
+          return (kTiles == 2 && (i & 1)) || have(k_full + 8 * (at % S::kStages), at / S::kStages);
+        };
         auto scores = [&](int32_t i) {
           const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
           const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
-          if (w == 0 && !have(k_full + 8 * st, (tiles + t) / S::kStages)) return false;
           const uint64_t qd = qdesc + ((w * S::kQTile) >> 4), kd = kdesc + ((st * S::kTileBytes) >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -461,9 +503,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           warp_commit(elected, s_full + 8 * buf);
           if (w == kTiles - 1) warp_commit(elected, k_empty + 8 * st);
           if (i == n - 1) warp_commit(elected, q_free);
-          return true;
         };
-        ok = have(q_full, k) && scores(0) && (n == 1 || scores(1));
+        ok = have(q_full, k);
+        for (int32_t i = 0; i < min(n, 2) && ok; ++i) {
+          ok = keys_there(i);
+          if (ok) scores(i);
+        }
         for (int32_t i = 0; i < n && ok; ++i) {
           const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
           const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
@@ -475,19 +520,26 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             break;
           }
 #endif
-          // O_w += P_w(t) V(t)
-          ok = have(p_full + 8 * buf, (pairs + i) >> 1);
-          if (ok && t == 0 && k > 0) ok = have(o_free + 8 * w, k - 1);
+          // O_w += P_w(t) V(t), as its weights come; what else it and the scores
+          // behind it need is waited for before them
+          ok = !(t == 0 && k > 0) || have(o_free + 8 * w, k - 1);
           if (ok && w == 0) ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
-          if (!ok) break;
+          if (ok && i + 2 < n) ok = keys_there(i + 2);
           const uint64_t vd = vdesc + ((st * S::kTileBytes) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
+          auto product = [&](int ks) {
             warp_mma_ta(elected, tmem + w * D, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
                         (t > 0 || ks > 0) ? 1u : 0u);
+          };
+          if (!ok || !(ok = have(p_first + 8 * buf, (pairs + i) >> 1))) break;
+#pragma unroll
+          for (int ks = 0; ks < S::kFirst / 16; ++ks) product(ks);
+          warp_commit(elected, o_first + 8 * buf);
+          if (!(ok = have(p_full + 8 * buf, (pairs + i) >> 1))) break;
+#pragma unroll
+          for (int ks = S::kFirst / 16; ks < kKeys / 16; ++ks) product(ks);
           warp_commit(elected, o_done + 8 * buf);
           if (w == kTiles - 1) warp_commit(elected, v_empty + 8 * st);
-          if (i + 2 < n) ok = scores(i + 2);
+          if (i + 2 < n) scores(i + 2);
         }
         pairs += n;
         tiles += keys.steps;
