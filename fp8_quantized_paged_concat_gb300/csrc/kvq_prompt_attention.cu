@@ -7,8 +7,10 @@
 //   lse = m + ln sum_j exp(s_j - m).
 // The products bound it: 4 D flops for each (row, visible key).
 //
-// Design: one CTA per SM, for (block of 128 kTiles query rows, key head,
-// sequence); the rows are (token, head) pairs of the sequence that share the
+// Design: one CTA per SM, which takes one item after the other: (block of 128
+// kTiles query rows, key head, sequence).  The grid has a CTA per item; one
+// that runs takes over the next that has not started, whose keys and queries
+// are copied while it finishes.  The rows are (token, head) pairs of the sequence that share the
 // key head, so that every tile of keys serves the whole group.
 //   - tensor memory: O of row tile w in columns [D w, +D), two score buffers
 //     of kKeys columns from column 256 on: with two row tiles one each, with
@@ -174,10 +176,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t o_free = bar + 160;                                            // [row tile]
   const uint32_t q_full = bar + 176, q_free = bar + 184, drain = bar + 192;
   const uint32_t item_full = bar + 200, item_free = bar + 216;                  // [kSlots]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 232);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 236);
-  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 240);
-  static_assert(240 + kSlots * sizeof(Item) <= 512, "barrier layout");
+  const uint32_t answer = bar + 240, answered = bar + 232;                      // of the request for a next item
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 256);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 260);
+  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 264);
+  static_assert(264 + kSlots * sizeof(Item) <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -204,6 +207,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     mbar_init(q_full, S::kQueryWarps);
     mbar_init(q_free, 1);
     mbar_init(drain, 1);
+    mbar_init(answered, 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -430,11 +434,39 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       // ---- items, and the copies of K and V ------------------------------------
       uint32_t tiles = 0;                           // of the items before
       uint32_t copied[2] = {0, 0};                  // tiles of K, of V
-      uint32_t index = blockIdx.x;
+      uint32_t asked = 0;                           // requests for a next item
+      bool waiting = false;                         // one is under way
+      it = item_at<kBlock>(a, blockIdx.x, lane);
       for (uint32_t k = 0;; ++k) {
-        it = item_at<kBlock>(a, index, lane);
-        if (k > 0) it.rows = 0;
-        if (k >= kSlots && !have(item_free + 8 * (k % kSlots), k / kSlots - 1)) break;
+        // an empty item is passed over; the request for the next one is under way
+        // while the keys of this one are copied
+        bool ok = true, more = true;
+        auto ask = [&]() {
+          if (elected) {
+            mbar_arrive_expect_tx(answered, 16);
+            ask_for_cta(answer, answered);
+          }
+          __syncwarp();
+          waiting = true;
+        };
+        auto take = [&]() {
+          ok = have(answered, asked);
+          if (!ok) return;
+          waiting = false;
+          ++asked;
+          const int64_t x = cta_of(answer);
+          fence_async_smem();                       // read before the next answer
+          __syncwarp();
+          more = x >= 0;
+          it = Item{};
+          if (more) it = item_at<kBlock>(a, static_cast<uint32_t>(x), lane);
+        };
+        if (k > 0) take();
+        while (ok && more && it.rows == 0) {
+          ask();
+          take();
+        }
+        if (!ok || (k >= kSlots && !have(item_free + 8 * (k % kSlots), k / kSlots - 1))) break;
         if (lane == 0) {
           volatile Item& s = items[k % kSlots];
           s.token0 = it.token0;
@@ -446,8 +478,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         }
         __syncwarp();
         if (it.rows == 0) break;
+        ask();
         const Keys<kKeys> keys = keys_of_item(it);
-        bool ok = true;
         for (int32_t t = 0; t < keys.steps && ok; ++t) {
           const uint32_t at = tiles + t, st = at % S::kStages;
           const int32_t key = it.token0 + keys.base(t);
@@ -468,8 +500,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         if (!ok) break;
         tiles += keys.steps;
       }
-      // no copy outlives the CTA (bounded, whatever the abort flag says)
+      // no copy or answer outlives the CTA (bounded, whatever the abort flag says)
       const long long start = clock64();
+      if (waiting)
+        while (!mbar_try_wait(answered, asked & 1))
+          if (clock64() - start > kDrainCycles) break;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         for (uint32_t i = copied[x] > S::kStages ? copied[x] - S::kStages : 0; i < copied[x]; ++i)

@@ -146,6 +146,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
 
+// Work taken over from a CTA of this grid that has not started (which then
+// never does): the request, whose 16-byte answer lands in shared memory and
+// completes on an mbarrier, and what the answer says: the other CTA's index
+// along x, or -1 where there was none left (no request may follow that).
+__device__ __forceinline__ void ask_for_cta(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      :: "r"(answer), "r"(bar) : "memory");
+}
+__device__ __forceinline__ int64_t cta_of(uint32_t answer) {
+  uint32_t taken, x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\tld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(taken), "=r"(x) : "r"(answer) : "memory");
+  return taken ? static_cast<int64_t>(x) : -1;
+}
+
 // One bounded wait step: the thread sleeps in the barrier (up to about 1 ms,
 // woken when the phase completes) instead of spinning on issue slots.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
