@@ -1241,9 +1241,8 @@ kvq_status kvq_prompt_attention(const void* q, int64_t q_stride_t, int64_t q_str
   if (kvq_status s = check_heads(fn, "v", v, v_stride_t, v_stride_h, num_kv_heads, head_size, false)) return s;
   if (kvq_status s = check_heads(fn, "out", out, out_stride_t, out_stride_h, num_heads, head_size, true)) return s;
   constexpr int64_t kMost = int64_t{1} << 38;        // bytes of a copied tensor's stride: below 2^40
-  KVQ_REQUIRE(k_stride_t > 0 && v_stride_t > 0 && k_stride_t < kMost && v_stride_t < kMost && k_stride_h < kMost &&
-                  v_stride_h < kMost,
-              "%s: k and v strides must be positive and below 2^38", fn);
+  for (const int64_t s : {q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h})
+    KVQ_REQUIRE(s > 0 && s < kMost, "%s: q, k and v strides must be positive and below 2^38", fn);
   KVQ_REQUIRE(lse == nullptr || (aligned(lse, 4) && lse_stride_t >= num_heads),
               "%s: lse must be 4-byte aligned with token stride >= num_heads", fn);
   KVQ_REQUIRE(seq_start != nullptr && aligned(seq_start, 4), "%s: seq_start must be non-NULL and 4-byte aligned", fn);
@@ -1269,6 +1268,9 @@ kvq_status kvq_prompt_attention(const void* q, int64_t q_stride_t, int64_t q_str
   a.group = num_heads / num_kv_heads;
   a.group_div = kvq::FastDiv::make(static_cast<uint32_t>(a.group));
   a.kv_heads_div = kvq::FastDiv::make(static_cast<uint32_t>(num_kv_heads));
+  a.tile_tokens = std::max(1, 128 / a.group);
+  a.chunks = (a.group + 127) / 128;
+  a.chunk_div = kvq::FastDiv::make(static_cast<uint32_t>(a.chunks));
   a.seq_start = seq_start;
   a.batch_size = batch_size;
   a.max_seq_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, num_tokens));

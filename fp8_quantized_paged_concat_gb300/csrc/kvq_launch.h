@@ -293,6 +293,10 @@ struct PromptAttentionArgs {
   int32_t group;                  // num_heads / num_kv_heads query heads share a key head
   FastDiv group_div;
   FastDiv kv_heads_div;
+  // a tile of 128 query rows: the group's heads of tile_tokens tokens; a group of
+  // more than 128 heads takes `chunks` tiles of 128 of them per token
+  int32_t tile_tokens, chunks;
+  FastDiv chunk_div;
   const int32_t* seq_start;       // [batch_size + 1]
   int32_t batch_size;
   int32_t max_seq_len;

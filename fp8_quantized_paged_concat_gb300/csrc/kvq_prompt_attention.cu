@@ -21,19 +21,20 @@
 //     are computed, the products of the other run.  The tensor core takes them
 //     in that order, so that S(i + 2) needs no wait for the PV(i) that reads
 //     its buffer.
-//   - one warp has the copy engine land the tiles of K and V (tensor maps,
-//     128-byte swizzle), two the query rows (their order is not a box's).
+//   - one warp has the copy engine land the query rows and the tiles of K and V
+//     (tensor maps, 128-byte swizzle); a tile of query rows holds all of the
+//     group's heads of as many whole tokens as it has room for.
 //   - four softmax warps per row tile, one thread per row, one pass over the
 //     scores: the weights are formed against the reference maximum of the tiles
 //     before, without a maximum of their own; only when their sum shows that
-//     one of them exceeds it by more than 2^kGrow is the tile's maximum taken,
+//     one of them may exceed it by more than 2^24 is the tile's maximum taken,
 //     the pass repeated and O rescaled.  (bf16 weights have fp32's range, so
 //     that a reference far behind costs no precision.)
 //   - a tile's copy may bring rows that no query sees: the next sequence's,
 //     padding, or later tokens.  Their scores are replaced, and their values,
 //     whose weight is 0, are made harmless in shared memory: rows past the
 //     sequence are zeroed, and in tiles that some row does not see whole NaN
-//     and infinities are (one warp looks through them).
+//     and infinities are (two warps look through them).
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
 // frees its tensor memory and leaves its rows unwritten.
@@ -55,9 +56,9 @@ struct Shape {
   static constexpr int kKeys = D == 256 ? 64 : 128;          // keys per tile
   static constexpr int kFirst = kKeys == 128 ? 96 : 32;      // of them, those whose weights are handed on first
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kQueryWarp = kProductWarp + 1;
-  static constexpr int kQueryWarps = 2, kCheckWarp = kQueryWarp + 1;
-  static constexpr int kWarps = kQueryWarp + kQueryWarps;
+  static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kCheckWarp = kProductWarp + 1;
+  static constexpr int kCheckWarps = 2;
+  static constexpr int kWarps = kCheckWarp + kCheckWarps;
   static constexpr int kThreads = 32 * kWarps;
   // (two row tiles: 168 registers a thread at launch, split by role)
   static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -78,11 +79,13 @@ struct Shape {
   static_assert(kTiles * D <= 256 && kSCol + 2 * kKeys <= kTmemCols, "tensor memory");
 };
 
-// What a CTA works on at a time.
+// What a CTA works on at a time: kTiles tiles of query rows of a sequence and
+// key head.  A unit is a token (of a group of more than 128 heads, a token and
+// 128 of its heads); a tile holds tile_tokens of them.
 struct Item {
   int32_t token0;              // the sequence's first token
-  int32_t n;                   // its tokens
-  int32_t row0, rows;          // the block of its rows; rows = 0: no more items
+  int32_t n;                   // its tokens; 0: no more items
+  int32_t unit0;               // first unit of the block
   int32_t head;                // key head
 };
 
@@ -98,17 +101,18 @@ __device__ __forceinline__ Keys<kKeys> prompt_keys(const PromptAttentionArgs& a,
   return k;
 }
 
-// The block of rows with number `index` of all key heads' blocks.  Sequence b's
-// blocks have the numbers from first(b) = floor(seq_start[b] group / block) + b
-// on: those of the sequences before it are fewer.  The last blocks of a
-// sequence, which see the most keys, come first.  One warp looks b up.
-template <int kBlock>
+// The block of kTiles tiles with number `index` of all key heads' blocks.
+// Sequence b's blocks have the numbers from first(b) = floor(units before it /
+// units of a block) + b on: those of the sequences before it are fewer.  The
+// last blocks of a sequence, which see the most keys, come first.  One warp
+// looks b up.
+template <int kTiles>
 __device__ __forceinline__ Item item_at(const PromptAttentionArgs& a, uint32_t index, int lane) {
-  const uint32_t j = a.kv_heads_div.div(index);
+  const uint32_t j = a.kv_heads_div.div(index), block = static_cast<uint32_t>(kTiles * a.tile_tokens);
   Item it{};
   it.head = static_cast<int32_t>(index - j * a.num_kv_heads);
-  auto first = [&](int32_t b) {
-    return static_cast<int64_t>(load_global(a.seq_start + b)) * a.group / kBlock + b;
+  auto first = [&](int32_t b) {                      // (tokens * chunks stay below 2^31; a bad start is skipped below)
+    return static_cast<uint32_t>(load_global(a.seq_start + b)) * static_cast<uint32_t>(a.chunks) / block + b;
   };
   // the largest b < batch_size with first(b) <= j, 32 candidates at a time
   int32_t lo = 0, hi = a.batch_size;                 // first(lo) <= j (or lo = 0), first(hi) > j (or hi = batch_size)
@@ -125,13 +129,12 @@ __device__ __forceinline__ Item item_at(const PromptAttentionArgs& a, uint32_t i
     if (lane == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
     return it;
   }
-  const int64_t total = n * a.group, blocks = (total + kBlock - 1) / kBlock;
-  const int64_t mine = blocks - 1 - (static_cast<int64_t>(j) - (static_cast<int64_t>(q0) * a.group / kBlock + lo));
-  if (mine < 0 || mine >= blocks) return it;
+  const uint32_t blocks = (static_cast<uint32_t>(n) * a.chunks + block - 1) / block;
+  const uint32_t at = j - (static_cast<uint32_t>(q0) * a.chunks / block + lo);     // (wraps where j is before the first)
+  if (at >= blocks) return it;
   it.token0 = q0;
   it.n = static_cast<int32_t>(n);
-  it.row0 = static_cast<int32_t>(mine * kBlock);
-  it.rows = static_cast<int32_t>(min(static_cast<int64_t>(kBlock), total - mine * kBlock));
+  it.unit0 = static_cast<int32_t>((blocks - 1 - at) * block);
   return it;
 }
 
@@ -159,11 +162,10 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[k
 
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
-    prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap kmap,
-                            const __grid_constant__ CUtensorMap vmap) {
+    prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap qmap,
+                            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<D, kTiles>;
   constexpr int kKeys = S::kKeys;
-  constexpr int kBlock = 128 * kTiles;
   wait_for_previous();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
       mbar_init(v_full + 8 * i, 1);
-      mbar_init(v_good + 8 * i, 1);
+      mbar_init(v_good + 8 * i, S::kCheckWarps);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_first + 8 * i, 4);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_free + 8 * i, S::kWarps - 1);
     }
-    mbar_init(q_full, S::kQueryWarps);
+    mbar_init(q_full, 1);
     mbar_init(q_free, 1);
     mbar_init(drain, 1);
     mbar_init(answered, 1);
@@ -228,17 +230,18 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     const volatile Item& s = items[k % kSlots];
     it.token0 = s.token0;
     it.n = s.n;
-    it.row0 = s.row0;
-    it.rows = s.rows;
+    it.unit0 = s.unit0;
     it.head = s.head;
     __syncwarp();
     if (lane == 0) mbar_arrive(item_free + 8 * (k % kSlots));
-    return it.rows > 0;
+    return it.n > 0;
   };
-  auto keys_of_item = [&](const Item& it) {
-    return prompt_keys<kKeys>(a, static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0))),
-                              static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0 + it.rows - 1))));
+  // its first and last token
+  auto first_token = [&](const Item& it) { return static_cast<int32_t>(a.chunk_div.div(static_cast<uint32_t>(it.unit0))); };
+  auto last_token = [&](const Item& it) {
+    return min(it.n - 1, static_cast<int32_t>(a.chunk_div.div(static_cast<uint32_t>(it.unit0 + kTiles * a.tile_tokens - 1))));
   };
+  auto keys_of_item = [&](const Item& it) { return prompt_keys<kKeys>(a, first_token(it), last_token(it)); };
   // Steps [full0, full1) of the keys are visible whole to every row with a
   // last key of at least hi and a first (but for the sinks) of at most lo.
   auto full_steps = [&](const Keys<kKeys>& keys, int32_t hi, int32_t lo, int32_t& full0, int32_t& full1) {
@@ -258,11 +261,19 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     uint32_t pairs = 0;                             // (row tile, key tile) pairs of the items before
     for (uint32_t k = 0; next_item(k, it); ++k) {
       const Keys<kKeys> keys = keys_of_item(it);
-      const int32_t row = static_cast<int32_t>(threadIdx.x);
-      const bool has_row = row < it.rows;
-      const uint32_t flat = static_cast<uint32_t>(it.row0 + min(row, it.rows - 1));
-      const int32_t pos = static_cast<int32_t>(a.group_div.div(flat));
-      const int32_t q_head = it.head * a.group + static_cast<int32_t>(flat - static_cast<uint32_t>(pos) * a.group);
+      // the thread's row: its token (at most the sequence's last) and head
+      const uint32_t row = threadIdx.x & 127, unit = static_cast<uint32_t>(it.unit0 + tile * a.tile_tokens);
+      uint32_t token_of = a.group_div.div(row), head_of = row - token_of * a.group;
+      bool has_row = token_of < static_cast<uint32_t>(a.tile_tokens);
+      token_of += unit;
+      if (a.chunks > 1) {
+        token_of = a.chunk_div.div(unit);
+        head_of = (unit - token_of * a.chunks) * 128 + row;
+        has_row = head_of < static_cast<uint32_t>(a.group);
+      }
+      has_row = has_row && token_of < static_cast<uint32_t>(it.n);
+      const int32_t pos = min(static_cast<int32_t>(token_of), it.n - 1);
+      const int32_t q_head = it.head * a.group + static_cast<int32_t>(head_of);
       const int32_t pos_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       int32_t full0, full1;
       full_steps(keys, __reduce_min_sync(kFull, pos), __reduce_max_sync(kFull, pos_lo), full0, full1);
@@ -319,10 +330,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           };
           // (a row takes a new reference of its own accord, so that its bits do not
           // depend on its neighbours')
-          bool behind = true;
+          bool behind = has_row;                    // (the other rows' queries may be anything)
           if (t > 0 || kFrom > 0) {
             weights();
-            behind = m == -INFINITY || !(sum <= kMaxSum);
+            behind = has_row && (m == -INFINITY || !(sum <= kMaxSum));
           }
           if (__any_sync(kFull, behind)) {
             if (t > 0 || kFrom > 0) {
@@ -436,7 +447,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       uint32_t copied[2] = {0, 0};                  // tiles of K, of V
       uint32_t asked = 0;                           // requests for a next item
       bool waiting = false;                         // one is under way
-      it = item_at<kBlock>(a, blockIdx.x, lane);
+      uint32_t queries = 0;                         // items whose queries were asked for
+      it = item_at<kTiles>(a, blockIdx.x, lane);
       for (uint32_t k = 0;; ++k) {
         // an empty item is passed over; the request for the next one is under way
         // while the keys of this one are copied
@@ -459,10 +471,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           __syncwarp();
           more = x >= 0;
           it = Item{};
-          if (more) it = item_at<kBlock>(a, static_cast<uint32_t>(x), lane);
+          if (more) it = item_at<kTiles>(a, static_cast<uint32_t>(x), lane);
         };
         if (k > 0) take();
-        while (ok && more && it.rows == 0) {
+        while (ok && more && it.n == 0) {
           ask();
           take();
         }
@@ -471,14 +483,30 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           volatile Item& s = items[k % kSlots];
           s.token0 = it.token0;
           s.n = it.n;
-          s.row0 = it.row0;
-          s.rows = it.rows;
+          s.unit0 = it.unit0;
           s.head = it.head;
           mbar_arrive(item_full + 8 * (k % kSlots));
         }
         __syncwarp();
-        if (it.rows == 0) break;
+        if (it.n == 0) break;
         ask();
+        // the query rows: the tile's tokens and heads as a box (heads past the
+        // group's and tokens past the sequence's are rows that no one stores)
+        if (k > 0 && !have(q_free, k - 1)) break;
+        if (elected) {
+          mbar_arrive_expect_tx(q_full, kTiles * S::kBlocks * 128 * a.tile_tokens * min(a.group, 128));
+#pragma unroll
+          for (int w = 0; w < kTiles; ++w) {
+            const int32_t unit = it.unit0 + w * a.tile_tokens;
+            const int32_t token = a.chunks > 1 ? static_cast<int32_t>(a.chunk_div.div(static_cast<uint32_t>(unit))) : unit;
+#pragma unroll
+            for (int i = 0; i < S::kBlocks; ++i)
+              tma_load_3d(base + w * S::kQTile + i * S::kQBlock, &qmap, 64 * i,
+                          it.head * a.group + (unit - token * a.chunks) * 128, it.token0 + token, q_full);
+          }
+        }
+        __syncwarp();
+        queries = k + 1;
         const Keys<kKeys> keys = keys_of_item(it);
         for (int32_t t = 0; t < keys.steps && ok; ++t) {
           const uint32_t at = tiles + t, st = at % S::kStages;
@@ -504,6 +532,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       const long long start = clock64();
       if (waiting)
         while (!mbar_try_wait(answered, asked & 1))
+          if (clock64() - start > kDrainCycles) break;
+      if (queries > 0)
+        while (!mbar_try_wait(q_full, (queries - 1) & 1))
           if (clock64() - start > kDrainCycles) break;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -590,8 +621,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---- the query rows; one of the two warps looks through V ----------------
-      const int me = warp - S::kQueryWarp;
+      // ---- V where some row does not see the whole tile ------------------------
+      const int me = warp - S::kCheckWarp;
       if (blockIdx.x == 0 && me == 0) {               // sequences that item_at may not come across
         for (int32_t b = lane; b < a.batch_size; b += 32) {
           const int32_t q0 = load_global(a.seq_start + b), q1 = load_global(a.seq_start + b + 1);
@@ -603,58 +634,46 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
         const Keys<kKeys> keys = keys_of_item(it);
-        if (k > 0 && !have(q_free, k - 1)) break;
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;        // lanes to a row, rows at once
-        const int c = lane % kLanes, sub = lane / kLanes;
-        constexpr int kRows = kBlock / S::kQueryWarps;
-#pragma unroll 4
-        for (int r = me * kRows; r < (me + 1) * kRows; r += kAtOnce) {
-          const int rr = r + sub;
-          const bool live = rr < it.rows;
-          const uint32_t flat = static_cast<uint32_t>(it.row0 + (live ? rr : 0)), tk = a.group_div.div(flat);
-          const int32_t h = it.head * a.group + static_cast<int32_t>(flat - tk * a.group);
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                     (static_cast<int64_t>(it.token0) + tk) * a.q_stride_t + h * a.q_stride_h + 8 * c;
-          cp_async<16>(base + (rr >> 7) * S::kQTile + (c >> 3) * S::kQBlock + sw128_offset(rr & 127, c & 7), src,
-                       live ? 16 : 0);
-        }
-        cp_commit();
-        cp_wait<0>();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        if (warp == S::kCheckWarp) {
-          const int32_t t0 = static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0)));
-          const int32_t t1 = static_cast<int32_t>(a.group_div.div(static_cast<uint32_t>(it.row0 + it.rows - 1)));
-          int32_t full0, full1;
-          full_steps(keys, t0, a.window > 0 ? max(0, t1 - a.window + 1) : 0, full0, full1);
-          for (int32_t t = 0; t < keys.steps; ++t) {
-            const uint32_t at = tiles + t, st = at % S::kStages;
-            ok = have(v_full + 8 * st, at / S::kStages);
-            if (!ok) break;
-            if (t < full0 || t >= full1) {
-              const int32_t there = keys.limit(t) - keys.base(t);   // the tile's rows of keys; those past them: zeros
-              const uint32_t v = base + S::kV + st * S::kTileBytes;
-#pragma unroll 4
-              for (uint32_t i = lane; i < S::kTileBytes / 16; i += 32) {
-                uint4 x = ld_shared16(v + 16 * i);
-                const bool in = static_cast<int32_t>((i >> 3) % kKeys) < there;
-                constexpr uint32_t kAbs = 0x7FFF7FFFu;
-                uint32_t top = __vimax3_u16x2(x.x & kAbs, x.y & kAbs, x.z & kAbs);
-                top = __vimax3_u16x2(top, x.w & kAbs, 0u);
-                if (!in || (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
-                  auto finite = [&](uint32_t w) {
-                    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
-                  };
-                  x = in ? make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w)) : make_uint4(0, 0, 0, 0);
-                  st_shared16(v + 16 * i, x);
+        int32_t full0, full1;
+        full_steps(keys, first_token(it), a.window > 0 ? max(0, last_token(it) - a.window + 1) : 0, full0, full1);
+        for (int32_t t = 0; t < keys.steps; ++t) {
+          const uint32_t at = tiles + t, st = at % S::kStages;
+          ok = have(v_full + 8 * st, at / S::kStages);
+          if (!ok) break;
+          if (t < full0 || t >= full1) {
+            const int32_t there = keys.limit(t) - keys.base(t);   // the tile's rows of keys; those past them: zeros
+            uint4* v = reinterpret_cast<uint4*>(smem + S::kV + st * S::kTileBytes) + lane;
+            constexpr int kBatch = 8;                             // loads under way at once
+#pragma unroll 1
+            for (uint32_t i = me * (32 * kBatch); i < S::kTileBytes / 16; i += S::kCheckWarps * 32 * kBatch) {
+              uint4 x[kBatch];
+#pragma unroll
+              for (int j = 0; j < kBatch; ++j) x[j] = v[i + 32 * j];
+              constexpr uint32_t kAbs = 0x7FFF7FFFu;
+              uint32_t top = 0;                                   // largest bits below the signs, of either half
+#pragma unroll
+              for (int j = 0; j < kBatch; ++j) {
+                top = __vimax3_u16x2(top, x[j].x & kAbs, x[j].y & kAbs);
+                top = __vimax3_u16x2(top, x[j].z & kAbs, x[j].w & kAbs);
+              }
+              // (rows of keys: eight chunks each, the batch's 4 kBatch in a row)
+              if (static_cast<int32_t>((i / 8) % kKeys) + 4 * kBatch > there || (top & 0xFFFFu) >= 0x7F80u ||
+                  (top >> 16) >= 0x7F80u) {
+                auto finite = [](uint32_t w) {
+                  return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+                };
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                  const bool in = static_cast<int32_t>(((i + 32 * j + lane) / 8) % kKeys) < there;
+                  v[i + 32 * j] = in ? make_uint4(finite(x[j].x), finite(x[j].y), finite(x[j].z), finite(x[j].w))
+                                     : make_uint4(0, 0, 0, 0);
                 }
               }
-              fence_async_smem();
-              __syncwarp();
             }
-            if (lane == 0) mbar_arrive(v_good + 8 * st);
+            fence_async_smem();
+            __syncwarp();
           }
+          if (lane == 0) mbar_arrive(v_good + 8 * st);
         }
         tiles += keys.steps;
       }
@@ -668,6 +687,22 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(*s_tmem), "r"(kTmemCols) : "memory");
   }
+}
+
+// Tensor map of the queries [tokens][heads][D], tiles of 64 dimensions of a
+// group's heads of tile_tokens tokens with the 128-byte swizzle.
+bool query_tensor_map(const PromptAttentionArgs& a, CUtensorMap* map) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.head_size), static_cast<cuuint64_t>(a.num_heads),
+                              static_cast<cuuint64_t>(a.num_tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.q_stride_h) * 2, static_cast<cuuint64_t>(a.q_stride_t) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.group < 128 ? a.group : 128),
+                             static_cast<cuuint32_t>(a.tile_tokens)};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, elem_strides,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tensor map of keys or values [tokens][heads][D], tiles of 64 dimensions of
@@ -688,23 +723,23 @@ bool key_tensor_map(const void* p, int64_t stride_t, int64_t stride_h, int32_t h
 template <int D, int kTiles>
 cudaError_t launch(const PromptAttentionArgs& a, cudaStream_t stream) {
   using S = Shape<D, kTiles>;
-  CUtensorMap kmap, vmap;
-  if (!key_tensor_map<D, S::kKeys>(a.k, a.k_stride_t, a.k_stride_h, a.num_kv_heads, a.num_tokens, &kmap) ||
+  CUtensorMap qmap, kmap, vmap;
+  if (!query_tensor_map(a, &qmap) || !key_tensor_map<D, S::kKeys>(a.k, a.k_stride_t, a.k_stride_h, a.num_kv_heads, a.num_tokens, &kmap) ||
       !key_tensor_map<D, S::kKeys>(a.v, a.v_stride_t, a.v_stride_h, a.num_kv_heads, a.num_tokens, &vmap))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kTiles>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = a.num_tokens * a.group / (128 * kTiles) + a.batch_size;     // the numbers of item_at
+  const int64_t blocks = a.num_tokens * a.chunks / (kTiles * a.tile_tokens) + a.batch_size;     // the numbers of item_at
   return launch_dependent(prompt_attention_kernel<D, kTiles>, dim3(static_cast<unsigned>(blocks * a.num_kv_heads)),
-                          S::kThreads, S::kSmem, 1, stream, a, kmap, vmap);
+                          S::kThreads, S::kSmem, 1, stream, a, qmap, kmap, vmap);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t stream) {
   // two row tiles share a key tile wherever a sequence can fill them
-  const bool two = static_cast<int64_t>(a.max_seq_len) * a.group > 128;
+  const bool two = static_cast<int64_t>(a.max_seq_len) * a.chunks > a.tile_tokens;
   switch (a.head_size) {
     case 64: return two ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
     case 128: return two ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);

@@ -866,8 +866,7 @@ int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_head
  * unwritten (KVQ_STATUS_TIMEOUT).
  * q: bf16 [num_tokens, num_heads, head_size]; k, v: bf16 [num_tokens,
  * num_kv_heads, head_size]; token and head strides in elements (multiples of
- * 8; those of k and v positive and below 2^38); head_size 64, 128 or 256;
- * num_heads a multiple of num_kv_heads.  out: as q, token stride >=
+ * 8; positive and below 2^38); head_size 64, 128 or 256; num_heads a multiple of num_kv_heads.  out: as q, token stride >=
  * (num_heads - 1) * head stride + head_size.  lse: fp32 [num_tokens,
  * num_heads], token stride lse_stride_t, or NULL.  out and lse overlap no
  * input.  softmax_scale: softmax_scale * log2(e) is finite in fp32.
