@@ -34,7 +34,7 @@
 //     padding, or later tokens.  Their scores are replaced, and their values,
 //     whose weight is 0, are made harmless in shared memory: rows past the
 //     sequence are zeroed, and in tiles that some row does not see whole NaN
-//     and infinities are (two warps look through them).
+//     and infinities are (another warp looks through them).
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
 // frees its tensor memory and leaves its rows unwritten.
@@ -53,18 +53,18 @@ constexpr int kSlots = 2;                         // work items known at once
 
 template <int D, int kTiles>
 struct Shape {
-  static constexpr int kKeys = D == 256 ? 64 : 128;          // keys per tile
-  static constexpr int kFirst = kKeys == 128 ? 96 : 32;      // of them, those whose weights are handed on first
+  static constexpr int kKeys = 64;                           // keys per tile
+  static constexpr int kFirst = 64;                          // of them, those whose weights are handed on first
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kCheckWarp = kProductWarp + 1;
-  static constexpr int kCheckWarps = 2;
+  static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kProductWarps = kTiles;
+  static constexpr int kCheckWarp = kProductWarp + kProductWarps, kCheckWarps = 3 - kTiles;
   static constexpr int kWarps = kCheckWarp + kCheckWarps;
   static constexpr int kThreads = 32 * kWarps;
   // (two row tiles: 168 registers a thread at launch, split by role)
   static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
   static_assert(kTiles == 1 || 32 * kSoftmaxWarps * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
-  static constexpr int kStages = 2;                          // tiles of K, of V
+  static constexpr int kStages = D == 256 ? 2 : 4;           // tiles of K, of V
   static constexpr uint32_t kQBlock = 128 * 128;             // 64 dimensions of a row tile
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKBlock = kKeys * 128;           // 64 dimensions of a key tile
@@ -76,7 +76,7 @@ struct Shape {
   // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
   static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kTiles * D <= 256 && kSCol + 2 * kKeys <= kTmemCols, "tensor memory");
+  static_assert(kTiles * D <= 256 && kSCol + 4 * kKeys <= kTmemCols, "tensor memory");
 };
 
 // What a CTA works on at a time: kTiles tiles of query rows of a sequence and
@@ -172,17 +172,20 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
   const uint32_t bar = base + S::kMisc;
-  const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_good = bar + 48, v_empty = bar + 64;   // [kStages]
-  // score buffers: scores there, first and all weights there, their products done
-  const uint32_t s_full = bar + 80, p_first = bar + 96, p_full = bar + 112, o_first = bar + 128, o_done = bar + 144;
-  const uint32_t o_free = bar + 160;                                            // [row tile]
-  const uint32_t q_full = bar + 176, q_free = bar + 184, drain = bar + 192;
-  const uint32_t item_full = bar + 200, item_free = bar + 216;                  // [kSlots]
-  const uint32_t answer = bar + 240, answered = bar + 232;                      // of the request for a next item
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 256);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 260);
-  volatile Item* items = reinterpret_cast<volatile Item*>(smem + S::kMisc + 264);
-  static_assert(264 + kSlots * sizeof(Item) <= 512, "barrier layout");
+  const uint32_t k_full = bar, k_empty = k_full + 8 * S::kStages, v_full = k_empty + 8 * S::kStages;     // [kStages]
+  const uint32_t v_good = v_full + 8 * S::kStages, v_empty = v_good + 8 * S::kStages;
+  // [score buffer]: scores there, first and all weights there, their products done
+  const uint32_t s_full = v_empty + 8 * S::kStages, p_first = s_full + 32, p_full = p_first + 32, o_first = p_full + 32;
+  const uint32_t o_done = o_first + 32;
+  const uint32_t o_free = o_done + 32, drain = o_free + 16;                     // [row tile]
+  const uint32_t item_full = drain + 16, item_free = item_full + 8 * kSlots;    // [kSlots]
+  const uint32_t q_full = item_free + 8 * kSlots, q_free = q_full + 8, answered = q_free + 8;
+  const uint32_t answer = (answered + 8 + 15) & ~15u;                           // of the request for a next item
+  uint8_t* words = smem + S::kMisc + (answer + 16 - bar);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(words);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(words + 4);
+  volatile Item* items = reinterpret_cast<volatile Item*>(words + 8);
+  static_assert(40 * S::kStages + 5 * 32 + 32 + 16 * kSlots + 24 + 32 + 8 + kSlots * sizeof(Item) <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -191,24 +194,30 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, S::kProductWarps);
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_good + 8 * i, S::kCheckWarps);
-      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, S::kProductWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_first + 8 * i, 4);
       mbar_init(p_full + 8 * i, 4);
       mbar_init(o_first + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(o_free + 8 * i, 4);
+      mbar_init(drain + 8 * i, 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(item_full + 8 * i, 1);
       mbar_init(item_free + 8 * i, S::kWarps - 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
-    mbar_init(drain, 1);
+    mbar_init(q_free, S::kProductWarps);
     mbar_init(answered, 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -228,10 +237,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   auto next_item = [&](uint32_t k, Item& it) {
     if (!have(item_full + 8 * (k % kSlots), k / kSlots)) return false;
     const volatile Item& s = items[k % kSlots];
-    it.token0 = s.token0;
-    it.n = s.n;
-    it.unit0 = s.unit0;
-    it.head = s.head;
+    // (uniform for the compiler too)
+    it.token0 = __shfl_sync(kFull, s.token0, 0);
+    it.n = __shfl_sync(kFull, s.n, 0);
+    it.unit0 = __shfl_sync(kFull, s.unit0, 0);
+    it.head = __shfl_sync(kFull, s.head, 0);
     __syncwarp();
     if (lane == 0) mbar_arrive(item_free + 8 * (k % kSlots));
     return it.n > 0;
@@ -242,6 +252,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     return min(it.n - 1, static_cast<int32_t>(a.chunk_div.div(static_cast<uint32_t>(it.unit0 + kTiles * a.tile_tokens - 1))));
   };
   auto keys_of_item = [&](const Item& it) { return prompt_keys<kKeys>(a, first_token(it), last_token(it)); };
+  // The score buffer of a row tile and its key tile `at` (of all items'), and
+  // which use of it that is.
+  auto buffer_of = [](int tile, uint32_t at) { return 2 * static_cast<uint32_t>(tile) + (at & 1); };
+  auto use_of = [](uint32_t at) { return at >> 1; };
   // Steps [full0, full1) of the keys are visible whole to every row with a
   // last key of at least hi and a first (but for the sinks) of at most lo.
   auto full_steps = [&](const Keys<kKeys>& keys, int32_t hi, int32_t lo, int32_t& full0, int32_t& full1) {
@@ -258,7 +272,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
     const float sc = a.scale_log2;
-    uint32_t pairs = 0;                             // (row tile, key tile) pairs of the items before
+    uint32_t tiles = 0;                             // of the items before
     for (uint32_t k = 0; next_item(k, it); ++k) {
       const Keys<kKeys> keys = keys_of_item(it);
       // the thread's row: its token (at most the sequence's last) and head
@@ -281,10 +295,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       float m = -INFINITY, l = 0.0f;                // reference maximum, sum
       bool done = true;                             // every wait was met
       for (int32_t t = 0; t < keys.steps; ++t) {
-        const uint32_t pair = pairs + (kTiles == 2 ? 2 * t + tile : t);
-        const uint32_t buf = pair & 1;
+        const uint32_t at = tiles + t, buf = buffer_of(tile, at), use = use_of(at);
         const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
-        if (!have(s_full + 8 * buf, pair >> 1)) {
+        if (!have(s_full + 8 * buf, use)) {
           done = false;
           break;
         }
@@ -298,7 +311,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         }
         // The weights of kCount keys from column kFrom on, against the reference m,
         // are formed, handed on and summed.  `before`: the barrier and phase of the
-        // product into O before these weights' (0: no wait needed, or nothing in O).
+        // product into O before these weights'.
         auto part = [&](auto from_c, auto& s, uint32_t before, uint32_t phase, bool in_o, uint32_t ready) {
           constexpr int kFrom = decltype(from_c)::value;
           constexpr int kCount = static_cast<int>(sizeof(s) / 4);
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             weights();
             l *= alpha;
             if (in_o) {
-              if (before != 0 && !have(before, phase)) return false;
+              if (!have(before, phase)) return false;
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 float o[32];
@@ -373,23 +386,26 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           if (lane == 0) mbar_arrive(ready + 8 * buf);
           return true;
         };
-        uint32_t first[S::kFirst], rest[kKeys - S::kFirst];
+        // (before O is rescaled: the product of the tile before is waited for; for
+        // the second part, that of the first one's weights)
+        uint32_t first[S::kFirst];
         tmem_load(s_col, first);
         tmem_loaded(first);
-        tmem_load(s_col + S::kFirst, rest);         // under way meanwhile
-        // The product before: of the tile before, which with two row tiles this
-        // tile's scores follow, with one they do not; then of these first weights.
-        done = part(std::integral_constant<int, 0>{}, first, kTiles == 1 ? o_done + 8 * (buf ^ 1) : 0, (pair - 1) >> 1, t > 0,
-                    p_first);
-        if (!done) break;
-        tmem_loaded(rest);
-        done = part(std::integral_constant<int, S::kFirst>{}, rest, o_first + 8 * buf, pair >> 1, true, p_full);
+        if constexpr (S::kFirst == kKeys) {
+          done = part(std::integral_constant<int, 0>{}, first, o_done + 8 * (buf ^ 1), use_of(at - 1), t > 0, p_full);
+        } else {
+          uint32_t rest[kKeys - S::kFirst];
+          tmem_load(s_col + S::kFirst, rest);       // under way meanwhile
+          done = part(std::integral_constant<int, 0>{}, first, o_done + 8 * (buf ^ 1), use_of(at - 1), t > 0, p_first);
+          if (!done) break;
+          tmem_loaded(rest);
+          done = part(std::integral_constant<int, S::kFirst>{}, rest, o_first + 8 * buf, use, true, p_full);
+        }
         if (!done) break;
       }
       // the last product is done: O is complete
-      const uint32_t last = pairs + (kTiles == 2 ? 2 * (keys.steps - 1) + tile : keys.steps - 1);
-      pairs += kTiles * keys.steps;
-      if (done) done = have(o_done + 8 * (last & 1), last >> 1);
+      tiles += keys.steps;
+      if (done) done = have(o_done + 8 * buffer_of(tile, tiles - 1), use_of(tiles - 1));
       if (!done) break;                             // uniform over the warp
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       // The rows leave in pieces of 64 values (128 bytes), eight lanes to a
@@ -543,41 +559,39 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             if (clock64() - start > kDrainCycles) break;
       }
       __syncwarp();
-    } else if (warp == S::kProductWarp) {
-      // ---- the products (one elected lane; the warp waits together) ------------
+    } else if (warp < S::kCheckWarp) {
+      // ---- a row tile's products (one elected lane; the warp waits together) ---
+      const int w = warp - S::kProductWarp;
       constexpr uint32_t kIdescS = idesc_bf16(128, kKeys, false), kIdescO = idesc_bf16(128, D, true);
-      const uint64_t qdesc = sw128_desc(base, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
+      constexpr int kAhead = 2;                     // scores before a tile's output
+      const uint64_t qdesc = sw128_desc(base + w * S::kQTile, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
       const uint64_t vdesc = sw128_desc(base + S::kV, S::kKBlock, 1024);
-      uint32_t pairs = 0, tiles = 0;
+      const uint32_t o = tmem + w * D;
+      uint32_t tiles = 0;                           // of the items before
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
-        const Keys<kKeys> keys = keys_of_item(it);
-        const int32_t n = kTiles * keys.steps;
-        // S_w(t) = Q_w K(t)^T
-        auto keys_there = [&](int32_t i) {
-          const uint32_t at = tiles + (kTiles == 2 ? i >> 1 : i);
-          return (kTiles == 2 && (i & 1)) || have(k_full + 8 * (at % S::kStages), at / S::kStages);
-        };
-        auto scores = [&](int32_t i) {
-          const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
-          const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
-          const uint64_t qd = qdesc + ((w * S::kQTile) >> 4), kd = kdesc + ((st * S::kTileBytes) >> 4);
+        const int32_t n = keys_of_item(it).steps;
+        auto keys_there = [&](int32_t t) { return have(k_full + 8 * ((tiles + t) % S::kStages), (tiles + t) / S::kStages); };
+        // S(t) = Q K(t)^T
+        auto scores = [&](int32_t t) {
+          const uint32_t st = (tiles + t) % S::kStages, buf = buffer_of(w, tiles + t);
+          const uint64_t kd = kdesc + ((st * S::kTileBytes) >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            warp_mma(elected, tmem + kSCol + kKeys * buf, qd + (((ks >> 2) * S::kQBlock + 32 * (ks & 3)) >> 4),
+            warp_mma(elected, tmem + kSCol + kKeys * buf, qdesc + (((ks >> 2) * S::kQBlock + 32 * (ks & 3)) >> 4),
                      kd + (((ks >> 2) * S::kKBlock + 32 * (ks & 3)) >> 4), kIdescS, ks != 0);
           warp_commit(elected, s_full + 8 * buf);
-          if (w == kTiles - 1) warp_commit(elected, k_empty + 8 * st);
-          if (i == n - 1) warp_commit(elected, q_free);
+          warp_commit(elected, k_empty + 8 * st);
+          if (t == n - 1) warp_commit(elected, q_free);
         };
         ok = have(q_full, k);
-        for (int32_t i = 0; i < min(n, 2) && ok; ++i) {
-          ok = keys_there(i);
-          if (ok) scores(i);
+        for (int32_t t = 0; t < min(n, kAhead) && ok; ++t) {
+          ok = keys_there(t);
+          if (ok) scores(t);
         }
-        for (int32_t i = 0; i < n && ok; ++i) {
-          const int32_t t = kTiles == 2 ? i >> 1 : i, w = kTiles == 2 ? i & 1 : 0;
-          const uint32_t st = (tiles + t) % S::kStages, buf = (pairs + i) & 1;
+        if (ok && k > 0) ok = have(o_free + 8 * w, k - 1);
+        for (int32_t t = 0; t < n && ok; ++t) {
+          const uint32_t st = (tiles + t) % S::kStages, buf = buffer_of(w, tiles + t), use = use_of(tiles + t);
 #ifdef KVQ_ATTN_STALL_TILE
           // Failure-detection build only: no product from this tile on, as if
           // the tensor work never completed; the other roles' bounded waits run out.
@@ -586,34 +600,34 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             break;
           }
 #endif
-          // O_w += P_w(t) V(t), as its weights come; what else it and the scores
+          // O += P(t) V(t), as its weights come; what else it and the scores
           // behind it need is waited for before them
-          ok = !(t == 0 && k > 0) || have(o_free + 8 * w, k - 1);
-          if (ok && w == 0) ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
-          if (ok && i + 2 < n) ok = keys_there(i + 2);
+          ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
+          if (ok && t + kAhead < n) ok = keys_there(t + kAhead);
           const uint64_t vd = vdesc + ((st * S::kTileBytes) >> 4);
           auto product = [&](int ks) {
-            warp_mma_ta(elected, tmem + w * D, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
+            warp_mma_ta(elected, o, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
                         (t > 0 || ks > 0) ? 1u : 0u);
           };
-          if (!ok || !(ok = have(p_first + 8 * buf, (pairs + i) >> 1))) break;
+          if constexpr (S::kFirst < kKeys) {
+            if (!ok || !(ok = have(p_first + 8 * buf, use))) break;
 #pragma unroll
-          for (int ks = 0; ks < S::kFirst / 16; ++ks) product(ks);
-          warp_commit(elected, o_first + 8 * buf);
-          if (!(ok = have(p_full + 8 * buf, (pairs + i) >> 1))) break;
+            for (int ks = 0; ks < S::kFirst / 16; ++ks) product(ks);
+            warp_commit(elected, o_first + 8 * buf);
+          }
+          if (!ok || !(ok = have(p_full + 8 * buf, use))) break;
 #pragma unroll
-          for (int ks = S::kFirst / 16; ks < kKeys / 16; ++ks) product(ks);
+          for (int ks = S::kFirst < kKeys ? S::kFirst / 16 : 0; ks < kKeys / 16; ++ks) product(ks);
           warp_commit(elected, o_done + 8 * buf);
-          if (w == kTiles - 1) warp_commit(elected, v_empty + 8 * st);
-          if (i + 2 < n) scores(i + 2);
+          warp_commit(elected, v_empty + 8 * st);
+          if (t + kAhead < n) scores(t + kAhead);
         }
-        pairs += n;
-        tiles += keys.steps;
+        tiles += n;
       }
       // the products still in flight are drained (bounded, whatever the abort flag says)
-      warp_commit(elected, drain);
+      warp_commit(elected, drain + 8 * w);
       const long long start = clock64();
-      while (!mbar_try_wait(drain, 0)) {
+      while (!mbar_try_wait(drain + 8 * w, 0)) {
         if (clock64() - start > kDrainCycles) {
           *s_abort = 1;
           break;
@@ -634,39 +648,48 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
         const Keys<kKeys> keys = keys_of_item(it);
+        const int32_t hi = first_token(it), lo = a.window > 0 ? max(0, last_token(it) - a.window + 1) : 0;
         int32_t full0, full1;
-        full_steps(keys, first_token(it), a.window > 0 ? max(0, last_token(it) - a.window + 1) : 0, full0, full1);
+        full_steps(keys, hi, lo, full0, full1);
         for (int32_t t = 0; t < keys.steps; ++t) {
           const uint32_t at = tiles + t, st = at % S::kStages;
           ok = have(v_full + 8 * st, at / S::kStages);
           if (!ok) break;
           if (t < full0 || t >= full1) {
-            const int32_t there = keys.limit(t) - keys.base(t);   // the tile's rows of keys; those past them: zeros
+            // Rows of the tile: those from `there` on are no keys (zeros); of the
+            // others, [all0, all1) are visible to every query and stay as they are.
+            const int32_t there = keys.limit(t) - keys.base(t);
+            const int32_t all0 = t < keys.sink_steps ? 0 : max(0, lo - keys.base(t));
+            const int32_t all1 = min(there, hi + 1 - keys.base(t));
             uint4* v = reinterpret_cast<uint4*>(smem + S::kV + st * S::kTileBytes) + lane;
-            constexpr int kBatch = 8;                             // loads under way at once
+            constexpr int kRows = 4, kBatch = 8;                  // rows to a load of the warp; loads under way at once
 #pragma unroll 1
-            for (uint32_t i = me * (32 * kBatch); i < S::kTileBytes / 16; i += S::kCheckWarps * 32 * kBatch) {
-              uint4 x[kBatch];
+            for (int32_t r = kRows * kBatch * me; r < kKeys; r += kRows * kBatch * S::kCheckWarps) {
+              if (r >= all0 && r + kRows * kBatch <= all1) continue;
+#pragma unroll 1
+              for (int block = 0; block < S::kBlocks; ++block) {
+                uint4* row = v + block * (S::kKBlock / 16) + r * 8;
+                uint4 x[kBatch];
 #pragma unroll
-              for (int j = 0; j < kBatch; ++j) x[j] = v[i + 32 * j];
-              constexpr uint32_t kAbs = 0x7FFF7FFFu;
-              uint32_t top = 0;                                   // largest bits below the signs, of either half
-#pragma unroll
-              for (int j = 0; j < kBatch; ++j) {
-                top = __vimax3_u16x2(top, x[j].x & kAbs, x[j].y & kAbs);
-                top = __vimax3_u16x2(top, x[j].z & kAbs, x[j].w & kAbs);
-              }
-              // (rows of keys: eight chunks each, the batch's 4 kBatch in a row)
-              if (static_cast<int32_t>((i / 8) % kKeys) + 4 * kBatch > there || (top & 0xFFFFu) >= 0x7F80u ||
-                  (top >> 16) >= 0x7F80u) {
-                auto finite = [](uint32_t w) {
-                  return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
-                };
+                for (int j = 0; j < kBatch; ++j) x[j] = row[32 * j];
+                constexpr uint32_t kAbs = 0x7FFF7FFFu;
+                uint32_t top = 0;                                 // largest bits below the signs, of either half
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                  const bool in = static_cast<int32_t>(((i + 32 * j + lane) / 8) % kKeys) < there;
-                  v[i + 32 * j] = in ? make_uint4(finite(x[j].x), finite(x[j].y), finite(x[j].z), finite(x[j].w))
-                                     : make_uint4(0, 0, 0, 0);
+                  top = __vimax3_u16x2(top, x[j].x & kAbs, x[j].y & kAbs);
+                  top = __vimax3_u16x2(top, x[j].z & kAbs, x[j].w & kAbs);
+                }
+                if (r + kRows * kBatch > there || (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+                  auto finite = [](uint32_t w) {
+                    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+                  };
+#pragma unroll
+                  for (int j = 0; j < kBatch; ++j) {
+                    const int32_t at = r + kRows * j + lane / 8;
+                    if (at >= all0 && at < all1) continue;
+                    row[32 * j] = at < there ? make_uint4(finite(x[j].x), finite(x[j].y), finite(x[j].z), finite(x[j].w))
+                                             : make_uint4(0, 0, 0, 0);
+                  }
                 }
               }
             }
