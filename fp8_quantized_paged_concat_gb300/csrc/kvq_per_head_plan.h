@@ -38,7 +38,7 @@ inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t
 // (The limit at D = 64 was set when the tensor memory kernel took 220 there; a
 // call this large is now past the crossing at 64 rows.)
 inline int64_t most_few_rows(int32_t head_size, bool fp8 = false) {
-  return fp8 ? INT32_MAX : head_size == 64 ? 64 : head_size == 128 ? 32 : 16;
+  return fp8 ? 64 : head_size == 64 ? 64 : head_size == 128 ? 32 : 16;
 }
 
 // Rows per block of the tensor memory kernel: one row tile, or two that share

@@ -58,7 +58,7 @@ constexpr int kValidRing = 16;
 constexpr uint32_t kBlockBytes = 128 * 128;       // 64 dimensions of 128 rows of q
 constexpr uint32_t kKBlock = kKeys * 128;         // 64 dimensions of a key tile
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kFp8>
 struct Shape {
   // Warps: softmax; those that decode keys, and the one that issues the
   // scores' products; those that decode values, and the one that issues the
@@ -78,20 +78,21 @@ struct Shape {
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
                     kThreads * kStartRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
-  static constexpr int kStages = D == 256 ? 2 : 3;           // decoded tiles of K, of V
+  static constexpr int kStages = D == 256 ? 2 : kFp8 ? 4 : 3;   // decoded tiles of K, of V
   static constexpr uint32_t kTileBytes = kBlocks * kKBlock;
   static constexpr uint32_t kQTile = kBlocks * kBlockBytes;
   static constexpr uint32_t kK = kTiles * kQTile;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   // raw entries of one side: rings of chunks of keys, data rows then scale rows
   static constexpr int kChunk = D == 256 ? 32 : 64;
-  static constexpr int kParts = kKeys / kChunk;              // chunks per tile
+  [[maybe_unused]] static constexpr int kParts = kKeys / kChunk;   // chunks per tile
   static constexpr int kRing = D == 256 ? 3 : 4;
   static constexpr uint32_t kRawScales = kChunk * (D / 2);
   static constexpr uint32_t kRawBytes = kRawScales + kChunk * (D / 16);
   static constexpr uint32_t kRawK = kV + kStages * kTileBytes;
   static constexpr uint32_t kRawV = kRawK + kRing * kRawBytes;
-  static constexpr uint32_t kMisc = kRawV + kRing * kRawBytes;
+  // (e4m3 codes go from global memory straight through registers)
+  static constexpr uint32_t kMisc = kFp8 ? kRawK : kRawV + kRing * kRawBytes;
   // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
   static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -210,7 +211,7 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
                                         int32_t s0, int32_t n_tiles, int me, int lane, bool bad_index, uint32_t base,
                                         uint32_t full, uint32_t empty, uint8_t* valid_ring,
                                         volatile int* s_abort) {
-  using S = Shape<D, kTiles>;
+  using S = Shape<D, kTiles, false>;
   constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
   constexpr int kGroups = S::kChunk / 8, kPasses = (kGroups + kWarps - 1) / kWarps;
   static_assert(kPasses <= 4, "a lane per row");
@@ -318,12 +319,158 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
 }
 
-template <int D, int kTiles>
-__global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
+// The same for e4m3 entries.  A side's tile is decoded relative to its largest
+// page scale, 2^(top - 127): a row's values are multiplied by the power of two
+// between its page's and that, which is exact in f16 while they are less than
+// 2^15 apart; `top` itself goes into the scores, and the weights, of the tile.
+//
+// Every warp looks up all of the tile's keys, lane l keys l and l + 32 (page
+// ids a tile before the loads that need them), and so knows `top`.  D / 16
+// lanes take a row, 16 codes each, 512 / D rows at once: groups me, me +
+// kWarps, ... of that many rows are the warp's.  The codes of the next tile are
+// under way while one is decoded.  Eight lanes that store at once hold half a
+// 64-dimension block of two neighbouring rows, which the swizzle keeps apart.
+template <int D, int kTiles, bool kValues>
+__device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b, uint32_t head, const Keys<kKeys>& keys,
+                                            int32_t s0, int32_t n_tiles, int32_t full0, int32_t full1, int me, int lane,
+                                            bool bad_index, uint32_t base, uint32_t full, uint32_t empty,
+                                            uint64_t* key_ring, volatile int* s_abort) {
+  using S = Shape<D, kTiles, true>;
+  constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
+  constexpr int kAtOnce = 512 / D, kGroups = kKeys / kAtOnce, kPasses = (kGroups + kWarps - 1) / kWarps;
+  const uint32_t tiles = base + (kValues ? S::kV : S::kK);
+  const uint32_t c = D == 64 ? lane & 3 : (lane & 3) + 4 * (D == 128 ? (lane >> 3) & 1 : lane >> 3);   // 16-code piece
+  const uint32_t sub = D == 64 ? lane >> 2 : ((lane >> 2) & 1) + (D == 128 ? 2 * (lane >> 4) : 0);     // row of its group
+  const uint8_t* side = a.cache + (kValues ? a.region : 0);
+  const int32_t* table = a.block_table + b * a.block_table_stride;
+  const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
+  LookUp next[2];
+  auto look_up = [&](int32_t t) {                   // keys lane, lane + 32 of tile t
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t step = s0 + t;
+      const uint32_t p = static_cast<uint32_t>(keys.base(step)) + 32 * h + lane;
+      next[h] = look_up_position(a, table, head_row, t < n_tiles && p < static_cast<uint32_t>(keys.limit(step)), p);
+    }
+  };
+  // A tile's codes, on their way, and what is known of its keys.
+  struct Tile {
+    uint4 w[kPasses];
+    uint32_t scale[2];             // this side's scale bytes of keys lane, lane + 32
+    uint32_t other[2];             // key warps: the value side's
+    uint32_t there[2];             // which keys exist
+  };
+  auto start = [&](Tile& tile) {
+    uint64_t from[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool ok = next[h].in && next[h].id >= 0 && next[h].id < a.num_pages;
+      bad_index = bad_index || (next[h].in && !ok);
+      tile.there[h] = __ballot_sync(kFull, ok);
+      const uint32_t id = ok ? next[h].id : 0;
+      from[h] = reinterpret_cast<uint64_t>(at_offset(at_offset(side, id, 2 * a.region), ok ? next[h].row : 0, D));
+      const uint8_t* scales = a.page_scales + static_cast<uint64_t>(id) * (2u * a.num_kv_heads) + head;
+      tile.scale[h] = tile.other[h] = 0;
+      if (ok) {
+        tile.scale[h] = load_global(scales + (kValues ? a.num_kv_heads : 0));
+        if constexpr (!kValues) tile.other[h] = load_global(scales + a.num_kv_heads);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r0 = (me + kWarps * i) * kAtOnce;   // uniform over the warp
+      tile.w[i] = make_uint4(0, 0, 0, 0);
+      if (r0 >= kKeys) continue;
+      const int from_lane = (r0 & 31) + sub;
+      const uint64_t x = r0 < 32 ? from[0] : from[1];
+      const uint64_t row = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(x >> 32), from_lane)) << 32 |
+                           __shfl_sync(kFull, static_cast<uint32_t>(x), from_lane);
+      if (((r0 < 32 ? tile.there[0] : tile.there[1]) >> from_lane) & 1)
+        tile.w[i] = load_global(reinterpret_cast<const uint4*>(row) + c);
+    }
+  };
+  look_up(0);
+  set_up_done();
+  Tile now;
+  start(now);
+  look_up(1);
+  for (int32_t t = 0; t < n_tiles; ++t) {
+    Tile after;
+    start(after);                                   // (of nothing past the last tile)
+    look_up(t + 2);
+    const int st = t % S::kStages;
+    if (t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
+    // the scale bytes as they are read; a key that is not there counts for nothing
+    uint32_t e[2];
+    uint32_t top = 0, top_v = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool ok = (now.there[h] >> lane) & 1;
+      e[h] = ok ? page_scale(now.scale[h]) : 0;
+      top = max(top, e[h]);
+      if constexpr (!kValues) top_v = max(top_v, ok ? page_scale(now.other[h]) : 0);
+    }
+    top = __reduce_max_sync(kFull, top);
+    if constexpr (!kValues) {
+      top_v = __reduce_max_sync(kFull, top_v);
+      // What the softmax has to know of the tile.  A slot's last reader is done:
+      // with the tile kStages before gone from its buffer, the scores of the one
+      // before that, whose weights had to leave theirs two tiles before.
+      static_assert(S::kStages + 4 <= kValidRing, "mask slots");
+      if (me == 0 && lane == 0) {
+        key_ring[2 * (t % kValidRing)] = static_cast<uint64_t>(now.there[1]) << 32 | now.there[0];
+        key_ring[2 * (t % kValidRing) + 1] = static_cast<uint64_t>(top_v) << 32 | top;
+      }
+    }
+    // (2^(e - top) in f16: from 2^-15 on a normal or the largest subnormals)
+    uint32_t factor[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int down = e[h] == 0 ? 0 : static_cast<int>(top - e[h]);
+      factor[h] = down <= 14 ? static_cast<uint32_t>(15 - down) << 10 : down <= 24 ? 0x400u >> (down - 14) : 0u;
+      factor[h] |= factor[h] << 16;
+    }
+    const bool one_scale = __all_sync(kFull, factor[0] == 0x3C003C00u && factor[1] == 0x3C003C00u);
+    const bool hidden = kValues && (s0 + t < full0 || s0 + t >= full1);   // from some row: no NaN may be left
+    const uint32_t to = tiles + st * S::kTileBytes;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r0 = (me + kWarps * i) * kAtOnce;
+      if (r0 >= kKeys) continue;
+      const uint32_t r = r0 + sub;
+      uint32_t w[4] = {now.w[i].x, now.w[i].y, now.w[i].z, now.w[i].w}, h[8];
+      if (hidden) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = finite_codes(w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[2 * j] = bits(e4m3x2_to_half2(w[j]));
+        h[2 * j + 1] = bits(e4m3x2_to_half2(w[j] >> 16));
+      }
+      if (!one_scale) {
+        const uint32_t f = __shfl_sync(kFull, r0 < 32 ? factor[0] : factor[1], (r0 & 31) + sub);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], f);
+      }
+      const uint32_t at = to + (c >> 2) * kKBlock;
+      st_shared16(at + sw128_offset(r, 2 * (c & 3)), make_uint4(h[0], h[1], h[2], h[3]));
+      st_shared16(at + sw128_offset(r, 2 * (c & 3) + 1), make_uint4(h[4], h[5], h[6], h[7]));
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + 8 * st);
+    now = after;
+  }
+  if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
+}
+
+template <int D, int kTiles, bool kFp8>
+__global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
     per_head_prefill_kernel(const PerHeadAttentionArgs a, int32_t row_blocks) {
-  using S = Shape<D, kTiles>;
+  using S = Shape<D, kTiles, kFp8>;
   wait_for_previous();
-  const float k_scale = load_global(a.k_scale);           // in flight beside the request
+  const float k_scale = kFp8 ? 1.0f : load_global(a.k_scale);   // in flight beside the request
   // the last row blocks of a causal chunk, which see the most keys, come first
   const Place place = place_of(a, row_blocks);
   const uint32_t head = place.head;
@@ -359,13 +506,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
   const uint32_t bar = base + S::kMisc;
-  const uint32_t k_full = bar, k_empty = bar + 24, v_full = bar + 48, v_empty = bar + 72;   // [kStages] each
-  const uint32_t s_full = bar + 96, p_full = bar + 128, o_done = bar + 160;                 // [row tile][buffer] each
-  const uint32_t drain = bar + 192, q_full = bar + 208;            // [2], 1
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 216);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 220);
-  uint8_t* valid_ring = smem + S::kMisc + 224;     // [kValidRing][8]: bit per key of the tile
-  static_assert(S::kStages <= 3 && 224 + 8 * kValidRing <= 512, "barrier layout");
+  const uint32_t k_full = bar, k_empty = bar + 32, v_full = bar + 64, v_empty = bar + 96;   // [kStages] each
+  const uint32_t s_full = bar + 128, p_full = bar + 160, o_done = bar + 192;                // [row tile][buffer] each
+  const uint32_t drain = bar + 224, q_full = bar + 240;            // [2], 1
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 248);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 252);
+  // [kValidRing][8]: bit per key of the tile; e4m3: [kValidRing][2]: these, and the tile's scale bytes
+  uint8_t* valid_ring = smem + S::kMisc + 256;
+  uint64_t* key_ring = reinterpret_cast<uint64_t*>(valid_ring);
+  static_assert(S::kStages <= 4 && 256 + 16 * kValidRing <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -475,7 +624,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
-    const float sc = a.scale_log2 * k_scale * rs.i[0] * rs.i[1];   // score -> base-2 exponent
+    const float row_sc = a.scale_log2 * k_scale * rs.i[0] * rs.i[1];   // score -> base-2 exponent
 
     float m = has_row ? -INFINITY : 0.0f, l = 0.0f; // reference maximum, sum
     bool done = true;                               // every wait was met
@@ -494,6 +643,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
     }
     bool fresh = true;                              // some row has no reference yet (uniform over the warp)
+    uint32_t v_ref = 0;                             // e4m3: O counts in units of the scale with this byte (0: none yet)
     for (int32_t t = 0; t < n_tiles; ++t) {
       const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
@@ -506,7 +656,24 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       tmem_ld64(s_col, s);
 
       // which of the tile's keys the row sees
-      const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
+      const uint2 valid = lds64(smem_u32(valid_ring) + (kFp8 ? 16 : 8) * (t % kValidRing));
+      // e4m3: the tile's scales go into its scores, and into its weights relative to
+      // that in whose units O counts, which follows them once they are above it, or
+      // more than 2^6 below (f16 weights keep their precision)
+      float sc = row_sc, shift = 0.0f, back = 1.0f, unit = 1.0f;
+      if constexpr (kFp8) {
+        const uint2 scales = lds64(smem_u32(valid_ring) + 16 * (t % kValidRing) + 8);
+        const uint32_t ek = __shfl_sync(kFull, scales.x, 0), ev = __shfl_sync(kFull, scales.y, 0);
+        sc = row_sc * __uint_as_float((ek == 0 ? 127 : ek) << 23);
+        if (ev != 0) {
+          if (ev > v_ref || ev + 6 < v_ref) {
+            unit = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ev) << 23);
+            v_ref = ev;
+          }
+          shift = static_cast<float>(static_cast<int>(ev - v_ref));
+          back = __uint_as_float((127 + v_ref - ev) << 23);
+        }
+      }
       const bool masked = s0 + t < full0 || s0 + t >= full1 || (valid.x & valid.y) != kFull;
       uint32_t see[2] = {0, 0};
       if (masked && has_row) {
@@ -540,10 +707,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           p[i >> 1] = pack_f16x2(w.x, w.y);
         }
         const float2 both = fadd2(sums[0], sums[1]);
-        sum = both.x + both.y;
+        sum = kFp8 ? (both.x + both.y) * back : both.x + both.y;
       };
       auto weights = [&]() {                        // warp-uniform choice
-        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float off = kShift - (m == -INFINITY ? 0.0f : m) + shift;
         if (masked)
           pass(off, std::true_type{});
         else
@@ -552,21 +719,25 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
       // sum is takes a new reference, its tile's maximum (as in its first tile).
       if (!fresh) weights();
-      if (fresh || __any_sync(kFull, sum > kMaxWeight)) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const float z = __uint_as_float(s[i]) * sc;
-          if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
-        }
+      const bool grow = fresh || __any_sync(kFull, sum > kMaxWeight);
+      if (grow || (kFp8 && unit != 1.0f)) {
         float alpha = 1.0f;
-        if (top > m) {
-          alpha = ex2(m - top);                     // 0 while m is -inf
-          m = top;
+        if (grow) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const float z = __uint_as_float(s[i]) * sc;
+            if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
+          }
+          if (top > m) {
+            alpha = ex2(m - top);                   // 0 while m is -inf
+            m = top;
+          }
+          fresh = __any_sync(kFull, m == -INFINITY);
+          weights();
+          l *= alpha;
         }
-        fresh = __any_sync(kFull, m == -INFINITY);
-        weights();
-        l *= alpha;
+        alpha *= unit;
         if (t > 0) {
           // O is rescaled once the product of the tile before is done.  (The
           // barrier is waited on only here: the scores of tile t - 1 followed
@@ -594,7 +765,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
-    const float v_scale = load_global(a.v_scale);
+    const float v_scale = kFp8 ? __uint_as_float(v_ref << 23) : load_global(a.v_scale);
     // the last product is done: O is complete
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
@@ -607,7 +778,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       // to a piece, through the shared memory of the warp's query rows, which
       // no product reads any more (each lane storing its own row touches 32
       // lines at a time: 2.2 us a CTA).
-      const float f = a.num_splits > 1 ? inv : inv * v_scale;
+      const float f = a.num_splits > 1 && !kFp8 ? inv : inv * v_scale;
       const uint32_t stage = bar - S::kMisc + tile * S::kQTile + (lanes >> 9);     // 32 rows of 128 bytes a warp
       const uint64_t mine =
           row >= rows ? 0
@@ -687,8 +858,24 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       }
       __syncwarp();
     };
-    if (warp < S::kScoreWarp) {
-      produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
+    // e4m3: steps [full0, full1) of the keys are visible whole to every row of the block
+    int32_t full0 = 0, full1 = 0;
+    if constexpr (kFp8) {
+      const int64_t lo = a.window > 0 ? max(int64_t{0}, rq.first_pos + t1 - a.window + 1) : 0;
+      const int32_t whole =
+          static_cast<int32_t>(min(rq.first_pos + t0, static_cast<int64_t>(keys.hi) - 1)) + 1 - keys.lo;
+      full0 = keys.sink_steps + static_cast<int32_t>((max(lo - keys.lo, int64_t{0}) + kKeys - 1) / kKeys);
+      full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
+    }
+    if (kFp8 && warp < S::kScoreWarp) {
+      produce_fp8<D, kTiles, false>(a, b, head, keys, s0, n_tiles, full0, full1, warp - S::kSoftmaxWarps, lane,
+                                    rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, key_ring,
+                                    s_abort);
+    } else if (kFp8 && warp > S::kScoreWarp && warp < S::kOutputWarp) {
+      produce_fp8<D, kTiles, true>(a, b, head, keys, s0, n_tiles, full0, full1, warp - S::kScoreWarp - 1, lane, false, base,
+                                   v_full, v_empty, key_ring, s_abort);
+    } else if (warp < S::kScoreWarp) {
+      if constexpr (!kFp8) produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
                                 rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty,
                                 valid_ring, s_abort);
     } else if (warp == S::kScoreWarp) {
@@ -722,7 +909,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       }
       drained(elected, drain);
     } else if (warp < S::kOutputWarp) {
-      produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
+      if constexpr (!kFp8) produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
                                v_empty, valid_ring, s_abort);
     } else {
       // ---- O_w += P_w(t) V(t) ---------------------------------------------------
@@ -766,28 +953,33 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   }
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kFp8>
 cudaError_t launch(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  using S = Shape<D, kTiles>;
-  const cudaError_t e = cudaFuncSetAttribute(per_head_prefill_kernel<D, kTiles>,
+  using S = Shape<D, kTiles, kFp8>;
+  const cudaError_t e = cudaFuncSetAttribute(per_head_prefill_kernel<D, kTiles, kFp8>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (static_cast<int64_t>(a.max_query_len) * a.group + 128 * kTiles - 1) / (128 * kTiles);
   const dim3 grid(static_cast<unsigned>(blocks * a.num_kv_heads * a.num_splits), static_cast<unsigned>(a.batch_size));
-  return launch_dependent(per_head_prefill_kernel<D, kTiles>, grid, S::kThreads, S::kSmem, 1, stream, a,
+  return launch_dependent(per_head_prefill_kernel<D, kTiles, kFp8>, grid, S::kThreads, S::kSmem, 1, stream, a,
                           static_cast<int32_t>(blocks));
+}
+
+template <bool kFp8>
+cudaError_t launch_size(const PerHeadAttentionArgs& a, cudaStream_t stream) {
+  // two row tiles share a decoded key tile wherever a request can fill them
+  const bool two = per_head_prefill_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size) == 256;
+  switch (a.head_size) {
+    case 64: return two ? launch<64, 2, kFp8>(a, stream) : launch<64, 1, kFp8>(a, stream);
+    case 128: return two ? launch<128, 2, kFp8>(a, stream) : launch<128, 1, kFp8>(a, stream);
+    default: return launch<256, 1, kFp8>(a, stream);       // one tile's O fills the tensor memory
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_per_head_prefill(const PerHeadAttentionArgs& a, cudaStream_t stream) {
-  // two row tiles share a decoded key tile wherever a request can fill them
-  const bool two = per_head_prefill_rows(static_cast<int64_t>(a.max_query_len) * a.group, a.head_size) == 256;
-  switch (a.head_size) {
-    case 64: return two ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
-    case 128: return two ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
-    default: return launch<256, 1>(a, stream);       // one tile's O fills the tensor memory
-  }
+  return a.page_scales != nullptr ? launch_size<true>(a, stream) : launch_size<false>(a, stream);
 }
 
 }  // namespace kvq
