@@ -16,13 +16,16 @@
 // magnitude, and the scale only has to keep the largest value in range.
 //
 // Bound: HBM (keys and values read once and written as one byte each, queries
-// read and written).  One warp per (page, side, head): it goes over the page's
-// new tokens twice, for the largest magnitude and, out of the cache by then,
-// for the codes, and nothing but its own lanes has to be waited for.  D / 8
-// lanes hold a token's head, 8 values (16 bytes) each; a pair's other half,
-// rot/16 lanes on, comes by shuffles of the raw bf16 values.  The queries are
-// other warps' work in the same launch: up to 8 heads of a token per lane
-// group, which share the token's row of the table.
+// read and written).  One warp, or four or eight, per (page, side, head), as
+// many as keep the page's new tokens in registers between the largest magnitude
+// and the codes (a page of more is read twice).  D / 8 lanes hold a token's
+// head, 8 values (16 bytes) each, eight tokens a lane, whose loads are all
+// under way at once; a pair's other half, rot/16 lanes on, comes by shuffles of
+// the raw bf16 values.  The queries are other CTAs' work in the same launch: up
+// to 8 heads of a token per lane group, which share the token's row of the
+// table.
+#include <algorithm>
+
 #include "kvq_dependent.cuh"
 #include "kvq_device.cuh"
 #include "kvq_launch.h"
@@ -30,9 +33,9 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 constexpr int kManyHeads = 8;                // query heads per lane group of a call that fills the GPU
+
+__host__ __device__ constexpr int threads_of(int warps) { return warps == 8 ? 256 : 128; }
 
 // 8 values as fp32 pairs.
 struct Values {
@@ -148,11 +151,13 @@ __device__ __forceinline__ uint32_t recode(uint32_t w, float f) {
   return e4m3x4(lo, hi, f);
 }
 
-// One warp: the new entries of one page, side and head.
-template <int kLanes, bool kInterleaved>
+// kWarps warps (of number `warp`, all of a CTA, or one): the new entries of one
+// page, side and head; a lane keeps kHeld tokens' between the two looks at them.
+template <int kLanes, int kWarps, int kHeld, bool kInterleaved>
 __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t token0, int32_t n, int32_t len,
-                                            uint32_t unit, int lane) {
-  constexpr int kTokens = 32 / kLanes;               // at a time
+                                            uint32_t unit, int warp, int lane) {
+  constexpr int kTokens = 32 / kLanes;               // of a warp at a time
+  constexpr int kAtOnce = kTokens * kWarps, kChunk = kAtOnce * kHeld;
   constexpr int D = 8 * kLanes;
   const uint32_t side_heads = 2u * a.num_kv_heads;
   const uint32_t ordinal = unit / side_heads, sh = unit - ordinal * side_heads;
@@ -166,81 +171,106 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
   const int32_t p1 = static_cast<int32_t>(min(base + a.block_size, static_cast<int64_t>(len)));
   int32_t id = -1;
   if (col < static_cast<uint32_t>(a.block_table_width)) id = load_global(a.block_table + b * a.block_table_stride + col);
-  const bool there = id >= 0 && id < a.num_pages;
-  if (!there && lane == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
 
-  const int li = lane % kLanes, sub = lane / kLanes;
+  const int li = lane % kLanes, sub = warp * kTokens + lane / kLanes;
   const Place<kInterleaved> at(li, a.rot_dim);
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) +
                              head * (is_v ? a.v_stride_h : a.k_stride_h) + 8 * li;
   const int64_t stride = is_v ? a.v_stride_t : a.k_stride_t;
-  // the values of the token at position p (any of the group's, past the last one too)
-  auto value = [&](int32_t p, bool& live, int64_t& token) {
-    token = token0 + (p - first);
-    live = p < p1;
-    int64_t pos = 0;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) {
-      raw = load_global(reinterpret_cast<const uint4*>(src + token * stride));
-      pos = load_global(a.positions + token);
-      live = pos >= 0 && pos < a.max_position;       // else skipped
-      if (!live && li == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
+  // The lane's values of the tokens at positions p + sub, kAtOnce on, ..., every
+  // load under way before the first is used; bit j of `live`: there is one, and
+  // its rotation position is in the table.
+  Values y[kHeld];
+  uint32_t live;
+  auto values = [&](int32_t p) {
+    uint4 raw[kHeld];
+    int64_t pos[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int32_t q = p + sub + kAtOnce * j;
+      raw[j] = make_uint4(0, 0, 0, 0);
+      pos[j] = -1;
+      if (q < p1) {
+        const int64_t token = token0 + (q - first);
+        raw[j] = load_global(reinterpret_cast<const uint4*>(src + token * stride));
+        pos[j] = load_global(a.positions + token);
+      }
     }
-    if (is_v) return unpack8(raw);
-    Turn t{};
-    if (live && at.rotated) t = load_turn<kInterleaved>(a, at, li, pos);
-    return rotate<kLanes, kInterleaved>(raw, at, t);
+    live = 0;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const bool ok = pos[j] >= 0 && pos[j] < a.max_position;
+      if (!ok && li == 0 && p + sub + kAtOnce * j < p1) report(a.status, KVQ_STATUS_BAD_INDEX);
+      live |= ok ? 1u << j : 0u;
+      if (is_v) {
+        y[j] = unpack8(raw[j]);
+      } else {
+        Turn t{};
+        if (ok && at.rotated) t = load_turn<kInterleaved>(a, at, li, pos[j]);
+        y[j] = rotate<kLanes, kInterleaved>(raw[j], at, t);
+      }
+    }
   };
 
   const int32_t held = static_cast<int32_t>(p0 - base);          // entries that stay
-  uint8_t* scale = a.scales + (static_cast<int64_t>(max(id, 0)) * side_heads + sh);
-  uint8_t* region = a.cache + (2 * static_cast<uint64_t>(max(id, 0)) + is_v) * a.region;
-  int e = 0;
-  if (there) {
-    float amax = 0.0f;
-    for (int32_t p = p0; p < p1; p += kTokens) {
-      bool live;
-      int64_t token;
-      const Values y = value(p + sub, live, token);
+  float amax = 0.0f;
+  for (int32_t p = p0; p < p1; p += kChunk) {
+    values(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (live) amax = fmaxf(amax, fmaxf(fabsf(y.v[i].x), fabsf(y.v[i].y)));
-    }
+    for (int j = 0; j < kHeld; ++j)
+      if ((live >> j) & 1) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    e = scale_exponent(amax);
-    if (held > 0) {
-      const int old = stored_exponent(load_global(scale));
-      e = max(e, old);
-      if (e > old) {
-        const float f = power_of_two(old - e);
-        constexpr int kChunks = D / 16;
-        for (int i = lane; i < held * kChunks; i += 32) {
-          const uint32_t row = static_cast<uint32_t>(i / kChunks) * a.row_offset + head * a.row_head;
-          uint4* w = reinterpret_cast<uint4*>(region + static_cast<uint64_t>(row) * D) + i % kChunks;
-          const uint4 x = *w;
-          *w = make_uint4(recode(x.x, f), recode(x.y, f), recode(x.z, f), recode(x.w, f));
-        }
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(y[j].v[i].x), fabsf(y[j].v[i].y)));
       }
-      __syncwarp();                                  // the scale has been read by every lane
+  }
+  const bool there = id >= 0 && id < a.num_pages;
+  if (!there && warp == 0 && lane == 0) report(a.status, KVQ_STATUS_BAD_INDEX);
+  uint8_t* scale = a.scales + (static_cast<int64_t>(there ? id : 0) * side_heads + sh);
+  uint8_t* region = a.cache + (2 * static_cast<uint64_t>(there ? id : 0) + is_v) * a.region;
+  const int old = there && held > 0 ? stored_exponent(load_global(scale)) : KVQ_FP8_SCALE_MIN_EXP;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  if constexpr (kWarps > 1) {
+    __shared__ float most[kWarps];
+    if (lane == 0) most[warp] = amax;
+    __syncthreads();                                 // (and every warp has read the scale)
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, most[w]);
+  }
+  __syncwarp();
+  const int e = max(scale_exponent(amax), old);
+  if (there) {
+    if (held > 0 && e > old) {
+      const float f = power_of_two(old - e);
+      constexpr int kChunks = D / 16;
+      for (int i = warp * 32 + lane; i < held * kChunks; i += 32 * kWarps) {
+        const uint32_t row = static_cast<uint32_t>(i / kChunks) * a.row_offset + head * a.row_head;
+        uint4* w = reinterpret_cast<uint4*>(region + static_cast<uint64_t>(row) * D) + i % kChunks;
+        const uint4 x = *w;
+        *w = make_uint4(recode(x.x, f), recode(x.y, f), recode(x.z, f), recode(x.w, f));
+      }
     }
-    if (lane == 0) *scale = static_cast<uint8_t>(e + KVQ_FP8_SCALE_BIAS);
+    if (warp == 0 && lane == 0) *scale = static_cast<uint8_t>(e + KVQ_FP8_SCALE_BIAS);
   }
   const bool keep = !is_v && a.k_out != nullptr;
   if (!there && !keep) return;
   const float f = power_of_two(-e);
-  for (int32_t p = p0; p < p1; p += kTokens) {
-    bool live;
-    int64_t token;
-    const Values y = value(p + sub, live, token);
-    if (!live) continue;                             // (no shuffle after this in the iteration)
-    if (there) {
-      const uint32_t row = static_cast<uint32_t>(p + sub - base) * a.row_offset + head * a.row_head;
-      st8(region + static_cast<uint64_t>(row) * D + 8 * li,
-          make_uint2(e4m3x4(y.v[0], y.v[1], f), e4m3x4(y.v[2], y.v[3], f)));
+  const bool again = p1 - p0 > kChunk;               // more tokens than are held
+  for (int32_t p = p0; p < p1; p += kChunk) {
+    if (again) values(p);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (!((live >> j) & 1)) continue;
+      const int32_t q = p + sub + kAtOnce * j;
+      if (there) {
+        const uint32_t row = static_cast<uint32_t>(q - base) * a.row_offset + head * a.row_head;
+        st8(region + static_cast<uint64_t>(row) * D + 8 * li,
+            make_uint2(e4m3x4(y[j].v[0], y[j].v[1], f), e4m3x4(y[j].v[2], y[j].v[3], f)));
+      }
+      if (keep)
+        st16(static_cast<__nv_bfloat16*>(a.k_out) + (token0 + (q - first)) * a.k_out_stride_t + head * a.k_out_stride_h +
+                 8 * li, pack8(y[j]));
     }
-    if (keep)
-      st16(static_cast<__nv_bfloat16*>(a.k_out) + token * a.k_out_stride_t + head * a.k_out_stride_h + 8 * li, pack8(y));
   }
 }
 
@@ -275,10 +305,12 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int64_t toke
   }
 }
 
-template <int kLanes, int kHeads, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, uint32_t page_ctas, uint32_t units) {
+// kWarps: warps of a page, side and head.
+template <int kLanes, int kWarps, int kHeld, int kHeads, bool kInterleaved>
+__global__ void __launch_bounds__(threads_of(kWarps), kWarps == 8 ? 3 : 6) append_kernel(const AppendArgs a, uint32_t page_ctas, uint32_t units) {
   wait_for_previous();
   allow_dependents();
+  constexpr int kThreads = threads_of(kWarps);
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t q0 = load_global(a.query_start + b), q1 = load_global(a.query_start + b + 1);
   const int32_t len = max(0, load_global(a.seq_lens + b));
@@ -289,41 +321,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, ui
   }
   if (n == 0) return;
   if (blockIdx.x < page_ctas) {
-    const uint32_t unit = blockIdx.x * kWarps + warp;
-    if (unit < units) append_page<kLanes, kInterleaved>(a, b, q0, static_cast<int32_t>(n), len, unit, lane);
+    const uint32_t unit = kWarps == 1 ? blockIdx.x * (kThreads / 32) + warp : blockIdx.x;
+    if (unit < units)
+      append_page<kLanes, kWarps, kHeld, kInterleaved>(a, b, q0, static_cast<int32_t>(n), len, unit, kWarps == 1 ? 0 : warp, lane);
   } else {
     rotate_queries<kLanes, kHeads, kInterleaved>(a, q0, static_cast<int32_t>(n),
                                                  static_cast<uint64_t>(blockIdx.x - page_ctas) * kThreads + threadIdx.x);
   }
 }
 
-template <int kLanes, int kHeads>
+template <int kLanes, int kWarps, int kHeld, int kHeads>
 cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int kThreads = threads_of(kWarps), kUnits = kThreads / (32 * kWarps);
   const int64_t pages = (static_cast<int64_t>(a.max_query_len) + a.block_size - 2) / a.block_size + 1;
-  const int64_t units = pages * 2 * a.num_kv_heads, page_ctas = (units + kWarps - 1) / kWarps;
+  const int64_t units = pages * 2 * a.num_kv_heads, page_ctas = (units + kUnits - 1) / kUnits;
   const int64_t chunks = (a.num_heads + kHeads - 1) / kHeads;
   const int64_t query_ctas =
       a.q == nullptr ? 0 : (static_cast<int64_t>(a.max_query_len) * chunks * kLanes + kThreads - 1) / kThreads;
   const dim3 grid(static_cast<unsigned>(page_ctas + query_ctas), static_cast<unsigned>(a.batch_size));
-  return launch_dependent(a.interleaved ? append_kernel<kLanes, kHeads, true> : append_kernel<kLanes, kHeads, false>, grid,
-                          kThreads, 0, 1, stream, a, static_cast<uint32_t>(page_ctas), static_cast<uint32_t>(units));
+  return launch_dependent(
+      a.interleaved ? append_kernel<kLanes, kWarps, kHeld, kHeads, true>
+                    : append_kernel<kLanes, kWarps, kHeld, kHeads, false>,
+      grid, kThreads, 0, 1, stream, a, static_cast<uint32_t>(page_ctas), static_cast<uint32_t>(units));
 }
 
 template <int kLanes>
-cudaError_t launch_heads(const AppendArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_size(const AppendArgs& a, int num_sms, cudaStream_t stream) {
+  // as many warps as hold a page's new tokens between the two looks at them
+  const int64_t tokens = std::min<int64_t>(a.max_query_len, a.block_size);
+  constexpr int kAtOnce = 32 / kLanes;
   const int64_t chunks = (a.num_heads + kManyHeads - 1) / kManyHeads;
-  return a.num_tokens * chunks * kLanes >= static_cast<int64_t>(num_sms) * kThreads
-             ? launch<kLanes, kManyHeads>(a, stream)
-             : launch<kLanes, 1>(a, stream);
+  const bool many = a.num_tokens * chunks * kLanes >= static_cast<int64_t>(num_sms) * 128;
+  if (tokens <= kAtOnce) return many ? launch<kLanes, 1, 1, kManyHeads>(a, stream) : launch<kLanes, 1, 1, 1>(a, stream);
+  if (tokens <= 4 * kAtOnce) return many ? launch<kLanes, 1, 4, kManyHeads>(a, stream) : launch<kLanes, 1, 4, 1>(a, stream);
+  if (tokens <= 16 * kAtOnce) return many ? launch<kLanes, 4, 4, kManyHeads>(a, stream) : launch<kLanes, 4, 4, 1>(a, stream);
+  return launch<kLanes, 8, 4, kManyHeads>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const AppendArgs& a, int num_sms, cudaStream_t stream) {
   switch (a.head_size) {
-    case 64: return launch_heads<8>(a, num_sms, stream);
-    case 128: return launch_heads<16>(a, num_sms, stream);
-    default: return launch_heads<32>(a, num_sms, stream);
+    case 64: return launch_size<8>(a, num_sms, stream);
+    case 128: return launch_size<16>(a, num_sms, stream);
+    default: return launch_size<32>(a, num_sms, stream);
   }
 }
 
