@@ -73,7 +73,7 @@ struct Stage {
   static constexpr int kV = kStep * kRow, kKs = 2 * kStep * kRow, kVs = kKs + kStep * kScales;
   static constexpr int kBytes = kVs + kStep * kScales;
   static constexpr int ctas(int row_tiles) {                     // per SM
-    return kFp8 ? (D == 64 ? (row_tiles == 2 ? 3 : 4) : 3) : D == 256 ? 2 : row_tiles == 2 ? 3 : 4;
+    return kFp8 ? (D == 64 ? 4 : 3) : D == 256 ? 2 : row_tiles == 2 ? 3 : 4;
   }
 };
 
@@ -837,12 +837,18 @@ cudaError_t launch_join(const PerHeadAttentionArgs& a, cudaStream_t stream) {
                           kJoinWarps * 32, 0, 1, stream, a);
 }
 
-template <bool kFp8>
 cudaError_t launch_few_rows(const PerHeadAttentionArgs& a, int64_t block, cudaStream_t stream) {
   switch (a.head_size) {
-    case 64: return block == 8 ? launch_rows<64, 1, kFp8>(a, stream) : launch_rows<64, 2, kFp8>(a, stream);
-    case 128: return block == 8 ? launch_rows<128, 1, kFp8>(a, stream) : launch_rows<128, 2, kFp8>(a, stream);
-    default: return launch_rows<256, 1, kFp8>(a, stream);
+    case 64: return block == 8 ? launch_rows<64, 1, false>(a, stream) : launch_rows<64, 2, false>(a, stream);
+    case 128: return block == 8 ? launch_rows<128, 1, false>(a, stream) : launch_rows<128, 2, false>(a, stream);
+    default: return launch_rows<256, 1, false>(a, stream);
+  }
+}
+cudaError_t launch_few_rows_fp8(const PerHeadAttentionArgs& a, cudaStream_t stream) {
+  switch (a.head_size) {
+    case 64: return launch_rows<64, 1, true>(a, stream);
+    case 128: return launch_rows<128, 1, true>(a, stream);
+    default: return launch_rows<256, 1, true>(a, stream);
   }
 }
 
@@ -854,8 +860,8 @@ cudaError_t launch_per_head_attention(const PerHeadAttentionArgs& a, int sms, cu
                                        static_cast<int64_t>(a.num_kv_heads) * a.batch_size, a.head_size, a.num_splits,
                                        a.cluster, sms, fp8);
   const cudaError_t e = block > 16 ? launch_per_head_prefill(a, stream)
-                        : fp8      ? launch_few_rows<true>(a, block, stream)
-                                   : launch_few_rows<false>(a, block, stream);
+                        : fp8      ? launch_few_rows_fp8(a, stream)
+                                   : launch_few_rows(a, block, stream);
   if (e != cudaSuccess || a.num_splits == 1 || a.cluster) return e;
   return a.head_size == 64 ? launch_join<64>(a, stream)
                            : a.head_size == 128 ? launch_join<128>(a, stream) : launch_join<256>(a, stream);

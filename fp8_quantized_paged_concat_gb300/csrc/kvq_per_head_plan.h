@@ -13,7 +13,7 @@ namespace kvq {
 
 // CTAs of the few-row kernel that share an SM (its launch bounds).
 constexpr int64_t resident_ctas(int32_t head_size, int64_t block, bool fp8 = false) {
-  return fp8 ? (head_size == 64 && block != 16 ? 4 : 3) : head_size == 256 ? 2 : block == 16 ? 3 : 4;
+  return fp8 ? (head_size == 64 ? 4 : 3) : head_size == 256 ? 2 : block == 16 ? 3 : 4;
 }
 
 // Rows per block of the few-row kernel.  16 rows share a decoded key where
@@ -22,9 +22,12 @@ constexpr int64_t resident_ctas(int32_t head_size, int64_t block, bool fp8 = fal
 // against 220); a smaller call is short of CTAs, and blocks of 8 halve its
 // chain (one request x 1024 keys, 16 rows: 6.9 us against 8.8; with long
 // contexts, whose ranges are many, blocks of 16 would be as good: 16384 keys
-// 16.9 against 15.7).  D = 256 has no registers for 16.
+// 16.9 against 15.7).  D = 256 has no registers for 16, and over the e4m3 cache,
+// whose entries are decoded in fewer instructions, blocks of 8 are as fast or
+// faster (16 rows, head size 128: 128 requests x 2000 keys 136 us against 149, 32
+// x 5000 keys 95 against 102; 32 rows, 128 x 1000 keys 146 against 143).
 inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, int sms, bool fp8 = false) {
-  return rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16, fp8) * int64_t{sms}
+  return !fp8 && rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16, fp8) * int64_t{sms}
              ? 16 : 8;
 }
 
@@ -115,7 +118,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
     const auto ranges = [&](int64_t per_place) {
       return whole(std::min<int64_t>(keys / 1024, (per_place * places() + blocks() - 1) / blocks()));
     };
-    if (few && rows > 8 && head_size != 256) {
+    if (few && !fp8 && rows > 8 && head_size != 256) {
       block = 16;
       n = ranges(4);
       if (few_rows(rows, groups, head_size, n, sms, fp8) != 16) block = 8;
@@ -124,6 +127,12 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
       const bool many = blocks() >= places();
       n = ranges(few ? (many ? 2 : 6) : (many ? 6 : 3));
     }
+  } else if (fp8 && few && keys >= 1024 && blocks() >= places() && blocks() < 3 * places()) {
+    // The last of few waves of CTAs leaves much of the GPU idle: half as long ones
+    // do less so (128 requests x window 4096, 1024 blocks on 456 places: 189 us
+    // against 201; 64 requests of 1000 to 3000 keys, 512 blocks: 56 against 62; 128
+    // requests x 16 rows x 2000 keys, 2048 blocks: 157 against 136).
+    n = whole(2);
   } else {
     // As many as the call is short of CTAs, of at least 256 keys in the tensor
     // memory kernel.  In the few-row kernel a range costs keys / n steps and the
