@@ -36,7 +36,7 @@ __all__ = [
     "kvq_per_head_attention_default_splits",
     "PER_HEAD_MAX_SPLITS", "PER_HEAD_CLUSTER_SPLITS",
     "kvq_rope_append_fp8_per_head", "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits",
-    "FP8_SCALE_BIAS", "kvq_prompt_attention",
+    "kvq_fp8_attention_workspace_bytes", "FP8_SCALE_BIAS", "kvq_prompt_attention",
     "kvq_last_error_string", "kvq_version", "library_path", "load_library",
     "NVFP4_DS_MLA_ENTRY_BYTES", "FP8_DS_MLA_ENTRY_BYTES", "STATUS_BAD_INDEX", "STATUS_BAD_BATCH",
     "STATUS_TIMEOUT",
@@ -120,6 +120,7 @@ _SIGNATURES = {
                                           _I32, _I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64,
                                           _I32, _I32, _P, _I64, _P, _P],
     "kvq_fp8_attention_default_splits": [_I32] * 8 + [_P],
+    "kvq_fp8_attention_workspace_bytes": [_I64] + [_I32] * 9,
     "kvq_prompt_attention": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32,
                              ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P],
     "kvq_compact_drafts_nvfp4_per_head": [_P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _P,
@@ -152,6 +153,7 @@ def load_library():
         handle.kvq_sparse_mla_attention_split_workspace_bytes.argtypes = [_I64, _I32, _I32]
         handle.kvq_per_head_attention_workspace_bytes.restype = _I64
         handle.kvq_per_head_attention_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32]
+        handle.kvq_fp8_attention_workspace_bytes.restype = _I64
         handle.kvq_per_head_attention_default_splits.restype = _I32
         handle.kvq_per_head_attention_default_splits.argtypes = [_I32] * 9 + [_P]
         _lib = handle
@@ -601,7 +603,7 @@ _native = None
 _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
                    "kvq_compact_drafts_nvfp4_per_head", "kvq_rope_append_fp8_per_head",
                    "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits", "kvq_prompt_attention",
-                   "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
+                   "kvq_fp8_attention_workspace_bytes", "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
 
 
 def _load_native():
@@ -728,12 +730,22 @@ def kvq_rope_append_fp8_per_head(q, k, v, positions, cos_sin, query_start, seq_l
 
 def kvq_fp8_attention_default_splits(max_query_len: int, num_heads: int, num_kv_heads: int, head_size: int,
                                      batch_size: int, max_seq_len: int, window: int = 0, num_sinks: int = 0) -> tuple:
-    """kvq_per_head_attention_default_splits for the per-head e4m3 cache."""
+    """kvq_per_head_attention_default_splits for the per-head e4m3 cache; (1,
+    True): a call that had better gather its entries into a workspace."""
     use_workspace = _I32(0)
     splits = load_library().kvq_fp8_attention_default_splits(
         max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks,
         ctypes.byref(use_workspace))
     return splits, bool(use_workspace.value)
+
+
+def kvq_fp8_attention_workspace_bytes(num_tokens: int, num_heads: int, num_kv_heads: int, head_size: int, batch_size: int,
+                                      max_query_len: int, max_seq_len: int, window: int = 0, num_sinks: int = 0,
+                                      num_splits: int = 1) -> int:
+    """Bytes of workspace that a call of kvq_window_attention_fp8_per_head of
+    these sizes can use (-1 for bad arguments)."""
+    return load_library().kvq_fp8_attention_workspace_bytes(num_tokens, num_heads, num_kv_heads, head_size, batch_size,
+                                                            max_query_len, max_seq_len, window, num_sinks, num_splits)
 
 
 def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_cache, kv_scales, softmax_scale: float,
@@ -744,8 +756,12 @@ def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_
     as kvq_rope_append_fp8_per_head fills them) with a sliding window (window
     <= 0: none) and num_sinks first tokens that stay visible; everything else
     as in kvq_window_attention_nvfp4_per_head, num_splits from
-    kvq_fp8_attention_default_splits.  Returns (out bf16 [T, H, D], lse fp32
-    [T, H]); lse=False skips the lse output."""
+    kvq_fp8_attention_default_splits.  A call of many query rows with
+    num_splits = 1 and a workspace gathers the entries it needs there, as many
+    requests at a time as it holds (kvq_fp8_attention_workspace_bytes; by
+    default up to 1 GiB is allocated, or one request's); max_seq_len then has
+    to hold.  Returns (out bf16 [T, H, D], lse fp32 [T, H]); lse=False skips
+    the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, kv_scales, False,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)

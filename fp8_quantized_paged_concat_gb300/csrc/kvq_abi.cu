@@ -815,6 +815,21 @@ kvq_status check_table(const char* fn, const int32_t* query_start, const int32_t
   return KVQ_OK;
 }
 
+// What the attention over whole prompts needs of a call's heads.
+kvq::PromptAttentionArgs prompt_args(int32_t num_heads, int32_t num_kv_heads, int32_t head_size) {
+  kvq::PromptAttentionArgs a{};
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_size = head_size;
+  a.group = num_heads / num_kv_heads;
+  a.group_div = kvq::FastDiv::make(static_cast<uint32_t>(a.group));
+  a.kv_heads_div = kvq::FastDiv::make(static_cast<uint32_t>(num_kv_heads));
+  a.tile_tokens = std::max(1, 128 / a.group);
+  a.chunks = (a.group + 127) / 128;
+  a.chunk_div = kvq::FastDiv::make(static_cast<uint32_t>(a.chunks));
+  return a;
+}
+
 struct TreeMask {
   const uint64_t* mask = nullptr;
   int64_t stride = 0;
@@ -886,8 +901,79 @@ kvq_status per_head_attention(
                 "%s: workspace must be non-NULL, 16-byte aligned and at least %lld bytes (got %lld)", fn,
                 static_cast<long long>(need), static_cast<long long>(workspace_bytes));
   }
+  const bool gathers =
+      fp8 && num_splits == 1 && workspace != nullptr && int64_t{max_query_len} * group > kvq::most_few_rows(head_size, true);
+  const int64_t gather_rows = kvq::fp8_gather_rows(max_query_len, max_seq_len, window, num_sinks);
+  if (gathers) {
+    const int64_t need = kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, 1);
+    KVQ_REQUIRE(aligned(workspace, 16) && workspace_bytes >= need,
+                "%s: workspace must be 16-byte aligned and at least %lld bytes (got %lld)", fn,
+                static_cast<long long>(need), static_cast<long long>(workspace_bytes));
+    KVQ_REQUIRE(gather_rows < (int64_t{1} << 31) - 256 && q_stride_t > 0 && q_stride_t < (int64_t{1} << 38) &&
+                    q_stride_h < (int64_t{1} << 38),
+                "%s: with a workspace, q strides must be positive and below 2^38, max_seq_len below 2^31 - 256", fn);
+  }
   int num_sms = 0;
   if (kvq_status s = check_device(fn, &num_sms)) return s;
+  if (gathers) {
+    // as many requests at a time as the workspace holds
+    int64_t most = std::min<int64_t>({batch_size, workspace_bytes / kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, 1),
+                                      ((int64_t{1} << 31) - 256) / gather_rows});
+    while (most > 1 && kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, most) > workspace_bytes) --most;
+    for (int64_t b = 0; b < batch_size; b += most) {
+      const int32_t n = static_cast<int32_t>(std::min<int64_t>(most, batch_size - b));
+      const int64_t side = n * gather_rows * num_kv_heads * head_size;
+      kvq::Fp8GatherArgs g{};
+      g.k = workspace;
+      g.v = static_cast<uint16_t*>(workspace) + side;
+      g.there = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(workspace) + 2 * side);
+      g.cached = {seq_lens + b, block_table_width * block_size, static_cast<int32_t>(gather_rows), g.there};
+      g.query_start = query_start + b;
+      g.num_tokens = num_tokens;
+      g.batch_size = n;
+      g.max_query_len = max_query_len;
+      g.window = window;
+      g.num_sinks = num_sinks;
+      g.block_table = block_table + b * block_table_stride;
+      g.block_table_stride = block_table_stride;
+      g.cache = kv_cache;
+      g.page_scales = page_scales;
+      g.num_pages = num_pages;
+      g.block_size = block_size;
+      g.block_div = kvq::FastDiv::make(static_cast<uint32_t>(block_size));
+      g.region = static_cast<uint32_t>(region);
+      g.row_offset = layout == KVQ_LAYOUT_HND ? 1 : num_kv_heads;
+      g.row_head = layout == KVQ_LAYOUT_HND ? block_size : 1;
+      g.num_kv_heads = num_kv_heads;
+      g.head_size = head_size;
+      g.status = d_status;
+      if (kvq_status s = launched(fn, kvq::launch_fp8_gather(g, reinterpret_cast<cudaStream_t>(stream)))) return s;
+      kvq::PromptAttentionArgs p = prompt_args(num_heads, num_kv_heads, head_size);
+      p.q = q;
+      p.q_stride_t = q_stride_t;
+      p.q_stride_h = q_stride_h;
+      p.k = g.k;
+      p.v = g.v;
+      p.k_stride_t = p.v_stride_t = int64_t{num_kv_heads} * head_size;
+      p.k_stride_h = p.v_stride_h = head_size;
+      p.num_tokens = num_tokens;
+      p.seq_start = query_start + b;
+      p.batch_size = n;
+      p.max_seq_len = max_query_len;
+      p.scale_log2 = static_cast<float>(scale_log2);
+      p.window = window;
+      p.num_sinks = num_sinks;
+      p.out = out;
+      p.out_stride_t = out_stride_t;
+      p.out_stride_h = out_stride_h;
+      p.lse = lse;
+      p.lse_stride_t = lse_stride_t;
+      p.status = d_status;
+      p.cached = g.cached;
+      if (kvq_status s = launched(fn, kvq::launch_prompt_attention(p, reinterpret_cast<cudaStream_t>(stream)))) return s;
+    }
+    return ok();
+  }
   kvq::PerHeadAttentionArgs a{};
   a.q = q;
   a.q_stride_t = q_stride_t;
@@ -1017,6 +1103,19 @@ kvq_status kvq_window_attention_fp8_per_head(
                             block_size, layout, num_kv_heads, head_size, nullptr, nullptr, kv_scales, softmax_scale,
                             window, num_sinks, nullptr, out, out_stride_t, out_stride_h, lse, lse_stride_t, max_seq_len,
                             num_splits, workspace, workspace_bytes, d_status, stream);
+}
+
+int64_t kvq_fp8_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                          int32_t head_size, int32_t batch_size, int32_t max_query_len,
+                                          int32_t max_seq_len, int32_t window, int32_t num_sinks, int32_t num_splits) {
+  if (num_tokens <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || head_size <= 0 || batch_size <= 0 ||
+      max_query_len <= 0 || max_seq_len < 0 || num_sinks < 0 || num_splits <= 0)
+    return -1;
+  if (num_splits > 1) return kvq_per_head_attention_workspace_bytes(num_tokens, num_heads, head_size, num_splits);
+  if (int64_t{max_query_len} * (num_heads / num_kv_heads) <= kvq::most_few_rows(head_size, true)) return 0;
+  const int64_t rows = kvq::fp8_gather_rows(max_query_len, max_seq_len, window, num_sinks);
+  const double bytes = 4.0 * static_cast<double>(rows) * num_kv_heads * head_size * batch_size;
+  return bytes > 4.0e18 ? -1 : kvq::fp8_gather_bytes(rows, num_kv_heads, head_size, batch_size);
 }
 
 int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
@@ -1251,7 +1350,7 @@ kvq_status kvq_prompt_attention(const void* q, int64_t q_stride_t, int64_t q_str
               "%s: softmax_scale must be finite, its product with log2(e) as well", fn);
   KVQ_REQUIRE(d_status == nullptr || aligned(d_status, 4), "%s: d_status misaligned", fn);
   if (kvq_status s = check_device(fn)) return s;
-  kvq::PromptAttentionArgs a{};
+  kvq::PromptAttentionArgs a = prompt_args(num_heads, num_kv_heads, head_size);
   a.q = q;
   a.q_stride_t = q_stride_t;
   a.q_stride_h = q_stride_h;
@@ -1262,15 +1361,6 @@ kvq_status kvq_prompt_attention(const void* q, int64_t q_stride_t, int64_t q_str
   a.v_stride_t = v_stride_t;
   a.v_stride_h = v_stride_h;
   a.num_tokens = num_tokens;
-  a.num_heads = num_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.head_size = head_size;
-  a.group = num_heads / num_kv_heads;
-  a.group_div = kvq::FastDiv::make(static_cast<uint32_t>(a.group));
-  a.kv_heads_div = kvq::FastDiv::make(static_cast<uint32_t>(num_kv_heads));
-  a.tile_tokens = std::max(1, 128 / a.group);
-  a.chunks = (a.group + 127) / 128;
-  a.chunk_div = kvq::FastDiv::make(static_cast<uint32_t>(a.chunks));
   a.seq_start = seq_start;
   a.batch_size = batch_size;
   a.max_seq_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, num_tokens));

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <optional>
 #include <sstream>
 #include <string>
@@ -41,6 +42,7 @@ struct Library {
   decltype(&kvq_window_attention_fp8_per_head) fp8_window = nullptr;
   decltype(&kvq_prompt_attention) prompt = nullptr;
   decltype(&kvq_fp8_attention_default_splits) fp8_default_splits = nullptr;
+  decltype(&kvq_fp8_attention_workspace_bytes) fp8_workspace_bytes = nullptr;
   decltype(&kvq_per_head_attention_workspace_bytes) workspace_bytes = nullptr;
   decltype(&kvq_per_head_attention_default_splits) default_splits = nullptr;
   decltype(&kvq_last_error_string) last_error = nullptr;
@@ -391,7 +393,18 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       // default ranges that join without one run without it
       if (use_workspace || a[14] != Py_None) workspace = given;
     } else if (use_workspace && T > 0) {
-      const int64_t bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
+      int64_t bytes;
+      if (fp8) {
+        // (gathered entries: all requests' at a time, or as many as fit into 1 GiB)
+        const auto of = [&](int64_t requests) {
+          return lib.fp8_workspace_bytes(T, dim(H), c.heads, c.head_size, dim(requests), max_query, max_seq, window, sinks,
+                                         splits);
+        };
+        bytes = of(B);
+        if (splits == 1) bytes = std::min(bytes, std::max(of(1), int64_t{1} << 30));
+      } else {
+        bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
+      }
       if (bytes > 0) workspace = scope.buffer({bytes}, at::kByte);
     }
     void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
@@ -591,6 +604,7 @@ PyObject* bind(PyObject*, PyObject* table) {
       !set("kvq_window_attention_fp8_per_head", found.fp8_window) ||
       !set("kvq_prompt_attention", found.prompt) ||
       !set("kvq_fp8_attention_default_splits", found.fp8_default_splits) ||
+      !set("kvq_fp8_attention_workspace_bytes", found.fp8_workspace_bytes) ||
       !set("kvq_per_head_attention_workspace_bytes", found.workspace_bytes) ||
       !set("kvq_per_head_attention_default_splits", found.default_splits) ||
       !set("kvq_last_error_string", found.last_error))

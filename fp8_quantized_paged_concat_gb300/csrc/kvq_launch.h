@@ -280,7 +280,16 @@ struct AppendArgs {
 cudaError_t launch_rope_append(const AppendArgs& a, int num_sms, cudaStream_t stream);
 
 // Attention over whole prompts: sequence b is the rows [seq_start[b],
-// seq_start[b+1]) of q, k, v and out.
+// seq_start[b+1]) of q, k, v and out.  Or over the e4m3 cache's gathered
+// entries (cached.there is set): the rows of q and out are the last tokens of
+// request b's sequence of seq_lens[b] keys, whose rows of k and v start at
+// cached.rows * b; seq_start is query_start, max_seq_len max_query_len.
+struct CachedArgs {
+  const int32_t* seq_lens;        // [batch_size]
+  int32_t table_positions;        // block_table_width * block_size, < 2^31 - 256 (host check)
+  int32_t rows;                   // of the workspace for each request, a multiple of 64
+  const uint32_t* there;          // [batch_size * rows / 32 + 3]: bit per row: the key exists
+};
 struct PromptAttentionArgs {
   const void* q;                  // bf16 [num_tokens, num_heads, head_size]
   int64_t q_stride_t, q_stride_h;
@@ -308,8 +317,32 @@ struct PromptAttentionArgs {
   float* lse;
   int64_t lse_stride_t;
   int32_t* status;
+  CachedArgs cached;
 };
 cudaError_t launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t stream);
+
+// The e4m3 cache's entries that the requests' queries see, as bf16 rows.
+struct Fp8GatherArgs {
+  CachedArgs cached;
+  const int32_t* query_start;
+  int64_t num_tokens;
+  int32_t batch_size, max_query_len, window, num_sinks;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const uint8_t* cache;
+  const uint8_t* page_scales;
+  int64_t num_pages;
+  int32_t block_size;
+  FastDiv block_div;
+  uint32_t region;
+  int32_t row_offset, row_head;
+  int32_t num_kv_heads, head_size;
+  void* k;                        // bf16 [batch_size * cached.rows, num_kv_heads, head_size]
+  void* v;
+  uint32_t* there;                // cached.there
+  int32_t* status;
+};
+cudaError_t launch_fp8_gather(const Fp8GatherArgs& a, cudaStream_t stream);
 
 struct CompactArgs {
   uint8_t* cache;

@@ -38,10 +38,14 @@ inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t
 //   D =  64: 48 rows 159 / 179, 64 rows 204 / 179, 96 rows 303 / 179
 //   D = 128: 24 rows 171 / 193, 32 rows 173 / 193, 48 rows 253 / 193
 //   D = 256: 16 rows 124 / 170, 24 rows 187 / 171, 32 rows 236 / 171
+// Over the e4m3 cache (32 requests x 6000 keys, unsplit):
+//   D =  64: 48 rows 175 / 169, 64 rows 221 / 169 (4 x 3000 keys: 19.7 / 21.5, 24.2 / 21.4)
+//   D = 128: 32 rows 190 / 193, 48 rows 272 / 194
+//   D = 256: 24 rows 167 / 156, 32 rows 208 / 156 (4 x 3000 keys: 21.8 / 22.6, 35.6 / 35.4)
 // (The limit at D = 64 was set when the tensor memory kernel took 220 there; a
 // call this large is now past the crossing at 64 rows.)
 inline int64_t most_few_rows(int32_t head_size, bool fp8 = false) {
-  return fp8 ? 64 : head_size == 64 ? 64 : head_size == 128 ? 32 : 16;
+  return fp8 ? (head_size == 64 ? 48 : head_size == 128 ? 32 : 24) : head_size == 64 ? 64 : head_size == 128 ? 32 : 16;
 }
 
 // Rows per block of the tensor memory kernel: one row tile, or two that share
@@ -56,6 +60,21 @@ inline int64_t per_head_block(int64_t rows, int64_t groups, int32_t head_size, i
                                                      : few_rows(rows, groups, head_size, splits, sms, fp8);
 }
 
+// Rows of the workspace into which the e4m3 cache's entries are gathered, for
+// each request: the keys that some of its queries may see.
+inline int64_t fp8_gather_rows(int64_t max_query_len, int64_t max_seq_len, int64_t window, int64_t num_sinks) {
+  const int64_t keys = window > 0 ? std::min<int64_t>(max_seq_len, window + max_query_len - 1 + num_sinks) : max_seq_len;
+  return (std::max<int64_t>(keys, 1) + 63) / 64 * 64;
+}
+inline int64_t fp8_gather_bytes(int64_t rows, int64_t num_kv_heads, int64_t head_size, int64_t batch_size) {
+  return batch_size * rows * num_kv_heads * head_size * 4 + (batch_size * rows / 32 + 3 + 3) / 4 * 16;
+}
+// Whether a call's default is to gather: where every entry is read for many
+// blocks of rows, and these blocks fill the GPU.
+inline bool fp8_default_gathers(int64_t rows, int64_t groups, int sms) {
+  return rows >= 1024 && (rows + 255) / 256 * groups >= sms;
+}
+
 // The default key ranges per block of rows, whether they join through a
 // workspace, and the block that they are sized for.
 struct PerHeadRanges {
@@ -67,6 +86,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
                                              int32_t head_size, int64_t batch_size, int64_t max_seq_len,
                                              int64_t window, int64_t num_sinks, int sms, bool fp8 = false) {
   const int64_t rows = max_query_len * group, groups = num_kv_heads * batch_size;
+  if (fp8 && fp8_default_gathers(rows, groups, sms)) return {1, true, per_head_prefill_rows(rows, head_size)};
   const bool windowed = window > 0 && window < max_seq_len;
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;

@@ -40,6 +40,7 @@
 // frees its tensor memory and leaves its rows unwritten.
 #include <type_traits>
 
+#include "kvq_fp8_gather.cuh"
 #include "kvq_per_head_attention.cuh"
 #include "kvq_tensor_map.h"
 
@@ -54,7 +55,6 @@ constexpr int kSlots = 2;                         // work items known at once
 template <int D, int kTiles>
 struct Shape {
   static constexpr int kKeys = 64;                           // keys per tile
-  static constexpr int kFirst = 64;                          // of them, those whose weights are handed on first
   static constexpr int kSoftmaxWarps = 4 * kTiles;
   static constexpr int kCopyWarp = kSoftmaxWarps, kProductWarp = kCopyWarp + 1, kProductWarps = kTiles;
   static constexpr int kCheckWarp = kProductWarp + kProductWarps, kCheckWarps = 3 - kTiles;
@@ -87,18 +87,48 @@ struct Item {
   int32_t n;                   // its tokens; 0: no more items
   int32_t unit0;               // first unit of the block
   int32_t head;                // key head
+  int32_t first;               // position of its first token (negative: padding)
+  int32_t len;                 // its keys
+  int32_t key0;                // row of K and V of its first key
+  int32_t shift;               // the rows of keys past the sinks are this much further on
 };
 
-// The keys that some token in [t0, t1] of a sequence of n sees.
+// The keys that some token in [t0, t1] of the item's sequence sees.
 template <int kKeys>
-__device__ __forceinline__ Keys<kKeys> prompt_keys(const PromptAttentionArgs& a, int32_t t0, int32_t t1) {
+__device__ __forceinline__ Keys<kKeys> item_keys(const PromptAttentionArgs& a, const Item& it, int32_t t0, int32_t t1) {
   Keys<kKeys> k;
-  k.hi = t1 + 1;
-  k.lo = a.window > 0 ? max(0, t0 - a.window + 1) : 0;
+  k.hi = max(0, min(it.len, it.first + t1 + 1));
+  k.lo = a.window > 0 ? min(k.hi, max(0, it.first + t0 - a.window + 1)) : 0;
   k.sinks = min(a.num_sinks, k.lo);
   k.sink_steps = (k.sinks + kKeys - 1) / kKeys;
   k.steps = k.sink_steps + (k.hi - k.lo + kKeys - 1) / kKeys;
   return k;
+}
+
+// Sequences of the cache: every request has as many block numbers as
+// max_seq_len (here of query tokens) takes.
+template <int kTiles>
+__device__ __forceinline__ Item request_item_at(const PromptAttentionArgs& a, uint32_t index, int lane) {
+  const uint32_t j = a.kv_heads_div.div(index), block = static_cast<uint32_t>(kTiles * a.tile_tokens);
+  const uint32_t per = (static_cast<uint32_t>(a.max_seq_len) * a.chunks + block - 1) / block;
+  const uint32_t b = j / per, unit0 = (per - 1 - (j - b * per)) * block;
+  Item it{};
+  if (b >= static_cast<uint32_t>(a.batch_size)) return it;
+  GatherPlan plan;
+  if (!gather_plan(a.cached, a.seq_start, a.num_tokens, a.max_seq_len, a.window, a.num_sinks, b, plan)) {
+    if (lane == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
+    return it;
+  }
+  if (unit0 >= static_cast<uint32_t>(plan.n) * a.chunks) return it;
+  it.head = static_cast<int32_t>(index - j * a.num_kv_heads);
+  it.token0 = plan.token0;
+  it.n = plan.n;
+  it.unit0 = static_cast<int32_t>(unit0);
+  it.first = plan.first;
+  it.len = plan.len;
+  it.key0 = static_cast<int32_t>(b) * a.cached.rows;
+  it.shift = plan.sinks - plan.lo;
+  return it;
 }
 
 // The block of kTiles tiles with number `index` of all key heads' blocks.
@@ -135,6 +165,8 @@ __device__ __forceinline__ Item item_at(const PromptAttentionArgs& a, uint32_t i
   it.token0 = q0;
   it.n = static_cast<int32_t>(n);
   it.unit0 = static_cast<int32_t>((blocks - 1 - at) * block);
+  it.len = it.n;
+  it.key0 = q0;
   return it;
 }
 
@@ -152,15 +184,8 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[kCount]) {
 #pragma unroll
   for (int i = 0; i < kCount; i += 32) held32(r + i);
 }
-// kCount (a multiple of 16) columns stored without waiting.
-template <int kCount>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[kCount]) {
-#pragma unroll
-  for (int i = 0; i + 32 <= kCount; i += 32) tmem_st32_start(taddr + i, v + i);
-  if constexpr (kCount % 32 != 0) tmem_st16_start(taddr + kCount / 32 * 32, v + kCount / 32 * 32);
-}
-
-template <int D, int kTiles>
+// kCached: over the e4m3 cache's gathered entries.
+template <int D, int kTiles, bool kCached>
 __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap qmap,
                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -174,9 +199,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t bar = base + S::kMisc;
   const uint32_t k_full = bar, k_empty = k_full + 8 * S::kStages, v_full = k_empty + 8 * S::kStages;     // [kStages]
   const uint32_t v_good = v_full + 8 * S::kStages, v_empty = v_good + 8 * S::kStages;
-  // [score buffer]: scores there, first and all weights there, their products done
-  const uint32_t s_full = v_empty + 8 * S::kStages, p_first = s_full + 32, p_full = p_first + 32, o_first = p_full + 32;
-  const uint32_t o_done = o_first + 32;
+  // [score buffer]: scores there, weights there, their product done
+  const uint32_t s_full = v_empty + 8 * S::kStages, p_full = s_full + 32, o_done = p_full + 32;
   const uint32_t o_free = o_done + 32, drain = o_free + 16;                     // [row tile]
   const uint32_t item_full = drain + 16, item_free = item_full + 8 * kSlots;    // [kSlots]
   const uint32_t q_full = item_free + 8 * kSlots, q_free = q_full + 8, answered = q_free + 8;
@@ -185,7 +209,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(words);
   volatile int* s_abort = reinterpret_cast<volatile int*>(words + 4);
   volatile Item* items = reinterpret_cast<volatile Item*>(words + 8);
-  static_assert(40 * S::kStages + 5 * 32 + 32 + 16 * kSlots + 24 + 32 + 8 + kSlots * sizeof(Item) <= 512, "barrier layout");
+  static_assert(40 * S::kStages + 3 * 32 + 32 + 16 * kSlots + 24 + 32 + 8 + kSlots * sizeof(Item) <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -203,9 +227,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_first + 8 * i, 4);
       mbar_init(p_full + 8 * i, 4);
-      mbar_init(o_first + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -242,6 +264,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     it.n = __shfl_sync(kFull, s.n, 0);
     it.unit0 = __shfl_sync(kFull, s.unit0, 0);
     it.head = __shfl_sync(kFull, s.head, 0);
+    it.first = kCached ? __shfl_sync(kFull, s.first, 0) : 0;
+    it.len = __shfl_sync(kFull, s.len, 0);
+    it.key0 = __shfl_sync(kFull, s.key0, 0);
+    it.shift = kCached ? __shfl_sync(kFull, s.shift, 0) : 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(item_free + 8 * (k % kSlots));
     return it.n > 0;
@@ -251,7 +277,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   auto last_token = [&](const Item& it) {
     return min(it.n - 1, static_cast<int32_t>(a.chunk_div.div(static_cast<uint32_t>(it.unit0 + kTiles * a.tile_tokens - 1))));
   };
-  auto keys_of_item = [&](const Item& it) { return prompt_keys<kKeys>(a, first_token(it), last_token(it)); };
+  auto keys_of_item = [&](const Item& it) { return item_keys<kKeys>(a, it, first_token(it), last_token(it)); };
+  // row of K and V of step t's first key
+  auto row_of = [&](const Item& it, const Keys<kKeys>& keys, int32_t t) {
+    return it.key0 + keys.base(t) + (kCached && t >= keys.sink_steps ? it.shift : 0);
+  };
   // The score buffer of a row tile and its key tile `at` (of all items'), and
   // which use of it that is.
   auto buffer_of = [](int tile, uint32_t at) { return 2 * static_cast<uint32_t>(tile) + (at & 1); };
@@ -264,6 +294,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
   };
 
+  auto block_item = [&](uint32_t index) {
+    if constexpr (kCached) return request_item_at<kTiles>(a, index, lane);
+    return item_at<kTiles>(a, index, lane);
+  };
   Item it;
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
@@ -286,14 +320,25 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         has_row = head_of < static_cast<uint32_t>(a.group);
       }
       has_row = has_row && token_of < static_cast<uint32_t>(it.n);
-      const int32_t pos = min(static_cast<int32_t>(token_of), it.n - 1);
+      const int32_t token_in = min(static_cast<int32_t>(token_of), it.n - 1);
+      const int32_t pos = it.first + token_in, pos_hi = min(pos, it.len - 1);
       const int32_t q_head = it.head * a.group + static_cast<int32_t>(head_of);
       const int32_t pos_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       int32_t full0, full1;
-      full_steps(keys, __reduce_min_sync(kFull, pos), __reduce_max_sync(kFull, pos_lo), full0, full1);
+      full_steps(keys, __reduce_min_sync(kFull, pos_hi), __reduce_max_sync(kFull, pos_lo), full0, full1);
 
       float m = -INFINITY, l = 0.0f;                // reference maximum, sum
       bool done = true;                             // every wait was met
+      // which of a step's keys exist, asked for a step ahead
+      uint32_t there[3] = {kFull, kFull, kFull};
+      auto ask_there = [&](int32_t t) {
+        if (kCached && t < keys.steps) {
+          const uint32_t* words = a.cached.there + (row_of(it, keys, t) >> 5);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) there[c] = load_global(words + c);
+        }
+      };
+      ask_there(0);
       for (int32_t t = 0; t < keys.steps; ++t) {
         const uint32_t at = tiles + t, buf = buffer_of(tile, at), use = use_of(at);
         const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
@@ -301,117 +346,105 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           done = false;
           break;
         }
-        uint32_t see[kKeys / 32] = {};
-        const bool masked = t < full0 || t >= full1;
+        uint32_t see[2] = {kFull, kFull};
+        if constexpr (kCached) {
+          const uint32_t by = row_of(it, keys, t) & 31;
+          see[0] = __shfl_sync(kFull, __funnelshift_r(there[0], there[1], by), 0);
+          see[1] = __shfl_sync(kFull, __funnelshift_r(there[1], there[2], by), 0);
+          ask_there(t + 1);
+        }
+        const bool masked = t < full0 || t >= full1 || (kCached && (see[0] & see[1]) != kFull);
         if (masked) {
-          const int32_t p0 = keys.base(t), end = min(pos, keys.limit(t) - 1);
+          const int32_t p0 = keys.base(t), end = min(pos_hi, keys.limit(t) - 1);
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-            see[c] = range_bits(p0 + 32 * c, pos_lo, end) | range_bits(p0 + 32 * c, 0, min(a.num_sinks - 1, end));
+          for (int c = 0; c < 2; ++c)
+            see[c] &= range_bits(p0 + 32 * c, pos_lo, end) | range_bits(p0 + 32 * c, 0, min(a.num_sinks - 1, end));
         }
-        // The weights of kCount keys from column kFrom on, against the reference m,
-        // are formed, handed on and summed.  `before`: the barrier and phase of the
-        // product into O before these weights'.
-        auto part = [&](auto from_c, auto& s, uint32_t before, uint32_t phase, bool in_o, uint32_t ready) {
-          constexpr int kFrom = decltype(from_c)::value;
-          constexpr int kCount = static_cast<int>(sizeof(s) / 4);
-          uint32_t p[kCount / 2];
-          float sum;
-          auto pass = [&](auto with_mask) {
-            const float off = m == -INFINITY ? 0.0f : -m;
-            float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t s[kKeys], p[kKeys / 2];
+        float sum;
+        auto pass = [&](auto with_mask) {           // weights against the reference m: p and their sum
+          const float off = m == -INFINITY ? 0.0f : -m;
+          float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < kCount; i += 2) {
-              float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
-                               make_float2(off, off));
-              if constexpr (with_mask.value) {
-                z.x = (see[(kFrom + i) >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
-                z.y = (see[(kFrom + i) >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
-              }
-              const float2 w = make_float2(ex2(z.x), ex2(z.y));
-              sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
-              p[i >> 1] = pack_bf16x2(w.x, w.y);
+          for (int i = 0; i < kKeys; i += 2) {
+            float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
+                             make_float2(off, off));
+            if constexpr (with_mask.value) {
+              z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
+              z.y = (see[i >> 5] >> ((i + 1) & 31)) & 1 ? z.y : -INFINITY;
             }
-            const float2 both = fadd2(sums[0], sums[1]);
-            sum = both.x + both.y;
-          };
-          auto weights = [&]() {                    // warp-uniform choice
-            if (masked)
-              pass(std::true_type{});
-            else
-              pass(std::false_type{});
-          };
-          // (a row takes a new reference of its own accord, so that its bits do not
-          // depend on its neighbours')
-          bool behind = has_row;                    // (the other rows' queries may be anything)
-          if (t > 0 || kFrom > 0) {
-            weights();
-            behind = has_row && (m == -INFINITY || !(sum <= kMaxSum));
+            const float2 w = make_float2(ex2(z.x), ex2(z.y));
+            sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
+            p[i >> 1] = pack_bf16x2(w.x, w.y);
           }
-          if (__any_sync(kFull, behind)) {
-            if (t > 0 || kFrom > 0) {
-              tmem_load(s_col + kFrom, s);
-              tmem_loaded(s);
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) {
-              const float z = __uint_as_float(s[i]) * sc;
-              if (!masked || ((see[(kFrom + i) >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
-            }
-            float alpha = 1.0f;
-            if (behind && top > m) {
-              alpha = ex2(m - top);                 // 0 while m is -inf
-              m = top;
-            }
-            weights();
-            l *= alpha;
-            if (in_o) {
-              if (!have(before, phase)) return false;
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tmem_ld32(o_col + 32 * c, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                tmem_st32(o_col + 32 * c, o);
-              }
-            }
-          }
-          l += sum;
-          tmem_store(s_col + kFrom / 2, p);
-          tmem_st_wait();
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ready + 8 * buf);
-          return true;
+          const float2 both = fadd2(sums[0], sums[1]);
+          sum = both.x + both.y;
         };
-        // (before O is rescaled: the product of the tile before is waited for; for
-        // the second part, that of the first one's weights)
-        uint32_t first[S::kFirst];
-        tmem_load(s_col, first);
-        tmem_loaded(first);
-        if constexpr (S::kFirst == kKeys) {
-          done = part(std::integral_constant<int, 0>{}, first, o_done + 8 * (buf ^ 1), use_of(at - 1), t > 0, p_full);
-        } else {
-          uint32_t rest[kKeys - S::kFirst];
-          tmem_load(s_col + S::kFirst, rest);       // under way meanwhile
-          done = part(std::integral_constant<int, 0>{}, first, o_done + 8 * (buf ^ 1), use_of(at - 1), t > 0, p_first);
-          if (!done) break;
-          tmem_loaded(rest);
-          done = part(std::integral_constant<int, S::kFirst>{}, rest, o_first + 8 * buf, use, true, p_full);
+        auto weights = [&]() {                      // warp-uniform choice
+          if (masked)
+            pass(std::true_type{});
+          else
+            pass(std::false_type{});
+        };
+        tmem_load(s_col, s);
+        tmem_loaded(s);
+        // (a row takes a new reference of its own accord, so that its bits do not
+        // depend on its neighbours'; the queries of rows that are none may be anything)
+        bool behind = has_row;
+        if (t > 0) {
+          weights();
+          behind = has_row && (m == -INFINITY || !(sum <= kMaxSum));
         }
-        if (!done) break;
+        if (__any_sync(kFull, behind)) {
+          if (t > 0) {
+            tmem_load(s_col, s);
+            tmem_loaded(s);
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) {
+            const float z = __uint_as_float(s[i]) * sc;
+            if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
+          }
+          float alpha = 1.0f;
+          if (behind && top > m) {
+            alpha = ex2(m - top);                   // 0 while m is -inf
+            m = top;
+          }
+          weights();
+          l *= alpha;
+          if (t > 0) {
+            // O is rescaled once the product of the tile before is done
+            if (!have(o_done + 8 * (buf ^ 1), use_of(at - 1))) {
+              done = false;
+              break;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(o_col + 32 * c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(o_col + 32 * c, o);
+            }
+          }
+        }
+        l += sum;
+        tmem_st32_start(s_col, p);
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * buf);
       }
       // the last product is done: O is complete
       tiles += keys.steps;
-      if (done) done = have(o_done + 8 * buffer_of(tile, tiles - 1), use_of(tiles - 1));
+      if (done && keys.steps > 0) done = have(o_done + 8 * buffer_of(tile, tiles - 1), use_of(tiles - 1));
       if (!done) break;                             // uniform over the warp
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       // The rows leave in pieces of 64 values (128 bytes), eight lanes to a
       // piece, through the warp's 4 KB of shared memory.
       const uint32_t stage = base + S::kOut + warp * 4096;
-      const int64_t token = static_cast<int64_t>(it.token0) + pos;
+      const int64_t token = static_cast<int64_t>(it.token0) + token_in;
       const uint64_t mine =
           has_row ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + token * a.out_stride_t +
                                                q_head * a.out_stride_h)
@@ -428,7 +461,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float o[32];
-          tmem_ld32(o_col + 64 * c + 32 * half, o);
+          if (!kCached || keys.steps > 0) {
+            tmem_ld32(o_col + 64 * c + 32 * half, o);
+          } else {                                  // rows that see nothing
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= inv;
 #pragma unroll
@@ -437,7 +475,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
                         make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
                                    pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
         }
-        if (c == D / 64 - 1) {
+        if (c == D / 64 - 1 && (!kCached || keys.steps > 0)) {
           fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free + 8 * tile);
@@ -464,7 +502,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       uint32_t asked = 0;                           // requests for a next item
       bool waiting = false;                         // one is under way
       uint32_t queries = 0;                         // items whose queries were asked for
-      it = item_at<kTiles>(a, blockIdx.x, lane);
+      it = block_item(blockIdx.x);
       for (uint32_t k = 0;; ++k) {
         // an empty item is passed over; the request for the next one is under way
         // while the keys of this one are copied
@@ -487,7 +525,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           __syncwarp();
           more = x >= 0;
           it = Item{};
-          if (more) it = item_at<kTiles>(a, static_cast<uint32_t>(x), lane);
+          if (more) it = block_item(static_cast<uint32_t>(x));
         };
         if (k > 0) take();
         while (ok && more && it.n == 0) {
@@ -501,14 +539,20 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           s.n = it.n;
           s.unit0 = it.unit0;
           s.head = it.head;
+          s.first = it.first;
+          s.len = it.len;
+          s.key0 = it.key0;
+          s.shift = it.shift;
           mbar_arrive(item_full + 8 * (k % kSlots));
         }
         __syncwarp();
         if (it.n == 0) break;
         ask();
+        const Keys<kKeys> keys = keys_of_item(it);
+        if (kCached && keys.steps == 0) continue;
         // the query rows: the tile's tokens and heads as a box (heads past the
         // group's and tokens past the sequence's are rows that no one stores)
-        if (k > 0 && !have(q_free, k - 1)) break;
+        if (queries > 0 && !have(q_free, queries - 1)) break;
         if (elected) {
           mbar_arrive_expect_tx(q_full, kTiles * S::kBlocks * 128 * a.tile_tokens * min(a.group, 128));
 #pragma unroll
@@ -522,11 +566,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           }
         }
         __syncwarp();
-        queries = k + 1;
-        const Keys<kKeys> keys = keys_of_item(it);
+        ++queries;
         for (int32_t t = 0; t < keys.steps && ok; ++t) {
           const uint32_t at = tiles + t, st = at % S::kStages;
-          const int32_t key = it.token0 + keys.base(t);
+          const int32_t key = row_of(it, keys, t);
           auto copy = [&](uint32_t full, uint32_t empty, uint32_t to, const CUtensorMap* map, uint32_t& count) {
             if (at >= S::kStages && !have(empty + 8 * st, at / S::kStages - 1)) return false;
             if (elected) {
@@ -567,10 +610,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       const uint64_t qdesc = sw128_desc(base + w * S::kQTile, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
       const uint64_t vdesc = sw128_desc(base + S::kV, S::kKBlock, 1024);
       const uint32_t o = tmem + w * D;
-      uint32_t tiles = 0;                           // of the items before
+      uint32_t tiles = 0, items_done = 0;           // of the items before, those items that have any
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
         const int32_t n = keys_of_item(it).steps;
+        if (kCached && n == 0) continue;
         auto keys_there = [&](int32_t t) { return have(k_full + 8 * ((tiles + t) % S::kStages), (tiles + t) / S::kStages); };
         // S(t) = Q K(t)^T
         auto scores = [&](int32_t t) {
@@ -584,12 +628,12 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
           warp_commit(elected, k_empty + 8 * st);
           if (t == n - 1) warp_commit(elected, q_free);
         };
-        ok = have(q_full, k);
+        ok = have(q_full, items_done);
         for (int32_t t = 0; t < min(n, kAhead) && ok; ++t) {
           ok = keys_there(t);
           if (ok) scores(t);
         }
-        if (ok && k > 0) ok = have(o_free + 8 * w, k - 1);
+        if (ok && items_done > 0) ok = have(o_free + 8 * w, items_done - 1);
         for (int32_t t = 0; t < n && ok; ++t) {
           const uint32_t st = (tiles + t) % S::kStages, buf = buffer_of(w, tiles + t), use = use_of(tiles + t);
 #ifdef KVQ_ATTN_STALL_TILE
@@ -600,8 +644,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             break;
           }
 #endif
-          // O += P(t) V(t), as its weights come; what else it and the scores
-          // behind it need is waited for before them
+          // O += P(t) V(t); what else it and the scores behind it need is waited for
+          // before its weights
           ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
           if (ok && t + kAhead < n) ok = keys_there(t + kAhead);
           const uint64_t vd = vdesc + ((st * S::kTileBytes) >> 4);
@@ -609,20 +653,15 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
             warp_mma_ta(elected, o, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
                         (t > 0 || ks > 0) ? 1u : 0u);
           };
-          if constexpr (S::kFirst < kKeys) {
-            if (!ok || !(ok = have(p_first + 8 * buf, use))) break;
-#pragma unroll
-            for (int ks = 0; ks < S::kFirst / 16; ++ks) product(ks);
-            warp_commit(elected, o_first + 8 * buf);
-          }
           if (!ok || !(ok = have(p_full + 8 * buf, use))) break;
 #pragma unroll
-          for (int ks = S::kFirst < kKeys ? S::kFirst / 16 : 0; ks < kKeys / 16; ++ks) product(ks);
+          for (int ks = 0; ks < kKeys / 16; ++ks) product(ks);
           warp_commit(elected, o_done + 8 * buf);
           warp_commit(elected, v_empty + 8 * st);
           if (t + kAhead < n) scores(t + kAhead);
         }
         tiles += n;
+        ++items_done;
       }
       // the products still in flight are drained (bounded, whatever the abort flag says)
       warp_commit(elected, drain + 8 * w);
@@ -637,7 +676,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     } else {
       // ---- V where some row does not see the whole tile ------------------------
       const int me = warp - S::kCheckWarp;
-      if (blockIdx.x == 0 && me == 0) {               // sequences that item_at may not come across
+      if (!kCached && blockIdx.x == 0 && me == 0) {   // sequences that item_at may not come across
         for (int32_t b = lane; b < a.batch_size; b += 32) {
           const int32_t q0 = load_global(a.seq_start + b), q1 = load_global(a.seq_start + b + 1);
           if (q0 < 0 || q1 < q0 || q1 > a.num_tokens || static_cast<int64_t>(q1) - q0 > a.max_seq_len)
@@ -648,7 +687,8 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       bool ok = true;
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
         const Keys<kKeys> keys = keys_of_item(it);
-        const int32_t hi = first_token(it), lo = a.window > 0 ? max(0, last_token(it) - a.window + 1) : 0;
+        const int32_t hi = min(it.len - 1, it.first + first_token(it));
+        const int32_t lo = a.window > 0 ? max(0, it.first + last_token(it) - a.window + 1) : 0;
         int32_t full0, full1;
         full_steps(keys, hi, lo, full0, full1);
         for (int32_t t = 0; t < keys.steps; ++t) {
@@ -743,31 +783,39 @@ bool key_tensor_map(const void* p, int64_t stride_t, int64_t stride_h, int32_t h
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kCached>
 cudaError_t launch(const PromptAttentionArgs& a, cudaStream_t stream) {
   using S = Shape<D, kTiles>;
+  const int64_t rows = kCached ? int64_t{a.cached.rows} * a.batch_size : a.num_tokens;
   CUtensorMap qmap, kmap, vmap;
-  if (!query_tensor_map(a, &qmap) || !key_tensor_map<D, S::kKeys>(a.k, a.k_stride_t, a.k_stride_h, a.num_kv_heads, a.num_tokens, &kmap) ||
-      !key_tensor_map<D, S::kKeys>(a.v, a.v_stride_t, a.v_stride_h, a.num_kv_heads, a.num_tokens, &vmap))
+  if (!query_tensor_map(a, &qmap) || !key_tensor_map<D, S::kKeys>(a.k, a.k_stride_t, a.k_stride_h, a.num_kv_heads, rows, &kmap) ||
+      !key_tensor_map<D, S::kKeys>(a.v, a.v_stride_t, a.v_stride_h, a.num_kv_heads, rows, &vmap))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kTiles>,
+  const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kTiles, kCached>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = a.num_tokens * a.chunks / (kTiles * a.tile_tokens) + a.batch_size;     // the numbers of item_at
-  return launch_dependent(prompt_attention_kernel<D, kTiles>, dim3(static_cast<unsigned>(blocks * a.num_kv_heads)),
+  const int64_t block = kTiles * a.tile_tokens;
+  const int64_t blocks = kCached ? (int64_t{a.max_seq_len} * a.chunks + block - 1) / block * a.batch_size
+                                 : a.num_tokens * a.chunks / block + a.batch_size;          // the numbers of item_at
+  return launch_dependent(prompt_attention_kernel<D, kTiles, kCached>, dim3(static_cast<unsigned>(blocks * a.num_kv_heads)),
                           S::kThreads, S::kSmem, 1, stream, a, qmap, kmap, vmap);
+}
+
+template <bool kCached>
+cudaError_t launch_size(const PromptAttentionArgs& a, cudaStream_t stream) {
+  // two row tiles share a key tile wherever a sequence can fill them
+  const bool two = static_cast<int64_t>(a.max_seq_len) * a.chunks > a.tile_tokens;
+  switch (a.head_size) {
+    case 64: return two ? launch<64, 2, kCached>(a, stream) : launch<64, 1, kCached>(a, stream);
+    case 128: return two ? launch<128, 2, kCached>(a, stream) : launch<128, 1, kCached>(a, stream);
+    default: return launch<256, 1, kCached>(a, stream);   // one tile's O fills half of the tensor memory
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptAttentionArgs& a, cudaStream_t stream) {
-  // two row tiles share a key tile wherever a sequence can fill them
-  const bool two = static_cast<int64_t>(a.max_seq_len) * a.chunks > a.tile_tokens;
-  switch (a.head_size) {
-    case 64: return two ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
-    case 128: return two ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
-    default: return launch<256, 1>(a, stream);       // one tile's O fills half of the tensor memory
-  }
+  return a.cached.there != nullptr ? launch_size<true>(a, stream) : launch_size<false>(a, stream);
 }
 
 }  // namespace kvq

@@ -813,12 +813,23 @@ kvq_status kvq_rope_append_fp8_per_head(
  * over this cache's values.  A NaN code in a visible key makes its rows NaN;
  * in a visible value it makes its dimension NaN or reads as zero; a row that
  * does not see it never has it.
- * Arithmetic: products on the tensor cores with fp32 sums (codes exact in
- * f16; a query row scaled by a power of two into f16, exact down to 2^-28 of
- * its largest value); a key's scale multiplies its fp32 scores, a value's its
- * weight (a power of two, relative to one among the 2^6 above the largest of
- * the keys processed together), which is then rounded to f16 (relative
- * 2^-11); the softmax in fp32; out rounded once to bf16.
+ * Calls of many query rows per request and key head (more than 48 at head_size
+ * 64, 32 at 128, 24 at 256) with num_splits = 1 and a workspace gather the
+ * entries that their queries see into it, as bf16 rows (exact), and attend over
+ * those, as many requests at a time as it holds: at least one request's, as
+ * kvq_fp8_attention_workspace_bytes gives them for batch_size 1.  Then
+ * max_seq_len bounds seq_lens for good: a request of a longer sequence is
+ * skipped (KVQ_STATUS_BAD_BATCH), and q's strides are positive and below 2^38.
+ * Without a workspace they decode the entries in the attention, once for every
+ * block of 256 rows.
+ * Arithmetic: products on the tensor cores with fp32 sums, the softmax in
+ * fp32, out rounded once to bf16.  Over gathered rows as in
+ * kvq_prompt_attention, the weights rounded to bf16 (relative 2^-8).  Else codes
+ * are exact in f16; a query row is scaled by a power of two into f16, exact
+ * down to 2^-28 of its largest value; a key's scale multiplies its scores, a
+ * value's its weight, both relative (by powers of two) to the largest among
+ * the keys processed together, which is exact for values but for those 2^15
+ * and more below it; the weights are rounded to f16 (relative 2^-11).
  */
 kvq_status kvq_window_attention_fp8_per_head(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
@@ -834,8 +845,20 @@ kvq_status kvq_window_attention_fp8_per_head(
     int32_t* d_status, kvq_stream_t stream);
 
 /*
+ * kvq_fp8_attention_workspace_bytes -- bytes of workspace that a call of
+ * kvq_window_attention_fp8_per_head with these sizes can use: for num_splits >
+ * 1 what kvq_per_head_attention_workspace_bytes gives, for num_splits = 1 the
+ * gathered entries of all requests (0 for calls of few rows).  -1 for bad
+ * arguments.
+ */
+int64_t kvq_fp8_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                          int32_t head_size, int32_t batch_size, int32_t max_query_len,
+                                          int32_t max_seq_len, int32_t window, int32_t num_sinks, int32_t num_splits);
+
+/*
  * kvq_fp8_attention_default_splits -- kvq_per_head_attention_default_splits
- * for the e4m3 cache.
+ * for the e4m3 cache; 1 with *use_workspace set: a call that had better gather
+ * its entries.
  */
 int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
                                          int32_t head_size, int32_t batch_size, int32_t max_seq_len,

@@ -154,11 +154,12 @@ def visible(n, length, first, window, sinks):
     return (j <= p) & ((window <= 0) | (j > p - window) | (j < sinks))
 
 
-def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0):
+def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0, gathered=False):
     """Attention over the cache.  Weights are f16 (2^-11), in units in which
     the largest is at least 2^6; what is below f16's normal range is off by
     2^-25 of them, times the reference scale, at most 2^6 above the largest of
-    a value's page."""
+    a value's page.  Over gathered entries they are bf16 (2^-8), and queries
+    stay bf16."""
     T, H, D = q.shape
     g = H // cache.heads
     out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
@@ -177,9 +178,9 @@ def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0):
             e = np.clip(cache.scales[page, :, kh].astype(int) - BIAS, LEAST, MOST)
             code = cache.codes[page, :, at % cache.block, kh]
             K, V = (e4m3(code[:, i]) * 2.0 ** e[:, i, None] for i in (0, 1))
-            tiny = 2.0 ** -25 * (2.0 ** e[:, 1].max() if length else 0.0) * 448
+            tiny = (2.0 ** -100 if gathered else 2.0 ** -25) * (2.0 ** e[:, 1].max() if length else 0.0) * 448
             rows = q[t0:t1, kh * g:(kh + 1) * g].reshape(n * g, D)
-            got = attend(rows, K, V, see, scale, 2.0 ** -11, tiny)
+            got = attend(rows, K, V, see, scale, *((2.0 ** -8, tiny, 0.0) if gathered else (2.0 ** -11, tiny)))
             for to, x in zip((out, lse, tol_o, tol_l), got):
                 to[t0:t1, kh * g:(kh + 1) * g] = x.reshape(n, g, *x.shape[1:])
     return out, lse, tol_o, tol_l

@@ -276,9 +276,21 @@ class Batch:
         return ref.cached_attention(self.cache, ref.bf16(self.q_bits), self.start, self.lens, self.table, self.scale, **mask)
 
 
+def gathering(kvq, call, requests, **mask):
+    """The arguments of a call that gathers its entries, so many requests at a time."""
+    (T, H, D), pages = call["q"].shape, call["kv_scales"]
+    need = kvq.kvq_fp8_attention_workspace_bytes(T, H, pages.shape[2], D, requests, call["max_query_len"],
+                                                 call["max_seq_len"], mask.get("window", 0), mask.get("num_sinks", 0))
+    assert need > 0
+    # NaN wherever nothing is written
+    return dict(call, num_splits=1, workspace=torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV))
+
+
 def attend(kvq, call, splits, **mask):
-    """splits < 0: through a workspace; None: the default."""
-    if splits is not None:
+    """splits < 0: through a workspace; None: the default; "gather": two requests' entries at a time."""
+    if splits == "gather":
+        call = gathering(kvq, call, 2, **mask)
+    elif splits is not None:
         call = dict(call, num_splits=splits) if splits > 0 else through_workspace(kvq, call, -splits)
     return kvq.kvq_window_attention_fp8_per_head(**call, **mask)
 
@@ -311,66 +323,76 @@ def test_decode(kvq, dim, layout, heads, kv, block, window, sinks, splits):
 
 
 @pytest.mark.parametrize("dim,layout,heads,kv,block", SHAPES)
-@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 1), (0, 0, -2), (29, 5, 1), (29, 5, -3), (100, 0, None)])
+@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 1), (0, 0, -2), (29, 5, 1), (29, 5, -3), (100, 0, None),
+                                                 (0, 0, "gather"), (29, 5, "gather"), (1, 70, "gather"), (70, 100, "gather")])
 def test_chunks(kvq, dim, layout, heads, kv, block, window, sinks, splits):
     b = Batch([(0, 70), (65, 33), (200, 1), (7, 64), (0, 0), (130, 129)], heads, kv, dim, block, layout, 57 + dim + block)
-    check(attend(kvq, b.device(), splits, window=window, num_sinks=sinks), b.want(window=window, sinks=sinks))
+    check(attend(kvq, b.device(), splits, window=window, num_sinks=sinks),
+          b.want(window=window, sinks=sinks, gathered=splits == "gather"))
+
+
+def skip_unless(splits, rows):
+    if splits == "gather" and rows <= 48:
+        pytest.skip("few rows are not gathered for")
+    if splits not in ("gather", None) and splits > 1 and rows > 32:
+        pytest.skip("clusters take few rows")
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("block", [8, 16, 64])
 @pytest.mark.parametrize("new", [1, 3, 40, 70])
-@pytest.mark.parametrize("splits", [1, 3, -2])
+@pytest.mark.parametrize("splits", [1, 3, -2, "gather"])
 def test_scales_far_apart(kvq, dim, block, new, splits):
     """Pages whose scales differ by up to 2^30 either way, so that the references rise and fall."""
-    if splits > 1 and new > 8:
-        pytest.skip("clusters take few rows")
+    skip_unless(splits, 4 * new)
     b = Batch([(700, new), (63, new)], 4, 1, dim, block, "NHD", 71 + dim + block + new)
     pages = b.cache.scales.shape[0]
     b.cache.scales[:, 0] = (127 - 7 + b.rng.integers(-3, 2, (pages, 1))).astype(np.uint8)
     b.cache.scales[:, 1] = (127 - 7 + b.rng.choice([0, 0, 1, -1, 5, 9, -8, 15, -15], (pages, 1))).astype(np.uint8)
-    check(attend(kvq, b.device(), splits), b.want())
+    check(attend(kvq, b.device(), splits), b.want(gathered=splits == "gather"))
 
 
-@pytest.mark.parametrize("new", [1, 70])
-def test_scales_at_and_past_the_ends(kvq, new):
+@pytest.mark.parametrize("new,splits", [(1, None), (70, None), (70, "gather")])
+def test_scales_at_and_past_the_ends(kvq, new, splits):
     """The least and the largest scale, and bytes outside them, which read as the nearer one."""
     b = Batch([(200, new), (90, new)], 4, 2, 128, 16, "HND", 83, q_scale=1.0)
     pages = b.cache.scales.shape[0]
     b.cache.scales[:, 0] = 127 - 9
+    gathered = splits == "gather"
     b.cache.scales[:, 1] = b.rng.choice([0, 66, 67, 70], (pages, 2)).astype(np.uint8)
-    check(attend(kvq, b.device(), None), b.want())
+    check(attend(kvq, b.device(), splits), b.want(gathered=gathered))
     b.cache.scales[:, 1] = b.rng.choice([255, 188, 187, 180], (pages, 2)).astype(np.uint8)
-    check(attend(kvq, b.device(), None), b.want())
+    check(attend(kvq, b.device(), splits), b.want(gathered=gathered))
     b.cache.scales[:, 0] = b.rng.choice([0, 67, 80], (pages, 2)).astype(np.uint8)     # scores of about zero
-    check(attend(kvq, b.device(), None, window=50), b.want(window=50))
+    check(attend(kvq, b.device(), splits, window=50), b.want(window=50, gathered=gathered))
 
 
 @pytest.mark.parametrize("new", [1, 130])
-@pytest.mark.parametrize("splits", [1, 5, -5])
+@pytest.mark.parametrize("splits", [1, 5, -5, "gather"])
 def test_padded_requests_see_nothing_and_other_rows_are_left(kvq, new, splits):
-    if splits > 1 and new > 8:
-        pytest.skip("clusters take few rows")
+    skip_unless(splits, 4 * new)
     b = Batch([(50, new), (0, new), (90, new)], 8, 2, 128, 16, "NHD", 91, extra_tokens=5)
     b.lens[1] = 0                                                     # its queries have negative positions
+    b.lens[0] = new // 2                                              # and half of these (one token: none)
     call = b.device()
     out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
     lse = torch.full(b.q_bits.shape[:2], 7.5, device=DEV)
     got = attend(kvq, dict(call, out=out, lse=lse), splits)
     live = b.start[-1]
-    check(got, b.want(), live)
+    check(got, b.want(gathered=splits == "gather"), live)
     assert np.all(bits_of(out)[live:] == CANARY) and bool((lse[live:] == 7.5).all())
     assert bool((out[b.start[1]:b.start[2]] == 0).all()) and bool(torch.isneginf(lse[b.start[1]:b.start[2]]).all())
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("new", [1, 70])
-@pytest.mark.parametrize("splits", [1, -4])
+@pytest.mark.parametrize("splits", [1, -4, "gather"])
 def test_hidden_entries_have_no_effect(kvq, dim, new, splits):
     """NaN codes wherever no query sees them: page tails, pages of no request, positions before the windows."""
+    skip_unless(splits, 2 * new)
     b = Batch([(130, new), (40, new)], 4, 2, dim, 16, "NHD", 97 + dim)
     mask = dict(window=50, sinks=3)
-    want = b.want(**mask)
+    want = b.want(**mask, gathered=splits == "gather")
     clean = b.device()
     seen = np.zeros(b.cache.codes.shape[:1] + (16,), bool)
     for r, length in enumerate(b.lens):
@@ -388,37 +410,53 @@ def test_hidden_entries_have_no_effect(kvq, dim, new, splits):
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("new", [5, 70])
-def test_later_tokens_nan_does_not_reach_earlier_rows(kvq, dim, new):
+@pytest.mark.parametrize("new,splits", [(5, None), (70, None), (70, "gather")])
+def test_later_tokens_nan_does_not_reach_earlier_rows(kvq, dim, new, splits):
     b = Batch([(40, new)], 4, 2, dim, 16, "NHD", 101 + dim)
-    want = b.want()
+    want = b.want(gathered=splits == "gather")
     p = 40 + new - 2                                                  # the last but one
     b.cache.codes[b.table[0, p // 16], :, p % 16] = 0x7F
-    got = attend(kvq, b.device(), None)
+    got = attend(kvq, b.device(), splits)
     out, lse = ref.bf16(bits_of(got[0])), got[1].cpu().numpy()
     assert np.all(np.abs(out[:new - 2] - want[0][:new - 2]) <= want[2][:new - 2])
     assert np.all(np.isfinite(lse[:new - 2])) and np.all(np.isnan(lse[new - 2:])) and np.all(np.isnan(out[new - 2:]))
 
 
-@pytest.mark.parametrize("new", [1, 40])
-def test_bad_pages_and_requests(kvq, new):
+@pytest.mark.parametrize("new,splits", [(1, None), (40, None), (40, "gather")])
+def test_bad_pages_and_requests(kvq, new, splits):
     b = Batch([(100, new), (60, new), (50, new), (200, new)], 8, 2, 128, 16, "HND", 103)
     b.table[0, 2] = -1
     b.table[1, 1] = b.cache.codes.shape[0]
     b.table = b.table[:, :10].copy()                                  # request 3 goes past the table
-    want = b.want()
+    want = b.want(gathered=splits == "gather")
     call = b.device()
     call["query_start"][3] += new + 1                                 # 2: too many tokens, 3: a negative range
     out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    got = attend(kvq, dict(call, out=out, status=status), None)
+    got = attend(kvq, dict(call, out=out, status=status), splits)
     check(got, want, 2 * new)
     assert np.all(bits_of(out)[2 * new:] == CANARY)
     assert int(status.item()) == kvq.STATUS_BAD_INDEX | kvq.STATUS_BAD_BATCH
     call = b.device()
     status.zero_()
-    check(attend(kvq, dict(call, status=status), None), want)
+    check(attend(kvq, dict(call, status=status), splits), want)
     assert int(status.item()) == kvq.STATUS_BAD_INDEX
+
+
+@pytest.mark.parametrize("window", [0, 120])
+def test_sequences_past_the_workspace_are_skipped(kvq, window):
+    """max_seq_len has to hold where entries are gathered: a longer sequence's rows stay as they are."""
+    b = Batch([(60, 40), (300, 40), (20, 40)], 8, 2, 128, 16, "NHD", 104)
+    call = dict(b.device(), max_seq_len=128)
+    out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = attend(kvq, dict(call, out=out, status=status), "gather", window=window)
+    want = b.want(gathered=True, window=window)
+    keep = np.r_[0:40, 80:120]
+    o = ref.bf16(bits_of(got[0]))
+    assert np.all(np.abs(o[keep] - want[0][keep]) <= want[2][keep])
+    skipped = np.all(bits_of(out)[40:80] == CANARY)
+    assert skipped == (int(status.item()) == kvq.STATUS_BAD_BATCH) and skipped
 
 
 @pytest.mark.parametrize("new", [2, 90])
@@ -443,6 +481,8 @@ def test_strides_and_extreme_queries(kvq, new):
         b.scale = scale
         b.q_bits[1, 1] = b.q_bits[2, 1]
         check(attend(kvq, b.device(), None, window=20), b.want(window=20))
+        if new > 48:
+            check(attend(kvq, b.device(), "gather", window=20), b.want(window=20, gathered=True))
 
 
 @pytest.mark.parametrize("new", [1, 64])
@@ -454,7 +494,7 @@ def test_offsets_past_32_bits(kvq, new):
     raw = torch.zeros((pages, 2, block, kv, dim), dtype=torch.uint8, device=DEV)
     scales = torch.zeros((pages, 2, kv), dtype=torch.uint8, device=DEV)
     call = b.device()
-    want = b.want()
+    want, gathered = b.want(), b.want(gathered=True)
     used = b.table[0][b.table[0] >= 0]
     moved = {int(p): pages - 1 - 3 * i for i, p in enumerate(used)}
     for p, to in moved.items():
@@ -462,6 +502,8 @@ def test_offsets_past_32_bits(kvq, new):
     b.table = np.array([[moved.get(int(p), -1) for p in b.table[0]]])
     call = dict(call, kv_cache=raw, kv_scales=scales, block_table=dev(b.table.astype(np.int32)))
     check(attend(kvq, call, None), want)
+    if new > 48:
+        check(attend(kvq, call, "gather"), gathered)
     # and appended there
     key = torch.randn((new, kv, dim), device=DEV).to(torch.bfloat16)
     kvq.kvq_rope_append_fp8_per_head(None, key, key, torch.zeros(new, dtype=torch.int64, device=DEV),
@@ -482,14 +524,15 @@ def test_long_sequences_with_default_splits(kvq, dim, new):
 
 @pytest.mark.parametrize("dim,layout", [(64, "HND"), (128, "NHD"), (256, "NHD")])
 @pytest.mark.parametrize("new", [1, 2, 20, 40])
-@pytest.mark.parametrize("splits", [1, -2])
+@pytest.mark.parametrize("splits", [1, -2, "gather"])
 def test_rows_whose_maximum_grows(kvq, dim, layout, new, splits):
     """Scores that rise along the keys, past every reference, and fall again."""
+    skip_unless(splits, 2 * new)
     b = Batch([(450, new), (200, new)], 4, 2, dim, 16, layout, 127 + dim + new)
     for r, length in enumerate(b.lens):
         for col in range(-(-length // 16)):
             b.cache.scales[b.table[r, col], 0] = 127 - 16 + min(col // 2, 9)
-    check(attend(kvq, b.device(), splits), b.want())
+    check(attend(kvq, b.device(), splits), b.want(gathered=splits == "gather"))
 
 
 @pytest.mark.parametrize("dim,heads,kv,new", [(64, 6, 2, 11), (64, 6, 2, 21), (64, 6, 2, 22), (128, 8, 2, 8), (128, 8, 2, 9),
@@ -507,7 +550,7 @@ def test_many_requests_of_a_few_rows(kvq, dim, heads, kv, new):
     check(attend(kvq, b.device(), None), b.want())
 
 
-@pytest.mark.parametrize("new,splits", [(1, 4), (1, -4), (1, 1), (40, 1), (40, -3)])
+@pytest.mark.parametrize("new,splits", [(1, 4), (1, -4), (1, 1), (40, 1), (40, -3), (40, "gather")])
 def test_graphs_and_streams(kvq, new, splits):
     b = Batch([(300, new), (90, new)], 8, 2, 128, 16, "NHD", 139)
     call = b.device()
