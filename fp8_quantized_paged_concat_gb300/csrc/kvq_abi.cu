@@ -917,7 +917,7 @@ kvq_status per_head_attention(
   if (kvq_status s = check_device(fn, &num_sms)) return s;
   if (gathers) {
     // as many requests at a time as the workspace holds
-    int64_t most = std::min<int64_t>({batch_size, workspace_bytes / kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, 1),
+    int64_t most = std::min<int64_t>({batch_size, workspace_bytes / (gather_rows * num_kv_heads * head_size * 4),
                                       ((int64_t{1} << 31) - 256) / gather_rows});
     while (most > 1 && kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, most) > workspace_bytes) --most;
     for (int64_t b = 0; b < batch_size; b += most) {
