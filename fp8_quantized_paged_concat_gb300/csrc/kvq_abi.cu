@@ -901,24 +901,25 @@ kvq_status per_head_attention(
                 "%s: workspace must be non-NULL, 16-byte aligned and at least %lld bytes (got %lld)", fn,
                 static_cast<long long>(need), static_cast<long long>(workspace_bytes));
   }
-  const bool gathers =
-      fp8 && num_splits == 1 && workspace != nullptr && int64_t{max_query_len} * group > kvq::most_few_rows(head_size, true);
-  const int64_t gather_rows = kvq::fp8_gather_rows(max_query_len, max_seq_len, window, num_sinks);
+  // (what the copy engine cannot address is decoded in the attention all the same)
+  constexpr int64_t kMostStride = int64_t{1} << 38;
+  const bool gathers = fp8 && num_splits == 1 && workspace != nullptr &&
+                       int64_t{max_query_len} * group > kvq::most_few_rows(head_size, true) && q_stride_t > 0 &&
+                       q_stride_h > 0 && std::max(q_stride_t, q_stride_h) < kMostStride;
   if (gathers) {
+    const int32_t most_new = static_cast<int32_t>(std::min<int64_t>(max_query_len, num_tokens));
+    const int64_t gather_rows =
+        kvq::fp8_gather_rows(most_new, std::min(max_seq_len, block_table_width * block_size), window, num_sinks);
     const int64_t need = kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, 1);
     KVQ_REQUIRE(aligned(workspace, 16) && workspace_bytes >= need,
                 "%s: workspace must be 16-byte aligned and at least %lld bytes (got %lld)", fn,
                 static_cast<long long>(need), static_cast<long long>(workspace_bytes));
-    KVQ_REQUIRE(gather_rows < (int64_t{1} << 31) - 256 && q_stride_t > 0 && q_stride_t < (int64_t{1} << 38) &&
-                    q_stride_h < (int64_t{1} << 38),
-                "%s: with a workspace, q strides must be positive and below 2^38, max_seq_len below 2^31 - 256", fn);
-  }
-  int num_sms = 0;
-  if (kvq_status s = check_device(fn, &num_sms)) return s;
-  if (gathers) {
-    // as many requests at a time as the workspace holds
+    if (kvq_status s = check_device(fn)) return s;
+    // as many requests at a time as the workspace holds, their rows and blocks below 2^31
+    const kvq::PromptAttentionArgs shape = prompt_args(num_heads, num_kv_heads, head_size);
+    const int64_t blocks = (int64_t{most_new} * shape.chunks + shape.tile_tokens - 1) / shape.tile_tokens * num_kv_heads;
     int64_t most = std::min<int64_t>({batch_size, workspace_bytes / (gather_rows * num_kv_heads * head_size * 4),
-                                      ((int64_t{1} << 31) - 256) / gather_rows});
+                                      ((int64_t{1} << 31) - 256) / gather_rows, ((int64_t{1} << 31) - 1) / blocks});
     while (most > 1 && kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, most) > workspace_bytes) --most;
     for (int64_t b = 0; b < batch_size; b += most) {
       const int32_t n = static_cast<int32_t>(std::min<int64_t>(most, batch_size - b));
@@ -931,7 +932,7 @@ kvq_status per_head_attention(
       g.query_start = query_start + b;
       g.num_tokens = num_tokens;
       g.batch_size = n;
-      g.max_query_len = max_query_len;
+      g.max_query_len = most_new;
       g.window = window;
       g.num_sinks = num_sinks;
       g.block_table = block_table + b * block_table_stride;
@@ -948,7 +949,7 @@ kvq_status per_head_attention(
       g.head_size = head_size;
       g.status = d_status;
       if (kvq_status s = launched(fn, kvq::launch_fp8_gather(g, reinterpret_cast<cudaStream_t>(stream)))) return s;
-      kvq::PromptAttentionArgs p = prompt_args(num_heads, num_kv_heads, head_size);
+      kvq::PromptAttentionArgs p = shape;
       p.q = q;
       p.q_stride_t = q_stride_t;
       p.q_stride_h = q_stride_h;
@@ -959,7 +960,7 @@ kvq_status per_head_attention(
       p.num_tokens = num_tokens;
       p.seq_start = query_start + b;
       p.batch_size = n;
-      p.max_seq_len = max_query_len;
+      p.max_seq_len = most_new;
       p.scale_log2 = static_cast<float>(scale_log2);
       p.window = window;
       p.num_sinks = num_sinks;
@@ -974,6 +975,8 @@ kvq_status per_head_attention(
     }
     return ok();
   }
+  int num_sms = 0;
+  if (kvq_status s = check_device(fn, &num_sms)) return s;
   kvq::PerHeadAttentionArgs a{};
   a.q = q;
   a.q_stride_t = q_stride_t;

@@ -358,7 +358,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       vs = scale_word("v_scale", a[7], dev);
     }
     const float scale = real(a[8]);
-    const int32_t max_query = int32("max_query_len", a[9]), max_seq = int32("max_seq_len", a[10]);
+    const int32_t max_query = int32("max_query_len", a[9]);
+    int32_t max_seq = int32("max_seq_len", a[10]);
+    if (fp8) max_seq = static_cast<int32_t>(std::min<int64_t>(max_seq, W * int64_t{c.block_size}));   // the table's reach
     const int32_t window = int32("window", a[11]), sinks = int32("num_sinks", a[12]);
     const bool tree = a[3] != Py_None;
     const Scope scope(a[19], dev);

@@ -819,9 +819,9 @@ kvq_status kvq_rope_append_fp8_per_head(
  * those, as many requests at a time as it holds: at least one request's, as
  * kvq_fp8_attention_workspace_bytes gives them for batch_size 1.  Then
  * max_seq_len bounds seq_lens for good: a request of a longer sequence is
- * skipped (KVQ_STATUS_BAD_BATCH), and q's strides are positive and below 2^38.
- * Without a workspace they decode the entries in the attention, once for every
- * block of 256 rows.
+ * skipped (KVQ_STATUS_BAD_BATCH).  Without a workspace, or where q's strides
+ * are not positive and below 2^38, they decode the entries in the attention,
+ * once for every block of 256 rows.
  * Arithmetic: products on the tensor cores with fp32 sums, the softmax in
  * fp32, out rounded once to bf16.  Over gathered rows as in
  * kvq_prompt_attention, the weights rounded to bf16 (relative 2^-8).  Else codes
@@ -889,10 +889,11 @@ int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_head
  * unwritten (KVQ_STATUS_TIMEOUT).
  * q: bf16 [num_tokens, num_heads, head_size]; k, v: bf16 [num_tokens,
  * num_kv_heads, head_size]; token and head strides in elements (multiples of
- * 8; positive and below 2^38); head_size 64, 128 or 256; num_heads a multiple of num_kv_heads.  out: as q, token stride >=
- * (num_heads - 1) * head stride + head_size.  lse: fp32 [num_tokens,
- * num_heads], token stride lse_stride_t, or NULL.  out and lse overlap no
- * input.  softmax_scale: softmax_scale * log2(e) is finite in fp32.
+ * 8; positive and below 2^38); head_size 64, 128 or 256; num_heads a multiple
+ * of num_kv_heads.  out: as q, token stride >= (num_heads - 1) * head stride +
+ * head_size.  lse: fp32 [num_tokens, num_heads], token stride lse_stride_t, or
+ * NULL.  out and lse overlap no input.  softmax_scale: softmax_scale * log2(e)
+ * is finite in fp32.
  * seq_start: int32 [batch_size + 1]; batch_size <= 65535; num_tokens *
  * num_heads + 65536 * num_kv_heads < 2^31.
  */

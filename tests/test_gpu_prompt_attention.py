@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp8_per_head_reference as ref
-from test_gpu_fp8_per_head import CANARY, DEV, bf16_dev, bits_of, check, dev, i32, kvq, pages_for   # noqa: F401
+from test_gpu_fp8_per_head import CANARY, DEV, Batch, attend, bf16_dev, bits_of, check, dev, i32, kvq, pages_for   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +211,139 @@ def test_refuses_what_does_not_fit(kvq):
     refused(RuntimeError, "num_sinks", num_sinks=-1)
     refused(RuntimeError, "max_seq_len", max_seq_len=-1)
     refused(RuntimeError, "strides", k=k[:1].expand(35, 2, 64))
+
+
+# --------------------------------------------------------------------------
+# the operators together
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dim,heads,kv,layout,block,rot,interleaved,window,sinks", [
+    (64, 7, 1, "HND", 24, 32, True, 0, 0), (128, 8, 2, "NHD", 16, 128, False, 50, 3), (256, 4, 2, "NHD", 32, 64, False, 0, 0)])
+def test_prompts_chunks_and_decoded_tokens(kvq, dim, heads, kv, layout, block, rot, interleaved, window, sinks):
+    """Prompts are rotated, appended and attended whole; then a chunk of tokens and single ones over the cache."""
+    rng = np.random.default_rng(67 + dim)
+    steps = [[90, 37, 150], [40, 3, 21]] + [[1, 1, 1]] * 5
+    total, table = pages_for([(0, sum(s[b] for s in steps)) for b in range(3)], block, rng)
+    cache = ref.Cache(total, block, kv, dim, layout, rng)
+    raw, scales, block_table = dev(cache.raw()), dev(cache.scales), dev(table.astype(np.int32))
+    angle = rng.uniform(-7, 7, (300, rot // 2))
+    cos_sin = np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)
+    scale, lens = dim ** -0.5, [0, 0, 0]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for step, new in enumerate(steps):
+        start = np.cumsum([0] + new).tolist()
+        positions = np.concatenate([np.arange(c, c + n) for c, n in zip(lens, new)])
+        lens = [c + n for c, n in zip(lens, new)]
+        x = ref.to_bf16(rng.standard_normal((start[-1], heads + 2 * kv, dim)))
+        q, k, v = x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+        on = bf16_dev(x)
+        begin, seq_lens, most = i32(start), i32(lens), max(new)
+        rq, rk = kvq.kvq_rope_append_fp8_per_head(
+            on[:, :heads], on[:, heads:heads + kv], on[:, heads + kv:], dev(positions), dev(cos_sin), begin, seq_lens,
+            block_table, raw, scales, most, interleaved=interleaved, layout=layout, status=status)
+        if step == 0:
+            got = kvq.kvq_prompt_attention(rq, rk, on[:, heads + kv:], begin, scale, most, window=window, num_sinks=sinks,
+                                           status=status)
+        else:
+            got = kvq.kvq_window_attention_fp8_per_head(rq, begin, seq_lens, block_table, raw, scales, scale, most, max(lens),
+                                                        window=window, num_sinks=sinks, layout=layout, status=status)
+        want_q, want_k = np.zeros_like(q), np.zeros_like(k)
+        assert ref.append(cache, q, k, v, positions, cos_sin, start, lens, table, interleaved, want_q, want_k) == 0
+        assert np.array_equal(bits_of(rq), want_q) and np.array_equal(bits_of(rk), want_k)
+        assert np.array_equal(cache.from_raw(raw.cpu().numpy()), cache.codes)
+        assert np.array_equal(scales.cpu().numpy(), cache.scales)
+        if step == 0:
+            want = ref.prompt_attention(ref.bf16(want_q), ref.bf16(want_k), ref.bf16(v), start, scale, window, sinks)
+        else:
+            want = ref.cached_attention(cache, ref.bf16(want_q), start, lens, table, scale, window, sinks)
+        check(got, want)
+        assert int(status.item()) == 0
+
+
+def test_values_the_cache_holds_exactly(kvq):
+    """Keys and values of e4m3's own: a prompt whole and in parts over the cache agree with one 64-bit form."""
+    rng = np.random.default_rng(71)
+    n, first, heads, kv, dim, block = 230, 100, 8, 2, 128, 16
+    total, table = pages_for([(0, n)], block, rng)
+    raw = torch.zeros((total, 2, block, kv, dim), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros((total, 2, kv), dtype=torch.uint8, device=DEV)
+    values = np.array([0.0, 0.25, -0.5, 1.0, -1.75, 3.5, -3.5])                    # 3.5 = 448 * 2^-7
+    q = ref.to_bf16(rng.standard_normal((n, heads, dim)))
+    k, v = (ref.to_bf16(rng.choice(values, (n, kv, dim))) for _ in range(2))
+    k[:, :, 0] = v[:, :, 0] = ref.to_bf16(np.float32(3.5))                        # every page's scale: the same
+    on = [bf16_dev(x) for x in (q, k, v)]
+    still = torch.tensor([[1.0] * 8 + [0.0] * 8], device=DEV).repeat(n, 1).contiguous()
+    block_table, where = dev(table.astype(np.int32)), torch.arange(n, device=DEV)
+    want = ref.prompt_attention(*(ref.bf16(x) for x in (q, k, v)), [0, n], dim ** -0.5)
+    check(kvq.kvq_prompt_attention(*on, i32([0, n]), dim ** -0.5, n), want)
+    got = []
+    for t0, t1 in [(0, first), (first, n - 3)] + [(t, t + 1) for t in range(n - 3, n)]:
+        rq, rk = kvq.kvq_rope_append_fp8_per_head(*(x[t0:t1] for x in on), where[t0:t1], still, i32([0, t1 - t0]), i32([t1]),
+                                                  block_table, raw, scales, t1 - t0)
+        assert torch.equal(rq, on[0][t0:t1]) and torch.equal(rk, on[1][t0:t1])
+        got.append(kvq.kvq_window_attention_fp8_per_head(rq, i32([0, t1 - t0]), i32([t1]), block_table, raw, scales,
+                                                         dim ** -0.5, t1 - t0, t1))
+    # (weights rounded more finely than the prompt's: the same tolerances hold)
+    check([torch.cat([g[i] for g in got]) for i in range(2)], want)
+
+
+def test_large_calls_gather_by_default(kvq):
+    b = Batch([(200, 130), (17, 130), (0, 130), (90, 101)], 64, 8, 64, 16, "NHD", 73)
+    call = b.device()
+    assert kvq.kvq_fp8_attention_default_splits(130, 64, 8, 64, 4, max(b.lens)) == (1, True)
+    want = b.want(gathered=True)
+    got = attend(kvq, call, None)
+    check(got, want)
+    # a bound on the lengths that is far off costs nothing: the block table's reach holds as well
+    loose = attend(kvq, dict(call, max_seq_len=(1 << 31) - 1), None)
+    assert torch.equal(loose[0], got[0]) and torch.equal(loose[1], got[1])
+    loose = attend(kvq, dict(call, max_query_len=100000), None)
+    assert torch.equal(loose[0], got[0]) and torch.equal(loose[1], got[1])
+    # queries that the copy engine cannot address: decoded in the attention
+    same = call["q"][:1].expand(b.q_bits.shape[0], -1, -1)
+    b.q_bits[:] = b.q_bits[:1]
+    check(attend(kvq, dict(call, q=same), None), b.want())
+
+
+def test_calls_at_once(kvq):
+    """Every operator on two streams at the same time, each call with its own outputs and workspace."""
+    b = Batch([(2000, 130), (700, 130), (40, 130), (900, 101)], 64, 8, 64, 16, "NHD", 79)
+    few = Batch([(3000, 1), (500, 1)], 64, 8, 64, 16, "NHD", 83)
+    p = Prompts([500, 300], 64, 8, 64, 89, pad=0)
+    big, small = b.device(), few.device()
+    jobs = [lambda s: attend(kvq, dict(big, stream=s), None), lambda s: attend(kvq, dict(small, stream=s), None),
+            lambda s: attend(kvq, dict(big, stream=s), 2), lambda s: p.run(kvq, stream=s)]
+    want = [f(None) for f in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for turn in range(4):
+        for i, f in enumerate(jobs):
+            got.append((i, f(streams[(i + turn) % 2])))
+            got.append((i, f(streams[(i + turn + 1) % 2])))
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1])
+
+
+def test_graphs_that_share_a_workspace(kvq):
+    one, two = (Batch(reqs, 8, 2, 128, 16, "NHD", 97 + len(reqs)) for reqs in ([(300, 90), (20, 64)], [(5, 90), (600, 90), (0, 90)]))
+    calls, need = [b.device() for b in (one, two)], 0
+    for c in calls:
+        need = max(need, kvq.kvq_fp8_attention_workspace_bytes(c["q"].shape[0], 8, 2, 128, 2, c["max_query_len"], c["max_seq_len"]))
+    held = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    want = [kvq.kvq_window_attention_fp8_per_head(**c, num_splits=1, workspace=held) for c in calls]
+    graphs, inside = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            inside.append(kvq.kvq_window_attention_fp8_per_head(**c, num_splits=1, workspace=held))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(inside, want):
+            assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+        for got in inside:
+            got[0].zero_()
