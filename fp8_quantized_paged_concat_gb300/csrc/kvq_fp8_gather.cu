@@ -57,16 +57,18 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_gather_kernel(const Fp8Gather
     }
     for (int32_t hs = warp; hs < 2 * a.num_kv_heads; hs += kWarps) {
       const int32_t side = hs & 1, head = hs >> 1;
-      uint4 w[kPasses];
+      uint2 w[kPasses][2];                          // values 8 c on, and D / 2 + 8 c on
       uint32_t e[kPasses];
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const int from = i * kAtOnce + row_in;
-        w[i] = make_uint4(0, 0, 0, 0);
+        w[i][0] = w[i][1] = make_uint2(0, 0);
         e[i] = KVQ_FP8_SCALE_BIAS;
         if ((there >> from) & 1) {
           const uint8_t* region = at_offset(a.cache + (side ? a.region : 0), page[i], 2 * a.region);
-          w[i] = load_global(reinterpret_cast<const uint4*>(at_offset(region, page_row[i] + head * a.row_head, D)) + c);
+          const uint2* x = reinterpret_cast<const uint2*>(at_offset(region, page_row[i] + head * a.row_head, D)) + c;
+          w[i][0] = load_global(x);
+          w[i][1] = load_global(x + kLanes);
           e[i] = load_global(a.page_scales + (static_cast<uint64_t>(page[i]) * 2 + side) * a.num_kv_heads + head);
         }
       }
@@ -76,16 +78,16 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_gather_kernel(const Fp8Gather
         const int from = i * kAtOnce + row_in;
         if (r0 + from >= rows) continue;
         const float f = __uint_as_float(page_scale(e[i]) << 23);
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const uint32_t x[4] = {w[i][0].x, w[i][0].y, w[i][1].x, w[i][1].y};
         uint32_t y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 v = __half22float2(e4m3x2_to_half2(x[j >> 1] >> (16 * (j & 1))));
           y[j] = pack_bf16x2(v.x * f, v.y * f);
         }
-        uint4* to = reinterpret_cast<uint4*>(out + ((out_row0 + from) * a.num_kv_heads + head) * D) + 2 * c;
+        uint4* to = reinterpret_cast<uint4*>(out + ((out_row0 + from) * a.num_kv_heads + head) * D) + c;
         to[0] = make_uint4(y[0], y[1], y[2], y[3]);
-        to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        to[kLanes] = make_uint4(y[4], y[5], y[6], y[7]);
       }
     }
   }
