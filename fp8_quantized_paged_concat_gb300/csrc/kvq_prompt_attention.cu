@@ -105,15 +105,28 @@ __device__ __forceinline__ Keys<kKeys> item_keys(const PromptAttentionArgs& a, c
   return k;
 }
 
+// Which place the lane's request has among up to 32 of them, longest first.
+__device__ __forceinline__ uint32_t request_rank(const PromptAttentionArgs& a, int lane) {
+  const int32_t len = lane < a.batch_size ? load_global(a.cached.seq_lens + lane) : INT32_MIN;
+  uint32_t rank = 0;
+  for (int j = 0; j < 32; ++j) {
+    const int32_t other = __shfl_sync(kFull, len, j);
+    rank += other > len || (other == len && j < lane);
+  }
+  return rank;
+}
+
 // Sequences of the cache: every request has as many block numbers as
-// max_seq_len (here of query tokens) takes.
+// max_seq_len (here of query tokens) takes; up to 32 requests come longest
+// first, so that short items are left for the end.
 template <int kTiles>
-__device__ __forceinline__ Item request_item_at(const PromptAttentionArgs& a, uint32_t index, int lane) {
+__device__ __forceinline__ Item request_item_at(const PromptAttentionArgs& a, uint32_t index, uint32_t rank, int lane) {
   const uint32_t j = a.kv_heads_div.div(index), block = static_cast<uint32_t>(kTiles * a.tile_tokens);
   const uint32_t per = (static_cast<uint32_t>(a.max_seq_len) * a.chunks + block - 1) / block;
-  const uint32_t b = j / per, unit0 = (per - 1 - (j - b * per)) * block;
+  const uint32_t place = j / per, unit0 = (per - 1 - (j - place * per)) * block;
   Item it{};
-  if (b >= static_cast<uint32_t>(a.batch_size)) return it;
+  if (place >= static_cast<uint32_t>(a.batch_size)) return it;
+  const uint32_t b = a.batch_size > 32 ? place : __ffs(__ballot_sync(kFull, rank == place)) - 1;
   GatherPlan plan;
   if (!gather_plan(a.cached, a.seq_start, a.num_tokens, a.max_seq_len, a.window, a.num_sinks, b, plan)) {
     if (lane == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
@@ -294,10 +307,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
     full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
   };
 
-  auto block_item = [&](uint32_t index) {
-    if constexpr (kCached) return request_item_at<kTiles>(a, index, lane);
-    return item_at<kTiles>(a, index, lane);
-  };
   Item it;
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
@@ -502,6 +511,11 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
       uint32_t asked = 0;                           // requests for a next item
       bool waiting = false;                         // one is under way
       uint32_t queries = 0;                         // items whose queries were asked for
+      const uint32_t rank = kCached && a.batch_size <= 32 ? request_rank(a, lane) : 0;
+      auto block_item = [&](uint32_t index) {
+        if constexpr (kCached) return request_item_at<kTiles>(a, index, rank, lane);
+        return item_at<kTiles>(a, index, lane);
+      };
       it = block_item(blockIdx.x);
       for (uint32_t k = 0;; ++k) {
         // an empty item is passed over; the request for the next one is under way
