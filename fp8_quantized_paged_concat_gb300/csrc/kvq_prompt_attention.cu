@@ -7,20 +7,24 @@
 //   lse = m + ln sum_j exp(s_j - m).
 // The products bound it: 4 D flops for each (row, visible key).
 //
-// Design: one CTA per SM, which takes one item after the other: (block of 128
-// kTiles query rows, key head, sequence).  The grid has a CTA per item; one
+// Design: one CTA per SM (two where sequences fit one row tile, and head_size
+// <= 128: 256 sequences of 30 tokens, 32 query heads of 128, 61 -> 48 us; where
+// they take more, blocks of two tiles read their keys half as often: 16 x 1000
+// tokens 133 us, 220 with one), which takes one item after the other: (block of
+// 128 kTiles query rows, key head, sequence).  The grid has a CTA per item; one
 // that runs takes over the next that has not started, whose keys and queries
-// are copied while it finishes.  The rows are (token, head) pairs of the sequence that share the
-// key head, so that every tile of keys serves the whole group.
-//   - tensor memory: O of row tile w in columns [D w, +D), two score buffers
-//     of kKeys columns from column 256 on: with two row tiles one each, with
-//     one row tile taken in turn.  A buffer's weights P (bf16) overwrite its
-//     first half.
-//   - one warp issues the products, in the order S(0) S(1) [PV(0) S(2)] [PV(1)
-//     S(3)] ... over the (row tile, key tile) pairs: while the weights of one
-//     are computed, the products of the other run.  The tensor core takes them
-//     in that order, so that S(i + 2) needs no wait for the PV(i) that reads
-//     its buffer.
+// are copied while it finishes.  Long items come first.  The rows are (token,
+// head) pairs of the sequence that share the key head, so that every tile of
+// keys serves the whole group.
+//   - tensor memory: O of row tile w in columns [D w, +D), behind them two score
+//     buffers of kKeys columns for each row tile.  A buffer's weights P (bf16)
+//     overwrite its first half.
+//   - one warp per row tile issues its products, in the order S(0) S(1) [PV(0)
+//     S(2)] [PV(1) S(3)] ... over the key tiles: while the weights of one are
+//     computed, the products of the other row tile run.  The tensor core takes
+//     them in that order, so that S(i + 2) needs no wait for the PV(i) that
+//     reads its buffer.  (128-key tiles with one buffer per row tile, and one
+//     warp for both: 1 x 16384 tokens 1574 us against 1250.)
 //   - one warp has the copy engine land the query rows and the tiles of K and V
 //     (tensor maps, 128-byte swizzle); a tile of query rows holds all of the
 //     group's heads of as many whole tokens as it has room for.
@@ -34,7 +38,17 @@
 //     padding, or later tokens.  Their scores are replaced, and their values,
 //     whose weight is 0, are made harmless in shared memory: rows past the
 //     sequence are zeroed, and in tiles that some row does not see whole NaN
-//     and infinities are (another warp looks through them).
+//     and infinities are (one or two warps look through them).
+// Measured (32 query heads, 8 key heads; calls one after the other), and of
+// 1947 TFLOP/s: D = 128, 1 x 16384 tokens 1200 us = 1830 TFLOP/s, 0.94; 4 x 4096
+// 344 us = 1600, 0.82; 16 x 1024 136 us = 1009, 0.52.  A pair of row tiles takes
+// about 1330 clocks a key tile, of which the products take 1280 (S at 48 clocks
+// per 16 dimensions, bound by shared memory, PV at 64 per 16 keys); an item
+// costs some 4000 more, for its first and last tiles' masks and its output.
+// D = 64: 1 x 16384 1070 us = 1030 TFLOP/s, where the chain from a tile's scores
+// to its weights (1170 clocks) is longer than the products of the other row
+// tile (384).  D = 256: 1 x 8192 1140 us = 965, one row tile, whose keys come
+// from L2 twice as often.
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
 // frees its tensor memory and leaves its rows unwritten.
@@ -47,8 +61,6 @@
 namespace kvq {
 namespace {
 
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 256;
 constexpr float kMaxSum = 16777216.0f;            // 2^24: weights against a reference this far behind are still finite
 constexpr int kSlots = 2;                         // work items known at once
 
@@ -60,11 +72,15 @@ struct Shape {
   static constexpr int kCheckWarp = kProductWarp + kProductWarps, kCheckWarps = 3 - kTiles;
   static constexpr int kWarps = kCheckWarp + kCheckWarps;
   static constexpr int kThreads = 32 * kWarps;
-  // (two row tiles: 168 registers a thread at launch, split by role)
-  static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-  static_assert(kTiles == 1 || 32 * kSoftmaxWarps * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+  // One row tile leaves room for a second CTA on the SM (but for D = 256).
+  static constexpr int kCtas = kTiles == 1 && D <= 128 ? 2 : 1;
+  static constexpr uint32_t kTmemCols = 512 / kCtas, kSCol = kTmemCols / 2;
+  // the registers of a thread at launch, split by role
+  static constexpr bool kSplitRegs = D <= 128;
+  static constexpr int kRegs = kCtas == 2 ? 128 : 168, kSoftmaxRegs = kCtas == 2 ? 168 : 208, kOtherRegs = 88;
+  static_assert(!kSplitRegs || 32 * kSoftmaxWarps * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
-  static constexpr int kStages = D == 256 ? 2 : 4;           // tiles of K, of V
+  static constexpr int kStages = D == 256 || (D == 128 && kCtas == 2) ? 2 : 4;           // tiles of K, of V
   static constexpr uint32_t kQBlock = 128 * 128;             // 64 dimensions of a row tile
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKBlock = kKeys * 128;           // 64 dimensions of a key tile
@@ -73,10 +89,11 @@ struct Shape {
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   static constexpr uint32_t kOut = kV + kStages * kTileBytes;          // 4 KB of output rows per softmax warp
   static constexpr uint32_t kMisc = kOut + kSoftmaxWarps * 4096;
-  // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
-  static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
-  static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kTiles * D <= 256 && kSCol + 4 * kKeys <= kTmemCols, "tensor memory");
+  // The tiles begin on a 1024-byte boundary; 512 bytes of barriers take what is left before or behind them.
+  // At least 116 KB where a second CTA, which would wait for tensor memory, must not share the SM.
+  static constexpr uint32_t kSmem = kCtas == 2 || kMisc + 1024 > 116 * 1024 ? kMisc + 1024 : 116 * 1024;
+  static_assert(kSmem <= 232448 && kCtas * (kSmem + 1024) <= 233472, "shared memory of an SM's CTAs");
+  static_assert(kTiles * D <= kSCol && 2 * kTiles * kKeys <= kTmemCols - kSCol, "tensor memory");
 };
 
 // What a CTA works on at a time: kTiles tiles of query rows of a sequence and
@@ -199,17 +216,19 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[kCount]) {
 }
 // kCached: over the e4m3 cache's gathered entries.
 template <int D, int kTiles, bool kCached>
-__global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::kCtas)
     prompt_attention_kernel(const PromptAttentionArgs a, const __grid_constant__ CUtensorMap qmap,
                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<D, kTiles>;
   constexpr int kKeys = S::kKeys;
+  constexpr uint32_t kTmemCols = S::kTmemCols, kSCol = S::kSCol;
   wait_for_previous();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
-  const uint32_t bar = base + S::kMisc;
+  const bool before = smem - smem_raw >= 512;
+  const uint32_t bar = before ? smem_u32(smem_raw) : base + S::kMisc;
   const uint32_t k_full = bar, k_empty = k_full + 8 * S::kStages, v_full = k_empty + 8 * S::kStages;     // [kStages]
   const uint32_t v_good = v_full + 8 * S::kStages, v_empty = v_good + 8 * S::kStages;
   // [score buffer]: scores there, weights there, their product done
@@ -218,7 +237,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   const uint32_t item_full = drain + 16, item_free = item_full + 8 * kSlots;    // [kSlots]
   const uint32_t q_full = item_free + 8 * kSlots, q_free = q_full + 8, answered = q_free + 8;
   const uint32_t answer = (answered + 8 + 15) & ~15u;                           // of the request for a next item
-  uint8_t* words = smem + S::kMisc + (answer + 16 - bar);
+  uint8_t* words = (before ? smem_raw : smem + S::kMisc) + (answer + 16 - bar);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(words);
   volatile int* s_abort = reinterpret_cast<volatile int*>(words + 4);
   volatile Item* items = reinterpret_cast<volatile Item*>(words + 8);
@@ -310,7 +329,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
   Item it;
   if (warp < S::kSoftmaxWarps) {
     // ---- softmax: thread = query row ----------------------------------------
-    if constexpr (kTiles == 2) more_registers<S::kSoftmaxRegs>();
+    if constexpr (S::kSplitRegs) more_registers<S::kSoftmaxRegs>();
     const int tile = warp >> 2;
     const uint32_t lanes = (warp & 3) * 32u << 16;
     const uint32_t o_col = tmem + lanes + tile * D;
@@ -502,7 +521,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, 1)
         a.lse[token * a.lse_stride_t + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   } else {
-    if constexpr (kTiles == 2) fewer_registers<S::kOtherRegs>();
+    if constexpr (S::kSplitRegs) fewer_registers<S::kOtherRegs>();
     const uint32_t elected = elect_lane();
     if (warp == S::kCopyWarp) {
       // ---- items, and the copies of K and V ------------------------------------
