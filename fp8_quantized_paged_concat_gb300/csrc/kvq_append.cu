@@ -23,7 +23,10 @@
 // under way at once; a pair's other half, rot/16 lanes on, comes by shuffles of
 // the raw bf16 values.  The queries are other CTAs' work in the same launch: up
 // to 8 heads of a token per lane group, which share the token's row of the
-// table.
+// table.  Measured (32 query heads, 8 key heads of 128): 4 x 4096 tokens, 411
+// MB, into pages of 32 70 us = 5.9 TB/s, of 64 75 us = 5.5; 128 decoded tokens
+// 3.3 us and one 2.4 in a graph, of which the launch and three dependent loads
+// (the request, its page, the scale) are most.
 #include <algorithm>
 
 #include "kvq_dependent.cuh"
@@ -307,7 +310,8 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int64_t toke
 
 // kWarps: warps of a page, side and head.
 template <int kLanes, int kWarps, int kHeld, int kHeads, bool kInterleaved>
-__global__ void __launch_bounds__(threads_of(kWarps), kWarps == 8 ? 3 : 6) append_kernel(const AppendArgs a, uint32_t page_ctas, uint32_t units) {
+__global__ void __launch_bounds__(threads_of(kWarps), kWarps == 8 ? 3 : kWarps == 4 && kHeld == 2 ? 8 : 6)
+    append_kernel(const AppendArgs a, uint32_t page_ctas, uint32_t units) {
   wait_for_previous();
   allow_dependents();
   constexpr int kThreads = threads_of(kWarps);
@@ -347,13 +351,23 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
 
 template <int kLanes>
 cudaError_t launch_size(const AppendArgs& a, int num_sms, cudaStream_t stream) {
-  // as many warps as hold a page's new tokens between the two looks at them
+  // As many warps as hold a page's new tokens between the two looks at them, and
+  // no more (us at D = 128, 8 key heads, 32 query heads; 1 warp x 1 token a lane,
+  // 1 x 4, 4 x 2, 4 x 4, 8 x 4): 128 requests x 1 token 3.3, 4.9, -, 8.4, 14; 128 x
+  // 4 tokens 5.5, 5.7, 8.9, 11, 19; pages of 16: 32 x 16 tokens 9.1, 9.4, 5.8, 6.3,
+  // 9.0, 4 x 4096 82, 80, 78, 87, 140; pages of 32: 32 x 32 17, 16, -, 8.4, 10, 4 x
+  // 4096 95, 83, 78, 70, 96; pages of 64: 16 x 64 33, 27, 11, 10, 8.0, 16 x 500 70,
+  // 60, 41, 40, 38, 4 x 4096 116, 101, 74, 73, 75.
   const int64_t tokens = std::min<int64_t>(a.max_query_len, a.block_size);
   constexpr int kAtOnce = 32 / kLanes;
+  // Query heads of a lane group: eight where the call has the lanes for it (256
+  // tokens x 32 heads 4.8 us, one head each 5.2; 180 tokens 4.0 / 4.3; 128 tokens
+  // 3.9 / 3.3; 4 x 4096 70 / 119).
   const int64_t chunks = (a.num_heads + kManyHeads - 1) / kManyHeads;
-  const bool many = a.num_tokens * chunks * kLanes >= static_cast<int64_t>(num_sms) * 128;
+  const bool many = a.num_tokens * chunks * kLanes >= static_cast<int64_t>(num_sms) * 64;
   if (tokens <= kAtOnce) return many ? launch<kLanes, 1, 1, kManyHeads>(a, stream) : launch<kLanes, 1, 1, 1>(a, stream);
   if (tokens <= 4 * kAtOnce) return many ? launch<kLanes, 1, 4, kManyHeads>(a, stream) : launch<kLanes, 1, 4, 1>(a, stream);
+  if (tokens <= 8 * kAtOnce) return many ? launch<kLanes, 4, 2, kManyHeads>(a, stream) : launch<kLanes, 4, 2, 1>(a, stream);
   if (tokens <= 16 * kAtOnce) return many ? launch<kLanes, 4, 4, kManyHeads>(a, stream) : launch<kLanes, 4, 4, 1>(a, stream);
   return launch<kLanes, 8, 4, kManyHeads>(a, stream);
 }

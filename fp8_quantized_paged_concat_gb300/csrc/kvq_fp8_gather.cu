@@ -6,8 +6,10 @@
 //
 // Bound: HBM (a byte read and two written for each value).  One warp takes 32
 // rows and every fourth (head, side): lane l looks up row l's page once; then
-// D / 16 lanes take a row, 16 values each, every row's load of a (head, side)
-// under way at once.
+// D / 16 lanes take a row, twice 8 values each, so that loads and stores of a
+// warp fill whole sectors (16 neighbouring values to a lane: 38 us for the 27
+// below), every row's load of a (head, side) under way at once.  Measured: 24139
+// entries of 8 heads of 128, 148 MB: 27 us = 5.5 TB/s.
 #include "kvq_fp8_gather.cuh"
 #include "kvq_per_head_attention.cuh"
 
