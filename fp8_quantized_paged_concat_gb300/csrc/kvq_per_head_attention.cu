@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(Stage<D, kFp8>::kThreads, Stage<D, kFp8>::ctas
 #pragma unroll
     for (int nt = 0; nt < kRowTiles; ++nt) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
 
-  uint32_t v_ref = 0;                            // e4m3: o counts in units of the scale with this byte (0: none yet)
+  uint32_t v_ref = 0, v_top = 0;                 // e4m3: o counts in units of the scale with this byte (0: none yet); the largest
   const uint32_t rg = key_row(g), r0 = key_row(2 * c), r1 = key_row(2 * c + 1);
   int stage = 0;
   for (int32_t step = first; step < s1; step += kWarps) {
@@ -462,15 +462,13 @@ __global__ void __launch_bounds__(Stage<D, kFp8>::kThreads, Stage<D, kFp8>::ctas
     }
     // e4m3: the scales of the thread's four keys.  A key's scale multiplies its
     // scores; a value's multiplies its weight, relative to a reference v_ref in
-    // whose units o counts, so that f16 weights keep their precision: the
-    // reference follows the step's largest scale once that is above it, or more
-    // than 2^6 below.
+    // whose units o counts.
     float kf[4], vf[4];
     if constexpr (kFp8) {
-      const uint32_t top = __reduce_max_sync(kFull, page_scales >> 8);
-      if (top > v_ref || (top != 0 && top + 6 < v_ref)) {
-        const float f = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - top) << 23);
-        v_ref = top;
+      const uint32_t ref = next_scale_ref(v_ref, __reduce_max_sync(kFull, page_scales >> 8), v_top);
+      if (ref != v_ref) {
+        const float f = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ref) << 23);
+        v_ref = ref;
 #pragma unroll
         for (int t = 0; t < kDimTiles; ++t)
 #pragma unroll

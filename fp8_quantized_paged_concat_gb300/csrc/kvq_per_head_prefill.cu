@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
     }
     bool fresh = true;                              // some row has no reference yet (uniform over the warp)
-    uint32_t v_ref = 0;                             // e4m3: O counts in units of the scale with this byte (0: none yet)
+    uint32_t v_ref = 0, v_top = 0;                  // e4m3: O counts in units of the scale with this byte (0: none yet); the largest
     for (int32_t t = 0; t < n_tiles; ++t) {
       const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
@@ -658,17 +658,17 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       // which of the tile's keys the row sees
       const uint2 valid = lds64(smem_u32(valid_ring) + (kFp8 ? 16 : 8) * (t % kValidRing));
       // e4m3: the tile's scales go into its scores, and into its weights relative to
-      // that in whose units O counts, which follows them once they are above it, or
-      // more than 2^6 below (f16 weights keep their precision)
+      // that in whose units O counts
       float sc = row_sc, shift = 0.0f, back = 1.0f, unit = 1.0f;
       if constexpr (kFp8) {
         const uint2 scales = lds64(smem_u32(valid_ring) + 16 * (t % kValidRing) + 8);
         const uint32_t ek = __shfl_sync(kFull, scales.x, 0), ev = __shfl_sync(kFull, scales.y, 0);
         sc = row_sc * __uint_as_float((ek == 0 ? 127 : ek) << 23);
         if (ev != 0) {
-          if (ev > v_ref || ev + 6 < v_ref) {
-            unit = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ev) << 23);
-            v_ref = ev;
+          const uint32_t ref = next_scale_ref(v_ref, ev, v_top);
+          if (ref != v_ref) {
+            unit = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ref) << 23);
+            v_ref = ref;
           }
           shift = static_cast<float>(static_cast<int>(ev - v_ref));
           back = __uint_as_float((127 + v_ref - ev) << 23);

@@ -829,7 +829,8 @@ kvq_status kvq_rope_append_fp8_per_head(
  * down to 2^-28 of its largest value; a key's scale multiplies its scores, a
  * value's its weight, both relative (by powers of two) to the largest among
  * the keys processed together, which is exact for values but for those 2^15
- * and more below it; the weights are rounded to f16 (relative 2^-11).
+ * and more below it, and 2^80 and more below the largest that came before; the
+ * weights are rounded to f16 (relative 2^-11).
  */
 kvq_status kvq_window_attention_fp8_per_head(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,

@@ -367,6 +367,24 @@ def test_scales_at_and_past_the_ends(kvq, new, splits):
     check(attend(kvq, b.device(), splits, window=50), b.want(window=50, gathered=gathered))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,splits", [(1, None), (1, 1), (3, -2), (70, 1), (70, None), (70, "gather")])
+def test_the_largest_scale_before_the_least(kvq, dim, new, splits):
+    """Pages of huge values before pages of zeros, whose scale is the least: sums stay finite, either way round."""
+    b = Batch([(600, new), (700, new)], 4, 1, dim, 16, "NHD", 87)
+    b.cache.scales[:, 0] = 127 - 9
+    codes = b.cache.codes.copy()
+    for order in (1, -1):
+        b.cache.codes[:] = codes
+        for r, n in enumerate(b.lens):
+            used = b.table[r][:-(-n // 16)][::order]
+            b.cache.scales[used, 1] = np.where(np.arange(len(used)) < len(used) // 2, 187, 67)[:, None]
+            b.cache.codes[used[len(used) // 2:], 1] = 0
+        want = b.want(gathered=splits == "gather")
+        assert np.abs(want[0]).max() > 2.0 ** 60
+        check(attend(kvq, b.device(), splits), want)
+
+
 @pytest.mark.parametrize("new", [1, 130])
 @pytest.mark.parametrize("splits", [1, 5, -5, "gather"])
 def test_padded_requests_see_nothing_and_other_rows_are_left(kvq, new, splits):
