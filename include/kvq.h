@@ -883,6 +883,8 @@ int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_head
  * may be left untouched too), as are rows of no sequence, which may hold
  * anything.  NaN and infinities in a key or value have no effect on queries
  * that do not see it; in a visible value they come through or read as zero.
+ * Values of magnitudes up to 2^78 give finite sums whatever the scores (larger
+ * ones may overflow where the result would not).
  * Arithmetic: products on the tensor cores (bf16, fp32 sums); the softmax in
  * fp32; the weights rounded to bf16 (relative 2^-8) for the weighted sum,
  * their sum taken before; out rounded once to bf16.  Waits of the kernel's

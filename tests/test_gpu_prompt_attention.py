@@ -133,6 +133,19 @@ def test_strides_scales_and_no_lse(kvq):
         check(p.run(kvq), p.want())
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** 78, 2.0 ** -60])
+def test_values_far_from_one(kvq, dim, size):
+    """Sums over large values stay finite behind a reference that is far off; small ones keep their precision."""
+    p = Prompts([600, 130], 4, 2, dim, 45)
+    ramp = np.linspace(0.05, 12.0, p.qkv.shape[0])[:, None, None]
+    k, v = slice(*p.split), slice(p.split[1], None)
+    p.qkv[:, k] = ref.to_bf16(ref.bf16(p.qkv[:, k]) * ramp)
+    p.qkv[:, v] = ref.to_bf16(np.clip(ref.bf16(p.qkv[:, v]), -1, 1) * size)
+    p.qkv[p.start[-1]:] = 0x7FC0
+    check_prompts(kvq, p)
+
+
 def test_bad_sequences_are_skipped(kvq):
     p = Prompts([60, 50, 70, 40], 4, 2, 128, 47)
     want = p.want()
