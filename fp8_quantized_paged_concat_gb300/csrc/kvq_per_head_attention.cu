@@ -472,28 +472,11 @@ __global__ void __launch_bounds__(Stage<D, kFp8>::kThreads, Stage<D, kFp8>::ctas
           }
         }
     }
-    // e4m3: the scales of the thread's four keys.  A key's scale multiplies its
-    // scores; a value's multiplies its weight, relative to a reference v_ref in
-    // whose units o counts.
-    float kf[4], vf[4];
+    // e4m3: the scales of the thread's four keys.  A key's scale multiplies its scores.
+    float kf[4];
     if constexpr (kFp8) {
-      const uint32_t ref = next_scale_ref(v_ref, __reduce_max_sync(kFull, page_scales >> 8), v_top);
-      if (ref != v_ref) {
-        const float f = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ref) << 23);
-        v_ref = ref;
 #pragma unroll
-        for (int t = 0; t < kDimTiles; ++t)
-#pragma unroll
-          for (int nt = 0; nt < kRowTiles; ++nt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[t][nt][x] *= f;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w = __shfl_sync(kFull, page_scales, 8 * e + rg);
-        kf[e] = __uint_as_float((w & 0xFF) << 23);
-        vf[e] = __uint_as_float((w >> 8) == 0 ? 0u : (127 + (w >> 8) - v_ref) << 23);
-      }
+      for (int e = 0; e < 4; ++e) kf[e] = __uint_as_float((__shfl_sync(kFull, page_scales, 8 * e + rg) & 0xFF) << 23);
     }
     // Weights against the reference m, the maximum of steps before: no
     // maximum of their own is taken unless their sum shows that one of them
@@ -555,113 +538,144 @@ __global__ void __launch_bounds__(Stage<D, kFp8>::kThreads, Stage<D, kFp8>::ctas
       }
       weights();
     }
-    uint32_t p[2][kRowTiles][2];                 // P^T, keys 2c, 2c + 1 and 8 on, of query row g
 #pragma unroll
     for (int nt = 0; nt < kRowTiles; ++nt) {
       l[nt][0] += sum[nt].x;
       l[nt][1] += sum[nt].y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = kFp8 ? fmul2(w[nt][e], make_float2(vf[e], vf[e])) : w[nt][e];
-        p[e >> 1][nt][e & 1] = transpose8(pack_f16x2(x.x, x.y));
-      }
     }
-
-    // ---- O^T += V^T P^T ----------------------------------------------------
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      // keys 2c and 2c + 1 (rows x0, x1) and the two 8 keys on (y0, y1)
-      const uint32_t x0 = 16 * mt + r0, x1 = 16 * mt + r1, y0 = x0 + 8, y1 = x1 + 8;
+    // e4m3: a value's scale multiplies its weight, relative to a reference v_ref
+    // in whose units o counts.  Values whose scales are within 2^8 of the largest
+    // go first, then the largest of the others, and so on: a value keeps its
+    // precision beside much larger ones, which its row need not see.
+    uint32_t left = kFp8 ? page_scales >> 8 : 0; // the lane's key's scale, while it is to come
+    do {
+      float vf[4];
       if constexpr (kFp8) {
-        const uint32_t vd = st + St::kV;
+        const uint32_t top = __reduce_max_sync(kFull, left), ref = next_scale_ref(v_ref, top, v_top);
+        if (ref != v_ref) {
+          const float f = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ref) << 23);
+          v_ref = ref;
 #pragma unroll
-        for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {  // 16 of the lane's dimensions (8 at D = 64)
-          uint32_t w[4][4];
-          auto load = [&](uint32_t row, uint32_t (&d)[4]) {
-            const uint32_t at = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
-            const uint32_t from = vd + row * St::kRow + 16 * v_chunk<D, true>(row, at);
-            if constexpr (D == 64) {
-              const uint2 x = lds64(from + 8 * (g & 1));
-              d[0] = x.x;
-              d[1] = x.y;
-            } else {
-              const uint4 x = ld_shared16(from);
-              d[0] = x.x;
-              d[1] = x.y;
-              d[2] = x.z;
-              d[3] = x.w;
-            }
-          };
-          load(x0, w[0]);
-          load(x1, w[1]);
-          load(y0, w[2]);
-          load(y1, w[3]);
-          constexpr int kWords = D == 64 ? 2 : 4;
-          if (!all) {                            // else no entry of the step is hidden from any row
+          for (int t = 0; t < kDimTiles; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int nt = 0; nt < kRowTiles; ++nt)
 #pragma unroll
-              for (int j = 0; j < kWords; ++j) w[k][j] = finite_codes(w[k][j]);
-          }
-#pragma unroll
-          for (int j = 0; j < kWords; ++j)       // 4 dimensions
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {        // dimensions 2 e and 2 e + 1 of the four, a pair of keys each
-              const uint32_t x = prmt(w[0][j], w[1][j], e ? 0x7362 : 0x5140);
-              const uint32_t y = prmt(w[2][j], w[3][j], e ? 0x7362 : 0x5140);
-              const uint32_t a0 = bits(e4m3x2_to_half2(x)), a1 = bits(e4m3x2_to_half2(x >> 16));
-              const uint32_t a2 = bits(e4m3x2_to_half2(y)), a3 = bits(e4m3x2_to_half2(y >> 16));
-              const int t = 8 * i + 2 * j + e;
-#pragma unroll
-              for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
-            }
+              for (int x = 0; x < 4; ++x) o[t][nt][x] *= f;
         }
-      } else {
-        const uint32_t vs = st + St::kVs, vd = st + St::kV;
+        const uint32_t now = left + 8 >= top ? left : 0;
+        left -= now;
 #pragma unroll
-        for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {    // one scale group (16 dimensions; 8 at D = 64) at a time
-          const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
-          uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
-          uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
-          if (!all) {                              // else no entry of the step is hidden from any row
-            sx = finite_scales(sx);
-            sy = finite_scales(sy);
-          }
-          uint32_t w[4][2];
-          auto load = [&](uint32_t row, uint32_t (&d)[2]) {
-            if constexpr (D == 64) {
-              d[0] = lds32(vd + row * St::kRow + 4 * g);
-            } else {
-              const uint32_t at = D == 128 ? 8 * g : 16 * g + 8 * i;
-              const uint2 x = lds64(vd + row * St::kRow + 16 * v_chunk<D, false>(row, at >> 4) + (at & 8));
-              d[0] = x.x;
-              d[1] = x.y;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = __shfl_sync(kFull, now, 8 * e + rg);
+          vf[e] = __uint_as_float(w == 0 ? 0u : (127 + w - v_ref) << 23);
+        }
+      }
+      uint32_t p[2][kRowTiles][2];                 // P^T, keys 2c, 2c + 1 and 8 on, of query row g
+#pragma unroll
+      for (int nt = 0; nt < kRowTiles; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = kFp8 ? fmul2(w[nt][e], make_float2(vf[e], vf[e])) : w[nt][e];
+          p[e >> 1][nt][e & 1] = transpose8(pack_f16x2(x.x, x.y));
+        }
+      }
+
+      // ---- O^T += V^T P^T ----------------------------------------------------
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        // keys 2c and 2c + 1 (rows x0, x1) and the two 8 keys on (y0, y1)
+        const uint32_t x0 = 16 * mt + r0, x1 = 16 * mt + r1, y0 = x0 + 8, y1 = x1 + 8;
+        if constexpr (kFp8) {
+          const uint32_t vd = st + St::kV;
+#pragma unroll
+          for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {  // 16 of the lane's dimensions (8 at D = 64)
+            uint32_t w[4][4];
+            auto load = [&](uint32_t row, uint32_t (&d)[4]) {
+              const uint32_t at = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
+              const uint32_t from = vd + row * St::kRow + 16 * v_chunk<D, true>(row, at);
+              if constexpr (D == 64) {
+                const uint2 x = lds64(from + 8 * (g & 1));
+                d[0] = x.x;
+                d[1] = x.y;
+              } else {
+                const uint4 x = ld_shared16(from);
+                d[0] = x.x;
+                d[1] = x.y;
+                d[2] = x.z;
+                d[3] = x.w;
+              }
+            };
+            load(x0, w[0]);
+            load(x1, w[1]);
+            load(y0, w[2]);
+            load(y1, w[3]);
+            constexpr int kWords = D == 64 ? 2 : 4;
+            if (!all) {                            // else no entry of the step is hidden from any row
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) w[k][j] = finite_codes(w[k][j]);
             }
-          };
-          load(x0, w[0]);
-          load(x1, w[1]);
-          load(y0, w[2]);
-          load(y1, w[3]);
 #pragma unroll
-          for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {   // 8 dimensions
-            // bytes holding (first key's, second key's) codes of the even and odd dimensions
-            constexpr uint32_t kLow = 0x0F0F0F0Fu;
-            uint32_t ex[4], od[4], ey[4], oy[4];
-            e2m1x8((w[0][j] & kLow) | ((w[1][j] << 4) & ~kLow), ex);
-            e2m1x8(((w[0][j] >> 4) & kLow) | (w[1][j] & ~kLow), od);
-            e2m1x8((w[2][j] & kLow) | ((w[3][j] << 4) & ~kLow), ey);
-            e2m1x8(((w[2][j] >> 4) & kLow) | (w[3][j] & ~kLow), oy);
+            for (int j = 0; j < kWords; ++j)       // 4 dimensions
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {          // dimensions 2 e and 2 e + 1 of the eight
-              const uint32_t a0 = hmul2(ex[e], sx), a1 = hmul2(od[e], sx), a2 = hmul2(ey[e], sy), a3 = hmul2(oy[e], sy);
-              const int t = (D == 64 ? 0 : 8 * i + 4 * j) + e;
+              for (int e = 0; e < 2; ++e) {        // dimensions 2 e and 2 e + 1 of the four, a pair of keys each
+                const uint32_t x = prmt(w[0][j], w[1][j], e ? 0x7362 : 0x5140);
+                const uint32_t y = prmt(w[2][j], w[3][j], e ? 0x7362 : 0x5140);
+                const uint32_t a0 = bits(e4m3x2_to_half2(x)), a1 = bits(e4m3x2_to_half2(x >> 16));
+                const uint32_t a2 = bits(e4m3x2_to_half2(y)), a3 = bits(e4m3x2_to_half2(y >> 16));
+                const int t = 8 * i + 2 * j + e;
 #pragma unroll
-              for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+                for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+              }
+          }
+        } else {
+          const uint32_t vs = st + St::kVs, vd = st + St::kV;
+#pragma unroll
+          for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {    // one scale group (16 dimensions; 8 at D = 64) at a time
+            const uint32_t so = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + i;
+            uint32_t sx = bits(e4m3x2_to_half2(lds8(vs + x0 * St::kScales + so) | lds8(vs + x1 * St::kScales + so) << 8));
+            uint32_t sy = bits(e4m3x2_to_half2(lds8(vs + y0 * St::kScales + so) | lds8(vs + y1 * St::kScales + so) << 8));
+            if (!all) {                              // else no entry of the step is hidden from any row
+              sx = finite_scales(sx);
+              sy = finite_scales(sy);
+            }
+            uint32_t w[4][2];
+            auto load = [&](uint32_t row, uint32_t (&d)[2]) {
+              if constexpr (D == 64) {
+                d[0] = lds32(vd + row * St::kRow + 4 * g);
+              } else {
+                const uint32_t at = D == 128 ? 8 * g : 16 * g + 8 * i;
+                const uint2 x = lds64(vd + row * St::kRow + 16 * v_chunk<D, false>(row, at >> 4) + (at & 8));
+                d[0] = x.x;
+                d[1] = x.y;
+              }
+            };
+            load(x0, w[0]);
+            load(x1, w[1]);
+            load(y0, w[2]);
+            load(y1, w[3]);
+#pragma unroll
+            for (int j = 0; j < (D == 64 ? 1 : 2); ++j) {   // 8 dimensions
+              // bytes holding (first key's, second key's) codes of the even and odd dimensions
+              constexpr uint32_t kLow = 0x0F0F0F0Fu;
+              uint32_t ex[4], od[4], ey[4], oy[4];
+              e2m1x8((w[0][j] & kLow) | ((w[1][j] << 4) & ~kLow), ex);
+              e2m1x8(((w[0][j] >> 4) & kLow) | (w[1][j] & ~kLow), od);
+              e2m1x8((w[2][j] & kLow) | ((w[3][j] << 4) & ~kLow), ey);
+              e2m1x8(((w[2][j] >> 4) & kLow) | (w[3][j] & ~kLow), oy);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {          // dimensions 2 e and 2 e + 1 of the eight
+                const uint32_t a0 = hmul2(ex[e], sx), a1 = hmul2(od[e], sx), a2 = hmul2(ey[e], sy), a3 = hmul2(oy[e], sy);
+                const int t = (D == 64 ? 0 : 8 * i + 4 * j) + e;
+#pragma unroll
+                for (int nt = 0; nt < kRowTiles; ++nt) mma_f16(o[t][nt], a0, a1, a2, a3, p[mt][nt][0], p[mt][nt][1]);
+              }
             }
           }
         }
       }
-    }
+    } while (kFp8 && __any_sync(kFull, left != 0));
   }
   if (bad_index) report(a.status, KVQ_STATUS_BAD_INDEX);
 

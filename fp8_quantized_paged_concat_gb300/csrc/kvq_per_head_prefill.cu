@@ -43,12 +43,17 @@
 // for the kernel before, at the block's barrier, which every thread reaches,
 // and for tensor memory, which whoever holds it gives back without this CTA.)
 // Over the e4m3 cache (kFp8, window form): codes go from global memory through
-// registers into the f16 tiles, whose four stages take the raw entries' place;
-// a side's tile is relative to its largest page scale (produce_fp8).  4 requests
-// x 2048 new tokens behind up to 8192, 32 heads (8 key heads) of 128: 733 us =
-// 918 TFLOP/s, bound by the decoding, which is done again for every 256 rows;
-// calls that are given a workspace for it gather their entries once instead
-// (450 us).
+// registers into bf16 tiles, whose four stages take the raw entries' place,
+// their page's scale in them (produce_fp8); queries stay as they are, and the
+// weights are bf16 (2^-8, of an fp32 sum taken before), the type that the
+// product takes beside them.  (f16 tiles, relative to the largest of their page
+// scales, took 733 us for the 1111 below, but lost the keys and values beside
+// others 2^15 larger, which their rows need not see.)  4 requests x 2048 new
+// tokens behind up to 8192, 32 heads (8 key heads) of 128: 1111 us = 606
+// TFLOP/s, bound by the decoding warps' instructions, which are spent again for
+// every 256 rows; calls that are given a workspace for it gather their entries
+// once instead (450 us).  32 requests x 32 new tokens x 6000 keys, 128 rows a key
+// head: 199 us, as with f16.
 #include <type_traits>
 
 #include "kvq_per_head_attention.cuh"
@@ -326,13 +331,12 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
   if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
 }
 
-// The same for e4m3 entries.  A side's tile is decoded relative to its largest
-// page scale, 2^(top - 127): a row's values are multiplied by the power of two
-// between its page's and that, which is exact in f16 while they are less than
-// 2^15 apart; `top` itself goes into the scores, and the weights, of the tile.
+// The same for e4m3 entries, decoded into bf16, which holds them exactly with
+// their page's scale: so that no key's scale bears on another's values, not on
+// those of rows that do not see it either.
 //
 // Every warp looks up all of the tile's keys, lane l keys l and l + 32 (page
-// ids a tile before the loads that need them), and so knows `top`.  D / 16
+// ids a tile before the loads that need them).  D / 16
 // lanes take a row, 16 codes each, 512 / D rows at once: groups me, me +
 // kWarps, ... of that many rows are the warp's.  The codes of the next tile are
 // under way while one is decoded.  Eight lanes that store at once hold half a
@@ -363,8 +367,7 @@ __device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b
   // A tile's codes, on their way, and what is known of its keys.
   struct Tile {
     uint4 w[kPasses];
-    uint32_t scale[2];             // this side's scale bytes of keys lane, lane + 32
-    uint32_t other[2];             // key warps: the value side's
+    uint32_t scale[2];             // scale bytes of keys lane, lane + 32
     uint32_t there[2];             // which keys exist
   };
   auto start = [&](Tile& tile) {
@@ -377,11 +380,8 @@ __device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b
       const uint32_t id = ok ? next[h].id : 0;
       from[h] = reinterpret_cast<uint64_t>(at_offset(at_offset(side, id, 2 * a.region), ok ? next[h].row : 0, D));
       const uint8_t* scales = a.page_scales + static_cast<uint64_t>(id) * (2u * a.num_kv_heads) + head;
-      tile.scale[h] = tile.other[h] = 0;
-      if (ok) {
-        tile.scale[h] = load_global(scales + (kValues ? a.num_kv_heads : 0));
-        if constexpr (!kValues) tile.other[h] = load_global(scales + a.num_kv_heads);
-      }
+      tile.scale[h] = 0;
+      if (ok) tile.scale[h] = load_global(scales + (kValues ? a.num_kv_heads : 0));
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -407,37 +407,14 @@ __device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b
     look_up(t + 2);
     const int st = t % S::kStages;
     if (t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
-    // the scale bytes as they are read; a key that is not there counts for nothing
-    uint32_t e[2];
-    uint32_t top = 0, top_v = 0;
+    // What the softmax has to know of the tile.  A slot's last reader is done:
+    // with the tile kStages before gone from its buffer, the scores of the one
+    // before that, whose weights had to leave theirs two tiles before.
+    static_assert(S::kStages + 4 <= kValidRing, "mask slots");
+    if (!kValues && me == 0 && lane == 0) key_ring[t % kValidRing] = static_cast<uint64_t>(now.there[1]) << 32 | now.there[0];
+    float factor[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool ok = (now.there[h] >> lane) & 1;
-      e[h] = ok ? page_scale(now.scale[h]) : 0;
-      top = max(top, e[h]);
-      if constexpr (!kValues) top_v = max(top_v, ok ? page_scale(now.other[h]) : 0);
-    }
-    top = __reduce_max_sync(kFull, top);
-    if constexpr (!kValues) {
-      top_v = __reduce_max_sync(kFull, top_v);
-      // What the softmax has to know of the tile.  A slot's last reader is done:
-      // with the tile kStages before gone from its buffer, the scores of the one
-      // before that, whose weights had to leave theirs two tiles before.
-      static_assert(S::kStages + 4 <= kValidRing, "mask slots");
-      if (me == 0 && lane == 0) {
-        key_ring[2 * (t % kValidRing)] = static_cast<uint64_t>(now.there[1]) << 32 | now.there[0];
-        key_ring[2 * (t % kValidRing) + 1] = static_cast<uint64_t>(top_v) << 32 | top;
-      }
-    }
-    // (2^(e - top) in f16: from 2^-15 on a normal or the largest subnormals)
-    uint32_t factor[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int down = e[h] == 0 ? 0 : static_cast<int>(top - e[h]);
-      factor[h] = down <= 14 ? static_cast<uint32_t>(15 - down) << 10 : down <= 24 ? 0x400u >> (down - 14) : 0u;
-      factor[h] |= factor[h] << 16;
-    }
-    const bool one_scale = __all_sync(kFull, factor[0] == 0x3C003C00u && factor[1] == 0x3C003C00u);
+    for (int h = 0; h < 2; ++h) factor[h] = __uint_as_float(page_scale(now.scale[h]) << 23);
     const bool hidden = kValues && (s0 + t < full0 || s0 + t >= full1);   // from some row: no NaN may be left
     const uint32_t to = tiles + st * S::kTileBytes;
 #pragma unroll
@@ -450,15 +427,11 @@ __device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = finite_codes(w[j]);
       }
+      const float f = __shfl_sync(kFull, r0 < 32 ? factor[0] : factor[1], (r0 & 31) + sub);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[2 * j] = bits(e4m3x2_to_half2(w[j]));
-        h[2 * j + 1] = bits(e4m3x2_to_half2(w[j] >> 16));
-      }
-      if (!one_scale) {
-        const uint32_t f = __shfl_sync(kFull, r0 < 32 ? factor[0] : factor[1], (r0 & 31) + sub);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], f);
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = __half22float2(e4m3x2_to_half2(w[j >> 1] >> (16 * (j & 1))));
+        h[j] = pack_bf16x2(v.x * f, v.y * f);
       }
       const uint32_t at = to + (c >> 2) * kKBlock;
       st_shared16(at + sw128_offset(r, 2 * (c & 3)), make_uint4(h[0], h[1], h[2], h[3]));
@@ -518,10 +491,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
   const uint32_t drain = bar + 224, q_full = bar + 240;            // [2], 1
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kMisc + 248);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 252);
-  // [kValidRing][8]: bit per key of the tile; e4m3: [kValidRing][2]: these, and the tile's scale bytes
+  // [kValidRing][8]: bit per key of the tile
   uint8_t* valid_ring = smem + S::kMisc + 256;
   uint64_t* key_ring = reinterpret_cast<uint64_t*>(valid_ring);
-  static_assert(S::kStages <= 4 && 256 + 16 * kValidRing <= 512, "barrier layout");
+  static_assert(S::kStages <= 4 && 256 + 8 * kValidRing <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
   if (warp == 0) {
@@ -594,44 +567,47 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
     __syncwarp();
     // (eight pieces at a time: the decoding warps' copies keep a load waiting
     // for a hundred clocks)
-    uint32_t top = 0;                               // largest bits below the signs, of either half
+    float row_sc = a.scale_log2;                    // score -> base-2 exponent
+    if constexpr (!kFp8) {
+      uint32_t top = 0;                               // largest bits below the signs, of either half
 #pragma unroll 1
-    for (int c = 0; c < D / 8; c += 8) {
-      const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
-      uint4 x[8];
+      for (int c = 0; c < D / 8; c += 8) {
+        const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
+        uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
+        for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        constexpr uint32_t kAbs = 0x7FFF7FFFu;
-        top = __vimax3_u16x2(top, x[i].x & kAbs, x[i].y & kAbs);
-        top = __vimax3_u16x2(top, x[i].z & kAbs, x[i].w & kAbs);
-      }
-    }
-    const RowScale rs = row_scale(__uint_as_float(max(top << 16, top & 0xFFFF0000u)));
-#pragma unroll 1
-    for (int c = 0; c < D / 8; c += 8) {
-      const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
-      uint4 x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = fmul2(fmul2(make_float2(bf16_lo(w[j]), bf16_hi(w[j])), make_float2(rs.f[0], rs.f[0])),
-                                 make_float2(rs.f[1], rs.f[1]));
-          h[j] = pack_f16x2(v.x, v.y);
+        for (int i = 0; i < 8; ++i) {
+          constexpr uint32_t kAbs = 0x7FFF7FFFu;
+          top = __vimax3_u16x2(top, x[i].x & kAbs, x[i].y & kAbs);
+          top = __vimax3_u16x2(top, x[i].z & kAbs, x[i].w & kAbs);
         }
-        st_shared16(at + sw128_offset(lane, i), make_uint4(h[0], h[1], h[2], h[3]));
       }
+      const RowScale rs = row_scale(__uint_as_float(max(top << 16, top & 0xFFFF0000u)));
+#pragma unroll 1
+      for (int c = 0; c < D / 8; c += 8) {
+        const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = ld_shared16(at + sw128_offset(lane, i));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = fmul2(fmul2(make_float2(bf16_lo(w[j]), bf16_hi(w[j])), make_float2(rs.f[0], rs.f[0])),
+                                   make_float2(rs.f[1], rs.f[1]));
+            h[j] = pack_f16x2(v.x, v.y);
+          }
+          st_shared16(at + sw128_offset(lane, i), make_uint4(h[0], h[1], h[2], h[3]));
+        }
+      }
+      row_sc *= k_scale * rs.i[0] * rs.i[1];
     }
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
-    const float row_sc = a.scale_log2 * k_scale * rs.i[0] * rs.i[1];   // score -> base-2 exponent
 
     float m = has_row ? -INFINITY : 0.0f, l = 0.0f; // reference maximum, sum
     bool done = true;                               // every wait was met
@@ -650,7 +626,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       full1 = keys.sink_steps + (whole > 0 ? whole / kKeys : 0);
     }
     bool fresh = true;                              // some row has no reference yet (uniform over the warp)
-    uint32_t v_ref = 0, v_top = 0;                  // e4m3: O counts in units of the scale with this byte (0: none yet); the largest
     for (int32_t t = 0; t < n_tiles; ++t) {
       const int buf = 2 * tile + (t & 1);
       const uint32_t s_col = tmem + lanes + kSCol + kKeys * buf;
@@ -663,24 +638,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       tmem_ld64(s_col, s);
 
       // which of the tile's keys the row sees
-      const uint2 valid = lds64(smem_u32(valid_ring) + (kFp8 ? 16 : 8) * (t % kValidRing));
-      // e4m3: the tile's scales go into its scores, and into its weights relative to
-      // that in whose units O counts
-      float sc = row_sc, shift = 0.0f, back = 1.0f, unit = 1.0f;
-      if constexpr (kFp8) {
-        const uint2 scales = lds64(smem_u32(valid_ring) + 16 * (t % kValidRing) + 8);
-        const uint32_t ek = __shfl_sync(kFull, scales.x, 0), ev = __shfl_sync(kFull, scales.y, 0);
-        sc = row_sc * __uint_as_float((ek == 0 ? 127 : ek) << 23);
-        if (ev != 0) {
-          const uint32_t ref = next_scale_ref(v_ref, ev, v_top);
-          if (ref != v_ref) {
-            unit = v_ref == 0 ? 1.0f : __uint_as_float((127 + v_ref - ref) << 23);
-            v_ref = ref;
-          }
-          shift = static_cast<float>(static_cast<int>(ev - v_ref));
-          back = __uint_as_float((127 + v_ref - ev) << 23);
-        }
-      }
+      const uint2 valid = lds64(smem_u32(valid_ring) + 8 * (t % kValidRing));
       const bool masked = s0 + t < full0 || s0 + t >= full1 || (valid.x & valid.y) != kFull;
       uint32_t see[2] = {0, 0};
       if (masked && has_row) {
@@ -703,7 +661,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
         float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
-          float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(sc, sc),
+          float2 z = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(row_sc, row_sc),
                            make_float2(off, off));
           if constexpr (with_mask.value) {
             z.x = (see[i >> 5] >> (i & 31)) & 1 ? z.x : -INFINITY;
@@ -711,13 +669,13 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
           }
           const float2 w = make_float2(ex2(z.x), ex2(z.y));
           sums[(i >> 1) & 1] = fadd2(sums[(i >> 1) & 1], w);
-          p[i >> 1] = pack_f16x2(w.x, w.y);
+          p[i >> 1] = kFp8 ? pack_bf16x2(w.x, w.y) : pack_f16x2(w.x, w.y);
         }
         const float2 both = fadd2(sums[0], sums[1]);
-        sum = kFp8 ? (both.x + both.y) * back : both.x + both.y;
+        sum = both.x + both.y;
       };
       auto weights = [&]() {                        // warp-uniform choice
-        const float off = kShift - (m == -INFINITY ? 0.0f : m) + shift;
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
         if (masked)
           pass(off, std::true_type{});
         else
@@ -726,25 +684,21 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       // No weight is above 2^(kShift + kGrow) if their sum is not; a row whose
       // sum is takes a new reference, its tile's maximum (as in its first tile).
       if (!fresh) weights();
-      const bool grow = fresh || __any_sync(kFull, sum > kMaxWeight);
-      if (grow || (kFp8 && unit != 1.0f)) {
-        float alpha = 1.0f;
-        if (grow) {
-          float top = -INFINITY;
+      if (fresh || __any_sync(kFull, sum > kMaxWeight)) {
+        float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float z = __uint_as_float(s[i]) * sc;
-            if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
-          }
-          if (top > m) {
-            alpha = ex2(m - top);                   // 0 while m is -inf
-            m = top;
-          }
-          fresh = __any_sync(kFull, m == -INFINITY);
-          weights();
-          l *= alpha;
+        for (int i = 0; i < 64; ++i) {
+          const float z = __uint_as_float(s[i]) * row_sc;
+          if (!masked || ((see[i >> 5] >> (i & 31)) & 1)) top = fmaxf(top, z);
         }
-        alpha *= unit;
+        float alpha = 1.0f;
+        if (top > m) {
+          alpha = ex2(m - top);                     // 0 while m is -inf
+          m = top;
+        }
+        fresh = __any_sync(kFull, m == -INFINITY);
+        weights();
+        l *= alpha;
         if (t > 0) {
           // O is rescaled once the product of the tile before is done.  (The
           // barrier is waited on only here: the scores of tile t - 1 followed
@@ -772,7 +726,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * buf);
     }
-    const float v_scale = kFp8 ? __uint_as_float(v_ref << 23) : load_global(a.v_scale);
+    const float v_scale = kFp8 ? 1.0f : load_global(a.v_scale);
     // the last product is done: O is complete
     if (done && n_tiles > 0)
       done = warp_wait(o_done + 8 * (2 * tile + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, s_abort);
@@ -785,7 +739,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       // to a piece, through the shared memory of the warp's query rows, which
       // no product reads any more (each lane storing its own row touches 32
       // lines at a time: 2.2 us a CTA).
-      const float f = a.num_splits > 1 && !kFp8 ? inv : inv * v_scale;
+      const float f = a.num_splits > 1 ? inv : inv * v_scale;
       const uint32_t stage = bar - S::kMisc + tile * S::kQTile + (lanes >> 9);     // 32 rows of 128 bytes a warp
       const uint64_t mine =
           row >= rows ? 0
@@ -887,7 +841,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
                                 valid_ring, s_abort);
     } else if (warp == S::kScoreWarp) {
       // ---- S_w(t) = Q_w K(t)^T (one elected lane; the warp waits together) -----
-      constexpr uint32_t kIdesc = idesc_f16(128, kKeys, false);
+      constexpr uint32_t kIdesc = kFp8 ? idesc_bf16(128, kKeys, false) : idesc_f16(128, kKeys, false);
       set_up_done();
       const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
       const uint32_t elected = elect_lane();
@@ -920,7 +874,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
                                v_empty, valid_ring, s_abort);
     } else {
       // ---- O_w += P_w(t) V(t) ---------------------------------------------------
-      constexpr uint32_t kIdesc = idesc_f16(128, D, true);
+      constexpr uint32_t kIdesc = kFp8 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);
       set_up_done();
       const uint32_t tmem = __shfl_sync(kFull, *s_tmem, 0);
       const uint32_t elected = elect_lane();

@@ -823,14 +823,13 @@ kvq_status kvq_rope_append_fp8_per_head(
  * are not positive and below 2^38, they decode the entries in the attention,
  * once for every block of 256 rows.
  * Arithmetic: products on the tensor cores with fp32 sums, the softmax in
- * fp32, out rounded once to bf16.  Over gathered rows as in
- * kvq_prompt_attention, the weights rounded to bf16 (relative 2^-8).  Else codes
- * are exact in f16; a query row is scaled by a power of two into f16, exact
- * down to 2^-28 of its largest value; a key's scale multiplies its scores, a
- * value's its weight, both relative (by powers of two) to the largest among
- * the keys processed together, which is exact for values but for those 2^15
- * and more below it, and 2^80 and more below the largest that came before; the
- * weights are rounded to f16 (relative 2^-11).
+ * fp32, out rounded once to bf16.  Calls of many query rows (as above): entries
+ * with their scale are exact in bf16, queries stay as they are, and the weights
+ * are rounded to bf16 (relative 2^-8).  Few query rows: codes are exact in f16;
+ * a query row is scaled by a power of two into f16, exact down to 2^-28 of its
+ * largest value; a key's scale multiplies its scores, a value's its weight,
+ * which is rounded to f16 (relative 2^-11; values 2^80 and more below the
+ * largest of the call's others may be lost).
  */
 kvq_status kvq_window_attention_fp8_per_head(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,

@@ -158,13 +158,15 @@ def cached_attention(cache, q, start, lens, table, scale, window=0, sinks=0, gat
     """Attention over the cache.  Weights are f16 (2^-11), in units in which
     the largest is at least 2^6; what is below f16's normal range is off by
     2^-25 of them, times the reference scale, at most 2^6 above the largest of
-    a value's page.  Over gathered entries they are bf16 (2^-8), and queries
-    stay bf16."""
+    a value's page.  In calls of many rows per request and key head, and over
+    gathered entries, they are bf16 (2^-8), queries stay bf16, and nothing else
+    is rounded before the sums."""
     T, H, D = q.shape
     g = H // cache.heads
     out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
     tol_o, tol_l = np.zeros((T, H, D)), np.zeros((T, H))
     pages = cache.codes.shape[0]
+    gathered = gathered or max(np.diff(start), default=0) * g > {64: 48, 128: 32, 256: 24}[D]
     for b, length in enumerate(lens):
         t0, t1 = start[b], start[b + 1]
         n, length = t1 - t0, max(0, length)

@@ -385,6 +385,48 @@ def test_the_largest_scale_before_the_least(kvq, dim, new, splits):
         check(attend(kvq, b.device(), splits), want)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,splits", [(1, None), (1, 1), (70, 1), (70, "gather")])
+def test_subnormal_codes(kvq, dim, new, splits):
+    """Codes below e4m3's normal range alone, either zero among them."""
+    b = Batch([(200, new), (33, new)], 4, 2, dim, 16, "NHD", 85, exponents=(-3, 8))
+    b.cache.codes &= 0x87
+    b.scale = 4.0
+    check(attend(kvq, b.device(), splits), b.want(gathered=splits == "gather"))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,splits", [(4, None), (4, 1), (4, -3), (70, 1), (70, None), (70, -2), (70, "gather")])
+@pytest.mark.parametrize("block", [1, 16])
+def test_hidden_pages_of_any_scale_have_no_effect(kvq, dim, new, splits, block):
+    """Keys and values as large as the cache holds, where earlier tokens do not see them yet and later ones no longer do."""
+    b = Batch([(90, new), (33, new)], 4, 1, dim, block, "NHD", 89)
+    mask = dict(window=60, num_sinks=2)
+    clean = attend(kvq, b.device(), splits, **mask)
+    want = b.want(window=60, sinks=2, gathered=splits == "gather")
+    sees = np.ones(b.start[-1], bool)
+    for r, n in enumerate(b.lens):
+        first = n - new
+        cols = [(first - 60 + new // 2) // block - (block > 1)]       # no longer seen by about half of the new tokens
+        if block < new:
+            cols.append((n - 2) // block)                             # not seen yet by most of them
+        for col in cols:
+            if col * block < 2:                                       # (sinks stay visible)
+                continue
+            b.cache.scales[b.table[r][col]] = 187
+            for i in range(new):
+                if first + i - 60 < (col + 1) * block - 1 and col * block <= first + i:
+                    sees[b.start[r] + i] = False
+    assert sees.any() and not sees.all()
+    got = attend(kvq, b.device(), splits, **mask)
+    check((clean[0], clean[1]), want)
+    rows = np.flatnonzero(sees)
+    err = np.abs(ref.bf16(bits_of(got[0]))[rows] - want[0][rows])
+    assert np.all(err <= want[2][rows]), f"worst error / tolerance {np.max(err / want[2][rows])}"
+    le = np.abs(got[1].cpu().numpy().astype(np.float64)[rows] - want[1][rows])
+    assert np.all(le <= want[3][rows])
+
+
 @pytest.mark.parametrize("new", [1, 130])
 @pytest.mark.parametrize("splits", [1, 5, -5, "gather"])
 def test_padded_requests_see_nothing_and_other_rows_are_left(kvq, new, splits):
