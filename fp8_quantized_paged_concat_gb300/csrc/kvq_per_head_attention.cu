@@ -89,6 +89,20 @@ struct Stage {
   }
 };
 
+// Sums over the e4m3 cache's values count in units of a page scale, which
+// follows the scales: the reference that comes next, for keys whose largest
+// scale is `top` (stored bytes; 0: none), where `highest` is the largest so far.
+// It rises to any larger scale, and falls to one that is more than 2^6 below
+// (f16 weights keep their precision), but not to less than 2^-70 of the largest:
+// the sums, at most 2^50 in the units of the largest (2^14 for a weight, 2^9 for
+// a code, 2^27 keys), stay finite.  What is 2^80 and more below the largest may
+// be lost.
+__device__ __forceinline__ uint32_t next_scale_ref(uint32_t ref, uint32_t top, uint32_t& highest) {
+  if (top <= ref && (top == 0 || top + 6 >= ref)) return ref;
+  highest = max(highest, top);
+  return max(top, max(highest, 71u) - 70u);
+}
+
 // D += A B, A 16 x 16 (row), B 16 x 8 (col), f16 in, fp32 out.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {

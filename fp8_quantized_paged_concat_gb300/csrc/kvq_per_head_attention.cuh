@@ -110,20 +110,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(kFull, mbar_test_wait(bar, parity)) || warp_wait_or_abort(bar, parity, s_abort);
 }
 
-// Sums over the e4m3 cache's values count in units of a page scale, which
-// follows the scales: the reference that comes next, for keys whose largest
-// scale is `top` (stored bytes; 0: none), where `highest` is the largest so far.
-// It rises to any larger scale, and falls to one that is more than 2^6 below
-// (f16 weights keep their precision), but not to less than 2^-70 of the largest:
-// the sums, at most 2^50 in the units of the largest (2^14 for a weight, 2^9 for
-// a code, 2^27 keys), stay finite.  What is 2^80 and more below the largest may
-// be lost.
-__device__ __forceinline__ uint32_t next_scale_ref(uint32_t ref, uint32_t top, uint32_t& highest) {
-  if (top <= ref && (top == 0 || top + 6 >= ref)) return ref;
-  highest = max(highest, top);
-  return max(top, max(highest, 71u) - 70u);
-}
-
 // Bits i (0..31) with lo <= p0 + i <= hi.
 __device__ __forceinline__ uint32_t range_bits(int32_t p0, int32_t lo, int32_t hi) {
   const int32_t a = max(lo - p0, 0), b = min(hi - p0, 31);
