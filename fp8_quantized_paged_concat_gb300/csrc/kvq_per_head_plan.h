@@ -70,18 +70,17 @@ inline int64_t fp8_gather_bytes(int64_t rows, int64_t num_kv_heads, int64_t head
   return batch_size * rows * num_kv_heads * head_size * 4 + (batch_size * rows / 32 + 3 + 3) / 4 * 16;
 }
 // Whether a call's default is to gather: where every entry is read for many
-// blocks of rows, and these blocks fill enough of the GPU.  us of the attention
-// that decodes the entries (in its default ranges) and of gather and attention,
-// 8 key heads of 128: 32 requests x 6000 keys, 128 rows 225 / 366, 512 rows (512
-// blocks) 743 / 515, 1024 rows 1327 / 730; 8 x 6000 keys, 512 rows (128 blocks)
-// 213 / 145; 4 x 8000 keys, 256 rows 87 / 141, 512 rows (64 blocks) 146 / 143,
-// 1024 rows 260 / 147; 1 x 16000 keys, 512 rows 69 /
-// 197, 2048 rows (64 blocks) 232 / 209, 4096 rows 495 / 214.  (8 key heads of 64:
-// 4 x 8000 keys, 512 rows 86 / 107, 1024 rows 150 / 110; 4 of 256: 512 rows 155 /
-// 224, 1024 rows 282 / 227.)
+// blocks of rows, and these blocks about fill the GPU.  us of the attention that
+// decodes the entries (in its default ranges) and of gather and attention, 8 key
+// heads of 128: 32 requests x 6000 keys, 128 rows 232 / 366, 512 rows (512 blocks)
+// 548 / 515, 1024 rows 1006 / 732; 8 x 6000 keys, 512 rows (128 blocks) 146 / 145;
+// 4 x 8000 keys, 256 rows 74 / 141, 512 rows (64 blocks) 124 / 144, 1024 rows 193
+// / 149; 1 x 16000 keys, 512 rows 56 / 200, 2048 rows (64 blocks) 182 / 207, 4096
+// rows 391 / 215.  (8 key heads of 64: 4 x 8000 keys, 512 rows 85 / 107, 1024 rows
+// 122 / 110; 4 of 256: 512 rows 141 / 229, 1024 rows 233 / 230.)
 inline bool fp8_default_gathers(int64_t rows, int64_t groups, int sms) {
   const int64_t blocks = (rows + 255) / 256 * groups;
-  return (rows >= 512 && 4 * blocks >= 3 * int64_t{sms}) || (rows >= 1024 && 8 * blocks >= 3 * int64_t{sms});
+  return (rows >= 512 && blocks >= sms) || (rows >= 1024 && 4 * blocks >= 3 * int64_t{sms});
 }
 
 // The default key ranges per block of rows, whether they join through a

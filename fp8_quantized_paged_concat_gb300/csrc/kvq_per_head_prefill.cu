@@ -42,18 +42,18 @@
 // tensor memory and leaves its rows unwritten.  (The set-up waits otherwise:
 // for the kernel before, at the block's barrier, which every thread reaches,
 // and for tensor memory, which whoever holds it gives back without this CTA.)
-// Over the e4m3 cache (kFp8, window form): codes go from global memory through
-// registers into bf16 tiles, whose four stages take the raw entries' place,
-// their page's scale in them (produce_fp8); queries stay as they are, and the
-// weights are bf16 (2^-8, of an fp32 sum taken before), the type that the
-// product takes beside them.  (f16 tiles, relative to the largest of their page
-// scales, took 733 us for the 1111 below, but lost the keys and values beside
-// others 2^15 larger, which their rows need not see.)  4 requests x 2048 new
-// tokens behind up to 8192, 32 heads (8 key heads) of 128: 1111 us = 606
-// TFLOP/s, bound by the decoding warps' instructions, which are spent again for
-// every 256 rows; calls that are given a workspace for it gather their entries
-// once instead (450 us).  32 requests x 32 new tokens x 6000 keys, 128 rows a key
-// head: 199 us, as with f16.
+// Over the e4m3 cache (kFp8, window form): raw codes take the raw entries'
+// place, and are decoded into bf16 tiles with their page's scale in them
+// (produce_fp8); queries stay as they are, and the weights are bf16 (2^-8, of an
+// fp32 sum taken before), the type that the product takes beside them.  (f16
+// tiles, relative to the largest of their page scales, lost the keys and values
+// beside others 2^15 larger, which their rows need not see.)  4 requests x 2048
+// new tokens behind up to 8192, 32 heads (8 key heads) of 128: 832 us = 810
+// TFLOP/s, bound by the decoding warps, whose work is done again for every 256
+// rows (codes through registers a tile ahead: 1111; the loop over tiles unrolled
+// twice: 1461; one code for both sides, to spare instruction fetches: 861); calls that are given a workspace for it gather their
+// entries once instead (450 us).  32 requests x 32 new tokens x 6000 keys, 128 rows
+// a key head: 204 us.
 #include <type_traits>
 
 #include "kvq_per_head_attention.cuh"
@@ -90,21 +90,20 @@ struct Shape {
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
                     kThreads * kStartRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
-  static constexpr int kStages = D == 256 ? 2 : kFp8 ? 4 : 3;   // decoded tiles of K, of V
+  static constexpr int kStages = D == 256 ? 2 : kFp8 && (D == 64 || kTiles == 1) ? 4 : 3;   // decoded tiles of K, of V
   static constexpr uint32_t kTileBytes = kBlocks * kKBlock;
   static constexpr uint32_t kQTile = kBlocks * kBlockBytes;
   static constexpr uint32_t kK = kTiles * kQTile;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
   // raw entries of one side: rings of chunks of keys, data rows then scale rows
   static constexpr int kChunk = D == 256 ? 32 : 64;
-  [[maybe_unused]] static constexpr int kParts = kKeys / kChunk;   // chunks per tile
-  static constexpr int kRing = D == 256 ? 3 : 4;
+  static constexpr int kParts = kKeys / kChunk;              // chunks per tile
+  static constexpr int kRing = D == 256 ? (kFp8 ? 2 : 3) : 4;
   static constexpr uint32_t kRawScales = kChunk * (D / 2);
-  static constexpr uint32_t kRawBytes = kRawScales + kChunk * (D / 16);
+  static constexpr uint32_t kRawBytes = kFp8 ? kChunk * D : kRawScales + kChunk * (D / 16);
   static constexpr uint32_t kRawK = kV + kStages * kTileBytes;
   static constexpr uint32_t kRawV = kRawK + kRing * kRawBytes;
-  // (e4m3 codes go from global memory straight through registers)
-  static constexpr uint32_t kMisc = kFp8 ? kRawK : kRawV + kRing * kRawBytes;
+  static constexpr uint32_t kMisc = kRawV + kRing * kRawBytes;
   // at least 116 KB, so that a second CTA, which would wait for tensor memory, does not share the SM
   static constexpr uint32_t kSmem = kMisc + 512 + 1024 > 116 * 1024 ? kMisc + 512 + 1024 : 116 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -335,113 +334,130 @@ __device__ __forceinline__ void produce(const PerHeadAttentionArgs& a, int b, ui
 // their page's scale: so that no key's scale bears on another's values, not on
 // those of rows that do not see it either.
 //
-// Every warp looks up all of the tile's keys, lane l keys l and l + 32 (page
-// ids a tile before the loads that need them).  D / 16
-// lanes take a row, 16 codes each, 512 / D rows at once: groups me, me +
-// kWarps, ... of that many rows are the warp's.  The codes of the next tile are
-// under way while one is decoded.  Eight lanes that store at once hold half a
-// 64-dimension block of two neighbouring rows, which the swizzle keeps apart.
+// Every warp looks up all of a chunk's keys, lane l keys l and l + 32 (page ids
+// a chunk before the copies that need them).  D / 16 lanes take a row, 16 codes
+// each, 512 / D rows at once: groups me, me + kWarps, ... of that many rows are
+// the warp's, and a lane decodes what it copied itself.  Eight lanes that store
+// at once hold half a 64-dimension block of two neighbouring rows, which the
+// swizzle keeps apart.
 template <int D, int kTiles, bool kValues>
 __device__ __forceinline__ void produce_fp8(const PerHeadAttentionArgs& a, int b, uint32_t head, const Keys<kKeys>& keys,
                                             int32_t s0, int32_t n_tiles, int32_t full0, int32_t full1, int me, int lane,
                                             bool bad_index, uint32_t base, uint32_t full, uint32_t empty,
-                                            uint64_t* key_ring, volatile int* s_abort) {
+                                            uint32_t* key_ring, volatile int* s_abort) {
   using S = Shape<D, kTiles, true>;
   constexpr int kWarps = kValues ? S::kValueWarps : S::kKeyWarps;
-  constexpr int kAtOnce = 512 / D, kGroups = kKeys / kAtOnce, kPasses = (kGroups + kWarps - 1) / kWarps;
-  const uint32_t tiles = base + (kValues ? S::kV : S::kK);
+  constexpr int kAtOnce = 512 / D, kGroups = S::kChunk / kAtOnce, kPasses = (kGroups + kWarps - 1) / kWarps;
+  constexpr int kHalves = S::kChunk / 32, kRing = S::kRing;
+  const uint32_t tiles = base + (kValues ? S::kV : S::kK), raw = base + (kValues ? S::kRawV : S::kRawK) + 16 * lane;
   const uint32_t c = D == 64 ? lane & 3 : (lane & 3) + 4 * (D == 128 ? (lane >> 3) & 1 : lane >> 3);   // 16-code piece
   const uint32_t sub = D == 64 ? lane >> 2 : ((lane >> 2) & 1) + (D == 128 ? 2 * (lane >> 4) : 0);     // row of its group
   const uint8_t* side = a.cache + (kValues ? a.region : 0);
   const int32_t* table = a.block_table + b * a.block_table_stride;
   const uint32_t head_row = head * static_cast<uint32_t>(a.row_head);
-  LookUp next[2];
-  auto look_up = [&](int32_t t) {                   // keys lane, lane + 32 of tile t
+  const int32_t chunks = n_tiles * S::kParts;
+  LookUp next[kHalves];
+  auto look_up = [&](int32_t h) {
+    const int32_t step = s0 + h / S::kParts;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int32_t step = s0 + t;
-      const uint32_t p = static_cast<uint32_t>(keys.base(step)) + 32 * h + lane;
-      next[h] = look_up_position(a, table, head_row, t < n_tiles && p < static_cast<uint32_t>(keys.limit(step)), p);
+    for (int i = 0; i < kHalves; ++i) {
+      const uint32_t p = static_cast<uint32_t>(keys.base(step)) + (h % S::kParts) * S::kChunk + 32 * i + lane;
+      next[i] = look_up_position(a, table, head_row, h < chunks && p < static_cast<uint32_t>(keys.limit(step)), p);
     }
   };
-  // A tile's codes, on their way, and what is known of its keys.
-  struct Tile {
-    uint4 w[kPasses];
-    uint32_t scale[2];             // scale bytes of keys lane, lane + 32
-    uint32_t there[2];             // which keys exist
+  // What is known of a chunk whose codes are on their way: the scale bytes of
+  // keys lane, lane + 32, and which keys exist.
+  struct Chunk {
+    uint32_t scale[kHalves], there[kHalves];
   };
-  auto start = [&](Tile& tile) {
-    uint64_t from[2];
+  // one group of copies (empty past the last chunk)
+  auto start = [&](int32_t h, Chunk& chunk) {
+    uint64_t from[kHalves];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool ok = next[h].in && next[h].id >= 0 && next[h].id < a.num_pages;
-      bad_index = bad_index || (next[h].in && !ok);
-      tile.there[h] = __ballot_sync(kFull, ok);
-      const uint32_t id = ok ? next[h].id : 0;
-      from[h] = reinterpret_cast<uint64_t>(at_offset(at_offset(side, id, 2 * a.region), ok ? next[h].row : 0, D));
-      const uint8_t* scales = a.page_scales + static_cast<uint64_t>(id) * (2u * a.num_kv_heads) + head;
-      tile.scale[h] = 0;
-      if (ok) tile.scale[h] = load_global(scales + (kValues ? a.num_kv_heads : 0));
+    for (int i = 0; i < kHalves; ++i) {
+      const bool ok = next[i].in && next[i].id >= 0 && next[i].id < a.num_pages;
+      bad_index = bad_index || (next[i].in && !ok);
+      chunk.there[i] = __ballot_sync(kFull, ok);
+      const uint32_t id = ok ? next[i].id : 0;      // some page where there is none
+      from[i] = reinterpret_cast<uint64_t>(at_offset(at_offset(side, id, 2 * a.region), ok ? next[i].row : 0, D));
+      chunk.scale[i] = 0;
+      if (ok)
+        chunk.scale[i] = load_global(a.page_scales + static_cast<uint64_t>(id) * (2u * a.num_kv_heads) + head +
+                                     (kValues ? a.num_kv_heads : 0));
     }
+    if (h < chunks) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r0 = (me + kWarps * i) * kAtOnce;   // uniform over the warp
-      tile.w[i] = make_uint4(0, 0, 0, 0);
-      if (r0 >= kKeys) continue;
-      const int from_lane = (r0 & 31) + sub;
-      const uint64_t x = r0 < 32 ? from[0] : from[1];
-      const uint64_t row = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(x >> 32), from_lane)) << 32 |
-                           __shfl_sync(kFull, static_cast<uint32_t>(x), from_lane);
-      if (((r0 < 32 ? tile.there[0] : tile.there[1]) >> from_lane) & 1)
-        tile.w[i] = load_global(reinterpret_cast<const uint4*>(row) + c);
+      for (int i = 0; i < kPasses; ++i) {
+        const int group = me + kWarps * i, r0 = group * kAtOnce;      // uniform over the warp
+        if (group >= kGroups) continue;
+        const int half = kHalves == 2 && r0 >= 32 ? 1 : 0, from_lane = (r0 & 31) + sub;
+        const uint64_t x = half ? from[kHalves - 1] : from[0];
+        const uint64_t row = static_cast<uint64_t>(__shfl_sync(kFull, static_cast<uint32_t>(x >> 32), from_lane)) << 32 |
+                             __shfl_sync(kFull, static_cast<uint32_t>(x), from_lane);
+        const uint32_t there = half ? chunk.there[kHalves - 1] : chunk.there[0];
+        cp_async<16>(raw + (h % kRing) * S::kRawBytes + 512 * group, reinterpret_cast<const uint4*>(row) + c,
+                     (there >> from_lane) & 1 ? 16 : 0);
+      }
     }
+    cp_commit();
   };
+  Chunk ring[kRing - 1];
   look_up(0);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) {
+    start(i, ring[i]);
+    look_up(i + 1);
+  }
   set_up_done();
-  Tile now;
-  start(now);
-  look_up(1);
-  for (int32_t t = 0; t < n_tiles; ++t) {
-    Tile after;
-    start(after);                                   // (of nothing past the last tile)
-    look_up(t + 2);
+  for (int32_t h = 0; h < chunks; ++h) {
+    cp_wait<kRing - 2>();                           // the lane's own copies of chunk h are there
+    const Chunk now = ring[0];
+#pragma unroll
+    for (int i = 0; i + 2 < kRing; ++i) ring[i] = ring[i + 1];
+    start(h + kRing - 1, ring[kRing - 2]);
+    look_up(h + kRing);
+    const int32_t t = h / S::kParts, part = h % S::kParts;
     const int st = t % S::kStages;
-    if (t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
+    if (part == 0 && t >= S::kStages && !warp_wait(empty + 8 * st, (t / S::kStages - 1) & 1, s_abort)) break;
     // What the softmax has to know of the tile.  A slot's last reader is done:
     // with the tile kStages before gone from its buffer, the scores of the one
     // before that, whose weights had to leave theirs two tiles before.
     static_assert(S::kStages + 4 <= kValidRing, "mask slots");
-    if (!kValues && me == 0 && lane == 0) key_ring[t % kValidRing] = static_cast<uint64_t>(now.there[1]) << 32 | now.there[0];
-    float factor[2];
+    float factor[kHalves];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) factor[h] = __uint_as_float(page_scale(now.scale[h]) << 23);
+    for (int i = 0; i < kHalves; ++i) {
+      if (!kValues && me == 0 && lane == 0) key_ring[2 * (t % kValidRing) + part * kHalves + i] = now.there[i];
+      factor[i] = __uint_as_float(page_scale(now.scale[i]) << 23);
+    }
     const bool hidden = kValues && (s0 + t < full0 || s0 + t >= full1);   // from some row: no NaN may be left
     const uint32_t to = tiles + st * S::kTileBytes;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int r0 = (me + kWarps * i) * kAtOnce;
-      if (r0 >= kKeys) continue;
-      const uint32_t r = r0 + sub;
-      uint32_t w[4] = {now.w[i].x, now.w[i].y, now.w[i].z, now.w[i].w}, h[8];
+      const int group = me + kWarps * i, r0 = group * kAtOnce;
+      if (group >= kGroups) continue;
+      const uint4 x = ld_shared16(raw + (h % kRing) * S::kRawBytes + 512 * group);
+      uint32_t w[4] = {x.x, x.y, x.z, x.w}, y[8];
       if (hidden) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = finite_codes(w[j]);
       }
-      const float f = __shfl_sync(kFull, r0 < 32 ? factor[0] : factor[1], (r0 & 31) + sub);
+      const float f = __shfl_sync(kFull, kHalves == 2 && r0 >= 32 ? factor[kHalves - 1] : factor[0], (r0 & 31) + sub);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 v = __half22float2(e4m3x2_to_half2(w[j >> 1] >> (16 * (j & 1))));
-        h[j] = pack_bf16x2(v.x * f, v.y * f);
+        y[j] = pack_bf16x2(v.x * f, v.y * f);
       }
-      const uint32_t at = to + (c >> 2) * kKBlock;
-      st_shared16(at + sw128_offset(r, 2 * (c & 3)), make_uint4(h[0], h[1], h[2], h[3]));
-      st_shared16(at + sw128_offset(r, 2 * (c & 3) + 1), make_uint4(h[4], h[5], h[6], h[7]));
+      const uint32_t r = part * S::kChunk + r0 + sub, at = to + (c >> 2) * kKBlock;
+      st_shared16(at + sw128_offset(r, 2 * (c & 3)), make_uint4(y[0], y[1], y[2], y[3]));
+      st_shared16(at + sw128_offset(r, 2 * (c & 3) + 1), make_uint4(y[4], y[5], y[6], y[7]));
     }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + 8 * st);
-    now = after;
+    if (part == S::kParts - 1) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * st);
+    }
   }
+  cp_wait<0>();                                     // no copy outlives the CTA
   if (bad_index && !kValues) report(a.status, KVQ_STATUS_BAD_INDEX);
 }
 
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 252);
   // [kValidRing][8]: bit per key of the tile
   uint8_t* valid_ring = smem + S::kMisc + 256;
-  uint64_t* key_ring = reinterpret_cast<uint64_t*>(valid_ring);
+  uint32_t* key_ring = reinterpret_cast<uint32_t*>(valid_ring);
   static_assert(S::kStages <= 4 && 256 + 8 * kValidRing <= 512, "barrier layout");
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform for the compiler too
