@@ -1296,7 +1296,7 @@ kvq_status kvq_rope_append_fp8_per_head(
   a.query_start = query_start;
   a.seq_lens = seq_lens;
   a.batch_size = batch_size;
-  a.max_query_len = max_query_len;
+  a.max_query_len = static_cast<int32_t>(std::min<int64_t>(max_query_len, num_tokens));
   a.block_table = block_table;
   a.block_table_stride = block_table_stride;
   a.block_table_width = block_table_width;

@@ -51,9 +51,9 @@
 // new tokens behind up to 8192, 32 heads (8 key heads) of 128: 832 us = 810
 // TFLOP/s, bound by the decoding warps, whose work is done again for every 256
 // rows (codes through registers a tile ahead: 1111; the loop over tiles unrolled
-// twice: 1461; one code for both sides, to spare instruction fetches: 861); calls that are given a workspace for it gather their
-// entries once instead (450 us).  32 requests x 32 new tokens x 6000 keys, 128 rows
-// a key head: 204 us.
+// twice: 1461; one code for both sides, to spare instruction fetches: 861); calls
+// that are given a workspace for it gather their entries once instead (450 us).
+// 32 requests x 32 new tokens x 6000 keys, 128 rows a key head: 204 us.
 #include <type_traits>
 
 #include "kvq_per_head_attention.cuh"
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
     // for a hundred clocks)
     float row_sc = a.scale_log2;                    // score -> base-2 exponent
     if constexpr (!kFp8) {
-      uint32_t top = 0;                               // largest bits below the signs, of either half
+      uint32_t top = 0;                             // largest bits below the signs, of either half
 #pragma unroll 1
       for (int c = 0; c < D / 8; c += 8) {
         const uint32_t at = q_rows + (c >> 3) * kBlockBytes;
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
           st_shared16(at + sw128_offset(lane, i), make_uint4(h[0], h[1], h[2], h[3]));
         }
       }
-      row_sc *= k_scale * rs.i[0] * rs.i[1];
+      row_sc = row_sc * k_scale * rs.i[0] * rs.i[1];
     }
     fence_async_smem();
     __syncwarp();
@@ -852,9 +852,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       produce_fp8<D, kTiles, true>(a, b, head, keys, s0, n_tiles, full0, full1, warp - S::kScoreWarp - 1, lane, false, base,
                                    v_full, v_empty, key_ring, s_abort);
     } else if (warp < S::kScoreWarp) {
-      if constexpr (!kFp8) produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
-                                rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty,
-                                valid_ring, s_abort);
+      if constexpr (!kFp8)
+        produce<D, kTiles, false>(a, b, head, keys, s0, n_tiles, warp - S::kSoftmaxWarps, lane,
+                                  rq.cut && threadIdx.x == 32 * S::kSoftmaxWarps, base, k_full, k_empty, valid_ring,
+                                  s_abort);
     } else if (warp == S::kScoreWarp) {
       // ---- S_w(t) = Q_w K(t)^T (one elected lane; the warp waits together) -----
       constexpr uint32_t kIdesc = kFp8 ? idesc_bf16(128, kKeys, false) : idesc_f16(128, kKeys, false);
@@ -886,8 +887,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles, kFp8>::kThreads, 1)
       }
       drained(elected, drain);
     } else if (warp < S::kOutputWarp) {
-      if constexpr (!kFp8) produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
-                               v_empty, valid_ring, s_abort);
+      if constexpr (!kFp8)
+        produce<D, kTiles, true>(a, b, head, keys, s0, n_tiles, warp - S::kScoreWarp - 1, lane, false, base, v_full,
+                                 v_empty, valid_ring, s_abort);
     } else {
       // ---- O_w += P_w(t) V(t) ---------------------------------------------------
       constexpr uint32_t kIdesc = kFp8 ? idesc_bf16(128, D, true) : idesc_f16(128, D, true);

@@ -78,7 +78,7 @@ class Append:
     def parts(self, x):
         return x[:, :self.split[0]], x[:, self.split[0]:self.split[1]], x[:, self.split[1]:]
 
-    def run(self, kvq, status=None, in_place=False, no_q=False, no_k=False, stream=None, cos_sin=None):
+    def run(self, kvq, status=None, in_place=False, no_q=False, no_k=False, stream=None, cos_sin=None, most=None):
         """(q_out bits, k_out bits, codes, scales) of the call; outputs that it leaves alone hold CANARY."""
         qkv = bf16_dev(self.qkv)
         q, k, v = self.parts(qkv)
@@ -90,7 +90,7 @@ class Append:
             ko = bf16_dev(np.full(k.shape, CANARY, np.uint16))
         got = kvq.kvq_rope_append_fp8_per_head(
             None if no_q else q, k, v, dev(self.positions), dev(self.cos_sin) if cos_sin is None else cos_sin,
-            i32(self.start), i32(self.lens), dev(self.table.astype(np.int32)), cache, scales, max([n for _, n in self.reqs] + [0]),
+            i32(self.start), i32(self.lens), dev(self.table.astype(np.int32)), cache, scales, max([n for _, n in self.reqs] + [0]) if most is None else most,
             interleaved=self.interleaved, layout=self.layout, q_out=qo, k_out=False if no_k else ko, status=status,
             stream=stream)
         torch.cuda.synchronize()
@@ -180,6 +180,11 @@ def test_append_past_the_block_table(kvq):
     case = Append([(5, 60)], 4, 2, 64, 16, "NHD", 64, 15)
     case.table = case.table[:, :2].copy()
     check_append(kvq, case)
+
+
+def test_append_with_a_loose_bound(kvq):
+    """max_query_len far above what any request brings."""
+    check_append(kvq, Append([(5, 3), (70, 21), (0, 0)], 4, 2, 128, 16, "NHD", 128, 20), most=100000)
 
 
 def test_append_of_nothing(kvq):
