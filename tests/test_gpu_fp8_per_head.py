@@ -615,6 +615,19 @@ def test_many_requests_of_a_few_rows(kvq, dim, heads, kv, new):
     check(attend(kvq, b.device(), None), b.want())
 
 
+@pytest.mark.parametrize("at_once", [1, 31, 32, 33, 70])
+def test_gathering_many_requests(kvq, at_once):
+    """More and fewer requests at a time than are put in order of their lengths, equal lengths and none among them."""
+    rng = np.random.default_rng(151)
+    reqs = [(int(c), int(n)) for c, n in zip(rng.choice([0, 5, 5, 64, 200, 333], 70), rng.choice([0, 1, 13, 30, 30], 70))]
+    reqs[3] = (17, 30)
+    b = Batch(reqs, 4, 2, 64, 16, "HND", 151)
+    call = b.device()
+    for mask in ({}, dict(window=40, num_sinks=3)):
+        got = kvq.kvq_window_attention_fp8_per_head(**gathering(kvq, call, at_once, **mask), **mask)
+        check(got, b.want(gathered=True, window=mask.get("window", 0), sinks=mask.get("num_sinks", 0)))
+
+
 @pytest.mark.parametrize("new,splits", [(1, 4), (1, -4), (1, 1), (40, 1), (40, -3), (40, "gather")])
 def test_graphs_and_streams(kvq, new, splits):
     b = Batch([(300, new), (90, new)], 8, 2, 128, 16, "NHD", 139)
