@@ -47,8 +47,8 @@
 // costs some 4000 more, for its first and last tiles' masks and its output.
 // D = 64: 1 x 16384 1070 us = 1030 TFLOP/s, where the chain from a tile's scores
 // to its weights (1170 clocks) is longer than the products of the other row
-// tile (384).  D = 256: 1 x 8192 1140 us = 965, one row tile, whose keys come
-// from L2 twice as often.
+// tile (384).  D = 256: 1 x 8192 845 us = 1301, one row tile, whose keys
+// come from L2 twice as often, into two stages.
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
 // frees its tensor memory and leaves its rows unwritten.
@@ -81,6 +81,13 @@ struct Shape {
   static_assert(!kSplitRegs || 32 * kSoftmaxWarps * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "register split");
   static constexpr int kBlocks = D / 64;                     // 64-dimension blocks
   static constexpr int kStages = D == 256 || (D == 128 && kCtas == 2) ? 2 : 4;           // tiles of K, of V
+  static constexpr int kAhead = 2;                           // scores before a tile's output
+  // One row tile: a tile's output is issued before the keys of the scores behind
+  // it are waited for, which with two stages come late (D = 256, 1 x 8192 tokens:
+  // 845 us, 1137 the other way round).  Two row tiles: the keys are waited for
+  // before the weights, and the scores follow the output at once (D = 128, 1 x
+  // 16384 tokens: 1200 us, 1373 the other way round).
+  static constexpr bool kKeysLast = kTiles == 1;
   static constexpr uint32_t kQBlock = 128 * 128;             // 64 dimensions of a row tile
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKBlock = kKeys * 128;           // 64 dimensions of a key tile
@@ -639,7 +646,6 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
       // ---- a row tile's products (one elected lane; the warp waits together) ---
       const int w = warp - S::kProductWarp;
       constexpr uint32_t kIdescS = idesc_bf16(128, kKeys, false), kIdescO = idesc_bf16(128, D, true);
-      constexpr int kAhead = 2;                     // scores before a tile's output
       const uint64_t qdesc = sw128_desc(base + w * S::kQTile, 16, 1024), kdesc = sw128_desc(base + S::kK, 16, 1024);
       const uint64_t vdesc = sw128_desc(base + S::kV, S::kKBlock, 1024);
       const uint32_t o = tmem + w * D;
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
           if (t == n - 1) warp_commit(elected, q_free);
         };
         ok = have(q_full, items_done);
-        for (int32_t t = 0; t < min(n, kAhead) && ok; ++t) {
+        for (int32_t t = 0; t < min(n, S::kAhead) && ok; ++t) {
           ok = keys_there(t);
           if (ok) scores(t);
         }
@@ -677,10 +683,9 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
             break;
           }
 #endif
-          // O += P(t) V(t); what else it and the scores behind it need is waited for
-          // before its weights
+          // O += P(t) V(t)
           ok = have(v_good + 8 * st, (tiles + t) / S::kStages);
-          if (ok && t + kAhead < n) ok = keys_there(t + kAhead);
+          if (!S::kKeysLast && ok && t + S::kAhead < n) ok = keys_there(t + S::kAhead);
           const uint64_t vd = vdesc + ((st * S::kTileBytes) >> 4);
           auto product = [&](int ks) {
             warp_mma_ta(elected, o, tmem + kSCol + kKeys * buf + 8 * ks, vd + ((2048 * ks) >> 4), kIdescO,
@@ -691,7 +696,10 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
           for (int ks = 0; ks < kKeys / 16; ++ks) product(ks);
           warp_commit(elected, o_done + 8 * buf);
           warp_commit(elected, v_empty + 8 * st);
-          if (t + kAhead < n) scores(t + kAhead);
+          if (t + S::kAhead < n) {
+            if (S::kKeysLast) ok = keys_there(t + S::kAhead);
+            if (ok) scores(t + S::kAhead);
+          }
         }
         tiles += n;
         ++items_done;
