@@ -47,7 +47,7 @@
 // costs some 4000 more, for its first and last tiles' masks and its output.
 // D = 64: 1 x 16384 1070 us = 1030 TFLOP/s, where the chain from a tile's scores
 // to its weights (1170 clocks) is longer than the products of the other row
-// tile (384).  D = 256: 1 x 8192 845 us = 1301, one row tile, whose keys
+// tile (384).  D = 256: 1 x 8192 774 us = 1421, one row tile, whose keys
 // come from L2 twice as often, into two stages.
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
@@ -84,10 +84,13 @@ struct Shape {
   static constexpr int kAhead = 2;                           // scores before a tile's output
   // One row tile: a tile's output is issued before the keys of the scores behind
   // it are waited for, which with two stages come late (D = 256, 1 x 8192 tokens:
-  // 845 us, 1137 the other way round).  Two row tiles: the keys are waited for
-  // before the weights, and the scores follow the output at once (D = 128, 1 x
-  // 16384 tokens: 1200 us, 1373 the other way round).
+  // 845 us, 1137 the other way round), and keys are copied a tile before the
+  // values, their stage being free earlier (774 us).  Two row tiles: the keys are
+  // waited for before the weights, and the scores follow the output at once (D =
+  // 128, 1 x 16384 tokens: 1200 us, 1373 the other way round; with keys copied
+  // first 1225, and 16 x 1024 tokens 146 for 137).
   static constexpr bool kKeysLast = kTiles == 1;
+  static constexpr int kKeysFirst = kTiles == 1 ? 1 : 0;     // tiles that keys are copied ahead of values
   static constexpr uint32_t kQBlock = 128 * 128;             // 64 dimensions of a row tile
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKBlock = kKeys * 128;           // 64 dimensions of a key tile
@@ -607,23 +610,24 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
         }
         __syncwarp();
         ++queries;
-        for (int32_t t = 0; t < keys.steps && ok; ++t) {
+        auto copy = [&](int32_t t, uint32_t full, uint32_t empty, uint32_t to, const CUtensorMap* map, uint32_t& count) {
           const uint32_t at = tiles + t, st = at % S::kStages;
+          if (at >= S::kStages && !have(empty + 8 * st, at / S::kStages - 1)) return false;
           const int32_t key = row_of(it, keys, t);
-          auto copy = [&](uint32_t full, uint32_t empty, uint32_t to, const CUtensorMap* map, uint32_t& count) {
-            if (at >= S::kStages && !have(empty + 8 * st, at / S::kStages - 1)) return false;
-            if (elected) {
-              mbar_arrive_expect_tx(full + 8 * st, S::kTileBytes);
+          if (elected) {
+            mbar_arrive_expect_tx(full + 8 * st, S::kTileBytes);
 #pragma unroll
-              for (int i = 0; i < S::kBlocks; ++i)
-                tma_load_3d(base + to + st * S::kTileBytes + i * S::kKBlock, map, 64 * i, it.head, key, full + 8 * st);
-            }
-            __syncwarp();
-            ++count;
-            return true;
-          };
-          ok = copy(k_full, k_empty, S::kK, &kmap, copied[0]) && copy(v_full, v_empty, S::kV, &vmap, copied[1]);
-        }
+            for (int i = 0; i < S::kBlocks; ++i)
+              tma_load_3d(base + to + st * S::kTileBytes + i * S::kKBlock, map, 64 * i, it.head, key, full + 8 * st);
+          }
+          __syncwarp();
+          ++count;
+          return true;
+        };
+        auto copy_k = [&](int32_t t) { return t >= keys.steps || copy(t, k_full, k_empty, S::kK, &kmap, copied[0]); };
+        if (S::kKeysFirst == 1) ok = copy_k(0);
+        for (int32_t t = 0; t < keys.steps && ok; ++t)
+          ok = copy_k(t + S::kKeysFirst) && copy(t, v_full, v_empty, S::kV, &vmap, copied[1]);
         if (!ok) break;
         tiles += keys.steps;
       }
