@@ -77,9 +77,9 @@ inline int64_t fp8_gather_bytes(int64_t rows, int64_t num_kv_heads, int64_t head
 // 4 x 8000 keys, 256 rows 74 / 141, 512 rows (64 blocks) 124 / 144, 1024 rows 193
 // / 149; 1 x 16000 keys, 512 rows 56 / 200, 2048 rows (64 blocks) 182 / 207, 4096
 // rows 391 / 215.  (8 key heads of 64: 4 x 8000 keys, 512 rows 85 / 107, 1024 rows
-// 122 / 110; 4 of 256: 512 rows 141 / 229, 1024 rows 233 / 230.)
-inline bool fp8_default_gathers(int64_t rows, int64_t groups, int sms) {
-  const int64_t blocks = (rows + 255) / 256 * groups;
+// 122 / 110; 4 of 256, blocks of 128 rows: 512 rows 142 / 148, 1024 rows 262 / 153.)
+inline bool fp8_default_gathers(int64_t rows, int64_t groups, int32_t head_size, int sms) {
+  const int64_t block = per_head_prefill_rows(rows, head_size), blocks = (rows + block - 1) / block * groups;
   return (rows >= 512 && blocks >= sms) || (rows >= 1024 && 4 * blocks >= 3 * int64_t{sms});
 }
 
@@ -94,7 +94,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
                                              int32_t head_size, int64_t batch_size, int64_t max_seq_len,
                                              int64_t window, int64_t num_sinks, int sms, bool fp8 = false) {
   const int64_t rows = max_query_len * group, groups = num_kv_heads * batch_size;
-  if (fp8 && fp8_default_gathers(rows, groups, sms)) return {1, true, per_head_prefill_rows(rows, head_size)};
+  if (fp8 && fp8_default_gathers(rows, groups, head_size, sms)) return {1, true, per_head_prefill_rows(rows, head_size)};
   const bool windowed = window > 0 && window < max_seq_len;
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;
