@@ -9,6 +9,12 @@
 namespace kvq {
 namespace {
 
+// The first key that a window lets a query at `position` see (window <= 0:
+// none).  Negative positions, of padding, less a window may pass 32 bits.
+__device__ __forceinline__ int32_t first_seen(int32_t position, int32_t window) {
+  return window <= 0 || position < window ? 0 : position - window + 1;
+}
+
 // The request's rows of the workspace: the keys [0, sinks) that stay visible,
 // then [lo, len), the ones that some of its queries may see.
 struct GatherPlan {
@@ -32,7 +38,7 @@ __device__ __forceinline__ bool gather_plan(const CachedArgs& c, const int32_t* 
   p.first = len - p.n;
   p.len = min(len, c.table_positions);
   p.cut = p.len < len;
-  p.lo = window > 0 ? min(p.len, max(0, p.first - window + 1)) : 0;
+  p.lo = min(p.len, first_seen(p.first, window));
   p.sinks = min(num_sinks, p.lo);
   return p.len - p.lo + p.sinks <= c.rows;
 }

@@ -125,7 +125,7 @@ template <int kKeys>
 __device__ __forceinline__ Keys<kKeys> item_keys(const PromptAttentionArgs& a, const Item& it, int32_t t0, int32_t t1) {
   Keys<kKeys> k;
   k.hi = max(0, min(it.len, it.first + t1 + 1));
-  k.lo = a.window > 0 ? min(k.hi, max(0, it.first + t0 - a.window + 1)) : 0;
+  k.lo = min(k.hi, first_seen(it.first + t0, a.window));
   k.sinks = min(a.num_sinks, k.lo);
   k.sink_steps = (k.sinks + kKeys - 1) / kKeys;
   k.steps = k.sink_steps + (k.hi - k.lo + kKeys - 1) / kKeys;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
       const int32_t token_in = min(static_cast<int32_t>(token_of), it.n - 1);
       const int32_t pos = it.first + token_in, pos_hi = min(pos, it.len - 1);
       const int32_t q_head = it.head * a.group + static_cast<int32_t>(head_of);
-      const int32_t pos_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      const int32_t pos_lo = first_seen(pos, a.window);
       int32_t full0, full1;
       full_steps(keys, __reduce_min_sync(kFull, pos_hi), __reduce_max_sync(kFull, pos_lo), full0, full1);
 
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(Shape<D, kTiles>::kThreads, Shape<D, kTiles>::
       for (uint32_t k = 0; ok && next_item(k, it); ++k) {
         const Keys<kKeys> keys = keys_of_item(it);
         const int32_t hi = min(it.len - 1, it.first + first_token(it));
-        const int32_t lo = a.window > 0 ? max(0, it.first + last_token(it) - a.window + 1) : 0;
+        const int32_t lo = first_seen(it.first + last_token(it), a.window);
         int32_t full0, full1;
         full_steps(keys, hi, lo, full0, full1);
         for (int32_t t = 0; t < keys.steps; ++t) {

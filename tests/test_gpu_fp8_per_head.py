@@ -671,3 +671,20 @@ def test_attention_refuses_what_does_not_fit(kvq):
     refused(RuntimeError, "num_splits", num_splits=129)
     refused(RuntimeError, "softmax_scale", softmax_scale=float("nan"))
     refused(RuntimeError, "num_sinks", num_sinks=-1)
+
+
+@pytest.mark.parametrize("dim,heads,kv", [(64, 8, 2), (128, 8, 2), (256, 4, 1)])
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 100, 40])
+@pytest.mark.parametrize("splits", [1, -5, "gather"])
+def test_padded_requests_and_windows_of_any_size(kvq, dim, heads, kv, window, splits):
+    """Queries at negative positions beside others of their request, under windows that reach past the first position
+    by any amount: as if there were none, or the window of the others."""
+    b = Batch([(0, 130), (20, 130), (0, 130), (90, 130)], heads, kv, dim, 16, "NHD", 157)
+    b.lens[0], b.lens[2] = 80, 5                                      # their first 50 and 125 positions are negative
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = attend(kvq, b.device(), splits, window=window, num_sinks=3, status=status)
+    check(got, b.want(window=window, sinks=3))
+    assert int(status.item()) == 0
+    if window > 1000:
+        whole = attend(kvq, b.device(), splits)
+        assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
