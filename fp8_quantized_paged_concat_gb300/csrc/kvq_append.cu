@@ -170,8 +170,11 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
   const uint32_t col = a.block_div.div(static_cast<uint32_t>(first)) + ordinal;
   const int64_t base = static_cast<int64_t>(col) * a.block_size;
   if (base >= len) return;                           // past the request's last page
-  const int32_t p0 = static_cast<int32_t>(max(base, static_cast<int64_t>(first)));
-  const int32_t p1 = static_cast<int32_t>(min(base + a.block_size, static_cast<int64_t>(len)));
+  // Its new entries are [held, end).  (Entries are counted within their page:
+  // steps past the last one would wrap as positions of a sequence near 2^31.)
+  const int32_t held = static_cast<int32_t>(max(int64_t{0}, first - base));
+  const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(a.block_size), len - base));
+  const int64_t page_token = token0 + (base - first);          // the token of entry 0, were it new
   int32_t id = -1;
   if (col < static_cast<uint32_t>(a.block_table_width)) id = load_global(a.block_table + b * a.block_table_stride + col);
 
@@ -180,9 +183,9 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) +
                              head * (is_v ? a.v_stride_h : a.k_stride_h) + 8 * li;
   const int64_t stride = is_v ? a.v_stride_t : a.k_stride_t;
-  // The lane's values of the tokens at positions p + sub, kAtOnce on, ..., every
-  // load under way before the first is used; bit j of `live`: there is one, and
-  // its rotation position is in the table.
+  // The lane's values of the entries p + sub, kAtOnce on, ..., every load under
+  // way before the first is used; bit j of `live`: there is one, and its rotation
+  // position is in the table.
   Values y[kHeld];
   uint32_t live;
   auto values = [&](int32_t p) {
@@ -193,8 +196,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
       const int32_t q = p + sub + kAtOnce * j;
       raw[j] = make_uint4(0, 0, 0, 0);
       pos[j] = -1;
-      if (q < p1) {
-        const int64_t token = token0 + (q - first);
+      if (q < end) {
+        const int64_t token = page_token + q;
         raw[j] = load_global(reinterpret_cast<const uint4*>(src + token * stride));
         pos[j] = load_global(a.positions + token);
       }
@@ -203,7 +206,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       const bool ok = pos[j] >= 0 && pos[j] < a.max_position;
-      if (!ok && li == 0 && p + sub + kAtOnce * j < p1) report(a.status, KVQ_STATUS_BAD_INDEX);
+      if (!ok && li == 0 && p + sub + kAtOnce * j < end) report(a.status, KVQ_STATUS_BAD_INDEX);
       live |= ok ? 1u << j : 0u;
       if (is_v) {
         y[j] = unpack8(raw[j]);
@@ -215,9 +218,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
     }
   };
 
-  const int32_t held = static_cast<int32_t>(p0 - base);          // entries that stay
   float amax = 0.0f;
-  for (int32_t p = p0; p < p1; p += kChunk) {
+  for (int32_t p = held; p < end; p += kChunk) {
     values(p);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
@@ -258,20 +260,20 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int64_t 
   const bool keep = !is_v && a.k_out != nullptr;
   if (!there && !keep) return;
   const float f = power_of_two(-e);
-  const bool again = p1 - p0 > kChunk;               // more tokens than are held
-  for (int32_t p = p0; p < p1; p += kChunk) {
+  const bool again = end - held > kChunk;              // more tokens than are held
+  for (int32_t p = held; p < end; p += kChunk) {
     if (again) values(p);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       if (!((live >> j) & 1)) continue;
       const int32_t q = p + sub + kAtOnce * j;
       if (there) {
-        const uint32_t row = static_cast<uint32_t>(q - base) * a.row_offset + head * a.row_head;
+        const uint32_t row = static_cast<uint32_t>(q) * a.row_offset + head * a.row_head;
         st8(region + static_cast<uint64_t>(row) * D + 8 * li,
             make_uint2(e4m3x4(y[j].v[0], y[j].v[1], f), e4m3x4(y[j].v[2], y[j].v[3], f)));
       }
       if (keep)
-        st16(static_cast<__nv_bfloat16*>(a.k_out) + (token0 + (q - first)) * a.k_out_stride_t + head * a.k_out_stride_h +
+        st16(static_cast<__nv_bfloat16*>(a.k_out) + (page_token + q) * a.k_out_stride_t + head * a.k_out_stride_h +
                  8 * li, pack8(y[j]));
     }
   }

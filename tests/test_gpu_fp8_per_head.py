@@ -182,6 +182,15 @@ def test_append_past_the_block_table(kvq):
     check_append(kvq, case)
 
 
+@pytest.mark.parametrize("block,new", [(16, 3), (16, 40), (64, 200), (24, 1), (1024, 600)])
+def test_append_at_the_last_positions_of_all(kvq, block, new):
+    """Sequences that end at and next to the largest length, far past their block tables: nothing is appended, and
+    rotated rows are written as ever."""
+    case = Append([(5, new), (0, new), (9, new)], 4, 2, 64, block, "NHD", 64, 21)
+    case.lens[:2] = [(1 << 31) - 1, (1 << 31) - 1 - new // 2]
+    check_append(kvq, case)
+
+
 def test_append_with_a_loose_bound(kvq):
     """max_query_len far above what any request brings."""
     check_append(kvq, Append([(5, 3), (70, 21), (0, 0)], 4, 2, 128, 16, "NHD", 128, 20), most=100000)
