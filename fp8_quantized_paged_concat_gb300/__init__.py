@@ -731,7 +731,8 @@ def kvq_rope_append_fp8_per_head(q, k, v, positions, cos_sin, query_start, seq_l
 def kvq_fp8_attention_default_splits(max_query_len: int, num_heads: int, num_kv_heads: int, head_size: int,
                                      batch_size: int, max_seq_len: int, window: int = 0, num_sinks: int = 0) -> tuple:
     """kvq_per_head_attention_default_splits for the per-head e4m3 cache; (1,
-    True): a call that had better gather its entries into a workspace."""
+    True): a call that had better gather its entries, into a workspace of 1 GiB
+    at most (kvq_fp8_attention_workspace_bytes may be less)."""
     use_workspace = _I32(0)
     splits = load_library().kvq_fp8_attention_default_splits(
         max_query_len, num_heads, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks,
@@ -759,9 +760,8 @@ def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_
     kvq_fp8_attention_default_splits.  A call of many query rows with
     num_splits = 1 and a workspace gathers the entries it needs there, as many
     requests at a time as it holds (kvq_fp8_attention_workspace_bytes; by
-    default up to 1 GiB is allocated, or one request's); max_seq_len then has
-    to hold.  Returns (out bf16 [T, H, D], lse fp32 [T, H]); lse=False skips
-    the lse output."""
+    default up to 1 GiB is allocated); max_seq_len then has to hold.  Returns
+    (out bf16 [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, kv_scales, False,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)

@@ -374,43 +374,52 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check("lse", lse, at::kFloat, dev, 2);
       shaped("lse", lse, {T, H});
     }
+    at::Tensor given;
+    if (a[15] != Py_None) {
+      given = tensor("workspace", a[15]);
+      if (!given.is_cuda() || given.get_device() != dev || !given.is_contiguous())
+        bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
+    }
+    const auto size_of = [](const at::Tensor& t) {
+      return t.defined() ? t.numel() * static_cast<int64_t>(t.element_size()) : 0;
+    };
     // the ranges of a block join in a cluster, or through a workspace
     int32_t use_workspace = 0;
     int32_t splits;
-    if (a[14] == Py_None) {
-      splits = fp8 ? lib.fp8_default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks,
-                                            &use_workspace)
-                   : lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks, tree,
-                                        &use_workspace);
-    } else {
+    const auto fp8_bytes = [&](int32_t ranges) {
+      return lib.fp8_workspace_bytes(T, dim(H), c.heads, c.head_size, dim(B), max_query, max_seq, window, sinks, ranges);
+    };
+    if (a[14] != Py_None) {
       splits = int32("num_splits", a[14]);
       use_workspace = splits > KVQ_PER_HEAD_CLUSTER_SPLITS ||
                       (splits > 1 && c.heads > 0 && max_query * (H / c.heads) > KVQ_PER_HEAD_CLUSTER_ROWS);
+    } else if (fp8) {
+      const auto default_up_to = [&](int32_t keys, int32_t& through) {
+        return lib.fp8_default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), keys, window, sinks, &through);
+      };
+      splits = default_up_to(max_seq, use_workspace);
+      // A workspace with room for every entry to be gathered, more than the default
+      // counts on: whether to gather is then as for a few keys.
+      int32_t gathers = 0;
+      if (size_of(given) > KVQ_FP8_GATHER_BYTES && size_of(given) >= fp8_bytes(1) && default_up_to(1, gathers) == 1 &&
+          gathers)
+        splits = use_workspace = 1;
+    } else {
+      splits = lib.default_splits(max_query, dim(H), c.heads, c.head_size, dim(B), max_seq, window, sinks, tree,
+                                  &use_workspace);
     }
     at::Tensor workspace;
-    if (a[15] != Py_None) {
-      const at::Tensor& given = tensor("workspace", a[15]);
-      if (!given.is_cuda() || given.get_device() != dev || !given.is_contiguous())
-        bad("workspace: expected a contiguous tensor on cuda:" + std::to_string(dev));
+    if (given.defined()) {
       // default ranges that join without one run without it
       if (use_workspace || a[14] != Py_None) workspace = given;
     } else if (use_workspace && T > 0) {
-      int64_t bytes;
-      if (fp8) {
-        // (gathered entries: all requests' at a time, or as many as fit into 1 GiB)
-        const auto of = [&](int64_t requests) {
-          return lib.fp8_workspace_bytes(T, dim(H), c.heads, c.head_size, dim(requests), max_query, max_seq, window, sinks,
-                                         splits);
-        };
-        bytes = of(B);
-        if (splits == 1) bytes = std::min(bytes, std::max(of(1), int64_t{1} << 30));
-      } else {
-        bytes = lib.workspace_bytes(T, dim(H), c.head_size, splits);
-      }
+      int64_t bytes = fp8 ? fp8_bytes(splits) : lib.workspace_bytes(T, dim(H), c.head_size, splits);
+      // (entries of all requests at a time, or of as many as fit, of which one is sure)
+      if (fp8 && splits == 1) bytes = std::min<int64_t>(bytes, KVQ_FP8_GATHER_BYTES);
       if (bytes > 0) workspace = scope.buffer({bytes}, at::kByte);
     }
     void* ws = workspace.defined() ? workspace.data_ptr() : nullptr;
-    const int64_t ws_bytes = workspace.defined() ? workspace.numel() * static_cast<int64_t>(workspace.element_size()) : 0;
+    const int64_t ws_bytes = size_of(workspace);
     const Strides sq = head_strides(q), so = head_strides(out);
     float* lse_ptr = want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
     const int64_t lse_stride = want_lse ? row_stride(lse) : 0;

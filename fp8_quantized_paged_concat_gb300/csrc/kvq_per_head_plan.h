@@ -69,18 +69,43 @@ inline int64_t fp8_gather_rows(int64_t max_query_len, int64_t max_seq_len, int64
 inline int64_t fp8_gather_bytes(int64_t rows, int64_t num_kv_heads, int64_t head_size, int64_t batch_size) {
   return batch_size * rows * num_kv_heads * head_size * 4 + (batch_size * rows / 32 + 3 + 3) / 4 * 16;
 }
-// Whether a call's default is to gather: where every entry is read for many
-// blocks of rows, and these blocks about fill the GPU.  us of the attention that
-// decodes the entries (in its default ranges) and of gather and attention, 8 key
-// heads of 128: 32 requests x 6000 keys, 128 rows 232 / 366, 512 rows (512 blocks)
-// 548 / 515, 1024 rows 1006 / 732; 8 x 6000 keys, 512 rows (128 blocks) 146 / 145;
-// 4 x 8000 keys, 256 rows 74 / 141, 512 rows (64 blocks) 124 / 144, 1024 rows 193
-// / 149; 1 x 16000 keys, 512 rows 56 / 200, 2048 rows (64 blocks) 182 / 207, 4096
-// rows 391 / 215.  (8 key heads of 64: 4 x 8000 keys, 512 rows 85 / 107, 1024 rows
-// 122 / 110; 4 of 256, blocks of 128 rows: 512 rows 142 / 148, 1024 rows 262 / 153.)
-inline bool fp8_default_gathers(int64_t rows, int64_t groups, int32_t head_size, int sms) {
-  const int64_t block = per_head_prefill_rows(rows, head_size), blocks = (rows + block - 1) / block * groups;
-  return (rows >= 512 && blocks >= sms) || (rows >= 1024 && 4 * blocks >= 3 * int64_t{sms});
+// Requests whose entries are gathered at a time into `bytes` of workspace, one
+// launch each of the gather and of the attention (0: not one's fit).
+inline int64_t fp8_gather_at_once(int64_t rows, int64_t num_kv_heads, int64_t head_size, int64_t batch_size,
+                                  int64_t bytes) {
+  if (4.0 * static_cast<double>(rows) * num_kv_heads * head_size > static_cast<double>(bytes)) return 0;
+  int64_t n = std::min(batch_size, bytes / (rows * num_kv_heads * head_size * 4));
+  while (n > 0 && fp8_gather_bytes(rows, num_kv_heads, head_size, n) > bytes) --n;
+  return n;
+}
+// Whether a call's default is to gather, into KVQ_FP8_GATHER_BYTES at most:
+// where every entry is read for many blocks of rows, and these blocks about fill
+// the GPU.  us of the attention that decodes the entries (in its default ranges)
+// and of gather and attention, 8 key heads of 128: 32 requests x 6000 keys, 128
+// rows 232 / 366, 512 rows (512 blocks) 548 / 515, 1024 rows 1006 / 732; 8 x 6000
+// keys, 512 rows (128 blocks) 146 / 145; 4 x 8000 keys, 256 rows 74 / 141, 512
+// rows (64 blocks) 124 / 144, 1024 rows 193 / 149; 1 x 16000 keys, 512 rows 56 /
+// 200, 2048 rows (64 blocks) 182 / 207, 4096 rows 391 / 215.  (8 key heads of 64:
+// 4 x 8000 keys, 512 rows 85 / 107, 1024 rows 122 / 110; 4 of 256, blocks of 128
+// rows: 512 rows 142 / 148, 1024 rows 262 / 153.)
+// A batch that does not fit goes through in rounds, whose blocks fill the GPU each
+// for itself: from 1024 rows on, where their waves of blocks are no more than half
+// again the other attention's.  (Waves of the rounds and of the other, its us and
+// theirs: 1024 rows, 34000 keys, 16 requests 5 : 4, 2917 / 2343, 32 requests 9 : 7,
+// 5258 / 4382, 64 requests 19 : 14, 10454 / 9098; 131072 keys, 8 requests 8 : 2, 5103
+// / 11521; 2048 rows, 16 x 131072 keys 16 : 7, 20182 / 23045; 8192 rows, 4 x 131072
+// 8 : 7, 20045 / 11056.  512 rows: 64 x 8000 keys 8 : 7, 1261 / 1280, 64 x 34000
+// keys 10 : 7, 5269 / 5840, 16 x 131072 keys 16 : 2, 5109 / 23006.)
+inline bool fp8_default_gathers(int64_t max_query_len, int64_t group, int64_t num_kv_heads, int32_t head_size,
+                                int64_t batch_size, int64_t max_seq_len, int64_t window, int64_t num_sinks, int sms) {
+  const int64_t rows = max_query_len * group, block = per_head_prefill_rows(rows, head_size);
+  const int64_t each = (rows + block - 1) / block * num_kv_heads, blocks = each * batch_size;
+  if (rows < 512 || blocks < (rows < 1024 ? sms : (3 * int64_t{sms} + 3) / 4)) return false;
+  const int64_t n = fp8_gather_at_once(fp8_gather_rows(max_query_len, max_seq_len, window, num_sinks), num_kv_heads,
+                                       head_size, batch_size, KVQ_FP8_GATHER_BYTES);
+  if (n == 0 || n == batch_size) return n != 0;
+  const auto waves = [&](int64_t requests) { return (requests * each + sms - 1) / sms; };
+  return rows >= 1024 && 2 * (batch_size / n * waves(n) + waves(batch_size % n)) <= 3 * waves(batch_size);
 }
 
 // The default key ranges per block of rows, whether they join through a
@@ -94,7 +119,9 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
                                              int32_t head_size, int64_t batch_size, int64_t max_seq_len,
                                              int64_t window, int64_t num_sinks, int sms, bool fp8 = false) {
   const int64_t rows = max_query_len * group, groups = num_kv_heads * batch_size;
-  if (fp8 && fp8_default_gathers(rows, groups, head_size, sms)) return {1, true, per_head_prefill_rows(rows, head_size)};
+  if (fp8 && fp8_default_gathers(max_query_len, group, num_kv_heads, head_size, batch_size, max_seq_len, window, num_sinks,
+                                 sms))
+    return {1, true, per_head_prefill_rows(rows, head_size)};
   const bool windowed = window > 0 && window < max_seq_len;
   const int64_t keys =
       windowed ? std::min<int64_t>(max_seq_len, window + std::min<int64_t>(max_query_len, 256) + num_sinks) : max_seq_len;

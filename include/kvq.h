@@ -748,6 +748,7 @@ kvq_status kvq_compact_drafts_nvfp4_per_head(
 #define KVQ_FP8_SCALE_BIAS     127
 #define KVQ_FP8_SCALE_MIN_EXP  (-60)
 #define KVQ_FP8_SCALE_MAX_EXP  60
+#define KVQ_FP8_GATHER_BYTES   (1LL << 30)   /* workspace for gathered entries that defaults count on */
 
 /*
  * kvq_rope_append_fp8_per_head -- rotates the queries and keys of the
@@ -858,7 +859,8 @@ int64_t kvq_fp8_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
 /*
  * kvq_fp8_attention_default_splits -- kvq_per_head_attention_default_splits
  * for the e4m3 cache; 1 with *use_workspace set: a call that had better gather
- * its entries.
+ * its entries, into kvq_fp8_attention_workspace_bytes or, of those, no more than
+ * KVQ_FP8_GATHER_BYTES, where one request's fit.
  */
 int32_t kvq_fp8_attention_default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads,
                                          int32_t head_size, int32_t batch_size, int32_t max_seq_len,

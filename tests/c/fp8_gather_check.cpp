@@ -1,0 +1,47 @@
+// For calls over the e4m3 cache whose default is to gather their entries, over
+// the whole range of sizes: one request's fit into the room that the default
+// counts on, as many at a time as the call then takes are the most that do, and
+// a batch that goes through in rounds fills the GPU in each of them.
+#include <cstdio>
+
+#include "kvq_per_head_plan.h"
+
+int main() {
+  long long gathers = 0, rounds = 0, no_room = 0, not_most = 0, idle = 0, unlike = 0;
+  const long long room = KVQ_FP8_GATHER_BYTES;
+  for (int sms : {152, 148, 132})
+    for (int head_size : {64, 128, 256})
+      for (int kv_heads : {1, 2, 3, 8, 16})
+        for (int group : {1, 3, 4, 8, 16, 130})
+          for (int query : {1, 5, 33, 64, 128, 300, 640, 4096})
+            for (int batch : {1, 2, 3, 5, 8, 13, 32, 64, 128, 512, 4096})
+              for (int keys : {1, 1024, 9000, 34000, 131072, 300000, 1 << 20, 1 << 30})
+                for (int window : {0, 333, 8192}) {
+                  const kvq::PerHeadRanges r =
+                      kvq::per_head_default_ranges(query, group, kv_heads, head_size, batch, keys, window, 4, sms, true);
+                  if (r.splits != 1 || !r.workspace) continue;
+                  ++gathers;
+                  const long long held = kvq::fp8_gather_rows(query, keys, window, 4);
+                  const long long n = kvq::fp8_gather_at_once(held, kv_heads, head_size, batch, room);
+                  if (n < 1 || n > batch || kvq::fp8_gather_bytes(held, kv_heads, head_size, n) > room) ++no_room;
+                  if (n < batch && kvq::fp8_gather_bytes(held, kv_heads, head_size, n + 1) <= room) ++not_most;
+                  const long long rows = 1LL * query * group, block = kvq::per_head_prefill_rows(rows, head_size);
+                  const long long each = (rows + block - 1) / block * kv_heads;
+                  if (n == batch) {
+                    if (4 * each * n < 3 * sms) ++idle;
+                    continue;
+                  }
+                  ++rounds;
+                  // no round's blocks leave more than half of the GPU idle on average, and the rows pay for the gather
+                  long long waves = 0;
+                  for (long long b = 0; b < batch; b += n) waves += ((b + n < batch ? n : batch - b) * each + sms - 1) / sms;
+                  if (rows < 1024 || 2 * waves > 3 * ((batch * each + sms - 1) / sms)) ++idle;
+                  // the same rows as a batch that fits gather too
+                  if (!kvq::fp8_default_gathers(query, group, kv_heads, head_size, batch, 1, 0, 4, sms) &&
+                      kvq::fp8_gather_at_once(64, kv_heads, head_size, batch, room) == batch)
+                    ++unlike;
+                }
+  std::printf("gathers %lld, rounds %lld, no room %lld, not most %lld, idle %lld, unlike %lld\n", gathers, rounds, no_room,
+              not_most, idle, unlike);
+  return no_room + not_most + idle + unlike != 0 || gathers == 0 || rounds == 0;
+}

@@ -20,3 +20,13 @@ def test_defaults_fit_the_calls_they_are_for(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
     assert "other block 0, out of limits 0, no room 0" in r.stdout and "gathers 0" not in r.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_defaults_that_gather_fit_their_room_and_fill_the_gpu(tmp_path):
+    exe = tmp_path / "fp8_gather_check"
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-I" + os.path.join(ROOT, "include"),
+                           "-I" + os.path.join(ROOT, "fp8_quantized_paged_concat_gb300", "csrc"),
+                           os.path.join(HERE, "c", "fp8_gather_check.cpp"), "-o", str(exe)])
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout

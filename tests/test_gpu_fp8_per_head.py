@@ -697,3 +697,57 @@ def test_padded_requests_and_windows_of_any_size(kvq, dim, heads, kv, window, sp
     if window > 1000:
         whole = attend(kvq, b.device(), splits)
         assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
+
+
+def spare_bytes(call):
+    """The call's results, and the most memory that it held beside what was there before."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = call()
+    torch.cuda.synchronize()
+    return got, torch.cuda.max_memory_allocated() - before
+
+
+def widened(call, columns):
+    """The call with a block table of so many columns."""
+    table = torch.zeros((call["block_table"].shape[0], columns), dtype=torch.int32, device=DEV)
+    table[:, :call["block_table"].shape[1]] = call["block_table"]
+    return dict(call, block_table=table)
+
+
+def test_default_room_for_gathered_entries(kvq):
+    """A batch whose entries take more than 1 GiB for the bound on its lengths goes through in rounds within it; where
+    not one request's fit they are decoded as they are read."""
+    b = Batch([(300, 640), (0, 640), (77, 640)], 64, 8, 128, 64, "NHD", 163)
+    call, results = widened(b.device(), (1 << 20) // 64), 1920 * 64 * (2 * 128 + 4)
+    room = kvq.kvq_fp8_attention_workspace_bytes(1920, 64, 8, 128, 3, 640, 1000)
+    want = kvq.kvq_window_attention_fp8_per_head(**dict(call, max_seq_len=1000), num_splits=1,
+                                                 workspace=torch.empty(room, dtype=torch.uint8, device=DEV))
+    assert kvq.kvq_fp8_attention_default_splits(640, 64, 8, 128, 3, 131072) == (1, True)      # one request at a time
+    got, held = spare_bytes(lambda: attend(kvq, dict(call, max_seq_len=131072), None))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert results < held <= results + (1 << 30) + (1 << 22)
+    splits, through = kvq.kvq_fp8_attention_default_splits(640, 64, 8, 128, 3, 1 << 20)       # 4 GiB a request
+    assert splits > 1 or not through
+    call = dict(call, max_seq_len=1 << 20)
+    want = attend(kvq, call, -splits if through else splits)
+    got, held = spare_bytes(lambda: attend(kvq, call, None))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and held < results + (1 << 29)
+
+
+def test_a_larger_workspace_of_ones_own(kvq):
+    """With room given for every entry the default gathers, however much that takes."""
+    b = Batch([(10 * i, 128) for i in range(16)], 32, 8, 128, 64, "NHD", 173)
+    call = dict(widened(b.device(), 40000 // 64), max_seq_len=40000)
+    splits, through = kvq.kvq_fp8_attention_default_splits(128, 32, 8, 128, 16, 40000)
+    assert splits > 1 or not through
+    room = kvq.kvq_fp8_attention_workspace_bytes(2048, 32, 8, 128, 16, 128, 40000)
+    assert room > 1 << 31
+    held = torch.empty(room, dtype=torch.uint8, device=DEV)
+    want = kvq.kvq_window_attention_fp8_per_head(**call, num_splits=1, workspace=held)
+    held.fill_(0xFF)
+    got = kvq.kvq_window_attention_fp8_per_head(**call, workspace=held)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert not bool((held[:128 * 8 * 128 * 2] == 0xFF).all())         # (the first request's entries are there)
