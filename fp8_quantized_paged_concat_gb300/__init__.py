@@ -119,6 +119,9 @@ _SIGNATURES = {
     "kvq_window_attention_fp8_per_head": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _I64,
                                           _I32, _I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _I64, _I64, _P, _I64,
                                           _I32, _I32, _P, _I64, _P, _P],
+    "kvq_window_attention_fp8_per_head_any_length": [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _I32, _P, _I64, _I32, _P,
+                                                     _P, _I64, _I32, _I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P,
+                                                     _I64, _I64, _P, _I64, _I32, _I32, _P, _I64, _P, _P],
     "kvq_fp8_attention_default_splits": [_I32] * 8 + [_P],
     "kvq_fp8_attention_workspace_bytes": [_I64] + [_I32] * 9,
     "kvq_prompt_attention": [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _I32, _I32,
@@ -602,8 +605,10 @@ def _prefill(cname, entry, q, query_start, context_lens, block_table, kv_cache, 
 _native = None
 _NATIVE_ENTRIES = ("kvq_qk_norm_rope", "kvq_window_attention_nvfp4_per_head", "kvq_tree_attention_nvfp4_per_head",
                    "kvq_compact_drafts_nvfp4_per_head", "kvq_rope_append_fp8_per_head",
-                   "kvq_window_attention_fp8_per_head", "kvq_fp8_attention_default_splits", "kvq_prompt_attention",
-                   "kvq_fp8_attention_workspace_bytes", "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits", "kvq_last_error_string")
+                   "kvq_window_attention_fp8_per_head", "kvq_window_attention_fp8_per_head_any_length",
+                   "kvq_fp8_attention_default_splits", "kvq_prompt_attention", "kvq_fp8_attention_workspace_bytes",
+                   "kvq_per_head_attention_workspace_bytes", "kvq_per_head_attention_default_splits",
+                   "kvq_last_error_string")
 
 
 def _load_native():
@@ -760,8 +765,10 @@ def kvq_window_attention_fp8_per_head(q, query_start, seq_lens, block_table, kv_
     kvq_fp8_attention_default_splits.  A call of many query rows with
     num_splits = 1 and a workspace gathers the entries it needs there, as many
     requests at a time as it holds (kvq_fp8_attention_workspace_bytes; by
-    default up to 1 GiB is allocated); max_seq_len then has to hold.  Returns
-    (out bf16 [T, H, D], lse fp32 [T, H]); lse=False skips the lse output."""
+    default up to 1 GiB is allocated).  A sequence longer than max_seq_len is
+    attended in full all the same, but for a call given num_splits = 1 and a
+    workspace to gather into, which skips it.  Returns (out bf16 [T, H, D], lse
+    fp32 [T, H]); lse=False skips the lse output."""
     return (_native or _load_native()).attention(q, query_start, seq_lens, None, block_table, kv_cache, kv_scales, False,
                                                  softmax_scale, max_query_len, max_seq_len, window, num_sinks, layout,
                                                  num_splits, workspace, out, lse, status, stream)

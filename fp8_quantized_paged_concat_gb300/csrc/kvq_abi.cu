@@ -844,7 +844,7 @@ kvq_status per_head_attention(
     const float* k_scale, const float* v_scale, const uint8_t* page_scales, float softmax_scale, int32_t window,
     int32_t num_sinks, const TreeMask* tree, void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, int64_t lse_stride_t,
     int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes, int32_t* d_status,
-    kvq_stream_t stream) {
+    kvq_stream_t stream, bool any_length = false) {
   const bool fp8 = page_scales != nullptr;
   KVQ_REQUIRE(num_tokens >= 0 && batch_size >= 0 && max_query_len >= 0 && max_seq_len >= 0,
               "%s: num_tokens, batch_size, max_query_len and max_seq_len must be >= 0", fn);
@@ -903,13 +903,16 @@ kvq_status per_head_attention(
   }
   // (what the copy engine cannot address is decoded in the attention all the same)
   constexpr int64_t kMostStride = int64_t{1} << 38;
+  int32_t gathered_rows = 0;
   const bool gathers = fp8 && num_splits == 1 && workspace != nullptr &&
                        int64_t{max_query_len} * group > kvq::most_few_rows(head_size, true) && q_stride_t > 0 &&
                        q_stride_h > 0 && std::max(q_stride_t, q_stride_h) < kMostStride;
   if (gathers) {
     const int32_t most_new = static_cast<int32_t>(std::min<int64_t>(max_query_len, num_tokens));
-    const int64_t gather_rows =
-        kvq::fp8_gather_rows(most_new, std::min(max_seq_len, block_table_width * block_size), window, num_sinks);
+    const int32_t table_positions = block_table_width * block_size;
+    const int64_t gather_rows = kvq::fp8_gather_rows(most_new, std::min(max_seq_len, table_positions), window, num_sinks);
+    // (no request needs more rows than the block table's positions take)
+    const bool longer = any_length && gather_rows < kvq::fp8_gather_rows(most_new, table_positions, window, num_sinks);
     const int64_t need = kvq::fp8_gather_bytes(gather_rows, num_kv_heads, head_size, 1);
     KVQ_REQUIRE(aligned(workspace, 16) && workspace_bytes >= need,
                 "%s: workspace must be 16-byte aligned and at least %lld bytes (got %lld)", fn,
@@ -928,7 +931,7 @@ kvq_status per_head_attention(
       g.k = workspace;
       g.v = static_cast<uint16_t*>(workspace) + side;
       g.there = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(workspace) + 2 * side);
-      g.cached = {seq_lens + b, block_table_width * block_size, static_cast<int32_t>(gather_rows), g.there};
+      g.cached = {seq_lens + b, table_positions, static_cast<int32_t>(gather_rows), g.there, longer};
       g.query_start = query_start + b;
       g.num_tokens = num_tokens;
       g.batch_size = n;
@@ -973,7 +976,8 @@ kvq_status per_head_attention(
       p.cached = g.cached;
       if (kvq_status s = launched(fn, kvq::launch_prompt_attention(p, reinterpret_cast<cudaStream_t>(stream)))) return s;
     }
-    return ok();
+    if (!longer) return ok();
+    gathered_rows = static_cast<int32_t>(gather_rows);
   }
   int num_sms = 0;
   if (kvq_status s = check_device(fn, &num_sms)) return s;
@@ -1006,6 +1010,7 @@ kvq_status per_head_attention(
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.page_scales = page_scales;
+  a.gathered_rows = gathered_rows;
   a.scale_log2 = static_cast<float>(scale_log2);
   a.window = window;
   a.num_sinks = num_sinks;
@@ -1106,6 +1111,24 @@ kvq_status kvq_window_attention_fp8_per_head(
                             block_size, layout, num_kv_heads, head_size, nullptr, nullptr, kv_scales, softmax_scale,
                             window, num_sinks, nullptr, out, out_stride_t, out_stride_h, lse, lse_stride_t, max_seq_len,
                             num_splits, workspace, workspace_bytes, d_status, stream);
+}
+
+kvq_status kvq_window_attention_fp8_per_head_any_length(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width, const uint8_t* kv_cache,
+    const uint8_t* kv_scales, int64_t num_pages, int32_t block_size, int32_t layout, int32_t num_kv_heads,
+    int32_t head_size, float softmax_scale, int32_t window, int32_t num_sinks, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, int32_t max_seq_len, int32_t num_splits, void* workspace,
+    int64_t workspace_bytes, int32_t* d_status, kvq_stream_t stream) {
+  const char* fn = "kvq_window_attention_fp8_per_head_any_length";
+  KVQ_REQUIRE(kv_scales != nullptr || num_tokens == 0 || batch_size == 0 || max_query_len == 0,
+              "%s: kv_scales must be non-NULL", fn);
+  return per_head_attention(fn, q, q_stride_t, q_stride_h, num_tokens, num_heads, query_start, seq_lens, batch_size,
+                            max_query_len, block_table, block_table_stride, block_table_width, kv_cache, num_pages,
+                            block_size, layout, num_kv_heads, head_size, nullptr, nullptr, kv_scales, softmax_scale,
+                            window, num_sinks, nullptr, out, out_stride_t, out_stride_h, lse, lse_stride_t, max_seq_len,
+                            num_splits, workspace, workspace_bytes, d_status, stream, true);
 }
 
 int64_t kvq_fp8_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,

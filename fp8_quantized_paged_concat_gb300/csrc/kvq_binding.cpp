@@ -40,6 +40,7 @@ struct Library {
   decltype(&kvq_compact_drafts_nvfp4_per_head) compact = nullptr;
   decltype(&kvq_rope_append_fp8_per_head) append = nullptr;
   decltype(&kvq_window_attention_fp8_per_head) fp8_window = nullptr;
+  decltype(&kvq_window_attention_fp8_per_head_any_length) fp8_window_any_length = nullptr;
   decltype(&kvq_prompt_attention) prompt = nullptr;
   decltype(&kvq_fp8_attention_default_splits) fp8_default_splits = nullptr;
   decltype(&kvq_fp8_attention_workspace_bytes) fp8_workspace_bytes = nullptr;
@@ -430,10 +431,10 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* table_p = static_cast<const int32_t*>(table.data_ptr());
     const auto* cache_p = static_cast<const uint8_t*>(cache.data_ptr());
     if (fp8) {
-      must(lib.fp8_window(q.data_ptr(), sq.t, sq.h, T, dim(H), start_p, lens_p, dim(B), max_query, table_p,
-                          row_stride(table), dim(W), cache_p, page_scales, cache.size(0), c.block_size, c.layout, c.heads,
-                          c.head_size, scale, window, sinks, out.data_ptr(), so.t, so.h, lse_ptr, lse_stride, max_seq,
-                          splits, ws, ws_bytes, status, stream),
+      const auto call = a[14] == Py_None ? lib.fp8_window_any_length : lib.fp8_window;
+      must(call(q.data_ptr(), sq.t, sq.h, T, dim(H), start_p, lens_p, dim(B), max_query, table_p, row_stride(table), dim(W),
+                cache_p, page_scales, cache.size(0), c.block_size, c.layout, c.heads, c.head_size, scale, window, sinks,
+                out.data_ptr(), so.t, so.h, lse_ptr, lse_stride, max_seq, splits, ws, ws_bytes, status, stream),
            "kvq_window_attention_fp8_per_head");
     } else if (tree) {
       const at::Tensor& mask = tensor("tree_mask", a[3]);
@@ -613,6 +614,7 @@ PyObject* bind(PyObject*, PyObject* table) {
       !set("kvq_compact_drafts_nvfp4_per_head", found.compact) ||
       !set("kvq_rope_append_fp8_per_head", found.append) ||
       !set("kvq_window_attention_fp8_per_head", found.fp8_window) ||
+      !set("kvq_window_attention_fp8_per_head_any_length", found.fp8_window_any_length) ||
       !set("kvq_prompt_attention", found.prompt) ||
       !set("kvq_fp8_attention_default_splits", found.fp8_default_splits) ||
       !set("kvq_fp8_attention_workspace_bytes", found.fp8_workspace_bytes) ||

@@ -214,6 +214,7 @@ struct PerHeadAttentionArgs {
   const float* k_scale;           // NVFP4: the tensors' scales (e4m3: nullptr)
   const float* v_scale;
   const uint8_t* page_scales;     // e4m3: [num_pages, 2, num_kv_heads] (NVFP4: nullptr)
+  int32_t gathered_rows;          // e4m3, many rows: requests that need no more rows were gathered for, and are skipped (0: none)
   float scale_log2;               // softmax_scale * log2(e)
   int32_t window;                 // <= 0: none
   int32_t num_sinks;
@@ -289,6 +290,7 @@ struct CachedArgs {
   int32_t table_positions;        // block_table_width * block_size, < 2^31 - 256 (host check)
   int32_t rows;                   // of the workspace for each request, a multiple of 64
   const uint32_t* there;          // [batch_size * rows / 32 + 3]: bit per row: the key exists
+  bool longer_apart;              // requests that need more rows are another launch's, which reports what it skips
 };
 struct PromptAttentionArgs {
   const void* q;                  // bf16 [num_tokens, num_heads, head_size]

@@ -156,7 +156,7 @@ __device__ __forceinline__ Item request_item_at(const PromptAttentionArgs& a, ui
   const uint32_t b = a.batch_size > 32 ? place : __ffs(__ballot_sync(kFull, rank == place)) - 1;
   GatherPlan plan;
   if (!gather_plan(a.cached, a.seq_start, a.num_tokens, a.max_seq_len, a.window, a.num_sinks, b, plan)) {
-    if (lane == 0) report(a.status, KVQ_STATUS_BAD_BATCH);
+    if (lane == 0 && !a.cached.longer_apart) report(a.status, KVQ_STATUS_BAD_BATCH);
     return it;
   }
   if (unit0 >= static_cast<uint32_t>(plan.n) * a.chunks) return it;

@@ -846,6 +846,27 @@ kvq_status kvq_window_attention_fp8_per_head(
     int32_t* d_status, kvq_stream_t stream);
 
 /*
+ * kvq_window_attention_fp8_per_head_any_length -- the same, but that a call
+ * that gathers leaves no request out: one whose sequence is longer than
+ * max_seq_len has its entries decoded in the attention, in one more launch
+ * (which is left out where the block table's reach shows that there can be
+ * none).  For bounds that may come not to hold, as where a captured call is
+ * replayed with longer sequences.
+ */
+kvq_status kvq_window_attention_fp8_per_head_any_length(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    int64_t num_tokens, int32_t num_heads,
+    const int32_t* query_start, const int32_t* seq_lens, int32_t batch_size, int32_t max_query_len,
+    const int32_t* block_table, int64_t block_table_stride, int32_t block_table_width,
+    const uint8_t* kv_cache, const uint8_t* kv_scales, int64_t num_pages, int32_t block_size, int32_t layout,
+    int32_t num_kv_heads, int32_t head_size,
+    float softmax_scale, int32_t window, int32_t num_sinks,
+    void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* lse, int64_t lse_stride_t,
+    int32_t max_seq_len, int32_t num_splits, void* workspace, int64_t workspace_bytes,
+    int32_t* d_status, kvq_stream_t stream);
+
+/*
  * kvq_fp8_attention_workspace_bytes -- bytes of workspace that a call of
  * kvq_window_attention_fp8_per_head with these sizes can use: for num_splits >
  * 1 what kvq_per_head_attention_workspace_bytes gives, for num_splits = 1 the

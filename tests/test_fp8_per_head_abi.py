@@ -208,6 +208,19 @@ def test_attention_of_nothing_is_ok_without_a_device(lib, over):
     assert lib.kvq_window_attention_fp8_per_head(*window_args(**over, **nothing).values()) == 0
 
 
+@no_gpu_only
+def test_attention_of_any_length_checks_as_the_other_does(lib):
+    name = "kvq_window_attention_fp8_per_head_any_length"
+    for over, needle in ((dict(num_splits=0), "num_splits"), (dict(kv_scales=None), "kv_scales must be non-NULL"),
+                         (dict(workspace=A, workspace_bytes=HELD - 1, **ROWS), "workspace must be 16-byte aligned"),
+                         (dict(softmax_scale=float("inf")), "softmax_scale must be finite")):
+        rejected(lib, name, window_args(**over), needle)
+    for over in ({}, dict(workspace=A, workspace_bytes=HELD, **ROWS), dict(max_seq_len=0)):
+        assert getattr(lib, name)(*window_args(**over).values()) in (2, 3), lib.kvq_last_error_string()
+    nothing = dict(q=None, out=None, kv_cache=None, kv_scales=None, block_table=None, query_start=None, seq_lens=None)
+    assert getattr(lib, name)(*window_args(num_tokens=0, **nothing).values()) == 0
+
+
 @pytest.mark.parametrize("args,want", [
     ((40, 8, 2, 128, 1, 10, 256, 0, 0, 1), HELD),
     ((40, 8, 2, 128, 4, 10, 200, 0, 0, 1), 4 * 256 * 2 * 128 * 4 + (4 * 8 + 3 + 3) // 4 * 16),

@@ -751,3 +751,47 @@ def test_a_larger_workspace_of_ones_own(kvq):
     got = kvq.kvq_window_attention_fp8_per_head(**call, workspace=held)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert not bool((held[:128 * 8 * 128 * 2] == 0xFF).all())         # (the first request's entries are there)
+
+
+@pytest.mark.parametrize("dim,heads,kv,new,layout", [(64, 64, 8, 130, "NHD"), (128, 32, 8, 300, "HND"), (256, 32, 4, 130, "NHD")])
+@pytest.mark.parametrize("mask", [dict(), dict(window=400, num_sinks=5)])
+def test_default_calls_attend_sequences_of_any_length(kvq, dim, heads, kv, new, layout, mask):
+    """A bound on the lengths that does not hold, for one request, for all but one, and in a captured call whose
+    sequences grow: every row is as for a bound that does, or as where its entries are decoded as they are read."""
+    b = Batch([(100, new), (900, new), (0, new), (700, 7), (30, 0), (3, 1)], heads, kv, dim, 16, layout, 179)
+    call = b.device()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    gathered, read = attend(kvq, call, "gather", **mask), attend(kvq, call, 1, **mask)
+    for bound in (500, new + 1, 1, 0):
+        through = kvq.kvq_fp8_attention_default_splits(new, heads, kv, dim, 6, bound, *mask.values())
+        assert through == (1, bound > 0)                              # (a bound of 0 makes no call: not gathered)
+        got = attend(kvq, dict(call, max_seq_len=bound, status=status), None, **mask)
+        rows = kvq.kvq_fp8_attention_workspace_bytes(b.start[-1], heads, kv, dim, 1, new, bound, *mask.values()) // (
+            4 * kv * dim) // 64 * 64 if bound else -1
+        for r, length in enumerate(b.lens):
+            first = max(0, length - b.reqs[r][1] - 399) if mask else 0
+            want = gathered if length - first + min(mask.get("num_sinks", 0), first) <= rows else read
+            t = slice(b.start[r], b.start[r + 1])
+            assert torch.equal(got[0][t], want[0][t]) and torch.equal(got[1][t], want[1][t]), (bound, r)
+        assert int(status.item()) == 0
+    lens = call["seq_lens"].clone()
+    call["seq_lens"].copy_(torch.clamp(lens, max=new + 50))
+    short = dict(call, max_seq_len=new + 50)
+    attend(kvq, short, None, **mask)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        inside = attend(kvq, short, None, **mask)
+    call["seq_lens"].copy_(lens)
+    graph.replay()
+    torch.cuda.synchronize()
+    again = attend(kvq, short, None, **mask)
+    assert torch.equal(inside[0], again[0]) and torch.equal(inside[1], again[1])
+    assert bool(torch.isfinite(inside[1]).all())
+    # requests that are none are reported once more, and their rows left
+    call["query_start"][4] = b.start[-1] + 1
+    out = bf16_dev(np.full(b.q_bits.shape, CANARY, np.uint16))
+    attend(kvq, dict(call, max_seq_len=500, out=out, status=status), None, **mask)
+    assert int(status.item()) == kvq.STATUS_BAD_BATCH
+    left = np.all(bits_of(out) == CANARY, (1, 2))
+    assert np.all(left[b.start[3]:b.start[5]]) and not np.any(left[:b.start[3]]) and not np.any(left[b.start[5]:])
