@@ -918,12 +918,12 @@ kvq_status per_head_attention(
                 "%s: workspace must be 16-byte aligned and at least %lld bytes (got %lld)", fn,
                 static_cast<long long>(need), static_cast<long long>(workspace_bytes));
     if (kvq_status s = check_device(fn)) return s;
-    // as many requests at a time as the workspace holds, their rows and blocks below 2^31
+    // as many requests at a time as the workspace holds and a launch takes
     const kvq::PromptAttentionArgs shape = prompt_args(num_heads, num_kv_heads, head_size);
     const int64_t blocks = (int64_t{most_new} * shape.chunks + shape.tile_tokens - 1) / shape.tile_tokens * num_kv_heads;
-    const int64_t most = std::min<int64_t>(
-        {kvq::fp8_gather_at_once(gather_rows, num_kv_heads, head_size, batch_size, workspace_bytes),
-         ((int64_t{1} << 31) - 256) / gather_rows, ((int64_t{1} << 31) - 1) / blocks});
+    const int64_t most =
+        std::min(kvq::fp8_gather_at_once(gather_rows, num_kv_heads, head_size, batch_size, workspace_bytes),
+                 kvq::fp8_gather_most(gather_rows, blocks));
     for (int64_t b = 0; b < batch_size; b += most) {
       const int32_t n = static_cast<int32_t>(std::min<int64_t>(most, batch_size - b));
       const int64_t side = n * gather_rows * num_kv_heads * head_size;

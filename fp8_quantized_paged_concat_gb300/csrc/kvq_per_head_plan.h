@@ -78,6 +78,14 @@ inline int64_t fp8_gather_at_once(int64_t rows, int64_t num_kv_heads, int64_t he
   while (n > 0 && fp8_gather_bytes(rows, num_kv_heads, head_size, n) > bytes) --n;
   return n;
 }
+// The most requests of one launch, each of `rows` workspace rows and `blocks`
+// block numbers: their rows stay below 2^31, and their numbers at 2^25.  Numbers
+// that turn out empty (max_query_len is the longest request's, or a loose bound)
+// are passed over one after the other, 0.5 us each on 152 CTAs at once: 2^25 of
+// them in 0.1 s, where the waits for a next block are given up after 2 s.
+inline int64_t fp8_gather_most(int64_t rows, int64_t blocks) {
+  return std::max<int64_t>(1, std::min(((int64_t{1} << 31) - 256) / rows, (int64_t{1} << 25) / blocks));
+}
 // Whether a call's default is to gather, into KVQ_FP8_GATHER_BYTES at most:
 // where every entry is read for many blocks of rows, and these blocks about fill
 // the GPU.  us of the attention that decodes the entries (in its default ranges)

@@ -1,7 +1,9 @@
 // For calls over the e4m3 cache whose default is to gather their entries, over
 // the whole range of sizes: one request's fit into the room that the default
 // counts on, as many at a time as the call then takes are the most that do, and
-// a batch that goes through in rounds fills the GPU in each of them.
+// a batch that goes through in rounds fills the GPU in each of them.  And a
+// launch of any size, into workspaces of any size, has fewer than 2^31 rows and at
+// most 2^25 block numbers.
 #include <cstdio>
 
 #include "kvq_per_head_plan.h"
@@ -41,7 +43,19 @@ int main() {
                       kvq::fp8_gather_at_once(64, kv_heads, head_size, batch, room) == batch)
                     ++unlike;
                 }
-  std::printf("gathers %lld, rounds %lld, no room %lld, not most %lld, idle %lld, unlike %lld\n", gathers, rounds, no_room,
+  // 128 query rows to a block, of whole tokens where a token's rows are fewer
+  long long large = 0;
+  for (long long group : {1, 2, 3, 4, 7, 8, 16, 43, 64, 65, 127, 128, 129, 130, 500})
+    for (long long kv_heads : {1, 2, 3, 8, 128})
+      for (long long query : {1LL, 25LL, 300LL, 4096LL, 65536LL, 1LL << 20, (1LL << 31) - 1})
+        for (long long rows : {64LL, 4096LL, 1LL << 20, (1LL << 31) - 256}) {
+          if (query * group * kv_heads >= 1LL << 31) continue;
+          const long long tokens = group < 128 ? 128 / group : 1, chunks = (group + 127) / 128;
+          const long long blocks = (query * chunks + tokens - 1) / tokens * kv_heads;
+          const long long n = kvq::fp8_gather_most(rows, blocks);
+          if (n < 1 || n * rows > (1LL << 31) - 256 || n * blocks > 1LL << 25) ++large;
+        }
+  std::printf("large %lld, gathers %lld, rounds %lld, no room %lld, not most %lld, idle %lld, unlike %lld\n", large, gathers, rounds, no_room,
               not_most, idle, unlike);
-  return no_room + not_most + idle + unlike != 0 || gathers == 0 || rounds == 0;
+  return large + no_room + not_most + idle + unlike != 0 || gathers == 0 || rounds == 0;
 }
