@@ -795,3 +795,38 @@ def test_default_calls_attend_sequences_of_any_length(kvq, dim, heads, kv, new, 
     assert int(status.item()) == kvq.STATUS_BAD_BATCH
     left = np.all(bits_of(out) == CANARY, (1, 2))
     assert np.all(left[b.start[3]:b.start[5]]) and not np.any(left[:b.start[3]]) and not np.any(left[b.start[5]:])
+
+
+@pytest.mark.parametrize("splits", [1, -3, "gather", None])
+@pytest.mark.parametrize("mask", [dict(), dict(window=90, num_sinks=4)])
+def test_sequences_of_the_largest_lengths(kvq, splits, mask):
+    """Lengths next to 2^31, far past the block table: the keys that it holds are attended to, or none where the window
+    lies behind them but for the first."""
+    b = Batch([(200, 70), (50, 70), (90, 70)], 16, 8, 64, 16, "NHD", 181)
+    b.table = b.table[:, :9].copy()                                   # 144 positions
+    lens = [(1 << 31) - 1, 120, (1 << 31) - 70]
+    call = dict(b.device(), seq_lens=i32(lens))
+    b.table[b.table < 0] = b.cache.codes.shape[0]
+    call["block_table"] = dev(b.table.astype(np.int32))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = attend(kvq, dict(call, status=status), splits, **mask)
+    assert int(status.item()) == kvq.STATUS_BAD_INDEX
+    # every query of theirs is past the table: it sees all of it, or the first keys alone
+    b.lens = [144 + 70, 120, 144 + 70]
+    if mask:
+        b.lens = [144 + 1000, 120, 144 + 1000]
+    check(got, b.want(window=mask.get("window", 0), sinks=mask.get("num_sinks", 0)))
+
+
+@pytest.mark.parametrize("dim,heads,kv", [(64, 32, 4), (128, 32, 8), (256, 16, 4)])
+def test_a_chunk_beside_decoded_tokens(kvq, dim, heads, kv):
+    """One request's chunk and the decoded tokens of many in one call, appended and attended to as by default."""
+    reqs = [(int(c), 1) for c in np.random.default_rng(7).integers(0, 300, 40)]
+    reqs[17:17] = [(150, 400), (0, 33)]
+    b = Batch(reqs, heads, kv, dim, 16, "NHD", 191)
+    case = Append(reqs, heads, kv, dim, 16, "NHD", dim, 193)
+    check_append(kvq, case)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert kvq.kvq_fp8_attention_default_splits(400, heads, kv, dim, 42, max(b.lens)) == (1, True)
+    check(attend(kvq, dict(b.device(), status=status), None), b.want(gathered=True))
+    assert int(status.item()) == 0
