@@ -190,11 +190,17 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
       const bool many = blocks() >= places();
       n = ranges(few ? (many ? 2 : 6) : (many ? 6 : 3));
     }
-  } else if (fp8 && few && keys >= 1024 && blocks() >= places() && blocks() < 3 * places()) {
-    // The last of few waves of CTAs leaves much of the GPU idle: half as long ones
-    // do less so (128 requests x window 4096, 1024 blocks on 456 places: 189 us
-    // against 201; 64 requests of 1000 to 3000 keys, 512 blocks: 56 against 62; 128
-    // requests x 16 rows x 2000 keys, 2048 blocks: 157 against 136).
+  } else if (fp8 && few && keys >= 2048 && blocks() >= places() && blocks() < 3 * places() &&
+             3 * (blocks() % places()) <= places()) {
+    // A last wave of few CTAs leaves much of the GPU idle: half as long ones do
+    // less so (128 requests x window 4096, 1024 blocks on 456 places: 189 us
+    // against 201; 64 requests of 1000 to 3000 keys, 512 blocks: 56 against 62).
+    // us of one and two ranges by waves, 8 key heads, head size 128, 2500 keys: 1.05
+    // 71 / 66, 1.3 81 / 73, 1.6 84 / 90, 1.95 92 / 100, 2.3 121 / 119, 2.6 126 / 134,
+    // 2.95 135 / 145, 3.3 162 / 163; 4000 keys: 1.3 120 / 107, 1.6 127 / 130, 2.3 183 /
+    // 174, 2.95 205 / 214, 3.3 245 / 241; 1100 keys: 1.05 36.8 / 36.6, 1.3 41 / 42, 1.95
+    // 47 / 56, 2.3 62 / 65.  Head size 64, 2500 keys: 1.3 61 / 57, 1.6 65 / 70, 2.3 91 /
+    // 92; 256: 1.3 142 / 135, 1.6 162 / 167, 2.3 222 / 216.
     n = whole(2);
   } else {
     // As many as the call is short of CTAs, of at least 256 keys in the tensor

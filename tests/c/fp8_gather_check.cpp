@@ -3,7 +3,8 @@
 // counts on, as many at a time as the call then takes are the most that do, and
 // a batch that goes through in rounds fills the GPU in each of them.  And a
 // launch of any size, into workspaces of any size, has fewer than 2^31 rows and at
-// most 2^25 block numbers.
+// most 2^25 block numbers.  And single tokens' blocks are cut into two ranges for the
+// sake of a short last wave only.
 #include <cstdio>
 
 #include "kvq_per_head_plan.h"
@@ -55,7 +56,17 @@ int main() {
           const long long n = kvq::fp8_gather_most(rows, blocks);
           if (n < 1 || n * rows > (1LL << 31) - 256 || n * blocks > 1LL << 25) ++large;
         }
-  std::printf("large %lld, gathers %lld, rounds %lld, no room %lld, not most %lld, idle %lld, unlike %lld\n", large, gathers, rounds, no_room,
+  long long full = 0, cut = 0;
+  for (int batch = 1; batch < 400; ++batch)
+    for (int keys : {1100, 2047, 2500, 4000})
+      for (int sms : {152, 148}) {
+        const kvq::PerHeadRanges r = kvq::per_head_default_ranges(1, 4, 8, 128, batch, keys, 0, 0, sms, true);
+        const int places = 3 * sms, last = 8 * batch % places;
+        if (8 * batch < places) continue;
+        if (r.splits > 1) ++cut;
+        if (r.splits > 1 && (keys < 2048 || 3 * last > places)) ++full;
+      }
+  std::printf("full last waves cut %lld of %lld, large %lld, gathers %lld, rounds %lld, no room %lld, not most %lld, idle %lld, unlike %lld\n", full, cut, large, gathers, rounds, no_room,
               not_most, idle, unlike);
-  return large + no_room + not_most + idle + unlike != 0 || gathers == 0 || rounds == 0;
+  return (cut == 0) + full + large + no_room + not_most + idle + unlike != 0 || gathers == 0 || rounds == 0;
 }
