@@ -2,7 +2,8 @@
 // requests see, as bf16 rows of a workspace: exact, an e4m3 value has four
 // significant bits and the page scales are powers of two.  For chunks of many
 // query rows, whose attention reads every key many times: it decodes each once,
-// where the attention over the pages decodes it for every 256 rows.
+// where the attention over the pages decodes it for every 256 rows (128 at head
+// size 256).
 //
 // Bound: HBM (a byte read and two written for each value).  One warp takes 32
 // rows and every fourth (head, side): lane l looks up row l's page once; then

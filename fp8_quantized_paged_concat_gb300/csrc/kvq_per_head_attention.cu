@@ -62,7 +62,7 @@
 // Measured: 32 requests x 7k to 34k keys x 8 key heads of 128, 1.37 GB: 220 us =
 // 6.25 TB/s, 0.92 of a copy's 6.8; 128 requests x window 4096, 1.08 GB: 188 us =
 // 5.75 TB/s (the ranges' starts and the last wave of CTAs); one request x 8000
-// keys, 16 MB: 11.0 us in a graph, of which some 6 are the launch, the set-up's
+// keys, 16 MB: 11.0 to 11.5 us in a graph, of which some 6 are the launch, the set-up's
 // dependent loads and the join of its 21 ranges, at 7.3 ns a key of a range.
 #include "kvq_per_head_attention.cuh"
 #include "kvq_per_head_plan.h"

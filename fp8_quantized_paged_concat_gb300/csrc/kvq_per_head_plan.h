@@ -27,7 +27,7 @@ constexpr int64_t resident_ctas(int32_t head_size, int64_t block, bool fp8 = fal
 // faster (16 rows, head size 128: 128 requests x 2000 keys 136 us against 149, 32
 // x 5000 keys 95 against 102; 32 rows, 128 x 1000 keys 146 against 143).
 inline int64_t few_rows(int64_t rows, int64_t groups, int32_t head_size, int64_t splits, int sms, bool fp8 = false) {
-  return !fp8 && rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16, fp8) * int64_t{sms}
+  return !fp8 && rows > 8 && head_size != 256 && (rows + 15) / 16 * groups * splits >= resident_ctas(head_size, 16) * int64_t{sms}
              ? 16 : 8;
 }
 
@@ -184,7 +184,7 @@ inline PerHeadRanges per_head_default_ranges(int64_t max_query_len, int64_t grou
     if (few && !fp8 && rows > 8 && head_size != 256) {
       block = 16;
       n = ranges(4);
-      if (few_rows(rows, groups, head_size, n, sms, fp8) != 16) block = 8;
+      if (few_rows(rows, groups, head_size, n, sms) != 16) block = 8;
     }
     if (block != 16) {
       const bool many = blocks() >= places();

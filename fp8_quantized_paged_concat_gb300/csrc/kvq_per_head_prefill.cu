@@ -50,9 +50,9 @@
 // beside others 2^15 larger, which their rows need not see.)  4 requests x 2048
 // new tokens behind up to 8192, 32 heads (8 key heads) of 128: 832 us = 810
 // TFLOP/s, bound by the decoding warps, whose work is done again for every 256
-// rows (codes through registers a tile ahead: 1111; the loop over tiles unrolled
+// rows (128 at head size 256) (codes through registers a tile ahead: 1111; the loop over tiles unrolled
 // twice: 1461; one code for both sides, to spare instruction fetches: 861); calls
-// that are given a workspace for it gather their entries once instead (450 us).
+// that are given a workspace for it gather their entries once instead (468 us).
 // 32 requests x 32 new tokens x 6000 keys, 128 rows a key head: 204 us.
 #include <type_traits>
 

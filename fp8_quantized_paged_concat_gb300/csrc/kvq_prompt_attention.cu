@@ -40,15 +40,17 @@
 //     sequence are zeroed, and in tiles that some row does not see whole NaN
 //     and infinities are (one or two warps look through them).
 // Measured (32 query heads, 8 key heads; calls one after the other), and of
-// 1947 TFLOP/s: D = 128, 1 x 16384 tokens 1200 us = 1830 TFLOP/s, 0.94; 4 x 4096
-// 344 us = 1600, 0.82; 16 x 1024 136 us = 1009, 0.52.  A pair of row tiles takes
+// 1947 TFLOP/s: D = 128, 1 x 16384 tokens 1330 to 1370 us = 1600 to 1650 TFLOP/s,
+// 0.83, with the SM clock at 1665 MHz under the power cap (the first few calls on
+// an idle GPU, at 2070 MHz, 1200 us = 1830); 4 x 4096 375 us = 1465, 0.75 (first 345);
+// 16 x 1024 136 us = 1009, 0.52.  A pair of row tiles takes
 // about 1330 clocks a key tile, of which the products take 1280 (S at 48 clocks
 // per 16 dimensions, bound by shared memory, PV at 64 per 16 keys); an item
 // costs some 4000 more, for its first and last tiles' masks and its output.
-// D = 64: 1 x 16384 1070 us = 1030 TFLOP/s, where the chain from a tile's scores
-// to its weights (1170 clocks) is longer than the products of the other row
-// tile (384).  D = 256: 1 x 8192 774 us = 1421, one row tile, whose keys
-// come from L2 twice as often, into two stages.
+// D = 64: 1 x 16384 1086 us = 1012 TFLOP/s, where the chain from a tile's scores
+// to its weights (1170 clocks) is longer than the products of both row tiles (2 x
+// 384).  D = 256: 1 x 8192 770 us = 1430, one row tile, whose keys come from L2
+// twice as often, into two stages.
 // Every wait of a role on another role or on its products is bounded; on
 // expiry the CTA records KVQ_STATUS_TIMEOUT, drains its copies and products,
 // frees its tensor memory and leaves its rows unwritten.

@@ -820,9 +820,13 @@ kvq_status kvq_rope_append_fp8_per_head(
  * those, as many requests at a time as it holds: at least one request's, as
  * kvq_fp8_attention_workspace_bytes gives them for batch_size 1.  Then
  * max_seq_len bounds seq_lens for good: a request of a longer sequence is
- * skipped (KVQ_STATUS_BAD_BATCH).  Without a workspace, or where q's strides
- * are not positive and below 2^38, they decode the entries in the attention,
- * once for every block of 256 rows.
+ * skipped (KVQ_STATUS_BAD_BATCH; kvq_window_attention_fp8_per_head_any_length
+ * attends it too).  Without a workspace, or where q's strides are not positive
+ * and below 2^38, they decode the entries in the attention, once for every
+ * block of 256 rows (of 128 at head_size 256 and in calls of no more).  Blocks
+ * are counted by max_query_len for every request, and one that has no rows
+ * still costs: a bound far above the queries, or one long chunk beside many
+ * single tokens, takes half a microsecond for every 152 of them.
  * Arithmetic: products on the tensor cores with fp32 sums, the softmax in
  * fp32, out rounded once to bf16.  Calls of many query rows (as above): entries
  * with their scale are exact in bf16, queries stay as they are, and the weights
