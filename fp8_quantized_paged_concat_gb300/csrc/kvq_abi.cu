@@ -1045,8 +1045,8 @@ int32_t default_splits(int32_t max_query_len, int32_t num_heads, int32_t num_kv_
                        int32_t batch_size, int32_t max_seq_len, int32_t window, int32_t num_sinks, bool fp8,
                        int32_t* use_workspace) {
   if (use_workspace != nullptr) *use_workspace = 0;
-  if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || batch_size <= 0 || max_seq_len <= 0 ||
-      num_sinks < 0)
+  if (max_query_len <= 0 || num_kv_heads <= 0 || num_heads < num_kv_heads || head_size <= 0 || batch_size <= 0 ||
+      batch_size > 65535 || max_seq_len <= 0 || num_sinks < 0 || int64_t{max_query_len} * num_heads >= (int64_t{1} << 31))
     return 1;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -70,10 +70,10 @@ inline int64_t fp8_gather_bytes(int64_t rows, int64_t num_kv_heads, int64_t head
   return batch_size * rows * num_kv_heads * head_size * 4 + (batch_size * rows / 32 + 3 + 3) / 4 * 16;
 }
 // Requests whose entries are gathered at a time into `bytes` of workspace, one
-// launch each of the gather and of the attention (0: not one's fit).
+// launch each of the gather and of the attention (0: not one's fit, or no size).
 inline int64_t fp8_gather_at_once(int64_t rows, int64_t num_kv_heads, int64_t head_size, int64_t batch_size,
                                   int64_t bytes) {
-  if (4.0 * static_cast<double>(rows) * num_kv_heads * head_size > static_cast<double>(bytes)) return 0;
+  if (head_size <= 0 || 4.0 * static_cast<double>(rows) * num_kv_heads * head_size > static_cast<double>(bytes)) return 0;
   int64_t n = std::min(batch_size, bytes / (rows * num_kv_heads * head_size * 4));
   while (n > 0 && fp8_gather_bytes(rows, num_kv_heads, head_size, n) > bytes) --n;
   return n;

@@ -56,6 +56,11 @@ int main() {
           const long long n = kvq::fp8_gather_most(rows, blocks);
           if (n < 1 || n * rows > (1LL << 31) - 256 || n * blocks > 1LL << 25) ++large;
         }
+  // sizes that make no call are answered all the same
+  for (int head_size : {0, -1, -128})
+    if (kvq::fp8_gather_at_once(64, 8, head_size, 4, room) != 0 ||
+        kvq::per_head_default_ranges(4096, 4, 8, head_size, 64, 4096, 0, 0, 152, true).splits < 1)
+      ++large;
   long long full = 0, cut = 0;
   for (int batch = 1; batch < 400; ++batch)
     for (int keys : {1100, 2047, 2500, 4000})

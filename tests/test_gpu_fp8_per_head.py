@@ -830,3 +830,11 @@ def test_a_chunk_beside_decoded_tokens(kvq, dim, heads, kv):
     assert kvq.kvq_fp8_attention_default_splits(400, heads, kv, dim, 42, max(b.lens)) == (1, True)
     check(attend(kvq, dict(b.device(), status=status), None), b.want(gathered=True))
     assert int(status.item()) == 0
+
+
+def test_defaults_for_sizes_that_make_no_call(kvq):
+    most = (1 << 31) - 1
+    for args in ((300, 32, 8, 0, 64, 6000), (300, 32, 8, -128, 64, 6000), (most, most, 1, 128, most, most),
+                 (1 << 20, 1 << 20, 1 << 20, 128, 1 << 20, 6000), (300, 32, 8, 128, 65536, 6000)):
+        assert kvq.kvq_fp8_attention_default_splits(*args) == (1, False)
+        assert kvq.kvq_per_head_attention_default_splits(*args) == (1, False)
